@@ -67,6 +67,11 @@ SIGNATURES = {
     "tt_loss_scale_update": (_st, [_vp, _vp, _vp, _vp, _i, _f, _f]),
     "tt_gpt2_generate_arena_bytes": (_sz, [_vp, _i, _i, _i]),
     "tt_gpt2_generate": (_st, [_vp, _vp, _vp, _i, _i, _i, _vp]),
+    "tt_gpt2_step_distill": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _i, _i, _i, _vp,
+                                   C.POINTER(_f)]),
+    "tt_gpt2_top_logits": (_st, [_vp, _vp, _vp, _i, _i, _i, _f, _vp, _vp, _vp]),
+    "tt_gpt2_generate_beam_arena_bytes": (_sz, [_vp, _i, _i, _i, _i]),
+    "tt_gpt2_generate_beam": (_st, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
     # tt_ops.h
     "tt_ctx_set_gemm_backend": (_st, [_vp, _i]),
     "tt_ctx_set_wait_limit": (_st, [_vp, C.c_longlong]),
@@ -80,6 +85,10 @@ SIGNATURES = {
     "tt_op_xent": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _f]),
     "tt_op_embed_fwd": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i]),
     "tt_op_embed_bwd": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i]),
+    "tt_op_top_logits": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f]),
+    "tt_op_distill": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _f, _f]),
+    "tt_op_beam_select": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i]),
+    "tt_op_beam_reorder": (_st, [_vp, _vp, _vp, _i, _i, _i, _sz, _sz, _sz]),
     "tt_linear_bwd_dw_noalloc": (_st, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i]),
     # tt_graph.h (node handles are int32; negative = tt_status)
     "tt_node_new": (_i, [_vp, _i, C.POINTER(_i), _i]),

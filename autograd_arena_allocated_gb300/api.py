@@ -52,6 +52,11 @@ def generate_arena_bytes(cfg, B: int, T_prompt: int, n_new: int) -> int:
     return int(lib().tt_gpt2_generate_arena_bytes(C.byref(cfg), int(B), int(T_prompt), int(n_new)))
 
 
+def generate_beam_arena_bytes(cfg, B: int, T_prompt: int, n_new: int, K: int) -> int:
+    """Exact arena bytes of tt_gpt2_generate_beam."""
+    return int(lib().tt_gpt2_generate_beam_arena_bytes(C.byref(cfg), int(B), int(T_prompt), int(n_new), int(K)))
+
+
 def arena_bytes(cfg: GPT2Config, B: int, T: int) -> int:
     return int(lib().tt_gpt2_arena_bytes(C.byref(cfg), B, T))
 
@@ -164,6 +169,22 @@ class Context:
                                           C.byref(loss) if sync else None))
         return float(loss.value) if sync else None
 
+    def step_distill(self, params, grads, tokens, targets, t_vals, t_idx, t_lse, k: int, alpha: float, tau: float,
+                     B: int, T: int, accumulate: bool = False, loss_scale=None, sync: bool = True):
+        """tt_gpt2_step_distill: the step on a teacher's top logits (device
+        tensors of top_logits_of); targets may be None when alpha is 1."""
+        loss = C.c_float()
+        self._check(lib().tt_gpt2_step_distill(self.h, _ptr(params), _ptr(grads), _ptr(tokens), _ptr(targets),
+                                               _ptr(t_vals), _ptr(t_idx), _ptr(t_lse), int(k), float(alpha),
+                                               float(tau), int(B), int(T), 1 if accumulate else 0, _ptr(loss_scale),
+                                               C.byref(loss) if sync else None))
+        return float(loss.value) if sync else None
+
+    def top_logits_of(self, params, tokens, B: int, T: int, k: int, vals, idx, lse=None, tau: float = 1.0):
+        """tt_gpt2_top_logits: the k largest logits of every position."""
+        self._check(lib().tt_gpt2_top_logits(self.h, _ptr(params), _ptr(tokens), int(B), int(T), int(k), float(tau),
+                                             _ptr(vals), _ptr(idx), _ptr(lse)))
+
     def grad_stats(self, grads, stats, loss_scale=None, n=None):
         """stats (device float[2]) = (||grads / scale||, not finite)."""
         n = grads.numel() if n is None else n
@@ -193,6 +214,13 @@ class Context:
         """tt_gpt2_generate: greedy tokens; out [B, T_prompt + n_new] int32 (host or device)."""
         self._check(lib().tt_gpt2_generate(self.h, _ptr(params), _ptr(prompt), int(B), int(T_prompt), int(n_new),
                                            _ptr(out)))
+        return out
+
+    def generate_beam(self, params, prompt, B: int, T_prompt: int, n_new: int, K: int, out, scores, eos: int = -1):
+        """tt_gpt2_generate_beam: out [B, K, T_prompt + n_new] int32 and scores
+        [B, K] float32 (host or device), best hypothesis first."""
+        self._check(lib().tt_gpt2_generate_beam(self.h, _ptr(params), _ptr(prompt), int(B), int(T_prompt), int(n_new),
+                                                int(K), int(eos), _ptr(out), _ptr(scores)))
         return out
 
     def loss_device(self):
@@ -273,6 +301,24 @@ class Context:
     def embed_bwd(self, dtype, dx, tokens, dwte, dwpe, B, T, C_, V, maxT):
         self._check(lib().tt_op_embed_bwd(self.h, DTYPES[dtype], _ptr(dx), _ptr(tokens), _ptr(dwte),
                                           _ptr(dwpe), B, T, C_, V, maxT))
+
+    def top_logits(self, dtype, logits, vals, idx, lse, M, V, ld, k, tau=1.0):
+        self._check(lib().tt_op_top_logits(self.h, DTYPES[dtype], _ptr(logits), _ptr(vals), _ptr(idx), _ptr(lse),
+                                           M, V, ld, k, float(tau)))
+
+    def distill(self, dtype, logits, t_vals, t_idx, t_lse, targets, dlogits, row_loss, mean_loss, M, V, ld, k,
+                alpha, tau, dscale):
+        self._check(lib().tt_op_distill(self.h, DTYPES[dtype], _ptr(logits), _ptr(t_vals), _ptr(t_idx), _ptr(t_lse),
+                                        _ptr(targets), _ptr(dlogits), _ptr(row_loss), _ptr(mean_loss), M, V, ld, k,
+                                        float(alpha), float(tau), float(dscale)))
+
+    def beam_select(self, dtype, logits, scores, done, parent, token, out_scores, out_done, B, K, V, ld, n, eos=-1):
+        self._check(lib().tt_op_beam_select(self.h, DTYPES[dtype], _ptr(logits), _ptr(scores), _ptr(done),
+                                            _ptr(parent), _ptr(token), _ptr(out_scores), _ptr(out_done), B, K, V, ld,
+                                            n, eos))
+
+    def beam_reorder(self, state, parents, N, B, K, row_bytes, first, count):
+        self._check(lib().tt_op_beam_reorder(self.h, _ptr(state), _ptr(parents), N, B, K, row_bytes, first, count))
 
     # -------------------------------------------------------------- generic graph (tt_graph.h)
     def _node(self, h: int) -> int:

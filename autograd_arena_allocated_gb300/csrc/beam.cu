@@ -1,0 +1,227 @@
+// beam.cu -- beam search: the choice of the next hypotheses among the beams'
+// best continuations, the reordering of per-beam state, the prompt's cache
+// copied to every beam, and the walk back along the chosen parents.
+//
+//   k_beam_merge    per sequence the n best of its K beams' lists
+//   k_beam_reorder  state rows of K slots moved in place along parents[K]
+//   k_kv_fill_beams keys and values of a prompt into the K cache rows of its beams
+//   k_beam_walk     the K token sequences, from the last step's back to the first
+#include "tt_internal.h"
+
+#include <algorithm>
+
+namespace tt {
+namespace {
+
+// One CTA per sequence.  Candidate (j, v) of beam j has the score
+//   s_j + (z_v - lse_j)          for a live beam
+//   s_j for v = eos, else -inf   for a finished one (done_j != 0)
+// in 64 bits: the cumulative scores of long hypotheses are hundreds, where a
+// 32-bit sum would tie or swap candidates that differ by less than 1e-5.
+// A beam without a distribution (its log-sum-exp is not finite) or without a
+// finite score offers -inf only.  Order: score, then the lowest j V + v.
+constexpr int BM_THREADS = 256;
+constexpr int BM_MAX = 2048;  // K * n
+
+__global__ void __launch_bounds__(BM_THREADS)
+k_beam_merge(const float* __restrict__ vals, const int32_t* __restrict__ idx, const double* __restrict__ lse,
+             const float* scores, const int32_t* done, int K, int V, int kk, int n, int eos, int32_t* parent,
+             int32_t* token, float* out_scores, int32_t* out_done, int32_t* __restrict__ tok_hist,
+             int32_t* __restrict__ par_hist, int ld_hist, const int* __restrict__ pos_dev, int* flags) {
+    pdl_enter();
+    __shared__ double s_s[BM_MAX];
+    __shared__ int s_f[BM_MAX];  // j V + v
+    const int b = blockIdx.x, N = K * kk;
+    for (int i = threadIdx.x; i < N; i += BM_THREADS) {
+        const int j = i / kk, r = i % kk;
+        const long long row = (long long)b * K + j;
+        const float s = scores[row];
+        const bool over = done && done[row] != 0;
+        double c = -INFINITY;
+        int v = r;
+        if (over) {
+            if (s > -INFINITY) {
+                v = r == 0 ? eos : (r - 1 < eos ? r - 1 : r);
+                if (r == 0) c = (double)s;
+            }
+        } else {
+            const double l = lse[row];
+            if (r == 0 && (l != l || l == INFINITY)) atomicOr(&flags[FLAG_NONFINITE], 1);
+            if (isfinite(l) && s > -INFINITY) {
+                v = idx[row * kk + r];
+                c = (double)s + ((double)vals[row * kk + r] - l);
+            }
+        }
+        s_s[i] = c != c ? -INFINITY : c;
+        s_f[i] = j * V + v;
+    }
+    // a finished parent's flag, read before any output is written: outputs may be the inputs' arrays
+    uint32_t over_mask = 0;
+    if (done)
+        for (int j = 0; j < K; j++) over_mask |= (done[(long long)b * K + j] != 0 ? 1u : 0u) << j;
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += BM_THREADS) {
+        const double c = s_s[i];
+        const int f = s_f[i];
+        int rank = 0;
+        for (int o = 0; o < N; o++) rank += s_s[o] > c || (s_s[o] == c && s_f[o] < f);
+        if (rank >= n) continue;
+        const int j = f / V, v = f % V;
+        const long long at = (long long)b * n + rank;
+        parent[at] = j;
+        token[at] = v;
+        out_scores[at] = (float)c;
+        if (out_done) out_done[at] = ((over_mask >> j) & 1u) || v == eos;
+        if (tok_hist) {
+            tok_hist[at * ld_hist + *pos_dev] = v;
+            par_hist[at * ld_hist + *pos_dev] = j;
+        }
+    }
+}
+
+// Slot j of sequence b takes the bytes of slot parents[b, j].  A thread owns
+// one unit (1 to 16 bytes) of the row across all K slots: it reads every
+// moved slot's source before it writes any slot, so the move is in place
+// whatever the parents are (cycles, several children of one parent).
+template <typename U, int KM>
+__global__ void __launch_bounds__(256)
+k_beam_reorder(char* state, const int32_t* __restrict__ parents, int B, int K, long long row_bytes, long long first,
+               long long count, const int* __restrict__ pos_dev, long long pos_bytes, long long blocks_per_row,
+               int* flags) {
+    pdl_enter();
+    __shared__ int s_p[KM];
+    __shared__ int s_any;
+    const long long nb = blockIdx.x / blocks_per_row, blk = blockIdx.x % blocks_per_row;
+    if (pos_dev) count = (long long)*pos_dev * pos_bytes - first;
+    const long long u = (blk * 256 + threadIdx.x) * (long long)sizeof(U);
+    if (threadIdx.x == 0) s_any = 0;
+    __syncthreads();
+    if (threadIdx.x < KM) {
+        int p = threadIdx.x;
+        if (p < K) {
+            p = parents[(nb % B) * K + threadIdx.x];
+            if (p < 0 || p >= K) {
+                atomicOr(&flags[FLAG_BAD_TOKEN], 1);
+                p = threadIdx.x;
+            }
+        }
+        s_p[threadIdx.x] = p;
+        if (p != (int)threadIdx.x) s_any = 1;
+    }
+    __syncthreads();
+    if (!s_any || u >= count) return;
+    char* base = state + nb * K * row_bytes + first + u;
+    U v[KM];
+#pragma unroll
+    for (int j = 0; j < KM; j++)
+        if (s_p[j] != j) v[j] = *reinterpret_cast<const U*>(base + s_p[j] * row_bytes);
+#pragma unroll
+    for (int j = 0; j < KM; j++)
+        if (s_p[j] != j) *reinterpret_cast<U*>(base + j * row_bytes) = v[j];
+}
+
+// cache[b K + j][t][0 : 2C] = qkv[b T + t][C : 3C] for every beam j
+template <typename T>
+__global__ void k_kv_fill_beams(const T* __restrict__ qkv, T* __restrict__ cache, int B, int K, int Tn, int C,
+                                int maxT) {
+    const long long n = (long long)B * Tn * 2 * C;
+    for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+        const int c = (int)(i % (2 * C));
+        const long long r = i / (2 * C);
+        const int t = (int)(r % Tn), b = (int)(r / Tn);
+        const T v = qkv[r * 3 * C + C + c];
+        for (int j = 0; j < K; j++) cache[(((long long)b * K + j) * maxT + t) * 2 * C + c] = v;
+    }
+}
+
+// out[b, k, 0 : Tp] = prompt[b], then the tokens of hypothesis k of the last
+// step, found from its end: at position t slot j held tok[j][t], whose parent
+// slot at t - 1 is par[j][t].
+__global__ void k_beam_walk(const int32_t* __restrict__ prompt, const int32_t* __restrict__ tok,
+                            const int32_t* __restrict__ par, int32_t* __restrict__ out, int R, int K, int Tp, int T) {
+    const int r = blockIdx.x * blockDim.x + threadIdx.x;
+    if (r >= R) return;
+    const int b = r / K;
+    int j = r % K;
+    for (int t = T - 1; t >= Tp; t--) {
+        const long long at = ((long long)b * K + j) * T + t;
+        out[(long long)r * T + t] = tok[at];
+        j = par[at];
+    }
+    for (int t = 0; t < Tp; t++) out[(long long)r * T + t] = prompt[(long long)b * Tp + t];
+}
+
+template <typename U>
+bool reorder(const Launch& L, void* state, const int32_t* parents, int N, int B, int K, long long row_bytes,
+             long long first, long long count, const int* pos_dev, long long pos_bytes) {
+    const long long per = ((count + (long long)sizeof(U) - 1) / (long long)sizeof(U) + 255) / 256;
+    const long long grid = per * N * B;
+    if (grid > 0x7fffffffLL) return false;
+    L.count();
+#define RO(KM_)                                                                                                  \
+    launch_k(L, k_beam_reorder<U, KM_>, dim3((unsigned)grid), dim3(256), 0, (char*)state, parents, B, K, row_bytes, \
+             first, count, pos_dev, pos_bytes, per, L.flags)
+    if (K <= 4) RO(4);
+    else if (K <= 8) RO(8);
+    else if (K <= 16) RO(16);
+    else RO(32);
+#undef RO
+    return true;
+}
+
+}  // namespace
+
+size_t beam_select_scratch_bytes(int R, int V, int n) {
+    const size_t kk = (size_t)std::min(n, V);
+    return (size_t)R * 8 + (size_t)R * kk * 8;
+}
+
+bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long long ld, const float* scores,
+                        const int32_t* done, int32_t* parent, int32_t* token, float* out_scores, int32_t* out_done,
+                        int B, int K, int V, int n, int eos, void* scratch, int32_t* tok_hist, int32_t* par_hist,
+                        int ld_hist, const int* pos_dev) {
+    if (L.dry) return true;
+    const int R = B * K, kk = std::min(n, V);
+    if (K * kk > BM_MAX) return false;
+    double* lse = (double*)scratch;
+    float* vals = (float*)(lse + R);
+    int32_t* idx = (int32_t*)(vals + (size_t)R * kk);
+    if (!launch_top_rows(L, dtype, z, ld, R, V, kk, 1.0f, vals, idx, nullptr, lse, done)) return false;
+    L.count();
+    launch_k(L, k_beam_merge, dim3(B), dim3(BM_THREADS), 0, vals, idx, lse, scores, done, K, V, kk, n, eos, parent,
+             token, out_scores, out_done, tok_hist, par_hist, ld_hist, pos_dev, L.flags);
+    return true;
+}
+
+bool launch_beam_reorder(const Launch& L, void* state, const int32_t* parents, int N, int B, int K,
+                         long long row_bytes, long long first, long long count, const int* pos_dev,
+                         long long pos_bytes) {
+    if (L.dry || count <= 0) return true;
+    const unsigned long long all =
+        (unsigned long long)(uintptr_t)state | row_bytes | first | (pos_dev ? pos_bytes : count);
+    if (all % 16 == 0) return reorder<uint4>(L, state, parents, N, B, K, row_bytes, first, count, pos_dev, pos_bytes);
+    if (all % 4 == 0) return reorder<uint32_t>(L, state, parents, N, B, K, row_bytes, first, count, pos_dev, pos_bytes);
+    return reorder<uint8_t>(L, state, parents, N, B, K, row_bytes, first, count, pos_dev, pos_bytes);
+}
+
+void launch_kv_fill_beams(const Launch& L, bool bf16, const void* qkv, void* cache, int B, int K, int Tn, int C,
+                          int maxT) {
+    if (L.dry) return;
+    L.count();
+    const long long n = (long long)B * Tn * 2 * C;
+    const unsigned g = (unsigned)std::min<long long>((n + 255) / 256, 65535);
+    if (bf16)
+        k_kv_fill_beams<__nv_bfloat16><<<g, 256, 0, L.stream>>>((const __nv_bfloat16*)qkv, (__nv_bfloat16*)cache, B, K,
+                                                                Tn, C, maxT);
+    else
+        k_kv_fill_beams<float><<<g, 256, 0, L.stream>>>((const float*)qkv, (float*)cache, B, K, Tn, C, maxT);
+}
+
+void launch_beam_walk(const Launch& L, const int32_t* prompt, const int32_t* tok, const int32_t* par, int32_t* out,
+                      int B, int K, int Tp, int T) {
+    if (L.dry) return;
+    L.count();
+    k_beam_walk<<<(B * K + 63) / 64, 64, 0, L.stream>>>(prompt, tok, par, out, B * K, K, Tp, T);
+}
+
+}  // namespace tt

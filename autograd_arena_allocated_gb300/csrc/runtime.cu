@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -75,11 +76,13 @@ struct Record {
 // ------------------------------------------------------------------ profiling
 enum ProfKind : int {
     PK_GEMM_FWD, PK_GEMM_DX, PK_GEMM_DW, PK_COLSUM, PK_ATTN_FWD, PK_ATTN_BWD, PK_LN_FWD,
-    PK_LN_BWD, PK_XENT, PK_EMBED_FWD, PK_EMBED_BWD, PK_ADAMW, PK_CAST, PK_COUNT
+    PK_LN_BWD, PK_XENT, PK_EMBED_FWD, PK_EMBED_BWD, PK_ADAMW, PK_CAST, PK_TOP, PK_DISTILL,
+    PK_BEAM_SELECT, PK_BEAM_REORDER, PK_COUNT
 };
 static const char* const PROF_NAMES[PK_COUNT] = {
     "gemm_fwd", "gemm_dx", "gemm_dw", "colsum", "attn_fwd", "attn_bwd", "ln_fwd",
-    "ln_bwd", "xent", "embed_fwd", "embed_bwd", "adamw", "cast"};
+    "ln_bwd", "xent", "embed_fwd", "embed_bwd", "adamw", "cast", "top_logits", "distill",
+    "beam_select", "beam_reorder"};
 
 struct ProfEntry {
     int kind;
@@ -405,6 +408,37 @@ static void op_xent(tt_ctx* c, int z, const int32_t* targets, int V) {
     c->tensors[z].grad = c->tensors[z].data;
 }
 
+// A teacher's list per position, as tt_gpt2_step_distill gives it.
+struct Teacher {
+    const float* vals = nullptr;
+    const int32_t* idx = nullptr;
+    const float* lse = nullptr;
+    int k = 0;
+    float alpha = 1.0f, tau = 1.0f;
+};
+
+// Distillation in the place of the cross entropy: the logits are replaced by
+// their gradient in the same way.
+static bool op_distill(tt_ctx* c, int z, const int32_t* targets, int V, const Teacher& t) {
+    const tt_gpt2_config& m = c->cfg;
+    const int M = (int)c->tensors[z].rows, ld = (int)c->tensors[z].cols;
+    c->row_loss_dev = (float*)arena_alloc(c, (size_t)M * 4);
+    c->loss_dev = (float*)arena_alloc(c, 4);
+    ProfScope ps(c, PK_DISTILL, 0.0, 2.0 * M * ld * esize(m.dtype) + 8.0 * M * t.k);
+    bool ok = true;
+    if (!c->oom)
+        ok = launch_distill(launch_of(c), m.dtype, c->tensors[z].data, c->tensors[z].data, t.vals, t.idx, t.lse,
+                            targets, c->row_loss_dev, c->loss_dev, M, V, ld, t.k, t.alpha, t.tau, 1.0f / (float)M,
+                            c->loss_scale_dev);
+    Record r;
+    r.kind = R_XENT;
+    r.in = z; r.M = M; r.N = V; r.idx = targets;
+    c->tape.push_back(r);
+    add_consumer(c, z, (int)c->tape.size() - 1);
+    c->tensors[z].grad = c->tensors[z].data;
+    return ok;
+}
+
 // ------------------------------------------------------------------ backward
 static bool first_write(tt_ctx* c, const float* p) {
     return c->grad_written.insert(p).second;
@@ -676,144 +710,155 @@ static int gpt2_forward(tt_ctx* c, const void* params, float* grads, const int32
 }
 
 static tt_status gpt2_forward_backward(tt_ctx* c, const void* params, float* grads,
-                                       const int32_t* tok, const int32_t* tgt, int B, int T) {
+                                       const int32_t* tok, const int32_t* tgt, int B, int T,
+                                       const Teacher* teacher = nullptr) {
     int z = gpt2_forward(c, params, grads, tok, B, T);
-    op_xent(c, z, tgt, c->cfg.V);
+    if (!teacher) op_xent(c, z, tgt, c->cfg.V);
+    else if (!op_distill(c, z, tgt, c->cfg.V, *teacher)) return fail(c, TT_ERR_CUDA, "distillation: launch failed");
     if (c->oom) return TT_ERR_ARENA_OOM;
     return tape_backward(c);
 }
 
-// ------------------------------------------------------------------ greedy generation
+// ------------------------------------------------------------------ generation with a cache
 // Prefill: the forward over the prompt, whose qkv tensors fill the key/value
-// cache, and the greedy token after the prompt.  Then one decode step per new
+// cache, and the choice after the prompt.  Then one decode step per new
 // token: the newest token through every layer (its key and value appended to
-// the cache, its query against keys 0..pos) and the greedy choice from its
-// logits.  Tokens live in a device buffer [B, Tp + n_new]; nothing returns to
+// the cache, its query against keys 0..pos) and the choice from its
+// logits.  Tokens live in a device buffer; nothing returns to
 // the host until the end.  The decode kernels read the position from device
 // memory and the step advances it, so every step launches the same kernels
 // with the same arguments: the first step runs eagerly and the rest replay it
 // as a CUDA graph.
-static tt_status gpt2_generate(tt_ctx* c, const void* params, const int32_t* prompt_dev, int B, int Tp, int n_new,
-                               int32_t* tokbuf) {
+
+// Device buffers of a decode step over R rows: the cache, per layer [R, maxT,
+// 2C], and one set of tensors that every layer and step reuses.
+struct DecodeBufs {
+    int R = 0, max_keys = 0;  // keys seen by the last decode step
+    size_t layer_cache = 0;
+    char* cache = nullptr;
+    int *pos_dev = nullptr, *counters = nullptr;
+    float* part = nullptr;
+    void *xa, *xb, *h, *qkv, *att, *x1, *u, *g, *zl;
+    float *mean, *rstd;
+};
+
+static DecodeBufs decode_bufs(tt_ctx* c, int R, int max_keys) {
+    const tt_gpt2_config& m = c->cfg;
+    const size_t es = esize(m.dtype);
+    const int C = m.C;
+    DecodeBufs d;
+    d.R = R;
+    d.max_keys = max_keys;
+    d.layer_cache = (size_t)R * m.maxT * 2 * C * es;
+    d.cache = (char*)arena_alloc(c, d.layer_cache * (size_t)m.L);
+    d.pos_dev = (int*)arena_alloc(c, sizeof(int));
+    d.counters = (int*)arena_alloc(c, (size_t)R * m.H * sizeof(int));
+    d.part = (float*)arena_alloc(c, decode_attn_scratch_floats(R, m.H, max_keys) * sizeof(float));
+    auto buf = [&](int cols) { return arena_alloc(c, (size_t)R * cols * es); };
+    d.xa = buf(C);
+    d.xb = buf(C);
+    d.h = buf(C);
+    d.qkv = buf(3 * C);
+    d.att = buf(C);
+    d.x1 = buf(C);
+    d.u = buf(4 * C);
+    d.g = buf(4 * C);
+    d.zl = buf(padded_vocab(m.V));
+    d.mean = (float*)arena_alloc(c, (size_t)R * 4);
+    d.rstd = (float*)arena_alloc(c, (size_t)R * 4);
+    return d;
+}
+
+static tt_status decode_start(tt_ctx* c, const DecodeBufs& d, int pos) {
+    Launch L = launch_of(c);
+    if (!L.dry && cudaMemsetAsync(d.counters, 0, (size_t)d.R * c->cfg.H * sizeof(int), c->stream) != cudaSuccess)
+        return fail(c, TT_ERR_CUDA, "generate: counter reset failed");
+    launch_set_int(L, d.pos_dev, pos);
+    return TT_OK;
+}
+
+// One decode step up to the final LayerNorm: the token of each row at
+// tok[row * ld_tok + *pos_dev] through every layer into d.h.
+static tt_status decode_hidden(tt_ctx* c, const Launch& S, const void* params, const DecodeBufs& d, const int32_t* tok,
+                               int ld_tok) {
     const tt_gpt2_config& m = c->cfg;
     const bool bf = m.dtype == TT_BF16;
     const size_t es = esize(m.dtype);
     const Offsets o = offsets_of(&m);
     auto P = [&](size_t off) -> const void* { return (const char*)params + off * es; };
-    const int C = m.C, Vp = padded_vocab(m.V), Ttot = Tp + n_new;
-    const int max_keys = Ttot - 1;  // keys seen by the last decode step
-    Launch L = launch_of(c);
-    // the cache: per layer [B, maxT, 2C]
-    const size_t layer_cache = (size_t)B * m.maxT * 2 * C * es;
-    char* cache = (char*)arena_alloc(c, layer_cache * (size_t)m.L);
-    int* pos_dev = (int*)arena_alloc(c, sizeof(int));
-    int* counters = (int*)arena_alloc(c, (size_t)B * m.H * sizeof(int));
-    float* part = (float*)arena_alloc(c, decode_attn_scratch_floats(B, m.H, max_keys) * sizeof(float));
-    const int nct = skinny_pick_ctas(m.V);
-    auto* keys = (unsigned long long*)arena_alloc(c, (size_t)B * nct * sizeof(unsigned long long));
-    // one set of decode-step tensors, reused by every layer and step
-    auto buf = [&](int cols) { return arena_alloc(c, (size_t)B * cols * es); };
-    void* xa = buf(C);
-    void* xb = buf(C);
-    void* h = buf(C);
-    void* qkv = buf(3 * C);
-    void* att = buf(C);
-    void* x1 = buf(C);
-    void* u = buf(4 * C);
-    void* g = buf(4 * C);
-    void* zl = buf(Vp);
-    float* mean = (float*)arena_alloc(c, (size_t)B * 4);
-    float* rstd = (float*)arena_alloc(c, (size_t)B * 4);
-    // prefill
-    std::vector<int> qkv_ids;
-    int z = gpt2_forward(c, params, nullptr, prompt_dev, B, Tp, &qkv_ids);
-    if (c->oom) return TT_ERR_ARENA_OOM;
-    for (int l = 0; l < m.L; l++)
-        if (!launch_kv_fill(L, bf, c->tensors[qkv_ids[l]].data, cache + layer_cache * l, B, Tp, C, 0, m.maxT))
-            return fail(c, TT_ERR_ARG, "generate: sequence longer than maxT");
-    launch_argmax(L, bf, (const char*)c->tensors[z].data + (size_t)(Tp - 1) * Vp * es, (long long)Tp * Vp, B, m.V,
-                  tokbuf, Ttot, Tp, nullptr);
-    const int n_steps = n_new - 1;
-    if (n_steps <= 0) return TT_OK;
-    if (!L.dry && cudaMemsetAsync(counters, 0, (size_t)B * m.H * sizeof(int), c->stream) != cudaSuccess)
-        return fail(c, TT_ERR_CUDA, "generate: counter reset failed");
-    launch_set_int(L, pos_dev, Tp);
-
-    // one decode step: the token at *pos_dev gives the one at *pos_dev + 1
-    const size_t mark = c->off;
-    auto step = [&]() -> tt_status {
-        c->off = mark;
-        Launch S = launch_of(c);
-        S.pdl = true;
-        auto linear = [&](const void* in, int K, const void* W, const void* bias, int N, void* out, const void* res,
-                          void* pre) -> bool {
-            // a few rows: the weight-streaming skinny GEMM
-            if (launch_gemm_skinny(S, bf, in, W, bias, res, out, pre, B, N, K, N, N, pre != nullptr, nullptr))
-                return true;
-            GemmArgs ga;
-            ga.A = in; ga.lda = K; ga.a_kmajor = true;
-            ga.B = W; ga.ldb = K; ga.b_kmajor = true;
-            ga.M = B; ga.N = N; ga.K = K;
-            ga.in_bf16 = bf;
-            ga.D = out; ga.ldd = N; ga.d_f32 = !bf;
-            ga.epi = pre ? EPI_GELU : EPI_STORE;
-            ga.bias = bias;
-            ga.residual = res;
-            ga.aux = pre;
-            return run_gemm(c, ga, PK_GEMM_FWD);
-        };
-        // LayerNorm then a linear layer: one launch when the skinny GEMM takes the LayerNorm
-        auto ln_linear = [&](const void* xin, const void* lw, const void* lb, const void* W, const void* bias, int N,
-                             void* out, void* pre) -> bool {
-            if (bf && launch_gemm_skinny(S, bf, xin, W, bias, nullptr, out, pre, B, N, C, N, N, pre != nullptr,
-                                         nullptr, lw, lb))
-                return true;
-            launch_layernorm_fwd(S, bf, xin, lw, lb, h, mean, rstd, B, C);
-            return linear(h, C, W, bias, N, out, nullptr, pre);
-        };
-        void* x = xa;
-        void* x2 = xb;
-        launch_embed_at(S, bf, P(o.wte), P(o.wpe), tokbuf, Ttot, pos_dev, x, B, C, m.V);
-        for (int l = 0; l < m.L; l++) {
-            const size_t base = o.layers + (size_t)l * o.per_layer;
-            auto PL = [&](int i) { return P(base + o.sub[i]); };
-            if (!ln_linear(x, PL(0), PL(1), PL(2), PL(3), 3 * C, qkv, nullptr)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
-            if (!launch_decode_attn(S, bf, qkv, cache + layer_cache * l, att, B, m.H, C, pos_dev, max_keys, m.maxT,
-                                    part, counters))
-                return fail(c, TT_ERR_ARG, "generate: attention shape not supported");
-            if (!linear(att, C, PL(4), PL(5), C, x1, x, nullptr)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
-            if (!ln_linear(x1, PL(6), PL(7), PL(8), PL(9), 4 * C, g, u)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
-            if (!linear(g, 4 * C, PL(10), PL(11), C, x2, x1, nullptr)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
-            std::swap(x, x2);
-        }
-        // final LayerNorm (its own launch: folded into the LM head it would be
-        // redone by each of that GEMM's thousands of CTAs), then the tied LM head
-        // over the V real rows of wte, which also advances the position
-        launch_layernorm_fwd(S, bf, x, P(o.lnfw), P(o.lnfb), h, mean, rstd, B, C);
-        if (bf && launch_gemm_skinny_pick(S, h, P(o.wte), B, m.V, C, keys, pos_dev)) {
-            launch_pick(S, keys, nct, B, tokbuf, Ttot, pos_dev);
-            return TT_OK;
-        }
-        if (!launch_gemm_skinny(S, bf, h, P(o.wte), nullptr, nullptr, zl, nullptr, B, m.V, C, Vp, m.V, false,
-                                pos_dev)) {
-            GemmArgs ga;
-            ga.A = h; ga.lda = C; ga.a_kmajor = true;
-            ga.B = P(o.wte); ga.ldb = C; ga.b_kmajor = true;
-            ga.M = B; ga.N = Vp; ga.K = C;
-            ga.b_rows = m.V;
-            ga.in_bf16 = bf;
-            ga.D = zl; ga.ldd = Vp; ga.d_f32 = !bf;
-            if (!run_gemm(c, ga, PK_GEMM_FWD)) return fail(c, TT_ERR_CUDA, "generate: LM head GEMM");
-            launch_add_int(S, pos_dev, 1);
-        }
-        launch_argmax(S, bf, zl, Vp, B, m.V, tokbuf, Ttot, 0, pos_dev);
-        return TT_OK;
+    const int C = m.C, B = d.R;
+    auto linear = [&](const void* in, int K, const void* W, const void* bias, int N, void* out, const void* res,
+                      void* pre) -> bool {
+        // a few rows: the weight-streaming skinny GEMM
+        if (launch_gemm_skinny(S, bf, in, W, bias, res, out, pre, B, N, K, N, N, pre != nullptr, nullptr))
+            return true;
+        GemmArgs ga;
+        ga.A = in; ga.lda = K; ga.a_kmajor = true;
+        ga.B = W; ga.ldb = K; ga.b_kmajor = true;
+        ga.M = B; ga.N = N; ga.K = K;
+        ga.in_bf16 = bf;
+        ga.D = out; ga.ldd = N; ga.d_f32 = !bf;
+        ga.epi = pre ? EPI_GELU : EPI_STORE;
+        ga.bias = bias;
+        ga.residual = res;
+        ga.aux = pre;
+        return run_gemm(c, ga, PK_GEMM_FWD);
     };
+    // LayerNorm then a linear layer: one launch when the skinny GEMM takes the LayerNorm
+    auto ln_linear = [&](const void* xin, const void* lw, const void* lb, const void* W, const void* bias, int N,
+                         void* out, void* pre) -> bool {
+        if (bf && launch_gemm_skinny(S, bf, xin, W, bias, nullptr, out, pre, B, N, C, N, N, pre != nullptr, nullptr,
+                                     lw, lb))
+            return true;
+        launch_layernorm_fwd(S, bf, xin, lw, lb, d.h, d.mean, d.rstd, B, C);
+        return linear(d.h, C, W, bias, N, out, nullptr, pre);
+    };
+    void* x = d.xa;
+    void* x2 = d.xb;
+    launch_embed_at(S, bf, P(o.wte), P(o.wpe), tok, ld_tok, d.pos_dev, x, B, C, m.V);
+    for (int l = 0; l < m.L; l++) {
+        const size_t base = o.layers + (size_t)l * o.per_layer;
+        auto PL = [&](int i) { return P(base + o.sub[i]); };
+        if (!ln_linear(x, PL(0), PL(1), PL(2), PL(3), 3 * C, d.qkv, nullptr)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
+        if (!launch_decode_attn(S, bf, d.qkv, d.cache + d.layer_cache * l, d.att, B, m.H, C, d.pos_dev, d.max_keys,
+                                m.maxT, d.part, d.counters))
+            return fail(c, TT_ERR_ARG, "generate: attention shape not supported");
+        if (!linear(d.att, C, PL(4), PL(5), C, d.x1, x, nullptr)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
+        if (!ln_linear(d.x1, PL(6), PL(7), PL(8), PL(9), 4 * C, d.g, d.u)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
+        if (!linear(d.g, 4 * C, PL(10), PL(11), C, x2, d.x1, nullptr)) return fail(c, TT_ERR_CUDA, "generate: GEMM");
+        std::swap(x, x2);
+    }
+    // final LayerNorm (its own launch: folded into the LM head it would be
+    // redone by each of that GEMM's thousands of CTAs)
+    launch_layernorm_fwd(S, bf, x, P(o.lnfw), P(o.lnfb), d.h, d.mean, d.rstd, B, C);
+    return TT_OK;
+}
 
+// The tied LM head over the V real rows of wte into d.zl [R, Vp]; advances the position.
+static tt_status decode_logits(tt_ctx* c, const Launch& S, const void* params, const DecodeBufs& d) {
+    const tt_gpt2_config& m = c->cfg;
+    const bool bf = m.dtype == TT_BF16;
+    const int C = m.C, Vp = padded_vocab(m.V);
+    if (launch_gemm_skinny(S, bf, d.h, params, nullptr, nullptr, d.zl, nullptr, d.R, m.V, C, Vp, m.V, false, d.pos_dev))
+        return TT_OK;
+    GemmArgs ga;
+    ga.A = d.h; ga.lda = C; ga.a_kmajor = true;
+    ga.B = params; ga.ldb = C; ga.b_kmajor = true;
+    ga.M = d.R; ga.N = Vp; ga.K = C;
+    ga.b_rows = m.V;
+    ga.in_bf16 = bf;
+    ga.D = d.zl; ga.ldd = Vp; ga.d_f32 = !bf;
+    if (!run_gemm(c, ga, PK_GEMM_FWD)) return fail(c, TT_ERR_CUDA, "generate: LM head GEMM");
+    launch_add_int(S, d.pos_dev, 1);
+    return TT_OK;
+}
+
+// Runs `step` n_steps times: once eagerly, then captured once (its kernels go
+// to a private stream while it is recorded) and replayed for the remaining
+// positions; eagerly throughout if the capture fails.
+template <typename F> static tt_status run_decode_steps(tt_ctx* c, int n_steps, F&& step) {
     tt_status st = step();
-    if (st != TT_OK || c->oom || L.dry || n_steps == 1) return c->oom ? TT_ERR_ARENA_OOM : st;
-    // capture the step once (its kernels go to a private stream while it is
-    // recorded) and replay it for the remaining positions
+    if (st != TT_OK || c->oom || c->dry || n_steps == 1) return c->oom ? TT_ERR_ARENA_OOM : st;
     int done = 1;
     cudaStream_t cap = nullptr;
     cudaGraph_t graph = nullptr;
@@ -855,6 +900,133 @@ static tt_status gpt2_generate(tt_ctx* c, const void* params, const int32_t* pro
         if (st != TT_OK) return st;
     }
     return TT_OK;
+}
+
+// Greedy choice: the first index of the largest logit.
+static tt_status gpt2_generate(tt_ctx* c, const void* params, const int32_t* prompt_dev, int B, int Tp, int n_new,
+                               int32_t* tokbuf) {
+    const tt_gpt2_config& m = c->cfg;
+    const bool bf = m.dtype == TT_BF16;
+    const size_t es = esize(m.dtype);
+    const int C = m.C, Vp = padded_vocab(m.V), Ttot = Tp + n_new;
+    Launch L = launch_of(c);
+    const DecodeBufs d = decode_bufs(c, B, Ttot - 1);
+    const int nct = skinny_pick_ctas(m.V);
+    auto* keys = (unsigned long long*)arena_alloc(c, (size_t)B * nct * sizeof(unsigned long long));
+    // prefill
+    std::vector<int> qkv_ids;
+    int z = gpt2_forward(c, params, nullptr, prompt_dev, B, Tp, &qkv_ids);
+    if (c->oom) return TT_ERR_ARENA_OOM;
+    for (int l = 0; l < m.L; l++)
+        if (!launch_kv_fill(L, bf, c->tensors[qkv_ids[l]].data, d.cache + d.layer_cache * l, B, Tp, C, 0, m.maxT))
+            return fail(c, TT_ERR_ARG, "generate: sequence longer than maxT");
+    launch_argmax(L, bf, (const char*)c->tensors[z].data + (size_t)(Tp - 1) * Vp * es, (long long)Tp * Vp, B, m.V,
+                  tokbuf, Ttot, Tp, nullptr);
+    const int n_steps = n_new - 1;
+    if (n_steps <= 0) return TT_OK;
+    tt_status st = decode_start(c, d, Tp);
+    if (st != TT_OK) return st;
+
+    // one decode step: the token at *pos_dev gives the one at *pos_dev + 1
+    const size_t mark = c->off;
+    return run_decode_steps(c, n_steps, [&]() -> tt_status {
+        c->off = mark;
+        Launch S = launch_of(c);
+        S.pdl = true;
+        tt_status s = decode_hidden(c, S, params, d, tokbuf, Ttot);
+        if (s != TT_OK) return s;
+        // the tied LM head with the greedy choice folded in, which also advances the position
+        if (bf && launch_gemm_skinny_pick(S, d.h, params, B, m.V, C, keys, d.pos_dev)) {
+            launch_pick(S, keys, nct, B, tokbuf, Ttot, d.pos_dev);
+            return TT_OK;
+        }
+        s = decode_logits(c, S, params, d);
+        if (s != TT_OK) return s;
+        launch_argmax(S, bf, d.zl, Vp, B, m.V, tokbuf, Ttot, 0, d.pos_dev);
+        return TT_OK;
+    });
+}
+
+// Beam search over K hypotheses per sequence, which share the prompt's
+// prefill: its keys and values are copied to every beam's cache rows, and
+// reordering touches the generated positions only.  A step's choice goes to
+// per-position tables of tokens and parent slots; the K sequences are read
+// back along the parents at the end.
+static tt_status gpt2_generate_beam(tt_ctx* c, const void* params, const int32_t* prompt_dev, int B, int Tp, int n_new,
+                                    int K, int eos, int32_t* out, float* scores) {
+    const tt_gpt2_config& m = c->cfg;
+    const bool bf = m.dtype == TT_BF16;
+    const size_t es = esize(m.dtype);
+    const int C = m.C, Vp = padded_vocab(m.V), Ttot = Tp + n_new, R = B * K;
+    Launch L = launch_of(c);
+    const DecodeBufs d = decode_bufs(c, R, Ttot - 1);
+    int32_t* tok = (int32_t*)arena_alloc(c, (size_t)R * Ttot * 4);
+    int32_t* par = (int32_t*)arena_alloc(c, (size_t)R * Ttot * 4);
+    int32_t* parent = (int32_t*)arena_alloc(c, (size_t)R * 4);
+    int32_t* token = (int32_t*)arena_alloc(c, (size_t)R * 4);
+    int32_t* done = (int32_t*)arena_alloc(c, (size_t)R * 4);
+    float* zero = (float*)arena_alloc(c, (size_t)B * 4);
+    void* scratch = arena_alloc(c, beam_select_scratch_bytes(R, m.V, K));
+    std::vector<int> qkv_ids;
+    int z = gpt2_forward(c, params, nullptr, prompt_dev, B, Tp, &qkv_ids);
+    if (c->oom) return TT_ERR_ARENA_OOM;
+    for (int l = 0; l < m.L; l++)
+        launch_kv_fill_beams(L, bf, c->tensors[qkv_ids[l]].data, d.cache + d.layer_cache * l, B, K, Tp, C, m.maxT);
+    if (!L.dry && cudaMemsetAsync(zero, 0, (size_t)B * 4, c->stream) != cudaSuccess)
+        return fail(c, TT_ERR_CUDA, "generate_beam: score reset failed");
+    tt_status st = decode_start(c, d, Tp);
+    if (st != TT_OK) return st;
+    // the K best first tokens of the one hypothesis that each prompt is
+    if (!launch_beam_select(L, m.dtype, (const char*)c->tensors[z].data + (size_t)(Tp - 1) * Vp * es,
+                            (long long)Tp * Vp, zero, nullptr, parent, token, scores, done, B, 1, m.V, K, eos, scratch,
+                            tok, par, Ttot, d.pos_dev))
+        return fail(c, TT_ERR_CUDA, "generate_beam: selection");
+    const int n_steps = n_new - 1;
+    if (n_steps > 0) {
+        const size_t mark = c->off;
+        const long long pos_bytes = (long long)2 * C * es;
+        st = run_decode_steps(c, n_steps, [&]() -> tt_status {
+            c->off = mark;
+            Launch S = launch_of(c);
+            S.pdl = true;
+            tt_status s = decode_hidden(c, S, params, d, tok, Ttot);
+            if (s == TT_OK) s = decode_logits(c, S, params, d);
+            if (s != TT_OK) return s;
+            if (!launch_beam_select(S, m.dtype, d.zl, Vp, scores, eos >= 0 ? done : nullptr, parent, token, scores,
+                                    done, B, K, m.V, K, eos, scratch, tok, par, Ttot, d.pos_dev))
+                return fail(c, TT_ERR_CUDA, "generate_beam: selection");
+            if (!launch_beam_reorder(S, d.cache, parent, m.L, B, K, (long long)m.maxT * pos_bytes, Tp * pos_bytes,
+                                     (n_new - 1) * pos_bytes, d.pos_dev, pos_bytes))
+                return fail(c, TT_ERR_CUDA, "generate_beam: reordering");
+            return TT_OK;
+        });
+        if (st != TT_OK) return st;
+    }
+    launch_beam_walk(L, prompt_dev, tok, par, out, B, K, Tp, Ttot);
+    return TT_OK;
+}
+
+static tt_status op_epilogue(tt_ctx* c, const char* what) {
+    if (c->oom) { c->oom = false; return fail(c, TT_ERR_ARENA_OOM, "%s: scratch does not fit", what); }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(c, TT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return TT_OK;
+}
+
+// What the list operators refuse, as a text; NULL when the arguments are fine.
+static const char* list_refusal(tt_dtype dtype, int V, int k, float tau) {
+    if (k < 1 || k > TT_TOP_MAX || k > V) return "k must be 1 .. min(V, TT_TOP_MAX)";
+    if (!(tau > 0.0f) || !std::isfinite(tau) || !std::isfinite(1.0f / tau)) return "tau must be positive and finite";
+    if (!head_row_ok(dtype, V)) return "V is larger than a row may be";
+    return nullptr;
+}
+
+static const char* distill_refusal(tt_dtype dtype, const float* t_vals, const int32_t* t_idx, const int32_t* targets,
+                                   int V, int k, float alpha, float tau) {
+    if (!t_vals || !t_idx) return "NULL teacher list";
+    if (!(alpha >= 0.0f && alpha <= 1.0f)) return "alpha must be in [0, 1]";
+    if (alpha < 1.0f && !targets) return "alpha < 1 needs targets";
+    return list_refusal(dtype, V, k, tau);
 }
 
 static void begin_step(tt_ctx* c) {
@@ -1096,13 +1268,15 @@ tt_status tt_gpt2_step(tt_ctx* c, const void* params, float* grads, const int32_
     return tt_gpt2_step_ex(c, params, grads, tokens, targets, B, T, 0, nullptr, loss);
 }
 
-tt_status tt_gpt2_step_ex(tt_ctx* c, const void* params, float* grads, const int32_t* tokens,
-                          const int32_t* targets, int B, int T, int flags, const float* loss_scale, float* loss) {
+// The step with the cross entropy, or with the distillation loss of `teacher`
+// (targets may then be NULL).
+static tt_status step_with(tt_ctx* c, const void* params, float* grads, const int32_t* tokens, const int32_t* targets,
+                           const Teacher* teacher, int B, int T, int flags, const float* loss_scale, float* loss) {
     if (!c) return TT_ERR_ARG;
     if (!live(c)) return TT_ERR_STALE;
     if (c->capturing) return fail(c, TT_ERR_STATE, "GPT-2 calls cannot be recorded");
     if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
-    if (!params || !grads || !tokens || !targets)
+    if (!params || !grads || !tokens || (!targets && !teacher))
         return fail(c, TT_ERR_ARG, "NULL parameter, gradient or token pointer");
     if (B <= 0 || T <= 0 || T > c->cfg.maxT)
         return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
@@ -1126,7 +1300,7 @@ tt_status tt_gpt2_step_ex(tt_ctx* c, const void* params, float* grads, const int
             return fail(c, TT_ERR_CUDA, "token copy failed");
         tok = st_tok;
     }
-    if (is_host_pointer(targets)) {
+    if (targets && is_host_pointer(targets)) {
         if (cudaMemcpyAsync(st_tgt, targets, M * 4, cudaMemcpyHostToDevice, c->stream) != cudaSuccess)
             return fail(c, TT_ERR_CUDA, "target copy failed");
         tgt = st_tgt;
@@ -1134,7 +1308,7 @@ tt_status tt_gpt2_step_ex(tt_ctx* c, const void* params, float* grads, const int
     if (flags & ~TT_STEP_ACCUMULATE) return fail(c, TT_ERR_ARG, "unknown step flags 0x%x", (unsigned)flags);
     c->accum_params = (flags & TT_STEP_ACCUMULATE) != 0;
     c->loss_scale_dev = loss_scale;
-    tt_status s = gpt2_forward_backward(c, params, grads, tok, tgt, B, T);
+    tt_status s = gpt2_forward_backward(c, params, grads, tok, tgt, B, T, teacher);
     c->accum_params = false;
     c->loss_scale_dev = nullptr;
     if (s != TT_OK) {
@@ -1149,6 +1323,26 @@ tt_status tt_gpt2_step_ex(tt_ctx* c, const void* params, float* grads, const int
         return tt_ctx_sync(c);
     }
     return TT_OK;
+}
+
+tt_status tt_gpt2_step_ex(tt_ctx* c, const void* params, float* grads, const int32_t* tokens,
+                          const int32_t* targets, int B, int T, int flags, const float* loss_scale, float* loss) {
+    return step_with(c, params, grads, tokens, targets, nullptr, B, T, flags, loss_scale, loss);
+}
+
+tt_status tt_gpt2_step_distill(tt_ctx* c, const void* params, float* grads, const int32_t* tokens,
+                               const int32_t* targets, const float* t_vals, const int32_t* t_idx, const float* t_lse,
+                               int k, float alpha, float tau, int B, int T, int flags, const float* loss_scale,
+                               float* loss) {
+    if (!c) return TT_ERR_ARG;
+    if (!live(c)) return TT_ERR_STALE;
+    Teacher t;
+    t.vals = t_vals; t.idx = t_idx; t.lse = t_lse; t.k = k; t.alpha = alpha; t.tau = tau;
+    if (c->has_model) {
+        const char* why = distill_refusal(c->cfg.dtype, t_vals, t_idx, targets, c->cfg.V, k, alpha, tau);
+        if (why) return fail(c, TT_ERR_ARG, "step_distill: %s", why);
+    }
+    return step_with(c, params, grads, tokens, targets, &t, B, T, flags, loss_scale, loss);
 }
 
 // Token inputs may be host or device buffers; host ones are staged into the arena.
@@ -1262,6 +1456,113 @@ tt_status tt_gpt2_generate(tt_ctx* c, const void* params, const int32_t* prompt,
     return tt_ctx_sync(c);
 }
 
+tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* tokens, int B, int T, int k, float tau,
+                             float* vals, int32_t* idx, float* lse) {
+    if (!c) return TT_ERR_ARG;
+    if (!live(c)) return TT_ERR_STALE;
+    if (c->capturing) return fail(c, TT_ERR_STATE, "GPT-2 calls cannot be recorded");
+    if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
+    if (!params || !tokens || !vals || !idx) return fail(c, TT_ERR_ARG, "NULL parameter, token or list pointer");
+    if (B <= 0 || T <= 0 || T > c->cfg.maxT)
+        return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
+    const tt_gpt2_config& m = c->cfg;
+    const char* why = list_refusal(m.dtype, m.V, k, tau);
+    if (why) return fail(c, TT_ERR_ARG, "top_logits: %s", why);
+    {
+        const size_t need = tt_gpt2_arena_bytes(&c->cfg, B, T);
+        const size_t at = (c->off + ARENA_ALIGN - 1) & ~(ARENA_ALIGN - 1);
+        if (need == 0 || at + need > c->cap)
+            return fail(c, TT_ERR_ARENA_OOM, "arena too small: the forward needs %zu bytes, %zu free", need,
+                        c->cap > at ? c->cap - at : (size_t)0);
+    }
+    begin_step(c);
+    c->loss_dev = c->row_loss_dev = nullptr;  // no loss in this pass
+    tt_status st;
+    const int32_t* tok = stage_tokens(c, tokens, (size_t)B * T, &st);
+    if (st != TT_OK) return st;
+    const int z = gpt2_forward(c, params, nullptr, tok, B, T);
+    if (c->oom) return fail(c, TT_ERR_ARENA_OOM, "arena exhausted during the forward");
+    const int M = B * T, ld = (int)c->tensors[z].cols;
+    {
+        ProfScope ps(c, PK_TOP, 0.0, (double)M * m.V * esize(m.dtype) + 8.0 * M * k);
+        if (!launch_top_rows(launch_of(c), m.dtype, c->tensors[z].data, ld, M, m.V, k, tau, vals, idx, lse, nullptr,
+                             nullptr))
+            return fail(c, TT_ERR_CUDA, "top_logits: launch failed");
+    }
+    return op_epilogue(c, "top_logits");
+}
+
+size_t tt_gpt2_generate_beam_arena_bytes(const tt_gpt2_config* m, int B, int T_prompt, int n_new, int K) {
+    if (!cfg_ok(m) || m->dtype == TT_FP16 || B <= 0 || T_prompt <= 0 || n_new < 0 || T_prompt > m->maxT ||
+        n_new > m->maxT - T_prompt || K < 1 || K > TT_BEAM_MAX || K > m->V || B > INT32_MAX / K / m->maxT)
+        return 0;
+    tt_ctx c;
+    c.cap = (size_t)-1 / 2;
+    c.cfg = *m;
+    c.has_model = true;
+    c.dry = true;
+    int sms = 148, dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        c.num_sms = sms;
+    else
+        cudaGetLastError();
+    arena_alloc(&c, (size_t)B * T_prompt * 4);                  // staged prompt
+    arena_alloc(&c, (size_t)B * K * (T_prompt + n_new) * 4);    // token buffer
+    arena_alloc(&c, (size_t)B * K * 4);                         // scores
+    if (n_new > 0)
+        gpt2_generate_beam(&c, (const void*)(uintptr_t)0x1000, (const int32_t*)(uintptr_t)0x1000, B, T_prompt, n_new, K,
+                           -1, (int32_t*)(uintptr_t)0x1000, (float*)(uintptr_t)0x1000);
+    c.magic = TT_DEAD;
+    return c.high - ARENA_HEADER;
+}
+
+tt_status tt_gpt2_generate_beam(tt_ctx* c, const void* params, const int32_t* prompt, int B, int T_prompt, int n_new,
+                                int K, int eos, int32_t* out, float* scores) {
+    if (!c) return TT_ERR_ARG;
+    if (!live(c)) return TT_ERR_STALE;
+    if (c->capturing) return fail(c, TT_ERR_STATE, "GPT-2 calls cannot be recorded");
+    if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
+    if (c->cfg.dtype == TT_FP16) return fail(c, TT_ERR_ARG, "generation takes a TT_FP32 or TT_BF16 model");
+    if (!params || !prompt || !out || !scores) return fail(c, TT_ERR_ARG, "NULL parameter, prompt or output pointer");
+    const size_t need = tt_gpt2_generate_beam_arena_bytes(&c->cfg, B, T_prompt, n_new, K);
+    if (need == 0)
+        return fail(c, TT_ERR_ARG, "bad generation shape B=%d prompt=%d new=%d beams=%d (maxT=%d)", B, T_prompt, n_new,
+                    K, c->cfg.maxT);
+    if (eos < -1 || eos >= c->cfg.V) return fail(c, TT_ERR_ARG, "end token %d outside the vocabulary", eos);
+    const char* why = list_refusal(c->cfg.dtype, c->cfg.V, K, 1.0f);
+    if (why) return fail(c, TT_ERR_ARG, "generate_beam: %s", why);
+    {
+        const size_t at = (c->off + ARENA_ALIGN - 1) & ~(ARENA_ALIGN - 1);
+        if (at + need > c->cap)
+            return fail(c, TT_ERR_ARENA_OOM, "arena too small: generation needs %zu bytes, %zu free", need,
+                        c->cap > at ? c->cap - at : (size_t)0);
+    }
+    begin_step(c);
+    c->loss_dev = c->row_loss_dev = nullptr;  // no loss in this pass
+    const int Ttot = T_prompt + n_new, R = B * K;
+    tt_status st;
+    const int32_t* pr = stage_tokens(c, prompt, (size_t)B * T_prompt, &st);
+    if (st != TT_OK) return st;
+    int32_t* tokbuf = (int32_t*)arena_alloc(c, (size_t)R * Ttot * 4);
+    float* sc = (float*)arena_alloc(c, (size_t)R * 4);
+    if (c->oom) return fail(c, TT_ERR_ARENA_OOM, "arena exhausted during generation");
+    if (n_new > 0) {
+        st = gpt2_generate_beam(c, params, pr, B, T_prompt, n_new, K, eos, tokbuf, sc);
+        if (st != TT_OK) return st == TT_ERR_ARENA_OOM ? fail(c, st, "arena exhausted during generation") : st;
+    } else {
+        launch_beam_walk(launch_of(c), pr, tokbuf, tokbuf, tokbuf, B, K, T_prompt, Ttot);
+        if (cudaMemsetAsync(sc, 0, (size_t)R * 4, c->stream) != cudaSuccess)
+            return fail(c, TT_ERR_CUDA, "score reset failed");
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(c, TT_ERR_CUDA, "launch: %s", cudaGetErrorString(e));
+    if (cudaMemcpyAsync(out, tokbuf, (size_t)R * Ttot * 4, cudaMemcpyDefault, c->stream) != cudaSuccess ||
+        cudaMemcpyAsync(scores, sc, (size_t)R * 4, cudaMemcpyDefault, c->stream) != cudaSuccess)
+        return fail(c, TT_ERR_CUDA, "result copy failed");
+    return tt_ctx_sync(c);
+}
+
 tt_status tt_ctx_loss_device(const tt_ctx* c, const float** mean_loss, const float** row_losses) {
     if (!c) return TT_ERR_ARG;
     if (!live(c)) return TT_ERR_STALE;
@@ -1327,13 +1628,6 @@ tt_status tt_cast_f32_to_f16(tt_ctx* c, const float* src, void* dst, size_t n) {
     if (!c) return TT_ERR_ARG;                            \
     if (!live(c)) return TT_ERR_STALE;                    \
     if (dtype != TT_FP32 && dtype != TT_BF16) return fail(c, TT_ERR_ARG, "bad dtype");
-
-static tt_status op_epilogue(tt_ctx* c, const char* what) {
-    if (c->oom) { c->oom = false; return fail(c, TT_ERR_ARENA_OOM, "%s: scratch does not fit", what); }
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(c, TT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return TT_OK;
-}
 
 tt_status tt_op_linear_fwd(tt_ctx* c, tt_dtype dtype, const void* x, const void* W, const void* b,
                            const void* residual, void* y, void* pre, int M, int K, int N, int gelu) {
@@ -1494,6 +1788,85 @@ tt_status tt_op_embed_bwd(tt_ctx* c, tt_dtype dtype, const void* dx, const int32
     }
     c->off = mark;
     return op_epilogue(c, "embed_bwd");
+}
+
+// The list operators take half storage too, and belong to the context's device.
+#define TT_HEAD_PROLOGUE()                                \
+    if (!c) return TT_ERR_ARG;                            \
+    if (!live(c)) return TT_ERR_STALE;                    \
+    if (current_device() != c->device) return fail(c, TT_ERR_STATE, "the context's device is not the current one");
+
+tt_status tt_op_top_logits(tt_ctx* c, tt_dtype dtype, const void* logits, float* vals, int32_t* idx, float* lse, int M,
+                           int V, int ld, int k, float tau) {
+    TT_HEAD_PROLOGUE();
+    if (!logits || !vals || !idx || M <= 0 || V <= 0 || ld < V) return fail(c, TT_ERR_ARG, "top_logits: bad arguments");
+    const char* why = list_refusal(dtype, V, k, tau);
+    if (why) return fail(c, TT_ERR_ARG, "top_logits: %s", why);
+    {
+        ProfScope ps(c, PK_TOP, 0.0, (double)M * V * esize(dtype) + 8.0 * M * k);
+        if (!launch_top_rows(op_launch(c), dtype, logits, ld, M, V, k, tau, vals, idx, lse, nullptr, nullptr))
+            return fail(c, TT_ERR_CUDA, "top_logits: launch failed");
+    }
+    return op_epilogue(c, "top_logits");
+}
+
+tt_status tt_op_distill(tt_ctx* c, tt_dtype dtype, const void* logits, const float* t_vals, const int32_t* t_idx,
+                        const float* t_lse, const int32_t* targets, void* dlogits, float* row_loss, float* mean_loss,
+                        int M, int V, int ld, int k, float alpha, float tau, float dscale) {
+    TT_HEAD_PROLOGUE();
+    if (!logits || !row_loss || M <= 0 || V <= 0 || ld < V) return fail(c, TT_ERR_ARG, "distill: bad arguments");
+    const char* why = distill_refusal(dtype, t_vals, t_idx, targets, V, k, alpha, tau);
+    if (why) return fail(c, TT_ERR_ARG, "distill: %s", why);
+    {
+        ProfScope ps(c, PK_DISTILL, 0.0, (dlogits ? 2.0 : 1.0) * M * ld * esize(dtype) + 8.0 * M * k);
+        if (!launch_distill(op_launch(c), dtype, logits, dlogits, t_vals, t_idx, t_lse, targets, row_loss, mean_loss, M,
+                            V, ld, k, alpha, tau, dscale, nullptr))
+            return fail(c, TT_ERR_CUDA, "distill: launch failed");
+    }
+    return op_epilogue(c, "distill");
+}
+
+tt_status tt_op_beam_select(tt_ctx* c, tt_dtype dtype, const void* logits, const float* scores, const int32_t* done,
+                            int32_t* parent, int32_t* token, float* out_scores, int32_t* out_done, int B, int K, int V,
+                            int ld, int n, int eos) {
+    TT_HEAD_PROLOGUE();
+    if (!logits || !scores || !parent || !token || !out_scores || B <= 0 || V <= 0 || ld < V)
+        return fail(c, TT_ERR_ARG, "beam_select: bad arguments");
+    if (K < 1 || K > TT_BEAM_MAX || n < 1 || n > 2 * TT_BEAM_MAX || (long long)n > (long long)K * V)
+        return fail(c, TT_ERR_ARG, "beam_select: K must be 1 .. TT_BEAM_MAX, n 1 .. min(2 TT_BEAM_MAX, K V)");
+    if (eos < -1 || eos >= V || (done && eos < 0))
+        return fail(c, TT_ERR_ARG, "beam_select: eos outside the vocabulary, or finished beams without one");
+    if (B > INT32_MAX / K || (long long)K * V > INT32_MAX)
+        return fail(c, TT_ERR_ARG, "beam_select: too many rows or columns");
+    const char* why = list_refusal(dtype, V, std::min(n, V), 1.0f);
+    if (why) return fail(c, TT_ERR_ARG, "beam_select: %s", why);
+    const size_t mark = c->off;
+    c->oom = false;
+    void* s = arena_alloc(c, beam_select_scratch_bytes(B * K, V, n));
+    bool ok = true;
+    if (!c->oom) {
+        ProfScope ps(c, PK_BEAM_SELECT, 0.0, (double)B * K * V * esize(dtype) + 16.0 * B * n);
+        ok = launch_beam_select(op_launch(c), dtype, logits, ld, scores, done, parent, token, out_scores, out_done, B, K,
+                                V, n, eos, s, nullptr, nullptr, 0, nullptr);
+    }
+    c->off = mark;
+    if (!ok) return fail(c, TT_ERR_CUDA, "beam_select: launch failed");
+    return op_epilogue(c, "beam_select");
+}
+
+tt_status tt_op_beam_reorder(tt_ctx* c, void* state, const int32_t* parents, int N, int B, int K, size_t row_bytes,
+                             size_t first, size_t count) {
+    TT_HEAD_PROLOGUE();
+    if (!state || !parents || N <= 0 || B <= 0 || K < 1 || K > TT_BEAM_MAX || row_bytes > (size_t)INT64_MAX / K ||
+        first > row_bytes || count > row_bytes - first)
+        return fail(c, TT_ERR_ARG, "beam_reorder: bad arguments");
+    {
+        ProfScope ps(c, PK_BEAM_REORDER, 0.0, 2.0 * N * B * K * (double)count);
+        if (!launch_beam_reorder(op_launch(c), state, parents, N, B, K, (long long)row_bytes, (long long)first,
+                                 (long long)count, nullptr, 0))
+            return fail(c, TT_ERR_ARG, "beam_reorder: state too large");
+    }
+    return op_epilogue(c, "beam_reorder");
 }
 
 // ------------------------------------------------------------------ generic tensor graph

@@ -279,6 +279,35 @@ bool launch_gemm_skinny_pick(const Launch& L, const void* A, const void* W, int 
 void launch_pick(const Launch& L, const unsigned long long* keys, int nct, int rows, int32_t* tok, int ld_tok,
                  const int* pos_dev);
 
+// lists over the LM head's logits (head.cu); rows of ld elements, V of them real
+bool head_row_ok(tt_dtype dtype, int V);  // a row the kernels take
+// per row the k largest logits (ties: lowest column) and log sum exp(z / tau);
+// lse, lse64 and skip (rows left out where it is not 0) may be NULL
+bool launch_top_rows(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, float tau,
+                     float* vals, int32_t* idx, float* lse, double* lse64, const int32_t* skip);
+// distillation loss and gradient; dz (may be z, or NULL: loss only), t_lse,
+// targets, mean_loss and scale_dev may be NULL
+bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, const float* t_vals,
+                    const int32_t* t_idx, const float* t_lse, const int32_t* targets, float* row_loss,
+                    float* mean_loss, int M, int V, int ld, int k, float alpha, float tau, float dscale,
+                    const float* scale_dev);
+
+// beam search (beam.cu).  tok_hist/par_hist (may be NULL): the choice is also
+// written to [slot][*pos_dev] of these [B n, ld_hist] tables.
+size_t beam_select_scratch_bytes(int R, int V, int n);
+bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long long ld, const float* scores,
+                        const int32_t* done, int32_t* parent, int32_t* token, float* out_scores, int32_t* out_done,
+                        int B, int K, int V, int n, int eos, void* scratch, int32_t* tok_hist, int32_t* par_hist,
+                        int ld_hist, const int* pos_dev);
+// with pos_dev the moved bytes are [first, *pos_dev * pos_bytes), at most count of them
+bool launch_beam_reorder(const Launch& L, void* state, const int32_t* parents, int N, int B, int K,
+                         long long row_bytes, long long first, long long count, const int* pos_dev,
+                         long long pos_bytes);
+void launch_kv_fill_beams(const Launch& L, bool bf16, const void* qkv, void* cache, int B, int K, int Tn, int C,
+                          int maxT);
+void launch_beam_walk(const Launch& L, const int32_t* prompt, const int32_t* tok, const int32_t* par, int32_t* out,
+                      int B, int K, int Tp, int T);
+
 // the generic tensor graph (graph.cu), fp32
 constexpr int G_ZERO_MAX = 32;
 struct GZeroList {  // buffers to zero in one launch (passed by value)

@@ -210,6 +210,18 @@ tt_status tt_gpt2_step_ex(tt_ctx* ctx, const void* params, float* grads, const i
                           const int32_t* targets, int B, int T, int flags, const float* loss_scale,
                           float* loss);
 
+/* tt_gpt2_step_ex with the distillation loss of tt_op_distill (tt_ops.h) in
+ * the place of the cross entropy: t_vals, t_idx [B*T, k] and t_lse [B*T] or
+ * NULL are the teacher's lists, device pointers (tt_gpt2_top_logits makes
+ * them; with t_lse it must have used the same tau); targets may be NULL when
+ * alpha is 1, and a target of -1 leaves a position without a hard label.  The
+ * mean is over all B*T positions.  Arena, errors and the other arguments as
+ * for tt_gpt2_step_ex. */
+tt_status tt_gpt2_step_distill(tt_ctx* ctx, const void* params, float* grads, const int32_t* tokens,
+                               const int32_t* targets, const float* t_vals, const int32_t* t_idx,
+                               const float* t_lse, int k, float alpha, float tau, int B, int T, int flags,
+                               const float* loss_scale, float* loss);
+
 /* Global gradient statistics, on the device: stats[0] = sqrt(sum_i (g_i /
  * s)^2) and stats[1] = 1 if that sum is not finite (an Inf or NaN gradient, or
  * one whose square overflows), else 0; s = *loss_scale when loss_scale is not
@@ -270,6 +282,16 @@ tt_status tt_cast_f32_to_f16(tt_ctx* ctx, const float* src, void* dst, size_t n)
 tt_status tt_gpt2_eval(tt_ctx* ctx, const void* params, const int32_t* tokens,
                        const int32_t* targets, int B, int T, float* loss);
 
+/* The k largest logits of every position (tt_op_top_logits, tt_ops.h) after a
+ * forward pass over a B x T batch: a teacher's side of distillation, or the
+ * likeliest next tokens of a prompt.  vals, idx [B*T, k] and lse [B*T] (may
+ * be NULL) are device memory.  Does not synchronize (a token id out of range
+ * is reported by tt_ctx_sync); the arena needs at most
+ * tt_gpt2_arena_bytes(cfg, B, T) and is NOT reset by this call.  There is no
+ * last loss to read (tt_ctx_loss_device) until the next step. */
+tt_status tt_gpt2_top_logits(tt_ctx* ctx, const void* params, const int32_t* tokens, int B, int T, int k,
+                             float tau, float* vals, int32_t* idx, float* lse);
+
 /* Exact number of arena bytes tt_gpt2_generate needs (the same allocation
  * sequence, run without launching); 0 for invalid arguments. */
 size_t tt_gpt2_generate_arena_bytes(const tt_gpt2_config* cfg, int B, int T_prompt, int n_new);
@@ -291,6 +313,23 @@ size_t tt_gpt2_generate_arena_bytes(const tt_gpt2_config* cfg, int B, int T_prom
  * arena is NOT reset by this call. */
 tt_status tt_gpt2_generate(tt_ctx* ctx, const void* params, const int32_t* prompt, int B,
                            int T_prompt, int n_new, int32_t* out);
+
+/* Exact number of arena bytes tt_gpt2_generate_beam needs; 0 for invalid arguments. */
+size_t tt_gpt2_generate_beam_arena_bytes(const tt_gpt2_config* cfg, int B, int T_prompt, int n_new, int K);
+
+/* Beam search with a key/value cache: K hypotheses per prompt, each step
+ * keeping the K best continuations by cumulative log probability
+ * (tt_op_beam_select, tt_ops.h; equal ones by the lowest beam, then token).
+ *   out     int32 [B, K, T_prompt + n_new], device or host memory: the prompt
+ *           and n_new tokens of each hypothesis, best first;
+ *   scores  float [B, K], device or host memory: their log probabilities.
+ * eos: a hypothesis that takes this token is finished; it keeps its score and
+ * repeats eos (-1: none).  1 <= K <= min(V, TT_BEAM_MAX).  With K = 1 and no
+ * eos the tokens are greedy ones.  Otherwise as tt_gpt2_generate: the call
+ * synchronizes the stream, takes TT_FP32 and TT_BF16 models and returns
+ * the same errors.  There is no last loss to read until the next step. */
+tt_status tt_gpt2_generate_beam(tt_ctx* ctx, const void* params, const int32_t* prompt, int B, int T_prompt,
+                                int n_new, int K, int eos, int32_t* out, float* scores);
 
 #ifdef __cplusplus
 }

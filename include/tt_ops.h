@@ -5,7 +5,8 @@
  *
  * Every call enqueues on the context's stream and takes device pointers.
  * `dtype` selects the storage type of activations and weights: TT_FP32 (all
- * fp32) or TT_BF16 (bf16 storage, fp32 arithmetic).  Parameter gradients,
+ * fp32) or TT_BF16 (bf16 storage, fp32 arithmetic), and in the calls over
+ * lists of logits TT_FP16 as well.  Parameter gradients,
  * LayerNorm statistics, log-sum-exp values and losses are always fp32.
  * Scratch memory, where a call needs it, is bump-allocated from the context's
  * arena (reset the arena between calls to reclaim it); TT_ERR_ARENA_OOM if
@@ -108,6 +109,85 @@ tt_status tt_op_embed_fwd(tt_ctx* ctx, tt_dtype dtype, const void* wte, const vo
  *   is kept); dwpe[t] = sum_b dx[b*T+t] for t < T and 0 for T <= t < maxT. */
 tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int32_t* tokens,
                           float* dwte, float* dwpe, int B, int T, int C, int V, int maxT);
+
+/* ------------------------------------------------------ lists over the logits
+ * Operators on the LM head's logits that deal in lists of columns: the top
+ * logits of a row, distillation from a teacher's list of them, and the
+ * selection and reordering steps of a beam search.  They take TT_FP32,
+ * TT_BF16 and TT_FP16 storage; lists, statistics, losses and scores are fp32.
+ * Rows are ld elements apart, the columns V..ld-1 are padding that no result
+ * depends on; neither ld nor the pointers need more than the element's
+ * alignment.  The pages have no counterpart to these calls: they extend the
+ * fused cross entropy (tinytorch 三.5) and the greedy choice (八.3). */
+
+#define TT_TOP_MAX 128  /* longest list of a row */
+#define TT_BEAM_MAX 32  /* most beams of a sequence */
+
+/* The k largest logits of each row, in descending order, equal ones by
+ * ascending column (-0 equals +0):
+ *   vals [M, k] fp32, idx [M, k];  lse [M] fp32 or NULL: log sum_v exp(z_v / tau)
+ * over the V columns.  1 <= k <= min(V, TT_TOP_MAX), tau > 0.  A NaN logit
+ * stands in the list as -inf and makes the row's lse NaN; a row of -inf has
+ * lse = -inf, one with +inf has lse = +inf. */
+tt_status tt_op_top_logits(tt_ctx* ctx, tt_dtype dtype, const void* logits, float* vals, int32_t* idx, float* lse,
+                           int M, int V, int ld, int k, float tau);
+
+/* Distillation from a teacher's top logits, loss and gradient in one call.
+ * The teacher's list of row r: logits t_vals [M, k] at the columns t_idx
+ * [M, k]; an index of -1 is an unused entry.  With q = softmax(z / tau):
+ *   t_lse == NULL:  p_j = softmax of t_j / tau over the list's entries,
+ *     KL = sum_j p_j (ln p_j - ln q_ij)
+ *   t_lse [M] (the teacher's log sum exp(t / tau) over its whole vocabulary,
+ *   as tt_op_top_logits gives it):  p_j = exp(t_j / tau - t_lse), and the
+ *   teacher's remaining mass p_r = max(0, 1 - sum_j p_j) is compared with the
+ *   student's mass off the list, q_r:
+ *     KL = sum_j p_j (ln p_j - ln q_ij) + p_r (ln p_r - ln q_r)
+ *   (the last term is left out where q_r is 0)
+ *   row_loss[r] = alpha tau^2 KL + (1 - alpha) (log sum exp(z) - z[target_r])
+ *   dlogits = d row_loss / d z * dscale, pad columns 0
+ * mean_loss (may be NULL) receives the mean over the M rows; dscale is
+ * usually 1/M.  dlogits [M, ld] may be logits itself (the call is then in
+ * place, as tt_op_xent) or NULL (loss only); any other overlap is not
+ * allowed.  A row whose entries are all unused has no KL term; a target of -1
+ * means that the row has no cross entropy term (targets may be NULL when
+ * alpha is 1).  A row with neither has loss 0 and gradient 0, whatever its
+ * logits hold.  A target or index outside these ranges, or an index that a row
+ * lists twice, raises the bad token flag (tt_ctx_sync: TT_ERR_ARG); that entry
+ * does not count.  0 <= alpha <= 1, tau > 0, 1 <= k <= min(V, TT_TOP_MAX).
+ * Deterministic. */
+tt_status tt_op_distill(tt_ctx* ctx, tt_dtype dtype, const void* logits, const float* t_vals, const int32_t* t_idx,
+                        const float* t_lse, const int32_t* targets, void* dlogits, float* row_loss,
+                        float* mean_loss, int M, int V, int ld, int k, float alpha, float tau, float dscale);
+
+/* One selection step of a beam search.  logits [B * K, ld]: row b K + j is
+ * beam j of sequence b; scores [B, K] are the beams' cumulative log
+ * probabilities (finite, or -inf for a slot that holds no hypothesis).  The n
+ * best of the K V candidates
+ *   scores[b, j] + z_v - log sum exp(z)
+ * of each sequence, best first, equal ones by ascending j V + v:
+ *   parent [B, n] (j), token [B, n] (v), out_scores [B, n];
+ *   out_done [B, n] or NULL: 1 where the parent was done or token == eos.
+ * done [B, K] or NULL: a beam with done != 0 has the one candidate eos at its
+ * unchanged score (its logits are not read); the others count as -inf.  eos:
+ * the end token, or -1 for none (done must then be NULL).  Candidates are
+ * compared in 64 bits; within a beam they are ordered by logit.  A beam whose
+ * logits hold NaN or +inf raises the non-finite flag (tt_ctx_sync:
+ * TT_ERR_NONFINITE); it, a beam whose logits are all -inf and one whose score
+ * is not finite have candidates of -inf only.  1 <= K <= TT_BEAM_MAX,
+ * 1 <= n <= min(2 TT_BEAM_MAX, K V).  out_scores and out_done may be scores
+ * and done when n == K.  Scratch from the arena: B K (8 + 8 n) bytes. */
+tt_status tt_op_beam_select(tt_ctx* ctx, tt_dtype dtype, const void* logits, const float* scores,
+                            const int32_t* done, int32_t* parent, int32_t* token, float* out_scores,
+                            int32_t* out_done, int B, int K, int V, int ld, int n, int eos);
+
+/* Reorder per-beam state in place after a selection step: in each of the N
+ * blocks (for example a layer's cache) of B K rows of row_bytes bytes, the
+ * bytes [first, first + count) of row b K + j become those that row
+ * b K + parents[b, j] held before the call.  parents [B, K] in [0, K): any
+ * mapping; a value out of range raises the bad token flag and its row stays.
+ * Rows that are their own parent are not touched.  1 <= K <= TT_BEAM_MAX. */
+tt_status tt_op_beam_reorder(tt_ctx* ctx, void* state, const int32_t* parents, int N, int B, int K,
+                             size_t row_bytes, size_t first, size_t count);
 
 /* ------------------------------------------------------ allocation-free call
  * The pages have no counterpart to this entry point.  It serves callers of
