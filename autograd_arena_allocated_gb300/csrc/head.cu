@@ -1,4 +1,4 @@
-// head.cu -- operators on the LM head's logits that keep a list of columns:
+// head.cu -- operators on the LM head's logits that deal in lists of columns:
 //
 //   k_top_rows      per row the k largest logits (ties: the lowest column) and
 //                   the log-sum-exp
@@ -6,130 +6,411 @@
 //                   gradient of a row
 //   k_row_mean      the mean of the row losses (fixed order)
 //
-// A row of V logits is read in the storage type; sums, statistics and losses
-// are fp32.
-#include "tt_internal.h"
+// Both row kernels read a row of V logits from memory once, in the storage
+// type, and hold it on chip (head_row.cuh); sums, statistics and losses are
+// fp32.
+#include "head_row.cuh"
 
 #include <algorithm>
 
 namespace tt {
 namespace {
 
-template <typename T> __device__ __forceinline__ float ldf(const T* p);
-template <> __device__ __forceinline__ float ldf<float>(const float* p) { return *p; }
-template <> __device__ __forceinline__ float ldf<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-template <> __device__ __forceinline__ float ldf<__half>(const __half* p) { return __half2float(*p); }
-template <typename T> __device__ __forceinline__ T stf(float v);
-template <> __device__ __forceinline__ float stf<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 stf<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half stf<__half>(float v) { return __float2half_rn(v); }
+using namespace head;
 
-// Order-preserving key of (value, column): larger values first, then lower
-// columns.  -0 counts as +0 and a NaN as -inf.
-__device__ __forceinline__ unsigned long long top_key(float v, int col) {
-    if (v != v) v = -INFINITY;
-    uint32_t u = __float_as_uint(v);
-    if ((u & 0x7FFFFFFFu) == 0) u = 0;
-    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((unsigned long long)u << 32) | (unsigned long long)(0xFFFFFFFFu - (uint32_t)col);
+constexpr int LIST_MAX = TT_TOP_MAX;
+constexpr int LIST_PER_LANE = LIST_MAX / 32;
+constexpr int CS_MAX = 8;      // CTAs of a cluster (the portable limit)
+constexpr int CAND_MAX = 1024;  // candidates of a row's (or slice's) list
+
+__host__ __device__ constexpr int cta_threads(int NT) { return NT == 32 ? 256 : NT; }
+__host__ __device__ constexpr int cta_groups(int NT) { return NT == 32 ? 8 : 1; }
+__host__ __device__ constexpr int align16(int n) { return (n + 15) & ~15; }
+
+// ------------------------------------------------------------ top logits
+// Order-preserving whole number of a value: -0 counts as +0 and a NaN as -inf.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t u = __float_as_uint(fmaxf(v, -INFINITY) + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(unsigned long long key) {
-    uint32_t u = (uint32_t)(key >> 32);
-    u = (u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u;
-    return __uint_as_float(u);
+__device__ __forceinline__ float value_of(uint32_t u) {
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+// (value, column): larger values first, then lower columns.  Never 0.
+__device__ __forceinline__ unsigned long long top_key(float v, int col) {
+    return ((unsigned long long)order_of(v) << 32) | (unsigned long long)(0xFFFFFFFFu - (uint32_t)col);
 }
 __device__ __forceinline__ int key_col(unsigned long long key) {
     return (int)(0xFFFFFFFFu - (uint32_t)(key & 0xFFFFFFFFull));
 }
+// bits of order_of that tell two values of a storage type apart
+template <typename T> struct OrderBits { static constexpr int N = 32; };
+template <> struct OrderBits<__nv_bfloat16> { static constexpr int N = 16; };
+template <> struct OrderBits<__half> { static constexpr int N = 19; };  // sign, 8 exponent bits of fp32, 10 of mantissa
 
-constexpr int HD_THREADS = 256;
-constexpr int HD_WARPS = HD_THREADS / 32;
+struct TopArgs {
+    float* vals;
+    int32_t* idx;
+    float* lse;
+    double* lse64;
+    const int32_t* skip;
+    long long ld;
+    int M, V, k, Gs, cs, nbuf;
+    float inv_tau;
+};
 
-// block reductions in a fixed order; every thread gets the result
-__device__ __forceinline__ float block_sum(float v, float* s) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// shared memory of a group, in bytes from its start
+struct TopLayout {
+    int cand, thr, part, red, lists, x, cnt, total;
+    __host__ __device__ TopLayout(int nt, int Gs, int nbuf, int k, bool cl) {
+        int at = nbuf * Gs * 16;
+        cand = at; at += (nt > 32 ? CAND_MAX : LIST_MAX) * 8;  // a warp's candidates are exact ones
+        thr = at; at += nt > 32 ? 128 : 0;
+        part = at; at += nt > 32 ? 256 : 0;
+        red = at; at += nt > 32 ? 256 : 0;
+        lists = at; at += cl ? align16(2 * CS_MAX * k * 8) : 0;
+        x = at; at += cl ? 2 * CS_MAX * 8 : 0;
+        cnt = at; at += 16;
+        total = at;
+    }
+};
+
+// sum of c over the group; `turn` alternates between two rows of s_red, so
+// that one barrier a call is enough
+template <int NT> __device__ __forceinline__ int group_count(int c, int* s_red, int& turn) {
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (NT == 32) return c;
+    const int lane = threadIdx.x & 31;
+    int* r = s_red + (turn & 1) * 32;
+    turn++;
+    if (lane == 0) r[threadIdx.x >> 5] = c;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.0f;
-    for (int w = 0; w < HD_WARPS; w++) t += s[w];
-    return t;
+    return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? r[lane] : 0);
 }
-__device__ __forceinline__ float block_max(float v, float* s) {
+
+// f(key order, column) for every element of the thread's granules
+template <typename T, int NT, typename F>
+__device__ __forceinline__ void each_element(const Slice<T>& s, const char* buf, int V, int tid, F&& f) {
+    for (int g = s.g0 + tid; g < s.g1; g += NT) {
+        const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+        f2 e[Elem<T>::EPG / 2];
+        Elem<T>::unpack(u, e);
+        const int c0 = s.col(g);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = s[0];
-    for (int w = 1; w < HD_WARPS; w++) t = fmaxf(t, s[w]);
-    return t;
+        for (int i = 0; i < Elem<T>::EPG / 2; i++) {
+            float a, b;
+            unpk(e[i], a, b);
+            if (c0 + 2 * i >= 0 && c0 + 2 * i < V) f(a, c0 + 2 * i);
+            if (c0 + 2 * i + 1 >= 0 && c0 + 2 * i + 1 < V) f(b, c0 + 2 * i + 1);
+        }
+    }
 }
 
-// One CTA per row.  k rounds: each round finds the largest key below the last
-// one found.
-template <typename T>
-__global__ void __launch_bounds__(HD_THREADS)
-k_top_rows(const T* __restrict__ z, long long ld, int V, int k, float inv_tau, float* __restrict__ vals,
-           int32_t* __restrict__ idx, float* __restrict__ lse, double* __restrict__ lse64,
-           const int32_t* __restrict__ skip) {
+// The kk first elements of the slice in list order, exactly, as candidates:
+// the kk-th largest value is found bit by bit by counting, then, where equal
+// values are more than are needed, the last column that is taken.  Used where
+// the threads' maxima say too little: rows of a warp, rows with most columns
+// masked, rows of few different values.
+template <typename T, int NT>
+__device__ void exact_candidates(const Slice<T>& s, const char* buf, int V, int kk, int n_el,
+                                 unsigned long long* s_cand, int* s_cnt, int* s_red, int tid) {
+    int turn = 0;
+    if (tid == 0) *s_cnt = 0;
+    group_sync<NT>();
+    if (n_el <= (NT == 32 ? LIST_MAX : CAND_MAX / 2)) {
+        // few enough to rank them all
+        each_element<T, NT>(s, buf, V, tid, [&](float v, int c) { s_cand[atomicAdd(s_cnt, 1)] = top_key(v, c); });
+        group_sync<NT>();
+        return;
+    }
+    constexpr int LOW = 32 - OrderBits<T>::N;
+    uint32_t t = 0;
+    for (int bit = 31; bit >= LOW; bit--) {
+        const uint32_t cand = t | (1u << bit);
+        int c = 0;
+        each_element<T, NT>(s, buf, V, tid, [&](float v, int) { c += order_of(v) >= cand; });
+        if (group_count<NT>(c, s_red, turn) >= kk) t = cand;
+    }
+    const uint32_t above = t + (1u << LOW);  // no value's order is so large that this wraps
+    int c = 0, e = 0;
+    each_element<T, NT>(s, buf, V, tid, [&](float v, int) {
+        const uint32_t o = order_of(v);
+        c += o >= above;
+        e += o >= t && o < above;
+    });
+    const int need = kk - group_count<NT>(c, s_red, turn);
+    int last = V;  // equal values are taken up to this column
+    if (group_count<NT>(e, s_red, turn) > need) {
+        last = 0;
+        for (int bit = 20; bit >= 0; bit--) {  // V < 2^20
+            const int x = last | (1 << bit);
+            int n = 0;
+            each_element<T, NT>(s, buf, V, tid, [&](float v, int col) {
+                const uint32_t o = order_of(v);
+                n += o >= t && o < above && col < x;
+            });
+            if (group_count<NT>(n, s_red, turn) < need) last = x;
+        }
+    }
+    each_element<T, NT>(s, buf, V, tid, [&](float v, int col) {
+        const uint32_t o = order_of(v);
+        if (o >= above || (o >= t && col <= last)) s_cand[atomicAdd(s_cnt, 1)] = top_key(v, col);
+    });
+    group_sync<NT>();
+}
+
+// A row's list in four stages:
+//   1. one pass over the granules: each thread's largest value, and its sum of
+//      exponentials;
+//   2. a threshold: with fw warps that have work in every lane, the lowest of
+//      their q-th largest thread maxima, q = ceil(k / fw).  fw q >= k threads
+//      have a value at or above it, so the list lies there;
+//   3. the elements at or above the threshold become candidates (about 3 fw
+//      for small q on unordered data);
+//   4. each candidate's rank among them by counting, a warp per candidate.
+// With more than CAND_MAX candidates, or too few threads for a threshold, the
+// candidates are found exactly instead.  Clusters: each CTA lists its slice
+// and sends the list to CTA 0, which ranks every entry by binary searches in
+// the other lists.
+template <typename T, int NT, bool CL>
+__global__ void __launch_bounds__(cta_threads(NT), NT == 1024 ? 1 : 4)
+k_top_rows(const T* __restrict__ z, const TopArgs a) {
     pdl_enter();
-    __shared__ float s_f[HD_WARPS];
-    __shared__ unsigned long long s_k[HD_WARPS];
-    const long long row = blockIdx.x;
-    if (skip && skip[row]) return;
-    const T* zr = z + row * ld;
-    if (lse || lse64) {
-        float m = -INFINITY;
-        for (int v = threadIdx.x; v < V; v += HD_THREADS) m = fmaxf(m, ldf(zr + v));
-        m = block_max(m, s_f);
-        float s = 0.0f;
-        for (int v = threadIdx.x; v < V; v += HD_THREADS) s += expf((ldf(zr + v) - m) * inv_tau);
-        s = block_sum(s, s_f);
-        // an empty row (every logit -inf) and a row with +inf have that as their value, unless a NaN is there too
-        if (m == INFINITY) {
-            float n = 0.0f;
-            for (int v = threadIdx.x; v < V; v += HD_THREADS) n += ldf(zr + v) != ldf(zr + v) ? 1.0f : 0.0f;
-            if (block_sum(n, s_f) > 0.0f) m = NAN;
-        }
-        if (threadIdx.x == 0) {
-            const bool flat = m == -INFINITY || m == INFINITY;
-            if (lse) lse[row] = flat ? m : m * inv_tau + logf(s);
-            if (lse64) lse64[row] = flat ? (double)m : (double)m * (double)inv_tau + log((double)s);
-        }
+    extern __shared__ __align__(16) char smem[];
+    const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = tid >> 5;
+    const TopLayout lay(NT, a.Gs, a.nbuf, a.k, CL);
+    char* sm = smem + (NT == 32 ? threadIdx.x >> 5 : 0) * lay.total;
+    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + lay.cand);
+    float* s_thr = reinterpret_cast<float*>(sm + lay.thr);
+    float2* s_part = reinterpret_cast<float2*>(sm + lay.part);
+    int* s_red = reinterpret_cast<int*>(sm + lay.red);
+    auto* s_lists = reinterpret_cast<unsigned long long*>(sm + lay.lists);  // [2][cs][k]
+    float2* s_x = reinterpret_cast<float2*>(sm + lay.x);                    // [2][cs]
+    int* s_cnt = reinterpret_cast<int*>(sm + lay.cnt);
+    const int rank = CL ? (int)cluster_rank() : 0, cs = CL ? a.cs : 1;
+    const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
+    const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
+    const bool want = a.lse || a.lse64;
+    const float ct = LOG2E * a.inv_tau, lift = 28.0f / fmaxf(1.0f, a.inv_tau);
+    const int k = a.k, V = a.V;
+    auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, rank, a.Gs); };
+    auto here = [&](long long r) { return r < a.M && !(a.skip && a.skip[r]); };
+
+    for (int i = 0; i < a.nbuf; i++) {
+        const long long r = first + i * stride;
+        if (here(r)) fill<T, NT>(slice(r), sm + i * a.Gs * 16, tid);
+        cp_commit();
     }
-    unsigned long long last = ~0ull;
-    for (int j = 0; j < k; j++) {
-        unsigned long long best = 0;
-        for (int v = threadIdx.x; v < V; v += HD_THREADS) {
-            const unsigned long long key = top_key(ldf(zr + v), v);
-            if (key < last && key > best) best = key;
-        }
+    T edge = Elem<T>::put(0.0f);
+    if (here(first)) edge_store(slice(first), sm, edge_load(slice(first), V, tid), tid);
+    if (here(first + stride)) edge = edge_load(slice(first + stride), V, tid);
+    if (tid == 0) *s_cnt = 0;
+    if (CL) cluster_sync();  // the others run: their shared memory may be written
+
+    int it = 0;
+    for (long long row = first; row < a.M; row += stride, it++) {
+        const int par = it & 1;
+        char* buf = sm + (a.nbuf == 2 ? par : 0) * a.Gs * 16;
+        const Slice<T> s = slice(row);
+        cp_wait(a.nbuf);
+        group_sync<NT>();
+        const bool run = here(row);
+        const long long next = row + a.nbuf * stride;
+        if (run) {
+            // stage 1
+            float tmax = -INFINITY, R = -INFINITY, sum = 0.0f;
+            f2 acc = pk(0.0f, 0.0f);
+            const f2 ct2 = pk(ct, ct);
+            for (int g = s.g0 + tid; g < s.g1; g += NT) {
+                const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+                const float vm = Elem<T>::vmax(u);
+                tmax = fmaxf(tmax, vm);
+                if (want) {
+                    if (vm > R + lift) {
+                        const float f = rescale(R, vm, ct);
+                        acc = mul2(acc, pk(f, f));
+                        R = vm;
+                    }
+                    const float nr = -ref_of(R);
+                    f2 e[Elem<T>::EPG / 2];
+                    Elem<T>::unpack(u, e);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) s_k[threadIdx.x >> 5] = best;
-        __syncthreads();
-        best = s_k[0];
-        for (int w = 1; w < HD_WARPS; w++) best = max(best, s_k[w]);
-        last = best;
-        if (threadIdx.x == 0) {
-            vals[row * k + j] = key_value(best);
-            idx[row * k + j] = key_col(best);
+                    for (int i = 0; i < Elem<T>::EPG / 2; i++) {
+                        float x, y;
+                        unpk(mul2(add2(e[i], pk(nr, nr)), ct2), x, y);
+                        acc = add2(acc, pk(ex2f(x), ex2f(y)));
+                    }
+                }
+            }
+            if (want) {
+                float x, y;
+                unpk(acc, x, y);
+                sum = x + y;
+                if (R == INFINITY) {  // inf - inf above: what is left to know is whether there is a NaN
+                    sum = 0.0f;
+                    for (int g = s.g0 + tid; g < s.g1; g += NT)
+                        for (int i = 0; i < Elem<T>::EPG; i++) {
+                            const float v = Elem<T>::get(reinterpret_cast<const T*>(buf + (g - s.g0) * 16) + i);
+                            if (v != v) sum = v;
+                        }
+                }
+                warp_merge(R, sum, ct);
+            }
+            // stage 2
+            const int n_slots = s.g1 - s.g0;
+            const int n_el = max(0, min(V, s.col(s.g1)) - max(0, s.col(s.g0)));
+            const int kk = min(k, n_el);
+            const int fw = NT == 32 ? 0 : min(NT, n_slots) / 32;
+            const int q = fw ? (k + fw - 1) / fw : 33;
+            bool exact = q > 16;
+            int cnt = 0;
+            if (NT > 32) {
+                float m = INFINITY;
+                if (!exact && warp < fw) {
+                    float cur = tmax;
+                    for (int i = 0;; i++) {
+                        m = warp_max(cur);
+                        if (i == q - 1) break;
+                        if (lane == __ffs(__ballot_sync(0xffffffffu, cur == m)) - 1) cur = -INFINITY;
+                    }
+                }
+                if (lane == 0) {
+                    s_thr[warp] = m;
+                    s_part[warp] = make_float2(R, sum);
+                }
+                __syncthreads();
+                if (!exact) {
+                    // stage 3
+                    const float thr = -warp_max(lane < NT / 32 ? -s_thr[lane] : -INFINITY);
+                    if (tmax >= thr) {
+                        for (int g = s.g0 + tid; g < s.g1; g += NT) {
+                            const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+                            if (Elem<T>::vmax(u) < thr) continue;
+                            f2 e[Elem<T>::EPG / 2];
+                            Elem<T>::unpack(u, e);
+                            const int c0 = s.col(g);
+#pragma unroll
+                            for (int i = 0; i < Elem<T>::EPG; i++) {
+                                float x, y;
+                                unpk(e[i / 2], x, y);
+                                const float v = fmaxf(i & 1 ? y : x, -INFINITY);
+                                const int c = c0 + i;
+                                if (v >= thr && c >= 0 && c < V) {
+                                    const int p = atomicAdd(s_cnt, 1);
+                                    if (p < CAND_MAX) s_cand[p] = top_key(v, c);
+                                }
+                            }
+                        }
+                    }
+                    __syncthreads();
+                    cnt = *s_cnt;
+                    if (cnt > CAND_MAX) {
+                        __syncthreads();  // every thread has read the count
+                        exact = true;
+                    }
+                }
+            }
+            if (exact) {
+                exact_candidates<T, NT>(s, buf, V, kk, n_el, s_cand, s_cnt, s_red, tid);
+                cnt = *s_cnt;
+            }
+            if (here(next)) fill<T, NT>(slice(next), buf, tid);
+            cp_commit();
+            // stage 4
+            for (int i = warp; i < cnt; i += NT / 32) {
+                const unsigned long long key = s_cand[i];
+                int r = 0;
+                for (int j = lane; j < cnt; j += 32) r += s_cand[j] > key;
+                r = __reduce_add_sync(0xffffffffu, r);
+                if (lane == 0 && r < kk) {
+                    if (CL) {
+                        st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), key);
+                    } else {
+                        a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
+                        a.idx[row * k + r] = key_col(key);
+                    }
+                }
+            }
+            if (CL)
+                for (int r = kk + tid; r < k; r += NT) st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), 0ull);
+            if (want && warp == 0) {
+                if (NT > 32) {
+                    const float2 p = lane < NT / 32 ? s_part[lane] : make_float2(-INFINITY, 0.0f);
+                    R = p.x;
+                    sum = p.y;
+                    warp_merge(R, sum, ct);
+                }
+                if (CL && lane == 0) {
+                    const uint32_t at = remote(s_x + par * cs + rank, 0);
+                    st_remote(at, R);
+                    st_remote(at + 4, sum);
+                }
+            }
+            if (CL) {
+                cluster_sync();
+                if (rank == 0) {
+                    const unsigned long long* l = s_lists + par * cs * k;
+                    for (int i = tid; i < cs * k; i += NT) {
+                        const unsigned long long key = l[i];
+                        int r = i % k;
+                        if (key == 0) continue;
+                        for (int o = 0; o < cs; o++) {
+                            if (o == i / k) continue;
+                            int lo = 0, hi = k;  // entries of list o above key
+                            while (lo < hi) {
+                                const int mid = (lo + hi) >> 1;
+                                if (l[o * k + mid] > key) lo = mid + 1;
+                                else hi = mid;
+                            }
+                            r += lo;
+                        }
+                        if (r < k) {
+                            a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
+                            a.idx[row * k + r] = key_col(key);
+                        }
+                    }
+                    if (want && warp == 0) {
+                        const float2 p = lane < cs ? s_x[par * cs + lane] : make_float2(-INFINITY, 0.0f);
+                        R = p.x;
+                        sum = p.y;
+                        warp_merge(R, sum, ct);
+                    }
+                }
+            }
+            if (want && tid == 0 && rank == 0) {
+                // a row of -inf and a row with +inf have that as their value, unless a NaN is there too
+                const bool flat = sum == sum && (R == -INFINITY || R == INFINITY);
+                if (a.lse) a.lse[row] = flat ? R : R * a.inv_tau + logf(sum);
+                if (a.lse64) a.lse64[row] = flat ? (double)R : (double)R * (double)a.inv_tau + log((double)sum);
+            }
+        } else {
+            if (here(next)) fill<T, NT>(slice(next), buf, tid);
+            cp_commit();
+            if (CL) cluster_sync();
         }
+        group_sync<NT>();
+        if (tid == 0) *s_cnt = 0;
+        const long long n1 = row + stride, n2 = n1 + stride;
+        if (here(n1)) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
+        if (here(n2)) edge = edge_load(slice(n2), V, tid);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// One CTA per row.  With q = softmax(z / tau), s = softmax(z), the list's
-// probabilities p_j at columns i_j, W their sum (plus p_r, the teacher's mass
-// outside the list, when it is known and the student has any there, q_r):
+// ------------------------------------------------------------ distillation
+// With q = softmax(z / tau), s = softmax(z), the list's probabilities p_j at
+// columns i_j, W their sum (plus p_r, the teacher's mass outside the list,
+// when it is known and the student has any there, q_r):
 //   loss = alpha tau^2 (sum p_j (ln p_j - ln q_ij) + p_r (ln p_r - ln q_r)) + (1 - alpha) (lse(z) - z_y)
 //   dz_i = g alpha tau (W q_i - p_i)            on the list
 //        = g alpha tau q_i (W - p_r / q_r)      off it
 //        + g (1 - alpha) (s_i - [i = y])
-// The list's columns are marked in a bitmap, so that q_r is summed without the
-// list instead of as a difference.
+// One pass over the row's granules sums the exponentials, a second writes the
+// gradient as if no column were listed, and the list's columns are then
+// written over.  Where q_r is needed (t_lse) the listed logits are first
+// replaced by -inf in the on-chip copy, so that q_r is summed without them and
+// not as a difference; their own exponentials are added from the list.
 struct DistillArgs {
     const float* t_vals;
     const int32_t* t_idx;
@@ -137,119 +418,386 @@ struct DistillArgs {
     const int32_t* targets;
     const float* scale_dev;
     float* row_loss;
-    int V, ld, k;
-    float alpha, tau, dscale;
     int* flags;
+    long long ld;
+    int M, V, k, Gs, cs, nbuf;
+    float alpha, tau, dscale;
+    bool same_phase;  // a row of dz starts at the same place of a 16-byte line as its row of z
 };
 
-constexpr int LIST_MAX = 128;
+struct DistillLayout {
+    int bits, ti, tv, yl, zl, p, part, x, fin, total;
+    __host__ __device__ DistillLayout(int nt, int Gs, int nbuf, int k, int epg, bool cl) {
+        const int k4 = align16(4 * (k + 1));
+        int at = nbuf * Gs * 16;
+        bits = at; at += align16((Gs * epg + 31) / 32 * 4);
+        ti = at; at += nbuf * k4;
+        tv = at; at += nbuf * k4;
+        yl = at; at += 16;       // [nbuf] targets, [nbuf] t_lse
+        zl = at; at += 2 * k4;   // student logits of the list, and of the target
+        p = at; at += k4;
+        part = at; at += nt > 32 ? 32 * 16 : 0;
+        x = at; at += cl ? 2 * CS_MAX * 16 : 0;
+        fin = at; at += 32;
+        total = at;
+    }
+};
 
-template <typename T>
-__global__ void __launch_bounds__(HD_THREADS)
+template <typename T, int NT, bool CL>
+__global__ void __launch_bounds__(cta_threads(NT), NT == 1024 ? 1 : 4)
 k_distill(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
-    extern __shared__ uint32_t s_bits[];
-    __shared__ float s_f[HD_WARPS];
-    __shared__ int s_i[LIST_MAX];
-    __shared__ float s_z[LIST_MAX], s_p[LIST_MAX];
-    const long long row = blockIdx.x;
-    const int tid = threadIdx.x, V = a.V, k = a.k;
-    const T* zr = z + row * (long long)a.ld;
-    T* dr = dz ? dz + row * (long long)a.ld : nullptr;
-    const float it = 1.0f / a.tau;
-    float g = a.dscale;
-    if (a.scale_dev) g *= *a.scale_dev;
-    for (int w = tid; w < (V + 31) / 32; w += HD_THREADS) s_bits[w] = 0;
-    __syncthreads();
-    float t = -INFINITY;
-    int col = -1;
-    bool bad = false;
-    if (tid < k) {
-        col = a.t_idx[row * k + tid];
-        if (col >= 0 && col < V) {
-            const uint32_t bit = 1u << (col & 31);
-            if (atomicOr(&s_bits[col >> 5], bit) & bit) { bad = true; col = -1; }
-            else t = a.t_vals[row * k + tid] * it;
-        } else {
-            bad = col != -1;
-            col = -1;
+    extern __shared__ __align__(16) char smem[];
+    constexpr int EPG = Elem<T>::EPG;
+    const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = tid >> 5;
+    const DistillLayout lay(NT, a.Gs, a.nbuf, a.k, EPG, CL);
+    char* sm = smem + (NT == 32 ? threadIdx.x >> 5 : 0) * lay.total;
+    const int k = a.k, V = a.V, k4 = align16(4 * (k + 1)) / 4;
+    uint32_t* s_bits = reinterpret_cast<uint32_t*>(sm + lay.bits);
+    int* s_y = reinterpret_cast<int*>(sm + lay.yl);
+    float* s_tl = reinterpret_cast<float*>(sm + lay.yl) + 2;
+    float* s_p = reinterpret_cast<float*>(sm + lay.p);
+    float4* s_part = reinterpret_cast<float4*>(sm + lay.part);
+    float4* s_x = reinterpret_cast<float4*>(sm + lay.x);  // [2][cs]
+    float* s_fin = reinterpret_cast<float*>(sm + lay.fin);
+    const int rank = CL ? (int)cluster_rank() : 0, cs = CL ? a.cs : 1;
+    const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
+    const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
+    const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
+    const float it = 1.0f / a.tau, ct = LOG2E * it, lift = 28.0f / fmaxf(1.0f, it);
+    float g_all = a.dscale;
+    if (a.scale_dev) g_all *= *a.scale_dev;
+    auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, rank, a.Gs); };
+    auto copy_lists = [&](long long r, int b) {  // warp 0
+        for (int j = lane; j < k; j += 32) {
+            cp4(sm + lay.ti + (b * k4 + j) * 4, a.t_idx + r * k + j);
+            cp4(sm + lay.tv + (b * k4 + j) * 4, a.t_vals + r * k + j);
         }
-    }
-    int y = a.targets ? a.targets[row] : -1;
-    if (y < -1 || y >= V) { bad = true; y = -1; }
-    if (bad) atomicOr(&a.flags[FLAG_BAD_TOKEN], 1);
-    const int used = __syncthreads_count(col >= 0);
-    const bool soft = used > 0 && a.alpha > 0.0f, hard = y >= 0 && a.alpha < 1.0f;
-    if (!soft && !hard) {
-        if (tid == 0) a.row_loss[row] = 0.0f;
-        if (dr)
-            for (int v = tid; v < a.ld; v += HD_THREADS) dr[v] = stf<T>(0.0f);
-        return;
-    }
-    float m = -INFINITY;
-    for (int v = tid; v < V; v += HD_THREADS) m = fmaxf(m, ldf(zr + v));
-    m = block_max(m, s_f);
-    float s1 = 0.0f, st = 0.0f, sr = 0.0f;
-    for (int v = tid; v < V; v += HD_THREADS) {
-        const float d = ldf(zr + v) - m;
-        if (hard) s1 += expf(d);
-        if (soft) {
-            const float e = expf(d * it);
-            if (s_bits[v >> 5] >> (v & 31) & 1) st += e;
-            else sr += e;
-        }
-    }
-    s1 = block_sum(s1, s_f);
-    st = block_sum(st, s_f);
-    sr = block_sum(sr, s_f);
-    st += sr;
-    float loss = 0.0f, W = 0.0f, off = 0.0f;
-    if (soft) {
-        const float lse = logf(st);
-        const float zl = col >= 0 ? ldf(zr + col) : 0.0f;
-        float lp = -INFINITY;
-        if (a.t_lse) {
-            if (col >= 0) lp = t - a.t_lse[row];
-        } else {
-            const float tm = block_max(t, s_f);
-            const float sum = block_sum(col >= 0 ? expf(t - tm) : 0.0f, s_f);
-            if (col >= 0) lp = t - tm - logf(sum);
-        }
-        const float p = col >= 0 ? expf(lp) : 0.0f;
-        W = block_sum(p, s_f);
-        loss = block_sum(p > 0.0f || p != p ? p * (lp - ((zl - m) * it - lse)) : 0.0f, s_f);
-        off = W;
-        if (a.t_lse && sr > 0.0f) {
-            const float pr = fmaxf(1.0f - W, 0.0f);
-            if (pr > 0.0f) loss += pr * (logf(pr) - (logf(sr) - lse));
-            W += pr;
-            off = W - pr * st / sr;
-        }
-        if (tid < k) { s_i[tid] = col; s_z[tid] = zl; s_p[tid] = p; }
-        loss *= a.alpha * a.tau * a.tau;
-    }
-    const float zy = hard ? ldf(zr + y) : 0.0f;
-    if (hard) loss += (1.0f - a.alpha) * (m + logf(s1) - zy);
-    if (tid == 0) a.row_loss[row] = loss;
-    if (!dr) return;
-    const float ks = g * a.alpha * a.tau, kh = hard ? g * (1.0f - a.alpha) : 0.0f;
-    __syncthreads();
-    auto grad = [&](float zv, float w, float p, bool is_y) {
-        const float d = zv - m;
-        float r = 0.0f;
-        if (soft) r = ks * (w * expf(d * it) / st - p);
-        if (hard) r += kh * (expf(d) / s1 - (is_y ? 1.0f : 0.0f));
-        return r;
+        if (lane == 0 && a.targets) cp4(s_y + b, a.targets + r);
+        if (lane == 1 && rest) cp4(s_tl + b, a.t_lse + r);
     };
-    for (int v = tid; v < a.ld; v += HD_THREADS) {
-        float r = 0.0f;
-        if (v < V) {
-            if (soft && (s_bits[v >> 5] >> (v & 31) & 1)) continue;  // the list's columns: below
-            r = grad(ldf(zr + v), off, 0.0f, v == y);
+
+    for (int w = tid; w < (a.Gs * EPG + 31) / 32; w += NT) s_bits[w] = 0;
+    if (tid < 2) s_y[tid] = -1;
+    group_sync<NT>();
+    for (int i = 0; i < a.nbuf; i++) {
+        const long long r = first + i * stride;
+        if (r < a.M) {
+            fill<T, NT>(slice(r), sm + i * a.Gs * 16, tid);
+            if (warp == 0) copy_lists(r, i);
         }
-        dr[v] = stf<T>(r);
+        cp_commit();
     }
-    if (soft && tid < k && s_i[tid] >= 0) dr[s_i[tid]] = stf<T>(grad(s_z[tid], W, s_p[tid], s_i[tid] == y));
+    T edge = Elem<T>::put(0.0f);
+    if (first < a.M) edge_store(slice(first), sm, edge_load(slice(first), V, tid), tid);
+    if (first + stride < a.M) edge = edge_load(slice(first + stride), V, tid);
+
+    if (CL) cluster_sync();  // the others run: their shared memory may be written
+
+    int itn = 0;
+    for (long long row = first; row < a.M; row += stride, itn++) {
+        const int par = itn & 1, b = a.nbuf == 2 ? par : 0;
+        char* buf = sm + b * a.Gs * 16;
+        int* s_ti = reinterpret_cast<int*>(sm + lay.ti) + b * k4;
+        const float* s_tv = reinterpret_cast<const float*>(sm + lay.tv) + b * k4;
+        float* s_zl = reinterpret_cast<float*>(sm + lay.zl) + par * k4;
+        const Slice<T> s = slice(row);
+        cp_wait(a.nbuf);
+        group_sync<NT>();
+        int y = s_y[b];
+        const bool y_bad = y < -1 || y >= V;
+        if (y_bad) y = -1;
+
+        // the list: the student's logits at its columns (each CTA sends those
+        // of its slice to all), duplicates, and the replacement by -inf
+        int off[LIST_PER_LANE];
+        if (warp == 0) {
+            bool bad = y_bad && lane == 0;
+            if (lane == 0) {
+                const int o = y >= 0 ? s.at(y) : -1;
+                if (o >= 0) {
+                    const float v = Elem<T>::get(reinterpret_cast<const T*>(buf + o));
+                    s_zl[k] = v;
+                    if (CL)
+                        for (int r = 0; r < cs; r++) st_remote(remote(s_zl + k, r), v);
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < LIST_PER_LANE; e++) {
+                const int j = lane + 32 * e;
+                off[e] = -1;
+                if (j >= k) continue;
+                const int c = s_ti[j];
+                if (c < 0 || c >= V) {
+                    bad |= c != -1;
+                    s_ti[j] = -1;
+                    continue;
+                }
+                const int o = s.at(c);
+                if (o < 0) continue;
+                const int bit_at = o / (int)sizeof(T);
+                const uint32_t bit = 1u << (bit_at & 31);
+                if (atomicOr(&s_bits[bit_at >> 5], bit) & bit) {  // listed twice
+                    bad = true;
+                    s_ti[j] = -1;
+                    continue;
+                }
+                off[e] = o;
+                const float v = Elem<T>::get(reinterpret_cast<const T*>(buf + o));
+                s_zl[j] = v;
+                if (CL)
+                    for (int r = 0; r < cs; r++) st_remote(remote(s_zl + j, r), v);
+                if (rest) *reinterpret_cast<T*>(buf + o) = Elem<T>::put(-INFINITY);
+            }
+            if (bad) atomicOr(&a.flags[FLAG_BAD_TOKEN], 1);
+        }
+        if (rest) group_sync<NT>();
+        // the teacher's probabilities (every CTA of a cluster has them all)
+        float base = 0.0f, W = 0.0f;
+        bool used = false;
+        if (warp == 0) {
+            float t[LIST_PER_LANE];
+            float tm = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < LIST_PER_LANE; e++) {
+                const int j = lane + 32 * e;
+                const bool on = j < k && s_ti[j] >= 0;
+                used |= on;
+                t[e] = on ? s_tv[j] * it : -INFINITY;
+                tm = fmaxf(tm, t[e]);
+            }
+            used = __any_sync(0xffffffffu, used);
+            if (rest) {
+                base = s_tl[b];
+            } else {
+                tm = warp_max(tm);
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < LIST_PER_LANE; e++) sum += t[e] == -INFINITY ? 0.0f : ex2f((t[e] - tm) * LOG2E);
+                base = tm + logf(warp_sum(sum));
+            }
+#pragma unroll
+            for (int e = 0; e < LIST_PER_LANE; e++) {
+                const int j = lane + 32 * e;
+                const float p = t[e] == -INFINITY ? 0.0f : ex2f((t[e] - base) * LOG2E);
+                if (j < k) s_p[j] = p;
+                W += p;
+            }
+            W = warp_sum(W);
+        }
+
+        // first pass: sums of exponentials
+        const bool hard = hard_on && y >= 0;
+        float R = -INFINITY, s1, st;
+        {
+            f2 acc1 = pk(0.0f, 0.0f), acct = acc1;
+            const f2 c1 = pk(LOG2E, LOG2E), c2 = pk(ct, ct);
+            for (int g = s.g0 + tid; g < s.g1; g += NT) {
+                const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+                const float vm = Elem<T>::vmax(u);
+                if (vm > R + lift) {
+                    const float f1 = rescale(R, vm, LOG2E), ft = rescale(R, vm, ct);
+                    acc1 = mul2(acc1, pk(f1, f1));
+                    acct = mul2(acct, pk(ft, ft));
+                    R = vm;
+                }
+                const float nr = -ref_of(R);
+                f2 e[EPG / 2];
+                Elem<T>::unpack(u, e);
+#pragma unroll
+                for (int i = 0; i < EPG / 2; i++) e[i] = add2(e[i], pk(nr, nr));
+                float x, v;
+                if (soft_on) {
+#pragma unroll
+                    for (int i = 0; i < EPG / 2; i++) {
+                        unpk(mul2(e[i], c2), x, v);
+                        acct = add2(acct, pk(ex2f(x), ex2f(v)));
+                    }
+                }
+                if (hard) {
+#pragma unroll
+                    for (int i = 0; i < EPG / 2; i++) {
+                        unpk(mul2(e[i], c1), x, v);
+                        acc1 = add2(acc1, pk(ex2f(x), ex2f(v)));
+                    }
+                }
+            }
+            float x, v;
+            unpk(acc1, x, v);
+            s1 = x + v;
+            unpk(acct, x, v);
+            st = x + v;
+        }
+        warp_merge(R, s1, LOG2E, st, ct);
+        if (NT > 32) {
+            if (lane == 0) s_part[warp] = make_float4(R, s1, st, 0.0f);
+            __syncthreads();
+        }
+        if (warp == 0 && NT > 32) {
+            const float4 p = lane < NT / 32 ? s_part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            R = p.x; s1 = p.y; st = p.z;
+            warp_merge(R, s1, LOG2E, st, ct);
+        }
+        if (CL) {
+            if (warp == 0 && lane < cs) {
+                const uint32_t at = remote(s_x + par * cs + rank, lane);
+                st_remote(at, R);
+                st_remote(at + 4, s1);
+                st_remote(at + 8, st);
+            }
+            cluster_sync();
+            if (warp == 0) {
+                const float4 p = lane < cs ? s_x[par * cs + lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+                R = p.x; s1 = p.y; st = p.z;
+                warp_merge(R, s1, LOG2E, st, ct);
+            }
+        }
+        // the row's loss and the coefficients of its gradient
+        const float ks = g_all * a.alpha * a.tau, kh = hard ? g_all * (1.0f - a.alpha) : 0.0f;
+        if (warp == 0) {
+            __syncwarp();
+            const bool soft = used && soft_on;
+            float zl[LIST_PER_LANE];
+#pragma unroll
+            for (int e = 0; e < LIST_PER_LANE; e++) {
+                const int j = lane + 32 * e;
+                zl[e] = j < k && s_ti[j] >= 0 ? s_zl[j] : -INFINITY;
+            }
+            const float sr0 = st;
+            float sr = sr0;
+            if (rest) {  // the sums so far are without the list
+                float m = R;
+#pragma unroll
+                for (int e = 0; e < LIST_PER_LANE; e++) m = fmaxf(m, zl[e]);
+                m = warp_max(m);
+                float l1 = 0.0f, lt = 0.0f;
+#pragma unroll
+                for (int e = 0; e < LIST_PER_LANE; e++)
+                    if (zl[e] != -INFINITY) {
+                        l1 += exp_of(zl[e], m, LOG2E);
+                        lt += exp_of(zl[e], m, ct);
+                    }
+                s1 = s1 * rescale(R, m, LOG2E) + warp_sum(l1);
+                sr = sr0 * rescale(R, m, ct);
+                st = sr + warp_sum(lt);
+                R = m;
+            }
+            float loss = 0.0f, off_c = 0.0f, Wl = W;
+            if (soft) {
+                const float ls = logf(st);
+                float part = 0.0f;
+#pragma unroll
+                for (int e = 0; e < LIST_PER_LANE; e++) {
+                    const int j = lane + 32 * e;
+                    if (j < k && s_ti[j] >= 0) {
+                        const float p = s_p[j];
+                        if (p > 0.0f || p != p) part += p * ((s_tv[j] * it - base) - ((zl[e] - R) * it - ls));
+                    }
+                }
+                loss = warp_sum(part);
+                off_c = Wl;
+                if (rest && sr > 0.0f) {
+                    const float pr = fmaxf(1.0f - W, 0.0f);
+                    if (pr > 0.0f) loss += pr * (logf(pr) - (logf(sr) - ls));
+                    Wl += pr;
+                    off_c = Wl - pr * st / sr;
+                }
+                loss *= a.alpha * a.tau * a.tau;
+            }
+            if (hard) loss += (1.0f - a.alpha) * (R + logf(s1) - s_zl[k]);
+            if (lane == 0) {
+                s_fin[0] = R;
+                s_fin[1] = soft ? ks * off_c / st : 0.0f;
+                s_fin[2] = hard ? kh / s1 : 0.0f;
+                s_fin[3] = soft ? ks * Wl / st : 0.0f;
+                s_fin[4] = soft ? 1.0f : 0.0f;
+                if (rank == 0) a.row_loss[row] = loss;
+            }
+        }
+        group_sync<NT>();
+        const float m = s_fin[0], At = s_fin[1], A1 = s_fin[2];
+        const bool soft = s_fin[4] != 0.0f;
+        const long long next = row + a.nbuf * stride;
+        if (dz) {
+            // second pass: the gradient
+            char* drow = reinterpret_cast<char*>(dz + row * a.ld);
+            const f2 nm = pk(-m, -m), c1 = pk(LOG2E, LOG2E), c2 = pk(ct, ct), a1 = pk(A1, A1), at = pk(At, At);
+            for (int g = s.g0 + tid; g < s.g1; g += NT) {
+                const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+                f2 e[EPG / 2], r[EPG / 2];
+                Elem<T>::unpack(u, e);
+#pragma unroll
+                for (int i = 0; i < EPG / 2; i++) {
+                    e[i] = add2(e[i], nm);
+                    r[i] = pk(0.0f, 0.0f);
+                }
+                float x, v;
+                if (soft) {
+#pragma unroll
+                    for (int i = 0; i < EPG / 2; i++) {
+                        unpk(mul2(e[i], c2), x, v);
+                        r[i] = mul2(pk(ex2f(x), ex2f(v)), at);
+                    }
+                }
+                if (hard) {
+#pragma unroll
+                    for (int i = 0; i < EPG / 2; i++) {
+                        unpk(mul2(e[i], c1), x, v);
+                        r[i] = fma2(pk(ex2f(x), ex2f(v)), a1, r[i]);
+                    }
+                }
+                if (a.same_phase && s.inner(g)) {
+                    *reinterpret_cast<uint4*>(drow - s.ph + (long long)g * 16) = Elem<T>::pack(r);
+                } else {
+                    const int c0 = s.col(g);
+#pragma unroll
+                    for (int i = 0; i < EPG / 2; i++) {
+                        unpk(r[i], x, v);
+                        const int c = c0 + 2 * i;
+                        if (c >= 0 && c < V) reinterpret_cast<T*>(drow)[c] = Elem<T>::put(x);
+                        if (c + 1 >= 0 && c + 1 < V) reinterpret_cast<T*>(drow)[c + 1] = Elem<T>::put(v);
+                    }
+                }
+            }
+            if (rank == cs - 1)
+                for (long long c = V + tid; c < a.ld; c += NT) reinterpret_cast<T*>(drow)[c] = Elem<T>::put(0.0f);
+        }
+        if (next < a.M) fill<T, NT>(slice(next), buf, tid);
+        group_sync<NT>();  // the second pass's stores come before those of the list
+        if (warp == 0) {
+            T* drow = dz ? dz + row * a.ld : nullptr;
+            const float Al = s_fin[3];
+            bool y_listed = false;
+#pragma unroll
+            for (int e = 0; e < LIST_PER_LANE; e++) {
+                const int j = lane + 32 * e;
+                if (j >= k) continue;
+                const int c = s_ti[j];
+                y_listed |= c >= 0 && c == y;
+                if (off[e] < 0) continue;
+                s_bits[off[e] / (int)sizeof(T) >> 5] = 0;
+                if (!drow) continue;
+                float r = 0.0f;
+                if (soft) r = Al * exp_of(s_zl[j], m, ct) - ks * s_p[j];
+                if (hard) r += A1 * exp_of(s_zl[j], m, LOG2E) - (c == y ? kh : 0.0f);
+                drow[c] = Elem<T>::put(r);
+            }
+            y_listed = __any_sync(0xffffffffu, y_listed);
+            if (drow && hard && !y_listed && lane == 0 && s.at(y) >= 0) {
+                float r = A1 * exp_of(s_zl[k], m, LOG2E) - kh;
+                if (soft) r += At * exp_of(s_zl[k], m, ct);
+                drow[y] = Elem<T>::put(r);
+            }
+            if (next < a.M) copy_lists(next, b);
+        }
+        cp_commit();
+        const long long n1 = row + stride, n2 = n1 + stride;
+        if (n1 < a.M) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
+        if (n2 < a.M) edge = edge_load(slice(n2), V, tid);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // mean of M row losses: each thread adds rows t, t + 1024, ..., the threads'
@@ -260,14 +808,11 @@ __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row
     __shared__ float s_w[32];
     float s = 0.0f;
     for (int i = threadIdx.x; i < M; i += 1024) s += row_loss[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s = warp_sum(s);
     if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = s;
     __syncthreads();
     if (threadIdx.x < 32) {
-        s = s_w[threadIdx.x];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s = warp_sum(s_w[threadIdx.x]);
         if (threadIdx.x == 0) {
             s /= (float)M;
             out[0] = s;
@@ -276,40 +821,128 @@ __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row
     }
 }
 
-template <typename T>
-bool top_rows(const Launch& L, const void* z, long long ld, int V, int k, float inv_tau, float* vals, int32_t* idx,
-              float* lse, double* lse64, const int32_t* skip, int M) {
-    L.count();
-    launch_k(L, k_top_rows<T>, dim3(M), dim3(HD_THREADS), 0, (const T*)z, ld, V, k, inv_tau, vals, idx, lse, lse64,
-             skip);
+// ------------------------------------------------------------ launch
+// How M rows of G granules are spread: the group size, the CTAs a row is
+// shared by, and whether two rows of a group are on chip at once.
+struct Plan {
+    int nt = 0, cs = 1, nbuf = 2, Gs = 0, ctas = 0;
+    size_t smem = 0;
+};
+
+constexpr size_t SMEM_CTA = 232448;  // 227 KB
+constexpr size_t SMEM_SM = 233472;   // 228 KB, of which each CTA takes 1 KB more than its own
+
+template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, Bytes&& bytes) {
+    p.cs = 1;
+    // a row that does not fit twice is cut; few rows are cut so that every SM has a part
+    auto fits = [&](int cs, int nbuf) { return bytes(1024, (G + cs - 1) / cs, nbuf, cs > 1) <= SMEM_CTA; };
+    while (p.cs < CS_MAX && !fits(p.cs, 2)) p.cs *= 2;
+    p.nbuf = fits(p.cs, 2) ? 2 : 1;
+    if (!fits(p.cs, p.nbuf)) return false;
+    while (p.cs < CS_MAX && M * p.cs * 2 <= sms && G / (p.cs * 2) >= 256) p.cs *= 2;
+    p.Gs = (G + p.cs - 1) / p.cs;
+    p.nt = p.cs == 1 && G <= 128 ? 32 : p.Gs <= 2048 ? 256 : 1024;
+    p.smem = (size_t)bytes(p.nt, p.Gs, p.nbuf, p.cs > 1) * cta_groups(p.nt);
+    const long long groups = (M + cta_groups(p.nt) - 1) / cta_groups(p.nt);
+    const int per_sm = std::max<int>(1, std::min<int>(p.nt == 1024 ? 1 : 4, (int)(SMEM_SM / (p.smem + 1024))));
+    const long long room = std::max<long long>(1, (long long)sms * per_sm / p.cs);
+    p.ctas = (int)(std::min(groups, room) * p.cs);
     return true;
 }
 
-template <typename T>
-bool distill(const Launch& L, const void* z, void* dz, const DistillArgs& a, int M) {
-    static PerDevice attr;
-    const size_t smem = (size_t)((a.V + 31) / 32) * 4;
-    if (!attr.once([] {
-            return cudaFuncSetAttribute(k_distill<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) ==
-                   cudaSuccess;
+template <typename K> bool allow_smem(PerDevice& attr, K kern) {
+    return attr.once([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_CTA) == cudaSuccess;
+    });
+}
+
+template <typename... KA, typename... A>
+void launch_rows(const Launch& L, void (*kern)(KA...), const Plan& p, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    cfg.blockDim = dim3((unsigned)cta_threads(p.nt));
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute at[2];
+    unsigned n = 0;
+    if (L.pdl) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (p.cs > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = (unsigned)p.cs;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        n++;
+    }
+    cfg.attrs = at;
+    cfg.numAttrs = n;
+    L.count();
+    cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+
+#define ROW_KERNEL(NAME, NT_, CL_, ...)                            \
+    do {                                                           \
+        static PerDevice attr;                                     \
+        if (!allow_smem(attr, NAME<T, NT_, CL_>)) return false;    \
+        launch_rows(L, NAME<T, NT_, CL_>, p, __VA_ARGS__);         \
+        return true;                                               \
+    } while (0)
+
+// granules of a row, for the worst place of its start
+template <typename T> int row_granules(const void* z, long long ld, int V) {
+    const bool aligned = ((uintptr_t)z & 15) == 0 && ld * (long long)sizeof(T) % 16 == 0;
+    return (int)(((aligned ? 0 : 16 - (int)sizeof(T)) + (long long)V * (int)sizeof(T) + 15) / 16);
+}
+
+template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
+    Plan p;
+    const int k = a.k;
+    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), [k](int nt, int Gs, int nbuf, bool cl) {
+            return (size_t)TopLayout(nt, Gs, nbuf, k, cl).total;
         }))
         return false;
-    L.count();
-    launch_k(L, k_distill<T>, dim3(M), dim3(HD_THREADS), smem, (const T*)z, (T*)dz, a);
-    return true;
+    a.Gs = p.Gs; a.cs = p.cs; a.nbuf = p.nbuf;
+    if (p.nt == 32) ROW_KERNEL(k_top_rows, 32, false, (const T*)z, a);
+    if (p.nt == 256 && p.cs == 1) ROW_KERNEL(k_top_rows, 256, false, (const T*)z, a);
+    if (p.nt == 256) ROW_KERNEL(k_top_rows, 256, true, (const T*)z, a);
+    if (p.cs == 1) ROW_KERNEL(k_top_rows, 1024, false, (const T*)z, a);
+    ROW_KERNEL(k_top_rows, 1024, true, (const T*)z, a);
+}
+
+template <typename T> bool distill(const Launch& L, const void* z, void* dz, DistillArgs a) {
+    Plan p;
+    const int k = a.k;
+    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), [k](int nt, int Gs, int nbuf, bool cl) {
+            return (size_t)DistillLayout(nt, Gs, nbuf, k, Elem<T>::EPG, cl).total;
+        }))
+        return false;
+    a.Gs = p.Gs; a.cs = p.cs; a.nbuf = p.nbuf;
+    a.same_phase = (((uintptr_t)z ^ (uintptr_t)dz) & 15) == 0;
+    if (p.nt == 32) ROW_KERNEL(k_distill, 32, false, (const T*)z, (T*)dz, a);
+    if (p.nt == 256 && p.cs == 1) ROW_KERNEL(k_distill, 256, false, (const T*)z, (T*)dz, a);
+    if (p.nt == 256) ROW_KERNEL(k_distill, 256, true, (const T*)z, (T*)dz, a);
+    if (p.cs == 1) ROW_KERNEL(k_distill, 1024, false, (const T*)z, (T*)dz, a);
+    ROW_KERNEL(k_distill, 1024, true, (const T*)z, (T*)dz, a);
 }
 
 }  // namespace
 
-bool head_row_ok(tt_dtype dtype, int V) { return (dtype == TT_FP32 || dtype == TT_BF16 || dtype == TT_FP16) && V < 1048576; }
+// a row is held by at most CS_MAX CTAs, which also need room for the lists
+bool head_row_ok(tt_dtype dtype, int V) {
+    if (dtype != TT_FP32 && dtype != TT_BF16 && dtype != TT_FP16) return false;
+    return (long long)V * (dtype == TT_FP32 ? 4 : 2) <= TT_ROW_BYTES_MAX;
+}
 
 bool launch_top_rows(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, float tau,
                      float* vals, int32_t* idx, float* lse, double* lse64, const int32_t* skip) {
     if (L.dry) return true;
-    const float it = 1.0f / tau;
-    if (dtype == TT_FP32) return top_rows<float>(L, z, ld, V, k, it, vals, idx, lse, lse64, skip, M);
-    if (dtype == TT_FP16) return top_rows<__half>(L, z, ld, V, k, it, vals, idx, lse, lse64, skip, M);
-    return top_rows<__nv_bfloat16>(L, z, ld, V, k, it, vals, idx, lse, lse64, skip, M);
+    TopArgs a{};
+    a.vals = vals; a.idx = idx; a.lse = lse; a.lse64 = lse64; a.skip = skip;
+    a.ld = ld; a.M = M; a.V = V; a.k = k; a.inv_tau = 1.0f / tau;
+    if (dtype == TT_FP32) return top_rows<float>(L, z, a);
+    if (dtype == TT_FP16) return top_rows<__half>(L, z, a);
+    return top_rows<__nv_bfloat16>(L, z, a);
 }
 
 bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, const float* t_vals,
@@ -317,14 +950,14 @@ bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, co
                     float* mean_loss, int M, int V, int ld, int k, float alpha, float tau, float dscale,
                     const float* scale_dev) {
     if (L.dry) return true;
-    DistillArgs a;
+    DistillArgs a{};
     a.t_vals = t_vals; a.t_idx = t_idx; a.t_lse = t_lse; a.targets = targets; a.scale_dev = scale_dev;
-    a.row_loss = row_loss; a.V = V; a.ld = ld; a.k = k;
-    a.alpha = alpha; a.tau = tau; a.dscale = dscale; a.flags = L.flags;
+    a.row_loss = row_loss; a.flags = L.flags; a.ld = ld; a.M = M; a.V = V; a.k = k;
+    a.alpha = alpha; a.tau = tau; a.dscale = dscale;
     bool ok;
-    if (dtype == TT_FP32) ok = distill<float>(L, z, dz, a, M);
-    else if (dtype == TT_FP16) ok = distill<__half>(L, z, dz, a, M);
-    else ok = distill<__nv_bfloat16>(L, z, dz, a, M);
+    if (dtype == TT_FP32) ok = distill<float>(L, z, dz, a);
+    else if (dtype == TT_FP16) ok = distill<__half>(L, z, dz, a);
+    else ok = distill<__nv_bfloat16>(L, z, dz, a);
     if (!ok) return false;
     if (mean_loss) {
         L.count();

@@ -1,0 +1,285 @@
+// head_row.cuh -- how the list kernels (head.cu) hold a row of logits.
+//
+// A group of NT threads (a warp, or a CTA; NT = 32, 256 or 1024) works on one
+// row at a time and strides over the rows.  With clusters, the cs CTAs of a
+// cluster share a row, each a slice of it.  The row is cut into granules of 16
+// bytes on 16-byte boundaries of memory; granule i of the slice lives in slot
+// i of a shared-memory buffer and belongs to thread i mod NT, which copies it
+// in (cp.async), reads it in every pass, and refills it with a later row's as
+// soon as it has read it for the last time.  So a pass needs no barrier for
+// the row's data, a row is read from memory once, and the next row (or two)
+// is on its way while this one is computed on.
+//
+// Rows may start anywhere (odd ld, offset pointers): the row's first and last
+// granules, where they are not wholly inside the row, are fetched element by
+// element (by threads 0..15 of the group, a row ahead) and filled up with
+// -inf, which no result depends on; nothing outside the row is read.
+#pragma once
+
+#include "tt_internal.h"
+
+namespace tt {
+namespace head {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// pairs of floats in one 64-bit register: one instruction for two lanes
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pk(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpk(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// ------------------------------------------------------------ storage types
+// A granule of EPG elements as EPG / 2 pairs of floats, its largest element (a
+// NaN counts as -inf), and back.
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+    static constexpr int EPG = 4;
+    static __device__ __forceinline__ float get(const float* p) { return *p; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+    static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
+        f[0] = pk(__uint_as_float(u.x), __uint_as_float(u.y));
+        f[1] = pk(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+    static __device__ __forceinline__ float vmax(const uint4& u) {
+        return fmaxf(fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+                           fmaxf(__uint_as_float(u.z), __uint_as_float(u.w))), -INFINITY);
+    }
+    static __device__ __forceinline__ uint4 pack(const f2* f) {
+        float a, b, c, d;
+        unpk(f[0], a, b);
+        unpk(f[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
+};
+template <> struct Elem<__nv_bfloat16> {
+    static constexpr int EPG = 8;
+    static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+    static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ float vmax(const uint4& u) {
+        using P = __nv_bfloat162;
+        const P a = __hmax2(*reinterpret_cast<const P*>(&u.x), *reinterpret_cast<const P*>(&u.y));
+        const P b = __hmax2(*reinterpret_cast<const P*>(&u.z), *reinterpret_cast<const P*>(&u.w));
+        const P m = __hmax2(a, b);
+        return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+    }
+    static __device__ __forceinline__ uint4 pack(const f2* f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float a, b;
+            unpk(f[i], a, b);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Elem<__half> {
+    static constexpr int EPG = 8;
+    static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
+    static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            f[i] = pk(v.x, v.y);
+        }
+    }
+    static __device__ __forceinline__ float vmax(const uint4& u) {
+        const __half2 a = __hmax2(*reinterpret_cast<const __half2*>(&u.x), *reinterpret_cast<const __half2*>(&u.y));
+        const __half2 b = __hmax2(*reinterpret_cast<const __half2*>(&u.z), *reinterpret_cast<const __half2*>(&u.w));
+        const __half2 m = __hmax2(a, b);
+        return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+    }
+    static __device__ __forceinline__ uint4 pack(const f2* f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float a, b;
+            unpk(f[i], a, b);
+            const __half2 h = __floats2half2_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// ------------------------------------------------------------ copies
+__device__ __forceinline__ void cp16(void* s, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(s)), "l"(g)
+                 : "memory");
+}
+__device__ __forceinline__ void cp4(void* s, const void* g) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(s)), "l"(g)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest (nbuf - 1) groups have arrived
+__device__ __forceinline__ void cp_wait(int nbuf) {
+    if (nbuf == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// every CTA's writes to the others' shared memory before it are seen after it
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* s, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(s)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_remote(uint32_t at, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t at, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+
+// ------------------------------------------------------------ groups
+template <int NT> __device__ __forceinline__ void group_sync() {
+    if (NT == 32) __syncwarp();
+    else __syncthreads();
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// ------------------------------------------------------------ a row's slice
+template <typename T> struct Slice {
+    const char* base;  // the row's first granule (16-byte boundary at or below its start)
+    int ph;            // byte offset of column 0 from base
+    int g0, g1;        // granules of this CTA
+    int gi0, gi1;      // granules wholly inside the row
+    int G;             // granules of the row
+
+    __device__ __forceinline__ Slice(const T* z, long long row, long long ld, int V, int rank, int Gs) {
+        const char* p = reinterpret_cast<const char*>(z + row * ld);
+        ph = (int)((uintptr_t)p & 15);
+        base = p - ph;
+        const int end = ph + V * (int)sizeof(T);
+        G = (end + 15) >> 4;
+        g0 = min(rank * Gs, G);
+        g1 = min(g0 + Gs, G);
+        gi0 = ph ? 1 : 0;
+        gi1 = end >> 4;
+    }
+    // column of the first element of granule g (may be negative at the head)
+    __device__ __forceinline__ int col(int g) const { return (g * 16 - ph) / (int)sizeof(T); }
+    __device__ __forceinline__ bool inner(int g) const { return g >= gi0 && g < gi1; }
+    // byte offset in the buffer of column c, or -1 if another CTA has it
+    __device__ __forceinline__ int at(int c) const {
+        const int b = ph + c * (int)sizeof(T), g = b >> 4;
+        return g >= g0 && g < g1 ? b - g0 * 16 : -1;
+    }
+};
+
+// Copies thread tid's granules of the slice into buf.
+template <typename T, int NT>
+__device__ __forceinline__ void fill(const Slice<T>& s, char* buf, int tid) {
+    for (int g = s.g0 + tid; g < s.g1; g += NT)
+        if (s.inner(g)) cp16(buf + (g - s.g0) * 16, s.base + (long long)g * 16);
+}
+
+// The element of an edge granule that thread tid < 16 of the group looks
+// after: threads 0..7 the head's, 8..15 the tail's.
+template <typename T>
+__device__ __forceinline__ int edge_granule(const Slice<T>& s, int tid) {
+    if (tid >= 16) return -1;
+    const int i = tid & 7;
+    if (i >= Elem<T>::EPG) return -1;
+    int g;
+    if (tid < 8) g = s.gi0 > 0 ? 0 : -1;
+    else g = s.gi1 < s.G && !(s.gi0 > 0 && s.G == 1) ? s.G - 1 : -1;
+    return g >= s.g0 && g < s.g1 ? g : -1;
+}
+template <typename T>
+__device__ __forceinline__ T edge_load(const Slice<T>& s, int V, int tid) {
+    const int g = edge_granule(s, tid);
+    if (g < 0) return Elem<T>::put(-INFINITY);
+    const int c = s.col(g) + (tid & 7);
+    return c >= 0 && c < V ? reinterpret_cast<const T*>(s.base + s.ph)[c] : Elem<T>::put(-INFINITY);
+}
+template <typename T>
+__device__ __forceinline__ void edge_store(const Slice<T>& s, char* buf, T v, int tid) {
+    const int g = edge_granule(s, tid);
+    if (g >= 0) reinterpret_cast<T*>(buf + (g - s.g0) * 16)[tid & 7] = v;
+}
+
+// ------------------------------------------------------------ sums of exponentials
+// A running reference R and sums of e^((z - R) c).  R moves only when a value
+// is more than `lift` above it (the sums are then scaled), so one pass finds
+// the sum without knowing the maximum, at one exponential an element; the sums
+// stay below e^40 times the number of terms.  z - R is formed before the
+// scaling: it is exact or rounded once, and finite however large the logits
+// are (a mask of the type's lowest value).
+__device__ __forceinline__ float exp_of(float z, float r, float c) { return ex2f((z - r) * c); }
+
+// the reference that stands for R in arguments (an empty sum has R = -inf)
+__device__ __forceinline__ float ref_of(float R) { return R == -INFINITY ? 0.0f : R; }
+
+// what a sum with reference `from` is multiplied by to have the larger reference `to`
+__device__ __forceinline__ float rescale(float from, float to, float c) {
+    if (from == to) return 1.0f;
+    return from == -INFINITY ? 0.0f : ex2f((from - to) * c);
+}
+
+// Merges the lanes' sums; a lane without terms has R = -inf and 0.
+__device__ __forceinline__ void warp_merge(float& R, float& s, float c) {
+    const float m = warp_max(R);
+    s = warp_sum(s * rescale(R, m, c));
+    R = m;
+}
+__device__ __forceinline__ void warp_merge(float& R, float& s, float c, float& t, float ct) {
+    const float m = warp_max(R);
+    s = warp_sum(s * rescale(R, m, c));
+    t = warp_sum(t * rescale(R, m, ct));
+    R = m;
+}
+
+}  // namespace head
+}  // namespace tt

@@ -122,6 +122,7 @@ tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int
 
 #define TT_TOP_MAX 128  /* longest list of a row */
 #define TT_BEAM_MAX 32  /* most beams of a sequence */
+#define TT_ROW_BYTES_MAX 1600000  /* most bytes of the V logits of a row (a row is held on chip) */
 
 /* The k largest logits of each row, in descending order, equal ones by
  * ascending column (-0 equals +0):
@@ -152,8 +153,8 @@ tt_status tt_op_top_logits(tt_ctx* ctx, tt_dtype dtype, const void* logits, floa
  * means that the row has no cross entropy term (targets may be NULL when
  * alpha is 1).  A row with neither has loss 0 and gradient 0, whatever its
  * logits hold.  A target or index outside these ranges, or an index that a row
- * lists twice, raises the bad token flag (tt_ctx_sync: TT_ERR_ARG); that entry
- * does not count.  0 <= alpha <= 1, tau > 0, 1 <= k <= min(V, TT_TOP_MAX).
+ * lists twice, raises the bad token flag (tt_ctx_sync: TT_ERR_ARG); what the
+ * row then receives is undefined.  0 <= alpha <= 1, tau > 0, 1 <= k <= min(V, TT_TOP_MAX).
  * Deterministic. */
 tt_status tt_op_distill(tt_ctx* ctx, tt_dtype dtype, const void* logits, const float* t_vals, const int32_t* t_idx,
                         const float* t_lse, const int32_t* targets, void* dlogits, float* row_loss,
