@@ -20,6 +20,11 @@ namespace {
 // 32-bit sum would tie or swap candidates that differ by less than 1e-5.
 // A beam without a distribution (its log-sum-exp is not finite) or without a
 // finite score offers -inf only.  Order: score, then the lowest j V + v.
+//
+// Beams with the same score and the same list are the same hypothesis as far
+// as this step goes, and their candidates have to tie; but a row's
+// log-sum-exp depends in its last bits on how the row lies in memory.  Such a
+// beam takes the log-sum-exp of the first one it equals.
 constexpr int BM_THREADS = 256;
 constexpr int BM_MAX = 2048;  // K * n
 
@@ -31,34 +36,57 @@ k_beam_merge(const float* __restrict__ vals, const int32_t* __restrict__ idx, co
     pdl_enter();
     __shared__ double s_s[BM_MAX];
     __shared__ int s_f[BM_MAX];  // j V + v
-    const int b = blockIdx.x, N = K * kk;
-    for (int i = threadIdx.x; i < N; i += BM_THREADS) {
+    __shared__ double s_lse[TT_BEAM_MAX];
+    __shared__ float s_sc[TT_BEAM_MAX];
+    __shared__ int s_as[TT_BEAM_MAX];  // the beam whose log-sum-exp counts; -1: a finished one
+    const int b = blockIdx.x, N = K * kk, tid = threadIdx.x;
+    const long long row0 = (long long)b * K;
+    if (tid < K) {
+        const bool over = done && done[row0 + tid] != 0;
+        const double l = over ? 0.0 : lse[row0 + tid];
+        s_sc[tid] = scores[row0 + tid];
+        s_lse[tid] = l;
+        s_as[tid] = over ? -1 : tid;
+        if (l != l || l == INFINITY) atomicOr(&flags[FLAG_NONFINITE], 1);
+    }
+    __syncthreads();
+    if (tid > 0 && tid < K && s_as[tid] >= 0) {
+        for (int j = 0; j < tid; j++) {
+            if (s_sc[j] != s_sc[tid] || s_as[j] < 0 || !(fabs(s_lse[j] - s_lse[tid]) <= 1e-6 * (1.0 + fabs(s_lse[j])))) continue;
+            const long long p = (row0 + j) * kk, q = (row0 + tid) * kk;
+            int same = 0;
+            while (same < kk && vals[p + same] == vals[q + same] && idx[p + same] == idx[q + same]) same++;
+            if (same == kk) {
+                s_as[tid] = j;  // the first such: it stands for itself
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < N; i += BM_THREADS) {
         const int j = i / kk, r = i % kk;
-        const long long row = (long long)b * K + j;
-        const float s = scores[row];
-        const bool over = done && done[row] != 0;
+        const float s = s_sc[j];
         double c = -INFINITY;
         int v = r;
-        if (over) {
+        if (s_as[j] < 0) {
             if (s > -INFINITY) {
                 v = r == 0 ? eos : (r - 1 < eos ? r - 1 : r);
                 if (r == 0) c = (double)s;
             }
         } else {
-            const double l = lse[row];
-            if (r == 0 && (l != l || l == INFINITY)) atomicOr(&flags[FLAG_NONFINITE], 1);
+            const double l = s_lse[s_as[j]];
             if (isfinite(l) && s > -INFINITY) {
-                v = idx[row * kk + r];
-                c = (double)s + ((double)vals[row * kk + r] - l);
+                v = idx[(row0 + j) * kk + r];
+                c = (double)s + ((double)vals[(row0 + j) * kk + r] - l);
             }
         }
         s_s[i] = c != c ? -INFINITY : c;
         s_f[i] = j * V + v;
     }
-    // a finished parent's flag, read before any output is written: outputs may be the inputs' arrays
+    // everything of the inputs is read before an output is written: they may be the same arrays
     uint32_t over_mask = 0;
     if (done)
-        for (int j = 0; j < K; j++) over_mask |= (done[(long long)b * K + j] != 0 ? 1u : 0u) << j;
+        for (int j = 0; j < K; j++) over_mask |= (s_as[j] < 0 ? 1u : 0u) << j;
     __syncthreads();
     for (int i = threadIdx.x; i < N; i += BM_THREADS) {
         const double c = s_s[i];

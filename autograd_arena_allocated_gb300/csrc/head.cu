@@ -21,9 +21,11 @@ using namespace head;
 constexpr int LIST_MAX = TT_TOP_MAX;
 constexpr int LIST_PER_LANE = LIST_MAX / 32;
 constexpr int CS_MAX = 8;      // CTAs of a cluster (the portable limit)
-constexpr int CAND_MAX = 1024;  // candidates of a row's (or slice's) list
+constexpr int CAND_MAX = 512;  // candidates of a row's (or slice's) list, and granules that hold them
+constexpr int THR_MAX = 256;   // thread maxima that a threshold is chosen from
 
 __host__ __device__ constexpr int cta_threads(int NT) { return NT == 32 ? 256 : NT; }
+__host__ __device__ constexpr int cta_per_sm(int NT) { return NT == 512 ? 2 : 4; }
 __host__ __device__ constexpr int cta_groups(int NT) { return NT == 32 ? 8 : 1; }
 __host__ __device__ constexpr int align16(int n) { return (n + 15) & ~15; }
 
@@ -61,11 +63,12 @@ struct TopArgs {
 
 // shared memory of a group, in bytes from its start
 struct TopLayout {
-    int cand, thr, part, red, lists, x, cnt, total;
+    int cand, thr, gl, part, red, lists, x, cnt, total;
     __host__ __device__ TopLayout(int nt, int Gs, int nbuf, int k, bool cl) {
         int at = nbuf * Gs * 16;
         cand = at; at += (nt > 32 ? CAND_MAX : LIST_MAX) * 8;  // a warp's candidates are exact ones
-        thr = at; at += nt > 32 ? 128 : 0;
+        thr = at; at += nt > 32 ? 4 * THR_MAX + 16 : 0;
+        gl = at; at += nt > 32 ? 4 * CAND_MAX : 0;
         part = at; at += nt > 32 ? 256 : 0;
         red = at; at += nt > 32 ? 256 : 0;
         lists = at; at += cl ? align16(2 * CS_MAX * k * 8) : 0;
@@ -160,20 +163,22 @@ __device__ void exact_candidates(const Slice<T>& s, const char* buf, int V, int 
 }
 
 // A row's list in four stages:
-//   1. one pass over the granules: each thread's largest value, and its sum of
+//   1. one pass over the granules: each thread's largest value and its sum of
 //      exponentials;
-//   2. a threshold: with fw warps that have work in every lane, the lowest of
-//      their q-th largest thread maxima, q = ceil(k / fw).  fw q >= k threads
-//      have a value at or above it, so the list lies there;
-//   3. the elements at or above the threshold become candidates (about 3 fw
-//      for small q on unordered data);
+//   2. a threshold: each of the fw warps that have work in every lane gives its
+//      Q largest thread maxima, Q = ceil(k / fw) + 2, and the k-th largest of
+//      these fw Q values is the threshold.  At least k elements are at or
+//      above it;
+//   3. threads whose largest value is at or above it name their granules that
+//      are, and all threads look through those for the elements: the
+//      candidates, on unordered data a few more than k;
 //   4. each candidate's rank among them by counting, a warp per candidate.
 // With more than CAND_MAX candidates, or too few threads for a threshold, the
 // candidates are found exactly instead.  Clusters: each CTA lists its slice
 // and sends the list to CTA 0, which ranks every entry by binary searches in
 // the other lists.
 template <typename T, int NT, bool CL>
-__global__ void __launch_bounds__(cta_threads(NT), NT == 1024 ? 1 : 4)
+__global__ void __launch_bounds__(cta_threads(NT), cta_per_sm(NT))
 k_top_rows(const T* __restrict__ z, const TopArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) char smem[];
@@ -182,7 +187,8 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
     const TopLayout lay(NT, a.Gs, a.nbuf, a.k, CL);
     char* sm = smem + (NT == 32 ? threadIdx.x >> 5 : 0) * lay.total;
     auto* s_cand = reinterpret_cast<unsigned long long*>(sm + lay.cand);
-    float* s_thr = reinterpret_cast<float*>(sm + lay.thr);
+    uint32_t* s_thr = reinterpret_cast<uint32_t*>(sm + lay.thr);
+    int* s_gl = reinterpret_cast<int*>(sm + lay.gl);
     float2* s_part = reinterpret_cast<float2*>(sm + lay.part);
     int* s_red = reinterpret_cast<int*>(sm + lay.red);
     auto* s_lists = reinterpret_cast<unsigned long long*>(sm + lay.lists);  // [2][cs][k]
@@ -192,8 +198,9 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
     const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
     const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
     const bool want = a.lse || a.lse64;
-    const float ct = LOG2E * a.inv_tau, lift = 28.0f / fmaxf(1.0f, a.inv_tau);
+    const float ct = LOG2E * a.inv_tau, lift = 20.0f / fmaxf(1.0f, a.inv_tau);
     const int k = a.k, V = a.V;
+    using E = Elem<T>;
     auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, rank, a.Gs); };
     auto here = [&](long long r) { return r < a.M && !(a.skip && a.skip[r]); };
 
@@ -205,7 +212,7 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
     T edge = Elem<T>::put(0.0f);
     if (here(first)) edge_store(slice(first), sm, edge_load(slice(first), V, tid), tid);
     if (here(first + stride)) edge = edge_load(slice(first + stride), V, tid);
-    if (tid == 0) *s_cnt = 0;
+    if (tid == 0) s_cnt[0] = s_cnt[1] = 0;  // candidates, granules
     if (CL) cluster_sync();  // the others run: their shared memory may be written
 
     int it = 0;
@@ -219,95 +226,74 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
         const long long next = row + a.nbuf * stride;
         if (run) {
             // stage 1
-            float tmax = -INFINITY, R = -INFINITY, sum = 0.0f;
-            f2 acc = pk(0.0f, 0.0f);
-            const f2 ct2 = pk(ct, ct);
-            for (int g = s.g0 + tid; g < s.g1; g += NT) {
-                const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
-                const float vm = Elem<T>::vmax(u);
-                tmax = fmaxf(tmax, vm);
-                if (want) {
-                    if (vm > R + lift) {
-                        const float f = rescale(R, vm, ct);
-                        acc = mul2(acc, pk(f, f));
-                        R = vm;
-                    }
-                    const float nr = -ref_of(R);
-                    f2 e[Elem<T>::EPG / 2];
-                    Elem<T>::unpack(u, e);
-#pragma unroll
-                    for (int i = 0; i < Elem<T>::EPG / 2; i++) {
-                        float x, y;
-                        unpk(mul2(add2(e[i], pk(nr, nr)), ct2), x, y);
-                        acc = add2(acc, pk(ex2f(x), ex2f(y)));
-                    }
-                }
-            }
+            float tmax, R, sum, none;
             if (want) {
-                float x, y;
-                unpk(acc, x, y);
-                sum = x + y;
-                if (R == INFINITY) {  // inf - inf above: what is left to know is whether there is a NaN
-                    sum = 0.0f;
-                    for (int g = s.g0 + tid; g < s.g1; g += NT)
-                        for (int i = 0; i < Elem<T>::EPG; i++) {
-                            const float v = Elem<T>::get(reinterpret_cast<const T*>(buf + (g - s.g0) * 16) + i);
-                            if (v != v) sum = v;
-                        }
-                }
+                sum_pass<T, NT, true, false>(s, buf, tid, ct, ct, lift, tmax, R, sum, none);
                 warp_merge(R, sum, ct);
+            } else {
+                sum_pass<T, NT, false, false>(s, buf, tid, ct, ct, lift, tmax, R, sum, none);
             }
             // stage 2
             const int n_slots = s.g1 - s.g0;
             const int n_el = max(0, min(V, s.col(s.g1)) - max(0, s.col(s.g0)));
             const int kk = min(k, n_el);
             const int fw = NT == 32 ? 0 : min(NT, n_slots) / 32;
-            const int q = fw ? (k + fw - 1) / fw : 33;
-            bool exact = q > 16;
+            const int Q = fw ? min(32, (k + fw - 1) / fw + 2) : 0;
+            bool exact = fw * Q < k || fw * Q > THR_MAX;
             int cnt = 0;
             if (NT > 32) {
-                float m = INFINITY;
                 if (!exact && warp < fw) {
-                    float cur = tmax;
-                    for (int i = 0;; i++) {
-                        m = warp_max(cur);
-                        if (i == q - 1) break;
-                        if (lane == __ffs(__ballot_sync(0xffffffffu, cur == m)) - 1) cur = -INFINITY;
+                    uint32_t cur = order_of(tmax), mine = 0;
+                    for (int i = 0; i < Q; i++) {
+                        const uint32_t m = __reduce_max_sync(0xffffffffu, cur);
+                        if (lane == i) mine = m;
+                        if (lane == __ffs(__ballot_sync(0xffffffffu, cur == m)) - 1) cur = 0;
                     }
+                    if (lane < Q) s_thr[warp * Q + lane] = mine;
                 }
-                if (lane == 0) {
-                    s_thr[warp] = m;
-                    s_part[warp] = make_float2(R, sum);
-                }
+                if (lane == 0) s_part[warp] = make_float2(R, sum);
                 __syncthreads();
                 if (!exact) {
-                    // stage 3
-                    const float thr = -warp_max(lane < NT / 32 ? -s_thr[lane] : -INFINITY);
-                    if (tmax >= thr) {
-                        for (int g = s.g0 + tid; g < s.g1; g += NT) {
-                            const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
-                            if (Elem<T>::vmax(u) < thr) continue;
-                            f2 e[Elem<T>::EPG / 2];
-                            Elem<T>::unpack(u, e);
-                            const int c0 = s.col(g);
-#pragma unroll
-                            for (int i = 0; i < Elem<T>::EPG; i++) {
-                                float x, y;
-                                unpk(e[i / 2], x, y);
-                                const float v = fmaxf(i & 1 ? y : x, -INFINITY);
-                                const int c = c0 + i;
-                                if (v >= thr && c >= 0 && c < V) {
-                                    const int p = atomicAdd(s_cnt, 1);
-                                    if (p < CAND_MAX) s_cand[p] = top_key(v, c);
-                                }
-                            }
+                    // the k-th largest of the fw Q values
+                    const int nv = fw * Q;
+                    for (int i = warp; i < nv; i += NT / 32) {
+                        const uint32_t x = s_thr[i];
+                        int r = 0;  // how many are larger, and (in the upper half) at least as large
+                        for (int j = lane; j < nv; j += 32) {
+                            const uint32_t w = s_thr[j];
+                            r += (w > x) + ((w >= x) << 16);
                         }
+                        r = __reduce_add_sync(0xffffffffu, r);
+                        if (lane == 0 && (r & 0xFFFF) < k && (r >> 16) >= k) s_thr[THR_MAX] = x;
                     }
                     __syncthreads();
-                    cnt = *s_cnt;
-                    if (cnt > CAND_MAX) {
-                        __syncthreads();  // every thread has read the count
-                        exact = true;
+                    // stage 3
+                    const float thr = value_of(s_thr[THR_MAX]);
+                    const typename E::Max thr2 = E::to_max(thr);
+                    if (tmax >= thr) {
+                        for (int i = tid; i < n_slots; i += NT)
+                            if (E::at_least(E::gmax(reinterpret_cast<const uint4*>(buf)[i]), thr2)) {
+                                const int p = atomicAdd(s_cnt + 1, 1);
+                                if (p < CAND_MAX) s_gl[p] = i;
+                            }
+                    }
+                    __syncthreads();
+                    const int ng = s_cnt[1];
+                    exact = ng > CAND_MAX;
+                    if (!exact) {
+                        for (int i = tid; i < ng * E::EPG; i += NT) {
+                            const int slot = s_gl[i / E::EPG], e = i % E::EPG;
+                            const float w = fmaxf(E::get(reinterpret_cast<const T*>(buf + slot * 16) + e), -INFINITY);
+                            const int c = s.col(s.g0 + slot) + e;
+                            if (w >= thr && c >= 0 && c < V) {
+                                const int p = atomicAdd(s_cnt, 1);
+                                if (p < CAND_MAX) s_cand[p] = top_key(w, c);
+                            }
+                        }
+                        __syncthreads();
+                        cnt = s_cnt[0];
+                        exact = cnt > CAND_MAX;
+                        if (exact) __syncthreads();  // every thread has read the count
                     }
                 }
             }
@@ -390,7 +376,7 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
             if (CL) cluster_sync();
         }
         group_sync<NT>();
-        if (tid == 0) *s_cnt = 0;
+        if (tid == 0) s_cnt[0] = s_cnt[1] = 0;
         const long long n1 = row + stride, n2 = n1 + stride;
         if (here(n1)) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
         if (here(n2)) edge = edge_load(slice(n2), V, tid);
@@ -443,8 +429,74 @@ struct DistillLayout {
     }
 };
 
+// At 2^((z - m) ct) + A1 e^(z - m) for every column of the slice (S, H: which
+// of the two there are); both coefficients 0: zeros, whatever the logits are.
+template <typename T, int NT, bool S, bool H>
+__device__ __forceinline__ void grad_pass(const Slice<T>& s, const char* buf, char* drow, int V, int tid,
+                                          bool same_phase, float m, float ct, float At, float A1) {
+    using E = Elem<T>;
+    constexpr int P = E::EPG / 2;
+    const bool zero = At == 0.0f && A1 == 0.0f, far = is_far(m);
+    const float mm = far ? 0.0f : m;
+    const float nt = -(mm * ct), n1 = -(mm * LOG2E);
+    const float bt = At * unbias(mm, ct, nt), b1 = A1 * unbias(mm, LOG2E, n1);
+    const f2 c2 = pk(ct, ct), c1 = pk(LOG2E, LOG2E), nt2 = pk(nt, nt), n12 = pk(n1, n1), at2 = pk(bt, bt), a12 = pk(b1, b1);
+    auto store = [&](int g, const f2* r) {
+        if (same_phase && s.inner(g)) {
+            *reinterpret_cast<uint4*>(drow - s.ph + (long long)g * 16) = E::pack(r);
+            return;
+        }
+        const int c0 = s.col(g);
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+            float x, y;
+            unpk(r[i], x, y);
+            const int c = c0 + 2 * i;
+            if (c >= 0 && c < V) reinterpret_cast<T*>(drow)[c] = E::put(x);
+            if (c + 1 >= 0 && c + 1 < V) reinterpret_cast<T*>(drow)[c + 1] = E::put(y);
+        }
+    };
+    if (zero || far) {
+        for (int g = s.g0 + tid; g < s.g1; g += NT) {
+            f2 r[P];
+#pragma unroll
+            for (int i = 0; i < P; i++) {
+                const T* p = reinterpret_cast<const T*>(buf + (g - s.g0) * 16) + 2 * i;
+                float v[2];
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const float z = E::get(p + j);
+                    v[j] = zero ? 0.0f : (S ? At * exp_of(z, m, ct) : 0.0f) + (H ? A1 * exp_of(z, m, LOG2E) : 0.0f);
+                }
+                r[i] = pk(v[0], v[1]);
+            }
+            store(g, r);
+        }
+        return;
+    }
+#pragma unroll 2
+    for (int g = s.g0 + tid; g < s.g1; g += NT) {
+        const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+        f2 e[P], r[P];
+        E::unpack(u, e);
+        float x, y;
+#pragma unroll
+        for (int i = 0; i < P; i++) {
+            if (S) {
+                unpk(fma2(e[i], c2, nt2), x, y);
+                r[i] = mul2(pk(ex2f(x), ex2f(y)), at2);
+            }
+            if (H) {
+                unpk(fma2(e[i], c1, n12), x, y);
+                r[i] = S ? fma2(pk(ex2f(x), ex2f(y)), a12, r[i]) : mul2(pk(ex2f(x), ex2f(y)), a12);
+            }
+        }
+        store(g, r);
+    }
+}
+
 template <typename T, int NT, bool CL>
-__global__ void __launch_bounds__(cta_threads(NT), NT == 1024 ? 1 : 4)
+__global__ void __launch_bounds__(cta_threads(NT), cta_per_sm(NT))
 k_distill(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) char smem[];
@@ -465,7 +517,7 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
     const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
     const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
     const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
-    const float it = 1.0f / a.tau, ct = LOG2E * it, lift = 28.0f / fmaxf(1.0f, it);
+    const float it = 1.0f / a.tau, ct = LOG2E * it, lift = 20.0f / fmaxf(1.0f, it);
     float g_all = a.dscale;
     if (a.scale_dev) g_all *= *a.scale_dev;
     auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, rank, a.Gs); };
@@ -588,47 +640,16 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
             W = warp_sum(W);
         }
 
-        // first pass: sums of exponentials
-        const bool hard = hard_on && y >= 0;
-        float R = -INFINITY, s1, st;
-        {
-            f2 acc1 = pk(0.0f, 0.0f), acct = acc1;
-            const f2 c1 = pk(LOG2E, LOG2E), c2 = pk(ct, ct);
-            for (int g = s.g0 + tid; g < s.g1; g += NT) {
-                const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
-                const float vm = Elem<T>::vmax(u);
-                if (vm > R + lift) {
-                    const float f1 = rescale(R, vm, LOG2E), ft = rescale(R, vm, ct);
-                    acc1 = mul2(acc1, pk(f1, f1));
-                    acct = mul2(acct, pk(ft, ft));
-                    R = vm;
-                }
-                const float nr = -ref_of(R);
-                f2 e[EPG / 2];
-                Elem<T>::unpack(u, e);
-#pragma unroll
-                for (int i = 0; i < EPG / 2; i++) e[i] = add2(e[i], pk(nr, nr));
-                float x, v;
-                if (soft_on) {
-#pragma unroll
-                    for (int i = 0; i < EPG / 2; i++) {
-                        unpk(mul2(e[i], c2), x, v);
-                        acct = add2(acct, pk(ex2f(x), ex2f(v)));
-                    }
-                }
-                if (hard) {
-#pragma unroll
-                    for (int i = 0; i < EPG / 2; i++) {
-                        unpk(mul2(e[i], c1), x, v);
-                        acc1 = add2(acc1, pk(ex2f(x), ex2f(v)));
-                    }
-                }
-            }
-            float x, v;
-            unpk(acc1, x, v);
-            s1 = x + v;
-            unpk(acct, x, v);
-            st = x + v;
+        // first pass: sums of exponentials; at tau = 1 both are one
+        const bool hard = hard_on && y >= 0, same = it == 1.0f;
+        float R, s1, st, none;
+        if (!soft_on) {
+            sum_pass<T, NT, true, false>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+        } else if (!hard || same) {
+            sum_pass<T, NT, false, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            if (same) s1 = st;
+        } else {
+            sum_pass<T, NT, true, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
         }
         warp_merge(R, s1, LOG2E, st, ct);
         if (NT > 32) {
@@ -723,44 +744,9 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         if (dz) {
             // second pass: the gradient
             char* drow = reinterpret_cast<char*>(dz + row * a.ld);
-            const f2 nm = pk(-m, -m), c1 = pk(LOG2E, LOG2E), c2 = pk(ct, ct), a1 = pk(A1, A1), at = pk(At, At);
-            for (int g = s.g0 + tid; g < s.g1; g += NT) {
-                const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
-                f2 e[EPG / 2], r[EPG / 2];
-                Elem<T>::unpack(u, e);
-#pragma unroll
-                for (int i = 0; i < EPG / 2; i++) {
-                    e[i] = add2(e[i], nm);
-                    r[i] = pk(0.0f, 0.0f);
-                }
-                float x, v;
-                if (soft) {
-#pragma unroll
-                    for (int i = 0; i < EPG / 2; i++) {
-                        unpk(mul2(e[i], c2), x, v);
-                        r[i] = mul2(pk(ex2f(x), ex2f(v)), at);
-                    }
-                }
-                if (hard) {
-#pragma unroll
-                    for (int i = 0; i < EPG / 2; i++) {
-                        unpk(mul2(e[i], c1), x, v);
-                        r[i] = fma2(pk(ex2f(x), ex2f(v)), a1, r[i]);
-                    }
-                }
-                if (a.same_phase && s.inner(g)) {
-                    *reinterpret_cast<uint4*>(drow - s.ph + (long long)g * 16) = Elem<T>::pack(r);
-                } else {
-                    const int c0 = s.col(g);
-#pragma unroll
-                    for (int i = 0; i < EPG / 2; i++) {
-                        unpk(r[i], x, v);
-                        const int c = c0 + 2 * i;
-                        if (c >= 0 && c < V) reinterpret_cast<T*>(drow)[c] = Elem<T>::put(x);
-                        if (c + 1 >= 0 && c + 1 < V) reinterpret_cast<T*>(drow)[c + 1] = Elem<T>::put(v);
-                    }
-                }
-            }
+            if (soft && hard && !same) grad_pass<T, NT, true, true>(s, buf, drow, V, tid, a.same_phase, m, ct, At, A1);
+            else if (soft || !hard) grad_pass<T, NT, true, false>(s, buf, drow, V, tid, a.same_phase, m, ct, At + A1, 0.0f);
+            else grad_pass<T, NT, false, true>(s, buf, drow, V, tid, a.same_phase, m, ct, 0.0f, A1);
             if (rank == cs - 1)
                 for (long long c = V + tid; c < a.ld; c += NT) reinterpret_cast<T*>(drow)[c] = Elem<T>::put(0.0f);
         }
@@ -831,20 +817,23 @@ struct Plan {
 
 constexpr size_t SMEM_CTA = 232448;  // 227 KB
 constexpr size_t SMEM_SM = 233472;   // 228 KB, of which each CTA takes 1 KB more than its own
+constexpr size_t SMEM_HALF = SMEM_SM / 2 - 1024;
 
 template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, Bytes&& bytes) {
     p.cs = 1;
-    // a row that does not fit twice is cut; few rows are cut so that every SM has a part
-    auto fits = [&](int cs, int nbuf) { return bytes(1024, (G + cs - 1) / cs, nbuf, cs > 1) <= SMEM_CTA; };
-    while (p.cs < CS_MAX && !fits(p.cs, 2)) p.cs *= 2;
-    p.nbuf = fits(p.cs, 2) ? 2 : 1;
-    if (!fits(p.cs, p.nbuf)) return false;
+    p.nbuf = 1;
+    // two CTAs of an SM, each with a row (or slice) of its own: a larger row is cut
+    auto need = [&](int cs) { return bytes(512, (G + cs - 1) / cs, 1, cs > 1); };
+    while (p.cs < CS_MAX && need(p.cs) > SMEM_HALF) p.cs *= 2;
+    if (need(p.cs) > SMEM_CTA) return false;
+    // few rows are cut so that every SM has a part
     while (p.cs < CS_MAX && M * p.cs * 2 <= sms && G / (p.cs * 2) >= 256) p.cs *= 2;
     p.Gs = (G + p.cs - 1) / p.cs;
-    p.nt = p.cs == 1 && G <= 128 ? 32 : p.Gs <= 2048 ? 256 : 1024;
+    p.nt = p.cs == 1 && G <= 128 ? 32 : p.Gs <= 2048 ? 256 : 512;
+    if (p.nt != 512) p.nbuf = 2;
     p.smem = (size_t)bytes(p.nt, p.Gs, p.nbuf, p.cs > 1) * cta_groups(p.nt);
     const long long groups = (M + cta_groups(p.nt) - 1) / cta_groups(p.nt);
-    const int per_sm = std::max<int>(1, std::min<int>(p.nt == 1024 ? 1 : 4, (int)(SMEM_SM / (p.smem + 1024))));
+    const int per_sm = std::max<int>(1, std::min<int>(cta_per_sm(p.nt), (int)(SMEM_SM / (p.smem + 1024))));
     const long long room = std::max<long long>(1, (long long)sms * per_sm / p.cs);
     p.ctas = (int)(std::min(groups, room) * p.cs);
     return true;
@@ -906,8 +895,8 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     if (p.nt == 32) ROW_KERNEL(k_top_rows, 32, false, (const T*)z, a);
     if (p.nt == 256 && p.cs == 1) ROW_KERNEL(k_top_rows, 256, false, (const T*)z, a);
     if (p.nt == 256) ROW_KERNEL(k_top_rows, 256, true, (const T*)z, a);
-    if (p.cs == 1) ROW_KERNEL(k_top_rows, 1024, false, (const T*)z, a);
-    ROW_KERNEL(k_top_rows, 1024, true, (const T*)z, a);
+    if (p.cs == 1) ROW_KERNEL(k_top_rows, 512, false, (const T*)z, a);
+    ROW_KERNEL(k_top_rows, 512, true, (const T*)z, a);
 }
 
 template <typename T> bool distill(const Launch& L, const void* z, void* dz, DistillArgs a) {
@@ -922,8 +911,8 @@ template <typename T> bool distill(const Launch& L, const void* z, void* dz, Dis
     if (p.nt == 32) ROW_KERNEL(k_distill, 32, false, (const T*)z, (T*)dz, a);
     if (p.nt == 256 && p.cs == 1) ROW_KERNEL(k_distill, 256, false, (const T*)z, (T*)dz, a);
     if (p.nt == 256) ROW_KERNEL(k_distill, 256, true, (const T*)z, (T*)dz, a);
-    if (p.cs == 1) ROW_KERNEL(k_distill, 1024, false, (const T*)z, (T*)dz, a);
-    ROW_KERNEL(k_distill, 1024, true, (const T*)z, (T*)dz, a);
+    if (p.cs == 1) ROW_KERNEL(k_distill, 512, false, (const T*)z, (T*)dz, a);
+    ROW_KERNEL(k_distill, 512, true, (const T*)z, (T*)dz, a);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
 // head_row.cuh -- how the list kernels (head.cu) hold a row of logits.
 //
-// A group of NT threads (a warp, or a CTA; NT = 32, 256 or 1024) works on one
+// A group of NT threads (a warp, or a CTA; NT = 32, 256 or 512) works on one
 // row at a time and strides over the rows.  With clusters, the cs CTAs of a
 // cluster share a row, each a slice of it.  The row is cut into granules of 16
 // bytes on 16-byte boundaries of memory; granule i of the slice lives in slot
@@ -54,20 +54,18 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 }
 
 // ------------------------------------------------------------ storage types
-// A granule of EPG elements as EPG / 2 pairs of floats, its largest element (a
-// NaN counts as -inf), and back.
+// A granule of EPG elements as EPG / 2 pairs of floats, and back.  Max is what
+// maxima are kept in (a pair for the 16-bit types): exact, and a NaN is passed
+// over.
 template <typename T> struct Elem;
 template <> struct Elem<float> {
     static constexpr int EPG = 4;
+    using Max = float;
     static __device__ __forceinline__ float get(const float* p) { return *p; }
     static __device__ __forceinline__ float put(float v) { return v; }
     static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
         f[0] = pk(__uint_as_float(u.x), __uint_as_float(u.y));
         f[1] = pk(__uint_as_float(u.z), __uint_as_float(u.w));
-    }
-    static __device__ __forceinline__ float vmax(const uint4& u) {
-        return fmaxf(fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
-                           fmaxf(__uint_as_float(u.z), __uint_as_float(u.w))), -INFINITY);
     }
     static __device__ __forceinline__ uint4 pack(const f2* f) {
         float a, b, c, d;
@@ -75,9 +73,49 @@ template <> struct Elem<float> {
         unpk(f[1], c, d);
         return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
     }
+    static __device__ __forceinline__ Max gmax(const uint4& u) {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+                     fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+    static __device__ __forceinline__ Max max2(Max a, Max b) { return fmaxf(a, b); }
+    static __device__ __forceinline__ Max to_max(float v) { return v; }
+    static __device__ __forceinline__ float value(Max m) { return fmaxf(m, -INFINITY); }
+    static __device__ __forceinline__ bool above(Max m, Max t) { return m > t; }       // any of m > t
+    static __device__ __forceinline__ bool at_least(Max m, Max t) { return m >= t; }  // any of m >= t
 };
-template <> struct Elem<__nv_bfloat16> {
+template <typename T, typename P, typename Cvt> struct Elem16 {
     static constexpr int EPG = 8;
+    using Max = P;
+    static __device__ __forceinline__ P pair(uint32_t w) { return *reinterpret_cast<const P*>(&w); }
+    static __device__ __forceinline__ uint4 pack(const f2* f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float a, b;
+            unpk(f[i], a, b);
+            const P h = Cvt::pair(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ Max gmax(const uint4& u) {
+        return __hmax2(__hmax2(pair(u.x), pair(u.y)), __hmax2(pair(u.z), pair(u.w)));
+    }
+    static __device__ __forceinline__ Max max2(Max a, Max b) { return __hmax2(a, b); }
+    static __device__ __forceinline__ Max to_max(float v) { return Cvt::pair(v, v); }
+    static __device__ __forceinline__ float value(Max m) {
+        return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+    }
+    static __device__ __forceinline__ bool above(Max m, Max t) { return !__hble2(m, t); }     // or a NaN pair
+    static __device__ __forceinline__ bool at_least(Max m, Max t) { return !__hblt2(m, t); }  // or a NaN pair
+};
+struct CvtBf {
+    static __device__ __forceinline__ __nv_bfloat162 pair(float a, float b) { return __floats2bfloat162_rn(a, b); }
+};
+struct CvtHalf {
+    static __device__ __forceinline__ __half2 pair(float a, float b) { return __floats2half2_rn(a, b); }
+};
+template <> struct Elem<__nv_bfloat16> : Elem16<__nv_bfloat16, __nv_bfloat162, CvtBf> {
     static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
@@ -85,27 +123,8 @@ template <> struct Elem<__nv_bfloat16> {
 #pragma unroll
         for (int i = 0; i < 4; i++) f[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ float vmax(const uint4& u) {
-        using P = __nv_bfloat162;
-        const P a = __hmax2(*reinterpret_cast<const P*>(&u.x), *reinterpret_cast<const P*>(&u.y));
-        const P b = __hmax2(*reinterpret_cast<const P*>(&u.z), *reinterpret_cast<const P*>(&u.w));
-        const P m = __hmax2(a, b);
-        return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
-    }
-    static __device__ __forceinline__ uint4 pack(const f2* f) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float a, b;
-            unpk(f[i], a, b);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
 };
-template <> struct Elem<__half> {
-    static constexpr int EPG = 8;
+template <> struct Elem<__half> : Elem16<__half, __half2, CvtHalf> {
     static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
     static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
@@ -115,23 +134,6 @@ template <> struct Elem<__half> {
             const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
             f[i] = pk(v.x, v.y);
         }
-    }
-    static __device__ __forceinline__ float vmax(const uint4& u) {
-        const __half2 a = __hmax2(*reinterpret_cast<const __half2*>(&u.x), *reinterpret_cast<const __half2*>(&u.y));
-        const __half2 b = __hmax2(*reinterpret_cast<const __half2*>(&u.z), *reinterpret_cast<const __half2*>(&u.w));
-        const __half2 m = __hmax2(a, b);
-        return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
-    }
-    static __device__ __forceinline__ uint4 pack(const f2* f) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float a, b;
-            unpk(f[i], a, b);
-            const __half2 h = __floats2half2_rn(a, b);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
@@ -221,8 +223,11 @@ template <typename T> struct Slice {
 // Copies thread tid's granules of the slice into buf.
 template <typename T, int NT>
 __device__ __forceinline__ void fill(const Slice<T>& s, char* buf, int tid) {
-    for (int g = s.g0 + tid; g < s.g1; g += NT)
-        if (s.inner(g)) cp16(buf + (g - s.g0) * 16, s.base + (long long)g * 16);
+    const int lo = max(s.g0, s.gi0), hi = min(s.g1, s.gi1);
+    int g = s.g0 + tid;
+    if (g < lo) g += NT;  // the head's granule comes element by element
+#pragma unroll 4
+    for (; g < hi; g += NT) cp16(buf + (g - s.g0) * 16, s.base + (long long)g * 16);
 }
 
 // The element of an edge granule that thread tid < 16 of the group looks
@@ -251,16 +256,109 @@ __device__ __forceinline__ void edge_store(const Slice<T>& s, char* buf, T v, in
 }
 
 // ------------------------------------------------------------ sums of exponentials
-// A running reference R and sums of e^((z - R) c).  R moves only when a value
-// is more than `lift` above it (the sums are then scaled), so one pass finds
-// the sum without knowing the maximum, at one exponential an element; the sums
-// stay below e^40 times the number of terms.  z - R is formed before the
-// scaling: it is exact or rounded once, and finite however large the logits
-// are (a mask of the type's lowest value).
-__device__ __forceinline__ float exp_of(float z, float r, float c) { return ex2f((z - r) * c); }
+// Sums of 2^((z - R) c) over a thread's granules in one pass, at one
+// exponential an element, without knowing the maximum: R starts at the largest
+// of the warp's first granules and moves up only when a value is more than
+// `lift` above it (the sums are then scaled), which keeps every term below
+// e^20.  The argument is one fused multiply-add, z c + nb with nb = -(R c)
+// rounded; the rounding of nb is common to all terms and is taken out at the
+// end as the factor 2^-(R c + nb), which a fused multiply-add gives exactly.
+// Logits beyond 1e30 (a row that consists of the type's lowest value, an
+// infinity) would overflow z c: such threads form (z - R) first.
+constexpr float FAR = 1e30f;
 
-// the reference that stands for R in arguments (an empty sum has R = -inf)
-__device__ __forceinline__ float ref_of(float R) { return R == -INFINITY ? 0.0f : R; }
+__device__ __forceinline__ bool is_far(float v) { return !(fabsf(v) < FAR); }
+__device__ __forceinline__ float exp_of(float z, float r, float c) { return ex2f((z - r) * c); }
+// 2^-(R c + nb): what sums of 2^(z c + nb) are multiplied by
+__device__ __forceinline__ float unbias(float R, float c, float nb) { return ex2f(-fmaf(R, c, nb)); }
+
+// SA, SB: whether the sum with coefficient ca, cb is wanted.  tm: the thread's
+// largest value.  R = -inf where there is no value above -inf.
+template <typename T, int NT, bool SA, bool SB>
+__device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int tid, float ca, float cb, float lift,
+                                         float& tm, float& R, float& sa, float& sb) {
+    using E = Elem<T>;
+    constexpr int H = E::EPG / 2;
+    const int g1 = s.g1 - s.g0;
+    const uint4* v = reinterpret_cast<const uint4*>(buf);
+    typename E::Max m = E::to_max(-INFINITY);
+    if (tid < g1) m = E::gmax(v[tid]);
+    f2 xa = pk(0.0f, 0.0f), xb = xa;
+    R = warp_max(E::value(m));
+    bool far = is_far(R) && R != -INFINITY;
+    float lim = R + lift;  // a larger value moves the reference; -inf: there is none yet
+    if (is_far(R)) R = 0.0f;
+    float na = -(R * ca), nb = -(R * cb);
+    typename E::Max top = E::to_max(lim);
+    const f2 ca2 = pk(ca, ca), cb2 = pk(cb, cb);
+    f2 na2 = pk(na, na), nb2 = pk(nb, nb);
+#pragma unroll 2
+    for (int g = tid; g < g1; g += NT) {
+        const uint4 u = v[g];
+        const typename E::Max gm = E::gmax(u);
+        m = E::max2(m, gm);
+        if (SA || SB) {
+            if (E::above(gm, top)) {
+                const float vm = E::value(gm);
+                if (is_far(vm)) {
+                    far |= vm > 0.0f;
+                } else if (vm > lim) {
+                    R = vm;
+                    const float ma = -(R * ca), mb = -(R * cb);
+                    const float fa = lim == -INFINITY ? 0.0f : ex2f(ma - na);
+                    const float fb = lim == -INFINITY ? 0.0f : ex2f(mb - nb);
+                    if (SA) xa = mul2(xa, pk(fa, fa));
+                    if (SB) xb = mul2(xb, pk(fb, fb));
+                    na = ma;
+                    nb = mb;
+                    na2 = pk(na, na);
+                    nb2 = pk(nb, nb);
+                    lim = R + lift;
+                    top = E::to_max(lim);
+                }
+            }
+            f2 e[H];
+            E::unpack(u, e);
+            float x, y;
+            if (SA) {
+#pragma unroll
+                for (int i = 0; i < H; i++) {
+                    unpk(fma2(e[i], ca2, na2), x, y);
+                    xa = add2(xa, pk(ex2f(x), ex2f(y)));
+                }
+            }
+            if (SB) {
+#pragma unroll
+                for (int i = 0; i < H; i++) {
+                    unpk(fma2(e[i], cb2, nb2), x, y);
+                    xb = add2(xb, pk(ex2f(x), ex2f(y)));
+                }
+            }
+        }
+    }
+    tm = E::value(m);
+    sa = sb = 0.0f;
+    if (SA || SB) {
+        float x, y;
+        unpk(xa, x, y);
+        if (SA) sa = (x + y) * unbias(R, ca, na);
+        unpk(xb, x, y);
+        if (SB) sb = (x + y) * unbias(R, cb, nb);
+        if (far) {
+            R = tm;
+            sa = sb = 0.0f;
+            for (int g = tid; g < g1; g += NT)
+                for (int i = 0; i < E::EPG; i++) {
+                    const float z = E::get(reinterpret_cast<const T*>(v + g) + i);
+                    const float d = z == R ? 0.0f : z - R;  // inf - inf is a term of 1
+                    if (SA) sa += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * ca);
+                    if (SB) sb += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * cb);
+                }
+        } else if (tm == -INFINITY) {
+            R = -INFINITY;  // no terms, unless they are NaN
+        }
+    }
+}
 
 // what a sum with reference `from` is multiplied by to have the larger reference `to`
 __device__ __forceinline__ float rescale(float from, float to, float c) {
