@@ -24,8 +24,10 @@ constexpr int CS_MAX = 8;      // CTAs of a cluster (the portable limit)
 constexpr int CAND_MAX = 512;  // candidates of a row's (or slice's) list, and granules that hold them
 constexpr int THR_MAX = 256;   // thread maxima that a threshold is chosen from
 
+constexpr int LIST_CTA = 64;  // threads of a CTA that look after the list
+
 __host__ __device__ constexpr int cta_threads(int NT) { return NT == 32 ? 256 : NT; }
-__host__ __device__ constexpr int cta_per_sm(int NT) { return NT == 512 ? 2 : 4; }
+__host__ __device__ constexpr int cta_per_sm(int NT) { return NT == 32 ? 3 : 2; }
 __host__ __device__ constexpr int cta_groups(int NT) { return NT == 32 ? 8 : 1; }
 __host__ __device__ constexpr int align16(int n) { return (n + 15) & ~15; }
 
@@ -94,8 +96,8 @@ template <int NT> __device__ __forceinline__ int group_count(int c, int* s_red, 
 // f(key order, column) for every element of the thread's granules
 template <typename T, int NT, typename F>
 __device__ __forceinline__ void each_element(const Slice<T>& s, const char* buf, int V, int tid, F&& f) {
-    for (int g = s.g0 + tid; g < s.g1; g += NT) {
-        const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
+    for (int g = tid; g < s.n; g += NT) {
+        const uint4 u = reinterpret_cast<const uint4*>(buf)[g];
         f2 e[Elem<T>::EPG / 2];
         Elem<T>::unpack(u, e);
         const int c0 = s.col(g);
@@ -172,7 +174,7 @@ __device__ void exact_candidates(const Slice<T>& s, const char* buf, int V, int 
 //   3. threads whose largest value is at or above it name their granules that
 //      are, and all threads look through those for the elements: the
 //      candidates, on unordered data a few more than k;
-//   4. each candidate's rank among them by counting, a warp per candidate.
+//   4. each candidate's rank among them by counting.
 // With more than CAND_MAX candidates, or too few threads for a threshold, the
 // candidates are found exactly instead.  Clusters: each CTA lists its slice
 // and sends the list to CTA 0, which ranks every entry by binary searches in
@@ -229,13 +231,13 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
             float tmax, R, sum, none;
             if (want) {
                 sum_pass<T, NT, true, false>(s, buf, tid, ct, ct, lift, tmax, R, sum, none);
-                warp_merge(R, sum, ct);
+                merge(R, sum, ct);
             } else {
                 sum_pass<T, NT, false, false>(s, buf, tid, ct, ct, lift, tmax, R, sum, none);
             }
             // stage 2
-            const int n_slots = s.g1 - s.g0;
-            const int n_el = max(0, min(V, s.col(s.g1)) - max(0, s.col(s.g0)));
+            const int n_slots = s.n;
+            const int n_el = max(0, min(V, s.col(s.n)) - max(0, s.col(0)));
             const int kk = min(k, n_el);
             const int fw = NT == 32 ? 0 : min(NT, n_slots) / 32;
             const int Q = fw ? min(32, (k + fw - 1) / fw + 2) : 0;
@@ -254,23 +256,42 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
                 if (lane == 0) s_part[warp] = make_float2(R, sum);
                 __syncthreads();
                 if (!exact) {
-                    // the k-th largest of the fw Q values
-                    const int nv = fw * Q;
-                    for (int i = warp; i < nv; i += NT / 32) {
-                        const uint32_t x = s_thr[i];
-                        int r = 0;  // how many are larger, and (in the upper half) at least as large
-                        for (int j = lane; j < nv; j += 32) {
-                            const uint32_t w = s_thr[j];
-                            r += (w > x) + ((w >= x) << 16);
+                    // the k-th largest of the fw Q values, by one warp bit by bit
+                    // from the first bit that differs
+                    if (warp == 0) {
+                        const int nv = fw * Q;
+                        uint32_t v[THR_MAX / 32], hi = 0, lo = ~0u;
+#pragma unroll
+                        for (int j = 0; j < THR_MAX / 32; j++) {
+                            v[j] = 0;
+                            if (j * 32 + lane < nv) {
+                                v[j] = s_thr[j * 32 + lane];
+                                lo = min(lo, v[j]);
+                                hi = max(hi, v[j]);
+                            }
                         }
-                        r = __reduce_add_sync(0xffffffffu, r);
-                        if (lane == 0 && (r & 0xFFFF) < k && (r >> 16) >= k) s_thr[THR_MAX] = x;
+                        hi = __reduce_max_sync(0xffffffffu, hi);
+                        lo = __reduce_min_sync(0xffffffffu, lo);
+                        int bit = 31 - __clz(hi ^ lo);  // -1: all are equal
+                        uint32_t t = bit < 0 ? hi : hi & ~((2u << bit) - 1u);
+                        for (; bit >= 32 - OrderBits<T>::N; bit--) {
+                            const uint32_t cand = t | (1u << bit);
+                            int c = 0;
+#pragma unroll
+                            for (int j = 0; j < THR_MAX / 32; j++)
+                                if (j * 32 < nv) c += v[j] >= cand;
+                            c = __reduce_add_sync(0xffffffffu, c);
+                            if (c >= k) t = cand;
+                            if (c == k) break;
+                        }
+                        if (lane == 0) s_thr[THR_MAX] = t;
                     }
                     __syncthreads();
                     // stage 3
-                    const float thr = value_of(s_thr[THR_MAX]);
-                    const typename E::Max thr2 = E::to_max(thr);
-                    if (tmax >= thr) {
+                    const uint32_t thr = s_thr[THR_MAX];
+                    if (order_of(tmax) >= thr) {
+                        const typename E::Max thr2 = E::to_max(fmaxf(value_of(thr), -INFINITY));
+#pragma unroll 2
                         for (int i = tid; i < n_slots; i += NT)
                             if (E::at_least(E::gmax(reinterpret_cast<const uint4*>(buf)[i]), thr2)) {
                                 const int p = atomicAdd(s_cnt + 1, 1);
@@ -283,9 +304,9 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
                     if (!exact) {
                         for (int i = tid; i < ng * E::EPG; i += NT) {
                             const int slot = s_gl[i / E::EPG], e = i % E::EPG;
-                            const float w = fmaxf(E::get(reinterpret_cast<const T*>(buf + slot * 16) + e), -INFINITY);
-                            const int c = s.col(s.g0 + slot) + e;
-                            if (w >= thr && c >= 0 && c < V) {
+                            const float w = E::get(reinterpret_cast<const T*>(buf + slot * 16) + e);
+                            const int c = s.col(slot) + e;
+                            if (order_of(w) >= thr && c >= 0 && c < V) {
                                 const int p = atomicAdd(s_cnt, 1);
                                 if (p < CAND_MAX) s_cand[p] = top_key(w, c);
                             }
@@ -303,13 +324,17 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
             }
             if (here(next)) fill<T, NT>(slice(next), buf, tid);
             cp_commit();
-            // stage 4
-            for (int i = warp; i < cnt; i += NT / 32) {
-                const unsigned long long key = s_cand[i];
+            // stage 4: four lanes a candidate
+            for (int i0 = 0; i0 < cnt; i0 += NT / 4) {
+                const int i = i0 + tid / 4;
+                const unsigned long long key = i < cnt ? s_cand[i] : ~0ull;
+                if (__all_sync(0xffffffffu, i >= cnt)) break;
                 int r = 0;
-                for (int j = lane; j < cnt; j += 32) r += s_cand[j] > key;
-                r = __reduce_add_sync(0xffffffffu, r);
-                if (lane == 0 && r < kk) {
+#pragma unroll 4
+                for (int j = tid & 3; j < cnt; j += 4) r += s_cand[j] > key;
+                r += __shfl_xor_sync(0xffffffffu, r, 1);
+                r += __shfl_xor_sync(0xffffffffu, r, 2);
+                if ((tid & 3) == 0 && i < cnt && r < kk) {
                     if (CL) {
                         st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), key);
                     } else {
@@ -325,7 +350,7 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
                     const float2 p = lane < NT / 32 ? s_part[lane] : make_float2(-INFINITY, 0.0f);
                     R = p.x;
                     sum = p.y;
-                    warp_merge(R, sum, ct);
+                    merge(R, sum, ct);
                 }
                 if (CL && lane == 0) {
                     const uint32_t at = remote(s_x + par * cs + rank, 0);
@@ -360,7 +385,7 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
                         const float2 p = lane < cs ? s_x[par * cs + lane] : make_float2(-INFINITY, 0.0f);
                         R = p.x;
                         sum = p.y;
-                        warp_merge(R, sum, ct);
+                        merge<CS_MAX>(R, sum, ct);
                     }
                 }
             }
@@ -378,8 +403,10 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
         group_sync<NT>();
         if (tid == 0) s_cnt[0] = s_cnt[1] = 0;
         const long long n1 = row + stride, n2 = n1 + stride;
-        if (here(n1)) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
-        if (here(n2)) edge = edge_load(slice(n2), V, tid);
+        if (tid < 16) {
+            if (here(n1)) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
+            if (here(n2)) edge = edge_load(slice(n2), V, tid);
+        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -411,108 +438,173 @@ struct DistillArgs {
     bool same_phase;  // a row of dz starts at the same place of a 16-byte line as its row of z
 };
 
+__host__ __device__ constexpr int distill_threads(int NT) { return NT == 32 ? 256 : NT + LIST_CTA; }
+
+// tau as a power that one softmax's terms are of the other's: 1 to 4, else 0
+__device__ __forceinline__ int power_of(float tau) {
+    return tau == 1.0f ? 1 : tau == 2.0f ? 2 : tau == 3.0f ? 3 : tau == 4.0f ? 4 : 0;
+}
+
 struct DistillLayout {
-    int bits, ti, tv, yl, zl, p, part, x, fin, total;
+    int bits, ti, tv, yl, zl, zo, t, off, part, lw, ll, x, flag, total;
     __host__ __device__ DistillLayout(int nt, int Gs, int nbuf, int k, int epg, bool cl) {
         const int k4 = align16(4 * (k + 1));
         int at = nbuf * Gs * 16;
         bits = at; at += align16((Gs * epg + 31) / 32 * 4);
         ti = at; at += nbuf * k4;
         tv = at; at += nbuf * k4;
-        yl = at; at += 16;       // [nbuf] targets, [nbuf] t_lse
-        zl = at; at += 2 * k4;   // student logits of the list, and of the target
-        p = at; at += k4;
-        part = at; at += nt > 32 ? 32 * 16 : 0;
+        yl = at; at += 16;      // [nbuf] targets, [nbuf] t_lse
+        zl = at; at += 2 * k4;  // student logits of the list, and of the target
+        zo = at; at += k4;      // those of this CTA's slice
+        t = at; at += k4;       // t_j / tau
+        off = at; at += k4;     // where this CTA holds the column, or -1
+        part = at; at += nt > 32 ? (nt + LIST_CTA) / 32 * 16 : 0;
+        lw = at; at += LIST_CTA / 32 * 16;
+        ll = at; at += 16;
         x = at; at += cl ? 2 * CS_MAX * 16 : 0;
-        fin = at; at += 32;
+        flag = at; at += 16;
         total = at;
     }
 };
 
 // At 2^((z - m) ct) + A1 e^(z - m) for every column of the slice (S, H: which
 // of the two there are); both coefficients 0: zeros, whatever the logits are.
-template <typename T, int NT, bool S, bool H>
-__device__ __forceinline__ void grad_pass(const Slice<T>& s, const char* buf, char* drow, int V, int tid,
-                                          bool same_phase, float m, float ct, float At, float A1) {
+// Each slot is refilled from the next row nx (if there is one) once it has been read.
+template <typename T, int NT, bool S, bool H, int PW = 0>
+__device__ __forceinline__ void grad_pass(const Slice<T>& s, char* buf, T* drow, int V, int tid, bool same_phase,
+                                          float m, float ct, float At, float A1, const Slice<T>& nx, bool more) {
     using E = Elem<T>;
-    constexpr int P = E::EPG / 2;
+    constexpr int P = E::EPG / 2, U = 4;
     const bool zero = At == 0.0f && A1 == 0.0f, far = is_far(m);
-    const float mm = far ? 0.0f : m;
-    const float nt = -(mm * ct), n1 = -(mm * LOG2E);
-    const float bt = At * unbias(mm, ct, nt), b1 = A1 * unbias(mm, LOG2E, n1);
-    const f2 c2 = pk(ct, ct), c1 = pk(LOG2E, LOG2E), nt2 = pk(nt, nt), n12 = pk(n1, n1), at2 = pk(bt, bt), a12 = pk(b1, b1);
-    auto store = [&](int g, const f2* r) {
-        if (same_phase && s.inner(g)) {
-            *reinterpret_cast<uint4*>(drow - s.ph + (long long)g * 16) = E::pack(r);
-            return;
-        }
-        const int c0 = s.col(g);
+    uint4* const d0 = reinterpret_cast<uint4*>(drow + s.col(0));  // where slot 0 goes
+    const uint4* v = reinterpret_cast<const uint4*>(buf);
+    auto store_edge = [&](int i, const f2* r) {
+        const int c0 = s.col(i);
 #pragma unroll
-        for (int i = 0; i < P; i++) {
+        for (int j = 0; j < P; j++) {
             float x, y;
-            unpk(r[i], x, y);
-            const int c = c0 + 2 * i;
-            if (c >= 0 && c < V) reinterpret_cast<T*>(drow)[c] = E::put(x);
-            if (c + 1 >= 0 && c + 1 < V) reinterpret_cast<T*>(drow)[c + 1] = E::put(y);
+            unpk(r[j], x, y);
+            const int c = c0 + 2 * j;
+            if (c >= 0 && c < V) drow[c] = E::put(x);
+            if (c + 1 >= 0 && c + 1 < V) drow[c + 1] = E::put(y);
         }
     };
     if (zero || far) {
-        for (int g = s.g0 + tid; g < s.g1; g += NT) {
+#pragma unroll 1
+        for (int i = tid; i < s.n; i += NT) {
             f2 r[P];
 #pragma unroll
-            for (int i = 0; i < P; i++) {
-                const T* p = reinterpret_cast<const T*>(buf + (g - s.g0) * 16) + 2 * i;
-                float v[2];
+            for (int j = 0; j < P; j++) {
+                const T* p = reinterpret_cast<const T*>(v + i) + 2 * j;
+                float w[2];
 #pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const float z = E::get(p + j);
-                    v[j] = zero ? 0.0f : (S ? At * exp_of(z, m, ct) : 0.0f) + (H ? A1 * exp_of(z, m, LOG2E) : 0.0f);
+                for (int l = 0; l < 2; l++) {
+                    const float z = E::get(p + l);
+                    w[l] = zero ? 0.0f : (S ? At * exp_of(z, m, ct) : 0.0f) + (H ? A1 * exp_of(z, m, LOG2E) : 0.0f);
                 }
-                r[i] = pk(v[0], v[1]);
+                r[j] = pk(w[0], w[1]);
             }
-            store(g, r);
+            if (same_phase && s.inner(i)) d0[i] = E::pack(r);
+            else store_edge(i, r);
         }
+        if (more) fill<T, NT>(nx, buf, tid);
         return;
     }
-#pragma unroll 2
-    for (int g = s.g0 + tid; g < s.g1; g += NT) {
-        const uint4 u = *reinterpret_cast<const uint4*>(buf + (g - s.g0) * 16);
-        f2 e[P], r[P];
+    const float nt = -(m * ct), n1 = -(m * LOG2E);
+    const float bt = S ? At * unbias(m, ct, nt) : 0.0f, b1 = H ? A1 * (PW ? powi<PW>(unbias(m, ct, nt)) : unbias(m, LOG2E, n1)) : 0.0f;
+    const f2 c2 = pk(ct, ct), c1 = pk(LOG2E, LOG2E), nt2 = pk(nt, nt), n12 = pk(n1, n1), at2 = pk(bt, bt), a12 = pk(b1, b1);
+    auto grad = [&](const uint4& u, f2* r) {
+        f2 e[P];
         E::unpack(u, e);
         float x, y;
 #pragma unroll
-        for (int i = 0; i < P; i++) {
+        for (int j = 0; j < P; j++) {
+            if (PW) {
+                unpk(fma2(e[j], c2, nt2), x, y);
+                const f2 q = pk(ex2f(x), ex2f(y));
+                r[j] = fma2(powi<PW>(q), a12, mul2(q, at2));
+                continue;
+            }
             if (S) {
-                unpk(fma2(e[i], c2, nt2), x, y);
-                r[i] = mul2(pk(ex2f(x), ex2f(y)), at2);
+                unpk(fma2(e[j], c2, nt2), x, y);
+                r[j] = mul2(pk(ex2f(x), ex2f(y)), at2);
             }
             if (H) {
-                unpk(fma2(e[i], c1, n12), x, y);
-                r[i] = S ? fma2(pk(ex2f(x), ex2f(y)), a12, r[i]) : mul2(pk(ex2f(x), ex2f(y)), a12);
+                unpk(fma2(e[j], c1, n12), x, y);
+                r[j] = S ? fma2(pk(ex2f(x), ex2f(y)), a12, r[j]) : mul2(pk(ex2f(x), ex2f(y)), a12);
             }
         }
-        store(g, r);
+    };
+    const int nx0 = more ? nx.i0 : 0, nx1 = more ? nx.i1 : 0;
+    const char* g = nx.base + (long long)tid * 16;
+    uint32_t b = (uint32_t)__cvta_generic_to_shared(buf) + tid * 16;
+    int i = tid;
+    // blocks of four slots that are wholly inside the row
+    for (; same_phase && i + (U - 1) * NT < s.i1; i += U * NT, g += 16 * U * NT, b += 16 * U * NT) {
+        uint4 u[U];
+#pragma unroll
+        for (int j = 0; j < U; j++) u[j] = v[i + j * NT];
+#pragma unroll
+        for (int j = 0; j < U; j++) {
+            f2 r[P];
+            grad(u[j], r);
+            if (i >= s.i0) d0[i + j * NT] = E::pack(r);
+            else if (j > 0) d0[i + j * NT] = E::pack(r);
+            else store_edge(i, r);
+        }
+        if (i >= nx0 && i + (U - 1) * NT < nx1) {
+            cp16<0>(b, g);
+            cp16<16 * NT>(b, g);
+            cp16<32 * NT>(b, g);
+            cp16<48 * NT>(b, g);
+        } else {
+#pragma unroll
+            for (int j = 0; j < U; j++)
+                if (i + j * NT >= nx0 && i + j * NT < nx1) cp16<0>(b + j * 16 * NT, g + j * 16 * NT);
+        }
+    }
+#pragma unroll 1
+    for (; i < max(s.n, nx1); i += NT, g += 16 * NT, b += 16 * NT) {
+        if (i < s.n) {
+            f2 r[P];
+            grad(v[i], r);
+            if (same_phase && s.inner(i)) d0[i] = E::pack(r);
+            else store_edge(i, r);
+        }
+        if (i >= nx0 && i < nx1) cp16<0>(b, g);
     }
 }
 
+// In a CTA, LIST_CTA threads of their own look after the list, beside the NT
+// threads' passes over the row (as a part of one of those warps' work it held
+// the others up at every barrier: 1422 us for the 32768 rows of 50257).  Every
+// warp merges the warps' sums and forms the coefficients for itself, which
+// saves a barrier.
 template <typename T, int NT, bool CL>
-__global__ void __launch_bounds__(cta_threads(NT), cta_per_sm(NT))
+__global__ void __launch_bounds__(distill_threads(NT), cta_per_sm(NT))
 k_distill(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) char smem[];
     constexpr int EPG = Elem<T>::EPG;
+    constexpr int LT = NT == 32 ? 32 : LIST_CTA;
     const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int lane = threadIdx.x & 31, warp = tid >> 5;
+    const int lt = NT == 32 ? tid : tid - NT;  // >= 0: a thread of the list
+    const bool worker = NT == 32 || tid < NT, lister = lt >= 0;
     const DistillLayout lay(NT, a.Gs, a.nbuf, a.k, EPG, CL);
     char* sm = smem + (NT == 32 ? threadIdx.x >> 5 : 0) * lay.total;
-    const int k = a.k, V = a.V, k4 = align16(4 * (k + 1)) / 4;
+    const int k = a.k, V = a.V, k4 = align16(4 * (k + 1)) / 4, nlw = (min(k, LT) + 31) / 32, pw = power_of(a.tau);
     uint32_t* s_bits = reinterpret_cast<uint32_t*>(sm + lay.bits);
     int* s_y = reinterpret_cast<int*>(sm + lay.yl);
     float* s_tl = reinterpret_cast<float*>(sm + lay.yl) + 2;
-    float* s_p = reinterpret_cast<float*>(sm + lay.p);
+    float* s_t = reinterpret_cast<float*>(sm + lay.t);
+    int* s_off = reinterpret_cast<int*>(sm + lay.off);
+    float* s_zo = reinterpret_cast<float*>(sm + lay.zo);
     float4* s_part = reinterpret_cast<float4*>(sm + lay.part);
+    float4* s_lw = reinterpret_cast<float4*>(sm + lay.lw);
+    float* s_ll = reinterpret_cast<float*>(sm + lay.ll);
     float4* s_x = reinterpret_cast<float4*>(sm + lay.x);  // [2][cs]
-    float* s_fin = reinterpret_cast<float*>(sm + lay.fin);
+    int* s_flag = reinterpret_cast<int*>(sm + lay.flag);  // the target is on the list
     const int rank = CL ? (int)cluster_rank() : 0, cs = CL ? a.cs : 1;
     const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
     const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
@@ -521,30 +613,34 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
     float g_all = a.dscale;
     if (a.scale_dev) g_all *= *a.scale_dev;
     auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, rank, a.Gs); };
-    auto copy_lists = [&](long long r, int b) {  // warp 0
-        for (int j = lane; j < k; j += 32) {
-            cp4(sm + lay.ti + (b * k4 + j) * 4, a.t_idx + r * k + j);
-            cp4(sm + lay.tv + (b * k4 + j) * 4, a.t_vals + r * k + j);
-        }
-        if (lane == 0 && a.targets) cp4(s_y + b, a.targets + r);
-        if (lane == 1 && rest) cp4(s_tl + b, a.t_lse + r);
+    auto copy_lists = [&](long long r, int b) {
+        if (lister)
+            for (int j = lt; j < k; j += LT) {
+                cp4(sm + lay.ti + (b * k4 + j) * 4, a.t_idx + r * k + j);
+                cp4(sm + lay.tv + (b * k4 + j) * 4, a.t_vals + r * k + j);
+            }
+        if (lt == 0 && a.targets) cp4(s_y + b, a.targets + r);
+        if (lt == 1 && rest) cp4(s_tl + b, a.t_lse + r);
     };
 
-    for (int w = tid; w < (a.Gs * EPG + 31) / 32; w += NT) s_bits[w] = 0;
+    if (worker)
+        for (int w = tid; w < (a.Gs * EPG + 31) / 32; w += NT) s_bits[w] = 0;
     if (tid < 2) s_y[tid] = -1;
+    if (tid == 0) *s_flag = 0;
     group_sync<NT>();
     for (int i = 0; i < a.nbuf; i++) {
         const long long r = first + i * stride;
         if (r < a.M) {
-            fill<T, NT>(slice(r), sm + i * a.Gs * 16, tid);
-            if (warp == 0) copy_lists(r, i);
+            if (worker) fill<T, NT>(slice(r), sm + i * a.Gs * 16, tid);
+            copy_lists(r, i);
         }
         cp_commit();
     }
     T edge = Elem<T>::put(0.0f);
-    if (first < a.M) edge_store(slice(first), sm, edge_load(slice(first), V, tid), tid);
-    if (first + stride < a.M) edge = edge_load(slice(first + stride), V, tid);
-
+    if (lt >= 0 && lt < 16) {
+        if (first < a.M) edge_store(slice(first), sm, edge_load(slice(first), V, lt), lt);
+        if (first + stride < a.M) edge = edge_load(slice(first + stride), V, lt);
+    }
     if (CL) cluster_sync();  // the others run: their shared memory may be written
 
     int itn = 0;
@@ -560,106 +656,130 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         int y = s_y[b];
         const bool y_bad = y < -1 || y >= V;
         if (y_bad) y = -1;
+        const bool hard = hard_on && y >= 0;
 
-        // the list: the student's logits at its columns (each CTA sends those
-        // of its slice to all), duplicates, and the replacement by -inf
-        int off[LIST_PER_LANE];
-        if (warp == 0) {
-            bool bad = y_bad && lane == 0;
-            if (lane == 0) {
-                const int o = y >= 0 ? s.at(y) : -1;
-                if (o >= 0) {
-                    const float v = Elem<T>::get(reinterpret_cast<const T*>(buf + o));
-                    s_zl[k] = v;
-                    if (CL)
-                        for (int r = 0; r < cs; r++) st_remote(remote(s_zl + k, r), v);
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < LIST_PER_LANE; e++) {
-                const int j = lane + 32 * e;
-                off[e] = -1;
-                if (j >= k) continue;
-                const int c = s_ti[j];
+        // the list: the student's logits at its columns (in a cluster the
+        // column's CTA sends them to all), duplicates, the replacement by -inf
+        auto keep = [&](int j, float v) {
+            if (CL)
+                for (int r = 0; r < cs; r++) st_remote(remote(s_zl + j, r), v);
+            else s_zl[j] = v;
+        };
+        float Rl = -INFINITY, l1 = 0.0f, lts = 0.0f;  // sums of listed exponentials
+        const bool list_warp = lister && lt < nlw * 32;
+        if (list_warp) {
+            bool bad = y_bad && lt == 0;
+            for (int j = lt; j < k; j += LT) {
+                int c = s_ti[j], o = -1;
                 if (c < 0 || c >= V) {
                     bad |= c != -1;
-                    s_ti[j] = -1;
-                    continue;
+                    c = -1;
+                } else {
+                    o = s.at(c);
                 }
-                const int o = s.at(c);
-                if (o < 0) continue;
-                const int bit_at = o / (int)sizeof(T);
-                const uint32_t bit = 1u << (bit_at & 31);
-                if (atomicOr(&s_bits[bit_at >> 5], bit) & bit) {  // listed twice
-                    bad = true;
-                    s_ti[j] = -1;
-                    continue;
+                if (o >= 0) {
+                    const int at = o / (int)sizeof(T);
+                    const uint32_t bit = 1u << (at & 31);
+                    if (atomicOr(&s_bits[at >> 5], bit) & bit) {  // listed twice
+                        bad = true;
+                        c = o = -1;
+                    } else {
+                        T* p = reinterpret_cast<T*>(buf + o);
+                        const float v = Elem<T>::get(p);
+                        keep(j, v);
+                        s_zo[j] = v;
+                        if (rest) {
+                            *p = Elem<T>::put(-INFINITY);
+                            Rl = fmaxf(Rl, v);
+                        }
+                        if (c == y) {
+                            *s_flag = 1;
+                            if (rest) keep(k, v);
+                        }
+                    }
                 }
-                off[e] = o;
-                const float v = Elem<T>::get(reinterpret_cast<const T*>(buf + o));
-                s_zl[j] = v;
-                if (CL)
-                    for (int r = 0; r < cs; r++) st_remote(remote(s_zl + j, r), v);
-                if (rest) *reinterpret_cast<T*>(buf + o) = Elem<T>::put(-INFINITY);
+                s_ti[j] = c;
+                s_off[j] = o;
+                s_t[j] = c < 0 ? -INFINITY : s_tv[j] * it;
             }
             if (bad) atomicOr(&a.flags[FLAG_BAD_TOKEN], 1);
         }
-        if (rest) group_sync<NT>();
-        // the teacher's probabilities (every CTA of a cluster has them all)
-        float base = 0.0f, W = 0.0f;
-        bool used = false;
-        if (warp == 0) {
-            float t[LIST_PER_LANE];
-            float tm = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < LIST_PER_LANE; e++) {
-                const int j = lane + 32 * e;
-                const bool on = j < k && s_ti[j] >= 0;
-                used |= on;
-                t[e] = on ? s_tv[j] * it : -INFINITY;
-                tm = fmaxf(tm, t[e]);
+        // (a listed target may read as -inf here; its entry then gives the value)
+        const int oy = lt == 0 && hard ? s.at(y) : -1;
+        const float vy = oy >= 0 ? Elem<T>::get(reinterpret_cast<const T*>(buf + oy)) : 0.0f;
+        if (rest || !dz) group_sync<NT>();  // the list has been read (and replaced)
+        if (oy >= 0 && !(rest && *s_flag)) keep(k, vy);
+        // the teacher's side of a warp's entries: the largest and the sum of
+        // exponentials, or, where the normaliser is known, the probabilities' sum
+        if (list_warp) {
+            float tm = -INFINITY, ts = 0.0f;
+            bool used = false;
+            for (int j = lt; j < k; j += LT) {
+                tm = fmaxf(tm, s_t[j]);
+                used |= s_ti[j] >= 0;
             }
+            tm = rest ? s_tl[b] : warp_max(tm);
+            for (int j = lt; j < k; j += LT)
+                if (s_t[j] != -INFINITY) ts += ex2f((s_t[j] - tm) * LOG2E);
+            ts = warp_sum(ts);
             used = __any_sync(0xffffffffu, used);
+            if (lane == 0) s_lw[lt >> 5] = make_float4(tm, ts, used ? 1.0f : 0.0f, 0.0f);
             if (rest) {
-                base = s_tl[b];
-            } else {
-                tm = warp_max(tm);
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < LIST_PER_LANE; e++) sum += t[e] == -INFINITY ? 0.0f : ex2f((t[e] - tm) * LOG2E);
-                base = tm + logf(warp_sum(sum));
+                Rl = warp_max(Rl);
+                for (int j = lt; j < k; j += LT)
+                    if (s_off[j] >= 0) {
+                        const float v = s_zo[j];
+                        if (v != -INFINITY) {
+                            l1 += exp_of(v, Rl, LOG2E);
+                            lts += exp_of(v, Rl, ct);
+                        }
+                    }
+                l1 = warp_sum(l1);
+                lts = warp_sum(lts);
             }
-#pragma unroll
-            for (int e = 0; e < LIST_PER_LANE; e++) {
-                const int j = lane + 32 * e;
-                const float p = t[e] == -INFINITY ? 0.0f : ex2f((t[e] - base) * LOG2E);
-                if (j < k) s_p[j] = p;
-                W += p;
-            }
-            W = warp_sum(W);
         }
 
-        // first pass: sums of exponentials; at tau = 1 both are one
-        const bool hard = hard_on && y >= 0, same = it == 1.0f;
-        float R, s1, st, none;
-        if (!soft_on) {
-            sum_pass<T, NT, true, false>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-        } else if (!hard || same) {
-            sum_pass<T, NT, false, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-            if (same) s1 = st;
-        } else {
-            sum_pass<T, NT, true, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+        // first pass: sums of exponentials, s1 and st, and sl of the listed ones
+        float R = -INFINITY, s1 = 0.0f, st = 0.0f, sl = 0.0f, none;
+        const long long next = row + a.nbuf * stride;
+        const bool more = next < a.M;
+        const Slice<T> nx = slice(more ? next : row);
+        const int p2 = hard && soft_on ? pw : 0;
+        if (worker) {
+            if (!soft_on) sum_pass<T, NT, true, false>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (!hard || p2 == 1) sum_pass<T, NT, false, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (p2 == 2) sum_pass<T, NT, true, true, 2>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (p2 == 3) sum_pass<T, NT, true, true, 3>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (p2 == 4) sum_pass<T, NT, true, true, 4>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else sum_pass<T, NT, true, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            if (p2 == 1) s1 = st;
+            if (!dz && more) fill<T, NT>(nx, buf, tid);
+            merge(R, s1, st, sl, ct, hard, false);
         }
-        warp_merge(R, s1, LOG2E, st, ct);
+        if (rest && list_warp) {
+            if (NT == 32) {
+                const float m = fmaxf(R, Rl);
+                s1 = s1 * rescale(R, m, LOG2E) + l1 * rescale(Rl, m, LOG2E);
+                st *= rescale(R, m, ct);
+                sl = lts * rescale(Rl, m, ct);
+                R = m;
+            } else {
+                R = Rl;
+                s1 = l1;
+                sl = lts;
+            }
+        }
         if (NT > 32) {
-            if (lane == 0) s_part[warp] = make_float4(R, s1, st, 0.0f);
+            constexpr int W = (NT + LIST_CTA) / 32;
+            static_assert(W <= 16, "the merge below is over 16 lanes");
+            if (lane == 0) s_part[warp] = make_float4(R, s1, st, sl);
             __syncthreads();
-        }
-        if (warp == 0 && NT > 32) {
-            const float4 p = lane < NT / 32 ? s_part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-            R = p.x; s1 = p.y; st = p.z;
-            warp_merge(R, s1, LOG2E, st, ct);
+            if (!CL || warp == 0) {
+                const int l = lane & 15;
+                const float4 p = l < W ? s_part[l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+                R = p.x; s1 = p.y; st = p.z; sl = p.w;
+                merge<16>(R, s1, st, sl, ct, hard, rest);
+            }
         }
         if (CL) {
             if (warp == 0 && lane < cs) {
@@ -667,121 +787,112 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
                 st_remote(at, R);
                 st_remote(at + 4, s1);
                 st_remote(at + 8, st);
+                st_remote(at + 12, sl);
             }
             cluster_sync();
-            if (warp == 0) {
-                const float4 p = lane < cs ? s_x[par * cs + lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-                R = p.x; s1 = p.y; st = p.z;
-                warp_merge(R, s1, LOG2E, st, ct);
-            }
+            const int l = lane & (CS_MAX - 1);
+            const float4 p = l < cs ? s_x[par * cs + l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            R = p.x; s1 = p.y; st = p.z; sl = p.w;
+            merge<CS_MAX>(R, s1, st, sl, ct, hard, rest);
         }
-        // the row's loss and the coefficients of its gradient
+
+        // the teacher's normaliser and mass, and the coefficients of the gradient
+        if (NT == 32) __syncwarp();
+        float base = -INFINITY, W = 0.0f;
+        bool used = false;
+        if (rest) {
+            base = s_tl[b];
+            for (int w = 0; w < nlw; w++) {
+                W += s_lw[w].y;
+                used |= s_lw[w].z != 0.0f;
+            }
+        } else {
+            for (int w = 0; w < nlw; w++) {
+                base = fmaxf(base, s_lw[w].x);
+                used |= s_lw[w].z != 0.0f;
+            }
+            float ts = 0.0f;
+            for (int w = 0; w < nlw; w++) ts += s_lw[w].y * rescale(s_lw[w].x, base, LOG2E);
+            W = ts != 0.0f ? 1.0f : 0.0f;  // entries of probability 0 only: nothing
+            base += logf(ts);
+        }
+        const bool soft = used && soft_on;
         const float ks = g_all * a.alpha * a.tau, kh = hard ? g_all * (1.0f - a.alpha) : 0.0f;
-        if (warp == 0) {
-            __syncwarp();
-            const bool soft = used && soft_on;
-            float zl[LIST_PER_LANE];
-#pragma unroll
-            for (int e = 0; e < LIST_PER_LANE; e++) {
-                const int j = lane + 32 * e;
-                zl[e] = j < k && s_ti[j] >= 0 ? s_zl[j] : -INFINITY;
+        const float su = st;  // off the list
+        float pr = 0.0f;
+        if (rest) {
+            st += sl;
+            if (su > 0.0f) pr = fmaxf(1.0f - W, 0.0f);
+        }
+        const float rt = __fdividef(soft ? ks : 0.0f, st), A1 = hard ? __fdividef(kh, s1) : 0.0f;
+        const float Al = (W + pr) * rt, At = pr > 0.0f ? rt * (W + pr - pr * __fdividef(st, su)) : W * rt;
+        T* drow = dz ? dz + row * a.ld : nullptr;
+        if (dz && worker) {
+            // second pass: the gradient
+            const float As = soft ? At : 0.0f;
+            if (soft && hard && p2 == 2)
+                grad_pass<T, NT, true, true, 2>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+            else if (soft && hard && p2 == 3)
+                grad_pass<T, NT, true, true, 3>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+            else if (soft && hard && p2 == 4)
+                grad_pass<T, NT, true, true, 4>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+            else if (soft && hard && p2 != 1)
+                grad_pass<T, NT, true, true>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+            else if (soft || !hard)
+                grad_pass<T, NT, true, false>(s, buf, drow, V, tid, a.same_phase, R, ct, As + A1, 0.0f, nx, more);
+            else
+                grad_pass<T, NT, false, true>(s, buf, drow, V, tid, a.same_phase, R, ct, 0.0f, A1, nx, more);
+            if (rank == cs - 1)
+                for (long long c = V + tid; c < a.ld; c += NT) drow[c] = Elem<T>::put(0.0f);
+        }
+        if (list_warp && soft && rank == 0) {
+            const float ls = logf(st);
+            float part = 0.0f;
+            for (int j = lt; j < k; j += LT) {
+                const float lp = s_t[j] - base, p = ex2f(lp * LOG2E);
+                if (s_t[j] != -INFINITY && (p > 0.0f || p != p)) part += p * (lp - ((s_zl[j] - R) * it - ls));
             }
-            const float sr0 = st;
-            float sr = sr0;
-            if (rest) {  // the sums so far are without the list
-                float m = R;
-#pragma unroll
-                for (int e = 0; e < LIST_PER_LANE; e++) m = fmaxf(m, zl[e]);
-                m = warp_max(m);
-                float l1 = 0.0f, lt = 0.0f;
-#pragma unroll
-                for (int e = 0; e < LIST_PER_LANE; e++)
-                    if (zl[e] != -INFINITY) {
-                        l1 += exp_of(zl[e], m, LOG2E);
-                        lt += exp_of(zl[e], m, ct);
-                    }
-                s1 = s1 * rescale(R, m, LOG2E) + warp_sum(l1);
-                sr = sr0 * rescale(R, m, ct);
-                st = sr + warp_sum(lt);
-                R = m;
-            }
-            float loss = 0.0f, off_c = 0.0f, Wl = W;
+            part = warp_sum(part);
+            if (lane == 0) s_ll[lt >> 5] = part;
+        }
+        group_sync<NT>();  // the second pass's stores come before those of the list
+        if (lt == 0 && rank == 0) {
+            float loss = 0.0f;
             if (soft) {
-                const float ls = logf(st);
-                float part = 0.0f;
-#pragma unroll
-                for (int e = 0; e < LIST_PER_LANE; e++) {
-                    const int j = lane + 32 * e;
-                    if (j < k && s_ti[j] >= 0) {
-                        const float p = s_p[j];
-                        if (p > 0.0f || p != p) part += p * ((s_tv[j] * it - base) - ((zl[e] - R) * it - ls));
-                    }
-                }
-                loss = warp_sum(part);
-                off_c = Wl;
-                if (rest && sr > 0.0f) {
-                    const float pr = fmaxf(1.0f - W, 0.0f);
-                    if (pr > 0.0f) loss += pr * (logf(pr) - (logf(sr) - ls));
-                    Wl += pr;
-                    off_c = Wl - pr * st / sr;
-                }
+                for (int w = 0; w < nlw; w++) loss += s_ll[w];
+                if (pr > 0.0f) loss += pr * (logf(pr) - logf(__fdividef(su, st)));
                 loss *= a.alpha * a.tau * a.tau;
             }
             if (hard) loss += (1.0f - a.alpha) * (R + logf(s1) - s_zl[k]);
-            if (lane == 0) {
-                s_fin[0] = R;
-                s_fin[1] = soft ? ks * off_c / st : 0.0f;
-                s_fin[2] = hard ? kh / s1 : 0.0f;
-                s_fin[3] = soft ? ks * Wl / st : 0.0f;
-                s_fin[4] = soft ? 1.0f : 0.0f;
-                if (rank == 0) a.row_loss[row] = loss;
-            }
+            a.row_loss[row] = loss;
         }
-        group_sync<NT>();
-        const float m = s_fin[0], At = s_fin[1], A1 = s_fin[2];
-        const bool soft = s_fin[4] != 0.0f;
-        const long long next = row + a.nbuf * stride;
-        if (dz) {
-            // second pass: the gradient
-            char* drow = reinterpret_cast<char*>(dz + row * a.ld);
-            if (soft && hard && !same) grad_pass<T, NT, true, true>(s, buf, drow, V, tid, a.same_phase, m, ct, At, A1);
-            else if (soft || !hard) grad_pass<T, NT, true, false>(s, buf, drow, V, tid, a.same_phase, m, ct, At + A1, 0.0f);
-            else grad_pass<T, NT, false, true>(s, buf, drow, V, tid, a.same_phase, m, ct, 0.0f, A1);
-            if (rank == cs - 1)
-                for (long long c = V + tid; c < a.ld; c += NT) reinterpret_cast<T*>(drow)[c] = Elem<T>::put(0.0f);
-        }
-        if (next < a.M) fill<T, NT>(slice(next), buf, tid);
-        group_sync<NT>();  // the second pass's stores come before those of the list
-        if (warp == 0) {
-            T* drow = dz ? dz + row * a.ld : nullptr;
-            const float Al = s_fin[3];
-            bool y_listed = false;
-#pragma unroll
-            for (int e = 0; e < LIST_PER_LANE; e++) {
-                const int j = lane + 32 * e;
-                if (j >= k) continue;
-                const int c = s_ti[j];
-                y_listed |= c >= 0 && c == y;
-                if (off[e] < 0) continue;
-                s_bits[off[e] / (int)sizeof(T) >> 5] = 0;
-                if (!drow) continue;
+        if (list_warp) {
+            for (int j = lt; j < k; j += LT) {
+                const int o = s_off[j], c = s_ti[j];
+                if (o < 0) continue;
+                s_bits[o / (int)sizeof(T) >> 5] = 0;
+                if (!dz) continue;
                 float r = 0.0f;
-                if (soft) r = Al * exp_of(s_zl[j], m, ct) - ks * s_p[j];
-                if (hard) r += A1 * exp_of(s_zl[j], m, LOG2E) - (c == y ? kh : 0.0f);
+                if (soft) r = Al * exp_of(s_zl[j], R, ct) - (s_t[j] == -INFINITY ? 0.0f : ks * ex2f((s_t[j] - base) * LOG2E));
+                if (hard) r += A1 * exp_of(s_zl[j], R, LOG2E) - (c == y ? kh : 0.0f);
                 drow[c] = Elem<T>::put(r);
             }
-            y_listed = __any_sync(0xffffffffu, y_listed);
-            if (drow && hard && !y_listed && lane == 0 && s.at(y) >= 0) {
-                float r = A1 * exp_of(s_zl[k], m, LOG2E) - kh;
-                if (soft) r += At * exp_of(s_zl[k], m, ct);
+        }
+        if (lt == 0) {
+            if (dz && hard && !*s_flag && s.at(y) >= 0) {
+                float r = A1 * exp_of(s_zl[k], R, LOG2E) - kh;
+                if (soft) r += At * exp_of(s_zl[k], R, ct);
                 drow[y] = Elem<T>::put(r);
             }
-            if (next < a.M) copy_lists(next, b);
+            *s_flag = 0;
         }
+        if (more) copy_lists(next, b);
         cp_commit();
         const long long n1 = row + stride, n2 = n1 + stride;
-        if (n1 < a.M) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
-        if (n2 < a.M) edge = edge_load(slice(n2), V, tid);
+        if (lt >= 0 && lt < 16) {
+            if (n1 < a.M) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, lt);
+            if (n2 < a.M) edge = edge_load(slice(n2), V, lt);
+        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -811,7 +922,7 @@ __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row
 // How M rows of G granules are spread: the group size, the CTAs a row is
 // shared by, and whether two rows of a group are on chip at once.
 struct Plan {
-    int nt = 0, cs = 1, nbuf = 2, Gs = 0, ctas = 0;
+    int nt = 0, cs = 1, nbuf = 2, Gs = 0, ctas = 0, threads = 0;
     size_t smem = 0;
 };
 
@@ -819,7 +930,7 @@ constexpr size_t SMEM_CTA = 232448;  // 227 KB
 constexpr size_t SMEM_SM = 233472;   // 228 KB, of which each CTA takes 1 KB more than its own
 constexpr size_t SMEM_HALF = SMEM_SM / 2 - 1024;
 
-template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, Bytes&& bytes) {
+template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, int big, Bytes&& bytes) {
     p.cs = 1;
     p.nbuf = 1;
     // two CTAs of an SM, each with a row (or slice) of its own: a larger row is cut
@@ -829,13 +940,14 @@ template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, B
     // few rows are cut so that every SM has a part
     while (p.cs < CS_MAX && M * p.cs * 2 <= sms && G / (p.cs * 2) >= 256) p.cs *= 2;
     p.Gs = (G + p.cs - 1) / p.cs;
-    p.nt = p.cs == 1 && G <= 128 ? 32 : p.Gs <= 2048 ? 256 : 512;
-    if (p.nt != 512) p.nbuf = 2;
+    p.nt = p.cs == 1 && G <= 128 ? 32 : p.Gs <= 2048 ? 256 : big;
+    if (p.Gs <= 2048) p.nbuf = 2;
     p.smem = (size_t)bytes(p.nt, p.Gs, p.nbuf, p.cs > 1) * cta_groups(p.nt);
     const long long groups = (M + cta_groups(p.nt) - 1) / cta_groups(p.nt);
     const int per_sm = std::max<int>(1, std::min<int>(cta_per_sm(p.nt), (int)(SMEM_SM / (p.smem + 1024))));
     const long long room = std::max<long long>(1, (long long)sms * per_sm / p.cs);
     p.ctas = (int)(std::min(groups, room) * p.cs);
+    p.threads = cta_threads(p.nt);
     return true;
 }
 
@@ -849,7 +961,7 @@ template <typename... KA, typename... A>
 void launch_rows(const Launch& L, void (*kern)(KA...), const Plan& p, A&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.ctas);
-    cfg.blockDim = dim3((unsigned)cta_threads(p.nt));
+    cfg.blockDim = dim3((unsigned)p.threads);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = L.stream;
     cudaLaunchAttribute at[2];
@@ -887,7 +999,7 @@ template <typename T> int row_granules(const void* z, long long ld, int V) {
 template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     Plan p;
     const int k = a.k;
-    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), [k](int nt, int Gs, int nbuf, bool cl) {
+    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), 512, [k](int nt, int Gs, int nbuf, bool cl) {
             return (size_t)TopLayout(nt, Gs, nbuf, k, cl).total;
         }))
         return false;
@@ -902,17 +1014,16 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
 template <typename T> bool distill(const Launch& L, const void* z, void* dz, DistillArgs a) {
     Plan p;
     const int k = a.k;
-    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), [k](int nt, int Gs, int nbuf, bool cl) {
+    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), 256, [k](int nt, int Gs, int nbuf, bool cl) {
             return (size_t)DistillLayout(nt, Gs, nbuf, k, Elem<T>::EPG, cl).total;
         }))
         return false;
     a.Gs = p.Gs; a.cs = p.cs; a.nbuf = p.nbuf;
+    p.threads = distill_threads(p.nt);
     a.same_phase = (((uintptr_t)z ^ (uintptr_t)dz) & 15) == 0;
     if (p.nt == 32) ROW_KERNEL(k_distill, 32, false, (const T*)z, (T*)dz, a);
-    if (p.nt == 256 && p.cs == 1) ROW_KERNEL(k_distill, 256, false, (const T*)z, (T*)dz, a);
-    if (p.nt == 256) ROW_KERNEL(k_distill, 256, true, (const T*)z, (T*)dz, a);
-    if (p.cs == 1) ROW_KERNEL(k_distill, 512, false, (const T*)z, (T*)dz, a);
-    ROW_KERNEL(k_distill, 512, true, (const T*)z, (T*)dz, a);
+    if (p.cs == 1) ROW_KERNEL(k_distill, 256, false, (const T*)z, (T*)dz, a);
+    ROW_KERNEL(k_distill, 256, true, (const T*)z, (T*)dz, a);
 }
 
 }  // namespace

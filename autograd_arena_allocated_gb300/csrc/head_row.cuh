@@ -53,6 +53,16 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     return r;
 }
 
+// x^N for N = 2, 3, 4 (other N: x)
+template <int N> __device__ __forceinline__ f2 powi(f2 x) {
+    const f2 q = mul2(x, x);
+    return N == 2 ? q : N == 3 ? mul2(q, x) : N == 4 ? mul2(q, q) : x;
+}
+template <int N> __device__ __forceinline__ float powi(float x) {
+    const float q = x * x;
+    return N == 2 ? q : N == 3 ? q * x : N == 4 ? q * q : x;
+}
+
 // ------------------------------------------------------------ storage types
 // A granule of EPG elements as EPG / 2 pairs of floats, and back.  Max is what
 // maxima are kept in (a pair for the 16-bit types): exact, and a NaN is passed
@@ -138,9 +148,8 @@ template <> struct Elem<__half> : Elem16<__half, __half2, CvtHalf> {
 };
 
 // ------------------------------------------------------------ copies
-__device__ __forceinline__ void cp16(void* s, const void* g) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(s)), "l"(g)
-                 : "memory");
+template <int AT> __device__ __forceinline__ void cp16(uint32_t s, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(s), "l"(g), "n"(AT) : "memory");
 }
 __device__ __forceinline__ void cp4(void* s, const void* g) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(s)), "l"(g)
@@ -193,66 +202,68 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // ------------------------------------------------------------ a row's slice
 template <typename T> struct Slice {
-    const char* base;  // the row's first granule (16-byte boundary at or below its start)
-    int ph;            // byte offset of column 0 from base
-    int g0, g1;        // granules of this CTA
-    int gi0, gi1;      // granules wholly inside the row
-    int G;             // granules of the row
+    const char* base;  // the slice's first granule in memory
+    int ph;            // byte offset of column 0 from the row's first granule
+    int g0, n;         // first granule of this CTA, and how many
+    int i0, i1;        // slots whose granules are wholly inside the row
+    bool head, tail;   // this slice has a granule that column 0 (the last column) is inside of
 
     __device__ __forceinline__ Slice(const T* z, long long row, long long ld, int V, int rank, int Gs) {
         const char* p = reinterpret_cast<const char*>(z + row * ld);
         ph = (int)((uintptr_t)p & 15);
-        base = p - ph;
-        const int end = ph + V * (int)sizeof(T);
-        G = (end + 15) >> 4;
+        const int end = ph + V * (int)sizeof(T), G = (end + 15) >> 4, full = end >> 4;
         g0 = min(rank * Gs, G);
-        g1 = min(g0 + Gs, G);
-        gi0 = ph ? 1 : 0;
-        gi1 = end >> 4;
+        n = min(Gs, G - g0);
+        base = p - ph + (long long)g0 * 16;
+        i0 = ph && g0 == 0 ? 1 : 0;
+        i1 = min(n, max(0, full - g0));
+        head = ph && g0 == 0 && n > 0;
+        tail = i1 < n && !(head && n == 1);
     }
-    // column of the first element of granule g (may be negative at the head)
-    __device__ __forceinline__ int col(int g) const { return (g * 16 - ph) / (int)sizeof(T); }
-    __device__ __forceinline__ bool inner(int g) const { return g >= gi0 && g < gi1; }
+    // column of the first element of slot i (may be negative at the head)
+    __device__ __forceinline__ int col(int i) const { return ((g0 + i) * 16 - ph) / (int)sizeof(T); }
+    __device__ __forceinline__ bool inner(int i) const { return i >= i0 && i < i1; }
     // byte offset in the buffer of column c, or -1 if another CTA has it
     __device__ __forceinline__ int at(int c) const {
-        const int b = ph + c * (int)sizeof(T), g = b >> 4;
-        return g >= g0 && g < g1 ? b - g0 * 16 : -1;
+        const int b = ph + c * (int)sizeof(T) - g0 * 16;
+        return b >= 0 && b < n * 16 ? b : -1;
     }
 };
 
-// Copies thread tid's granules of the slice into buf.
+// Copies worker tid's granules (of NT workers) of the slice into buf.
 template <typename T, int NT>
 __device__ __forceinline__ void fill(const Slice<T>& s, char* buf, int tid) {
-    const int lo = max(s.g0, s.gi0), hi = min(s.g1, s.gi1);
-    int g = s.g0 + tid;
-    if (g < lo) g += NT;  // the head's granule comes element by element
-#pragma unroll 4
-    for (; g < hi; g += NT) cp16(buf + (g - s.g0) * 16, s.base + (long long)g * 16);
+    int i = tid < s.i0 ? tid + NT : tid;  // the head's granule comes element by element
+    const char* g = s.base + (long long)i * 16;
+    uint32_t b = (uint32_t)__cvta_generic_to_shared(buf) + i * 16;
+    for (; i + 3 * NT < s.i1; i += 4 * NT, g += 64 * NT, b += 64 * NT) {
+        cp16<0>(b, g);
+        cp16<16 * NT>(b, g);
+        cp16<32 * NT>(b, g);
+        cp16<48 * NT>(b, g);
+    }
+    for (; i < s.i1; i += NT, g += 16 * NT, b += 16 * NT) cp16<0>(b, g);
 }
 
-// The element of an edge granule that thread tid < 16 of the group looks
-// after: threads 0..7 the head's, 8..15 the tail's.
+// The slot of the edge granule that thread tid < 16 of the group looks after
+// one element of: threads 0..7 the head's, 8..15 the tail's; -1: none.
 template <typename T>
-__device__ __forceinline__ int edge_granule(const Slice<T>& s, int tid) {
-    if (tid >= 16) return -1;
-    const int i = tid & 7;
-    if (i >= Elem<T>::EPG) return -1;
-    int g;
-    if (tid < 8) g = s.gi0 > 0 ? 0 : -1;
-    else g = s.gi1 < s.G && !(s.gi0 > 0 && s.G == 1) ? s.G - 1 : -1;
-    return g >= s.g0 && g < s.g1 ? g : -1;
+__device__ __forceinline__ int edge_slot(const Slice<T>& s, int tid) {
+    if (tid >= 16 || (tid & 7) >= Elem<T>::EPG) return -1;
+    if (tid < 8) return s.head ? 0 : -1;
+    return s.tail ? s.n - 1 : -1;
 }
 template <typename T>
 __device__ __forceinline__ T edge_load(const Slice<T>& s, int V, int tid) {
-    const int g = edge_granule(s, tid);
-    if (g < 0) return Elem<T>::put(-INFINITY);
-    const int c = s.col(g) + (tid & 7);
-    return c >= 0 && c < V ? reinterpret_cast<const T*>(s.base + s.ph)[c] : Elem<T>::put(-INFINITY);
+    const int i = edge_slot(s, tid);
+    const int c = i < 0 ? -1 : s.col(i) + (tid & 7);
+    return c >= 0 && c < V ? reinterpret_cast<const T*>(s.base)[i * Elem<T>::EPG + (tid & 7)]
+                           : Elem<T>::put(-INFINITY);
 }
 template <typename T>
 __device__ __forceinline__ void edge_store(const Slice<T>& s, char* buf, T v, int tid) {
-    const int g = edge_granule(s, tid);
-    if (g >= 0) reinterpret_cast<T*>(buf + (g - s.g0) * 16)[tid & 7] = v;
+    const int i = edge_slot(s, tid);
+    if (i >= 0) reinterpret_cast<T*>(buf)[i * Elem<T>::EPG + (tid & 7)] = v;
 }
 
 // ------------------------------------------------------------ sums of exponentials
@@ -273,83 +284,120 @@ __device__ __forceinline__ float exp_of(float z, float r, float c) { return ex2f
 __device__ __forceinline__ float unbias(float R, float c, float nb) { return ex2f(-fmaf(R, c, nb)); }
 
 // SA, SB: whether the sum with coefficient ca, cb is wanted.  tm: the thread's
-// largest value.  R = -inf where there is no value above -inf.
-template <typename T, int NT, bool SA, bool SB>
+// largest value.  R = -inf where there is no value above -inf.  Granules are
+// taken four at a time, so that the reference is looked at once for four.
+//
+// PW = n (2, 3 or 4): ca is n cb, and the first sum's terms are the n-th powers
+// of the second's.  Two softmaxes at one exponential an element: with two, the
+// special-function unit (32 a cycle and SM) is what a pass waits for.
+template <typename T, int NT, bool SA, bool SB, int PW = 0>
 __device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int tid, float ca, float cb, float lift,
                                          float& tm, float& R, float& sa, float& sb) {
     using E = Elem<T>;
-    constexpr int H = E::EPG / 2;
-    const int g1 = s.g1 - s.g0;
+    constexpr int H = E::EPG / 2, U = 4;
     const uint4* v = reinterpret_cast<const uint4*>(buf);
     typename E::Max m = E::to_max(-INFINITY);
-    if (tid < g1) m = E::gmax(v[tid]);
     f2 xa = pk(0.0f, 0.0f), xb = xa;
-    R = warp_max(E::value(m));
-    bool far = is_far(R) && R != -INFINITY;
-    float lim = R + lift;  // a larger value moves the reference; -inf: there is none yet
-    if (is_far(R)) R = 0.0f;
-    float na = -(R * ca), nb = -(R * cb);
-    typename E::Max top = E::to_max(lim);
-    const f2 ca2 = pk(ca, ca), cb2 = pk(cb, cb);
+    float lim = -INFINITY, na = 0.0f, nb = 0.0f;  // lim: a larger value moves the reference; -inf: there is none yet
+    bool far = false;
+    R = 0.0f;
+    if (SA || SB) {
+        const float w = warp_max(tid < s.n ? E::value(E::gmax(v[tid])) : -INFINITY);
+        far = is_far(w) && w != -INFINITY;
+        if (!is_far(w)) {
+            R = w;
+            lim = R + lift;
+            na = -(R * ca);
+            nb = -(R * cb);
+        }
+    }
     f2 na2 = pk(na, na), nb2 = pk(nb, nb);
-#pragma unroll 2
-    for (int g = tid; g < g1; g += NT) {
-        const uint4 u = v[g];
-        const typename E::Max gm = E::gmax(u);
+    const f2 ca2 = pk(ca, ca), cb2 = pk(cb, cb);
+    auto look = [&](typename E::Max gm) {
         m = E::max2(m, gm);
-        if (SA || SB) {
-            if (E::above(gm, top)) {
-                const float vm = E::value(gm);
-                if (is_far(vm)) {
-                    far |= vm > 0.0f;
-                } else if (vm > lim) {
-                    R = vm;
-                    const float ma = -(R * ca), mb = -(R * cb);
-                    const float fa = lim == -INFINITY ? 0.0f : ex2f(ma - na);
-                    const float fb = lim == -INFINITY ? 0.0f : ex2f(mb - nb);
-                    if (SA) xa = mul2(xa, pk(fa, fa));
-                    if (SB) xb = mul2(xb, pk(fb, fb));
-                    na = ma;
-                    nb = mb;
-                    na2 = pk(na, na);
-                    nb2 = pk(nb, nb);
-                    lim = R + lift;
-                    top = E::to_max(lim);
-                }
+        if (!(SA || SB)) return;
+        const float vm = E::value(gm);
+        if (vm > lim) {
+            if (is_far(vm)) {
+                far |= vm > 0.0f;
+                return;
             }
-            f2 e[H];
-            E::unpack(u, e);
-            float x, y;
-            if (SA) {
+            R = vm;
+            const float ma = -(R * ca), mb = -(R * cb);
+            const float fb = lim == -INFINITY ? 0.0f : ex2f(mb - nb);
+            const float fa = PW ? powi<PW>(fb) : lim == -INFINITY ? 0.0f : ex2f(ma - na);
+            if (SA) xa = mul2(xa, pk(fa, fa));
+            if (SB) xb = mul2(xb, pk(fb, fb));
+            na = ma;
+            nb = mb;
+            na2 = pk(na, na);
+            nb2 = pk(nb, nb);
+            lim = R + lift;
+        }
+    };
+    auto take = [&](const uint4& u) {
+        f2 e[H];
+        E::unpack(u, e);
+        float x, y;
+        if (PW) {
 #pragma unroll
-                for (int i = 0; i < H; i++) {
-                    unpk(fma2(e[i], ca2, na2), x, y);
-                    xa = add2(xa, pk(ex2f(x), ex2f(y)));
-                }
+            for (int i = 0; i < H; i++) {
+                unpk(fma2(e[i], cb2, nb2), x, y);
+                const f2 q = pk(ex2f(x), ex2f(y));
+                xb = add2(xb, q);
+                xa = add2(xa, powi<PW>(q));
             }
-            if (SB) {
+            return;
+        }
+        if (SA) {
 #pragma unroll
-                for (int i = 0; i < H; i++) {
-                    unpk(fma2(e[i], cb2, nb2), x, y);
-                    xb = add2(xb, pk(ex2f(x), ex2f(y)));
-                }
+            for (int i = 0; i < H; i++) {
+                unpk(fma2(e[i], ca2, na2), x, y);
+                xa = add2(xa, pk(ex2f(x), ex2f(y)));
             }
         }
+        if (SB) {
+#pragma unroll
+            for (int i = 0; i < H; i++) {
+                unpk(fma2(e[i], cb2, nb2), x, y);
+                xb = add2(xb, pk(ex2f(x), ex2f(y)));
+            }
+        }
+    };
+    int i = tid;
+    for (; i + (U - 1) * NT < s.n; i += U * NT) {
+        uint4 u[U];
+#pragma unroll
+        for (int j = 0; j < U; j++) u[j] = v[i + j * NT];
+        look(E::max2(E::max2(E::gmax(u[0]), E::gmax(u[1])), E::max2(E::gmax(u[2]), E::gmax(u[3]))));
+        if (SA || SB) {
+#pragma unroll
+            for (int j = 0; j < U; j++) take(u[j]);
+        }
+    }
+#pragma unroll 1
+    for (; i < s.n; i += NT) {
+        const uint4 u = v[i];
+        look(E::gmax(u));
+        if (SA || SB) take(u);
     }
     tm = E::value(m);
     sa = sb = 0.0f;
     if (SA || SB) {
         float x, y;
         unpk(xa, x, y);
-        if (SA) sa = (x + y) * unbias(R, ca, na);
+        const float ub = unbias(R, cb, nb);
+        if (SA) sa = (x + y) * (PW ? powi<PW>(ub) : unbias(R, ca, na));
         unpk(xb, x, y);
-        if (SB) sb = (x + y) * unbias(R, cb, nb);
+        if (SB) sb = (x + y) * ub;
         if (far) {
             R = tm;
             sa = sb = 0.0f;
-            for (int g = tid; g < g1; g += NT)
-                for (int i = 0; i < E::EPG; i++) {
-                    const float z = E::get(reinterpret_cast<const T*>(v + g) + i);
+#pragma unroll 1
+            for (int g = tid; g < s.n; g += NT)
+#pragma unroll 1
+                for (int j = 0; j < E::EPG; j++) {
+                    const float z = E::get(reinterpret_cast<const T*>(v + g) + j);
                     const float d = z == R ? 0.0f : z - R;  // inf - inf is a term of 1
                     if (SA) sa += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * ca);
                     if (SB) sb += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * cb);
@@ -366,16 +414,37 @@ __device__ __forceinline__ float rescale(float from, float to, float c) {
     return from == -INFINITY ? 0.0f : ex2f((from - to) * c);
 }
 
-// Merges the lanes' sums; a lane without terms has R = -inf and 0.
-__device__ __forceinline__ void warp_merge(float& R, float& s, float c) {
-    const float m = warp_max(R);
-    s = warp_sum(s * rescale(R, m, c));
+// Merges the sums of lanes that differ in their lowest bits (all below N); a
+// lane without terms has R = -inf and 0.  The three have coefficients LOG2E, ct
+// and ct.
+template <int N = 32> __device__ __forceinline__ void merge(float& R, float& s, float c) {
+    float m = R;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    s *= rescale(R, m, c);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     R = m;
 }
-__device__ __forceinline__ void warp_merge(float& R, float& s, float c, float& t, float ct) {
-    const float m = warp_max(R);
-    s = warp_sum(s * rescale(R, m, c));
-    t = warp_sum(t * rescale(R, m, ct));
+template <int N = 32>
+__device__ __forceinline__ void merge(float& R, float& s1, float& st, float& sl, float ct, bool one, bool list) {
+    float m = R;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = rescale(R, m, ct);
+    st *= f;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) st += __shfl_xor_sync(0xffffffffu, st, o);
+    if (one) {
+        s1 *= rescale(R, m, LOG2E);
+#pragma unroll
+        for (int o = N / 2; o > 0; o >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+    }
+    if (list) {
+        sl *= f;
+#pragma unroll
+        for (int o = N / 2; o > 0; o >>= 1) sl += __shfl_xor_sync(0xffffffffu, sl, o);
+    }
     R = m;
 }
 
