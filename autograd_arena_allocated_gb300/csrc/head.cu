@@ -93,11 +93,25 @@ template <int NT> __device__ __forceinline__ int group_count(int c, int* s_red, 
     return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? r[lane] : 0);
 }
 
-// f(key order, column) for every element of the thread's granules
-template <typename T, int NT, typename F>
-__device__ __forceinline__ void each_element(const Slice<T>& s, const char* buf, int V, int tid, F&& f) {
+// where a thread's granules are read from: the on-chip copy, or memory
+struct OnChip {
+    const char* buf;
+    template <typename T> __device__ __forceinline__ uint4 get(const Slice<T>&, int i, int) const {
+        return reinterpret_cast<const uint4*>(buf)[i];
+    }
+};
+struct InMemory {
+    template <typename T> __device__ __forceinline__ uint4 get(const Slice<T>& s, int i, int V) const {
+        return s.inner(i) ? reinterpret_cast<const uint4*>(s.base)[i]
+                          : edge_granule(reinterpret_cast<const T*>(s.base) - s.col(0), s.col(i), V);
+    }
+};
+
+// f(value, column) for every element of the thread's granules
+template <typename T, int NT, typename S, typename F>
+__device__ __forceinline__ void each_element(const Slice<T>& s, const S& src, int V, int tid, F&& f) {
     for (int g = tid; g < s.n; g += NT) {
-        const uint4 u = reinterpret_cast<const uint4*>(buf)[g];
+        const uint4 u = src.get(s, g, V);
         f2 e[Elem<T>::EPG / 2];
         Elem<T>::unpack(u, e);
         const int c0 = s.col(g);
@@ -116,8 +130,8 @@ __device__ __forceinline__ void each_element(const Slice<T>& s, const char* buf,
 // values are more than are needed, the last column that is taken.  Used where
 // the threads' maxima say too little: rows of a warp, rows with most columns
 // masked, rows of few different values.
-template <typename T, int NT>
-__device__ void exact_candidates(const Slice<T>& s, const char* buf, int V, int kk, int n_el,
+template <typename T, int NT, typename S>
+__device__ __noinline__ void exact_candidates(const Slice<T>& s, const S& buf, int V, int kk, int n_el,
                                  unsigned long long* s_cand, int* s_cnt, int* s_red, int tid) {
     int turn = 0;
     if (tid == 0) *s_cnt = 0;
@@ -162,6 +176,22 @@ __device__ void exact_candidates(const Slice<T>& s, const char* buf, int V, int 
         if (o >= above || (o >= t && col <= last)) s_cand[atomicAdd(s_cnt, 1)] = top_key(v, col);
     });
     group_sync<NT>();
+}
+
+// out(rank, key) for the kk first of cnt candidates in list order; four lanes count for a candidate
+template <int NT, typename F>
+__device__ __forceinline__ void ranks(const unsigned long long* s_cand, int cnt, int kk, int tid, F&& out) {
+    for (int i0 = 0; i0 < cnt; i0 += NT / 4) {
+        const int i = i0 + tid / 4;
+        if (__all_sync(0xffffffffu, i >= cnt)) break;
+        const unsigned long long key = i < cnt ? s_cand[i] : ~0ull;
+        int r = 0;
+#pragma unroll 4
+        for (int j = tid & 3; j < cnt; j += 4) r += s_cand[j] > key;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if ((tid & 3) == 0 && i < cnt && r < kk) out(r, key);
+    }
 }
 
 // A row's list in four stages:
@@ -319,30 +349,20 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
                 }
             }
             if (exact) {
-                exact_candidates<T, NT>(s, buf, V, kk, n_el, s_cand, s_cnt, s_red, tid);
+                exact_candidates<T, NT>(s, OnChip{buf}, V, kk, n_el, s_cand, s_cnt, s_red, tid);
                 cnt = *s_cnt;
             }
             if (here(next)) fill<T, NT>(slice(next), buf, tid);
             cp_commit();
-            // stage 4: four lanes a candidate
-            for (int i0 = 0; i0 < cnt; i0 += NT / 4) {
-                const int i = i0 + tid / 4;
-                const unsigned long long key = i < cnt ? s_cand[i] : ~0ull;
-                if (__all_sync(0xffffffffu, i >= cnt)) break;
-                int r = 0;
-#pragma unroll 4
-                for (int j = tid & 3; j < cnt; j += 4) r += s_cand[j] > key;
-                r += __shfl_xor_sync(0xffffffffu, r, 1);
-                r += __shfl_xor_sync(0xffffffffu, r, 2);
-                if ((tid & 3) == 0 && i < cnt && r < kk) {
-                    if (CL) {
-                        st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), key);
-                    } else {
-                        a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
-                        a.idx[row * k + r] = key_col(key);
-                    }
+            // stage 4
+            ranks<NT>(s_cand, cnt, kk, tid, [&](int r, unsigned long long key) {
+                if (CL) {
+                    st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), key);
+                } else {
+                    a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
+                    a.idx[row * k + r] = key_col(key);
                 }
-            }
+            });
             if (CL)
                 for (int r = kk + tid; r < k; r += NT) st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), 0ull);
             if (want && warp == 0) {
@@ -407,6 +427,270 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
             if (here(n1)) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
             if (here(n2)) edge = edge_load(slice(n2), V, tid);
         }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ------------------------------------------------------------ top logits of many rows
+// A warp a row, for calls with more rows than the SMs hold warps: the row
+// streams through a ring of the warp's own (each lane reads what it copied, so
+// there is no barrier at all), and what stays of it is the largest value of
+// every block of UB granules of a lane.  The k-th largest of those is the
+// threshold; the few blocks at or above it (k, and those that tie) are read
+// again from memory, and their elements at or above it are ranked.  Reading
+// 64 blocks of four granules again is 8% of a row of 50257 16-bit logits; a
+// whole row on chip (k_top_rows) needs no second read but waits at its
+// barriers: 940 us for 32768 such rows.
+// A row with more candidates than there is room for (ties, masks) is gone
+// through bit by bit from memory.
+constexpr int TS_WARPS = 4;                 // of a CTA
+constexpr int TS_BLOCKS = 64;               // blocks of a lane
+constexpr int TS_CAND = 256;
+constexpr int TS_U = 4;                     // granules of a lane in a stage of the ring
+constexpr int TS_RING = 2 * TS_U * 32 * 16;  // two stages
+
+template <typename T> __host__ __device__ constexpr int stream_warp_smem() {
+    return TS_RING + TS_BLOCKS * 32 * (int)sizeof(T) + TS_CAND * (8 + 2) + 16;
+}
+
+// A lane's block maxima, as the counting below reads them: pairs for the 16-bit types.
+template <typename T> struct Blocks {
+    static constexpr int PER = sizeof(T) == 2 ? 2 : 1;  // blocks of a word
+    uint32_t* w;                                        // [word][lane]
+    __device__ __forceinline__ void put(int b, int lane, T v) {
+        reinterpret_cast<T*>(w + (b / PER) * 32 + lane)[b % PER] = v;
+    }
+    // how many of the lane's n words' blocks are at least t
+    __device__ __forceinline__ int count(int n, int lane, T t) const;
+};
+template <> __device__ __forceinline__ int Blocks<float>::count(int n, int lane, float t) const {
+    int c = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; i++) c += __uint_as_float(w[i * 32 + lane]) >= t;
+    return c;
+}
+template <> __device__ __forceinline__ int Blocks<__nv_bfloat16>::count(int n, int lane, __nv_bfloat16 t) const {
+    const __nv_bfloat162 t2 = __halves2bfloat162(t, t);
+    __nv_bfloat162 c = __floats2bfloat162_rn(0.0f, 0.0f);  // whole numbers up to 32: exact
+#pragma unroll 4
+    for (int i = 0; i < n; i++) c = __hadd2(c, __hge2(*reinterpret_cast<const __nv_bfloat162*>(w + i * 32 + lane), t2));
+    return (int)(__low2float(c) + __high2float(c));
+}
+template <> __device__ __forceinline__ int Blocks<__half>::count(int n, int lane, __half t) const {
+    const __half2 t2 = __halves2half2(t, t);
+    __half2 c = __floats2half2_rn(0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < n; i++) c = __hadd2(c, __hge2(*reinterpret_cast<const __half2*>(w + i * 32 + lane), t2));
+    return (int)(__low2float(c) + __high2float(c));
+}
+
+// a storage type's values in order as whole numbers
+template <typename T> struct Ordered {
+    static constexpr int N = 8 * sizeof(T);
+    static __device__ __forceinline__ uint32_t of(T v) {
+        uint32_t u = 0;
+        memcpy(&u, &v, sizeof(T));
+        return (u >> (N - 1)) & 1 ? ~u & (0xFFFFFFFFu >> (32 - N)) : u | (1u << (N - 1));
+    }
+    static __device__ __forceinline__ T value(uint32_t o) {
+        const uint32_t u = (o >> (N - 1)) & 1 ? o ^ (1u << (N - 1)) : ~o;
+        T v;
+        memcpy(&v, &u, sizeof(T));
+        return v;
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(TS_WARPS * 32, 6)
+k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log) {
+    pdl_enter();
+    extern __shared__ __align__(16) char smem[];
+    using E = Elem<T>;
+    constexpr int PER = Blocks<T>::PER;
+    const int lane = threadIdx.x & 31;
+    char* sm = smem + (threadIdx.x >> 5) * stream_warp_smem<T>();
+    uint4* ring = reinterpret_cast<uint4*>(sm) + lane;  // [stage][granule] at steps of 32
+    Blocks<T> blocks{reinterpret_cast<uint32_t*>(sm + TS_RING)};
+    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + TS_RING + TS_BLOCKS * 32 * sizeof(T));
+    auto* s_hit = reinterpret_cast<uint16_t*>(s_cand + TS_CAND);
+    int* s_cnt = reinterpret_cast<int*>(s_hit + TS_CAND);
+    const long long first = blockIdx.x * (long long)TS_WARPS + (threadIdx.x >> 5), stride = gridDim.x * (long long)TS_WARPS;
+    const bool want = a.lse || a.lse64;
+    const float ct = LOG2E * a.inv_tau, lift = 20.0f / fmaxf(1.0f, a.inv_tau);
+    const int k = a.k, V = a.V;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, 0, a.Gs); };
+    auto copy = [&](const Slice<T>& s, int st) {  // stage st of a row
+        const int i = st * (32 * TS_U) + lane;
+        const char* g = s.base + (long long)i * 16;
+        const uint32_t b = ring_at + (st & 1) * (TS_U * 512);
+        if (i >= s.i0 && i + (TS_U - 1) * 32 < s.i1) {
+            cp16<0>(b, g);
+            cp16<512>(b, g);
+            cp16<1024>(b, g);
+            cp16<1536>(b, g);
+        } else {
+#pragma unroll
+            for (int j = 0; j < TS_U; j++)
+                if (i + j * 32 >= s.i0 && i + j * 32 < s.i1) cp16<0>(b + j * 512, g + j * 512);
+        }
+    };
+    // stages are counted in pairs, so that a row always starts in the ring's first half
+    const int S = (((a.Gs + 32 * TS_U - 1) / (32 * TS_U)) + 1) & ~1;
+    for (long long row = first; row < a.M; row += stride) {
+        const Slice<T> s = slice(row);
+        const bool more = row + stride < a.M;
+        const Slice<T> nx = slice(more ? row + stride : row);
+        if (row == first) {
+            copy(s, 0);
+            cp_commit();
+            copy(s, 1);
+            cp_commit();
+        }
+        if (lane < 2) s_cnt[lane] = 0;  // candidates, blocks
+        const int ub = 1 << ub_log, nb = ((s.n + 31) / 32 + ub - 1) >> ub_log, nw = (nb + PER - 1) / PER;
+        Sums<T, true, false> q(ct, ct, lift);
+        typename E::Max bm = E::to_max(-INFINITY);
+        int nput = 0;
+        auto put = [&](typename E::Max m) {
+            const T v = E::top(m);
+            blocks.put(nput++, lane, v);
+        };
+        for (int st = 0; st < S; st++) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            uint4 u[TS_U];
+            const int i = st * (32 * TS_U) + lane;
+            const uint4* r = ring + (st & 1) * (TS_U * 32);
+#pragma unroll
+            for (int j = 0; j < TS_U; j++) {
+                if (i + j * 32 >= s.i0 && i + j * 32 < s.i1) u[j] = r[j * 32];
+                else if (i + j * 32 < s.n) u[j] = InMemory().get(s, i + j * 32, V);
+                else u[j] = make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
+            }
+            typename E::Max g[TS_U];
+#pragma unroll
+            for (int j = 0; j < TS_U; j++) g[j] = E::gmax(u[j]);
+            if (st == 0) q.start(want ? warp_max(E::value(g[0])) : -INFINITY);
+            const typename E::Max g01 = E::max2(g[0], g[1]), g23 = E::max2(g[2], g[3]), g4 = E::max2(g01, g23);
+            q.look(g4);
+            if (st + 2 < S) copy(s, st + 2);
+            else if (more) copy(nx, st + 2 - S);
+            cp_commit();
+            if (want) {
+#pragma unroll
+                for (int j = 0; j < TS_U; j++) q.take(u[j]);
+            }
+            if (ub == 1) {
+#pragma unroll
+                for (int j = 0; j < TS_U; j++)
+                    if (nput < nw * PER) put(g[j]);
+            } else if (ub == 2) {
+                if (nput < nw * PER) put(g01);
+                if (nput < nw * PER) put(g23);
+            } else {
+                bm = E::max2(bm, g4);
+                if (((st + 1) * TS_U & (ub - 1)) == 0 || st == S - 1) {
+                    if (nput < nw * PER) put(bm);
+                    bm = E::to_max(-INFINITY);
+                }
+            }
+        }
+        while (nput < nw * PER) put(E::to_max(-INFINITY));
+        float tmax, sum, none;
+        if (q.finish(tmax, sum, none) && want)
+            each_element<T, 32>(s, InMemory(), V, lane, [&](float v, int) { q.take_far(v, sum, none); });
+        float R = q.R;
+        if (want) merge(R, sum, ct);
+
+        // the threshold: the k-th largest of the blocks' maxima
+        uint32_t hi = 0, low = 0xFFFFFFFFu >> (32 - Ordered<T>::N);
+        for (int i = 0; i < nb; i++) {
+            T v = reinterpret_cast<const T*>(blocks.w + (i / PER) * 32 + lane)[i % PER];
+            const uint32_t o = Ordered<T>::of(v);
+            hi = max(hi, o);
+            low = min(low, o);
+        }
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        low = __reduce_min_sync(0xffffffffu, low);
+        int bit = 31 - __clz(hi ^ low);
+        uint32_t t = bit < 0 ? hi : hi & ~((2u << bit) - 1u);
+        for (; bit >= 0; bit--) {
+            const uint32_t cand = t | (1u << bit);
+            const int c = __reduce_add_sync(0xffffffffu, blocks.count(nw, lane, Ordered<T>::value(cand)));
+            if (c >= k) t = cand;
+            if (c == k) break;
+        }
+        const T tv = Ordered<T>::value(t);
+        const float thr = E::get(&tv);
+        const int kk = k;
+        bool exact = !(thr > -INFINITY);  // or no number
+        __syncwarp();
+        if (!exact) {
+            for (int i = 0; i < nb; i++) {
+                const T v = reinterpret_cast<const T*>(blocks.w + (i / PER) * 32 + lane)[i % PER];
+                if (E::get(&v) >= thr) {
+                    const int p = atomicAdd(s_cnt + 1, 1);
+                    if (p < TS_CAND) s_hit[p] = (uint16_t)(i * 32 + lane);
+                }
+            }
+            __syncwarp();
+            const int nh = s_cnt[1];
+            exact = nh > TS_CAND;
+            if (!exact) {
+                const int items = nh << ub_log;
+                const uint32_t thr_o = order_of(thr);
+                const typename E::Max thr2 = E::to_max(thr);
+                for (int i0 = 0; i0 < items; i0 += 128) {
+                    uint4 u[4];
+                    int slot[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int it = i0 + j * 32 + lane;
+                        slot[j] = s.n;
+                        if (it < items) {
+                            const int h = s_hit[it >> ub_log];
+                            slot[j] = (h & 31) + 32 * (((h >> 5) << ub_log) + (it & (ub - 1)));
+                        }
+                        u[j] = slot[j] < s.n ? InMemory().get(s, slot[j], V) : make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
+                    }
+#pragma unroll 1
+                    for (int j = 0; j < 4; j++) {
+                        const uint4 x = j == 0 ? u[0] : j == 1 ? u[1] : j == 2 ? u[2] : u[3];
+                        const int sl = j == 0 ? slot[0] : j == 1 ? slot[1] : j == 2 ? slot[2] : slot[3];
+                        if (!E::at_least(E::gmax(x), thr2)) continue;
+                        f2 e[E::EPG / 2];
+                        E::unpack(x, e);
+                        const int c0 = s.col(sl);
+#pragma unroll
+                        for (int l = 0; l < E::EPG; l++) {
+                            float v0, v1;
+                            unpk(e[l / 2], v0, v1);
+                            const float v = l & 1 ? v1 : v0;
+                            const int c = c0 + l;
+                            if (order_of(v) >= thr_o && c >= 0 && c < V) {
+                                const int p = atomicAdd(s_cnt, 1);
+                                if (p < TS_CAND) s_cand[p] = top_key(v, c);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                exact = s_cnt[0] > TS_CAND;
+                __syncwarp();
+            }
+        }
+        if (exact) exact_candidates<T, 32>(s, InMemory(), V, kk, V, s_cand, s_cnt, (int*)nullptr, lane);
+        __syncwarp();
+        ranks<32>(s_cand, s_cnt[0], kk, lane, [&](int r, unsigned long long key) {
+            a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
+            a.idx[row * k + r] = key_col(key);
+        });
+        if (want && lane == 0) {
+            const bool flat = sum == sum && (R == -INFINITY || R == INFINITY);
+            if (a.lse) a.lse[row] = flat ? R : R * a.inv_tau + logf(sum);
+            if (a.lse64) a.lse64[row] = flat ? (double)R : (double)R * (double)a.inv_tau + log((double)sum);
+        }
+        __syncwarp();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -998,8 +1282,22 @@ template <typename T> int row_granules(const void* z, long long ld, int V) {
 
 template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     Plan p;
-    const int k = a.k;
-    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), 512, [k](int nt, int Gs, int nbuf, bool cl) {
+    const int k = a.k, G = row_granules<T>(z, a.ld, a.V);
+    // many rows: a warp each
+    if (G > 128 && a.M >= L.num_sms * 12 && !a.skip) {
+        int ub_log = 0;
+        while (((G + 31) / 32 + (1 << ub_log) - 1) >> ub_log > TS_BLOCKS) ub_log++;
+        static PerDevice attr;
+        if (!allow_smem(attr, k_top_stream<T>)) return false;
+        a.Gs = G;
+        p.smem = TS_WARPS * stream_warp_smem<T>();
+        p.threads = TS_WARPS * 32;
+        const int per_sm = std::min(6, (int)(SMEM_SM / (p.smem + 1024)));
+        p.ctas = std::min((a.M + TS_WARPS - 1) / TS_WARPS, L.num_sms * per_sm);
+        launch_rows(L, k_top_stream<T>, p, (const T*)z, a, ub_log);
+        return true;
+    }
+    if (!make_plan(p, L.num_sms, a.M, G, 512, [k](int nt, int Gs, int nbuf, bool cl) {
             return (size_t)TopLayout(nt, Gs, nbuf, k, cl).total;
         }))
         return false;

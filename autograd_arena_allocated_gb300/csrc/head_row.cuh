@@ -71,6 +71,7 @@ template <typename T> struct Elem;
 template <> struct Elem<float> {
     static constexpr int EPG = 4;
     using Max = float;
+    static constexpr uint32_t NINF = 0xFF800000u;
     static __device__ __forceinline__ float get(const float* p) { return *p; }
     static __device__ __forceinline__ float put(float v) { return v; }
     static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
@@ -89,6 +90,7 @@ template <> struct Elem<float> {
     }
     static __device__ __forceinline__ Max max2(Max a, Max b) { return fmaxf(a, b); }
     static __device__ __forceinline__ Max to_max(float v) { return v; }
+    static __device__ __forceinline__ float top(Max m) { return m; }
     static __device__ __forceinline__ float value(Max m) { return fmaxf(m, -INFINITY); }
     static __device__ __forceinline__ bool above(Max m, Max t) { return m > t; }       // any of m > t
     static __device__ __forceinline__ bool at_least(Max m, Max t) { return m >= t; }  // any of m >= t
@@ -113,6 +115,7 @@ template <typename T, typename P, typename Cvt> struct Elem16 {
     }
     static __device__ __forceinline__ Max max2(Max a, Max b) { return __hmax2(a, b); }
     static __device__ __forceinline__ Max to_max(float v) { return Cvt::pair(v, v); }
+    static __device__ __forceinline__ T top(Max m) { return __hmax(m.x, m.y); }
     static __device__ __forceinline__ float value(Max m) {
         return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
     }
@@ -126,6 +129,7 @@ struct CvtHalf {
     static __device__ __forceinline__ __half2 pair(float a, float b) { return __floats2half2_rn(a, b); }
 };
 template <> struct Elem<__nv_bfloat16> : Elem16<__nv_bfloat16, __nv_bfloat162, CvtBf> {
+    static constexpr uint32_t NINF = 0xFF80FF80u;
     static __device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
@@ -135,6 +139,7 @@ template <> struct Elem<__nv_bfloat16> : Elem16<__nv_bfloat16, __nv_bfloat162, C
     }
 };
 template <> struct Elem<__half> : Elem16<__half, __half2, CvtHalf> {
+    static constexpr uint32_t NINF = 0xFC00FC00u;
     static __device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
     static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& u, f2* f) {
@@ -266,6 +271,17 @@ __device__ __forceinline__ void edge_store(const Slice<T>& s, char* buf, T v, in
     if (i >= 0) reinterpret_cast<T*>(buf)[i * Elem<T>::EPG + (tid & 7)] = v;
 }
 
+// Slot i of the slice, read from memory; what lies outside the row is -inf.
+template <typename T> __device__ __noinline__ uint4 edge_granule(const T* row, int c0, int V) {
+    union {
+        T e[Elem<T>::EPG];
+        uint4 u;
+    } x;
+#pragma unroll
+    for (int j = 0; j < Elem<T>::EPG; j++) x.e[j] = c0 + j >= 0 && c0 + j < V ? row[c0 + j] : Elem<T>::put(-INFINITY);
+    return x.u;
+}
+
 // ------------------------------------------------------------ sums of exponentials
 // Sums of 2^((z - R) c) over a thread's granules in one pass, at one
 // exponential an element, without knowing the maximum: R starts at the largest
@@ -283,26 +299,26 @@ __device__ __forceinline__ float exp_of(float z, float r, float c) { return ex2f
 // 2^-(R c + nb): what sums of 2^(z c + nb) are multiplied by
 __device__ __forceinline__ float unbias(float R, float c, float nb) { return ex2f(-fmaf(R, c, nb)); }
 
-// SA, SB: whether the sum with coefficient ca, cb is wanted.  tm: the thread's
-// largest value.  R = -inf where there is no value above -inf.  Granules are
-// taken four at a time, so that the reference is looked at once for four.
-//
-// PW = n (2, 3 or 4): ca is n cb, and the first sum's terms are the n-th powers
-// of the second's.  Two softmaxes at one exponential an element: with two, the
-// special-function unit (32 a cycle and SM) is what a pass waits for.
-template <typename T, int NT, bool SA, bool SB, int PW = 0>
-__device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int tid, float ca, float cb, float lift,
-                                         float& tm, float& R, float& sa, float& sb) {
+// SA, SB: whether the sum with coefficient ca, cb is wanted.  PW = n (2, 3 or
+// 4): ca is n cb, and the first sum's terms are the n-th powers of the second's:
+// two softmaxes at one exponential an element (with two, the special-function
+// unit, 32 a cycle and SM, is what a pass waits for).
+template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
     using E = Elem<T>;
-    constexpr int H = E::EPG / 2, U = 4;
-    const uint4* v = reinterpret_cast<const uint4*>(buf);
-    typename E::Max m = E::to_max(-INFINITY);
-    f2 xa = pk(0.0f, 0.0f), xb = xa;
-    float lim = -INFINITY, na = 0.0f, nb = 0.0f;  // lim: a larger value moves the reference; -inf: there is none yet
-    bool far = false;
-    R = 0.0f;
-    if (SA || SB) {
-        const float w = warp_max(tid < s.n ? E::value(E::gmax(v[tid])) : -INFINITY);
+    static constexpr int H = E::EPG / 2;
+    typename E::Max m;  // the thread's largest values
+    f2 xa, xb, na2, nb2;
+    float R, lim, na, nb;  // a value above lim moves the reference; -inf: there is none yet
+    const float ca, cb, lift;
+    bool far;
+
+    // w: a value to start the reference from (the same in all lanes), -inf for none
+    __device__ __forceinline__ Sums(float ca_, float cb_, float lift_) : ca(ca_), cb(cb_), lift(lift_) {}
+    __device__ __forceinline__ void start(float w) {
+        m = E::to_max(-INFINITY);
+        xa = xb = pk(0.0f, 0.0f);
+        R = na = nb = 0.0f;
+        lim = -INFINITY;
         far = is_far(w) && w != -INFINITY;
         if (!is_far(w)) {
             R = w;
@@ -310,10 +326,11 @@ __device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int
             na = -(R * ca);
             nb = -(R * cb);
         }
+        na2 = pk(na, na);
+        nb2 = pk(nb, nb);
     }
-    f2 na2 = pk(na, na), nb2 = pk(nb, nb);
-    const f2 ca2 = pk(ca, ca), cb2 = pk(cb, cb);
-    auto look = [&](typename E::Max gm) {
+    // the largest values of the granules that take() will be given next
+    __device__ __forceinline__ void look(typename E::Max gm) {
         m = E::max2(m, gm);
         if (!(SA || SB)) return;
         const float vm = E::value(gm);
@@ -334,8 +351,10 @@ __device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int
             nb2 = pk(nb, nb);
             lim = R + lift;
         }
-    };
-    auto take = [&](const uint4& u) {
+    }
+    __device__ __forceinline__ void take(const uint4& u) {
+        if (!(SA || SB)) return;
+        const f2 ca2 = pk(ca, ca), cb2 = pk(cb, cb);
         f2 e[H];
         E::unpack(u, e);
         float x, y;
@@ -363,49 +382,65 @@ __device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int
                 xb = add2(xb, pk(ex2f(x), ex2f(y)));
             }
         }
-    };
+    }
+    // one value of a far row, formed without overflow; R is its largest
+    __device__ __forceinline__ void take_far(float z, float& sa, float& sb) const {
+        const float d = z == R ? 0.0f : z - R;  // inf - inf is a term of 1
+        if (SA) sa += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * ca);
+        if (SB) sb += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * cb);
+    }
+    // tm: the largest value; R = -inf where there is none above -inf.  True
+    // where the row has to be gone through again with take_far (R = tm then).
+    __device__ __forceinline__ bool finish(float& tm, float& sa, float& sb) {
+        tm = E::value(m);
+        sa = sb = 0.0f;
+        if (!(SA || SB)) return false;
+        if (far) {
+            R = tm;
+            return true;
+        }
+        float x, y;
+        const float ub = unbias(R, cb, nb);
+        unpk(xa, x, y);
+        if (SA) sa = (x + y) * (PW ? powi<PW>(ub) : unbias(R, ca, na));
+        unpk(xb, x, y);
+        if (SB) sb = (x + y) * ub;
+        if (tm == -INFINITY) R = -INFINITY;  // no terms, unless they are NaN
+        return false;
+    }
+};
+
+// Granules are taken four at a time, so that the reference is looked at once for four.
+template <typename T, int NT, bool SA, bool SB, int PW = 0>
+__device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int tid, float ca, float cb, float lift,
+                                         float& tm, float& R, float& sa, float& sb) {
+    using E = Elem<T>;
+    constexpr int U = 4;
+    const uint4* v = reinterpret_cast<const uint4*>(buf);
+    Sums<T, SA, SB, PW> q(ca, cb, lift);
+    q.start(SA || SB ? warp_max(tid < s.n ? E::value(E::gmax(v[tid])) : -INFINITY) : -INFINITY);
     int i = tid;
     for (; i + (U - 1) * NT < s.n; i += U * NT) {
         uint4 u[U];
 #pragma unroll
         for (int j = 0; j < U; j++) u[j] = v[i + j * NT];
-        look(E::max2(E::max2(E::gmax(u[0]), E::gmax(u[1])), E::max2(E::gmax(u[2]), E::gmax(u[3]))));
-        if (SA || SB) {
+        q.look(E::max2(E::max2(E::gmax(u[0]), E::gmax(u[1])), E::max2(E::gmax(u[2]), E::gmax(u[3]))));
 #pragma unroll
-            for (int j = 0; j < U; j++) take(u[j]);
-        }
+        for (int j = 0; j < U; j++) q.take(u[j]);
     }
 #pragma unroll 1
     for (; i < s.n; i += NT) {
         const uint4 u = v[i];
-        look(E::gmax(u));
-        if (SA || SB) take(u);
+        q.look(E::gmax(u));
+        q.take(u);
     }
-    tm = E::value(m);
-    sa = sb = 0.0f;
-    if (SA || SB) {
-        float x, y;
-        unpk(xa, x, y);
-        const float ub = unbias(R, cb, nb);
-        if (SA) sa = (x + y) * (PW ? powi<PW>(ub) : unbias(R, ca, na));
-        unpk(xb, x, y);
-        if (SB) sb = (x + y) * ub;
-        if (far) {
-            R = tm;
-            sa = sb = 0.0f;
+    if (q.finish(tm, sa, sb)) {
 #pragma unroll 1
-            for (int g = tid; g < s.n; g += NT)
+        for (int g = tid; g < s.n; g += NT)
 #pragma unroll 1
-                for (int j = 0; j < E::EPG; j++) {
-                    const float z = E::get(reinterpret_cast<const T*>(v + g) + j);
-                    const float d = z == R ? 0.0f : z - R;  // inf - inf is a term of 1
-                    if (SA) sa += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * ca);
-                    if (SB) sb += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * cb);
-                }
-        } else if (tm == -INFINITY) {
-            R = -INFINITY;  // no terms, unless they are NaN
-        }
+            for (int j = 0; j < E::EPG; j++) q.take_far(E::get(reinterpret_cast<const T*>(v + g) + j), sa, sb);
     }
+    R = q.R;
 }
 
 // what a sum with reference `from` is multiplied by to have the larger reference `to`

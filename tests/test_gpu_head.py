@@ -134,6 +134,34 @@ def test_top_logits_hard_rows(ctx, dtype, V):
         check_top(ctx, dtype, z, V, k)
 
 
+@pytest.mark.parametrize("dtype,M,V,ld,k,offset", [("bf16", 2500, 5003, 5003, 64, 1), ("fp32", 2100, 4500, 4500, 128, 0),
+                                                   ("fp16", 2000, 33000, 33024, 7, 0), ("bf16", 1900, 50257, 50304, 128, 0),
+                                                   ("fp32", 1900, 20000, 20001, 1, 3)])
+def test_top_logits_of_many_rows(ctx, dtype, M, V, ld, k, offset):
+    """More rows than the SMs hold at once: ordinary ones, and among them rows
+    whose list is hard to find."""
+    z = make_logits(dtype, M, V, ld, 13 + V, offset, pad=math.nan)
+    z[0, :V] = 0.25
+    z[1, :V] = torch.sort(z[1, :V]).values
+    z[2, :V] = -INF
+    z[3, :V] = -INF
+    z[3, V // 2:V // 2 + 5] = torch.tensor([1.0, 2.0, 2.0, -1.0, 2.0])
+    z[4, 7] = math.nan
+    z[5, V - 1] = INF
+    z[6, 0], z[6, 1] = INF, math.nan
+    z[7, :V] = torch.finfo(TYPES[dtype]).min
+    z[8, :V] = (torch.arange(V, device=DEV) % 3).float()
+    z[9, V // 3:V // 3 + 300] = 30.0
+    z[10, :V] = math.nan
+    z[11, :V] = -0.0
+    z[11, 5:V:9] = 0.0
+    z[12, :V] += 3000.0
+    z[M - 1, :V] = -INF
+    z[M - 1, 0:V:max(1, V // 60)] = 1.5
+    check_top(ctx, dtype, z, V, k, tau=2.0)
+    check_top(ctx, dtype, z, V, k, with_lse=False)
+
+
 # ---------------------------------------------------------------- distillation
 def ref_distill(z, V, t_vals, t_idx, t_lse, targets, alpha, tau, want_scale=False):
     """Row losses in 64 bits (differentiable in z [M, V]); with want_scale also
