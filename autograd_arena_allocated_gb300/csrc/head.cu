@@ -433,24 +433,28 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
 
 // ------------------------------------------------------------ top logits of many rows
 // A warp a row, for calls with more rows than the SMs hold warps: the row
-// streams through a ring of the warp's own (each lane reads what it copied, so
-// there is no barrier at all), and what stays of it is the largest value of
-// every block of UB granules of a lane.  The k-th largest of those is the
-// threshold; the few blocks at or above it (k, and those that tie) are read
-// again from memory, and their elements at or above it are ranked.  Reading
-// 64 blocks of four granules again is 8% of a row of 50257 16-bit logits; a
-// whole row on chip (k_top_rows) needs no second read but waits at its
-// barriers: 940 us for 32768 such rows.
+// streams through a ring of the warp's own, without a barrier, and what stays
+// of it is the largest value of every block of UB granules of a lane.  The
+// k-th largest of those is the threshold; the few blocks at or above it (k,
+// and those that tie) are read again from memory, and their elements at or
+// above it are ranked.  A lane's four granules of a stage are neighbours in
+// memory (64 bytes; in shared memory they are permuted so that eight lanes'
+// reads fall into different banks): reading 64 blocks again then is 4% of a
+// row of 50257 16-bit logits, where blocks of four granules 512 bytes apart
+// cost 26% more DRAM traffic.  A whole row on chip (k_top_rows) needs no
+// second read but waits at its barriers: 940 us for 32768 such rows.
 // A row with more candidates than there is room for (ties, masks) is gone
 // through bit by bit from memory.
-constexpr int TS_WARPS = 4;                 // of a CTA
-constexpr int TS_BLOCKS = 64;               // blocks of a lane
-constexpr int TS_CAND = 256;
+constexpr int TS_WARPS = 8;                 // of a CTA
+constexpr int TS_BLOCKS = 64;               // most blocks of a lane
 constexpr int TS_U = 4;                     // granules of a lane in a stage of the ring
 constexpr int TS_RING = 2 * TS_U * 32 * 16;  // two stages
 
-template <typename T> __host__ __device__ constexpr int stream_warp_smem() {
-    return TS_RING + TS_BLOCKS * 32 * (int)sizeof(T) + TS_CAND * (8 + 2) + 16;
+// candidates, and blocks that hold them: 24 warps of an SM have room for their
+// rings with the smaller number, 20 with the larger
+__host__ __device__ constexpr int stream_cand(int k) { return k <= 64 ? 160 : 256; }
+__host__ __device__ constexpr int stream_warp_smem(int words, int k) {
+    return TS_RING + words * 128 + stream_cand(k) * (8 + 2) + 16;
 }
 
 // A lane's block maxima, as the counting below reads them: pairs for the 16-bit types.
@@ -458,10 +462,22 @@ template <typename T> struct Blocks {
     static constexpr int PER = sizeof(T) == 2 ? 2 : 1;  // blocks of a word
     uint32_t* w;                                        // [word][lane]
     __device__ __forceinline__ void put(int b, int lane, T v) {
-        reinterpret_cast<T*>(w + (b / PER) * 32 + lane)[b % PER] = v;
+        reinterpret_cast<T*>(w + ((unsigned)b / PER) * 32 + lane)[(unsigned)b % PER] = v;
     }
     // how many of the lane's n words' blocks are at least t
     __device__ __forceinline__ int count(int n, int lane, T t) const;
+    // blocks b (even) and b + 1
+    __device__ __forceinline__ void put2(int b, int lane, typename Elem<T>::Max x, typename Elem<T>::Max y) {
+        if constexpr (PER == 2) {
+            *reinterpret_cast<typename Elem<T>::Max*>(w + b * 16 + lane) = Elem<T>::fold(x, y);
+        } else {
+            put(b, lane, x);
+            put(b + 1, lane, y);
+        }
+    }
+    __device__ __forceinline__ typename Elem<T>::Max word(int i, int lane) const {
+        return *reinterpret_cast<const typename Elem<T>::Max*>(w + i * 32 + lane);
+    }
 };
 template <> __device__ __forceinline__ int Blocks<float>::count(int n, int lane, float t) const {
     int c = 0;
@@ -500,102 +516,160 @@ template <typename T> struct Ordered {
     }
 };
 
+// element l of N pairs
+template <int N> __device__ __forceinline__ float pick(const f2 (&e)[N], int l) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        float x, y;
+        unpk(e[i], x, y);
+        v = l == 2 * i ? x : l == 2 * i + 1 ? y : v;
+    }
+    return v;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(TS_WARPS * 32, 6)
-k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log) {
+__global__ void __launch_bounds__(TS_WARPS * 32, 3)
+k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
     pdl_enter();
     extern __shared__ __align__(16) char smem[];
     using E = Elem<T>;
     constexpr int PER = Blocks<T>::PER;
     const int lane = threadIdx.x & 31;
-    char* sm = smem + (threadIdx.x >> 5) * stream_warp_smem<T>();
-    uint4* ring = reinterpret_cast<uint4*>(sm) + lane;  // [stage][granule] at steps of 32
+    const int TS_CAND = stream_cand(a.k);
+    char* sm = smem + (threadIdx.x >> 5) * stream_warp_smem(words, a.k);
     Blocks<T> blocks{reinterpret_cast<uint32_t*>(sm + TS_RING)};
-    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + TS_RING + TS_BLOCKS * 32 * sizeof(T));
+    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + TS_RING + words * 128);
     auto* s_hit = reinterpret_cast<uint16_t*>(s_cand + TS_CAND);
     int* s_cnt = reinterpret_cast<int*>(s_hit + TS_CAND);
     const long long first = blockIdx.x * (long long)TS_WARPS + (threadIdx.x >> 5), stride = gridDim.x * (long long)TS_WARPS;
     const bool want = a.lse || a.lse64;
     const float ct = LOG2E * a.inv_tau, lift = 20.0f / fmaxf(1.0f, a.inv_tau);
     const int k = a.k, V = a.V;
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, 0, a.Gs); };
+    // Granule g of a stage (128 of them) is in slot (g & ~7) | (g ^ (g >> 3 & 3)) & 7:
+    // a lane copies granules lane + 32 j and reads 4 lane + j.
+    const uint32_t ring_at =
+        (uint32_t)__cvta_generic_to_shared(sm) + ((lane & ~7) | ((lane ^ ((lane >> 3) & 3)) & 7)) * 16;
+    const uint4* own[TS_U];
+#pragma unroll
+    for (int j = 0; j < TS_U; j++) own[j] = reinterpret_cast<const uint4*>(sm) + 4 * lane + (j ^ ((lane >> 1) & 3));
+    auto whole = [&](const Slice<T>& s, int st) { return (st > 0 || s.i0 == 0) && (st + 1) * 128 <= s.i1; };
     auto copy = [&](const Slice<T>& s, int st) {  // stage st of a row
-        const int i = st * (32 * TS_U) + lane;
-        const char* g = s.base + (long long)i * 16;
-        const uint32_t b = ring_at + (st & 1) * (TS_U * 512);
-        if (i >= s.i0 && i + (TS_U - 1) * 32 < s.i1) {
+        const char* g = s.base + (long long)(st * 128 + lane) * 16;
+        const uint32_t b = ring_at + (st & 1) * 2048;
+        if (whole(s, st)) {
             cp16<0>(b, g);
             cp16<512>(b, g);
             cp16<1024>(b, g);
             cp16<1536>(b, g);
         } else {
+            const int i = st * 128 + lane;
 #pragma unroll
             for (int j = 0; j < TS_U; j++)
                 if (i + j * 32 >= s.i0 && i + j * 32 < s.i1) cp16<0>(b + j * 512, g + j * 512);
         }
+        cp_commit();
     };
     // stages are counted in pairs, so that a row always starts in the ring's first half
-    const int S = (((a.Gs + 32 * TS_U - 1) / (32 * TS_U)) + 1) & ~1;
+    const int SX = (a.Gs + 127) / 128, S = (SX + 1) & ~1;
+    const int ub = 1 << ub_log, nb = (4 * SX + ub - 1) >> ub_log, nw = words;
     for (long long row = first; row < a.M; row += stride) {
         const Slice<T> s = slice(row);
         const bool more = row + stride < a.M;
         const Slice<T> nx = slice(more ? row + stride : row);
         if (row == first) {
             copy(s, 0);
-            cp_commit();
             copy(s, 1);
-            cp_commit();
         }
-        if (lane < 2) s_cnt[lane] = 0;  // candidates, blocks
-        const int ub = 1 << ub_log, nb = ((s.n + 31) / 32 + ub - 1) >> ub_log, nw = (nb + PER - 1) / PER;
+        if (lane == 0) *s_cnt = 0;
+        if (PER == 2 && nb % 2) blocks.put(nb, lane, E::put(-INFINITY));
         Sums<T, true, false> q(ct, ct, lift);
         typename E::Max bm = E::to_max(-INFINITY);
-        int nput = 0;
-        auto put = [&](typename E::Max m) {
-            const T v = E::top(m);
-            blocks.put(nput++, lane, v);
-        };
-        for (int st = 0; st < S; st++) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            uint4 u[TS_U];
-            const int i = st * (32 * TS_U) + lane;
-            const uint4* r = ring + (st & 1) * (TS_U * 32);
-#pragma unroll
-            for (int j = 0; j < TS_U; j++) {
-                if (i + j * 32 >= s.i0 && i + j * 32 < s.i1) u[j] = r[j * 32];
-                else if (i + j * 32 < s.n) u[j] = InMemory().get(s, i + j * 32, V);
-                else u[j] = make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
-            }
-            typename E::Max g[TS_U];
-#pragma unroll
-            for (int j = 0; j < TS_U; j++) g[j] = E::gmax(u[j]);
-            if (st == 0) q.start(want ? warp_max(E::value(g[0])) : -INFINITY);
-            const typename E::Max g01 = E::max2(g[0], g[1]), g23 = E::max2(g[2], g[3]), g4 = E::max2(g01, g23);
-            q.look(g4);
-            if (st + 2 < S) copy(s, st + 2);
-            else if (more) copy(nx, st + 2 - S);
-            cp_commit();
-            if (want) {
-#pragma unroll
-                for (int j = 0; j < TS_U; j++) q.take(u[j]);
-            }
+        // two stages at a time: the usual form, where both and the two after
+        // them are wholly inside the row, and the form that looks at every granule
+        auto block = [&](int st, typename E::Max g4, const typename E::Max* g) {
+            if (st >= SX) return;
             if (ub == 1) {
 #pragma unroll
-                for (int j = 0; j < TS_U; j++)
-                    if (nput < nw * PER) put(g[j]);
-            } else if (ub == 2) {
-                if (nput < nw * PER) put(g01);
-                if (nput < nw * PER) put(g23);
+                for (int j = 0; j < TS_U; j++) blocks.put(st * 4 + j, lane, E::top(g[j]));
             } else {
                 bm = E::max2(bm, g4);
-                if (((st + 1) * TS_U & (ub - 1)) == 0 || st == S - 1) {
-                    if (nput < nw * PER) put(bm);
+                if (((st + 1) * 4 & (ub - 1)) == 0 || st == SX - 1) {
+                    blocks.put((st * 4) >> ub_log, lane, E::top(bm));
                     bm = E::to_max(-INFINITY);
                 }
             }
+        };
+        const int whole0 = s.i0 == 0 ? 0 : 2, whole1 = s.i1 / 128 - 4;  // st in [whole0, whole1]: the usual form
+        for (int st = 0; st < S; st += 2) {
+            if (st >= whole0 && st <= whole1) {
+                typename E::Max g4[2];
+                const char* src = s.base + (long long)((st + 2) * 128 + lane) * 16;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    __syncwarp();
+                    uint4 u[TS_U];
+                    typename E::Max g[TS_U];
+#pragma unroll
+                    for (int j = 0; j < TS_U; j++) u[j] = own[j][h * 128];
+#pragma unroll
+                    for (int j = 0; j < TS_U; j++) g[j] = E::gmax(u[j]);
+                    if (h == 0 && st == 0) q.start(want ? warp_max(E::value(g[0])) : -INFINITY);
+                    g4[h] = E::max2(E::max2(g[0], g[1]), E::max2(g[2], g[3]));
+                    if (want) q.look(g4[h]);
+                    __syncwarp();  // the stage has been read
+                    if (h == 0) {
+                        cp16<0>(ring_at, src);
+                        cp16<512>(ring_at, src);
+                        cp16<1024>(ring_at, src);
+                        cp16<1536>(ring_at, src);
+                    } else {
+                        cp16<2048>(ring_at, src);
+                        cp16<2560>(ring_at, src);
+                        cp16<3072>(ring_at, src);
+                        cp16<3584>(ring_at, src);
+                    }
+                    cp_commit();
+                    if (want) {
+#pragma unroll
+                        for (int j = 0; j < TS_U; j++) q.take(u[j]);
+                    }
+                    if (ub != 4) block(st + h, g4[h], g);
+                }
+                if (ub == 4) blocks.put2(st, lane, g4[0], g4[1]);
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < 2; h++) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    __syncwarp();
+                    uint4 u[TS_U];
+                    typename E::Max g[TS_U];
+#pragma unroll
+                    for (int j = 0; j < TS_U; j++) {
+                        const int i = (st + h) * 128 + 4 * lane + j;
+                        if (i >= s.i0 && i < s.i1) u[j] = own[j][h * 128];
+                        else if (i < s.n) u[j] = InMemory().get(s, i, V);
+                        else u[j] = make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
+                    }
+#pragma unroll
+                    for (int j = 0; j < TS_U; j++) g[j] = E::gmax(u[j]);
+                    if (h == 0 && st == 0) q.start(want ? warp_max(E::value(g[0])) : -INFINITY);
+                    const typename E::Max g4 = E::max2(E::max2(g[0], g[1]), E::max2(g[2], g[3]));
+                    if (want) q.look(g4);
+                    __syncwarp();
+                    if (st + 2 < S) copy(s, st + 2 + h);
+                    else if (more) copy(nx, h);
+                    else cp_commit();
+                    if (want) {
+#pragma unroll
+                        for (int j = 0; j < TS_U; j++) q.take(u[j]);
+                    }
+                    block(st + h, g4, g);
+                }
+            }
         }
-        while (nput < nw * PER) put(E::to_max(-INFINITY));
         float tmax, sum, none;
         if (q.finish(tmax, sum, none) && want)
             each_element<T, 32>(s, InMemory(), V, lane, [&](float v, int) { q.take_far(v, sum, none); });
@@ -603,13 +677,14 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log) {
         if (want) merge(R, sum, ct);
 
         // the threshold: the k-th largest of the blocks' maxima
-        uint32_t hi = 0, low = 0xFFFFFFFFu >> (32 - Ordered<T>::N);
-        for (int i = 0; i < nb; i++) {
-            T v = reinterpret_cast<const T*>(blocks.w + (i / PER) * 32 + lane)[i % PER];
-            const uint32_t o = Ordered<T>::of(v);
-            hi = max(hi, o);
-            low = min(low, o);
+        typename E::Max mx = E::to_max(-INFINITY), mn = E::to_max(INFINITY);
+#pragma unroll 4
+        for (int i = 0; i < nw; i++) {
+            const typename E::Max v = blocks.word(i, lane);
+            mx = E::max2(mx, v);
+            mn = E::min2(mn, v);
         }
+        uint32_t hi = Ordered<T>::of(E::top(mx)), low = Ordered<T>::of(E::bottom(mn));
         hi = __reduce_max_sync(0xffffffffu, hi);
         low = __reduce_min_sync(0xffffffffu, low);
         int bit = 31 - __clz(hi ^ low);
@@ -618,59 +693,67 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log) {
             const uint32_t cand = t | (1u << bit);
             const int c = __reduce_add_sync(0xffffffffu, blocks.count(nw, lane, Ordered<T>::value(cand)));
             if (c >= k) t = cand;
-            if (c == k) break;
+            if (c >= k && c <= k + 16) break;  // a few blocks more cost less than another bit
         }
         const T tv = Ordered<T>::value(t);
         const float thr = E::get(&tv);
-        const int kk = k;
         bool exact = !(thr > -INFINITY);  // or no number
         __syncwarp();
         if (!exact) {
-            for (int i = 0; i < nb; i++) {
-                const T v = reinterpret_cast<const T*>(blocks.w + (i / PER) * 32 + lane)[i % PER];
-                if (E::get(&v) >= thr) {
-                    const int p = atomicAdd(s_cnt + 1, 1);
-                    if (p < TS_CAND) s_hit[p] = (uint16_t)(i * 32 + lane);
-                }
+            unsigned long long mine = 0;  // the lane's blocks at or above it
+#pragma unroll 4
+            for (int i = 0; i < nw; i++) {
+                const typename E::Max v = blocks.word(i, lane);
+#pragma unroll
+                for (int j = 0; j < PER; j++)
+                    if (E::get(reinterpret_cast<const T*>(&v) + j) >= thr) mine |= 1ull << (i * PER + j);
             }
-            __syncwarp();
-            const int nh = s_cnt[1];
+            const int n_mine = __popcll(mine);
+            int at = n_mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += x;
+            }
+            const int nh = __shfl_sync(0xffffffffu, at, 31);
+            at -= n_mine;
             exact = nh > TS_CAND;
             if (!exact) {
+                while (mine) {
+                    s_hit[at++] = (uint16_t)((__ffsll(mine) - 1) * 32 + lane);
+                    mine &= mine - 1;
+                }
+                __syncwarp();
                 const int items = nh << ub_log;
-                const uint32_t thr_o = order_of(thr);
-                const typename E::Max thr2 = E::to_max(thr);
-                for (int i0 = 0; i0 < items; i0 += 128) {
-                    uint4 u[4];
-                    int slot[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int it = i0 + j * 32 + lane;
-                        slot[j] = s.n;
-                        if (it < items) {
-                            const int h = s_hit[it >> ub_log];
-                            slot[j] = (h & 31) + 32 * (((h >> 5) << ub_log) + (it & (ub - 1)));
-                        }
-                        u[j] = slot[j] < s.n ? InMemory().get(s, slot[j], V) : make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
-                    }
 #pragma unroll 1
-                    for (int j = 0; j < 4; j++) {
-                        const uint4 x = j == 0 ? u[0] : j == 1 ? u[1] : j == 2 ? u[2] : u[3];
-                        const int sl = j == 0 ? slot[0] : j == 1 ? slot[1] : j == 2 ? slot[2] : slot[3];
-                        if (!E::at_least(E::gmax(x), thr2)) continue;
-                        f2 e[E::EPG / 2];
-                        E::unpack(x, e);
-                        const int c0 = s.col(sl);
+                for (int i0 = 0; i0 < items; i0 += 32 * TS_U) {
+                    uint4 u[TS_U];
+                    int col[TS_U];
 #pragma unroll
-                        for (int l = 0; l < E::EPG; l++) {
-                            float v0, v1;
-                            unpk(e[l / 2], v0, v1);
-                            const float v = l & 1 ? v1 : v0;
-                            const int c = c0 + l;
-                            if (order_of(v) >= thr_o && c >= 0 && c < V) {
-                                const int p = atomicAdd(s_cnt, 1);
-                                if (p < TS_CAND) s_cand[p] = top_key(v, c);
-                            }
+                    for (int j = 0; j < TS_U; j++) {
+                        const int it = min(i0 + j * 32 + lane, items - 1);
+                        const int h = s_hit[it >> ub_log], t = ub == 1 ? h >> 5 : ((h >> 5) << ub_log) + (it & (ub - 1));
+                        const int slot = (t >> 2) * 128 + 4 * (h & 31) + (t & 3);
+                        const bool on = slot < s.n && i0 + j * 32 + lane < items;
+                        u[j] = on ? InMemory().get(s, slot, V) : make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
+                        col[j] = s.col(slot);
+                    }
+#pragma unroll
+                    for (int j = 0; j < TS_U; j++) {
+                        f2 e[E::EPG / 2];
+                        E::unpack(u[j], e);
+                        uint32_t mask = 0;  // what lies outside the row is -inf: not at or above the threshold
+#pragma unroll
+                        for (int l = 0; l < E::EPG / 2; l++) {
+                            float x, y;
+                            unpk(e[l], x, y);
+                            mask |= (x >= thr ? 1u << (2 * l) : 0u) | (y >= thr ? 2u << (2 * l) : 0u);
+                        }
+                        while (mask) {
+                            const int l = __ffs(mask) - 1;
+                            mask &= mask - 1;
+                            const int p = atomicAdd(s_cnt, 1);
+                            if (p < TS_CAND) s_cand[p] = top_key(pick(e, l), col[j] + l);
                         }
                     }
                 }
@@ -679,9 +762,9 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log) {
                 __syncwarp();
             }
         }
-        if (exact) exact_candidates<T, 32>(s, InMemory(), V, kk, V, s_cand, s_cnt, (int*)nullptr, lane);
+        if (exact) exact_candidates<T, 32>(s, InMemory(), V, k, V, s_cand, s_cnt, (int*)nullptr, lane);
         __syncwarp();
-        ranks<32>(s_cand, s_cnt[0], kk, lane, [&](int r, unsigned long long key) {
+        ranks<32>(s_cand, s_cnt[0], k, lane, [&](int r, unsigned long long key) {
             a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
             a.idx[row * k + r] = key_col(key);
         });
@@ -1285,16 +1368,19 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     const int k = a.k, G = row_granules<T>(z, a.ld, a.V);
     // many rows: a warp each
     if (G > 128 && a.M >= L.num_sms * 12 && !a.skip) {
-        int ub_log = 0;
-        while (((G + 31) / 32 + (1 << ub_log) - 1) >> ub_log > TS_BLOCKS) ub_log++;
+        const int granules = (G + 127) / 128 * 4;  // of a lane, whole stages
+        int ub_log = granules <= TS_BLOCKS ? 0 : 2;
+        while ((granules + (1 << ub_log) - 1) >> ub_log > TS_BLOCKS) ub_log++;
+        const int nb = (granules + (1 << ub_log) - 1) >> ub_log;
+        const int words = (nb + Blocks<T>::PER - 1) / Blocks<T>::PER;
         static PerDevice attr;
         if (!allow_smem(attr, k_top_stream<T>)) return false;
         a.Gs = G;
-        p.smem = TS_WARPS * stream_warp_smem<T>();
+        p.smem = TS_WARPS * stream_warp_smem(words, k);
         p.threads = TS_WARPS * 32;
-        const int per_sm = std::min(6, (int)(SMEM_SM / (p.smem + 1024)));
+        const int per_sm = std::min(3, (int)(SMEM_SM / (p.smem + 1024)));
         p.ctas = std::min((a.M + TS_WARPS - 1) / TS_WARPS, L.num_sms * per_sm);
-        launch_rows(L, k_top_stream<T>, p, (const T*)z, a, ub_log);
+        launch_rows(L, k_top_stream<T>, p, (const T*)z, a, ub_log, words);
         return true;
     }
     if (!make_plan(p, L.num_sms, a.M, G, 512, [k](int nt, int Gs, int nbuf, bool cl) {

@@ -90,7 +90,9 @@ template <> struct Elem<float> {
     }
     static __device__ __forceinline__ Max max2(Max a, Max b) { return fmaxf(a, b); }
     static __device__ __forceinline__ Max to_max(float v) { return v; }
+    static __device__ __forceinline__ Max min2(Max a, Max b) { return fminf(a, b); }
     static __device__ __forceinline__ float top(Max m) { return m; }
+    static __device__ __forceinline__ float bottom(Max m) { return m; }
     static __device__ __forceinline__ float value(Max m) { return fmaxf(m, -INFINITY); }
     static __device__ __forceinline__ bool above(Max m, Max t) { return m > t; }       // any of m > t
     static __device__ __forceinline__ bool at_least(Max m, Max t) { return m >= t; }  // any of m >= t
@@ -115,7 +117,14 @@ template <typename T, typename P, typename Cvt> struct Elem16 {
     }
     static __device__ __forceinline__ Max max2(Max a, Max b) { return __hmax2(a, b); }
     static __device__ __forceinline__ Max to_max(float v) { return Cvt::pair(v, v); }
+    static __device__ __forceinline__ Max min2(Max a, Max b) { return __hmin2(a, b); }
     static __device__ __forceinline__ T top(Max m) { return __hmax(m.x, m.y); }
+    static __device__ __forceinline__ T bottom(Max m) { return __hmin(m.x, m.y); }
+    // (top(a), top(b))
+    static __device__ __forceinline__ P fold(P a, P b) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(&a), y = *reinterpret_cast<const uint32_t*>(&b);
+        return __hmax2(pair(__byte_perm(x, y, 0x5410)), pair(__byte_perm(x, y, 0x7632)));
+    }
     static __device__ __forceinline__ float value(Max m) {
         return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
     }
