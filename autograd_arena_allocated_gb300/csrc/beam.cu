@@ -6,14 +6,17 @@
 //   k_beam_reorder  state rows of K slots moved in place along parents[K]
 //   k_kv_fill_beams keys and values of a prompt into the K cache rows of its beams
 //   k_beam_walk     the K token sequences, from the last step's back to the first
-#include "tt_internal.h"
+#include "head_row.cuh"
 
 #include <algorithm>
 
 namespace tt {
 namespace {
 
-// One CTA per sequence.  Candidate (j, v) of beam j has the score
+using namespace head;
+
+// One CTA per sequence: it joins the parts' lists of each beam, then ranks the
+// beams' candidates.  Candidate (j, v) of beam j has the score
 //   s_j + (z_v - lse_j)          for a live beam
 //   s_j for v = eos, else -inf   for a finished one (done_j != 0)
 // in 64 bits: the cumulative scores of long hypotheses are hundreds, where a
@@ -26,36 +29,66 @@ namespace {
 // log-sum-exp depends in its last bits on how the row lies in memory.  Such a
 // beam takes the log-sum-exp of the first one it equals.
 constexpr int BM_THREADS = 256;
-constexpr int BM_MAX = 2048;  // K * n
+
+// Scores are compared as whole numbers: the 64-bit float unit is so narrow that
+// 128 candidates' comparisons took longer than all the rest.
+__device__ __forceinline__ unsigned long long order_of(double v) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+    return u >> 63 ? ~u : u | (1ull << 63);
+}
+__device__ __forceinline__ double value_of(unsigned long long u) {
+    return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
+
+constexpr int BM_ENTRIES = 4096;  // of a sequence's lists: K * parts * n
 
 __global__ void __launch_bounds__(BM_THREADS)
-k_beam_merge(const float* __restrict__ vals, const int32_t* __restrict__ idx, const double* __restrict__ lse,
-             const float* scores, const int32_t* done, int K, int V, int kk, int n, int eos, int32_t* parent,
-             int32_t* token, float* out_scores, int32_t* out_done, int32_t* __restrict__ tok_hist,
-             int32_t* __restrict__ par_hist, int ld_hist, const int* __restrict__ pos_dev, int* flags) {
+k_beam_merge(const unsigned long long* __restrict__ keys, const float2* __restrict__ parts, const float* scores,
+             const int32_t* done, int K, int P, int V, int kk, int n, int eos, int32_t* parent, int32_t* token,
+             float* out_scores, int32_t* out_done, int32_t* __restrict__ tok_hist, int32_t* __restrict__ par_hist,
+             int ld_hist, const int* __restrict__ pos_dev, int* flags) {
     pdl_enter();
-    __shared__ double s_s[BM_MAX];
-    __shared__ int s_f[BM_MAX];  // j V + v
+    extern __shared__ __align__(16) char smem[];
+    const int N = K * kk, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto* s_in = reinterpret_cast<unsigned long long*>(smem);  // [K][P][kk]
+    auto* s_j = s_in + (P > 1 ? N * P : 0);                    // [K][kk]
+    auto* s_s = s_j + N;                                       // [K][kk] scores, as whole numbers in order
+    int* s_f = reinterpret_cast<int*>(s_s + N);                // [K][kk] j V + v
+    __shared__ unsigned long long s_key[BM_THREADS / 32][JOIN_ROOM];
     __shared__ double s_lse[TT_BEAM_MAX];
     __shared__ float s_sc[TT_BEAM_MAX];
     __shared__ int s_as[TT_BEAM_MAX];  // the beam whose log-sum-exp counts; -1: a finished one
-    const int b = blockIdx.x, N = K * kk, tid = threadIdx.x;
+    const int b = blockIdx.x;
     const long long row0 = (long long)b * K;
-    if (tid < K) {
-        const bool over = done && done[row0 + tid] != 0;
-        const double l = over ? 0.0 : lse[row0 + tid];
-        s_sc[tid] = scores[row0 + tid];
-        s_lse[tid] = l;
-        s_as[tid] = over ? -1 : tid;
-        if (l != l || l == INFINITY) atomicOr(&flags[FLAG_NONFINITE], 1);
+    for (int i = tid; i < N * P; i += BM_THREADS) s_in[i] = keys[row0 * P * kk + i];
+    for (int j = warp; j < K; j += BM_THREADS / 32) {
+        const bool over = done && done[row0 + j] != 0;
+        double l = 0.0;
+        if (!over) {
+            float R, s;
+            join_parts(parts + (row0 + j) * P, P, LOG2E, R, s);
+            l = lse_of(R, s, 1.0f);
+        }
+        if (lane == 0) {
+            s_sc[j] = scores[row0 + j];
+            s_lse[j] = l;
+            s_as[j] = over ? -1 : j;
+            if (l != l || l == INFINITY) atomicOr(&flags[FLAG_NONFINITE], 1);
+        }
     }
     __syncthreads();
+    if (P > 1) {
+        for (int j = warp; j < K; j += BM_THREADS / 32)
+            if (s_as[j] >= 0)  // a finished beam's lists were not made
+                join_lists(s_in + j * P * kk, P * kk, kk, s_key[warp],
+                           [&](int r, unsigned long long key) { s_j[j * kk + r] = key; });
+        __syncthreads();
+    }
     if (tid > 0 && tid < K && s_as[tid] >= 0) {
         for (int j = 0; j < tid; j++) {
             if (s_sc[j] != s_sc[tid] || s_as[j] < 0 || !(fabs(s_lse[j] - s_lse[tid]) <= 1e-6 * (1.0 + fabs(s_lse[j])))) continue;
-            const long long p = (row0 + j) * kk, q = (row0 + tid) * kk;
             int same = 0;
-            while (same < kk && vals[p + same] == vals[q + same] && idx[p + same] == idx[q + same]) same++;
+            while (same < kk && s_j[j * kk + same] == s_j[tid * kk + same]) same++;
             if (same == kk) {
                 s_as[tid] = j;  // the first such: it stands for itself
                 break;
@@ -76,11 +109,11 @@ k_beam_merge(const float* __restrict__ vals, const int32_t* __restrict__ idx, co
         } else {
             const double l = s_lse[s_as[j]];
             if (isfinite(l) && s > -INFINITY) {
-                v = idx[(row0 + j) * kk + r];
-                c = (double)s + ((double)vals[(row0 + j) * kk + r] - l);
+                v = key_col(s_j[i]);
+                c = (double)s + ((double)head::value_of((uint32_t)(s_j[i] >> 32)) - l);
             }
         }
-        s_s[i] = c != c ? -INFINITY : c;
+        s_s[i] = order_of(c != c ? -INFINITY : c);
         s_f[i] = j * V + v;
     }
     // everything of the inputs is read before an output is written: they may be the same arrays
@@ -88,17 +121,22 @@ k_beam_merge(const float* __restrict__ vals, const int32_t* __restrict__ idx, co
     if (done)
         for (int j = 0; j < K; j++) over_mask |= (s_as[j] < 0 ? 1u : 0u) << j;
     __syncthreads();
-    for (int i = threadIdx.x; i < N; i += BM_THREADS) {
-        const double c = s_s[i];
-        const int f = s_f[i];
+    // a candidate's rank, by four lanes
+    for (int i0 = 0; i0 < N; i0 += BM_THREADS / 4) {
+        const int i = i0 + tid / 4;
+        const unsigned long long c = i < N ? s_s[i] : 0ull;
+        const int f = i < N ? s_f[i] : 0;
         int rank = 0;
-        for (int o = 0; o < N; o++) rank += s_s[o] > c || (s_s[o] == c && s_f[o] < f);
-        if (rank >= n) continue;
+        if (i < N)
+            for (int o = tid & 3; o < N; o += 4) rank += s_s[o] > c || (s_s[o] == c && s_f[o] < f);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if ((tid & 3) || i >= N || rank >= n) continue;
         const int j = f / V, v = f % V;
         const long long at = (long long)b * n + rank;
         parent[at] = j;
         token[at] = v;
-        out_scores[at] = (float)c;
+        out_scores[at] = (float)value_of(c);
         if (out_done) out_done[at] = ((over_mask >> j) & 1u) || v == eos;
         if (tok_hist) {
             tok_hist[at * ld_hist + *pos_dev] = v;
@@ -199,9 +237,9 @@ bool reorder(const Launch& L, void* state, const int32_t* parents, int N, int B,
 
 }  // namespace
 
-size_t beam_select_scratch_bytes(int R, int V, int n) {
-    const size_t kk = (size_t)std::min(n, V);
-    return (size_t)R * 8 + (size_t)R * kk * 8;
+size_t beam_select_scratch_bytes(tt_dtype dtype, int B, int K, int V, int n) {
+    const int kk = std::min(n, V);
+    return (size_t)B * K * top_parts(dtype, B * K, V, kk, BM_ENTRIES / K) * 8 * ((size_t)kk + 1);
 }
 
 bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long long ld, const float* scores,
@@ -209,14 +247,19 @@ bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long lon
                         int B, int K, int V, int n, int eos, void* scratch, int32_t* tok_hist, int32_t* par_hist,
                         int ld_hist, const int* pos_dev) {
     if (L.dry) return true;
-    const int R = B * K, kk = std::min(n, V);
-    if (K * kk > BM_MAX) return false;
-    double* lse = (double*)scratch;
-    float* vals = (float*)(lse + R);
-    int32_t* idx = (int32_t*)(vals + (size_t)R * kk);
-    if (!launch_top_rows(L, dtype, z, ld, R, V, kk, 1.0f, vals, idx, nullptr, lse, done)) return false;
+    const int R = B * K, kk = std::min(n, V), P = top_parts(dtype, R, V, kk, BM_ENTRIES / K), N = K * kk;
+    const size_t smem = (size_t)(P > 1 ? N * P : 0) * 8 + (size_t)N * (8 + 8 + 4);
+    static PerDevice attr;
+    if (!attr.once([] {
+            return cudaFuncSetAttribute(k_beam_merge, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        BM_ENTRIES * 8 + 2 * TT_BEAM_MAX * TT_BEAM_MAX * 20) == cudaSuccess;
+        }))
+        return false;
+    auto* keys = (unsigned long long*)scratch;
+    float2* parts = (float2*)(keys + (size_t)R * P * kk);
+    if (!launch_top_parts(L, dtype, z, ld, R, V, kk, P, keys, parts, done)) return false;
     L.count();
-    launch_k(L, k_beam_merge, dim3(B), dim3(BM_THREADS), 0, vals, idx, lse, scores, done, K, V, kk, n, eos, parent,
+    launch_k(L, k_beam_merge, dim3(B), dim3(BM_THREADS), smem, keys, parts, scores, done, K, P, V, kk, n, eos, parent,
              token, out_scores, out_done, tok_hist, par_hist, ld_hist, pos_dev, L.flags);
     return true;
 }

@@ -1,14 +1,15 @@
 // head.cu -- operators on the LM head's logits that deal in lists of columns:
 //
-//   k_top_rows      per row the k largest logits (ties: the lowest column) and
-//                   the log-sum-exp
+//   k_top_stream    per row (or part of one) the k largest logits (ties: the
+//                   lowest column) and the log-sum-exp
+//   k_top_join      the parts' lists of a row as one
 //   k_distill       distillation from a teacher's top logits: loss and
 //                   gradient of a row
+//   k_distill_short the same for rows of up to 512 logits
 //   k_row_mean      the mean of the row losses (fixed order)
 //
-// Both row kernels read a row of V logits from memory once, in the storage
-// type, and hold it on chip (head_row.cuh); sums, statistics and losses are
-// fp32.
+// The kernels read a row of V logits from memory once, in the storage type
+// (head_row.cuh); sums, statistics and losses are fp32.
 #include "head_row.cuh"
 
 #include <algorithm>
@@ -19,101 +20,44 @@ namespace {
 using namespace head;
 
 constexpr int LIST_MAX = TT_TOP_MAX;
-constexpr int LIST_PER_LANE = LIST_MAX / 32;
 constexpr int CS_MAX = 8;      // CTAs of a cluster (the portable limit)
-constexpr int CAND_MAX = 512;  // candidates of a row's (or slice's) list, and granules that hold them
-constexpr int THR_MAX = 256;   // thread maxima that a threshold is chosen from
 
-constexpr int LIST_CTA = 64;  // threads of a CTA that look after the list
+constexpr int NT = 256;        // threads of a CTA that pass over a row
+constexpr int LIST_CTA = 64;   // and those that look after its list
 
-__host__ __device__ constexpr int cta_threads(int NT) { return NT == 32 ? 256 : NT; }
-__host__ __device__ constexpr int cta_per_sm(int NT) { return NT == 32 ? 3 : 2; }
-__host__ __device__ constexpr int cta_groups(int NT) { return NT == 32 ? 8 : 1; }
 __host__ __device__ constexpr int align16(int n) { return (n + 15) & ~15; }
 
 // ------------------------------------------------------------ top logits
-// Order-preserving whole number of a value: -0 counts as +0 and a NaN as -inf.
-__device__ __forceinline__ uint32_t order_of(float v) {
-    const uint32_t u = __float_as_uint(fmaxf(v, -INFINITY) + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint32_t u) {
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
-}
-// (value, column): larger values first, then lower columns.  Never 0.
-__device__ __forceinline__ unsigned long long top_key(float v, int col) {
-    return ((unsigned long long)order_of(v) << 32) | (unsigned long long)(0xFFFFFFFFu - (uint32_t)col);
-}
-__device__ __forceinline__ int key_col(unsigned long long key) {
-    return (int)(0xFFFFFFFFu - (uint32_t)(key & 0xFFFFFFFFull));
-}
 // bits of order_of that tell two values of a storage type apart
 template <typename T> struct OrderBits { static constexpr int N = 32; };
 template <> struct OrderBits<__nv_bfloat16> { static constexpr int N = 16; };
 template <> struct OrderBits<__half> { static constexpr int N = 19; };  // sign, 8 exponent bits of fp32, 10 of mantissa
 
 struct TopArgs {
-    float* vals;
+    float* vals;  // the lists, where a row is one part
     int32_t* idx;
     float* lse;
-    double* lse64;
+    unsigned long long* keys;  // [M][P][k] the parts' lists (NULL: one part), 0 where a part has fewer
+    float2* parts;             // [M][P] the parts' references and sums of exponentials
     const int32_t* skip;
     long long ld;
-    int M, V, k, Gs, cs, nbuf;
+    int M, V, k, Gs, P;
+    bool want;  // the sums
     float inv_tau;
 };
 
-// shared memory of a group, in bytes from its start
-struct TopLayout {
-    int cand, thr, gl, part, red, lists, x, cnt, total;
-    __host__ __device__ TopLayout(int nt, int Gs, int nbuf, int k, bool cl) {
-        int at = nbuf * Gs * 16;
-        cand = at; at += (nt > 32 ? CAND_MAX : LIST_MAX) * 8;  // a warp's candidates are exact ones
-        thr = at; at += nt > 32 ? 4 * THR_MAX + 16 : 0;
-        gl = at; at += nt > 32 ? 4 * CAND_MAX : 0;
-        part = at; at += nt > 32 ? 256 : 0;
-        red = at; at += nt > 32 ? 256 : 0;
-        lists = at; at += cl ? align16(2 * CS_MAX * k * 8) : 0;
-        x = at; at += cl ? 2 * CS_MAX * 8 : 0;
-        cnt = at; at += 16;
-        total = at;
-    }
-};
-
-// sum of c over the group; `turn` alternates between two rows of s_red, so
-// that one barrier a call is enough
-template <int NT> __device__ __forceinline__ int group_count(int c, int* s_red, int& turn) {
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (NT == 32) return c;
-    const int lane = threadIdx.x & 31;
-    int* r = s_red + (turn & 1) * 32;
-    turn++;
-    if (lane == 0) r[threadIdx.x >> 5] = c;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? r[lane] : 0);
+// Slot i of the slice, read from memory.
+template <typename T> __device__ __forceinline__ uint4 granule(const Slice<T>& s, int i, int V) {
+    return s.inner(i) ? reinterpret_cast<const uint4*>(s.base)[i]
+                      : edge_granule(reinterpret_cast<const T*>(s.base) - s.col(0), s.col(i), V);
 }
 
-// where a thread's granules are read from: the on-chip copy, or memory
-struct OnChip {
-    const char* buf;
-    template <typename T> __device__ __forceinline__ uint4 get(const Slice<T>&, int i, int) const {
-        return reinterpret_cast<const uint4*>(buf)[i];
-    }
-};
-struct InMemory {
-    template <typename T> __device__ __forceinline__ uint4 get(const Slice<T>& s, int i, int V) const {
-        return s.inner(i) ? reinterpret_cast<const uint4*>(s.base)[i]
-                          : edge_granule(reinterpret_cast<const T*>(s.base) - s.col(0), s.col(i), V);
-    }
-};
-
-// f(value, column) for every element of the thread's granules
-template <typename T, int NT, typename S, typename F>
-__device__ __forceinline__ void each_element(const Slice<T>& s, const S& src, int V, int tid, F&& f) {
-    for (int g = tid; g < s.n; g += NT) {
-        const uint4 u = src.get(s, g, V);
+// f(value, column) for every element of the lane's granules, read from memory
+template <typename T, typename F>
+__device__ __forceinline__ void each_element(const Slice<T>& s, int V, int lane, F&& f) {
+    for (int g = lane; g < s.n; g += 32) {
         f2 e[Elem<T>::EPG / 2];
-        Elem<T>::unpack(u, e);
+        Elem<T>::unpack(granule(s, g, V), e);
         const int c0 = s.col(g);
 #pragma unroll
         for (int i = 0; i < Elem<T>::EPG / 2; i++) {
@@ -128,18 +72,17 @@ __device__ __forceinline__ void each_element(const Slice<T>& s, const S& src, in
 // The kk first elements of the slice in list order, exactly, as candidates:
 // the kk-th largest value is found bit by bit by counting, then, where equal
 // values are more than are needed, the last column that is taken.  Used where
-// the threads' maxima say too little: rows of a warp, rows with most columns
-// masked, rows of few different values.
-template <typename T, int NT, typename S>
-__device__ __noinline__ void exact_candidates(const Slice<T>& s, const S& buf, int V, int kk, int n_el,
-                                 unsigned long long* s_cand, int* s_cnt, int* s_red, int tid) {
-    int turn = 0;
-    if (tid == 0) *s_cnt = 0;
-    group_sync<NT>();
-    if (n_el <= (NT == 32 ? LIST_MAX : CAND_MAX / 2)) {
-        // few enough to rank them all
-        each_element<T, NT>(s, buf, V, tid, [&](float v, int c) { s_cand[atomicAdd(s_cnt, 1)] = top_key(v, c); });
-        group_sync<NT>();
+// the blocks' maxima say too little: most columns masked, few different values.
+template <typename T>
+__device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, int n_el, unsigned long long* s_cand,
+                                              int* s_cnt, int lane) {
+    __syncwarp();
+    if (lane == 0) *s_cnt = 0;
+    __syncwarp();
+    auto sum = [](int c) { return __reduce_add_sync(0xffffffffu, c); };
+    if (n_el <= LIST_MAX) {  // few enough to rank them all
+        each_element(s, V, lane, [&](float v, int c) { s_cand[atomicAdd(s_cnt, 1)] = top_key(v, c); });
+        __syncwarp();
         return;
     }
     constexpr int LOW = 32 - OrderBits<T>::N;
@@ -147,292 +90,40 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, const S& buf, i
     for (int bit = 31; bit >= LOW; bit--) {
         const uint32_t cand = t | (1u << bit);
         int c = 0;
-        each_element<T, NT>(s, buf, V, tid, [&](float v, int) { c += order_of(v) >= cand; });
-        if (group_count<NT>(c, s_red, turn) >= kk) t = cand;
+        each_element(s, V, lane, [&](float v, int) { c += order_of(v) >= cand; });
+        if (sum(c) >= kk) t = cand;
     }
     const uint32_t above = t + (1u << LOW);  // no value's order is so large that this wraps
     int c = 0, e = 0;
-    each_element<T, NT>(s, buf, V, tid, [&](float v, int) {
+    each_element(s, V, lane, [&](float v, int) {
         const uint32_t o = order_of(v);
         c += o >= above;
         e += o >= t && o < above;
     });
-    const int need = kk - group_count<NT>(c, s_red, turn);
+    const int need = kk - sum(c);
     int last = V;  // equal values are taken up to this column
-    if (group_count<NT>(e, s_red, turn) > need) {
+    if (sum(e) > need) {
         last = 0;
         for (int bit = 20; bit >= 0; bit--) {  // V < 2^20
             const int x = last | (1 << bit);
             int n = 0;
-            each_element<T, NT>(s, buf, V, tid, [&](float v, int col) {
+            each_element(s, V, lane, [&](float v, int col) {
                 const uint32_t o = order_of(v);
                 n += o >= t && o < above && col < x;
             });
-            if (group_count<NT>(n, s_red, turn) < need) last = x;
+            if (sum(n) < need) last = x;
         }
     }
-    each_element<T, NT>(s, buf, V, tid, [&](float v, int col) {
+    each_element(s, V, lane, [&](float v, int col) {
         const uint32_t o = order_of(v);
         if (o >= above || (o >= t && col <= last)) s_cand[atomicAdd(s_cnt, 1)] = top_key(v, col);
     });
-    group_sync<NT>();
+    __syncwarp();
 }
 
-// out(rank, key) for the kk first of cnt candidates in list order; four lanes count for a candidate
-template <int NT, typename F>
-__device__ __forceinline__ void ranks(const unsigned long long* s_cand, int cnt, int kk, int tid, F&& out) {
-    for (int i0 = 0; i0 < cnt; i0 += NT / 4) {
-        const int i = i0 + tid / 4;
-        if (__all_sync(0xffffffffu, i >= cnt)) break;
-        const unsigned long long key = i < cnt ? s_cand[i] : ~0ull;
-        int r = 0;
-#pragma unroll 4
-        for (int j = tid & 3; j < cnt; j += 4) r += s_cand[j] > key;
-        r += __shfl_xor_sync(0xffffffffu, r, 1);
-        r += __shfl_xor_sync(0xffffffffu, r, 2);
-        if ((tid & 3) == 0 && i < cnt && r < kk) out(r, key);
-    }
-}
-
-// A row's list in four stages:
-//   1. one pass over the granules: each thread's largest value and its sum of
-//      exponentials;
-//   2. a threshold: each of the fw warps that have work in every lane gives its
-//      Q largest thread maxima, Q = ceil(k / fw) + 2, and the k-th largest of
-//      these fw Q values is the threshold.  At least k elements are at or
-//      above it;
-//   3. threads whose largest value is at or above it name their granules that
-//      are, and all threads look through those for the elements: the
-//      candidates, on unordered data a few more than k;
-//   4. each candidate's rank among them by counting.
-// With more than CAND_MAX candidates, or too few threads for a threshold, the
-// candidates are found exactly instead.  Clusters: each CTA lists its slice
-// and sends the list to CTA 0, which ranks every entry by binary searches in
-// the other lists.
-template <typename T, int NT, bool CL>
-__global__ void __launch_bounds__(cta_threads(NT), cta_per_sm(NT))
-k_top_rows(const T* __restrict__ z, const TopArgs a) {
-    pdl_enter();
-    extern __shared__ __align__(16) char smem[];
-    const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int lane = threadIdx.x & 31, warp = tid >> 5;
-    const TopLayout lay(NT, a.Gs, a.nbuf, a.k, CL);
-    char* sm = smem + (NT == 32 ? threadIdx.x >> 5 : 0) * lay.total;
-    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + lay.cand);
-    uint32_t* s_thr = reinterpret_cast<uint32_t*>(sm + lay.thr);
-    int* s_gl = reinterpret_cast<int*>(sm + lay.gl);
-    float2* s_part = reinterpret_cast<float2*>(sm + lay.part);
-    int* s_red = reinterpret_cast<int*>(sm + lay.red);
-    auto* s_lists = reinterpret_cast<unsigned long long*>(sm + lay.lists);  // [2][cs][k]
-    float2* s_x = reinterpret_cast<float2*>(sm + lay.x);                    // [2][cs]
-    int* s_cnt = reinterpret_cast<int*>(sm + lay.cnt);
-    const int rank = CL ? (int)cluster_rank() : 0, cs = CL ? a.cs : 1;
-    const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
-    const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
-    const bool want = a.lse || a.lse64;
-    const float ct = LOG2E * a.inv_tau, lift = 20.0f / fmaxf(1.0f, a.inv_tau);
-    const int k = a.k, V = a.V;
-    using E = Elem<T>;
-    auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, rank, a.Gs); };
-    auto here = [&](long long r) { return r < a.M && !(a.skip && a.skip[r]); };
-
-    for (int i = 0; i < a.nbuf; i++) {
-        const long long r = first + i * stride;
-        if (here(r)) fill<T, NT>(slice(r), sm + i * a.Gs * 16, tid);
-        cp_commit();
-    }
-    T edge = Elem<T>::put(0.0f);
-    if (here(first)) edge_store(slice(first), sm, edge_load(slice(first), V, tid), tid);
-    if (here(first + stride)) edge = edge_load(slice(first + stride), V, tid);
-    if (tid == 0) s_cnt[0] = s_cnt[1] = 0;  // candidates, granules
-    if (CL) cluster_sync();  // the others run: their shared memory may be written
-
-    int it = 0;
-    for (long long row = first; row < a.M; row += stride, it++) {
-        const int par = it & 1;
-        char* buf = sm + (a.nbuf == 2 ? par : 0) * a.Gs * 16;
-        const Slice<T> s = slice(row);
-        cp_wait(a.nbuf);
-        group_sync<NT>();
-        const bool run = here(row);
-        const long long next = row + a.nbuf * stride;
-        if (run) {
-            // stage 1
-            float tmax, R, sum, none;
-            if (want) {
-                sum_pass<T, NT, true, false>(s, buf, tid, ct, ct, lift, tmax, R, sum, none);
-                merge(R, sum, ct);
-            } else {
-                sum_pass<T, NT, false, false>(s, buf, tid, ct, ct, lift, tmax, R, sum, none);
-            }
-            // stage 2
-            const int n_slots = s.n;
-            const int n_el = max(0, min(V, s.col(s.n)) - max(0, s.col(0)));
-            const int kk = min(k, n_el);
-            const int fw = NT == 32 ? 0 : min(NT, n_slots) / 32;
-            const int Q = fw ? min(32, (k + fw - 1) / fw + 2) : 0;
-            bool exact = fw * Q < k || fw * Q > THR_MAX;
-            int cnt = 0;
-            if (NT > 32) {
-                if (!exact && warp < fw) {
-                    uint32_t cur = order_of(tmax), mine = 0;
-                    for (int i = 0; i < Q; i++) {
-                        const uint32_t m = __reduce_max_sync(0xffffffffu, cur);
-                        if (lane == i) mine = m;
-                        if (lane == __ffs(__ballot_sync(0xffffffffu, cur == m)) - 1) cur = 0;
-                    }
-                    if (lane < Q) s_thr[warp * Q + lane] = mine;
-                }
-                if (lane == 0) s_part[warp] = make_float2(R, sum);
-                __syncthreads();
-                if (!exact) {
-                    // the k-th largest of the fw Q values, by one warp bit by bit
-                    // from the first bit that differs
-                    if (warp == 0) {
-                        const int nv = fw * Q;
-                        uint32_t v[THR_MAX / 32], hi = 0, lo = ~0u;
-#pragma unroll
-                        for (int j = 0; j < THR_MAX / 32; j++) {
-                            v[j] = 0;
-                            if (j * 32 + lane < nv) {
-                                v[j] = s_thr[j * 32 + lane];
-                                lo = min(lo, v[j]);
-                                hi = max(hi, v[j]);
-                            }
-                        }
-                        hi = __reduce_max_sync(0xffffffffu, hi);
-                        lo = __reduce_min_sync(0xffffffffu, lo);
-                        int bit = 31 - __clz(hi ^ lo);  // -1: all are equal
-                        uint32_t t = bit < 0 ? hi : hi & ~((2u << bit) - 1u);
-                        for (; bit >= 32 - OrderBits<T>::N; bit--) {
-                            const uint32_t cand = t | (1u << bit);
-                            int c = 0;
-#pragma unroll
-                            for (int j = 0; j < THR_MAX / 32; j++)
-                                if (j * 32 < nv) c += v[j] >= cand;
-                            c = __reduce_add_sync(0xffffffffu, c);
-                            if (c >= k) t = cand;
-                            if (c == k) break;
-                        }
-                        if (lane == 0) s_thr[THR_MAX] = t;
-                    }
-                    __syncthreads();
-                    // stage 3
-                    const uint32_t thr = s_thr[THR_MAX];
-                    if (order_of(tmax) >= thr) {
-                        const typename E::Max thr2 = E::to_max(fmaxf(value_of(thr), -INFINITY));
-#pragma unroll 2
-                        for (int i = tid; i < n_slots; i += NT)
-                            if (E::at_least(E::gmax(reinterpret_cast<const uint4*>(buf)[i]), thr2)) {
-                                const int p = atomicAdd(s_cnt + 1, 1);
-                                if (p < CAND_MAX) s_gl[p] = i;
-                            }
-                    }
-                    __syncthreads();
-                    const int ng = s_cnt[1];
-                    exact = ng > CAND_MAX;
-                    if (!exact) {
-                        for (int i = tid; i < ng * E::EPG; i += NT) {
-                            const int slot = s_gl[i / E::EPG], e = i % E::EPG;
-                            const float w = E::get(reinterpret_cast<const T*>(buf + slot * 16) + e);
-                            const int c = s.col(slot) + e;
-                            if (order_of(w) >= thr && c >= 0 && c < V) {
-                                const int p = atomicAdd(s_cnt, 1);
-                                if (p < CAND_MAX) s_cand[p] = top_key(w, c);
-                            }
-                        }
-                        __syncthreads();
-                        cnt = s_cnt[0];
-                        exact = cnt > CAND_MAX;
-                        if (exact) __syncthreads();  // every thread has read the count
-                    }
-                }
-            }
-            if (exact) {
-                exact_candidates<T, NT>(s, OnChip{buf}, V, kk, n_el, s_cand, s_cnt, s_red, tid);
-                cnt = *s_cnt;
-            }
-            if (here(next)) fill<T, NT>(slice(next), buf, tid);
-            cp_commit();
-            // stage 4
-            ranks<NT>(s_cand, cnt, kk, tid, [&](int r, unsigned long long key) {
-                if (CL) {
-                    st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), key);
-                } else {
-                    a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
-                    a.idx[row * k + r] = key_col(key);
-                }
-            });
-            if (CL)
-                for (int r = kk + tid; r < k; r += NT) st_remote(remote(s_lists + (par * cs + rank) * k + r, 0), 0ull);
-            if (want && warp == 0) {
-                if (NT > 32) {
-                    const float2 p = lane < NT / 32 ? s_part[lane] : make_float2(-INFINITY, 0.0f);
-                    R = p.x;
-                    sum = p.y;
-                    merge(R, sum, ct);
-                }
-                if (CL && lane == 0) {
-                    const uint32_t at = remote(s_x + par * cs + rank, 0);
-                    st_remote(at, R);
-                    st_remote(at + 4, sum);
-                }
-            }
-            if (CL) {
-                cluster_sync();
-                if (rank == 0) {
-                    const unsigned long long* l = s_lists + par * cs * k;
-                    for (int i = tid; i < cs * k; i += NT) {
-                        const unsigned long long key = l[i];
-                        int r = i % k;
-                        if (key == 0) continue;
-                        for (int o = 0; o < cs; o++) {
-                            if (o == i / k) continue;
-                            int lo = 0, hi = k;  // entries of list o above key
-                            while (lo < hi) {
-                                const int mid = (lo + hi) >> 1;
-                                if (l[o * k + mid] > key) lo = mid + 1;
-                                else hi = mid;
-                            }
-                            r += lo;
-                        }
-                        if (r < k) {
-                            a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
-                            a.idx[row * k + r] = key_col(key);
-                        }
-                    }
-                    if (want && warp == 0) {
-                        const float2 p = lane < cs ? s_x[par * cs + lane] : make_float2(-INFINITY, 0.0f);
-                        R = p.x;
-                        sum = p.y;
-                        merge<CS_MAX>(R, sum, ct);
-                    }
-                }
-            }
-            if (want && tid == 0 && rank == 0) {
-                // a row of -inf and a row with +inf have that as their value, unless a NaN is there too
-                const bool flat = sum == sum && (R == -INFINITY || R == INFINITY);
-                if (a.lse) a.lse[row] = flat ? R : R * a.inv_tau + logf(sum);
-                if (a.lse64) a.lse64[row] = flat ? (double)R : (double)R * (double)a.inv_tau + log((double)sum);
-            }
-        } else {
-            if (here(next)) fill<T, NT>(slice(next), buf, tid);
-            cp_commit();
-            if (CL) cluster_sync();
-        }
-        group_sync<NT>();
-        if (tid == 0) s_cnt[0] = s_cnt[1] = 0;
-        const long long n1 = row + stride, n2 = n1 + stride;
-        if (tid < 16) {
-            if (here(n1)) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, tid);
-            if (here(n2)) edge = edge_load(slice(n2), V, tid);
-        }
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-// ------------------------------------------------------------ top logits of many rows
-// A warp a row, for calls with more rows than the SMs hold warps: the row
+// A warp takes a row, or a part of one where there are fewer rows than the SMs
+// hold warps (the parts' lists are then joined, by k_top_join or by the beams'
+// merge).  The row
 // streams through a ring of the warp's own, without a barrier, and what stays
 // of it is the largest value of every block of UB granules of a lane.  The
 // k-th largest of those is the threshold; the few blocks at or above it (k,
@@ -441,11 +132,15 @@ k_top_rows(const T* __restrict__ z, const TopArgs a) {
 // memory (64 bytes; in shared memory they are permuted so that eight lanes'
 // reads fall into different banks): reading 64 blocks again then is 4% of a
 // row of 50257 16-bit logits, where blocks of four granules 512 bytes apart
-// cost 26% more DRAM traffic.  A whole row on chip (k_top_rows) needs no
-// second read but waits at its barriers: 940 us for 32768 such rows.
+// cost 26% more DRAM traffic.  A CTA a row, the row held on chip, needs no
+// second read but waits at its barriers: 940 us for 32768 such rows, and 75 us
+// for a selection step of 256 fp32 rows.
 // A row with more candidates than there is room for (ties, masks) is gone
 // through bit by bit from memory.
-constexpr int TS_WARPS = 8;                 // of a CTA
+constexpr int TS_WARPS = 8;                 // most warps of a CTA
+constexpr int TS_TASKS = 3648;              // rows, or parts, that are worked on at once: 24 warps on each of 152 SMs
+constexpr int TS_PARTS = 64;                // most parts of a row
+constexpr int TS_JOIN = 2048;               // most entries of a row's parts' lists
 constexpr int TS_BLOCKS = 64;               // most blocks of a lane
 constexpr int TS_U = 4;                     // granules of a lane in a stage of the ring
 constexpr int TS_RING = 2 * TS_U * 32 * 16;  // two stages
@@ -531,7 +226,9 @@ template <int N> __device__ __forceinline__ float pick(const f2 (&e)[N], int l) 
 template <typename T>
 __global__ void __launch_bounds__(TS_WARPS * 32, 3)
 k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
-    pdl_enter();
+    // no early trigger: the next kernel's CTAs, resident and waiting, take the room of this grid's last ones
+    // (a selection step of 256 fp32 rows 93 us with it, 34 us without)
+    pdl_wait();
     extern __shared__ __align__(16) char smem[];
     using E = Elem<T>;
     constexpr int PER = Blocks<T>::PER;
@@ -542,11 +239,16 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
     auto* s_cand = reinterpret_cast<unsigned long long*>(sm + TS_RING + words * 128);
     auto* s_hit = reinterpret_cast<uint16_t*>(s_cand + TS_CAND);
     int* s_cnt = reinterpret_cast<int*>(s_hit + TS_CAND);
-    const long long first = blockIdx.x * (long long)TS_WARPS + (threadIdx.x >> 5), stride = gridDim.x * (long long)TS_WARPS;
-    const bool want = a.lse || a.lse64;
+    const int warps = blockDim.x >> 5, P = a.P;
+    const long long tasks = (long long)a.M * P, stride = (long long)gridDim.x * warps;
+    const bool want = a.want;
     const float ct = LOG2E * a.inv_tau, lift = 20.0f / fmaxf(1.0f, a.inv_tau);
     const int k = a.k, V = a.V;
-    auto slice = [&](long long r) { return Slice<T>(z, r, a.ld, V, 0, a.Gs); };
+    auto slice = [&](long long q) { return Slice<T>(z, q / P, a.ld, V, (int)(q % P), a.Gs); };
+    auto from = [&](long long q) {  // the first task of this warp at or after q
+        while (a.skip && q < tasks && a.skip[q / P]) q += stride;
+        return q;
+    };
     // Granule g of a stage (128 of them) is in slot (g & ~7) | (g ^ (g >> 3 & 3)) & 7:
     // a lane copies granules lane + 32 j and reads 4 lane + j.
     const uint32_t ring_at =
@@ -574,11 +276,13 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
     // stages are counted in pairs, so that a row always starts in the ring's first half
     const int SX = (a.Gs + 127) / 128, S = (SX + 1) & ~1;
     const int ub = 1 << ub_log, nb = (4 * SX + ub - 1) >> ub_log, nw = words;
-    for (long long row = first; row < a.M; row += stride) {
-        const Slice<T> s = slice(row);
-        const bool more = row + stride < a.M;
-        const Slice<T> nx = slice(more ? row + stride : row);
-        if (row == first) {
+    const long long first = from(blockIdx.x * (long long)warps + (threadIdx.x >> 5));
+    for (long long task = first, next; task < tasks; task = next) {
+        const Slice<T> s = slice(task);
+        next = from(task + stride);
+        const bool more = next < tasks;
+        const Slice<T> nx = slice(more ? next : task);
+        if (task == first) {
             copy(s, 0);
             copy(s, 1);
         }
@@ -650,7 +354,7 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                     for (int j = 0; j < TS_U; j++) {
                         const int i = (st + h) * 128 + 4 * lane + j;
                         if (i >= s.i0 && i < s.i1) u[j] = own[j][h * 128];
-                        else if (i < s.n) u[j] = InMemory().get(s, i, V);
+                        else if (i < s.n) u[j] = granule(s, i, V);
                         else u[j] = make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
                     }
 #pragma unroll
@@ -671,8 +375,13 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
             }
         }
         float tmax, sum, none;
-        if (q.finish(tmax, sum, none) && want)
-            each_element<T, 32>(s, InMemory(), V, lane, [&](float v, int) { q.take_far(v, sum, none); });
+        const bool far = q.finish(tmax, sum, none);
+        if (want && __any_sync(0xffffffffu, far)) {
+            // (the lanes take other elements than they did above, so all have one reference)
+            q.R = warp_max(tmax);
+            sum = 0.0f;
+            each_element(s, V, lane, [&](float v, int) { q.take_far(v, sum, none); });
+        }
         float R = q.R;
         if (want) merge(R, sum, ct);
 
@@ -735,7 +444,7 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                         const int h = s_hit[it >> ub_log], t = ub == 1 ? h >> 5 : ((h >> 5) << ub_log) + (it & (ub - 1));
                         const int slot = (t >> 2) * 128 + 4 * (h & 31) + (t & 3);
                         const bool on = slot < s.n && i0 + j * 32 + lane < items;
-                        u[j] = on ? InMemory().get(s, slot, V) : make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
+                        u[j] = on ? granule(s, slot, V) : make_uint4(E::NINF, E::NINF, E::NINF, E::NINF);
                         col[j] = s.col(slot);
                     }
 #pragma unroll
@@ -762,20 +471,44 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                 __syncwarp();
             }
         }
-        if (exact) exact_candidates<T, 32>(s, InMemory(), V, k, V, s_cand, s_cnt, (int*)nullptr, lane);
+        const int n_el = max(0, min(V, s.col(s.n)) - max(0, s.col(0))), kk = min(k, n_el);
+        if (exact) exact_candidates(s, V, kk, n_el, s_cand, s_cnt, lane);
         __syncwarp();
-        ranks<32>(s_cand, s_cnt[0], k, lane, [&](int r, unsigned long long key) {
-            a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
-            a.idx[row * k + r] = key_col(key);
-        });
-        if (want && lane == 0) {
-            const bool flat = sum == sum && (R == -INFINITY || R == INFINITY);
-            if (a.lse) a.lse[row] = flat ? R : R * a.inv_tau + logf(sum);
-            if (a.lse64) a.lse64[row] = flat ? (double)R : (double)R * (double)a.inv_tau + log((double)sum);
+        if (a.keys) {
+            unsigned long long* out = a.keys + task * k;
+            ranks(s_cand, *s_cnt, kk, [&](int r, unsigned long long key) { out[r] = key; });
+            for (int r = kk + lane; r < k; r += 32) out[r] = 0;
+            if (want && lane == 0) a.parts[task] = make_float2(R, sum);
+        } else {
+            ranks(s_cand, *s_cnt, kk, [&](int r, unsigned long long key) {
+                a.vals[task * k + r] = value_of((uint32_t)(key >> 32));
+                a.idx[task * k + r] = key_col(key);
+            });
+            if (want && lane == 0) a.lse[task] = (float)lse_of(R, sum, a.inv_tau);
         }
         __syncwarp();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// The lists of a row's parts as one, a warp a row.
+constexpr int TJ_WARPS = 2;
+
+__global__ void __launch_bounds__(TJ_WARPS * 32) k_top_join(const TopArgs a) {
+    pdl_enter();
+    __shared__ unsigned long long s_l[TJ_WARPS][TS_JOIN], s_key[TJ_WARPS][JOIN_ROOM];
+    const int P = a.P, k = a.k, N = P * k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = blockIdx.x * (long long)TJ_WARPS + warp;
+    if (row >= a.M) return;
+    for (int i = lane; i < N; i += 32) s_l[warp][i] = a.keys[row * N + i];
+    float R = -INFINITY, s = 0.0f;
+    if (a.want) join_parts(a.parts + row * P, P, LOG2E * a.inv_tau, R, s);
+    __syncwarp();
+    join_lists(s_l[warp], N, k, s_key[warp], [&](int r, unsigned long long key) {
+        a.vals[row * k + r] = value_of((uint32_t)(key >> 32));
+        a.idx[row * k + r] = key_col(key);
+    });
+    if (a.want && lane == 0) a.lse[row] = (float)lse_of(R, s, a.inv_tau);
 }
 
 // ------------------------------------------------------------ distillation
@@ -805,8 +538,6 @@ struct DistillArgs {
     bool same_phase;  // a row of dz starts at the same place of a 16-byte line as its row of z
 };
 
-__host__ __device__ constexpr int distill_threads(int NT) { return NT == 32 ? 256 : NT + LIST_CTA; }
-
 // tau as a power that one softmax's terms are of the other's: 1 to 4, else 0
 __device__ __forceinline__ int power_of(float tau) {
     return tau == 1.0f ? 1 : tau == 2.0f ? 2 : tau == 3.0f ? 3 : tau == 4.0f ? 4 : 0;
@@ -814,7 +545,7 @@ __device__ __forceinline__ int power_of(float tau) {
 
 struct DistillLayout {
     int bits, ti, tv, yl, zl, zo, t, off, part, lw, ll, x, flag, total;
-    __host__ __device__ DistillLayout(int nt, int Gs, int nbuf, int k, int epg, bool cl) {
+    __host__ __device__ DistillLayout(int Gs, int nbuf, int k, int epg, bool cl) {
         const int k4 = align16(4 * (k + 1));
         int at = nbuf * Gs * 16;
         bits = at; at += align16((Gs * epg + 31) / 32 * 4);
@@ -825,7 +556,7 @@ struct DistillLayout {
         zo = at; at += k4;      // those of this CTA's slice
         t = at; at += k4;       // t_j / tau
         off = at; at += k4;     // where this CTA holds the column, or -1
-        part = at; at += nt > 32 ? (nt + LIST_CTA) / 32 * 16 : 0;
+        part = at; at += (NT + LIST_CTA) / 32 * 16;
         lw = at; at += LIST_CTA / 32 * 16;
         ll = at; at += 16;
         x = at; at += cl ? 2 * CS_MAX * 16 : 0;
@@ -947,19 +678,19 @@ __device__ __forceinline__ void grad_pass(const Slice<T>& s, char* buf, T* drow,
 // the others up at every barrier: 1422 us for the 32768 rows of 50257).  Every
 // warp merges the warps' sums and forms the coefficients for itself, which
 // saves a barrier.
-template <typename T, int NT, bool CL>
-__global__ void __launch_bounds__(distill_threads(NT), cta_per_sm(NT))
+template <typename T, bool CL>
+__global__ void __launch_bounds__(NT + LIST_CTA, 2)
 k_distill(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) char smem[];
     constexpr int EPG = Elem<T>::EPG;
-    constexpr int LT = NT == 32 ? 32 : LIST_CTA;
-    const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int lane = threadIdx.x & 31, warp = tid >> 5;
-    const int lt = NT == 32 ? tid : tid - NT;  // >= 0: a thread of the list
-    const bool worker = NT == 32 || tid < NT, lister = lt >= 0;
-    const DistillLayout lay(NT, a.Gs, a.nbuf, a.k, EPG, CL);
-    char* sm = smem + (NT == 32 ? threadIdx.x >> 5 : 0) * lay.total;
+    constexpr int LT = LIST_CTA;
+    const int tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
+    const int lt = tid - NT;  // >= 0: a thread of the list
+    const bool worker = tid < NT, lister = lt >= 0;
+    const DistillLayout lay(a.Gs, a.nbuf, a.k, EPG, CL);
+    char* sm = smem;
     const int k = a.k, V = a.V, k4 = align16(4 * (k + 1)) / 4, nlw = (min(k, LT) + 31) / 32, pw = power_of(a.tau);
     uint32_t* s_bits = reinterpret_cast<uint32_t*>(sm + lay.bits);
     int* s_y = reinterpret_cast<int*>(sm + lay.yl);
@@ -973,8 +704,7 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
     float4* s_x = reinterpret_cast<float4*>(sm + lay.x);  // [2][cs]
     int* s_flag = reinterpret_cast<int*>(sm + lay.flag);  // the target is on the list
     const int rank = CL ? (int)cluster_rank() : 0, cs = CL ? a.cs : 1;
-    const long long first = CL ? blockIdx.x / cs : blockIdx.x * (long long)cta_groups(NT) + (NT == 32 ? threadIdx.x >> 5 : 0);
-    const long long stride = CL ? gridDim.x / cs : gridDim.x * (long long)cta_groups(NT);
+    const long long first = blockIdx.x / cs, stride = gridDim.x / cs;
     const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
     const float it = 1.0f / a.tau, ct = LOG2E * it, lift = 20.0f / fmaxf(1.0f, it);
     float g_all = a.dscale;
@@ -994,7 +724,7 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         for (int w = tid; w < (a.Gs * EPG + 31) / 32; w += NT) s_bits[w] = 0;
     if (tid < 2) s_y[tid] = -1;
     if (tid == 0) *s_flag = 0;
-    group_sync<NT>();
+    __syncthreads();
     for (int i = 0; i < a.nbuf; i++) {
         const long long r = first + i * stride;
         if (r < a.M) {
@@ -1019,7 +749,7 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         float* s_zl = reinterpret_cast<float*>(sm + lay.zl) + par * k4;
         const Slice<T> s = slice(row);
         cp_wait(a.nbuf);
-        group_sync<NT>();
+        __syncthreads();
         int y = s_y[b];
         const bool y_bad = y < -1 || y >= V;
         if (y_bad) y = -1;
@@ -1074,7 +804,7 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         // (a listed target may read as -inf here; its entry then gives the value)
         const int oy = lt == 0 && hard ? s.at(y) : -1;
         const float vy = oy >= 0 ? Elem<T>::get(reinterpret_cast<const T*>(buf + oy)) : 0.0f;
-        if (rest || !dz) group_sync<NT>();  // the list has been read (and replaced)
+        if (rest || !dz) __syncthreads();  // the list has been read (and replaced)
         if (oy >= 0 && !(rest && *s_flag)) keep(k, vy);
         // the teacher's side of a warp's entries: the largest and the sum of
         // exponentials, or, where the normaliser is known, the probabilities' sum
@@ -1124,29 +854,19 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
             merge(R, s1, st, sl, ct, hard, false);
         }
         if (rest && list_warp) {
-            if (NT == 32) {
-                const float m = fmaxf(R, Rl);
-                s1 = s1 * rescale(R, m, LOG2E) + l1 * rescale(Rl, m, LOG2E);
-                st *= rescale(R, m, ct);
-                sl = lts * rescale(Rl, m, ct);
-                R = m;
-            } else {
-                R = Rl;
-                s1 = l1;
-                sl = lts;
-            }
+            R = Rl;
+            s1 = l1;
+            sl = lts;
         }
-        if (NT > 32) {
-            constexpr int W = (NT + LIST_CTA) / 32;
-            static_assert(W <= 16, "the merge below is over 16 lanes");
-            if (lane == 0) s_part[warp] = make_float4(R, s1, st, sl);
-            __syncthreads();
-            if (!CL || warp == 0) {
-                const int l = lane & 15;
-                const float4 p = l < W ? s_part[l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-                R = p.x; s1 = p.y; st = p.z; sl = p.w;
-                merge<16>(R, s1, st, sl, ct, hard, rest);
-            }
+        constexpr int WARPS = (NT + LIST_CTA) / 32;
+        static_assert(WARPS <= 16, "the merge below is over 16 lanes");
+        if (lane == 0) s_part[warp] = make_float4(R, s1, st, sl);
+        __syncthreads();
+        if (!CL || warp == 0) {
+            const int l = lane & 15;
+            const float4 p = l < WARPS ? s_part[l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            R = p.x; s1 = p.y; st = p.z; sl = p.w;
+            merge<16>(R, s1, st, sl, ct, hard, rest);
         }
         if (CL) {
             if (warp == 0 && lane < cs) {
@@ -1164,7 +884,6 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         }
 
         // the teacher's normaliser and mass, and the coefficients of the gradient
-        if (NT == 32) __syncwarp();
         float base = -INFINITY, W = 0.0f;
         bool used = false;
         if (rest) {
@@ -1222,7 +941,7 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
             part = warp_sum(part);
             if (lane == 0) s_ll[lt >> 5] = part;
         }
-        group_sync<NT>();  // the second pass's stores come before those of the list
+        __syncthreads();  // the second pass's stores come before those of the list
         if (lt == 0 && rank == 0) {
             float loss = 0.0f;
             if (soft) {
@@ -1264,6 +983,155 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Short rows (a warp holds one in its registers, lane l the columns l + 32 e):
+// the same sums, with the list spread over the columns, ln p_j at column i_j in
+// shared memory, so that every column knows whether it is listed and nothing
+// is written twice.  By the kernel above a row of 65 took as long as its list
+// handling: 38 us for 16384 rows.
+constexpr int DS_WARPS = 4;
+constexpr uint32_t DS_UNLISTED = 0x7FC0DEADu;  // a NaN that no arithmetic makes
+
+template <typename T, int E>
+__global__ void __launch_bounds__(DS_WARPS * 32)
+k_distill_short(const T* z, T* dz, const DistillArgs a) {
+    pdl_enter();
+    __shared__ uint32_t s_all[DS_WARPS][32 * E];
+    using El = Elem<T>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = a.k, V = a.V;
+    uint32_t* s_lp = s_all[warp] + lane;  // the lane's columns at steps of 32
+    const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
+    const float it = 1.0f / a.tau, ct = LOG2E * it;
+    float g_all = a.dscale;
+    if (a.scale_dev) g_all *= *a.scale_dev;
+    for (long long row = blockIdx.x * (long long)DS_WARPS + warp; row < a.M; row += gridDim.x * (long long)DS_WARPS) {
+        const T* zr = z + row * a.ld;
+        float x[E];
+        float m = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const int c = lane + 32 * e;
+            x[e] = c < V ? El::get(zr + c) : -INFINITY;
+        }
+        int col[LIST_MAX / 32];
+        float t[LIST_MAX / 32];
+#pragma unroll
+        for (int i = 0; i < LIST_MAX / 32; i++) {
+            const int j = lane + 32 * i;
+            col[i] = j < k ? a.t_idx[row * k + j] : -1;
+            t[i] = j < k ? a.t_vals[row * k + j] * it : -INFINITY;
+        }
+        int y = a.targets ? a.targets[row] : -1;
+        const float tl = rest ? a.t_lse[row] : 0.0f;
+        bool bad = y < -1 || y >= V;
+        if (bad) y = -1;
+        const bool hard = hard_on && y >= 0;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            s_lp[32 * e] = DS_UNLISTED;
+            m = fmaxf(m, x[e]);
+        }
+        m = warp_max(m);
+        // the teacher's normaliser
+        float base = tl;
+        bool used = false;
+        float tm = -INFINITY, ts = 0.0f;
+#pragma unroll
+        for (int i = 0; i < LIST_MAX / 32; i++) {
+            if (col[i] < 0 || col[i] >= V) {
+                bad |= col[i] != -1;
+                col[i] = -1;
+                t[i] = -INFINITY;
+            }
+            used |= col[i] >= 0;
+            tm = fmaxf(tm, t[i]);
+        }
+        used = __any_sync(0xffffffffu, used);
+        if (!rest) {
+            tm = warp_max(tm);
+#pragma unroll
+            for (int i = 0; i < LIST_MAX / 32; i++)
+                if (t[i] != -INFINITY) ts += ex2f((t[i] - tm) * LOG2E);
+            ts = warp_sum(ts);
+            base = tm + logf(ts);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < LIST_MAX / 32; i++)
+            if (col[i] >= 0) {
+                const float lp = t[i] == -INFINITY ? -INFINITY : t[i] - base;
+                bad |= atomicCAS(s_all[warp] + col[i], DS_UNLISTED, __float_as_uint(lp)) != DS_UNLISTED;  // listed twice
+            }
+        if (bad) atomicOr(&a.flags[FLAG_BAD_TOKEN], 1);
+        __syncwarp();
+        const bool soft = used && soft_on;
+        float s1 = 0.0f, su = 0.0f, sl = 0.0f, W = 0.0f, part = 0.0f, zy = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const int c = lane + 32 * e;
+            if (c >= V) continue;
+            const float d = x[e] - m;
+            if (hard) s1 += ex2f(d * LOG2E);
+            if (c == y) zy = x[e];
+            if (soft) {
+                const float et = ex2f(d * ct);
+                const uint32_t u = s_lp[32 * e];
+                if (u == DS_UNLISTED) {
+                    su += et;
+                } else {
+                    const float lp = __uint_as_float(u), p = ex2f(lp * LOG2E);
+                    sl += et;
+                    W += p;
+                    if (p > 0.0f || p != p) part += p * (lp - d * it);
+                }
+            }
+        }
+        if (hard) {
+            s1 = warp_sum(s1);
+            zy = __shfl_sync(0xffffffffu, zy, y & 31);
+        }
+        float st = 0.0f, pr = 0.0f;
+        if (soft) {
+            su = warp_sum(su);
+            sl = warp_sum(sl);
+            W = warp_sum(W);
+            part = warp_sum(part);
+            st = su + sl;
+            if (rest && su > 0.0f) pr = fmaxf(1.0f - W, 0.0f);
+        }
+        if (lane == 0) {
+            float loss = 0.0f;
+            if (soft) {
+                loss = part + W * logf(st);
+                if (pr > 0.0f) loss += pr * (logf(pr) - logf(__fdividef(su, st)));
+                loss *= a.alpha * a.tau * a.tau;
+            }
+            if (hard) loss += (1.0f - a.alpha) * (m + logf(s1) - zy);
+            a.row_loss[row] = loss;
+        }
+        if (dz) {
+            T* dr = dz + row * a.ld;
+            const float ks = g_all * a.alpha * a.tau, kh = hard ? g_all * (1.0f - a.alpha) : 0.0f;
+            const float rt = soft ? __fdividef(ks, st) : 0.0f, A1 = hard ? __fdividef(kh, s1) : 0.0f;
+            const float Al = (W + pr) * rt, At = pr > 0.0f ? rt * (W + pr - pr * __fdividef(st, su)) : W * rt;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                const int c = lane + 32 * e;
+                const float d = x[e] - m;
+                float r = 0.0f;
+                if (soft) {
+                    const uint32_t u = s_lp[32 * e];
+                    const float et = ex2f(d * ct);
+                    r = u == DS_UNLISTED ? At * et : Al * et - ks * ex2f(__uint_as_float(u) * LOG2E);
+                }
+                if (hard) r += A1 * ex2f(d * LOG2E) - (c == y ? kh : 0.0f);
+                if (c < a.ld) dr[c] = El::put(c < V ? r : 0.0f);
+            }
+            for (long long c = 32 * E + lane; c < a.ld; c += 32) dr[c] = El::put(0.0f);
+        }
+        __syncwarp();
+    }
+}
+
 // mean of M row losses: each thread adds rows t, t + 1024, ..., the threads'
 // sums meet in a fixed tree
 __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row_loss, int M, float* __restrict__ out,
@@ -1286,10 +1154,10 @@ __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row
 }
 
 // ------------------------------------------------------------ launch
-// How M rows of G granules are spread: the group size, the CTAs a row is
-// shared by, and whether two rows of a group are on chip at once.
+// How a kernel's CTAs are laid out; for distillation also the CTAs that share
+// a row, their slices, and whether two rows of a CTA are on chip at once.
 struct Plan {
-    int nt = 0, cs = 1, nbuf = 2, Gs = 0, ctas = 0, threads = 0;
+    int cs = 1, nbuf = 1, Gs = 0, ctas = 0, threads = 0;
     size_t smem = 0;
 };
 
@@ -1297,24 +1165,19 @@ constexpr size_t SMEM_CTA = 232448;  // 227 KB
 constexpr size_t SMEM_SM = 233472;   // 228 KB, of which each CTA takes 1 KB more than its own
 constexpr size_t SMEM_HALF = SMEM_SM / 2 - 1024;
 
-template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, int big, Bytes&& bytes) {
-    p.cs = 1;
-    p.nbuf = 1;
+template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, Bytes&& bytes) {
     // two CTAs of an SM, each with a row (or slice) of its own: a larger row is cut
-    auto need = [&](int cs) { return bytes(512, (G + cs - 1) / cs, 1, cs > 1); };
-    while (p.cs < CS_MAX && need(p.cs) > SMEM_HALF) p.cs *= 2;
-    if (need(p.cs) > SMEM_CTA) return false;
+    auto need = [&](int cs, int nbuf) { return bytes((G + cs - 1) / cs, nbuf, cs > 1); };
+    while (p.cs < CS_MAX && need(p.cs, 1) > SMEM_HALF) p.cs *= 2;
+    if (need(p.cs, 1) > SMEM_CTA) return false;
     // few rows are cut so that every SM has a part
-    while (p.cs < CS_MAX && M * p.cs * 2 <= sms && G / (p.cs * 2) >= 256) p.cs *= 2;
+    while (p.cs < CS_MAX && M * p.cs <= sms && G / (p.cs * 2) >= 256) p.cs *= 2;
     p.Gs = (G + p.cs - 1) / p.cs;
-    p.nt = p.cs == 1 && G <= 128 ? 32 : p.Gs <= 2048 ? 256 : big;
-    if (p.Gs <= 2048) p.nbuf = 2;
-    p.smem = (size_t)bytes(p.nt, p.Gs, p.nbuf, p.cs > 1) * cta_groups(p.nt);
-    const long long groups = (M + cta_groups(p.nt) - 1) / cta_groups(p.nt);
-    const int per_sm = std::max<int>(1, std::min<int>(cta_per_sm(p.nt), (int)(SMEM_SM / (p.smem + 1024))));
-    const long long room = std::max<long long>(1, (long long)sms * per_sm / p.cs);
-    p.ctas = (int)(std::min(groups, room) * p.cs);
-    p.threads = cta_threads(p.nt);
+    p.nbuf = need(p.cs, 2) <= SMEM_HALF ? 2 : 1;
+    p.smem = need(p.cs, p.nbuf);
+    const long long per_sm = p.smem <= SMEM_HALF ? 2 : 1;
+    p.ctas = (int)(std::min(M, std::max<long long>(1, sms * per_sm / p.cs)) * p.cs);
+    p.threads = NT + LIST_CTA;
     return true;
 }
 
@@ -1349,12 +1212,12 @@ void launch_rows(const Launch& L, void (*kern)(KA...), const Plan& p, A&&... arg
     cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
-#define ROW_KERNEL(NAME, NT_, CL_, ...)                            \
-    do {                                                           \
-        static PerDevice attr;                                     \
-        if (!allow_smem(attr, NAME<T, NT_, CL_>)) return false;    \
-        launch_rows(L, NAME<T, NT_, CL_>, p, __VA_ARGS__);         \
-        return true;                                               \
+#define ROW_KERNEL(NAME, CL_, ...)                            \
+    do {                                                      \
+        static PerDevice attr;                                \
+        if (!allow_smem(attr, NAME<T, CL_>)) return false;    \
+        launch_rows(L, NAME<T, CL_>, p, __VA_ARGS__);         \
+        return true;                                          \
     } while (0)
 
 // granules of a row, for the worst place of its start
@@ -1365,65 +1228,97 @@ template <typename T> int row_granules(const void* z, long long ld, int V) {
 
 template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     Plan p;
-    const int k = a.k, G = row_granules<T>(z, a.ld, a.V);
-    // many rows: a warp each
-    if (G > 128 && a.M >= L.num_sms * 12 && !a.skip) {
-        const int granules = (G + 127) / 128 * 4;  // of a lane, whole stages
-        int ub_log = granules <= TS_BLOCKS ? 0 : 2;
-        while ((granules + (1 << ub_log) - 1) >> ub_log > TS_BLOCKS) ub_log++;
-        const int nb = (granules + (1 << ub_log) - 1) >> ub_log;
-        const int words = (nb + Blocks<T>::PER - 1) / Blocks<T>::PER;
-        static PerDevice attr;
-        if (!allow_smem(attr, k_top_stream<T>)) return false;
-        a.Gs = G;
-        p.smem = TS_WARPS * stream_warp_smem(words, k);
-        p.threads = TS_WARPS * 32;
-        const int per_sm = std::min(3, (int)(SMEM_SM / (p.smem + 1024)));
-        p.ctas = std::min((a.M + TS_WARPS - 1) / TS_WARPS, L.num_sms * per_sm);
-        launch_rows(L, k_top_stream<T>, p, (const T*)z, a, ub_log, words);
-        return true;
-    }
-    if (!make_plan(p, L.num_sms, a.M, G, 512, [k](int nt, int Gs, int nbuf, bool cl) {
-            return (size_t)TopLayout(nt, Gs, nbuf, k, cl).total;
-        }))
-        return false;
-    a.Gs = p.Gs; a.cs = p.cs; a.nbuf = p.nbuf;
-    if (p.nt == 32) ROW_KERNEL(k_top_rows, 32, false, (const T*)z, a);
-    if (p.nt == 256 && p.cs == 1) ROW_KERNEL(k_top_rows, 256, false, (const T*)z, a);
-    if (p.nt == 256) ROW_KERNEL(k_top_rows, 256, true, (const T*)z, a);
-    if (p.cs == 1) ROW_KERNEL(k_top_rows, 512, false, (const T*)z, a);
-    ROW_KERNEL(k_top_rows, 512, true, (const T*)z, a);
+    const int G = row_granules<T>(z, a.ld, a.V);
+    a.Gs = (G + a.P - 1) / a.P;
+    const int granules = (a.Gs + 127) / 128 * 4;  // of a lane, whole stages
+    // blocks of four granules where they are enough to tell k of them from the rest
+    int ub_log = granules <= TS_BLOCKS && granules * 8 < 4 * a.k ? 0 : 2;
+    while ((granules + (1 << ub_log) - 1) >> ub_log > TS_BLOCKS) ub_log++;
+    const int nb = (granules + (1 << ub_log) - 1) >> ub_log;
+    const int words = (nb + Blocks<T>::PER - 1) / Blocks<T>::PER;
+    static PerDevice attr;
+    if (!allow_smem(attr, k_top_stream<T>)) return false;
+    // few tasks are spread over the SMs
+    const long long tasks = (long long)a.M * a.P;
+    const int warps = (int)std::min<long long>(TS_WARPS, std::max<long long>(1, tasks / L.num_sms));
+    p.smem = (size_t)warps * stream_warp_smem(words, a.k);
+    p.threads = warps * 32;
+    const long long per_sm = std::min<long long>(24 / warps, (long long)(SMEM_SM / (p.smem + 1024)));
+    p.ctas = (int)std::min((tasks + warps - 1) / warps, L.num_sms * per_sm);
+    launch_rows(L, k_top_stream<T>, p, (const T*)z, a, ub_log, words);
+    return true;
+}
+
+template <typename T, int E> bool distill_short(const Launch& L, const void* z, void* dz, const DistillArgs& a) {
+    L.count();
+    const unsigned ctas = (unsigned)std::min((a.M + DS_WARPS - 1) / DS_WARPS, L.num_sms * 12);
+    launch_k(L, k_distill_short<T, E>, dim3(ctas), dim3(DS_WARPS * 32), 0, (const T*)z, (T*)dz, a);
+    return true;
 }
 
 template <typename T> bool distill(const Launch& L, const void* z, void* dz, DistillArgs a) {
     Plan p;
     const int k = a.k;
-    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), 256, [k](int nt, int Gs, int nbuf, bool cl) {
-            return (size_t)DistillLayout(nt, Gs, nbuf, k, Elem<T>::EPG, cl).total;
+    if (a.V <= 128) return distill_short<T, 4>(L, z, dz, a);
+    if (a.V <= 512) return distill_short<T, 16>(L, z, dz, a);
+    if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), [k](int Gs, int nbuf, bool cl) {
+            return (size_t)DistillLayout(Gs, nbuf, k, Elem<T>::EPG, cl).total;
         }))
         return false;
     a.Gs = p.Gs; a.cs = p.cs; a.nbuf = p.nbuf;
-    p.threads = distill_threads(p.nt);
     a.same_phase = (((uintptr_t)z ^ (uintptr_t)dz) & 15) == 0;
-    if (p.nt == 32) ROW_KERNEL(k_distill, 32, false, (const T*)z, (T*)dz, a);
-    if (p.cs == 1) ROW_KERNEL(k_distill, 256, false, (const T*)z, (T*)dz, a);
-    ROW_KERNEL(k_distill, 256, true, (const T*)z, (T*)dz, a);
+    if (p.cs == 1) ROW_KERNEL(k_distill, false, (const T*)z, (T*)dz, a);
+    ROW_KERNEL(k_distill, true, (const T*)z, (T*)dz, a);
 }
 
 }  // namespace
 
-// a row is held by at most CS_MAX CTAs, which also need room for the lists
+// distillation: a row is held by at most CS_MAX CTAs, which also need room for the list
 bool head_row_ok(tt_dtype dtype, int V) {
     if (dtype != TT_FP32 && dtype != TT_BF16 && dtype != TT_FP16) return false;
     return (long long)V * (dtype == TT_FP32 ? 4 : 2) <= TT_ROW_BYTES_MAX;
 }
 
+int top_parts(tt_dtype dtype, int M, int V, int k, int entries) {
+    const long long G = ((long long)V * (dtype == TT_FP32 ? 4 : 2) + 15) / 16;
+    const long long p = std::min<long long>(std::min<long long>(TS_TASKS / M, G / 192),
+                                            std::min<long long>(entries / k, TS_PARTS));
+    return (int)std::max<long long>(p, 1);
+}
+
+size_t top_rows_scratch_bytes(tt_dtype dtype, int M, int V, int k) {
+    const size_t P = (size_t)top_parts(dtype, M, V, k, TS_JOIN);
+    return P == 1 ? 0 : (size_t)M * P * 8 * ((size_t)k + 1);
+}
+
 bool launch_top_rows(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, float tau,
-                     float* vals, int32_t* idx, float* lse, double* lse64, const int32_t* skip) {
+                     float* vals, int32_t* idx, float* lse, void* scratch) {
     if (L.dry) return true;
     TopArgs a{};
-    a.vals = vals; a.idx = idx; a.lse = lse; a.lse64 = lse64; a.skip = skip;
+    a.vals = vals; a.idx = idx; a.lse = lse; a.want = lse != nullptr;
     a.ld = ld; a.M = M; a.V = V; a.k = k; a.inv_tau = 1.0f / tau;
+    a.P = top_parts(dtype, M, V, k, TS_JOIN);
+    if (a.P > 1) {
+        a.keys = (unsigned long long*)scratch;
+        a.parts = (float2*)(a.keys + (size_t)M * a.P * k);
+    }
+    const bool ok = dtype == TT_FP32   ? top_rows<float>(L, z, a)
+                    : dtype == TT_FP16 ? top_rows<__half>(L, z, a)
+                                       : top_rows<__nv_bfloat16>(L, z, a);
+    if (!ok) return false;
+    if (a.P > 1) {
+        L.count();
+        launch_k(L, k_top_join, dim3((M + TJ_WARPS - 1) / TJ_WARPS), dim3(TJ_WARPS * 32), 0, a);
+    }
+    return true;
+}
+
+bool launch_top_parts(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, int P,
+                      unsigned long long* keys, float2* parts, const int32_t* skip) {
+    if (L.dry) return true;
+    TopArgs a{};
+    a.keys = keys; a.parts = parts; a.skip = skip; a.want = true;
+    a.ld = ld; a.M = M; a.V = V; a.k = k; a.P = P; a.inv_tau = 1.0f;
     if (dtype == TT_FP32) return top_rows<float>(L, z, a);
     if (dtype == TT_FP16) return top_rows<__half>(L, z, a);
     return top_rows<__nv_bfloat16>(L, z, a);

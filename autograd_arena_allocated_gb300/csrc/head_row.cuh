@@ -1,19 +1,17 @@
-// head_row.cuh -- how the list kernels (head.cu) hold a row of logits.
+// head_row.cuh -- what the list kernels (head.cu, beam.cu) share: a row of
+// logits in granules, its sums of exponentials, and lists of its columns.
 //
-// A group of NT threads (a warp, or a CTA; NT = 32, 256 or 512) works on one
-// row at a time and strides over the rows.  With clusters, the cs CTAs of a
-// cluster share a row, each a slice of it.  The row is cut into granules of 16
-// bytes on 16-byte boundaries of memory; granule i of the slice lives in slot
-// i of a shared-memory buffer and belongs to thread i mod NT, which copies it
-// in (cp.async), reads it in every pass, and refills it with a later row's as
-// soon as it has read it for the last time.  So a pass needs no barrier for
-// the row's data, a row is read from memory once, and the next row (or two)
-// is on its way while this one is computed on.
+// A row is cut into granules of 16 bytes on 16-byte boundaries of memory.
+// Rows may start anywhere (odd ld, offset pointers): granules wholly inside
+// the row are copied and read as 16 bytes; the first and the last, where they
+// are not, are fetched element by element and filled up with -inf, which no
+// result depends on.  Nothing outside the row is read.
 //
-// Rows may start anywhere (odd ld, offset pointers): the row's first and last
-// granules, where they are not wholly inside the row, are fetched element by
-// element (by threads 0..15 of the group, a row ahead) and filled up with
-// -inf, which no result depends on; nothing outside the row is read.
+// In distillation a granule of the row (or, in a cluster, of the CTA's slice
+// of it) is in slot i of a shared-memory buffer and belongs to thread i mod NT,
+// which copies it in (cp.async), reads it in every pass, and refills it with
+// the next row's as soon as it has read it for the last time: the passes need
+// no barrier for the row's data, and a row is read from memory once.
 #pragma once
 
 #include "tt_internal.h"
@@ -198,11 +196,7 @@ __device__ __forceinline__ void st_remote(uint32_t at, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
 
-// ------------------------------------------------------------ groups
-template <int NT> __device__ __forceinline__ void group_sync() {
-    if (NT == 32) __syncwarp();
-    else __syncthreads();
-}
+// ------------------------------------------------------------ warps
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -490,6 +484,107 @@ __device__ __forceinline__ void merge(float& R, float& s1, float& st, float& sl,
         for (int o = N / 2; o > 0; o >>= 1) sl += __shfl_xor_sync(0xffffffffu, sl, o);
     }
     R = m;
+}
+
+// log sum exp(z / tau) of merged sums: a row of -inf and a row with +inf have
+// that as their value, unless a NaN is there too.  The logarithm is taken of
+// the mantissa, so that it adds no error to speak of to the sum's.
+__device__ __forceinline__ double lse_of(float R, float s, float inv_tau) {
+    if (s == s && (R == -INFINITY || R == INFINITY)) return (double)R;
+    int e = 0;
+    const float m = frexpf(s, &e);
+    return (double)R * (double)inv_tau + ((double)e * 0.6931471805599453 + (double)logf(m));
+}
+
+// ------------------------------------------------------------ lists
+// Order-preserving whole number of a value: -0 counts as +0 and a NaN as -inf.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t u = __float_as_uint(fmaxf(v, -INFINITY) + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t u) {
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+// (value, column): larger values first, then lower columns.  Never 0.
+__device__ __forceinline__ unsigned long long top_key(float v, int col) {
+    return ((unsigned long long)order_of(v) << 32) | (unsigned long long)(0xFFFFFFFFu - (uint32_t)col);
+}
+__device__ __forceinline__ int key_col(unsigned long long key) {
+    return (int)(0xFFFFFFFFu - (uint32_t)(key & 0xFFFFFFFFull));
+}
+// out(rank, key) for the kk first of cnt keys in list order, by a warp; four lanes count for a key
+template <typename F>
+__device__ __forceinline__ void ranks(const unsigned long long* s_key, int cnt, int kk, F&& out) {
+    const int lane = threadIdx.x & 31;
+    for (int i0 = 0; i0 < cnt; i0 += 8) {
+        const int i = i0 + lane / 4;
+        const unsigned long long key = i < cnt ? s_key[i] : ~0ull;
+        int r = 0;
+#pragma unroll 4
+        for (int j = lane & 3; j < cnt; j += 4) r += s_key[j] > key;
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        if ((lane & 3) == 0 && i < cnt && r < kk) out(r, key);
+    }
+}
+
+// The kk first of n keys (0: no entry; at least kk are entries) by a warp: a
+// bound that kk to JOIN_ROOM keys reach is found bit by bit by counting (keys
+// are all different, so there is one), and those are ranked.  s_key holds
+// JOIN_ROOM keys.
+constexpr int JOIN_ROOM = 160;
+
+template <typename F>
+__device__ __forceinline__ void join_lists(const unsigned long long* l, int n, int kk, unsigned long long* s_key,
+                                           F&& out) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long t = 0;
+    if (n > min(kk + 32, JOIN_ROOM)) {  // few enough are ranked as they are
+        uint32_t hi = 0, lo = ~0u;
+        for (int i = lane; i < n; i += 32) {
+            const uint32_t w = (uint32_t)(l[i] >> 32);
+            hi = max(hi, w);
+            lo = min(lo, w);
+        }
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        int bit = hi == lo ? 31 : 63 - __clz(hi ^ lo);
+        t = (unsigned long long)hi << 32;
+        t &= ~((2ull << bit) - 1ull);
+        for (; bit >= 0; bit--) {
+            const unsigned long long cand = t | (1ull << bit);
+            int c = 0;
+#pragma unroll 4
+            for (int i = lane; i < n; i += 32) c += l[i] >= cand;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (c >= kk) t = cand;
+            if (c >= kk && c <= min(kk + 16, JOIN_ROOM)) break;
+        }
+    }
+    int cnt = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const unsigned long long key = i0 + lane < n ? l[i0 + lane] : 0ull;
+        const bool on = key != 0 && key >= t;
+        const uint32_t m = __ballot_sync(0xffffffffu, on);
+        if (on) s_key[cnt + __popc(m & ((1u << lane) - 1u))] = key;
+        cnt += __popc(m);
+    }
+    __syncwarp();
+    ranks(s_key, cnt, kk, out);
+}
+
+// A warp merges P parts' references and sums.
+__device__ __forceinline__ void join_parts(const float2* parts, int P, float c, float& R, float& s) {
+    const int lane = threadIdx.x & 31;
+    R = -INFINITY;
+    s = 0.0f;
+    for (int p = lane; p < P; p += 32) {
+        const float2 x = parts[p];
+        const float m = fmaxf(R, x.x);
+        s = s * rescale(R, m, c) + x.y * rescale(x.x, m, c);
+        R = m;
+    }
+    merge(R, s, c);
 }
 
 }  // namespace head

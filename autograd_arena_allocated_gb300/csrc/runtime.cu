@@ -966,7 +966,8 @@ static tt_status gpt2_generate_beam(tt_ctx* c, const void* params, const int32_t
     int32_t* token = (int32_t*)arena_alloc(c, (size_t)R * 4);
     int32_t* done = (int32_t*)arena_alloc(c, (size_t)R * 4);
     float* zero = (float*)arena_alloc(c, (size_t)B * 4);
-    void* scratch = arena_alloc(c, beam_select_scratch_bytes(R, m.V, K));
+    void* scratch = arena_alloc(c, std::max(beam_select_scratch_bytes(m.dtype, B, 1, m.V, K),
+                                            beam_select_scratch_bytes(m.dtype, B, K, m.V, K)));
     std::vector<int> qkv_ids;
     int z = gpt2_forward(c, params, nullptr, prompt_dev, B, Tp, &qkv_ids);
     if (c->oom) return TT_ERR_ARENA_OOM;
@@ -1469,10 +1470,10 @@ tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* token
     const char* why = list_refusal(m.dtype, m.V, k, tau);
     if (why) return fail(c, TT_ERR_ARG, "top_logits: %s", why);
     {
-        const size_t need = tt_gpt2_arena_bytes(&c->cfg, B, T);
+        const size_t need = tt_gpt2_arena_bytes(&c->cfg, B, T) + top_rows_scratch_bytes(m.dtype, B * T, m.V, k);
         const size_t at = (c->off + ARENA_ALIGN - 1) & ~(ARENA_ALIGN - 1);
-        if (need == 0 || at + need > c->cap)
-            return fail(c, TT_ERR_ARENA_OOM, "arena too small: the forward needs %zu bytes, %zu free", need,
+        if (at + need > c->cap)
+            return fail(c, TT_ERR_ARENA_OOM, "arena too small: the forward and the lists need %zu bytes, %zu free", need,
                         c->cap > at ? c->cap - at : (size_t)0);
     }
     begin_step(c);
@@ -1483,10 +1484,11 @@ tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* token
     const int z = gpt2_forward(c, params, nullptr, tok, B, T);
     if (c->oom) return fail(c, TT_ERR_ARENA_OOM, "arena exhausted during the forward");
     const int M = B * T, ld = (int)c->tensors[z].cols;
-    {
+    const size_t sb = top_rows_scratch_bytes(m.dtype, M, m.V, k);
+    void* scratch = sb ? arena_alloc(c, sb) : nullptr;
+    if (!c->oom) {
         ProfScope ps(c, PK_TOP, 0.0, (double)M * m.V * esize(m.dtype) + 8.0 * M * k);
-        if (!launch_top_rows(launch_of(c), m.dtype, c->tensors[z].data, ld, M, m.V, k, tau, vals, idx, lse, nullptr,
-                             nullptr))
+        if (!launch_top_rows(launch_of(c), m.dtype, c->tensors[z].data, ld, M, m.V, k, tau, vals, idx, lse, scratch))
             return fail(c, TT_ERR_CUDA, "top_logits: launch failed");
     }
     return op_epilogue(c, "top_logits");
@@ -1802,11 +1804,16 @@ tt_status tt_op_top_logits(tt_ctx* c, tt_dtype dtype, const void* logits, float*
     if (!logits || !vals || !idx || M <= 0 || V <= 0 || ld < V) return fail(c, TT_ERR_ARG, "top_logits: bad arguments");
     const char* why = list_refusal(dtype, V, k, tau);
     if (why) return fail(c, TT_ERR_ARG, "top_logits: %s", why);
-    {
+    const size_t mark = c->off, sb = top_rows_scratch_bytes(dtype, M, V, k);
+    c->oom = false;
+    void* s = sb ? arena_alloc(c, sb) : nullptr;
+    bool ok = true;
+    if (!c->oom) {
         ProfScope ps(c, PK_TOP, 0.0, (double)M * V * esize(dtype) + 8.0 * M * k);
-        if (!launch_top_rows(op_launch(c), dtype, logits, ld, M, V, k, tau, vals, idx, lse, nullptr, nullptr))
-            return fail(c, TT_ERR_CUDA, "top_logits: launch failed");
+        ok = launch_top_rows(op_launch(c), dtype, logits, ld, M, V, k, tau, vals, idx, lse, s);
     }
+    c->off = mark;
+    if (!ok) return fail(c, TT_ERR_CUDA, "top_logits: launch failed");
     return op_epilogue(c, "top_logits");
 }
 
@@ -1842,7 +1849,7 @@ tt_status tt_op_beam_select(tt_ctx* c, tt_dtype dtype, const void* logits, const
     if (why) return fail(c, TT_ERR_ARG, "beam_select: %s", why);
     const size_t mark = c->off;
     c->oom = false;
-    void* s = arena_alloc(c, beam_select_scratch_bytes(B * K, V, n));
+    void* s = arena_alloc(c, beam_select_scratch_bytes(dtype, B, K, V, n));
     bool ok = true;
     if (!c->oom) {
         ProfScope ps(c, PK_BEAM_SELECT, 0.0, (double)B * K * V * esize(dtype) + 16.0 * B * n);

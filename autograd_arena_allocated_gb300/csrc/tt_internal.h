@@ -281,10 +281,17 @@ void launch_pick(const Launch& L, const unsigned long long* keys, int nct, int r
 
 // lists over the LM head's logits (head.cu); rows of ld elements, V of them real
 bool head_row_ok(tt_dtype dtype, int V);  // a row the kernels take
-// per row the k largest logits (ties: lowest column) and log sum exp(z / tau);
-// lse, lse64 and skip (rows left out where it is not 0) may be NULL
+// per row the k largest logits (ties: lowest column) and log sum exp(z / tau)
+// (lse may be NULL); scratch: top_rows_scratch_bytes()
+size_t top_rows_scratch_bytes(tt_dtype dtype, int M, int V, int k);
 bool launch_top_rows(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, float tau,
-                     float* vals, int32_t* idx, float* lse, double* lse64, const int32_t* skip);
+                     float* vals, int32_t* idx, float* lse, void* scratch);
+// the same in P parts a row, left as lists of keys (head_row.cuh) and sums of
+// exponentials; rows with skip[row] != 0 are left out.  top_parts: how many
+// parts M rows are best cut into, their lists having at most `entries` in all
+int top_parts(tt_dtype dtype, int M, int V, int k, int entries);
+bool launch_top_parts(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, int P,
+                      unsigned long long* keys, float2* parts, const int32_t* skip);
 // distillation loss and gradient; dz (may be z, or NULL: loss only), t_lse,
 // targets, mean_loss and scale_dev may be NULL
 bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, const float* t_vals,
@@ -294,7 +301,7 @@ bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, co
 
 // beam search (beam.cu).  tok_hist/par_hist (may be NULL): the choice is also
 // written to [slot][*pos_dev] of these [B n, ld_hist] tables.
-size_t beam_select_scratch_bytes(int R, int V, int n);
+size_t beam_select_scratch_bytes(tt_dtype dtype, int B, int K, int V, int n);
 bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long long ld, const float* scores,
                         const int32_t* done, int32_t* parent, int32_t* token, float* out_scores, int32_t* out_done,
                         int B, int K, int V, int n, int eos, void* scratch, int32_t* tok_hist, int32_t* par_hist,

@@ -287,7 +287,8 @@ tt_status tt_gpt2_eval(tt_ctx* ctx, const void* params, const int32_t* tokens,
  * likeliest next tokens of a prompt.  vals, idx [B*T, k] and lse [B*T] (may
  * be NULL) are device memory.  Does not synchronize (a token id out of range
  * is reported by tt_ctx_sync); the arena needs at most
- * tt_gpt2_arena_bytes(cfg, B, T) and is NOT reset by this call.  There is no
+ * tt_gpt2_arena_bytes(cfg, B, T) + TT_TOP_SCRATCH_BYTES (tt_ops.h) and is NOT
+ * reset by this call.  There is no
  * last loss to read (tt_ctx_loss_device) until the next step. */
 tt_status tt_gpt2_top_logits(tt_ctx* ctx, const void* params, const int32_t* tokens, int B, int T, int k,
                              float tau, float* vals, int32_t* idx, float* lse);

@@ -122,6 +122,7 @@ tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int
 
 #define TT_TOP_MAX 128  /* longest list of a row */
 #define TT_BEAM_MAX 32  /* most beams of a sequence */
+#define TT_TOP_SCRATCH_BYTES (4u << 20) /* most arena scratch of tt_op_top_logits */
 #define TT_ROW_BYTES_MAX 1600000  /* most bytes of the V logits of a row (a row is held on chip) */
 
 /* The k largest logits of each row, in descending order, equal ones by
@@ -129,7 +130,8 @@ tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int
  *   vals [M, k] fp32, idx [M, k];  lse [M] fp32 or NULL: log sum_v exp(z_v / tau)
  * over the V columns.  1 <= k <= min(V, TT_TOP_MAX), tau > 0.  A NaN logit
  * stands in the list as -inf and makes the row's lse NaN; a row of -inf has
- * lse = -inf, one with +inf has lse = +inf. */
+ * lse = -inf, one with +inf has lse = +inf.  Scratch from the arena where
+ * there are few rows: at most TT_TOP_SCRATCH_BYTES. */
 tt_status tt_op_top_logits(tt_ctx* ctx, tt_dtype dtype, const void* logits, float* vals, int32_t* idx, float* lse,
                            int M, int V, int ld, int k, float tau);
 
@@ -176,7 +178,8 @@ tt_status tt_op_distill(tt_ctx* ctx, tt_dtype dtype, const void* logits, const f
  * TT_ERR_NONFINITE); it, a beam whose logits are all -inf and one whose score
  * is not finite have candidates of -inf only.  1 <= K <= TT_BEAM_MAX,
  * 1 <= n <= min(2 TT_BEAM_MAX, K V).  out_scores and out_done may be scores
- * and done when n == K.  Scratch from the arena: B K (8 + 8 n) bytes. */
+ * and done when n == K.  Scratch from the arena: 8 B K (n + 1) bytes, times
+ * the parts that few rows are cut into; at most TT_TOP_SCRATCH_BYTES more. */
 tt_status tt_op_beam_select(tt_ctx* ctx, tt_dtype dtype, const void* logits, const float* scores,
                             const int32_t* done, int32_t* parent, int32_t* token, float* out_scores,
                             int32_t* out_done, int B, int K, int V, int ld, int n, int eos);
