@@ -544,19 +544,20 @@ __device__ __forceinline__ int power_of(float tau) {
 }
 
 struct DistillLayout {
-    int bits, ti, tv, yl, zl, zo, t, off, part, lw, ll, x, flag, total;
+    int bits, ti, tv, tl, edge, zl, zo, t, off, part, lw, ll, x, flag, total;
     __host__ __device__ DistillLayout(int Gs, int nbuf, int k, int epg, bool cl) {
         const int k4 = align16(4 * (k + 1));
         int at = nbuf * Gs * 16;
         bits = at; at += align16((Gs * epg + 31) / 32 * 4);
         ti = at; at += nbuf * k4;
         tv = at; at += nbuf * k4;
-        yl = at; at += 16;      // [nbuf] targets, [nbuf] t_lse
+        tl = at; at += 16;      // [nbuf] t_lse
+        edge = at; at += 64;
         zl = at; at += 2 * k4;  // student logits of the list, and of the target
         zo = at; at += k4;      // those of this CTA's slice
         t = at; at += k4;       // t_j / tau
         off = at; at += k4;     // where this CTA holds the column, or -1
-        part = at; at += (NT + LIST_CTA) / 32 * 16;
+        part = at; at += 2 * (NT + LIST_CTA) / 32 * 16;
         lw = at; at += LIST_CTA / 32 * 16;
         ll = at; at += 16;
         x = at; at += cl ? 2 * CS_MAX * 16 : 0;
@@ -564,6 +565,15 @@ struct DistillLayout {
         total = at;
     }
 };
+
+// A CTA's threads meet at barrier ID, or arrive there without waiting.
+template <int ID> __device__ __forceinline__ void meet() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(NT + LIST_CTA) : "memory");
+}
+template <int ID> __device__ __forceinline__ void arrive() {
+    __threadfence_block();
+    asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(NT + LIST_CTA) : "memory");
+}
 
 // At 2^((z - m) ct) + A1 e^(z - m) for every column of the slice (S, H: which
 // of the two there are); both coefficients 0: zeros, whatever the logits are.
@@ -675,13 +685,15 @@ __device__ __forceinline__ void grad_pass(const Slice<T>& s, char* buf, T* drow,
 
 // In a CTA, LIST_CTA threads of their own look after the list, beside the NT
 // threads' passes over the row (as a part of one of those warps' work it held
-// the others up at every barrier: 1422 us for the 32768 rows of 50257).  Every
-// warp merges the warps' sums and forms the coefficients for itself, which
-// saves a barrier.
+// the others up at every barrier: 1422 us for the 32768 rows of 50257).  They
+// wait for the others at the start of a row (its copies have arrived) and at
+// its end (its gradient is written), the others do not wait for them there; all
+// meet where the sums do.  Every warp merges the warps' sums and forms the
+// coefficients for itself, which saves a barrier.
 template <typename T, bool CL>
 __global__ void __launch_bounds__(NT + LIST_CTA, 2)
 k_distill(const T* z, T* dz, const DistillArgs a) {
-    pdl_enter();
+    pdl_wait();
     extern __shared__ __align__(16) char smem[];
     constexpr int EPG = Elem<T>::EPG;
     constexpr int LT = LIST_CTA;
@@ -693,8 +705,8 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
     char* sm = smem;
     const int k = a.k, V = a.V, k4 = align16(4 * (k + 1)) / 4, nlw = (min(k, LT) + 31) / 32, pw = power_of(a.tau);
     uint32_t* s_bits = reinterpret_cast<uint32_t*>(sm + lay.bits);
-    int* s_y = reinterpret_cast<int*>(sm + lay.yl);
-    float* s_tl = reinterpret_cast<float*>(sm + lay.yl) + 2;
+    float* s_tl = reinterpret_cast<float*>(sm + lay.tl);
+    T* s_edge = reinterpret_cast<T*>(sm + lay.edge);  // [2][head, tail] granules
     float* s_t = reinterpret_cast<float*>(sm + lay.t);
     int* s_off = reinterpret_cast<int*>(sm + lay.off);
     float* s_zo = reinterpret_cast<float*>(sm + lay.zo);
@@ -716,15 +728,12 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
                 cp4(sm + lay.ti + (b * k4 + j) * 4, a.t_idx + r * k + j);
                 cp4(sm + lay.tv + (b * k4 + j) * 4, a.t_vals + r * k + j);
             }
-        if (lt == 0 && a.targets) cp4(s_y + b, a.targets + r);
-        if (lt == 1 && rest) cp4(s_tl + b, a.t_lse + r);
+        if (lt == 0 && rest) cp4(s_tl + b, a.t_lse + r);
     };
 
     if (worker)
         for (int w = tid; w < (a.Gs * EPG + 31) / 32; w += NT) s_bits[w] = 0;
-    if (tid < 2) s_y[tid] = -1;
     if (tid == 0) *s_flag = 0;
-    __syncthreads();
     for (int i = 0; i < a.nbuf; i++) {
         const long long r = first + i * stride;
         if (r < a.M) {
@@ -733,11 +742,18 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         }
         cp_commit();
     }
+    // edge granules: this row's are put beside the buffers a row ahead, by the
+    // list's threads; their slots' threads move them in
+    auto put_edge = [&](const Slice<T>& e, int q, T v) {
+        if (edge_slot(e, lt) >= 0) s_edge[(q * 2 + (lt >> 3)) * EPG + (lt & 7)] = v;
+    };
     T edge = Elem<T>::put(0.0f);
-    if (lt >= 0 && lt < 16) {
-        if (first < a.M) edge_store(slice(first), sm, edge_load(slice(first), V, lt), lt);
+    if (lister && lt < 16) {
+        if (first < a.M) put_edge(slice(first), 0, edge_load(slice(first), V, lt));
         if (first + stride < a.M) edge = edge_load(slice(first + stride), V, lt);
     }
+    int y_next = a.targets && first < a.M ? a.targets[first] : -1;
+    __syncthreads();
     if (CL) cluster_sync();  // the others run: their shared memory may be written
 
     int itn = 0;
@@ -748,12 +764,20 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         const float* s_tv = reinterpret_cast<const float*>(sm + lay.tv) + b * k4;
         float* s_zl = reinterpret_cast<float*>(sm + lay.zl) + par * k4;
         const Slice<T> s = slice(row);
-        cp_wait(a.nbuf);
-        __syncthreads();
-        int y = s_y[b];
+        int y = y_next;
+        if (a.targets && row + stride < a.M) y_next = a.targets[row + stride];
         const bool y_bad = y < -1 || y >= V;
         if (y_bad) y = -1;
         const bool hard = hard_on && y >= 0;
+        cp_wait(a.nbuf);
+        if (worker) {
+            const uint4* e = reinterpret_cast<const uint4*>(s_edge) + par * 2;
+            if (s.head && tid == 0) reinterpret_cast<uint4*>(buf)[0] = e[0];
+            if (s.tail && tid == (s.n - 1) % NT) reinterpret_cast<uint4*>(buf)[s.n - 1] = e[1];
+            arrive<1>();
+        } else {
+            meet<1>();
+        }
 
         // the list: the student's logits at its columns (in a cluster the
         // column's CTA sends them to all), duplicates, the replacement by -inf
@@ -765,47 +789,55 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         float Rl = -INFINITY, l1 = 0.0f, lts = 0.0f;  // sums of listed exponentials
         const bool list_warp = lister && lt < nlw * 32;
         if (list_warp) {
+            for (int j = lt; j < k; j += LT) {
+                const int c = s_ti[j], o = c >= 0 && c < V ? s.at(c) : -1;
+                s_off[j] = o;
+                if (o < 0) continue;
+                T* p = reinterpret_cast<T*>(buf + o);
+                s_zo[j] = Elem<T>::get(p);
+                if (rest) *p = Elem<T>::put(-INFINITY);
+            }
+        }
+        // the target's logit; listed, it is the entry's to give (here it may read as -inf)
+        const int oy = lt == 0 && hard ? s.at(y) : -1;
+        const float vy = oy >= 0 ? Elem<T>::get(reinterpret_cast<const T*>(buf + oy)) : 0.0f;
+        if (list_warp && hard)
+            for (int j = lt; j < k; j += LT)
+                if (s_ti[j] == y && s_off[j] >= 0) {
+                    *s_flag = 1;
+                    if (rest) keep(k, s_zo[j]);
+                }
+        if (rest || !dz) __syncthreads();  // the list has been read (and replaced)
+        if (oy >= 0 && !(rest && *s_flag)) keep(k, vy);
+        if (lister && lt < 16) {
+            const long long n1 = row + stride, n2 = n1 + stride;
+            if (n1 < a.M) put_edge(slice(n1), par ^ 1, edge);
+            if (n2 < a.M) edge = edge_load(slice(n2), V, lt);
+        }
+        if (list_warp) {
             bool bad = y_bad && lt == 0;
             for (int j = lt; j < k; j += LT) {
-                int c = s_ti[j], o = -1;
+                int c = s_ti[j];
+                const int o = s_off[j];
                 if (c < 0 || c >= V) {
                     bad |= c != -1;
                     c = -1;
-                } else {
-                    o = s.at(c);
-                }
-                if (o >= 0) {
+                } else if (o >= 0) {
                     const int at = o / (int)sizeof(T);
                     const uint32_t bit = 1u << (at & 31);
                     if (atomicOr(&s_bits[at >> 5], bit) & bit) {  // listed twice
                         bad = true;
-                        c = o = -1;
+                        c = s_off[j] = -1;
                     } else {
-                        T* p = reinterpret_cast<T*>(buf + o);
-                        const float v = Elem<T>::get(p);
-                        keep(j, v);
-                        s_zo[j] = v;
-                        if (rest) {
-                            *p = Elem<T>::put(-INFINITY);
-                            Rl = fmaxf(Rl, v);
-                        }
-                        if (c == y) {
-                            *s_flag = 1;
-                            if (rest) keep(k, v);
-                        }
+                        keep(j, s_zo[j]);
+                        Rl = fmaxf(Rl, s_zo[j]);
                     }
                 }
                 s_ti[j] = c;
-                s_off[j] = o;
                 s_t[j] = c < 0 ? -INFINITY : s_tv[j] * it;
             }
             if (bad) atomicOr(&a.flags[FLAG_BAD_TOKEN], 1);
         }
-        // (a listed target may read as -inf here; its entry then gives the value)
-        const int oy = lt == 0 && hard ? s.at(y) : -1;
-        const float vy = oy >= 0 ? Elem<T>::get(reinterpret_cast<const T*>(buf + oy)) : 0.0f;
-        if (rest || !dz) __syncthreads();  // the list has been read (and replaced)
-        if (oy >= 0 && !(rest && *s_flag)) keep(k, vy);
         // the teacher's side of a warp's entries: the largest and the sum of
         // exponentials, or, where the normaliser is known, the probabilities' sum
         if (list_warp) {
@@ -860,11 +892,11 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         }
         constexpr int WARPS = (NT + LIST_CTA) / 32;
         static_assert(WARPS <= 16, "the merge below is over 16 lanes");
-        if (lane == 0) s_part[warp] = make_float4(R, s1, st, sl);
+        if (lane == 0) s_part[par * WARPS + warp] = make_float4(R, s1, st, sl);
         __syncthreads();
         if (!CL || warp == 0) {
             const int l = lane & 15;
-            const float4 p = l < WARPS ? s_part[l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            const float4 p = l < WARPS ? s_part[par * WARPS + l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             R = p.x; s1 = p.y; st = p.z; sl = p.w;
             merge<16>(R, s1, st, sl, ct, hard, rest);
         }
@@ -941,7 +973,12 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
             part = warp_sum(part);
             if (lane == 0) s_ll[lt >> 5] = part;
         }
-        __syncthreads();  // the second pass's stores come before those of the list
+        if (worker) {
+            cp_commit();
+            arrive<2>();  // the second pass's stores come before those of the list
+            continue;
+        }
+        meet<2>();
         if (lt == 0 && rank == 0) {
             float loss = 0.0f;
             if (soft) {
@@ -974,11 +1011,6 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         }
         if (more) copy_lists(next, b);
         cp_commit();
-        const long long n1 = row + stride, n2 = n1 + stride;
-        if (lt >= 0 && lt < 16) {
-            if (n1 < a.M) edge_store(slice(n1), sm + (a.nbuf == 2 ? par ^ 1 : 0) * a.Gs * 16, edge, lt);
-            if (n2 < a.M) edge = edge_load(slice(n2), V, lt);
-        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }

@@ -257,7 +257,7 @@ __device__ __forceinline__ void fill(const Slice<T>& s, char* buf, int tid) {
 // one element of: threads 0..7 the head's, 8..15 the tail's; -1: none.
 template <typename T>
 __device__ __forceinline__ int edge_slot(const Slice<T>& s, int tid) {
-    if (tid >= 16 || (tid & 7) >= Elem<T>::EPG) return -1;
+    if (tid < 0 || tid >= 16 || (tid & 7) >= Elem<T>::EPG) return -1;
     if (tid < 8) return s.head ? 0 : -1;
     return s.tail ? s.n - 1 : -1;
 }
@@ -268,12 +268,6 @@ __device__ __forceinline__ T edge_load(const Slice<T>& s, int V, int tid) {
     return c >= 0 && c < V ? reinterpret_cast<const T*>(s.base)[i * Elem<T>::EPG + (tid & 7)]
                            : Elem<T>::put(-INFINITY);
 }
-template <typename T>
-__device__ __forceinline__ void edge_store(const Slice<T>& s, char* buf, T v, int tid) {
-    const int i = edge_slot(s, tid);
-    if (i >= 0) reinterpret_cast<T*>(buf)[i * Elem<T>::EPG + (tid & 7)] = v;
-}
-
 // Slot i of the slice, read from memory; what lies outside the row is -inf.
 template <typename T> __device__ __noinline__ uint4 edge_granule(const T* row, int c0, int V) {
     union {
