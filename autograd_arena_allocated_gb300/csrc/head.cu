@@ -13,6 +13,7 @@
 #include "head_row.cuh"
 
 #include <algorithm>
+#include <cfloat>
 
 namespace tt {
 namespace {
@@ -72,7 +73,7 @@ __device__ __forceinline__ void each_element(const Slice<T>& s, int V, int lane,
 // The kk first elements of the slice in list order, exactly, as candidates:
 // the kk-th largest value is found bit by bit by counting, then, where equal
 // values are more than are needed, the last column that is taken.  Used where
-// the blocks' maxima say too little: most columns masked, few different values.
+// the blocks' maxima say too little: few different values.
 template <typename T>
 __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, int n_el, unsigned long long* s_cand,
                                               int* s_cnt, int lane) {
@@ -135,8 +136,8 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, 
 // cost 26% more DRAM traffic.  A CTA a row, the row held on chip, needs no
 // second read but waits at its barriers: 940 us for 32768 such rows, and 75 us
 // for a selection step of 256 fp32 rows.
-// A row with more candidates than there is room for (ties, masks) is gone
-// through bit by bit from memory.
+// A row with more candidates than there is room for (ties: few different
+// values) is gone through bit by bit from memory.
 constexpr int TS_WARPS = 8;                 // most warps of a CTA
 constexpr int TS_TASKS = 3648;              // rows, or parts, that are worked on at once: 24 warps on each of 152 SMs
 constexpr int TS_PARTS = 64;                // most parts of a row
@@ -405,10 +406,13 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
             if (c >= k && c <= k + 16) break;  // a few blocks more cost less than another bit
         }
         const T tv = Ordered<T>::value(t);
-        const float thr = E::get(&tv);
-        bool exact = !(thr > -INFINITY);  // or no number
+        // fewer than k blocks hold anything above -inf: then all that they hold is taken
+        const bool few = !(E::get(&tv) > -INFINITY);
+        const float thr = few ? -FLT_MAX : E::get(&tv);
+        const int n_el = max(0, min(V, s.col(s.n)) - max(0, s.col(0))), kk = min(k, n_el);
+        bool exact = false;
         __syncwarp();
-        if (!exact) {
+        {
             unsigned long long mine = 0;  // the lane's blocks at or above it
 #pragma unroll 4
             for (int i = 0; i < nw; i++) {
@@ -467,11 +471,25 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                     }
                 }
                 __syncwarp();
-                exact = s_cnt[0] > TS_CAND;
+                const int cnt = *s_cnt;
+                exact = cnt > TS_CAND;
                 __syncwarp();
+                if (few && cnt < kk) {
+                    // the list ends with the first columns of -inf (or NaN), found among the first cnt + kk
+                    const int c0 = max(0, s.col(0)), need = kk - cnt;
+                    for (int i0 = 0, got = 0; i0 < n_el && got < need; i0 += 32) {
+                        const T* zr = reinterpret_cast<const T*>(s.base) - s.col(0);
+                        const bool on = i0 + lane < n_el && !(E::get(zr + c0 + min(i0 + lane, n_el - 1)) > -INFINITY);
+                        const uint32_t m = __ballot_sync(0xffffffffu, on);
+                        const int p = got + __popc(m & ((1u << lane) - 1u));
+                        if (on && p < need) s_cand[cnt + p] = top_key(-INFINITY, c0 + i0 + lane);
+                        got += __popc(m);
+                    }
+                    __syncwarp();
+                    if (lane == 0) *s_cnt = kk;
+                }
             }
         }
-        const int n_el = max(0, min(V, s.col(s.n)) - max(0, s.col(0))), kk = min(k, n_el);
         if (exact) exact_candidates(s, V, kk, n_el, s_cand, s_cnt, lane);
         __syncwarp();
         if (a.keys) {

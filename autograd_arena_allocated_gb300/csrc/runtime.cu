@@ -1798,10 +1798,14 @@ tt_status tt_op_embed_bwd(tt_ctx* c, tt_dtype dtype, const void* dx, const int32
     if (!live(c)) return TT_ERR_STALE;                    \
     if (current_device() != c->device) return fail(c, TT_ERR_STATE, "the context's device is not the current one");
 
+static bool misaligned(tt_dtype dtype, const void* a, const void* b = nullptr) {
+    return (((uintptr_t)a | (uintptr_t)b) & (dtype == TT_FP32 ? 3 : 1)) != 0;
+}
+
 tt_status tt_op_top_logits(tt_ctx* c, tt_dtype dtype, const void* logits, float* vals, int32_t* idx, float* lse, int M,
                            int V, int ld, int k, float tau) {
     TT_HEAD_PROLOGUE();
-    if (!logits || !vals || !idx || M <= 0 || V <= 0 || ld < V) return fail(c, TT_ERR_ARG, "top_logits: bad arguments");
+    if (!logits || !vals || !idx || M <= 0 || V <= 0 || ld < V || misaligned(dtype, logits)) return fail(c, TT_ERR_ARG, "top_logits: bad arguments");
     const char* why = list_refusal(dtype, V, k, tau);
     if (why) return fail(c, TT_ERR_ARG, "top_logits: %s", why);
     const size_t mark = c->off, sb = top_rows_scratch_bytes(dtype, M, V, k);
@@ -1812,7 +1816,7 @@ tt_status tt_op_top_logits(tt_ctx* c, tt_dtype dtype, const void* logits, float*
         ProfScope ps(c, PK_TOP, 0.0, (double)M * V * esize(dtype) + 8.0 * M * k);
         ok = launch_top_rows(op_launch(c), dtype, logits, ld, M, V, k, tau, vals, idx, lse, s);
     }
-    c->off = mark;
+    if (!c->capturing || c->oom) c->off = mark;  // a recording keeps its scratch: it is written at every replay
     if (!ok) return fail(c, TT_ERR_CUDA, "top_logits: launch failed");
     return op_epilogue(c, "top_logits");
 }
@@ -1821,7 +1825,7 @@ tt_status tt_op_distill(tt_ctx* c, tt_dtype dtype, const void* logits, const flo
                         const float* t_lse, const int32_t* targets, void* dlogits, float* row_loss, float* mean_loss,
                         int M, int V, int ld, int k, float alpha, float tau, float dscale) {
     TT_HEAD_PROLOGUE();
-    if (!logits || !row_loss || M <= 0 || V <= 0 || ld < V) return fail(c, TT_ERR_ARG, "distill: bad arguments");
+    if (!logits || !row_loss || M <= 0 || V <= 0 || ld < V || misaligned(dtype, logits, dlogits)) return fail(c, TT_ERR_ARG, "distill: bad arguments");
     const char* why = distill_refusal(dtype, t_vals, t_idx, targets, V, k, alpha, tau);
     if (why) return fail(c, TT_ERR_ARG, "distill: %s", why);
     {
@@ -1837,7 +1841,8 @@ tt_status tt_op_beam_select(tt_ctx* c, tt_dtype dtype, const void* logits, const
                             int32_t* parent, int32_t* token, float* out_scores, int32_t* out_done, int B, int K, int V,
                             int ld, int n, int eos) {
     TT_HEAD_PROLOGUE();
-    if (!logits || !scores || !parent || !token || !out_scores || B <= 0 || V <= 0 || ld < V)
+    if (!logits || !scores || !parent || !token || !out_scores || B <= 0 || V <= 0 || ld < V ||
+        misaligned(dtype, logits))
         return fail(c, TT_ERR_ARG, "beam_select: bad arguments");
     if (K < 1 || K > TT_BEAM_MAX || n < 1 || n > 2 * TT_BEAM_MAX || (long long)n > (long long)K * V)
         return fail(c, TT_ERR_ARG, "beam_select: K must be 1 .. TT_BEAM_MAX, n 1 .. min(2 TT_BEAM_MAX, K V)");
@@ -1856,7 +1861,7 @@ tt_status tt_op_beam_select(tt_ctx* c, tt_dtype dtype, const void* logits, const
         ok = launch_beam_select(op_launch(c), dtype, logits, ld, scores, done, parent, token, out_scores, out_done, B, K,
                                 V, n, eos, s, nullptr, nullptr, 0, nullptr);
     }
-    c->off = mark;
+    if (!c->capturing || c->oom) c->off = mark;  // a recording keeps its scratch: it is written at every replay
     if (!ok) return fail(c, TT_ERR_CUDA, "beam_select: launch failed");
     return op_epilogue(c, "beam_select");
 }

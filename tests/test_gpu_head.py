@@ -492,6 +492,22 @@ def test_beam_select(ctx, dtype, B, K, V, ld, n, offset):
     check_select(ctx, dtype, z, scores, done, K, V, n, 0)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("allowed", [0, 1, 5, 40])
+def test_beam_select_of_few_allowed_tokens(ctx, dtype, allowed):
+    """A vocabulary masked down to a few tokens (decoding after a grammar):
+    the candidates beyond them are the first masked columns."""
+    B, K, V, n = 3, 4, 50257, 8
+    z = make_logits(dtype, B * K, V, V + 1, 75)
+    keep = torch.randperm(V, generator=gen(76), device=DEV)[:allowed]
+    hide = torch.ones(V, dtype=torch.bool, device=DEV)
+    hide[keep] = False
+    z[:, :V][:, hide] = -INF
+    scores = -1.0 - torch.rand(B, K, generator=gen(77), device=DEV)
+    check_select(ctx, dtype, z, scores, None, K, V, n, -1)
+    check_top(ctx, dtype, z, V, 64)
+
+
 @pytest.mark.parametrize("V", [65, 6000, 50257])
 def test_beam_select_ties_and_masks(ctx, V):
     """Equal beams, whole-number logits (many ties), masked vocabularies, slots
@@ -643,6 +659,10 @@ def test_refusals(ctx):
         ctx._check(api.lib().tt_op_top_logits(ctx.h, 7, z.data_ptr(), vals.data_ptr(), idx.data_ptr(), None, M, V, V, k,
                                               1.0))
     assert ctx.launches == n0
+    for call, name in ((top, "logits"), (dis, "logits"), (dis, "dlogits"), (sel, "logits")):
+        with pytest.raises(api.TTError, match="TT_ERR_ARG"):  # off an element's boundary
+            call(**{name: z.data_ptr() + 2})
+    assert ctx.launches == n0
     with pytest.raises(ValueError, match="contiguous"):
         top(logits=make_logits("fp32", M, V, 2 * V, 1)[:, ::2])
     small = api.Context(256)  # 4 rows of 50 entries need 1632 bytes
@@ -692,6 +712,29 @@ def test_recorded_calls_replay(ctx):
         c.sync()
         for a, b in zip(got, (par, tok, sc, state, tv, ti, tl, row, mean, d)):
             assert torch.equal(a, b)
+
+
+def test_a_recording_keeps_its_scratch(ctx):
+    """What is allocated after a recording is not written over by its replay."""
+    V = 50257
+    z = make_logits("fp32", 8, V, V, 97)
+    scores = torch.zeros(2, 4, device=DEV)
+    par, tok = torch.empty(2, 4, dtype=torch.int32, device=DEV), torch.empty(2, 4, dtype=torch.int32, device=DEV)
+    sc, tv, ti = torch.empty(2, 4, device=DEV), torch.empty(8, 9, device=DEV), torch.empty(8, 9, dtype=torch.int32, device=DEV)
+    with api.Context(16 << 20, stream=torch.cuda.Stream().cuda_stream) as c:
+        def calls():
+            c.beam_select("fp32", z, scores, None, par, tok, sc, None, 2, 4, V, V, 4)
+            c.top_logits("fp32", z, tv, ti, None, 8, V, V, 9)
+
+        torch.cuda.synchronize()
+        c.record(calls)
+        node = c.tensor(1 << 20)
+        node.fill(np.full(1 << 20, 3.0, dtype=np.float32))
+        c.replay(2)
+        assert np.all(node.numpy() == 3.0)
+        rp, rt, _, _ = ref_select(z, scores, None, 4, V, 4, -1)
+        assert torch.equal(par, rp) and torch.equal(tok, rt)
+        assert np.array_equal(ti.cpu().numpy(), ref_top(z, V, 9, 1.0)[1])
 
 
 def test_two_contexts_at_once(ctx):
