@@ -139,18 +139,22 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, 
 // A row with more candidates than there is room for (ties: few different
 // values) is gone through bit by bit from memory.
 constexpr int TS_WARPS = 8;                 // most warps of a CTA
-constexpr int TS_TASKS = 3648;              // rows, or parts, that are worked on at once: 24 warps on each of 152 SMs
+constexpr int TS_CTAS = 3;                  // CTAs of an SM
+constexpr int TS_TASKS = 152 * TS_CTAS * TS_WARPS;  // rows, or parts, that are worked on at once
 constexpr int TS_PARTS = 64;                // most parts of a row
 constexpr int TS_JOIN = 2048;               // most entries of a row's parts' lists
 constexpr int TS_BLOCKS = 64;               // most blocks of a lane
 constexpr int TS_U = 4;                     // granules of a lane in a stage of the ring
 constexpr int TS_RING = 2 * TS_U * 32 * 16;  // two stages
 
-// candidates, and blocks that hold them: 24 warps of an SM have room for their
-// rings with the smaller number, 20 with the larger
+// room for candidates, and for blocks that hold them
 __host__ __device__ constexpr int stream_cand(int k) { return k <= 64 ? 160 : 256; }
+// the candidates take the place of the blocks' maxima once these are done with
+__host__ __device__ constexpr int stream_blocks(int words, int k) {
+    return words * 128 > stream_cand(k) * 8 ? words * 128 : stream_cand(k) * 8;
+}
 __host__ __device__ constexpr int stream_warp_smem(int words, int k) {
-    return TS_RING + words * 128 + stream_cand(k) * (8 + 2) + 16;
+    return TS_RING + stream_blocks(words, k) + align16(stream_cand(k) * 2) + 16;
 }
 
 // A lane's block maxima, as the counting below reads them: pairs for the 16-bit types.
@@ -225,7 +229,7 @@ template <int N> __device__ __forceinline__ float pick(const f2 (&e)[N], int l) 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(TS_WARPS * 32, 3)
+__global__ void __launch_bounds__(TS_WARPS * 32, TS_CTAS)
 k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
     // no early trigger: the next kernel's CTAs, resident and waiting, take the room of this grid's last ones
     // (a selection step of 256 fp32 rows 93 us with it, 34 us without)
@@ -237,9 +241,9 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
     const int TS_CAND = stream_cand(a.k);
     char* sm = smem + (threadIdx.x >> 5) * stream_warp_smem(words, a.k);
     Blocks<T> blocks{reinterpret_cast<uint32_t*>(sm + TS_RING)};
-    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + TS_RING + words * 128);
-    auto* s_hit = reinterpret_cast<uint16_t*>(s_cand + TS_CAND);
-    int* s_cnt = reinterpret_cast<int*>(s_hit + TS_CAND);
+    auto* s_cand = reinterpret_cast<unsigned long long*>(sm + TS_RING);
+    auto* s_hit = reinterpret_cast<uint16_t*>(sm + TS_RING + stream_blocks(words, a.k));
+    int* s_cnt = reinterpret_cast<int*>(sm + stream_warp_smem(words, a.k) - 16);
     const int warps = blockDim.x >> 5, P = a.P;
     const long long tasks = (long long)a.M * P, stride = (long long)gridDim.x * warps;
     const bool want = a.want;
@@ -1293,7 +1297,7 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     const int warps = (int)std::min<long long>(TS_WARPS, std::max<long long>(1, tasks / L.num_sms));
     p.smem = (size_t)warps * stream_warp_smem(words, a.k);
     p.threads = warps * 32;
-    const long long per_sm = std::min<long long>(24 / warps, (long long)(SMEM_SM / (p.smem + 1024)));
+    const long long per_sm = std::min<long long>(TS_CTAS * TS_WARPS / warps, (long long)(SMEM_SM / (p.smem + 1024)));
     p.ctas = (int)std::min((tasks + warps - 1) / warps, L.num_sms * per_sm);
     launch_rows(L, k_top_stream<T>, p, (const T*)z, a, ub_log, words);
     return true;
