@@ -5,7 +5,7 @@
 //   k_top_join      the parts' lists of a row as one
 //   k_distill       distillation from a teacher's top logits: loss and
 //                   gradient of a row
-//   k_distill_short the same for rows of up to 512 logits
+//   k_distill_short the same for rows of up to 2048 logits
 //   k_row_mean      the mean of the row losses (fixed order)
 //
 // The kernels read a row of V logits from memory once, in the storage type
@@ -124,9 +124,9 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, 
 
 // A warp takes a row, or a part of one where there are fewer rows than the SMs
 // hold warps (the parts' lists are then joined, by k_top_join or by the beams'
-// merge).  The row
-// streams through a ring of the warp's own, without a barrier, and what stays
-// of it is the largest value of every block of UB granules of a lane.  The
+// merge).  The row streams through a ring of the warp's own, without a barrier,
+// and what stays of it is the largest value of every block of UB granules of a
+// lane.  The
 // k-th largest of those is the threshold; the few blocks at or above it (k,
 // and those that tie) are read again from memory, and their elements at or
 // above it are ranked.  A lane's four granules of a stage are neighbours in
@@ -138,7 +138,11 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, 
 // for a selection step of 256 fp32 rows.
 // A row with more candidates than there is room for (ties: few different
 // values) is gone through bit by bit from memory.
+// 32768 rows of 50257 16-bit logits, k = 64: 624 us, 5.3 TB/s, 78% of the
+// measured copy rate; what is left is instructions (15 thousand a row, 5
+// thousand of them for the exponentials' sum).
 constexpr int TS_WARPS = 8;                 // most warps of a CTA
+// (28 warps of an SM at 72 registers: 642 us; 18 with a ring twice as deep: 686 us)
 constexpr int TS_CTAS = 3;                  // CTAs of an SM
 constexpr int TS_TASKS = 152 * TS_CTAS * TS_WARPS;  // rows, or parts, that are worked on at once
 constexpr int TS_PARTS = 64;                // most parts of a row
@@ -513,7 +517,7 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// The lists of a row's parts as one, a warp a row.
+// The lists of a row's parts as one, a warp a row (300 rows of 12 parts, k = 10: under 8 us).
 constexpr int TJ_WARPS = 2;
 
 __global__ void __launch_bounds__(TJ_WARPS * 32) k_top_join(const TopArgs a) {
@@ -546,6 +550,18 @@ __global__ void __launch_bounds__(TJ_WARPS * 32) k_top_join(const TopArgs a) {
 // written over.  Where q_r is needed (t_lse) the listed logits are first
 // replaced by -inf in the on-chip copy, so that q_r is summed without them and
 // not as a difference; their own exponentials are added from the list.
+//
+// What has to be moved is the row in and the gradient out.  A row of 50257
+// 16-bit logits (100 KB) is held by one CTA, two CTAs an SM, so that one's
+// passes run beside the other's loads; a longer one is cut over a cluster.  At
+// two exponentials an element and pass the special-function unit (32 a cycle
+// and SM) would take 3.1 of the 4.5 us that such a row's traffic takes an SM,
+// hence the powers (Sums).  32768 rows, k = 64, tau = 2, with hard labels:
+// 1116 us, 5.9 TB/s, 87% of the measured copy rate (75% with t_lse, whose
+// replacement holds up the first pass); then the rows' own chains (barrier,
+// merge, coefficients: about 4 us of a row's 10) are what is left.  999 rows of
+// 50257 fp32 logits, two CTAs a row: 92 us, 64%, of which 6% are the last
+// round's empty places.
 struct DistillArgs {
     const float* t_vals;
     const int32_t* t_idx;
@@ -1040,13 +1056,15 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
 // Short rows (a warp holds one in its registers, lane l the columns l + 32 e):
 // the same sums, with the list spread over the columns, ln p_j at column i_j in
 // shared memory, so that every column knows whether it is listed and nothing
-// is written twice.  By the kernel above a row of 65 took as long as its list
-// handling: 38 us for 16384 rows.
+// is written twice.  A row takes a few hundred instructions whatever its
+// length, which is what bounds the shortest: 16384 rows of 65 with k = 8 take
+// 15.5 us (38 us as a warp's form of the kernel above, whose list handling is
+// made for long rows), 30400 rows of 1024 102 us (401 us a CTA a row).
 constexpr int DS_WARPS = 4;
 constexpr uint32_t DS_UNLISTED = 0x7FC0DEADu;  // a NaN that no arithmetic makes
 
 template <typename T, int E>
-__global__ void __launch_bounds__(DS_WARPS * 32)
+__global__ void __launch_bounds__(DS_WARPS * 32, E <= 4 ? 8 : E <= 16 ? 6 : E <= 32 ? 5 : 3)
 k_distill_short(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
     __shared__ uint32_t s_all[DS_WARPS][32 * E];
@@ -1187,7 +1205,7 @@ k_distill_short(const T* z, T* dz, const DistillArgs a) {
 }
 
 // mean of M row losses: each thread adds rows t, t + 1024, ..., the threads'
-// sums meet in a fixed tree
+// sums meet in a fixed tree (3 us for 32768)
 __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row_loss, int M, float* __restrict__ out,
                                                    int* flags) {
     pdl_enter();
@@ -1315,6 +1333,9 @@ template <typename T> bool distill(const Launch& L, const void* z, void* dz, Dis
     const int k = a.k;
     if (a.V <= 128) return distill_short<T, 4>(L, z, dz, a);
     if (a.V <= 512) return distill_short<T, 16>(L, z, dz, a);
+    if (a.V <= 1024) return distill_short<T, 32>(L, z, dz, a);
+    // (64 registers of a row a lane: 30400 rows of 2048 215 us, 20 rows 14 us; a CTA a row 450 and 9 us)
+    if (a.V <= 2048 && a.M >= 2 * L.num_sms) return distill_short<T, 64>(L, z, dz, a);
     if (!make_plan(p, L.num_sms, a.M, row_granules<T>(z, a.ld, a.V), [k](int Gs, int nbuf, bool cl) {
             return (size_t)DistillLayout(Gs, nbuf, k, Elem<T>::EPG, cl).total;
         }))

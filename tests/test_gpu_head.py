@@ -299,6 +299,8 @@ DISTILL_CASES = [  # M, V, ld, k, offset, alpha, tau, rest
     (3, 50257, 50257, 64, 3, 0.25, 2.0, True), (160, 50257, 50304, 16, 0, 1.0, 2.0, False),
     (5, 32000, 32000, 128, 0, 0.5, 1.0, True), (2, 151936, 151936, 20, 0, 0.5, 2.0, True),
     (1, 262144, 262147, 50, 1, 0.8, 1.3, True),
+    (320, 2048, 2048, 128, 0, 0.5, 2.0, True), (310, 1500, 1503, 16, 1, 0.4, 1.3, False), (40, 700, 704, 20, 0, 1.0, 3.0, True),
+    (320, 9000, 9000, 30, 0, 0.5, 4.0, False), (161, 40001, 40001, 12, 1, 0.6, 3.0, True),
 ]
 
 
