@@ -27,11 +27,14 @@ using namespace head;
 // Beams with the same score and the same list are the same hypothesis as far
 // as this step goes, and their candidates have to tie; but a row's
 // log-sum-exp depends in its last bits on how the row lies in memory.  Such a
-// beam takes the log-sum-exp of the first one it equals.
+// beam takes the log-sum-exp of the first one it equals, where the two are
+// within LSE_EPS: the rounding of arguments of up to 20 log2(e) by half a step
+// (1.3e-6) and of a few hundred additions, whatever the logits' own size is.
 //
 // A step's time is the two kernels' latency: the lists of 4 rows in 32 parts
 // and this merge take 12 us, those of 256 fp32 rows (51 MB) in 14 parts 28 us.
 constexpr int BM_THREADS = 256;
+constexpr double LSE_EPS = 1e-5;
 
 // Scores are compared as whole numbers: the 64-bit float unit is so narrow that
 // 128 candidates' comparisons took longer than all the rest.
@@ -89,7 +92,7 @@ k_beam_merge(const unsigned long long* __restrict__ keys, const float2* __restri
     }
     if (tid > 0 && tid < K && s_as[tid] >= 0) {
         for (int j = 0; j < tid; j++) {
-            if (s_sc[j] != s_sc[tid] || s_as[j] < 0 || !(fabs(s_lse[j] - s_lse[tid]) <= 1e-6 * (1.0 + fabs(s_lse[j])))) continue;
+            if (s_sc[j] != s_sc[tid] || s_as[j] < 0 || !(fabs(s_lse[j] - s_lse[tid]) <= LSE_EPS)) continue;
             int same = 0;
             while (same < kk && s_j[j * kk + same] == s_j[tid * kk + same]) same++;
             if (same == kk) {
@@ -105,13 +108,13 @@ k_beam_merge(const unsigned long long* __restrict__ keys, const float2* __restri
         double c = -INFINITY;
         int v = r;
         if (s_as[j] < 0) {
-            if (s > -INFINITY) {
+            if (isfinite(s)) {
                 v = r == 0 ? eos : (r - 1 < eos ? r - 1 : r);
                 if (r == 0) c = (double)s;
             }
         } else {
             const double l = s_lse[s_as[j]];
-            if (isfinite(l) && s > -INFINITY) {
+            if (isfinite(l) && isfinite(s)) {
                 v = key_col(s_j[i]);
                 c = (double)s + ((double)head::value_of((uint32_t)(s_j[i] >> 32)) - l);
             }

@@ -1211,7 +1211,7 @@ __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row
     pdl_enter();
     __shared__ float s_w[32];
     float s = 0.0f;
-    for (int i = threadIdx.x; i < M; i += 1024) s += row_loss[i];
+    for (long long i = threadIdx.x; i < M; i += 1024) s += row_loss[i];
     s = warp_sum(s);
     if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = s;
     __syncthreads();
@@ -1323,7 +1323,7 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
 
 template <typename T, int E> bool distill_short(const Launch& L, const void* z, void* dz, const DistillArgs& a) {
     L.count();
-    const unsigned ctas = (unsigned)std::min((a.M + DS_WARPS - 1) / DS_WARPS, L.num_sms * 12);
+    const unsigned ctas = (unsigned)std::min((a.M - 1) / DS_WARPS + 1, L.num_sms * 12);
     launch_k(L, k_distill_short<T, E>, dim3(ctas), dim3(DS_WARPS * 32), 0, (const T*)z, (T*)dz, a);
     return true;
 }

@@ -92,8 +92,6 @@ template <> struct Elem<float> {
     static __device__ __forceinline__ float top(Max m) { return m; }
     static __device__ __forceinline__ float bottom(Max m) { return m; }
     static __device__ __forceinline__ float value(Max m) { return fmaxf(m, -INFINITY); }
-    static __device__ __forceinline__ bool above(Max m, Max t) { return m > t; }       // any of m > t
-    static __device__ __forceinline__ bool at_least(Max m, Max t) { return m >= t; }  // any of m >= t
 };
 template <typename T, typename P, typename Cvt> struct Elem16 {
     static constexpr int EPG = 8;
@@ -126,8 +124,6 @@ template <typename T, typename P, typename Cvt> struct Elem16 {
     static __device__ __forceinline__ float value(Max m) {
         return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
     }
-    static __device__ __forceinline__ bool above(Max m, Max t) { return !__hble2(m, t); }     // or a NaN pair
-    static __device__ __forceinline__ bool at_least(Max m, Max t) { return !__hblt2(m, t); }  // or a NaN pair
 };
 struct CvtBf {
     static __device__ __forceinline__ __nv_bfloat162 pair(float a, float b) { return __floats2bfloat162_rn(a, b); }

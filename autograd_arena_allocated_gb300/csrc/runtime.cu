@@ -1163,7 +1163,7 @@ tt_status tt_ctx_sync(tt_ctx* c) {
     if (flags[FLAG_TIMEOUT])
         return fail(c, TT_ERR_TIMEOUT, "a device-side wait timed out (site 0x%x)", (unsigned)flags[FLAG_SITE]);
     if (flags[FLAG_BAD_TOKEN]) return fail(c, TT_ERR_ARG, "token id out of range");
-    if (flags[FLAG_NONFINITE]) return fail(c, TT_ERR_NONFINITE, "non-finite loss");
+    if (flags[FLAG_NONFINITE]) return fail(c, TT_ERR_NONFINITE, "non-finite loss or logits");
     return TT_OK;
 }
 
@@ -1342,6 +1342,8 @@ tt_status tt_gpt2_step_distill(tt_ctx* c, const void* params, float* grads, cons
     if (c->has_model) {
         const char* why = distill_refusal(c->cfg.dtype, t_vals, t_idx, targets, c->cfg.V, k, alpha, tau);
         if (why) return fail(c, TT_ERR_ARG, "step_distill: %s", why);
+        if (is_host_pointer(t_vals) || is_host_pointer(t_idx) || (t_lse && is_host_pointer(t_lse)))
+            return fail(c, TT_ERR_ARG, "step_distill: the lists must be device memory");
     }
     return step_with(c, params, grads, tokens, targets, &t, B, T, flags, loss_scale, loss);
 }
@@ -1464,6 +1466,8 @@ tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* token
     if (c->capturing) return fail(c, TT_ERR_STATE, "GPT-2 calls cannot be recorded");
     if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
     if (!params || !tokens || !vals || !idx) return fail(c, TT_ERR_ARG, "NULL parameter, token or list pointer");
+    if (is_host_pointer(vals) || is_host_pointer(idx) || (lse && is_host_pointer(lse)))
+        return fail(c, TT_ERR_ARG, "top_logits: the lists must be device memory");
     if (B <= 0 || T <= 0 || T > c->cfg.maxT)
         return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
     const tt_gpt2_config& m = c->cfg;

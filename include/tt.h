@@ -64,7 +64,8 @@ typedef enum { TT_FP32 = 0, TT_BF16 = 1, TT_FP16 = 2 } tt_dtype;
  * activation gradients underflow unless the loss is scaled
  * (tt_gpt2_step_ex's loss_scale).  The half step runs on the SIMT kernels
  * (the tensor-core kernels are bf16).  tt_gpt2_eval takes it too; the
- * op-level calls and tt_gpt2_generate take TT_FP32 and TT_BF16 only. */
+ * generating calls take TT_FP32 and TT_BF16 only, and so do the op-level calls
+ * but those over lists of logits (tt_ops.h). */
 typedef struct {
     int L, C, H, V, maxT;
     tt_dtype dtype;

@@ -15,7 +15,6 @@ of fp32):
    relative errors of the terms that it is made of.
 The functions below write these out."""
 import math
-import os
 
 import numpy as np
 import pytest
@@ -406,6 +405,59 @@ def test_distill_own_list_gives_nothing(ctx):
     assert float(row.abs().max()) <= tol and float(d.float().abs().max()) <= tol
 
 
+def test_distill_of_the_most_rows(ctx):
+    """2^31 - 1 rows of one logit: a softmax over one column has no loss."""
+    M = 2 ** 31 - 1
+    z = torch.ones(M, 1, dtype=torch.float16, device=DEV)
+    vals = torch.ones(M, 1, device=DEV)
+    idx = torch.zeros(M, 1, dtype=torch.int32, device=DEV)
+    row = torch.full((M,), 7.0, device=DEV)
+    mean = torch.full((1,), 7.0, device=DEV)
+    ctx.reset()
+    ctx.distill("fp16", z, vals, idx, None, None, None, row, mean, M, 1, 1, 1, 1.0, 2.0, 1.0)
+    ctx.sync()
+    assert float(row.max()) == 0.0 and float(row.min()) == 0.0 and float(mean) == 0.0
+    del z, vals, idx, row
+    torch.cuda.empty_cache()
+
+
+def test_rows_past_32_bits(ctx):
+    """More than 2^31 logits: the last rows of each operator over them."""
+    V, ld, k = 50257, 50304, 8
+    M = 2 ** 31 // ld + 40
+    z = torch.zeros(M, ld, dtype=torch.bfloat16, device=DEV)
+    last = 64
+    z[-last:] = make_logits("bf16", last, V, ld, 21)
+    tail = z[-last:].clone()
+    vals, idx = torch.empty(M, k, device=DEV), torch.empty(M, k, dtype=torch.int32, device=DEV)
+    lse = torch.empty(M, device=DEV)
+    ctx.reset()
+    ctx.top_logits("bf16", z, vals, idx, lse, M, V, ld, k, 1.0)
+    ctx.sync()
+    rv, ri, rl = ref_top(tail, V, k, 1.0)
+    assert np.array_equal(idx[-last:].cpu().numpy(), ri) and np.array_equal(vals[-last:].double().cpu().numpy(), rv)
+    assert bool(((lse[-last:].double() - rl).abs() <= lse_tol(rl, 30.0)).all())
+    # the choice of the last sequence
+    B, K = M // 4, 4
+    scores = -torch.rand(B, K, generator=gen(22), device=DEV)
+    par, tok = torch.empty(B, K, dtype=torch.int32, device=DEV), torch.empty(B, K, dtype=torch.int32, device=DEV)
+    sc = torch.empty(B, K, device=DEV)
+    ctx.beam_select("bf16", z, scores, None, par, tok, sc, None, B, K, V, ld, K, -1)
+    ctx.sync()
+    rows = z[(B - 8) * K:B * K]
+    rp, rt, _, _ = ref_select(rows, scores[-8:], None, K, V, K, -1)
+    assert torch.equal(par[-8:], rp) and torch.equal(tok[-8:], rt)
+    # a model's own whole list gives (nearly) no loss; in place
+    row = torch.full((M,), 7.0, device=DEV)
+    ctx.distill("bf16", z, vals, idx, lse, None, z, row, None, M, V, ld, k, 1.0, 1.0, 1.0)
+    ctx.sync()
+    tol = (2 * DEPTH + 200) * U * 40
+    assert float(row[-last:].abs().max()) <= tol and float(z[-last:, :V].float().abs().max()) <= tol
+    assert float(z[-last:, V:].float().abs().max()) == 0.0
+    del z
+    torch.cuda.empty_cache()
+
+
 def test_distill_flags(ctx):
     M, V, k = 4, 300, 5
     z = make_logits("fp32", M, V, V, 51)
@@ -547,6 +599,35 @@ def test_beam_select_in_place_and_far_scores(ctx):
     ctx.sync()
     assert torch.equal(par, rp) and torch.equal(tok, rt) and torch.equal(done, rd)
     assert bool(((scores.double() - rs).abs() <= 1e-4 * 3 + U * rs.abs() * 1.01).all())
+
+
+def test_beam_select_of_nearly_equal_beams(ctx):
+    """Two beams with the same score and the same best tokens, whose
+    distributions differ by 3e-4 under logits of a thousand: no tie."""
+    V, n = 1000, 4
+    z = torch.full((2, V), 1000.0, device=DEV)
+    z[:, 5] = 1010.0
+    z[:, 9] = 1009.0
+    z[1, 100:110] = 900.0
+    check_select(ctx, "fp32", z, torch.full((1, 2), -7.0, device=DEV), None, 2, V, n, -1)
+
+
+@pytest.mark.parametrize("over", [False, True])
+def test_beam_select_of_scores_that_are_not_finite(ctx, over):
+    """Such beams offer -inf only, finished or not."""
+    B, K, V, n = 2, 4, 700, 4
+    z = make_logits("fp32", B * K, V, V, 84)
+    scores = torch.tensor([[INF, -1.0, -2.0, math.nan], [-3.0, math.nan, INF, -2.5]], device=DEV)
+    done = torch.full((B, K), int(over), dtype=torch.int32, device=DEV)
+    par = torch.empty(B, n, dtype=torch.int32, device=DEV)
+    tok, sc = par.clone(), torch.empty(B, n, device=DEV)
+    ctx.reset()
+    ctx.beam_select("fp32", z, scores, done, par, tok, sc, None, B, K, V, V, n, 3)
+    ctx.sync()
+    rp, rt, rs, _ = ref_select(z, torch.where(torch.isfinite(scores), scores, -INF), done, K, V, n, 3)
+    assert torch.equal(par, rp) and torch.equal(tok, rt)
+    fin = torch.isfinite(rs)
+    assert torch.equal(fin, torch.isfinite(sc)) and not bool(torch.isnan(sc).any() | (sc == INF).any())
 
 
 def check_reorder(ctx, state, parents, first, count):
@@ -922,6 +1003,25 @@ def test_step_distill_refusals(ctx):
         ctx.step_distill(**{**base, "targets": t2})
     ctx.reset()
     assert math.isfinite(ctx.step_distill(**base))
+
+
+def test_model_lists_in_host_memory_are_refused(ctx):
+    sh = synth.WORKLOADS["tiny_fp32"].shape
+    p = synth.init_params(sh)
+    _, w = device_params(ctx, sh, p, "fp32")
+    B, T, k = 2, 8, 4
+    tok, tgt = synth.token_stream(B, T, sh.V, "uniform")
+    lists = dict(zip(("vals", "idx", "lse"), make_lists(B * T, sh.V, k, 1)))
+    grads = torch.empty(p.size, device=DEV)
+    ctx.reset()
+    n0 = ctx.launches
+    for name in lists:
+        a = {**lists, name: lists[name].cpu()}
+        with pytest.raises(api.TTError, match="device memory"):
+            ctx.step_distill(w, grads, tok, tgt, a["vals"], a["idx"], a["lse"], k, 0.5, 1.0, B, T)
+        with pytest.raises(api.TTError, match="device memory"):
+            ctx.top_logits_of(w, tok, B, T, k, a["vals"], a["idx"], a["lse"])
+    assert ctx.launches == n0
 
 
 def ref_beam(oracle, sh, po, prompt, n_new, K, eos):
