@@ -1,4 +1,4 @@
-// head_row.cuh -- what the list kernels (head.cu, beam.cu) share: a row of
+// head_row.cuh -- what the list kernels (head.cu, distill.cu, beam.cu) share: a row of
 // logits in granules, its sums of exponentials, and lists of its columns.
 //
 // A row is cut into granules of 16 bytes on 16-byte boundaries of memory.
@@ -16,9 +16,13 @@
 
 #include "tt_internal.h"
 
+#include <algorithm>
+
 namespace tt {
 namespace head {
 
+constexpr int LIST_MAX = TT_TOP_MAX;
+__host__ __device__ constexpr int align16(int n) { return (n + 15) & ~15; }
 constexpr float LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -273,6 +277,12 @@ template <typename T> __device__ __noinline__ uint4 edge_granule(const T* row, i
 #pragma unroll
     for (int j = 0; j < Elem<T>::EPG; j++) x.e[j] = c0 + j >= 0 && c0 + j < V ? row[c0 + j] : Elem<T>::put(-INFINITY);
     return x.u;
+}
+
+// Slot i of the slice, read from memory.
+template <typename T> __device__ __forceinline__ uint4 granule(const Slice<T>& s, int i, int V) {
+    return s.inner(i) ? reinterpret_cast<const uint4*>(s.base)[i]
+                      : edge_granule(reinterpret_cast<const T*>(s.base) - s.col(0), s.col(i), V);
 }
 
 // ------------------------------------------------------------ sums of exponentials
@@ -575,6 +585,55 @@ __device__ __forceinline__ void join_parts(const float2* parts, int P, float c, 
         R = m;
     }
     merge(R, s, c);
+}
+
+// ------------------------------------------------------------ launch
+// How a kernel's CTAs are laid out; for distillation also the CTAs that share
+// a row, their slices, and whether two rows of a CTA are on chip at once.
+struct Plan {
+    int cs = 1, nbuf = 1, Gs = 0, ctas = 0, threads = 0;
+    size_t smem = 0;
+};
+
+constexpr size_t SMEM_CTA = 231424;  // 226 KB, and 1 KB for what is not dynamic
+constexpr size_t SMEM_SM = 233472;   // 228 KB, of which each CTA takes 1 KB more than its own
+constexpr size_t SMEM_HALF = SMEM_SM / 2 - 1024;
+
+template <typename K> bool allow_smem(PerDevice& attr, K kern) {
+    return attr.once([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_CTA) == cudaSuccess;
+    });
+}
+
+template <typename... KA, typename... A>
+void launch_rows(const Launch& L, void (*kern)(KA...), const Plan& p, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    cfg.blockDim = dim3((unsigned)p.threads);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute at[2];
+    unsigned n = 0;
+    if (L.pdl) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (p.cs > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = (unsigned)p.cs;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        n++;
+    }
+    cfg.attrs = at;
+    cfg.numAttrs = n;
+    L.count();
+    cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+
+// granules of a row, for the worst place of its start
+template <typename T> int row_granules(const void* z, long long ld, int V) {
+    const bool aligned = ((uintptr_t)z & 15) == 0 && ld * (long long)sizeof(T) % 16 == 0;
+    return (int)(((aligned ? 0 : 16 - (int)sizeof(T)) + (long long)V * (int)sizeof(T) + 15) / 16);
 }
 
 }  // namespace head

@@ -125,7 +125,7 @@ tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int
 #define TT_TOP_MAX 128  /* longest list of a row */
 #define TT_BEAM_MAX 32  /* most beams of a sequence */
 #define TT_TOP_SCRATCH_BYTES (4u << 20) /* most arena scratch of tt_op_top_logits */
-#define TT_ROW_BYTES_MAX 1600000  /* most bytes of the V logits of a row (a row is held on chip) */
+#define TT_ROW_BYTES_MAX 1600000  /* most bytes of the V logits of a row (few rows are held on chip) */
 
 /* The k largest logits of each row, in descending order, equal ones by
  * ascending column (-0 equals +0):

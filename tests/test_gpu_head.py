@@ -319,6 +319,93 @@ def test_distill(ctx, dtype, M, V, ld, k, offset, alpha, tau, rest):
     assert none is None and torch.equal(row, r3)
 
 
+DISTILL_STREAMED = [  # rows in such numbers that they are not held on chip
+    (420, 2049, 2049, 128, 0, 0.5, 2.0, True), (400, 2100, 2103, 9, 1, 1.0, 1.0, False),
+    (333, 4097, 4100, 50, 2, 0.4, 3.0, True), (310, 9001, 9088, 1, 0, 0.5, 4.0, True),
+    (700, 5000, 5000, 20, 0, 0.0, 2.0, False), (307, 10007, 10007, 64, 3, 0.7, 0.8, True),
+    (153, 60001, 60001, 64, 1, 0.5, 2.0, True), (160, 58000, 58112, 10, 0, 1.0, 2.5, False),
+    (80, 120011, 120013, 100, 0, 0.3, 1.0, True), (60, 151936, 151936, 16, 0, 0.5, 1.7, True),
+    (60, 300001, 300003, 7, 1, 0.5, 4.0, True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("M,V,ld,k,offset,alpha,tau,rest", DISTILL_STREAMED)
+def test_distill_of_many_rows(ctx, dtype, M, V, ld, k, offset, alpha, tau, rest):
+    test_distill(ctx, dtype, M, V, ld, k, offset, alpha, tau, rest)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,copies", [(3000, 40), (60000, 20)])
+@pytest.mark.parametrize("rest", [True, False])
+def test_distill_masks_of_many_rows(ctx, dtype, V, copies, rest):
+    """The rows of test_distill_masks in such numbers that they are not held on
+    chip; every copy of a row receives the same, bit by bit (its rows lie at
+    one place of a 16-byte line)."""
+    M, k, ld = 12, 20, V + 8
+    z = make_logits(dtype, M, V, ld, 21, pad=math.nan)
+    vals, idx, lse = make_lists(M, V, k, 22)
+    y = torch.randint(0, V, (M,), generator=gen(6), device=DEV, dtype=torch.int32)
+    idx[1] = -1
+    y[2] = -1
+    idx[3], y[3] = -1, -1
+    z[3] = math.nan
+    free = torch.ones(V, dtype=torch.bool, device=DEV)
+    free[idx[4].long().clamp(min=0)] = False
+    free[y[4].long()] = False
+    z[4, :V][free] = -INF
+    vals[5, 3:7] = -INF
+    z[6, :V] = 0.5
+    z[7, :V] += 3000.0
+    z[8, :V] = torch.finfo(TYPES[dtype]).min / 4
+    z[8, idx[8, 0].long()] = 1.0
+    vals[8, 1:] = -INF
+    z[8, y[8].long()] = 0.5
+    idx[9, 1:] = -1
+    lse[9] = vals[9, 0] / 2.0
+    lse[10] = 200.0
+    z[11, :V] = torch.finfo(TYPES[dtype]).min  # a whole row of the lowest value
+    many = z.repeat(copies, 1)
+    lists = tuple(t.repeat(copies, *([1] * (t.dim() - 1))) for t in (vals, idx, lse))
+    for alpha in (0.5, 1.0):
+        empty = (3,) if alpha < 1 else (1, 3)
+        skip = tuple(r + 12 * c for c in range(copies) for r in empty)
+        row, _, d = check_distill(ctx, dtype, many, V, lists, y.repeat(copies), alpha, 2.0, rest, skip_rows=skip)
+        assert bool((row.view(copies, M) == row[:M]).all())
+        assert bool((d.view(copies, M, ld) == d[:M]).all())
+
+
+@pytest.mark.parametrize("V,M", [(3000, 400), (70000, 160)])
+def test_distill_of_many_rows_other_alignment_and_flags(ctx, V, M):
+    """dlogits that starts at another place of a line; bad columns and labels."""
+    ld, k = V + 2, 9
+    z = make_logits("bf16", M, V, ld, 9, offset=1)
+    lists = make_lists(M, V, k, 2)
+    y = torch.randint(0, V, (M,), generator=gen(5), device=DEV, dtype=torch.int32)
+    _, _, want = run_distill(ctx, "bf16", z, V, lists, y, 0.5, 2.0, True)
+    for off in (0, 7):
+        buf = torch.full((M * ld + 72,), 55.0, dtype=torch.bfloat16, device=DEV)
+        d = buf[off:off + M * ld].view(M, ld)
+        row = torch.empty(M, device=DEV)
+        ctx.reset()
+        ctx.distill("bf16", z, *lists, y, d, row, None, M, V, ld, k, 0.5, 2.0, 1.0 / M)
+        ctx.sync()
+        assert torch.equal(d, want)
+        assert bool((buf[:off] == 55).all()) and bool((buf[off + M * ld:] == 55).all())
+    for name in ("column", "twice", "label"):
+        idx, t = lists[1].clone(), y.clone()
+        if name == "column":
+            idx[M - 1, 3] = V
+        elif name == "twice":
+            idx[M - 2, 4] = idx[M - 2, 1]
+        else:
+            t[M - 1] = -2
+        run_distill(ctx, "bf16", z, V, (lists[0], idx, lists[2]), t, 0.5, 1.0, True, sync=False)
+        with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+            ctx.sync()
+    check_distill(ctx, "bf16", z, V, lists, y, 0.5, 2.0, True)
+
+
 @pytest.mark.parametrize("V", [65, 5000, 50257])
 def test_distill_gradient_buffer_of_another_alignment(ctx, V):
     """logits and dlogits that start at different places of a 16-byte line."""
