@@ -60,7 +60,7 @@ k_beam_merge(const unsigned long long* __restrict__ keys, const float2* __restri
     auto* s_j = s_in + (P > 1 ? N * P : 0);                    // [K][kk]
     auto* s_s = s_j + N;                                       // [K][kk] scores, as whole numbers in order
     int* s_f = reinterpret_cast<int*>(s_s + N);                // [K][kk] j V + v
-    __shared__ unsigned long long s_key[BM_THREADS / 32][JOIN_ROOM];
+    __shared__ __align__(16) unsigned long long s_key[BM_THREADS / 32][JOIN_ROOM];
     __shared__ double s_lse[TT_BEAM_MAX];
     __shared__ float s_sc[TT_BEAM_MAX];
     __shared__ int s_as[TT_BEAM_MAX];  // the beam whose log-sum-exp counts; -1: a finished one

@@ -3,6 +3,7 @@
 //   k_top_stream    per row (or part of one) the k largest logits (ties: the
 //                   lowest column) and the log-sum-exp
 //   k_top_join      the parts' lists of a row as one
+//   k_top_short     the same of rows of up to 128 logits
 //
 // A row of V logits is read from memory once, in the storage type, but for the
 // few blocks that hold its largest (head_row.cuh); sums are fp32.
@@ -481,21 +482,69 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
         }
         if (exact) exact_candidates(s, V, kk, n_el, s_cand, s_cnt, lane);
         __syncwarp();
-        if (a.keys) {
-            unsigned long long* out = a.keys + task * k;
-            ranks(s_cand, *s_cnt, kk, [&](int r, unsigned long long key) { out[r] = key; });
-            for (int r = kk + lane; r < k; r += 32) out[r] = 0;
-            if (want && lane == 0) a.parts[task] = make_float2(R, sum);
-        } else {
-            ranks(s_cand, *s_cnt, kk, [&](int r, unsigned long long key) {
+        unsigned long long* const part = a.keys ? a.keys + task * k : nullptr;
+        ranks(s_cand, *s_cnt, kk, [&](int r, unsigned long long key) {
+            if (part) {
+                part[r] = key;
+            } else {
                 a.vals[task * k + r] = value_of((uint32_t)(key >> 32));
                 a.idx[task * k + r] = key_col(key);
-            });
-            if (want && lane == 0) a.lse[task] = (float)lse_of(R, sum, a.inv_tau);
+            }
+        });
+        if (part)
+            for (int r = kk + lane; r < k; r += 32) part[r] = 0;
+        if (want && lane == 0) {
+            if (part) a.parts[task] = make_float2(R, sum);
+            else a.lse[task] = (float)lse_of(R, sum, a.inv_tau);
         }
         __syncwarp();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Rows of up to 32 E logits: a warp holds one, lane l the columns l + 32 e, and
+// sorts it.  What a row takes is the sort's instructions (E = 4: about 800):
+// 30000 rows of 100 SHORT_US, 65 and 166 us (k = 10, 64) by the kernel above,
+// whose ring, threshold and second read are made for long rows.
+constexpr int TH_WARPS = 4;
+
+template <typename T, int E>
+__global__ void __launch_bounds__(TH_WARPS * 32) k_top_short(const T* __restrict__ z, const TopArgs a) {
+    pdl_enter();
+    const int lane = threadIdx.x & 31, k = a.k, V = a.V;
+    const float ct = LOG2E * a.inv_tau;
+    for (long long row = blockIdx.x * (long long)TH_WARPS + (threadIdx.x >> 5); row < a.M;
+         row += gridDim.x * (long long)TH_WARPS) {
+        const T* zr = z + row * a.ld;
+        float v[E];
+        unsigned long long x[E];
+        float R = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const int c = lane + 32 * e;
+            v[e] = c < V ? Elem<T>::get(zr + c) : -INFINITY;
+            x[e] = c < V ? top_key(v[e], c) : 0ull;
+            R = fmaxf(R, v[e]);
+        }
+        if (a.want) {
+            R = warp_max(R);
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                if (lane + 32 * e < V) s += v[e] == R ? 1.0f : exp_of(v[e], R, ct);  // (inf - inf is a term of 1)
+            s = warp_sum(s);
+            if (lane == 0) a.lse[row] = (float)lse_of(R, s, a.inv_tau);
+        }
+        sort_keys(x);
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const int r = 32 * e + lane;
+            if (r < k) {
+                a.vals[row * k + r] = value_of((uint32_t)(x[e] >> 32));
+                a.idx[row * k + r] = key_col(x[e]);
+            }
+        }
+    }
 }
 
 // The lists of a row's parts as one, a warp a row (300 rows of 12 parts, k = 10: under 8 us).
@@ -503,7 +552,7 @@ constexpr int TJ_WARPS = 2;
 
 __global__ void __launch_bounds__(TJ_WARPS * 32) k_top_join(const TopArgs a) {
     pdl_enter();
-    __shared__ unsigned long long s_l[TJ_WARPS][TS_JOIN], s_key[TJ_WARPS][JOIN_ROOM];
+    __shared__ __align__(16) unsigned long long s_l[TJ_WARPS][TS_JOIN], s_key[TJ_WARPS][JOIN_ROOM];
     const int P = a.P, k = a.k, N = P * k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = blockIdx.x * (long long)TJ_WARPS + warp;
     if (row >= a.M) return;
@@ -518,7 +567,17 @@ __global__ void __launch_bounds__(TJ_WARPS * 32) k_top_join(const TopArgs a) {
     if (a.want && lane == 0) a.lse[row] = (float)lse_of(R, s, a.inv_tau);
 }
 
+template <typename T, int E> bool top_short(const Launch& L, const void* z, const TopArgs& a) {
+    L.count();
+    const unsigned ctas = (unsigned)std::min((a.M - 1) / TH_WARPS + 1, L.num_sms * 16);
+    launch_k(L, k_top_short<T, E>, dim3(ctas), dim3(TH_WARPS * 32), 0, (const T*)z, a);
+    return true;
+}
+
 template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
+    if (!a.keys && a.V <= 32) return top_short<T, 1>(L, z, a);
+    if (!a.keys && a.V <= 64) return top_short<T, 2>(L, z, a);
+    if (!a.keys && a.V <= 128) return top_short<T, 4>(L, z, a);
     Plan p;
     const int G = row_granules<T>(z, a.ld, a.V);
     a.Gs = (G + a.P - 1) / a.P;

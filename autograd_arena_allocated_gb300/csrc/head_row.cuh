@@ -512,20 +512,70 @@ __device__ __forceinline__ unsigned long long top_key(float v, int col) {
 __device__ __forceinline__ int key_col(unsigned long long key) {
     return (int)(0xFFFFFFFFu - (uint32_t)(key & 0xFFFFFFFFull));
 }
-// out(rank, key) for the kk first of cnt keys in list order, by a warp; four lanes count for a key
+// out(rank, key) for the kk first of cnt keys in list order, by a warp: a lane
+// counts the keys above its own, two a load.  s_key is 16-byte aligned and has
+// room for an even number.
 template <typename F>
-__device__ __forceinline__ void ranks(const unsigned long long* s_key, int cnt, int kk, F&& out) {
+__device__ __forceinline__ void ranks(unsigned long long* s_key, int cnt, int kk, F&& out) {
     const int lane = threadIdx.x & 31;
-    for (int i0 = 0; i0 < cnt; i0 += 8) {
-        const int i = i0 + lane / 4;
-        const unsigned long long key = i < cnt ? s_key[i] : ~0ull;
+    if (lane == 0 && cnt % 2) s_key[cnt] = 0;  // counts for nothing
+    __syncwarp();
+    for (int i0 = 0; i0 < cnt; i0 += 32) {
+        const unsigned long long key = i0 + lane < cnt ? s_key[i0 + lane] : ~0ull;
         int r = 0;
 #pragma unroll 4
-        for (int j = lane & 3; j < cnt; j += 4) r += s_key[j] > key;
-        r += __shfl_xor_sync(0xffffffffu, r, 1);
-        r += __shfl_xor_sync(0xffffffffu, r, 2);
-        if ((lane & 3) == 0 && i < cnt && r < kk) out(r, key);
+        for (int j = 0; j < cnt; j += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s_key + j);
+            r += o.x > key;
+            r += o.y > key;
+        }
+        if (i0 + lane < cnt && r < kk) out(r, key);
     }
+}
+
+// Sorts keys over a warp, the largest first: key 32 e + lane of the list is
+// x[e].  A bitonic sort: 28 steps for 128 keys, where a lane's loop over as
+// many loads is longer (the join of 32 lists of 64: JOIN_US).  k_top_stream's
+// many warps are better served by ranks(), which has a third of the shuffles'
+// pressure on the memory pipes (32768 rows 629 us, sorted 663).
+template <int E> __device__ __forceinline__ void sort_keys(unsigned long long (&x)[E]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32 * E; size *= 2) {
+#pragma unroll
+        for (int d = size / 2; d > 0; d /= 2) {
+            if (d >= 32) {
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    if (e & (d / 32)) continue;
+                    const int o = e | (d / 32);
+                    const unsigned long long a = x[e], b = x[o];
+                    const bool swap = (a < b) == ((32 * e & size) == 0);
+                    x[e] = swap ? b : a;
+                    x[o] = swap ? a : b;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const unsigned long long y = __shfl_xor_sync(0xffffffffu, x[e], d);
+                    const bool larger = ((lane & d) == 0) == (((32 * e + lane) & size) == 0);
+                    x[e] = (x[e] > y) == larger ? x[e] : y;
+                }
+            }
+        }
+    }
+}
+// ranks() by sorting
+template <int E, typename F>
+__device__ __forceinline__ void sorted(const unsigned long long* s_key, int cnt, int kk, F&& out) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long x[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) x[e] = 32 * e + lane < cnt ? s_key[32 * e + lane] : 0ull;
+    sort_keys(x);
+#pragma unroll
+    for (int e = 0; e < E; e++)
+        if (32 * e + lane < min(cnt, kk)) out(32 * e + lane, x[e]);
 }
 
 // The kk first of n keys (0: no entry; at least kk are entries) by a warp: a
@@ -570,7 +620,9 @@ __device__ __forceinline__ void join_lists(const unsigned long long* l, int n, i
         cnt += __popc(m);
     }
     __syncwarp();
-    ranks(s_key, cnt, kk, out);
+    if (cnt <= 32) sorted<1>(s_key, cnt, kk, out);
+    else if (cnt <= 128) sorted<4>(s_key, cnt, kk, out);
+    else ranks(s_key, cnt, kk, out);
 }
 
 // A warp merges P parts' references and sums.

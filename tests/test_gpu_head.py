@@ -161,6 +161,26 @@ def test_top_logits_of_many_rows(ctx, dtype, M, V, ld, k, offset):
     check_top(ctx, dtype, z, V, k, with_lse=False)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,ld,k", [(1, 1, 1), (31, 33, 31), (32, 32, 5), (33, 40, 33), (64, 64, 64), (65, 65, 1),
+                                    (127, 130, 100), (128, 128, 128), (129, 129, 128)])
+def test_top_logits_of_short_rows(ctx, dtype, V, ld, k):
+    """Many rows of few logits: plain ones, whole numbers (ties), rows of -inf,
+    of the lowest value, with infinities and NaN."""
+    M = 3000
+    z = make_logits(dtype, M, V, ld, 5 + V, 1)
+    z[::7, :V] = torch.round(z[::7, :V])
+    check_top(ctx, dtype, z, V, k, tau=1.3)
+    z[3::9, :V] = -INF
+    z[4::9, :V] = torch.finfo(TYPES[dtype]).min
+    z[5::9, : V // 2] = -INF
+    z[6::9, V - 1] = math.nan
+    z[7::9, V // 2] = INF
+    z[8::9, :V] = 0.25
+    check_top(ctx, dtype, z, V, k)
+    check_top(ctx, dtype, z, V, k, with_lse=False)
+
+
 # ---------------------------------------------------------------- distillation
 def ref_distill(z, V, t_vals, t_idx, t_lse, targets, alpha, tau, want_scale=False):
     """Row losses in 64 bits (differentiable in z [M, V]); with want_scale also
