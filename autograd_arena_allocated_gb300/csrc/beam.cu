@@ -249,7 +249,7 @@ bool reorder(const Launch& L, void* state, const int32_t* parents, int N, int B,
 
 size_t beam_select_scratch_bytes(tt_dtype dtype, int B, int K, int V, int n) {
     const int kk = std::min(n, V);
-    return (size_t)B * K * top_parts(dtype, B * K, V, kk, BM_ENTRIES / K) * 8 * ((size_t)kk + 1);
+    return (size_t)B * K * top_parts(dtype, B * K, V, kk, BM_ENTRIES / K, TOP_TASKS) * 8 * ((size_t)kk + 1);
 }
 
 bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long long ld, const float* scores,
@@ -257,7 +257,7 @@ bool launch_beam_select(const Launch& L, tt_dtype dtype, const void* z, long lon
                         int B, int K, int V, int n, int eos, void* scratch, int32_t* tok_hist, int32_t* par_hist,
                         int ld_hist, const int* pos_dev) {
     if (L.dry) return true;
-    const int R = B * K, kk = std::min(n, V), P = top_parts(dtype, R, V, kk, BM_ENTRIES / K), N = K * kk;
+    const int R = B * K, kk = std::min(n, V), P = top_parts(dtype, R, V, kk, BM_ENTRIES / K, TOP_TASKS), N = K * kk;
     const size_t smem = (size_t)(P > 1 ? N * P : 0) * 8 + (size_t)N * (8 + 8 + 4);
     static PerDevice attr;
     if (!attr.once([] {

@@ -120,15 +120,16 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, 
 // for a selection step of 256 fp32 rows.
 // A row with more candidates than there is room for (ties: few different
 // values) is gone through bit by bit from memory.
-// 32768 rows of 50257 16-bit logits, k = 64: 624 us, 5.3 TB/s, 78% of the
-// measured copy rate; what is left is instructions (15 thousand a row, 5
+// 32768 rows of 50257 16-bit logits, k = 64: 628 us, 5.3 TB/s, 78% of the
+// measured copy rate; what is left is instructions (13 thousand a row, 5
 // thousand of them for the exponentials' sum).
 constexpr int TS_WARPS = 8;                 // most warps of a CTA
 // (28 warps of an SM at 72 registers: 642 us; 18 with a ring twice as deep: 686 us)
 constexpr int TS_CTAS = 3;                  // CTAs of an SM
-constexpr int TS_TASKS = 152 * TS_CTAS * TS_WARPS;  // rows, or parts, that are worked on at once
+constexpr int TS_TASKS = TOP_TASKS;           // rows, or parts, that are worked on at once
+static_assert(TS_TASKS == 152 * TS_CTAS * TS_WARPS, "a warp a task");
 constexpr int TS_PARTS = 64;                // most parts of a row
-constexpr int TS_JOIN = 2048;               // most entries of a row's parts' lists
+constexpr int TS_JOIN = 1024;               // most entries of a row's parts' lists
 constexpr int TS_BLOCKS = 64;               // most blocks of a lane
 constexpr int TS_U = 4;                     // granules of a lane in a stage of the ring
 constexpr int TS_RING = 2 * TS_U * 32 * 16;  // two stages
@@ -504,8 +505,8 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
 
 // Rows of up to 32 E logits: a warp holds one, lane l the columns l + 32 e, and
 // sorts it.  What a row takes is the sort's instructions (E = 4: about 800):
-// 30000 rows of 100 SHORT_US, 65 and 166 us (k = 10, 64) by the kernel above,
-// whose ring, threshold and second read are made for long rows.
+// 30000 rows of 100 37 us; 91 and 166 us (k = 10, 64) by the kernel above, whose
+// ring, threshold and second read are made for long rows.
 constexpr int TH_WARPS = 4;
 
 template <typename T, int E>
@@ -582,16 +583,20 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
     const int G = row_granules<T>(z, a.ld, a.V);
     a.Gs = (G + a.P - 1) / a.P;
     const int granules = (a.Gs + 127) / 128 * 4;  // of a lane, whole stages
-    // blocks of four granules where they are enough to tell k of them from the rest
-    int ub_log = granules <= TS_BLOCKS && granules * 8 < 4 * a.k ? 0 : 2;
+    // blocks of four granules where they are enough (8 k) to tell k of them from
+    // the rest: fewer make the second read long (100 rows of 120000 16-bit
+    // logits, k = 64: 34 us from 4 k blocks on, 26 us so)
+    int ub_log = granules <= TS_BLOCKS && granules < a.k ? 0 : 2;
     while ((granules + (1 << ub_log) - 1) >> ub_log > TS_BLOCKS) ub_log++;
     const int nb = (granules + (1 << ub_log) - 1) >> ub_log;
     const int words = (nb + Blocks<T>::PER - 1) / Blocks<T>::PER;
     static PerDevice attr;
     if (!allow_smem(attr, k_top_stream<T>)) return false;
-    // few tasks are spread over the SMs
+    // tasks that are all worked on at once are spread evenly over the SMs by
+    // small CTAs (100 rows of 120000 16-bit logits in 16 parts: 38 us as 200
+    // CTAs of 8 warps, which are 16 warps on some SMs and 8 on others; 34 us so)
     const long long tasks = (long long)a.M * a.P;
-    const int warps = (int)std::min<long long>(TS_WARPS, std::max<long long>(1, tasks / L.num_sms));
+    const int warps = tasks > TS_CTAS * TS_WARPS * L.num_sms ? TS_WARPS : tasks > L.num_sms ? 2 : 1;
     p.smem = (size_t)warps * stream_warp_smem(words, a.k);
     p.threads = warps * 32;
     const long long per_sm = std::min<long long>(TS_CTAS * TS_WARPS / warps, (long long)(SMEM_SM / (p.smem + 1024)));
@@ -602,15 +607,26 @@ template <typename T> bool top_rows(const Launch& L, const void* z, TopArgs a) {
 
 }  // namespace
 
-int top_parts(tt_dtype dtype, int M, int V, int k, int entries) {
+// A part has 192 granules at least, and 8 more for each entry of its list: what
+// the list takes of a part's time does not shrink with the part (300 rows of
+// 20000 16-bit logits, k = 64: 12 parts 26.6 us, 3 to 8 parts 22 to 25).
+int top_parts(tt_dtype dtype, int M, int V, int k, int entries, int tasks) {
     const long long G = ((long long)V * (dtype == TT_FP32 ? 4 : 2) + 15) / 16;
-    const long long p = std::min<long long>(std::min<long long>(TS_TASKS / M, G / 192),
+    const long long p = std::min<long long>(std::min<long long>(tasks / M, G / (192 + 8 * k)),
                                             std::min<long long>(entries / k, TS_PARTS));
     return (int)std::max<long long>(p, 1);
 }
 
+// Two thirds of the SMs' warps (1000 rows of 50257 16-bit logits, k = 64, in 2
+// parts 40 us, in 3 parts 48; 300 rows in 8 parts 26 us, in 12 parts 30), but
+// two parts rather than one.
+static int row_parts(tt_dtype dtype, int M, int V, int k) {
+    const int p = top_parts(dtype, M, V, k, TS_JOIN, TS_TASKS * 2 / 3);
+    return p > 1 ? p : top_parts(dtype, M, V, k, TS_JOIN, TS_TASKS);
+}
+
 size_t top_rows_scratch_bytes(tt_dtype dtype, int M, int V, int k) {
-    const size_t P = (size_t)top_parts(dtype, M, V, k, TS_JOIN);
+    const size_t P = (size_t)row_parts(dtype, M, V, k);
     return P == 1 ? 0 : (size_t)M * P * 8 * ((size_t)k + 1);
 }
 
@@ -620,7 +636,7 @@ bool launch_top_rows(const Launch& L, tt_dtype dtype, const void* z, long long l
     TopArgs a{};
     a.vals = vals; a.idx = idx; a.lse = lse; a.want = lse != nullptr;
     a.ld = ld; a.M = M; a.V = V; a.k = k; a.inv_tau = 1.0f / tau;
-    a.P = top_parts(dtype, M, V, k, TS_JOIN);
+    a.P = row_parts(dtype, M, V, k);
     if (a.P > 1) {
         a.keys = (unsigned long long*)scratch;
         a.parts = (float2*)(a.keys + (size_t)M * a.P * k);

@@ -534,10 +534,10 @@ __device__ __forceinline__ void ranks(unsigned long long* s_key, int cnt, int kk
 }
 
 // Sorts keys over a warp, the largest first: key 32 e + lane of the list is
-// x[e].  A bitonic sort: 28 steps for 128 keys, where a lane's loop over as
-// many loads is longer (the join of 32 lists of 64: JOIN_US).  k_top_stream's
-// many warps are better served by ranks(), which has a third of the shuffles'
-// pressure on the memory pipes (32768 rows 629 us, sorted 663).
+// x[e].  A bitonic sort, for a warp that has little beside it: 28 steps for 128
+// keys.  The many warps of k_top_stream fare better with ranks(), which asks
+// less of the pipe that shuffles share with shared memory (32768 rows of 50257
+// 16-bit logits, k = 64: 628 us, sorted 663).
 template <int E> __device__ __forceinline__ void sort_keys(unsigned long long (&x)[E]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll

@@ -288,8 +288,10 @@ bool launch_top_rows(const Launch& L, tt_dtype dtype, const void* z, long long l
                      float* vals, int32_t* idx, float* lse, void* scratch);
 // the same in P parts a row, left as lists of keys (head_row.cuh) and sums of
 // exponentials; rows with skip[row] != 0 are left out.  top_parts: how many
-// parts M rows are best cut into, their lists having at most `entries` in all
-int top_parts(tt_dtype dtype, int M, int V, int k, int entries);
+// parts M rows are best cut into, their lists having at most `entries` in all,
+// all rows at most `tasks` parts
+constexpr int TOP_TASKS = 3648;  // what the SMs hold at once
+int top_parts(tt_dtype dtype, int M, int V, int k, int entries, int tasks);
 bool launch_top_parts(const Launch& L, tt_dtype dtype, const void* z, long long ld, int M, int V, int k, int P,
                       unsigned long long* keys, float2* parts, const int32_t* skip);
 // distillation loss and gradient; dz (may be z, or NULL: loss only), t_lse,
