@@ -121,7 +121,7 @@ __device__ __noinline__ void exact_candidates(const Slice<T>& s, int V, int kk, 
 // A row with more candidates than there is room for (ties: few different
 // values) is gone through bit by bit from memory.
 // 32768 rows of 50257 16-bit logits, k = 64: 628 us, 5.3 TB/s, 78% of the
-// measured copy rate; what is left is instructions (13 thousand a row, 5
+// measured copy rate; what is left is instructions (14 thousand a row, 5
 // thousand of them for the exponentials' sum).
 constexpr int TS_WARPS = 8;                 // most warps of a CTA
 // (28 warps of an SM at 72 registers: 642 us; 18 with a ring twice as deep: 686 us)

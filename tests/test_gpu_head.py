@@ -395,6 +395,21 @@ def test_distill_masks_of_many_rows(ctx, dtype, V, copies, rest):
         assert bool((d.view(copies, M, ld) == d[:M]).all())
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,V", [(40, 65), (40, 900), (12, 3000), (400, 3000), (3, 120000), (160, 60000)])
+def test_distill_of_labels_only_with_a_known_normaliser(ctx, dtype, M, V):
+    """alpha 0: the list has no weight, but its columns still count in the cross entropy."""
+    z = make_logits(dtype, M, V, V + 1, 8)
+    lists = make_lists(M, V, 30, 9)
+    y = torch.randint(0, V, (M,), generator=gen(10), device=DEV, dtype=torch.int32)
+    y[::2] = lists[1][::2, 3]
+    z[1, lists[1][1, :20].long()] += 12.0  # most of the mass is on the list
+    for tau in (1.0, 2.0):
+        a = check_distill(ctx, dtype, z, V, lists, y, 0.0, tau, True)
+        b = check_distill(ctx, dtype, z, V, lists, y, 0.0, tau, False)
+        assert bool(((a[0] - b[0]).abs() <= 4 * (DEPTH + 64) * U * (20 + b[0].abs())).all())
+
+
 @pytest.mark.parametrize("V,M", [(3000, 400), (70000, 160)])
 def test_distill_of_many_rows_other_alignment_and_flags(ctx, V, M):
     """dlogits that starts at another place of a line; bad columns and labels."""
