@@ -322,10 +322,10 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                         cp16<1024>(ring_at, src);
                         cp16<1536>(ring_at, src);
                     } else {
-                        cp16<2048>(ring_at, src);
-                        cp16<2560>(ring_at, src);
-                        cp16<3072>(ring_at, src);
-                        cp16<3584>(ring_at, src);
+                        cp16<4 * 512>(ring_at, src);
+                        cp16<5 * 512>(ring_at, src);
+                        cp16<6 * 512>(ring_at, src);
+                        cp16<7 * 512>(ring_at, src);
                     }
                     cp_commit();
                     if (want) {
