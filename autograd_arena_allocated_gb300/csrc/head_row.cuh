@@ -293,8 +293,8 @@ template <typename T> __device__ __forceinline__ uint4 granule(const Slice<T>& s
 // e^20.  The argument is one fused multiply-add, z c + nb with nb = -(R c)
 // rounded; the rounding of nb is common to all terms and is taken out at the
 // end as the factor 2^-(R c + nb), which a fused multiply-add gives exactly.
-// Logits beyond 1e30 (a row that consists of the type's lowest value, an
-// infinity) would overflow z c: such threads form (z - R) first.
+// Logits beyond 1e30 (the type's lowest value, +inf) would overflow z c: threads
+// that start from one, meet a positive one or nothing else form (z - R) first.
 constexpr float FAR = 1e30f;
 
 __device__ __forceinline__ bool is_far(float v) { return !(fabsf(v) < FAR); }
@@ -398,7 +398,8 @@ template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
         tm = E::value(m);
         sa = sb = 0.0f;
         if (!(SA || SB)) return false;
-        if (far) {
+        // a thread that has met nothing but -inf and values below -FAR has no reference
+        if (far || (lim == -INFINITY && tm > -INFINITY)) {
             R = tm;
             return true;
         }

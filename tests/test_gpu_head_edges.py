@@ -1,0 +1,183 @@
+"""The list operators at the edges of their arithmetic: rows that mix two kinds
+of mask, mass off the list that is tiny beside it, long sums, many rows.
+
+The references are the definitions in 64 bits and in logarithms, so that no
+term is lost to underflow, and every comparison asks for `error <= bound`: a
+NaN on either side fails.
+
+Tolerances of distillation, with u = 2^-24 (half a step of fp32):
+ - p_j = exp(t_j / tau - base): the quotient, the difference and the product
+   with log2 e are each off by half a step of at most |t_j| / tau + |base|, the
+   exponential by two steps: (4 (|t_j| / tau + |base|) + 8) u relative;
+ - p_r is 1 less their sum: off by the sum of their errors and 12 additions;
+ - a student's probability is exp((z - R) / tau) over a sum: (3 |ln q| + depth +
+   64) u relative, the numerator's argument, the sum (as in test_gpu_head.py)
+   and the reference's rounding;
+ - the gradient adds these and half a step of its storage type; the loss
+   multiplies them by the logarithms that it weighs, which are themselves off
+   by their own size in u and by the sum's relative error."""
+import math
+
+import pytest
+import torch
+
+import test_gpu_head as base
+from autograd_arena_allocated_gb300 import api
+from test_gpu_head import DEPTH, DEV, INF, TYPES, U, ctx, gen, make_lists, make_logits  # noqa: F401 (ctx: a fixture)
+
+pytestmark = pytest.mark.gpu
+OFF_MIN = -700.0  # ln q_r below this counts as no mass off the list
+
+
+def exact_distill(z, V, lists, targets, alpha, tau, rest):
+    """Losses, d loss / d z and the bounds of their errors, in 64 bits."""
+    vals, idx, lse = lists
+    M = z.shape[0]
+    x = z[:, :V].double()
+    used = idx >= 0
+    at = torch.where(used, idx, V).long()
+    logq = torch.log_softmax(x / tau, 1)
+    wide = torch.cat([logq, torch.zeros(M, 1, dtype=torch.float64, device=z.device)], 1)
+    lq = wide.gather(1, at)
+    t = torch.where(used, vals.double() / tau, -INF)
+    norm = lse.double()[:, None] if rest else torch.logsumexp(t, 1, keepdim=True)
+    some = used.any(1, keepdim=True)
+    lp = torch.where(used, t - norm, -INF)
+    p = torch.where(some, lp.exp(), 0.0)
+    on = p > 0
+    lp0, lq0 = torch.where(on, lp, 0.0), torch.where(on, lq, 0.0)
+    arg = torch.where(on, t.abs() + norm.abs(), 0.0)
+    dp = p * (4 * arg + 8) * U
+    total = p.sum(1, keepdim=True)
+    dpr = dp.sum(1, keepdim=True) + 12 * U * total.clamp(min=1.0)
+    kl = (p * (lp0 - lq0)).sum(1)
+    size = (dp * (lp0.abs() + lq0.abs() + 1) + p * (2 * arg + 4 * lq0.abs() + DEPTH + 64) * U).sum(1)
+    listed = torch.zeros(M, V + 1, dtype=torch.bool, device=z.device).scatter_(1, at, True)[:, :V]
+    off = torch.zeros_like(logq)
+    pr = torch.zeros_like(total)
+    if rest:
+        lqr = torch.logsumexp(torch.where(listed, -INF, logq), 1, keepdim=True)
+        pr = torch.where(some & (lqr >= OFF_MIN), (1 - total).clamp(min=0), 0.0)
+        have = pr > 0
+        lr = torch.where(have, lqr, 0.0)
+        lpr = torch.where(have, pr, 1.0).log()
+        kl = kl + (pr * (lpr - lr))[:, 0]
+        ask = some & (lqr >= OFF_MIN)
+        size = size + torch.where(ask, dpr * (torch.where(have, lpr.abs(), 17.0) + torch.where(ask, lqr, 0.0).abs() + 1)
+                                  + pr * (2 * DEPTH + 64 + 4 * lr.abs()) * U, 0.0)[:, 0]
+        off = torch.where(ask & ~listed, (logq - torch.where(ask, lqr, 0.0)).exp(), 0.0)
+    q = logq.exp()
+    W = total + pr
+    spread = lambda v: torch.zeros(M, V + 1, dtype=torch.float64, device=z.device).scatter_add_(1, at, v)[:, :V]
+    soft = torch.where(some, 1.0, 0.0) * alpha * tau
+    rel = (2 * DEPTH + 64 + 3 * logq.abs().clamp(max=800.0)) * U
+    grad = soft * (W * q - spread(p) - pr * off)
+    bound = soft * (W * q * rel + dpr * q + spread(dp) + (dpr + pr * rel) * off)
+    loss = torch.where(some[:, 0], alpha * tau * tau * kl, 0.0)
+    lb = torch.where(some[:, 0], alpha * tau * tau * size, 0.0)
+    if targets is not None and alpha < 1:
+        y = targets.long()
+        hard = (y >= 0)[:, None]
+        ls = torch.log_softmax(x, 1)
+        s = ls.exp()
+        hot = torch.zeros_like(s).scatter_(1, y.clamp(min=0)[:, None], 1.0)
+        ce = -ls.gather(1, y.clamp(min=0)[:, None])[:, 0]
+        grad = grad + torch.where(hard, (1 - alpha) * (s - hot), 0.0)
+        bound = bound + torch.where(hard, (1 - alpha) * (s * (2 * DEPTH + 64 + 3 * ls.abs().clamp(max=800.0)) + 2 * hot) * U, 0.0)
+        loss = loss + torch.where(hard[:, 0], (1 - alpha) * ce, 0.0)
+        zs = torch.logsumexp(x, 1).abs() + x.gather(1, y.clamp(min=0)[:, None])[:, 0].abs()
+        lb = lb + torch.where(hard[:, 0], (1 - alpha) * (DEPTH + 64 + 4 * zs) * U, 0.0)
+    return loss, lb + 4 * U * loss.abs(), grad, bound
+
+
+def within(got, want, bound, what):
+    ok = (got - want).abs() <= bound
+    assert bool(torch.isfinite(want).all()) and bool(torch.isfinite(got).all()), what
+    assert bool(ok.all()), (what, int((~ok).sum()), ok.shape, float(((got - want).abs() / bound)[~ok].max()))
+
+
+def check_strict(ctx, dtype, z, V, lists, targets, alpha, tau, rest, dscale=None):
+    dscale = 1.0 / z.shape[0] if dscale is None else dscale
+    row, mean, d = base.run_distill(ctx, dtype, z, V, lists, targets, alpha, tau, rest, dscale=dscale)
+    loss, lb, grad, gb = exact_distill(z, V, lists, targets, alpha, tau, rest)
+    within(row.double(), loss, lb, "loss")
+    f = torch.finfo(TYPES[dtype])
+    within(d[:, :V].double(), grad * dscale,
+           f.eps / 2 * 1.001 * (grad * dscale).abs() + gb * abs(dscale) + f.smallest_normal * f.eps / 2 + 1e-37, "gradient")
+    assert bool((d[:, V:] == 0).all())
+    in_place = base.run_distill(ctx, dtype, z, V, lists, targets, alpha, tau, rest, dscale=dscale, in_place=True)
+    assert torch.equal(in_place[0], row) and torch.equal(in_place[2], d)
+    only = base.run_distill(ctx, dtype, z, V, lists, targets, alpha, tau, rest, dscale=dscale, grad=False)
+    assert torch.equal(only[0], row)
+    return row, mean, d
+
+
+# ---------------------------------------------------------------- two kinds of mask
+def mixed_masks(dtype, V, ld, extra=0):
+    """Eight rows whose columns are -inf here and the type's lowest value (or
+    half of it) there, with a few real logits or none; -> z, the real columns
+    (the rows that have none: columns of their largest value)."""
+    low = torch.finfo(TYPES[dtype]).min
+    cut = min(V // 2, 6000)
+    z = make_logits(dtype, 8, V, ld, 33 + V, extra, pad=math.nan)
+    z[:, :cut] = -INF
+    z[:, cut:V] = low
+    at = [torch.linspace(cut + 3, V - 2, 6).long().tolist() for _ in range(8)]
+    z[1, at[1][:3]] = torch.tensor([-100.0, -101.0, -100.5], device=DEV).to(z.dtype)
+    z[2, :V] = low
+    z[2, cut:V] = -INF
+    at[2] = torch.linspace(1, cut - 2, 6).long().tolist()
+    z[2, at[2][:3]] = torch.tensor([-200.0, -201.0, -200.5], device=DEV).to(z.dtype)
+    z[3, :V] = -INF
+    z[3, V - 40:V] = low
+    z[3, V - 7] = -1000.0
+    at[3] = [V - 7]
+    blocks = (torch.arange(V, device=DEV) // 64) % 2 == 0
+    z[4, :V] = torch.where(blocks, -INF, low).to(z.dtype)
+    z[4, V // 3] = 5.0
+    at[4] = [V // 3]
+    z[5, cut:V] = low / 2
+    z[5, cut:cut + 5] = low
+    at[5] = [c for c in at[5] if c >= cut + 5]
+    z[6, :V] = -INF
+    z[6, V - 9:V] = low
+    at[6] = [V - 9, V - 1]
+    z[7, V // 2:V] = -INF
+    z[7, cut:V // 2 + 1] = low
+    at[7] = [cut] if V // 2 == cut else [cut, V // 2]
+    return z, at
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,copies", [(100, 1), (700, 1), (6000, 1), (6000, 600), (50257, 1), (50257, 500)])
+def test_top_logits_of_two_kinds_of_mask(ctx, dtype, V, copies):
+    """A grammar's -inf and a library's lowest value in one row."""
+    z, _ = mixed_masks(dtype, V, V + 3)
+    z = z.repeat(copies, 1)
+    for tau in (1.0, 2.5):
+        base.check_top(ctx, dtype, z, V, 12, tau=tau)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [700, 6000, 50257])
+def test_beam_select_of_two_kinds_of_mask(ctx, dtype, V):
+    z, _ = mixed_masks(dtype, V, V)
+    scores = torch.tensor([[-2.0, -1.0, -3.0, -4.0], [-2.5, -1.5, -0.5, -3.5]], device=DEV)
+    base.check_select(ctx, dtype, z, scores, None, 4, V, 4, -1)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,copies", [(100, 1), (700, 1), (6000, 1), (6000, 50), (50257, 1), (50257, 40), (60001, 20)])
+@pytest.mark.parametrize("rest", [True, False])
+def test_distill_of_two_kinds_of_mask(ctx, dtype, V, copies, rest):
+    z, at = mixed_masks(dtype, V, V + 1)
+    k = 4
+    vals, idx, lse = make_lists(8, V, k, 7, unused=False)
+    y = torch.empty(8, dtype=torch.int32, device=DEV)
+    for r in range(8):
+        c = at[r]
+        idx[r] = torch.tensor((c[:2] + [-1] * k)[:k])
+        y[r] = c[-1] if r in (0, 5, 6, 7) else c[0] if r % 2 else c[:3][-1]
+    lists = tuple(x.repeat(copies, *([1] * (x.dim() - 1))) for x in (vals, idx, lse))
+    for alpha in (0.5, 1.0):
+        check_strict(ctx, dtype, z.repeat(copies, 1), V, lists, y.repeat(copies), alpha, 2.0, rest)
