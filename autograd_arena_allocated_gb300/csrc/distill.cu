@@ -48,7 +48,7 @@ struct DistillLayout {
         part = at; at += 2 * (NT + LIST_CTA) / 32 * 16;
         lw = at; at += LIST_CTA / 32 * 16;
         ll = at; at += 16;
-        x = at; at += cl ? 2 * CS_MAX * 16 : 0;
+        x = at; at += cl ? 2 * CS_MAX * (16 + 8) : 0;
         flag = at; at += 16;
         total = at;
     }
@@ -131,7 +131,7 @@ __device__ __forceinline__ void grad_pass(const Slice<T>& s, char* buf, T* drow,
 // its end (its gradient is written), the others do not wait for them there; all
 // meet where the sums do.  Every warp merges the warps' sums and forms the
 // coefficients for itself, which saves a barrier.
-template <typename T, bool CL>
+template <typename T, bool CL, bool REST>
 __global__ void __launch_bounds__(NT + LIST_CTA, 2)
 k_distill(const T* z, T* dz, const DistillArgs a) {
     pdl_wait();
@@ -155,10 +155,12 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
     float4* s_lw = reinterpret_cast<float4*>(sm + lay.lw);
     float* s_ll = reinterpret_cast<float*>(sm + lay.ll);
     float4* s_x = reinterpret_cast<float4*>(sm + lay.x);  // [2][cs]
+    float2* s_xo = reinterpret_cast<float2*>(s_x + 2 * CS_MAX);  // [2][cs] off the list, at its own reference
     int* s_flag = reinterpret_cast<int*>(sm + lay.flag);  // the target is on the list
     const int rank = CL ? (int)cluster_rank() : 0, cs = CL ? a.cs : 1;
     const long long first = blockIdx.x / cs, stride = gridDim.x / cs;
-    const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
+    constexpr bool rest = REST;
+    const bool soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
     const float it = 1.0f / a.tau, ct = LOG2E * it, lift = 20.0f / fmaxf(1.0f, it);
     float g_all = a.dscale;
     if (a.scale_dev) g_all *= *a.scale_dev;
@@ -335,11 +337,19 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         static_assert(WARPS <= 16, "the merge below is over 16 lanes");
         if (lane == 0) s_part[par * WARPS + warp] = make_float4(R, s1, st, sl);
         __syncthreads();
+        float Ro = -INFINITY, so = 0.0f;  // the sum off the list at a reference of its own
         if (!CL || warp == 0) {
             const int l = lane & 15;
             const float4 p = l < WARPS ? s_part[par * WARPS + l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             R = p.x; s1 = p.y; st = p.z; sl = p.w;
             merge<16>(R, s1, st, sl, ct, hard, rest);
+            if (rest && (CL || off_own(st, sl))) {
+                if (l < NT / 32) Ro = p.x, so = p.z;  // the other warps have none
+                merge<16>(Ro, so, ct);
+                if (!CL) st = so;
+            } else {
+                Ro = R;
+            }
         }
         if (CL) {
             if (warp == 0 && lane < cs) {
@@ -348,33 +358,45 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
                 st_remote(at + 4, s1);
                 st_remote(at + 8, st);
                 st_remote(at + 12, sl);
+                if (rest) {
+                    const uint32_t off = remote(s_xo + par * cs + rank, lane);
+                    st_remote(off, Ro);
+                    st_remote(off + 4, so);
+                }
             }
             cluster_sync();
             const int l = lane & (CS_MAX - 1);
             const float4 p = l < cs ? s_x[par * cs + l] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             R = p.x; s1 = p.y; st = p.z; sl = p.w;
             merge<CS_MAX>(R, s1, st, sl, ct, hard, rest);
+            Ro = R;
+            if (rest && off_own(st, sl)) {
+                const float2 o = l < cs ? s_xo[par * cs + l] : make_float2(-INFINITY, 0.0f);
+                Ro = o.x; st = o.y;
+                merge<CS_MAX>(Ro, st, ct);
+            }
         }
 
-        const Coefs f(a, s_lw, nlw, rest, soft_on, hard, rest ? s_tl[b] : 0.0f, g_all, s1, st, sl);
+        const Coefs f(a, s_lw, nlw, rest, soft_on, hard, rest ? s_tl[b] : 0.0f, g_all, R, Ro, s1, st, sl, it,
+                      ct);
         const bool soft = f.soft;
-        const float A1 = f.A1;
+        const float m = f.Rp, A1 = f.A1p;
         T* drow = dz ? dz + row * a.ld : nullptr;
         if (dz && worker) {
             // second pass: the gradient
             const float As = soft ? f.At : 0.0f;
             if (soft && hard && p2 == 2)
-                grad_pass<T, NT, true, true, 2>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+                grad_pass<T, NT, true, true, 2>(s, buf, drow, V, tid, a.same_phase, m, ct, As, A1, nx, more);
             else if (soft && hard && p2 == 3)
-                grad_pass<T, NT, true, true, 3>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+                grad_pass<T, NT, true, true, 3>(s, buf, drow, V, tid, a.same_phase, m, ct, As, A1, nx, more);
             else if (soft && hard && p2 == 4)
-                grad_pass<T, NT, true, true, 4>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+                grad_pass<T, NT, true, true, 4>(s, buf, drow, V, tid, a.same_phase, m, ct, As, A1, nx, more);
             else if (soft && hard && p2 != 1)
-                grad_pass<T, NT, true, true>(s, buf, drow, V, tid, a.same_phase, R, ct, As, A1, nx, more);
+                grad_pass<T, NT, true, true>(s, buf, drow, V, tid, a.same_phase, m, ct, As, A1, nx, more);
             else if (soft || !hard)
-                grad_pass<T, NT, true, false>(s, buf, drow, V, tid, a.same_phase, R, ct, As + A1, 0.0f, nx, more);
+                grad_pass<T, NT, true, false>(s, buf, drow, V, tid, a.same_phase, m, ct, As + A1, 0.0f, nx, more);
             else
-                grad_pass<T, NT, false, true>(s, buf, drow, V, tid, a.same_phase, R, ct, 0.0f, A1, nx, more);
+                grad_pass<T, NT, false, true>(s, buf, drow, V, tid, a.same_phase, m, ct, 0.0f, A1, nx, more);
             if (rank == cs - 1)
                 for (long long c = V + tid; c < a.ld; c += NT) drow[c] = Elem<T>::put(0.0f);
         }
@@ -416,19 +438,46 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
 // is written twice.  A row takes a few hundred instructions whatever its
 // length, which is what bounds the shortest: 16384 rows of 65 with k = 8 take
 // 15.5 us (38 us as a warp's form of the kernel above, whose list handling is
-// made for long rows), 30400 rows of 1024 102 us (401 us a CTA a row).
+// made for long rows), 30400 rows of 1024 102 us (401 us a CTA a row; with t_lse
+// at five CTAs an SM and 96 registers 105 us, at four and 122 102 us).
 constexpr int DS_WARPS = 4;
 constexpr uint32_t DS_UNLISTED = 0x7FC0DEADu;  // a NaN that no arithmetic makes
 
-template <typename T, int E>
-__global__ void __launch_bounds__(DS_WARPS * 32, E <= 4 ? 8 : E <= 16 ? 6 : 5)
+// Columns off the list that need a reference of their own (Coefs; rare): their
+// largest logit and their sum, then the gradient, from memory.
+template <typename T>
+__device__ __noinline__ float2 short_off_sum(const T* zr, const uint32_t* s_lp, int V, float ct) {
+    float mo = -INFINITY, su = 0.0f;
+    for (int c = threadIdx.x & 31; c < V; c += 32)
+        if (s_lp[c] == DS_UNLISTED) mo = fmaxf(mo, Elem<T>::get(zr + c));
+    mo = warp_max(mo);
+    for (int c = threadIdx.x & 31; c < V; c += 32)
+        if (mo != -INFINITY && s_lp[c] == DS_UNLISTED) su += exp_of(Elem<T>::get(zr + c), mo, ct);
+    return make_float2(mo, warp_sum(su));
+}
+template <typename T>
+__device__ __noinline__ void short_gradient(const T* zr, T* dr, const uint32_t* s_lp, int V, float m, float mo, float ct,
+                                            float Al, float Ao, float ks, float A1, float A1o, int y, float kh) {
+    for (int c = threadIdx.x & 31; c < V; c += 32) {
+        const uint32_t u = s_lp[c];
+        const bool off = u == DS_UNLISTED;
+        const float v = Elem<T>::get(zr + c), et = exp_of(v, off ? mo : m, ct);
+        float r = off ? Ao * et : Al * et - ks * ex2f(__uint_as_float(u) * LOG2E);
+        if (kh != 0.0f) r += (off ? A1o : A1) * exp_of(v, off ? mo : m, LOG2E) - (c == y ? kh : 0.0f);
+        dr[c] = Elem<T>::put(r);
+    }
+}
+
+template <typename T, int E, bool REST>
+__global__ void __launch_bounds__(DS_WARPS * 32, E <= 4 ? 8 : E <= 16 ? 6 : REST ? 4 : 5)
 k_distill_short(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
     __shared__ uint32_t s_all[DS_WARPS][32 * E];
     using El = Elem<T>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = a.k, V = a.V;
     uint32_t* s_lp = s_all[warp] + lane;  // the lane's columns at steps of 32
-    const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
+    constexpr bool rest = REST;
+    const bool soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
     const float it = 1.0f / a.tau, ct = LOG2E * it;
     float g_all = a.dscale;
     if (a.scale_dev) g_all *= *a.scale_dev;
@@ -518,20 +567,25 @@ k_distill_short(const T* z, T* dz, const DistillArgs a) {
             s1 = warp_sum(s1);
             zy = __shfl_sync(0xffffffffu, zy, y & 31);
         }
-        float st = 0.0f, pr = 0.0f;
+        float st = 0.0f, pr = 0.0f, mo = m;  // mo: the reference of su
         if (soft) {
             su = warp_sum(su);
             sl = warp_sum(sl);
             W = warp_sum(W);
             part = warp_sum(part);
             st = su + sl;
+            if (rest && off_own(su, sl)) {
+                const float2 o = short_off_sum(zr, s_all[warp], V, ct);
+                if (Coefs::ln_off(o.y, st, o.x, m, it) >= OFF_MIN) mo = o.x;
+                su = mo == o.x ? o.y : 0.0f;
+            }
             if (rest && su > 0.0f) pr = fmaxf(1.0f - W, 0.0f);
         }
         if (lane == 0) {
             float loss = 0.0f;
             if (soft) {
                 loss = part + W * logf(st);
-                if (pr > 0.0f) loss += pr * (logf(pr) - logf(__fdividef(su, st)));
+                if (pr > 0.0f) loss += pr * (logf(pr) - Coefs::ln_off(su, st, mo, m, it));
                 loss *= a.alpha * a.tau * a.tau;
             }
             if (hard) loss += (1.0f - a.alpha) * (m + logf(s1) - zy);
@@ -542,6 +596,13 @@ k_distill_short(const T* z, T* dz, const DistillArgs a) {
             const float ks = g_all * a.alpha * a.tau, kh = hard ? g_all * (1.0f - a.alpha) : 0.0f;
             const float rt = soft ? __fdividef(ks, st) : 0.0f, A1 = hard ? __fdividef(kh, s1) : 0.0f;
             const float Al = (W + pr) * rt, At = pr > 0.0f ? rt * (W + pr - pr * __fdividef(st, su)) : W * rt;
+            if (rest && mo < m) {
+                short_gradient(zr, dr, s_all[warp], V, m, mo, ct, Al, Al * rescale(mo, m, ct) - ks * __fdividef(pr, su),
+                               ks, A1, A1 * rescale(mo, m, LOG2E), hard ? y : -1, kh);
+                for (long long c = V + lane; c < a.ld; c += 32) dr[c] = El::put(0.0f);
+                __syncwarp();
+                continue;
+            }
 #pragma unroll
             for (int e = 0; e < E; e++) {
                 const int c = lane + 32 * e;
@@ -598,18 +659,19 @@ template <typename Bytes> bool make_plan(Plan& p, int sms, long long M, int G, i
     return true;
 }
 
-#define ROW_KERNEL(NAME, CL_, ...)                            \
+#define ROW_KERNEL(NAME, CL_, REST_, ...)                            \
     do {                                                      \
         static PerDevice attr;                                \
-        if (!allow_smem(attr, NAME<T, CL_>)) return false;    \
-        launch_rows(L, NAME<T, CL_>, p, __VA_ARGS__);         \
+        if (!allow_smem(attr, NAME<T, CL_, REST_>)) return false;    \
+        launch_rows(L, NAME<T, CL_, REST_>, p, __VA_ARGS__);         \
         return true;                                          \
     } while (0)
 
 template <typename T, int E> bool distill_short(const Launch& L, const void* z, void* dz, const DistillArgs& a) {
     L.count();
     const unsigned ctas = (unsigned)std::min((a.M - 1) / DS_WARPS + 1, L.num_sms * 12);
-    launch_k(L, k_distill_short<T, E>, dim3(ctas), dim3(DS_WARPS * 32), 0, (const T*)z, (T*)dz, a);
+    if (a.t_lse) launch_k(L, k_distill_short<T, E, true>, dim3(ctas), dim3(DS_WARPS * 32), 0, (const T*)z, (T*)dz, a);
+    else launch_k(L, k_distill_short<T, E, false>, dim3(ctas), dim3(DS_WARPS * 32), 0, (const T*)z, (T*)dz, a);
     return true;
 }
 
@@ -635,8 +697,10 @@ template <typename T> bool distill(const Launch& L, const void* z, void* dz, Dis
     if (G <= 2560 && a.M > 2 * L.num_sms) return distill_stream<T>(L, z, dz, a, G, 128);
     if (!make_plan(p, L.num_sms, a.M, G, cs, bytes)) return false;
     a.Gs = p.Gs; a.cs = p.cs; a.nbuf = p.nbuf;
-    if (p.cs == 1) ROW_KERNEL(k_distill, false, (const T*)z, (T*)dz, a);
-    ROW_KERNEL(k_distill, true, (const T*)z, (T*)dz, a);
+    if (p.cs == 1 && a.t_lse) ROW_KERNEL(k_distill, false, true, (const T*)z, (T*)dz, a);
+    if (p.cs == 1) ROW_KERNEL(k_distill, false, false, (const T*)z, (T*)dz, a);
+    if (a.t_lse) ROW_KERNEL(k_distill, true, true, (const T*)z, (T*)dz, a);
+    ROW_KERNEL(k_distill, true, false, (const T*)z, (T*)dz, a);
 }
 
 }  // namespace

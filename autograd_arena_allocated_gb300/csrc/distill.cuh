@@ -18,6 +18,14 @@ namespace head {
 // if no column were listed, and the list's columns are then written over.
 // Where q_r is needed (t_lse) the first pass leaves the listed logits out, so
 // that q_r is not a difference; their own exponentials are added from the list.
+// The sum off the list, su, may be any fraction of the sum of all, sa.  At the
+// common reference R a column 87 tau below it is lost; so below OFF_OWN of sa
+// the sum is formed again at a reference of its own, Ro: ln q_r is then a
+// difference of logarithms, and the second pass takes
+//   ks ((W + p_r) e^((Ro - R) / tau) / sa - p_r / su) e^((z - Ro) / tau)
+// whose coefficient does not grow with the list's lead.  Below e^-700 q_r
+// counts as 0, as it nearly is in 64 bits: so low are columns that a mask of
+// large negative numbers hides.
 struct DistillArgs {
     const float* t_vals;
     const int32_t* t_idx;
@@ -112,12 +120,23 @@ __device__ __forceinline__ void store_edge(const Slice<T>& s, int i, T* drow, in
 // The teacher's normaliser and mass from its list's warps (s_lw: largest logit
 // and sum of exponentials, or, where the normaliser is known, the probabilities'
 // sum; whether an entry is used), and the coefficients of loss and gradient.
-// st is off the list until then, sl on it.
+// su_ is off the list, sl on it, where these are apart.
+constexpr float OFF_OWN = 1e-8f;    // of sa: 18 tau, which leaves 69 to the columns
+constexpr float OFF_MIN = -700.0f;  // of ln q_r
+
+// whether a sum off the list, of sums st and sl off and on it, needs that reference
+__device__ __forceinline__ bool off_own(float st, float sl) { return st <= OFF_OWN * (st + sl); }
+
 struct Coefs {
     float base = -INFINITY, W = 0.0f, pr = 0.0f, ks, kh, Al, At, A1, su, sa;  // su: the sum off the list, sa: of all
-    bool soft, used = false;
+    float Rp, A1p;  // the second pass's reference, that of At, and A1 for it
+    float lq = 0.0f;  // ln q_r where su has a reference of its own
+    bool soft, own, used = false;
+    // R, Ro: the reference of s1 and sl, and of su_
     __device__ __forceinline__ Coefs(const DistillArgs& a, const float4* s_lw, int nlw, bool rest, bool soft_on, bool hard,
-                                     float tl, float g_all, float s1, float& st, float sl) {
+                                     float tl, float g_all, float R, float Ro, float s1, float su_, float sl, float it,
+                                     float ct)
+        : su(su_), sa(su_), own(Ro != R) {
         if (rest) {
             base = tl;
             for (int w = 0; w < nlw; w++) {
@@ -137,16 +156,31 @@ struct Coefs {
         soft = used && soft_on;
         ks = g_all * a.alpha * a.tau;
         kh = hard ? g_all * (1.0f - a.alpha) : 0.0f;
-        su = st;
+        Rp = R;
+        A1 = A1p = hard ? __fdividef(kh, s1) : 0.0f;
         if (rest) {
-            st += sl;
+            sa = (own ? su * rescale(Ro, R, ct) : su) + sl;
             if (su > 0.0f) pr = fmaxf(1.0f - W, 0.0f);
+            if (own) {
+                lq = ln_off(su, sa, Ro, R, it);
+                if (!(lq >= OFF_MIN)) pr = 0.0f;
+            }
         }
-        sa = st;
-        const float rt = __fdividef(soft ? ks : 0.0f, st);
-        A1 = hard ? __fdividef(kh, s1) : 0.0f;
+        const float rt = __fdividef(soft ? ks : 0.0f, sa);
         Al = (W + pr) * rt;
-        At = pr > 0.0f ? rt * (W + pr - pr * __fdividef(st, su)) : W * rt;
+        At = W * rt;
+        if (pr > 0.0f) {
+            if (own) {
+                At = Al * rescale(Ro, R, ct) - (soft ? ks * __fdividef(pr, su) : 0.0f);
+                A1p = A1 * rescale(Ro, R, LOG2E);
+                Rp = Ro;
+            } else {
+                At = rt * (W + pr - pr * __fdividef(sa, su));
+            }
+        }
+    }
+    static __device__ __forceinline__ float ln_off(float su, float sa, float Ro, float R, float it) {
+        return (Ro - R) * it + logf(__fdividef(su, sa));
     }
     // an entry's part of sum p (ln p - ln q): teacher's logit t, student's z
     __device__ __forceinline__ float kl(float t, float z, float R, float it) const {
@@ -158,7 +192,7 @@ struct Coefs {
         float l = 0.0f;
         if (soft) {
             for (int w = 0; w < nlw; w++) l += s_ll[w];
-            if (pr > 0.0f) l += pr * (logf(pr) - logf(__fdividef(su, sa)));
+            if (pr > 0.0f) l += pr * (logf(pr) - (own ? lq : logf(__fdividef(su, sa))));
             l *= a.alpha * a.tau * a.tau;
         }
         if (hard) l += (1.0f - a.alpha) * (R + logf(s1) - zy);
@@ -172,7 +206,7 @@ struct Coefs {
     }
     // the target's column, off the list
     __device__ __forceinline__ float target(float z, float R, float ct) const {
-        return A1 * exp_of(z, R, LOG2E) - kh + (soft ? At * exp_of(z, R, ct) : 0.0f);
+        return A1 * exp_of(z, R, LOG2E) - kh + (soft ? At * exp_of(z, Rp, ct) : 0.0f);
     }
 };
 

@@ -151,7 +151,7 @@ template <typename T> struct RowView {
     }
 };
 
-template <typename T>
+template <typename T, bool REST>
 __global__ void __launch_bounds__(DL_THREADS, 2) k_distill_stream(const T* z, T* dz, const DistillArgs a) {
     pdl_wait();
     extern __shared__ __align__(16) char smem[];
@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(DL_THREADS, 2) k_distill_stream(const T* z, T*
     __shared__ int s_flag;  // the target is on the list
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int k = a.k, V = a.V, nlw = (k + 31) / 32, pw = power_of(a.tau);
-    const bool rest = a.t_lse != nullptr, soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
+    constexpr bool rest = REST;
+    const bool soft_on = a.alpha > 0.0f, hard_on = a.targets && a.alpha < 1.0f;
     const float it = 1.0f / a.tau, ct = LOG2E * it, lift = 20.0f / fmaxf(1.0f, it);
     float g_all = a.dscale;
     if (a.scale_dev) g_all *= *a.scale_dev;
@@ -235,23 +236,30 @@ __global__ void __launch_bounds__(DL_THREADS, 2) k_distill_stream(const T* z, T*
             }
         }
         __syncthreads();
+        float Ro;
         {
             const float4 p = lane < N / 32 + (rest ? nlw : 0) ? s_part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             R = p.x; s1 = p.y; st = p.z; sl = p.w;
             merge(R, s1, st, sl, ct, hard, rest);
+            Ro = R;
+            if (rest && off_own(st, sl)) {
+                Ro = lane < N / 32 ? p.x : -INFINITY;  // the other parts are the list's
+                st = lane < N / 32 ? p.z : 0.0f;
+                merge(Ro, st, ct);
+            }
         }
-        const Coefs f(a, s_lw, nlw, rest, soft_on, hard, tl, g_all, s1, st, sl);
+        const Coefs f(a, s_lw, nlw, rest, soft_on, hard, tl, g_all, R, Ro, s1, st, sl, it, ct);
 
         // second pass
         T* drow = dz ? dz + row * a.ld : nullptr;
         if (dz) {
             const float As = f.soft ? f.At : 0.0f;
-            if (f.soft && hard && p2 == 2) view.template gradient<true, true, 2>(tid, N, drow, a.same_phase, R, ct, As, f.A1);
-            else if (f.soft && hard && p2 == 3) view.template gradient<true, true, 3>(tid, N, drow, a.same_phase, R, ct, As, f.A1);
-            else if (f.soft && hard && p2 == 4) view.template gradient<true, true, 4>(tid, N, drow, a.same_phase, R, ct, As, f.A1);
-            else if (f.soft && hard && p2 != 1) view.template gradient<true, true>(tid, N, drow, a.same_phase, R, ct, As, f.A1);
-            else if (f.soft || !hard) view.template gradient<true, false>(tid, N, drow, a.same_phase, R, ct, As + f.A1, 0.0f);
-            else view.template gradient<false, true>(tid, N, drow, a.same_phase, R, ct, 0.0f, f.A1);
+            if (f.soft && hard && p2 == 2) view.template gradient<true, true, 2>(tid, N, drow, a.same_phase, f.Rp, ct, As, f.A1p);
+            else if (f.soft && hard && p2 == 3) view.template gradient<true, true, 3>(tid, N, drow, a.same_phase, f.Rp, ct, As, f.A1p);
+            else if (f.soft && hard && p2 == 4) view.template gradient<true, true, 4>(tid, N, drow, a.same_phase, f.Rp, ct, As, f.A1p);
+            else if (f.soft && hard && p2 != 1) view.template gradient<true, true>(tid, N, drow, a.same_phase, f.Rp, ct, As, f.A1p);
+            else if (f.soft || !hard) view.template gradient<true, false>(tid, N, drow, a.same_phase, f.Rp, ct, As + f.A1p, 0.0f);
+            else view.template gradient<false, true>(tid, N, drow, a.same_phase, f.Rp, ct, 0.0f, f.A1p);
             for (long long p = V + tid; p < a.ld; p += N) drow[p] = Elem<T>::put(0.0f);
         }
         if (warp < nlw && f.soft) {
@@ -274,16 +282,20 @@ __global__ void __launch_bounds__(DL_THREADS, 2) k_distill_stream(const T* z, T*
 }  // namespace
 
 namespace head {
-template <typename T> bool distill_stream(const Launch& L, const void* z, void* dz, DistillArgs a, int G, int N) {
+template <typename T, bool REST>
+static bool stream(const Launch& L, const void* z, void* dz, const DistillArgs& a, const Plan& p) {
     static PerDevice attr;
+    if (!allow_smem(attr, k_distill_stream<T, REST>)) return false;
+    launch_rows(L, k_distill_stream<T, REST>, p, (const T*)z, (T*)dz, a);
+    return true;
+}
+template <typename T> bool distill_stream(const Launch& L, const void* z, void* dz, DistillArgs a, int G, int N) {
     a.Gs = G;
-    if (!allow_smem(attr, k_distill_stream<T>)) return false;
     Plan p;
     p.threads = N;
     p.smem = align16((a.Gs * Elem<T>::EPG + 31) / 32 * 4);
     p.ctas = (int)std::min<long long>(a.M, L.num_sms * (2 * DL_THREADS / N));
-    launch_rows(L, k_distill_stream<T>, p, (const T*)z, (T*)dz, a);
-    return true;
+    return a.t_lse ? stream<T, true>(L, z, dz, a, p) : stream<T, false>(L, z, dz, a, p);
 }
 template bool distill_stream<float>(const Launch&, const void*, void*, DistillArgs, int, int);
 template bool distill_stream<__nv_bfloat16>(const Launch&, const void*, void*, DistillArgs, int, int);

@@ -147,7 +147,8 @@ tt_status tt_op_top_logits(tt_ctx* ctx, tt_dtype dtype, const void* logits, floa
  *   teacher's remaining mass p_r = max(0, 1 - sum_j p_j) is compared with the
  *   student's mass off the list, q_r:
  *     KL = sum_j p_j (ln p_j - ln q_ij) + p_r (ln p_r - ln q_r)
- *   (the last term is left out where q_r is 0)
+ *   (the last term is left out where q_r is below e^-700: no column off the list,
+ *   or all of them masked)
  *   row_loss[r] = alpha tau^2 KL + (1 - alpha) (log sum exp(z) - z[target_r])
  *   dlogits = d row_loss / d z * dscale, pad columns 0
  * mean_loss (may be NULL) receives the mean over the M rows; dscale is

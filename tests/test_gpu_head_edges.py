@@ -181,3 +181,40 @@ def test_distill_of_two_kinds_of_mask(ctx, dtype, V, copies, rest):
     lists = tuple(x.repeat(copies, *([1] * (x.dim() - 1))) for x in (vals, idx, lse))
     for alpha in (0.5, 1.0):
         check_strict(ctx, dtype, z.repeat(copies, 1), V, lists, y.repeat(copies), alpha, 2.0, rest)
+
+
+# ---------------------------------------------------------------- little mass off the list
+GAPS = [0.0, 40.0, 60.0, 80.0, 86.0, 90.0, 120.0, 200.0, 300.0, 640.0, 760.0]
+
+
+def little_off_the_list(dtype, V, ld, k, tau, seed):
+    """A row for each of GAPS, whose listed logits are that many tau above the
+    others, and a teacher with 0.3 of its mass off the list."""
+    M = len(GAPS)
+    z = make_logits(dtype, M, V, ld, seed, pad=math.nan)
+    vals, idx, _ = make_lists(M, V, k, seed + 1)
+    up = torch.tensor(GAPS, device=DEV)[:, None] * tau
+    for r in range(M):
+        c = idx[r][idx[r] >= 0].long()
+        z[r, c] = (z[r, c].float() + up[r]).to(z.dtype)
+    lse = torch.logsumexp(torch.where(idx >= 0, vals.double() / tau, -INF), 1) - math.log(0.7)
+    return z, (vals, idx, lse.float())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,copies", [(100, 1), (500, 1), (900, 4), (6000, 1), (6000, 40), (50257, 1), (50257, 14),
+                                      (60001, 14)])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 1.7, 2.0, 3.0])
+def test_distill_with_little_mass_off_the_list(ctx, dtype, V, copies, tau):
+    """The remaining mass's term and its gradient count however small q_r is,
+    at coefficients as large as a loss scale makes them on a small batch."""
+    M, k = len(GAPS), 5
+    z, lists = little_off_the_list(dtype, V, V + 2, k, tau, 40 + V)
+    y = torch.randint(0, V, (M,), generator=gen(3), device=DEV, dtype=torch.int32)
+    y[::2] = lists[1][::2, 1]
+    y[4] = -1
+    many = z.repeat(copies, 1)
+    lists = tuple(x.repeat(copies, *([1] * (x.dim() - 1))) for x in lists)
+    for alpha in (1.0, 0.6):
+        check_strict(ctx, dtype, many, V, lists, y.repeat(copies) if alpha < 1 else None, alpha, tau, True,
+                     dscale=32768.0 / 16)
