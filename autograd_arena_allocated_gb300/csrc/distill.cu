@@ -622,14 +622,19 @@ k_distill_short(const T* z, T* dz, const DistillArgs a) {
     }
 }
 
-// mean of M row losses: each thread adds rows t, t + 1024, ..., the threads'
-// sums meet in a fixed tree (3 us for 32768)
+// mean of M row losses: each thread adds rows t, t + 1024, ... by compensated
+// summation (Kahan 1965: c is what the last addition lost; there may be 2^21 of
+// them), the threads' sums meet in a fixed tree (3 us for 32768)
 __global__ void __launch_bounds__(1024) k_row_mean(const float* __restrict__ row_loss, int M, float* __restrict__ out,
                                                    int* flags) {
     pdl_enter();
     __shared__ float s_w[32];
-    float s = 0.0f;
-    for (long long i = threadIdx.x; i < M; i += 1024) s += row_loss[i];
+    float s = 0.0f, c = 0.0f;
+    for (long long i = threadIdx.x; i < M; i += 1024) {
+        const float y = row_loss[i] - c, t = s + y;
+        c = isfinite(t) ? (t - s) - y : 0.0f;
+        s = t;
+    }
     s = warp_sum(s);
     if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = s;
     __syncthreads();

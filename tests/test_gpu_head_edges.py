@@ -218,3 +218,26 @@ def test_distill_with_little_mass_off_the_list(ctx, dtype, V, copies, tau):
     for alpha in (1.0, 0.6):
         check_strict(ctx, dtype, many, V, lists, y.repeat(copies) if alpha < 1 else None, alpha, tau, True,
                      dscale=32768.0 / 16)
+
+
+# ---------------------------------------------------------------- the mean of many rows
+@pytest.mark.parametrize("M", [1000, 40000, (1 << 25) + 7])
+def test_mean_loss_of_many_rows(ctx, M):
+    """The mean of losses that no power of two divides: compensated sums (two
+    half steps a thread) and a tree of ten additions, then one division."""
+    z = torch.zeros(M, 2, dtype=torch.float16, device=DEV)
+    z[:, 1] = torch.rand(M, generator=gen(2), device=DEV) * 0.01 - 2.0
+    vals, idx = torch.zeros(M, 1, device=DEV), torch.zeros(M, 1, dtype=torch.int32, device=DEV)
+    row, mean = torch.empty(M, device=DEV), torch.empty(1, device=DEV)
+    ctx.reset()
+    ctx.distill("fp16", z, vals, idx, None, None, None, row, mean, M, 2, 2, 1, 1.0, 1.0, 1.0)
+    ctx.sync()
+    want = float(row.double().mean())
+    assert 0.12 < want < 0.13
+    assert abs(float(mean) - want) <= 14 * U * want
+    row[:] = 7.0
+    z[M // 2, 0] = -INF  # the listed column ruled out: this row's loss is +inf, and so is the mean
+    ctx.distill("fp16", z, vals, idx, None, None, None, row, mean, M, 2, 2, 1, 1.0, 1.0, 1.0)
+    with pytest.raises(api.TTError, match="TT_ERR_NONFINITE"):
+        ctx.sync()
+    assert float(row[M // 2]) == INF and float(mean) == INF
