@@ -27,6 +27,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <unordered_set>
 
 using namespace tt;
@@ -1014,6 +1015,13 @@ static tt_status op_epilogue(tt_ctx* c, const char* what) {
     return TT_OK;
 }
 
+// Lists, indices, scores and losses are read and written as 32-bit words.
+static bool off_words(std::initializer_list<const void*> ptrs) {
+    uintptr_t all = 0;
+    for (const void* p : ptrs) all |= (uintptr_t)p;
+    return (all & 3) != 0;
+}
+
 // What the list operators refuse, as a text; NULL when the arguments are fine.
 static const char* list_refusal(tt_dtype dtype, int V, int k, float tau) {
     if (k < 1 || k > TT_TOP_MAX || k > V) return "k must be 1 .. min(V, TT_TOP_MAX)";
@@ -1344,6 +1352,8 @@ tt_status tt_gpt2_step_distill(tt_ctx* c, const void* params, float* grads, cons
         if (why) return fail(c, TT_ERR_ARG, "step_distill: %s", why);
         if (is_host_pointer(t_vals) || is_host_pointer(t_idx) || (t_lse && is_host_pointer(t_lse)))
             return fail(c, TT_ERR_ARG, "step_distill: the lists must be device memory");
+        if (off_words({t_vals, t_idx, t_lse}) || (targets && !is_host_pointer(targets) && off_words({targets})))
+            return fail(c, TT_ERR_ARG, "step_distill: lists off a 4-byte boundary");
     }
     return step_with(c, params, grads, tokens, targets, &t, B, T, flags, loss_scale, loss);
 }
@@ -1468,6 +1478,7 @@ tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* token
     if (!params || !tokens || !vals || !idx) return fail(c, TT_ERR_ARG, "NULL parameter, token or list pointer");
     if (is_host_pointer(vals) || is_host_pointer(idx) || (lse && is_host_pointer(lse)))
         return fail(c, TT_ERR_ARG, "top_logits: the lists must be device memory");
+    if (off_words({vals, idx, lse})) return fail(c, TT_ERR_ARG, "top_logits: lists off a 4-byte boundary");
     if (B <= 0 || T <= 0 || T > c->cfg.maxT)
         return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
     const tt_gpt2_config& m = c->cfg;
@@ -1809,7 +1820,8 @@ static bool misaligned(tt_dtype dtype, const void* a, const void* b = nullptr) {
 tt_status tt_op_top_logits(tt_ctx* c, tt_dtype dtype, const void* logits, float* vals, int32_t* idx, float* lse, int M,
                            int V, int ld, int k, float tau) {
     TT_HEAD_PROLOGUE();
-    if (!logits || !vals || !idx || M <= 0 || V <= 0 || ld < V || misaligned(dtype, logits)) return fail(c, TT_ERR_ARG, "top_logits: bad arguments");
+    if (!logits || !vals || !idx || M <= 0 || V <= 0 || ld < V || misaligned(dtype, logits) || off_words({vals, idx, lse}))
+        return fail(c, TT_ERR_ARG, "top_logits: bad arguments");
     const char* why = list_refusal(dtype, V, k, tau);
     if (why) return fail(c, TT_ERR_ARG, "top_logits: %s", why);
     const size_t mark = c->off, sb = top_rows_scratch_bytes(dtype, M, V, k);
@@ -1829,7 +1841,9 @@ tt_status tt_op_distill(tt_ctx* c, tt_dtype dtype, const void* logits, const flo
                         const float* t_lse, const int32_t* targets, void* dlogits, float* row_loss, float* mean_loss,
                         int M, int V, int ld, int k, float alpha, float tau, float dscale) {
     TT_HEAD_PROLOGUE();
-    if (!logits || !row_loss || M <= 0 || V <= 0 || ld < V || misaligned(dtype, logits, dlogits)) return fail(c, TT_ERR_ARG, "distill: bad arguments");
+    if (!logits || !row_loss || M <= 0 || V <= 0 || ld < V || misaligned(dtype, logits, dlogits) ||
+        off_words({t_vals, t_idx, t_lse, targets, row_loss, mean_loss}))
+        return fail(c, TT_ERR_ARG, "distill: bad arguments");
     const char* why = distill_refusal(dtype, t_vals, t_idx, targets, V, k, alpha, tau);
     if (why) return fail(c, TT_ERR_ARG, "distill: %s", why);
     {
@@ -1846,7 +1860,7 @@ tt_status tt_op_beam_select(tt_ctx* c, tt_dtype dtype, const void* logits, const
                             int ld, int n, int eos) {
     TT_HEAD_PROLOGUE();
     if (!logits || !scores || !parent || !token || !out_scores || B <= 0 || V <= 0 || ld < V ||
-        misaligned(dtype, logits))
+        misaligned(dtype, logits) || off_words({scores, done, parent, token, out_scores, out_done}))
         return fail(c, TT_ERR_ARG, "beam_select: bad arguments");
     if (K < 1 || K > TT_BEAM_MAX || n < 1 || n > 2 * TT_BEAM_MAX || (long long)n > (long long)K * V)
         return fail(c, TT_ERR_ARG, "beam_select: K must be 1 .. TT_BEAM_MAX, n 1 .. min(2 TT_BEAM_MAX, K V)");
@@ -1874,7 +1888,7 @@ tt_status tt_op_beam_reorder(tt_ctx* c, void* state, const int32_t* parents, int
                              size_t first, size_t count) {
     TT_HEAD_PROLOGUE();
     if (!state || !parents || N <= 0 || B <= 0 || K < 1 || K > TT_BEAM_MAX || row_bytes > (size_t)INT64_MAX / K ||
-        first > row_bytes || count > row_bytes - first)
+        first > row_bytes || count > row_bytes - first || off_words({parents}))
         return fail(c, TT_ERR_ARG, "beam_reorder: bad arguments");
     {
         ProfScope ps(c, PK_BEAM_REORDER, 0.0, 2.0 * N * B * K * (double)count);

@@ -117,7 +117,8 @@ tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int
  * TT_BF16 and TT_FP16 storage; lists, statistics, losses and scores are fp32.
  * Rows are ld elements apart, the columns V..ld-1 are padding that no result
  * depends on; neither ld nor the pointers need more than the element's
- * alignment (without it: TT_ERR_ARG).  They can be recorded (tt_graph.h); a
+ * alignment, 4 bytes for lists, indices, scores and losses (without it:
+ * TT_ERR_ARG).  They can be recorded (tt_graph.h); a
  * recorded call keeps its scratch until the reset.  The context's device has
  * to be the current one (else TT_ERR_STATE).  The pages have no counterpart to these calls: they extend the
  * fused cross entropy (tinytorch 三.5) and the greedy choice (八.3). */

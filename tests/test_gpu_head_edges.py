@@ -22,7 +22,7 @@ import pytest
 import torch
 
 import test_gpu_head as base
-from autograd_arena_allocated_gb300 import api
+from autograd_arena_allocated_gb300 import api, synth
 from test_gpu_head import DEPTH, DEV, INF, TYPES, U, ctx, gen, make_lists, make_logits  # noqa: F401 (ctx: a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -241,3 +241,51 @@ def test_mean_loss_of_many_rows(ctx, M):
     with pytest.raises(api.TTError, match="TT_ERR_NONFINITE"):
         ctx.sync()
     assert float(row[M // 2]) == INF and float(mean) == INF
+
+
+# ---------------------------------------------------------------- refusals
+def test_pointers_off_a_word_are_refused(ctx):
+    """Every 32-bit argument of the four operators and of the model's calls, one
+    at a time two bytes off: an error, and nothing is launched."""
+    M, V, k = 4, 50, 5
+    z = make_logits("fp32", M, V, V, 1)
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device=DEV)
+    f32 = lambda *n: torch.zeros(*n, device=DEV)
+    off = lambda t: t.data_ptr() + 2
+
+    def refused(call, args, names):
+        call(**args)
+        ctx.sync()
+        ctx.reset()
+        n0 = ctx.launches
+        for name in names:
+            with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+                call(**{**args, name: off(args[name])})
+        assert ctx.launches == n0
+        ctx.sync()
+
+    vals, idx, lse = make_lists(M, V, k, 2)
+    lists = lambda: dict(vals=f32(M, k), idx=i32(M, k), lse=f32(M))
+    refused(lambda **a: ctx.top_logits("fp32", **a), dict(logits=z, M=M, V=V, ld=V, k=k, **lists()), ["vals", "idx", "lse"])
+    refused(lambda **a: ctx.distill("fp32", **a),
+            dict(logits=z, t_vals=vals, t_idx=idx, t_lse=lse, targets=i32(M), dlogits=None, row_loss=f32(M), mean_loss=f32(1),
+                 M=M, V=V, ld=V, k=k, alpha=0.5, tau=1.0, dscale=1.0),
+            ["t_vals", "t_idx", "t_lse", "targets", "row_loss", "mean_loss"])
+    refused(lambda **a: ctx.beam_select("fp32", **a),
+            dict(logits=z, scores=f32(2, 2), done=i32(2, 2), parent=i32(2, 2), token=i32(2, 2), out_scores=f32(2, 2),
+                 out_done=i32(2, 2), B=2, K=2, V=V, ld=V, n=2, eos=3),
+            ["scores", "done", "parent", "token", "out_scores", "out_done"])
+    refused(ctx.beam_reorder, dict(state=z.clone(), parents=i32(2, 2), N=1, B=2, K=2, row_bytes=200, first=0, count=200),
+            ["parents"])
+    sh = synth.WORKLOADS["tiny_fp32"].shape
+    p = synth.init_params(sh)
+    _, w = base.device_params(ctx, sh, p, "fp32")
+    B, T = 2, 8
+    tok, _ = synth.token_stream(B, T, sh.V, "uniform")
+    vals, idx, lse = make_lists(B * T, sh.V, k, 1)
+    refused(ctx.step_distill,
+            dict(params=w, grads=f32(p.size), tokens=tok, targets=i32(B * T), t_vals=vals, t_idx=idx, t_lse=lse, k=k,
+                 alpha=0.5, tau=1.0, B=B, T=T), ["targets", "t_vals", "t_idx", "t_lse"])
+    refused(ctx.top_logits_of,
+            dict(params=w, tokens=tok, B=B, T=T, k=k, vals=f32(B * T, k), idx=i32(B * T, k), lse=f32(B * T)),
+            ["vals", "idx", "lse"])
