@@ -654,6 +654,11 @@ static bool cfg_ok(const tt_gpt2_config* m) {
     return true;
 }
 
+// positions are counted in an int
+static bool batch_ok(const tt_gpt2_config* m, int B, int T) {
+    return B > 0 && T > 0 && T <= m->maxT && B <= INT32_MAX / T;
+}
+
 static int padded_vocab(int V) { return ((V + 127) / 128) * 128; }
 
 struct Offsets {
@@ -1251,7 +1256,7 @@ tt_status tt_gpt2_param_offset(const tt_gpt2_config* m, int layer, int which, si
 }
 
 size_t tt_gpt2_arena_bytes(const tt_gpt2_config* m, int B, int T) {
-    if (!cfg_ok(m) || B <= 0 || T <= 0 || T > m->maxT) return 0;
+    if (!cfg_ok(m) || !batch_ok(m, B, T)) return 0;
     tt_ctx c;
     c.cap = (size_t)-1 / 2;
     c.cfg = *m;
@@ -1287,7 +1292,7 @@ static tt_status step_with(tt_ctx* c, const void* params, float* grads, const in
     if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
     if (!params || !grads || !tokens || (!targets && !teacher))
         return fail(c, TT_ERR_ARG, "NULL parameter, gradient or token pointer");
-    if (B <= 0 || T <= 0 || T > c->cfg.maxT)
+    if (!batch_ok(&c->cfg, B, T))
         return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
     const size_t M = (size_t)B * T;
     // exact plan first: nothing is launched if it does not fit
@@ -1479,7 +1484,7 @@ tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* token
     if (is_host_pointer(vals) || is_host_pointer(idx) || (lse && is_host_pointer(lse)))
         return fail(c, TT_ERR_ARG, "top_logits: the lists must be device memory");
     if (off_words({vals, idx, lse})) return fail(c, TT_ERR_ARG, "top_logits: lists off a 4-byte boundary");
-    if (B <= 0 || T <= 0 || T > c->cfg.maxT)
+    if (!batch_ok(&c->cfg, B, T))
         return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
     const tt_gpt2_config& m = c->cfg;
     const char* why = list_refusal(m.dtype, m.V, k, tau);

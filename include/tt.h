@@ -147,7 +147,8 @@ tt_status tt_gpt2_param_offset(const tt_gpt2_config* cfg, int layer, int which,
                                size_t* off, size_t* numel);
 
 /* Exact number of arena bytes tt_gpt2_step needs for a B x T batch (the same
- * allocation sequence, run without launching).  0 for an invalid config. */
+ * allocation sequence, run without launching).  0 for an invalid config or
+ * batch (1 <= T <= maxT, B T within an int). */
 size_t tt_gpt2_arena_bytes(const tt_gpt2_config* cfg, int B, int T);
 
 /* ------------------------------------------------------------- training */

@@ -289,3 +289,18 @@ def test_pointers_off_a_word_are_refused(ctx):
     refused(ctx.top_logits_of,
             dict(params=w, tokens=tok, B=B, T=T, k=k, vals=f32(B * T, k), idx=i32(B * T, k), lse=f32(B * T)),
             ["vals", "idx", "lse"])
+
+
+def test_more_positions_than_an_int_counts_are_refused(ctx):
+    cfg = api.make_config(1, 64, 4, 65, 1024, "fp32")
+    ctx.set_model(cfg)
+    w = torch.zeros(1 << 17, device=DEV)
+    f, i = torch.zeros(8, device=DEV), torch.zeros(8, dtype=torch.int32, device=DEV)
+    ctx.reset()
+    n0 = ctx.launches
+    for B in (1 << 22, 1 << 21, 2 ** 31 - 1):
+        with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+            ctx.top_logits_of(w, i, B, 1024, 1, f, i, None)
+        with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+            ctx.step_distill(w, w, i, i, f, i, None, 1, 0.5, 1.0, B, 1024)
+    assert ctx.launches == n0
