@@ -254,6 +254,7 @@ def test_pointers_off_a_word_are_refused(ctx):
     off = lambda t: t.data_ptr() + 2
 
     def refused(call, args, names):
+        ctx.reset()
         call(**args)
         ctx.sync()
         ctx.reset()
@@ -304,3 +305,49 @@ def test_more_positions_than_an_int_counts_are_refused(ctx):
         with pytest.raises(api.TTError, match="TT_ERR_ARG"):
             ctx.step_distill(w, w, i, i, f, i, None, 1, 0.5, 1.0, B, 1024)
     assert ctx.launches == n0
+
+
+# ---------------------------------------------------------------- long sums
+def long_row(dtype, V, head, masked=0):
+    """A row whose sum has a few terms of 1 and then terms so small that an
+    addition to what has gathered by then loses each of them; before them
+    `masked` columns of the type's lowest value."""
+    z = torch.full((1, V), -14.0, device=DEV, dtype=TYPES[dtype])
+    z[0, :masked] = torch.finfo(TYPES[dtype]).min
+    z[0, masked:masked + head] = 0.0
+    return z
+
+
+@pytest.mark.parametrize("dtype,V,M", [("bf16", 50257, 2000), ("fp32", 50257, 2000), ("bf16", 50257, 3), ("fp16", 300001, 1900),
+                                       ("bf16", 800000, 1900), ("fp32", 400000, 1900), ("fp32", 400000, 1)])
+@pytest.mark.parametrize("head", [1024, 4096])
+@pytest.mark.parametrize("masked", [0, 4096])
+def test_top_logits_of_long_sums(ctx, dtype, V, M, head, masked):
+    """The bound of a sum of n exponentials holds for chains of any length that
+    a row can have."""
+    one = long_row(dtype, V, head, masked)
+    want = torch.logsumexp(one.double(), 1)
+    z = one.expand(M, V).contiguous()
+    vals, idx, lse = torch.empty(M, 1, device=DEV), torch.empty(M, 1, dtype=torch.int32, device=DEV), torch.empty(M, device=DEV)
+    ctx.reset()
+    ctx.top_logits(dtype, z, vals, idx, lse, M, V, V, 1, 1.0)
+    ctx.sync()
+    assert bool((idx == masked).all()) and bool((vals == 0).all())
+    assert bool(((lse.double() - want).abs() <= base.lse_tol(want, 30.0)).all()), float((lse.double() - want).abs().max())
+
+
+@pytest.mark.parametrize("dtype,V,M", [("bf16", 900, 8), ("bf16", 50257, 160), ("fp32", 25000, 160), ("bf16", 3000, 400),
+                                       ("bf16", 50257, 1), ("bf16", 800000, 1), ("bf16", 800000, 60), ("fp32", 400000, 60)])
+@pytest.mark.parametrize("rest", [True, False])
+@pytest.mark.parametrize("masked", [False, True])
+def test_distill_of_long_sums(ctx, dtype, V, M, rest, masked):
+    """The same in every kernel of distillation: the cross entropy of a label
+    whose logit is 0 is the row's log-sum-exp."""
+    head = min(V // 4, 4096)
+    one = long_row(dtype, V, head, head if masked else 0)
+    want = torch.logsumexp(one.double(), 1)
+    z = one.expand(M, V).contiguous()
+    lists = make_lists(M, V, 4, 5)
+    row, _, _ = base.run_distill(ctx, dtype, z, V, lists, torch.full((M,), head, dtype=torch.int32, device=DEV) - (0 if masked else 1),
+                                0.0, 1.0, rest)
+    assert bool(((row.double() - want).abs() <= base.lse_tol(want, 30.0)).all()), float((row.double() - want).abs().max())
