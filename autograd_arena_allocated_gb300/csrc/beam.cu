@@ -29,7 +29,7 @@ using namespace head;
 // log-sum-exp depends in its last bits on how the row lies in memory.  Such a
 // beam takes the log-sum-exp of the first one it equals, where the two are
 // within LSE_EPS: the rounding of arguments of up to 20 log2(e) by half a step
-// (1.3e-6) and of a few hundred additions, whatever the logits' own size is.
+// (1.3e-6) and of 100 additions in a row (6e-6), whatever the logits' own size is.
 //
 // A step's time is the two kernels' latency: the lists of 4 rows in 32 parts
 // and this merge take 12 us, those of 256 fp32 rows (51 MB) in 14 parts 28 us.

@@ -318,12 +318,12 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
         const Slice<T> nx = slice(more ? next : row);
         const int p2 = hard && soft_on ? pw : 0;
         if (worker) {
-            if (!soft_on) sum_pass<T, NT, true, false>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-            else if (!hard || p2 == 1) sum_pass<T, NT, false, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-            else if (p2 == 2) sum_pass<T, NT, true, true, 2>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-            else if (p2 == 3) sum_pass<T, NT, true, true, 3>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-            else if (p2 == 4) sum_pass<T, NT, true, true, 4>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
-            else sum_pass<T, NT, true, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            if (!soft_on) sum_pass<T, NT, CL, true, false>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (!hard || p2 == 1) sum_pass<T, NT, CL, false, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (p2 == 2) sum_pass<T, NT, CL, true, true, 2>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (p2 == 3) sum_pass<T, NT, CL, true, true, 3>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else if (p2 == 4) sum_pass<T, NT, CL, true, true, 4>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
+            else sum_pass<T, NT, CL, true, true>(s, buf, tid, LOG2E, ct, lift, none, R, s1, st);
             if (p2 == 1) s1 = st;
             if (!dz && more) fill<T, NT>(nx, buf, tid);
             merge(R, s1, st, sl, ct, hard, false);

@@ -66,8 +66,7 @@ template <typename T> struct RowView {
 #pragma unroll
             for (int j = 0; j < U; j++) u[j] = masked(i + j * N, u[j]);
             q.look(E::max2(E::max2(E::gmax(u[0]), E::gmax(u[1])), E::max2(E::gmax(u[2]), E::gmax(u[3]))));
-#pragma unroll
-            for (int j = 0; j < U; j++) q.take(u[j]);
+            q.take(u);
         }
         if (i < s.i1) {
             uint4 u[U - 1];

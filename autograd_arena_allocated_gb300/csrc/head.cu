@@ -280,7 +280,7 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
         }
         if (lane == 0) *s_cnt = 0;
         if (PER == 2 && nb % 2) blocks.put(nb, lane, E::put(-INFINITY));
-        Sums<T, true, false> q(ct, ct, lift);
+        Sums<T, true, false, 0, true> q(ct, ct, lift);
         typename E::Max bm = E::to_max(-INFINITY);
         // two stages at a time: the usual form, where both and the two after
         // them are wholly inside the row, and the form that looks at every granule
@@ -328,10 +328,7 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                         cp16<7 * 512>(ring_at, src);
                     }
                     cp_commit();
-                    if (want) {
-#pragma unroll
-                        for (int j = 0; j < TS_U; j++) q.take(u[j]);
-                    }
+                    if (want) q.take(u);
                     if (ub != 4) block(st + h, g4[h], g);
                 }
                 if (ub == 4) blocks.put2(st, lane, g4[0], g4[1]);
@@ -358,13 +355,12 @@ k_top_stream(const T* __restrict__ z, const TopArgs a, int ub_log, int words) {
                     if (st + 2 < S) copy(s, st + 2 + h);
                     else if (more) copy(nx, h);
                     else cp_commit();
-                    if (want) {
-#pragma unroll
-                        for (int j = 0; j < TS_U; j++) q.take(u[j]);
-                    }
+                    if (want) q.take(u);
                     block(st + h, g4, g);
                 }
             }
+            // a chain of additions is 64 stages at most, and a few granules at the row's ends
+            if (want && (st & 62) == 62) q.fold();
         }
         float tmax, sum, none;
         const bool far = q.finish(tmax, sum, none);

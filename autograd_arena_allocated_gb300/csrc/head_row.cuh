@@ -306,11 +306,14 @@ __device__ __forceinline__ float unbias(float R, float c, float nb) { return ex2
 // 4): ca is n cb, and the first sum's terms are the n-th powers of the second's:
 // two softmaxes at one exponential an element (with two, the special-function
 // unit, 32 a cycle and SM, is what a pass waits for).
-template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
+// FOLD: the first sum may be put aside (fold).
+template <typename T, bool SA, bool SB, int PW = 0, bool FOLD = false> struct Sums {
     using E = Elem<T>;
     static constexpr int H = E::EPG / 2;
     typename E::Max m;  // the thread's largest values
     f2 xa, xb, na2, nb2;
+    float ya = 0.0f;  // what was put aside
+    float la, lb;
     float R, lim, na, nb;  // a value above lim moves the reference; -inf: there is none yet
     const float ca, cb, lift;
     bool far;
@@ -320,6 +323,7 @@ template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
     __device__ __forceinline__ void start(float w) {
         m = E::to_max(-INFINITY);
         xa = xb = pk(0.0f, 0.0f);
+        ya = 0.0f;
         R = na = nb = 0.0f;
         lim = -INFINITY;
         far = is_far(w) && w != -INFINITY;
@@ -347,6 +351,7 @@ template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
             const float fb = lim == -INFINITY ? 0.0f : ex2f(mb - nb);
             const float fa = PW ? powi<PW>(fb) : lim == -INFINITY ? 0.0f : ex2f(ma - na);
             if (SA) xa = mul2(xa, pk(fa, fa));
+            if (FOLD) ya *= fa;
             if (SB) xb = mul2(xb, pk(fb, fb));
             na = ma;
             nb = mb;
@@ -386,17 +391,84 @@ template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
             }
         }
     }
-    // one value of a far row, formed without overflow; R is its largest
-    __device__ __forceinline__ void take_far(float z, float& sa, float& sb) const {
+    // The same number of additions for N granules in a shorter chain: a granule's
+    // terms meet in a tree, the granules' sums in a row, and one addition adds them
+    // to the sums.  (Rows that one CTA holds are at most 28 granules a thread and
+    // keep to the other form: 32768 of 50257 16-bit logits 1059 us, 1078 us by this
+    // one.)  The longest chain of additions on the way of a term into a row's sum,
+    // threads' and warps' sums included: 100 in k_top_stream (whose chains start
+    // anew after 64 stages), 125 in k_distill, 75 in k_distill_stream.
+    template <int N> __device__ __forceinline__ void take(const uint4 (&u)[N]) {
+        if (!(SA || SB)) return;
+        const f2 ca2 = pk(ca, ca), cb2 = pk(cb, cb);
+        f2 ta = 0, tb = 0;
+#pragma unroll
+        for (int g = 0; g < N; g++) {
+            f2 e[H], p[H];
+            E::unpack(u[g], e);
+            auto terms = [&](f2 c2, f2 n2) {
+#pragma unroll
+                for (int i = 0; i < H; i++) {
+                    float x, y;
+                    unpk(fma2(e[i], c2, n2), x, y);
+                    p[i] = pk(ex2f(x), ex2f(y));
+                }
+            };
+            auto tree = [&](f2& t) {
+#pragma unroll
+                for (int d = 1; d < H; d *= 2)
+#pragma unroll
+                    for (int i = 0; i < H; i += 2 * d) p[i] = add2(p[i], p[i + d]);
+                t = g ? add2(t, p[0]) : p[0];
+            };
+            if (PW) {
+                f2 q[H];
+                terms(cb2, nb2);
+#pragma unroll
+                for (int i = 0; i < H; i++) q[i] = powi<PW>(p[i]);
+                tree(tb);
+#pragma unroll
+                for (int i = 0; i < H; i++) p[i] = q[i];
+                tree(ta);
+                continue;
+            }
+            if (SA) {
+                terms(ca2, na2);
+                tree(ta);
+            }
+            if (SB) {
+                terms(cb2, nb2);
+                tree(tb);
+            }
+        }
+        if (SA) xa = add2(xa, ta);
+        if (SB) xb = add2(xb, tb);
+    }
+    // what has gathered so far is put aside: a chain starts anew
+    __device__ __forceinline__ void fold() {
+        float x, y;
+        unpk(xa, x, y);
+        ya += x + y;
+        xa = pk(0.0f, 0.0f);
+    }
+    // one value of a far row, formed without overflow; R is its largest.  A
+    // thread's chain is its whole share of the row, so the sums are compensated
+    // (Kahan 1965: l is what the last addition lost).
+    __device__ __forceinline__ void take_far(float z, float& sa, float& sb) {
         const float d = z == R ? 0.0f : z - R;  // inf - inf is a term of 1
-        if (SA) sa += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * ca);
-        if (SB) sb += R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * cb);
+        auto add = [&](float c, float& s, float& l) {
+            const float y = (R == -INFINITY && d == 0.0f ? 0.0f : ex2f(d * c)) - l, t = s + y;
+            l = (t - s) - y;
+            s = t;
+        };
+        if (SA) add(ca, sa, la);
+        if (SB) add(cb, sb, lb);
     }
     // tm: the largest value; R = -inf where there is none above -inf.  True
     // where the row has to be gone through again with take_far (R = tm then).
     __device__ __forceinline__ bool finish(float& tm, float& sa, float& sb) {
         tm = E::value(m);
-        sa = sb = 0.0f;
+        sa = sb = la = lb = 0.0f;
         if (!(SA || SB)) return false;
         // a thread that has met nothing but -inf and values below -FAR has no reference
         if (far || (lim == -INFINITY && tm > -INFINITY)) {
@@ -406,7 +478,7 @@ template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
         float x, y;
         const float ub = unbias(R, cb, nb);
         unpk(xa, x, y);
-        if (SA) sa = (x + y) * (PW ? powi<PW>(ub) : unbias(R, ca, na));
+        if (SA) sa = (FOLD ? x + y + ya : x + y) * (PW ? powi<PW>(ub) : unbias(R, ca, na));
         unpk(xb, x, y);
         if (SB) sb = (x + y) * ub;
         if (tm == -INFINITY) R = -INFINITY;  // no terms, unless they are NaN
@@ -415,7 +487,8 @@ template <typename T, bool SA, bool SB, int PW = 0> struct Sums {
 };
 
 // Granules are taken four at a time, so that the reference is looked at once for four.
-template <typename T, int NT, bool SA, bool SB, int PW = 0>
+// TREE: in the form with the shorter chain.
+template <typename T, int NT, bool TREE, bool SA, bool SB, int PW = 0>
 __device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int tid, float ca, float cb, float lift,
                                          float& tm, float& R, float& sa, float& sb) {
     using E = Elem<T>;
@@ -429,8 +502,12 @@ __device__ __forceinline__ void sum_pass(const Slice<T>& s, const char* buf, int
 #pragma unroll
         for (int j = 0; j < U; j++) u[j] = v[i + j * NT];
         q.look(E::max2(E::max2(E::gmax(u[0]), E::gmax(u[1])), E::max2(E::gmax(u[2]), E::gmax(u[3]))));
+        if (TREE) {
+            q.take(u);
+        } else {
 #pragma unroll
-        for (int j = 0; j < U; j++) q.take(u[j]);
+            for (int j = 0; j < U; j++) q.take(u[j]);
+        }
     }
 #pragma unroll 1
     for (; i < s.n; i += NT) {
