@@ -588,7 +588,7 @@ k_distill_short(const T* z, T* dz, const DistillArgs a) {
                 if (pr > 0.0f) loss += pr * (logf(pr) - Coefs::ln_off(su, st, mo, m, it));
                 loss *= a.alpha * a.tau * a.tau;
             }
-            if (hard) loss += (1.0f - a.alpha) * (m + logf(s1) - zy);
+            if (hard) loss += (1.0f - a.alpha) * ((m - zy) + logf(s1));
             a.row_loss[row] = loss;
         }
         if (dz) {

@@ -195,7 +195,7 @@ struct Coefs {
             if (pr > 0.0f) l += pr * (logf(pr) - (own ? lq : logf(__fdividef(su, sa))));
             l *= a.alpha * a.tau * a.tau;
         }
-        if (hard) l += (1.0f - a.alpha) * (R + logf(s1) - zy);
+        if (hard) l += (1.0f - a.alpha) * ((R - zy) + logf(s1));  // R may be far from 0
         return l;
     }
     __device__ __forceinline__ float listed(float t, float z, float R, float ct, bool hard, bool target) const {

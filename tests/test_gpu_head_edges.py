@@ -351,3 +351,22 @@ def test_distill_of_long_sums(ctx, dtype, V, M, rest, masked):
     row, _, _ = base.run_distill(ctx, dtype, z, V, lists, torch.full((M,), head, dtype=torch.int32, device=DEV) - (0 if masked else 1),
                                 0.0, 1.0, rest)
     assert bool(((row.double() - want).abs() <= base.lse_tol(want, 30.0)).all()), float((row.double() - want).abs().max())
+
+
+# ---------------------------------------------------------------- logits far from 0
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,copies", [(100, 1), (900, 1), (6000, 1), (6000, 100), (50257, 1), (50257, 40), (60001, 40)])
+@pytest.mark.parametrize("rest", [True, False])
+def test_cross_entropy_far_from_zero(ctx, dtype, V, copies, rest):
+    """The cross entropy is a matter of differences: z_y and the log-sum-exp
+    may be thousands, or the type's lowest value, and the loss is as exact."""
+    z = make_logits(dtype, 4, V, V, 3 + V)
+    z[0] = (z[0].float() + 3000.0).to(z.dtype)
+    z[1] = torch.finfo(TYPES[dtype]).min
+    z[2] = (z[2].float() - 20000.0).to(z.dtype)
+    y = torch.randint(0, V, (4,), generator=gen(8), device=DEV, dtype=torch.int32)
+    want = -torch.log_softmax(z.double(), 1).gather(1, y.long()[:, None])[:, 0]
+    lists = make_lists(4 * copies, V, 3, 9)
+    row, _, _ = base.run_distill(ctx, dtype, z.repeat(copies, 1), V, lists, y.repeat(copies), 0.0, 1.0, rest)
+    err = (row.double() - want.repeat(copies)).abs()
+    assert bool((err <= (DEPTH + 34) * U + 4 * U * want.repeat(copies)).all()), float(err.max())
