@@ -1030,7 +1030,8 @@ static bool off_words(std::initializer_list<const void*> ptrs) {
 // What the list operators refuse, as a text; NULL when the arguments are fine.
 static const char* list_refusal(tt_dtype dtype, int V, int k, float tau) {
     if (k < 1 || k > TT_TOP_MAX || k > V) return "k must be 1 .. min(V, TT_TOP_MAX)";
-    if (!(tau > 0.0f) || !std::isfinite(tau) || !std::isfinite(1.0f / tau)) return "tau must be positive and finite";
+    if (!(tau > 0.0f) || !std::isfinite(tau) || !std::isfinite(1.4426950408889634f / tau))
+        return "tau must be positive and finite, and so must log2(e) / tau";
     if (!head_row_ok(dtype, V)) return "V is larger than a row may be";
     return nullptr;
 }
@@ -1040,6 +1041,7 @@ static const char* distill_refusal(tt_dtype dtype, const float* t_vals, const in
     if (!t_vals || !t_idx) return "NULL teacher list";
     if (!(alpha >= 0.0f && alpha <= 1.0f)) return "alpha must be in [0, 1]";
     if (alpha < 1.0f && !targets) return "alpha < 1 needs targets";
+    if (tau > 0.0f && !std::isfinite(tau * tau)) return "tau squared must be finite";
     return list_refusal(dtype, V, k, tau);
 }
 

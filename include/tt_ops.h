@@ -131,7 +131,7 @@ tt_status tt_op_embed_bwd(tt_ctx* ctx, tt_dtype dtype, const void* dx, const int
 /* The k largest logits of each row, in descending order, equal ones by
  * ascending column (-0 equals +0):
  *   vals [M, k] fp32, idx [M, k];  lse [M] fp32 or NULL: log sum_v exp(z_v / tau)
- * over the V columns.  1 <= k <= min(V, TT_TOP_MAX), tau > 0.  A NaN logit
+ * over the V columns.  1 <= k <= min(V, TT_TOP_MAX), tau > 0 (log2(e) / tau within fp32).  A NaN logit
  * stands in the list as -inf and makes the row's lse NaN; a row of -inf has
  * lse = -inf, one with +inf has lse = +inf.  Scratch from the arena where
  * there are few rows: at most TT_TOP_SCRATCH_BYTES. */
@@ -160,7 +160,8 @@ tt_status tt_op_top_logits(tt_ctx* ctx, tt_dtype dtype, const void* logits, floa
  * alpha is 1).  A row with neither has loss 0 and gradient 0, whatever its
  * logits hold.  A target or index outside these ranges, or an index that a row
  * lists twice, raises the bad token flag (tt_ctx_sync: TT_ERR_ARG); what the
- * row then receives is undefined.  0 <= alpha <= 1, tau > 0, 1 <= k <= min(V, TT_TOP_MAX).
+ * row then receives is undefined.  0 <= alpha <= 1, tau > 0 (tau^2 and log2(e) / tau within fp32),
+ * 1 <= k <= min(V, TT_TOP_MAX).
  * Deterministic. */
 tt_status tt_op_distill(tt_ctx* ctx, tt_dtype dtype, const void* logits, const float* t_vals, const int32_t* t_idx,
                         const float* t_lse, const int32_t* targets, void* dlogits, float* row_loss,

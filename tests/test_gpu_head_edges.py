@@ -370,3 +370,23 @@ def test_cross_entropy_far_from_zero(ctx, dtype, V, copies, rest):
     row, _, _ = base.run_distill(ctx, dtype, z.repeat(copies, 1), V, lists, y.repeat(copies), 0.0, 1.0, rest)
     err = (row.double() - want.repeat(copies)).abs()
     assert bool((err <= (DEPTH + 34) * U + 4 * U * want.repeat(copies)).all()), float(err.max())
+
+
+def test_temperatures_whose_arithmetic_overflows_are_refused(ctx):
+    M, V, k = 3, 300, 4
+    z = make_logits("fp32", M, V, V, 1)
+    vals, idx, lse = make_lists(M, V, k, 2)
+    row = torch.empty(M, device=DEV)
+    ctx.reset()
+    n0 = ctx.launches
+    for tau in (4e-39, 1e-40):  # 1 / tau is finite for the first, log2(e) / tau is not
+        with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+            ctx.top_logits("fp32", z, vals.clone(), idx.clone(), None, M, V, V, k, tau)
+    for tau in (4e-39, 2e19, 1e38):
+        with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+            ctx.distill("fp32", z, vals, idx, lse, None, None, row, None, M, V, V, k, 1.0, tau, 1.0)
+    assert ctx.launches == n0
+    ctx.distill("fp32", z, vals, idx, None, None, None, row, None, M, V, V, k, 1.0, 1e18, 1.0)
+    ctx.top_logits("fp32", z, vals.clone(), idx.clone(), row, M, V, V, k, 1e38)
+    ctx.sync()
+    assert bool(((row.double() - math.log(V)).abs() <= base.lse_tol(row.double(), 30.0)).all())
