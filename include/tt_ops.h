@@ -178,7 +178,10 @@ tt_status tt_op_distill(tt_ctx* ctx, tt_dtype dtype, const void* logits, const f
  * done [B, K] or NULL: a beam with done != 0 has the one candidate eos at its
  * unchanged score (its logits are not read); the others count as -inf.  eos:
  * the end token, or -1 for none (done must then be NULL).  Candidates are
- * compared in 64 bits; within a beam they are ordered by logit.  A beam whose
+ * compared in 64 bits; within a beam they are ordered by logit.  Beams of equal
+ * score with the same n best tokens and logits count as equal, and their
+ * candidates tie, where their log-sum-exps differ by no more than 1e-5 (what
+ * fp32 sums can differ by with the place of a row in memory).  A beam whose
  * logits hold NaN or +inf raises the non-finite flag (tt_ctx_sync:
  * TT_ERR_NONFINITE); it, a beam whose logits are all -inf and one whose score
  * is not finite have candidates of -inf only.  1 <= K <= TT_BEAM_MAX,

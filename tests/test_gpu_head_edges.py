@@ -390,3 +390,53 @@ def test_temperatures_whose_arithmetic_overflows_are_refused(ctx):
     ctx.top_logits("fp32", z, vals.clone(), idx.clone(), row, M, V, V, k, 1e38)
     ctx.sync()
     assert bool(((row.double() - math.log(V)).abs() <= base.lse_tol(row.double(), 30.0)).all())
+
+
+# ---------------------------------------------------------------- the model's paths at larger vocabularies
+def wide(monkeypatch, V, C, H, maxT=32):
+    sh = synth.GPT2Shape(2, C, H, V, maxT)
+    monkeypatch.setitem(synth.WORKLOADS, "wide", synth.Workload("wide", sh, 1, 8, "fp32", "uniform"))
+    return sh
+
+
+@pytest.mark.parametrize("V,B,T", [(3000, 2, 17), (3000, 20, 20), (50257, 2, 17), (50257, 10, 20), (60001, 8, 20)])
+@pytest.mark.parametrize("dtype,tol", [("fp32", 1e-4), ("bf16", 2e-2), ("fp16", 2.5e-3)])
+@pytest.mark.parametrize("rest,alpha", [(True, 0.5), (False, 1.0)])
+def test_teacher_and_student_step_of_a_larger_vocabulary(oracle, monkeypatch, V, B, T, dtype, tol, rest, alpha):
+    """The lists from a forward whose rows are cut into parts, then the step in
+    the kernels that hold a row on chip, in a cluster, or stream it; in half
+    with a device loss scale.  Bounds as at the small vocabularies."""
+    wide(monkeypatch, V, 64, 1)
+    base.test_teacher_and_student_step(oracle, "wide", B, T, dtype, tol, rest, alpha)
+
+
+@pytest.mark.parametrize("V,B,T", [(100, 2, 9), (3000, 2, 17), (3000, 20, 20), (50257, 2, 17), (50257, 10, 20), (60001, 8, 20)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_step_distill_loss_scale(ctx, monkeypatch, V, B, T, dtype):
+    """A device loss scale of 2^8 multiplies every gradient by it (a power of
+    two: no other rounding; the sums' order is the step's own)."""
+    sh = wide(monkeypatch, V, 64, 1)
+    p = synth.init_params(sh, jitter=0.05)
+    tok, tgt = synth.token_stream(B, T, V, "uniform", seed=3)
+    k = 9
+    lists = make_lists(B * T, V, k, 4)
+    cfg = api.make_config(sh.L, sh.C, sh.H, sh.V, sh.maxT, dtype)
+    with api.Context(api.arena_bytes(cfg, B, T)) as c:
+        _, w = base.device_params(c, sh, p, dtype)
+        out = []
+        for scale in (None, torch.tensor([256.0], device=DEV)):
+            grads = torch.full((p.size,), math.nan, device=DEV)
+            c.reset()
+            loss = c.step_distill(w, grads, tok, tgt, *lists, k, 0.5, 2.0, B, T, loss_scale=scale)
+            out.append((loss, grads.double()))
+    assert out[0][0] == out[1][0]
+    assert bool(torch.isfinite(out[0][1]).all()) and float(out[0][1].norm()) > 0
+    assert float((out[1][1] - 256 * out[0][1]).norm()) <= 1e-6 * 256 * float(out[0][1].norm())
+
+
+@pytest.mark.parametrize("B,K,n_new,seed", [(1, 4, 6, 13), (1, 4, 6, 16), (1, 12, 5, 14), (5, 4, 5, 11)])
+def test_generate_beam_of_a_whole_vocabulary(oracle, monkeypatch, B, K, n_new, seed):
+    """Rows of 50257 logits are cut into parts, whose lists the recorded step
+    joins; few rows and more than the few-row linear layers take."""
+    wide(monkeypatch, 50257, 64, 4)
+    base.test_generate_beam_matches_a_plain_search(oracle, "wide", B, 5, n_new, K, False, seed)
