@@ -85,8 +85,7 @@ def exact_distill(z, V, lists, targets, alpha, tau, rest):
         grad = grad + torch.where(hard, (1 - alpha) * (s - hot), 0.0)
         bound = bound + torch.where(hard, (1 - alpha) * (s * (2 * DEPTH + 64 + 3 * ls.abs().clamp(max=800.0)) + 2 * hot) * U, 0.0)
         loss = loss + torch.where(hard[:, 0], (1 - alpha) * ce, 0.0)
-        zs = torch.logsumexp(x, 1).abs() + x.gather(1, y.clamp(min=0)[:, None])[:, 0].abs()
-        lb = lb + torch.where(hard[:, 0], (1 - alpha) * (DEPTH + 64 + 4 * zs) * U, 0.0)
+        lb = lb + torch.where(hard[:, 0], (1 - alpha) * (DEPTH + 64 + 4 * (ce.abs() + 30)) * U, 0.0)
     return loss, lb + 4 * U * loss.abs(), grad, bound
 
 
@@ -440,3 +439,38 @@ def test_generate_beam_of_a_whole_vocabulary(oracle, monkeypatch, B, K, n_new, s
     joins; few rows and more than the few-row linear layers take."""
     wide(monkeypatch, 50257, 64, 4)
     base.test_generate_beam_matches_a_plain_search(oracle, "wide", B, 5, n_new, K, False, seed)
+
+
+# ---------------------------------------------------------------- masks, strictly
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,copies", [(65, 1), (700, 1), (3000, 1), (3000, 40), (50257, 1), (50257, 20), (60001, 20)])
+@pytest.mark.parametrize("rest", [True, False])
+def test_distill_masks_strictly(ctx, dtype, V, copies, rest):
+    """Empty lists, rows without a label, masked logits, entries of probability
+    0, one entry that has all the mass or a list that has next to none: every
+    gradient is finite and within its bound, at every weight of the two losses."""
+    M, k = 10, 20
+    low = torch.finfo(TYPES[dtype]).min
+    z = make_logits(dtype, M, V, V + 5, 21, pad=math.nan)
+    vals, idx, lse = make_lists(M, V, k, 22)
+    y = torch.randint(0, V, (M,), generator=gen(6), device=DEV, dtype=torch.int32)
+    idx[0] = -1
+    y[1] = -1
+    free = torch.ones(V, dtype=torch.bool, device=DEV)
+    free[idx[2].long().clamp(min=0)] = False
+    free[y[2].long()] = False
+    z[2, :V][free] = -INF
+    vals[3, 3:7] = -INF
+    z[4, :V] = 0.5
+    z[5, :V] += 300.0
+    z[6, :V] = low / 4
+    z[6, idx[6, 0].long()] = 1.0
+    vals[6, 1:] = -INF
+    z[6, y[6].long()] = 0.5
+    idx[7, 1:] = -1
+    lse[7] = vals[7, 0] / 2.0
+    lse[8] = 200.0
+    z[9, :V] = low
+    lists = tuple(t.repeat(copies, *([1] * (t.dim() - 1))) for t in (vals, idx, lse))
+    for alpha in (0.0, 0.5, 1.0):
+        check_strict(ctx, dtype, z.repeat(copies, 1), V, lists, y.repeat(copies), alpha, 2.0, rest)
