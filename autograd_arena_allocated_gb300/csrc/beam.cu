@@ -158,7 +158,7 @@ k_beam_merge(const unsigned long long* __restrict__ keys, const float2* __restri
 // whose sequence moves nothing end at once.  The traffic is the distinct
 // sources in and the moved slots out; the 124M model's cache at 500 positions,
 // B = 8, K = 4 (737 MB): 116 to 123 us, 88 to 94% of the measured copy rate;
-// 4.4 GB of the 350M model's in fp32: 699 us, 93%.
+// 4.4 GB of the 350M model's in fp32: 699 to 790 us, 82 to 93%.
 template <typename U, int KM>
 __global__ void __launch_bounds__(256)
 k_beam_reorder(char* state, const int32_t* __restrict__ parents, int B, int K, long long row_bytes, long long first,

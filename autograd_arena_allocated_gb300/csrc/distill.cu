@@ -26,9 +26,11 @@ constexpr int LIST_CTA = 64;   // and those that look after its list
 // two exponentials an element and pass the special-function unit (32 a cycle
 // and SM) would take 3.1 of the 4.5 us that such a row's traffic takes an SM,
 // hence the powers (Sums).  32768 rows, k = 64, tau = 2, with hard labels:
-// 1116 us, 5.9 TB/s, 87% of the measured copy rate (75% with t_lse, whose
-// replacement holds up the first pass); then the rows' own chains (barrier,
-// merge, coefficients: about 4 us of a row's 10) are what is left.  Longer rows
+// 1069 us, 6.2 TB/s, 91% of the measured copy rate (8192 half rows with t_lse,
+// whose replacement holds up the first pass, 75%); then the rows' own chains
+// (barrier, merge, coefficients: about 4 us of a row's 10) are what is left.
+// REST: with t_lse, in a kernel of its own (as a flag of one kernel it cost the
+// others 5%: 1121 us).  Longer rows
 // are cut over a cluster only where there are few of them.
 
 struct DistillLayout {
@@ -697,7 +699,7 @@ template <typename T> bool distill(const Launch& L, const void* z, void* dz, Dis
     // 40 such rows 13 us by clusters, 17 us streamed)
     if (cs > 1 && 2LL * a.M * cs > 3LL * L.num_sms) return distill_stream<T>(L, z, dz, a, G, DL_THREADS);
     // a row of at most 40 KB, where there are more than two to an SM (10000 rows
-    // of 3000 16-bit logits 149 us on chip, 70 us streamed; 4000 rows of 20000
+    // of 3000 16-bit logits 149 us on chip, 61 us streamed; 4000 rows of 20000
     // 93 and 74; from 52 KB on, and with fewer rows, no difference or a loss)
     if (G <= 2560 && a.M > 2 * L.num_sms) return distill_stream<T>(L, z, dz, a, G, 128);
     if (!make_plan(p, L.num_sms, a.M, G, cs, bytes)) return false;

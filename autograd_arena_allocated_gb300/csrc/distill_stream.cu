@@ -20,7 +20,7 @@ using namespace head;
 // rate; forwards without the marks 122 us, a cluster of CTAs that hold the row
 // 194 us), 214 us in 32 bits; 999 rows of 50257 in 32 bits 89 us (92 us by
 // clusters).  Short rows, 128 threads: a row's fixed work, at 32 warps an SM;
-// 10000 rows of 3000 16-bit logits 70 us, 4000 of 8192 40 us (149 and 73 on chip).
+// 10000 rows of 3000 16-bit logits 61 us, 4000 of 8192 40 us (149 and 73 on chip).
 template <typename T> __device__ __forceinline__ uint4 drop(uint4 u, uint32_t bits) {
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
     constexpr int PER = 4 / sizeof(T);
