@@ -441,7 +441,8 @@ k_distill(const T* z, T* dz, const DistillArgs a) {
 // length, which is what bounds the shortest: 16384 rows of 65 with k = 8 take
 // 15.5 us (38 us as a warp's form of the kernel above, whose list handling is
 // made for long rows), 30400 rows of 1024 102 us (401 us a CTA a row; with t_lse
-// at five CTAs an SM and 96 registers 105 us, at four and 122 102 us).
+// at five CTAs an SM and 96 registers 105 us, at four and 122 102 us; 30000 of
+// 500 with t_lse at six CTAs 48.8 us, at seven and 72 registers 47.6 us).
 constexpr int DS_WARPS = 4;
 constexpr uint32_t DS_UNLISTED = 0x7FC0DEADu;  // a NaN that no arithmetic makes
 
@@ -471,7 +472,7 @@ __device__ __noinline__ void short_gradient(const T* zr, T* dr, const uint32_t* 
 }
 
 template <typename T, int E, bool REST>
-__global__ void __launch_bounds__(DS_WARPS * 32, E <= 4 ? 8 : E <= 16 ? 6 : REST ? 4 : 5)
+__global__ void __launch_bounds__(DS_WARPS * 32, E <= 4 ? 8 : E <= 16 ? (REST ? 7 : 6) : REST ? 4 : 5)
 k_distill_short(const T* z, T* dz, const DistillArgs a) {
     pdl_enter();
     __shared__ uint32_t s_all[DS_WARPS][32 * E];
