@@ -89,6 +89,12 @@ SIGNATURES = {
     "tt_op_distill": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _f, _f]),
     "tt_op_beam_select": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i]),
     "tt_op_beam_reorder": (_st, [_vp, _vp, _vp, _i, _i, _i, _sz, _sz, _sz]),
+    "tt_op_logprobs": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _f]),
+    "tt_op_policy": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _f, _f, _f, _f]),
+    "tt_op_preference": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _f, _f, _i, _f,
+                               _f]),
+    "tt_op_group_attention_fwd": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i]),
+    "tt_op_group_attention_bwd": (_st, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i]),
     "tt_linear_bwd_dw_noalloc": (_st, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i]),
     # tt_graph.h (node handles are int32; negative = tt_status)
     "tt_node_new": (_i, [_vp, _i, C.POINTER(_i), _i]),

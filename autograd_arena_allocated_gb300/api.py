@@ -320,6 +320,32 @@ class Context:
     def beam_reorder(self, state, parents, N, B, K, row_bytes, first, count):
         self._check(lib().tt_op_beam_reorder(self.h, _ptr(state), _ptr(parents), N, B, K, row_bytes, first, count))
 
+    def logprobs(self, dtype, logits, targets, logp, lse, M, V, ld, tau=1.0):
+        self._check(lib().tt_op_logprobs(self.h, DTYPES[dtype], _ptr(logits), _ptr(targets), _ptr(logp), _ptr(lse), M, V,
+                                         ld, float(tau)))
+
+    def policy(self, dtype, logits, targets, old_logp, ref_logp, adv, weight, dlogits, logp, row_loss, mean_loss, M, V, ld,
+               eps_low, eps_high, beta, tau, dscale):
+        self._check(lib().tt_op_policy(self.h, DTYPES[dtype], _ptr(logits), _ptr(targets), _ptr(old_logp), _ptr(ref_logp),
+                                       _ptr(adv), _ptr(weight), _ptr(dlogits), _ptr(logp), _ptr(row_loss),
+                                       _ptr(mean_loss), M, V, ld, float(eps_low), float(eps_high), float(beta),
+                                       float(tau), float(dscale)))
+
+    def preference(self, dtype, logits, targets, ref_logp, spans, dlogits, seq_logp, pair_loss, mean_loss, M, V, ld, pairs,
+                   beta, gamma, smoothing, mean, tau, dscale):
+        self._check(lib().tt_op_preference(self.h, DTYPES[dtype], _ptr(logits), _ptr(targets), _ptr(ref_logp),
+                                           _ptr(spans), _ptr(dlogits), _ptr(seq_logp), _ptr(pair_loss),
+                                           _ptr(mean_loss), M, V, ld, pairs, float(beta), float(gamma),
+                                           float(smoothing), int(bool(mean)), float(tau), float(dscale)))
+
+    def group_attention_fwd(self, dtype, qkv, starts, y, lse, B, T, C_, H, K):
+        self._check(lib().tt_op_group_attention_fwd(self.h, DTYPES[dtype], _ptr(qkv), _ptr(starts), _ptr(y), _ptr(lse), B,
+                                                    T, C_, H, K))
+
+    def group_attention_bwd(self, dtype, qkv, starts, y, lse, dy, dqkv, B, T, C_, H, K):
+        self._check(lib().tt_op_group_attention_bwd(self.h, DTYPES[dtype], _ptr(qkv), _ptr(starts), _ptr(y), _ptr(lse),
+                                                    _ptr(dy), _ptr(dqkv), B, T, C_, H, K))
+
     # -------------------------------------------------------------- generic graph (tt_graph.h)
     def _node(self, h: int) -> int:
         if h < 0:

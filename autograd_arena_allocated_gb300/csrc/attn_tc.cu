@@ -30,7 +30,15 @@
 //     dP^T = V dO_j^T; P^T and dS^T; dV += P^T dO_j, dK += dS^T Q_j in TMEM
 //     (Q_j and dO_j, loaded K-major, are read again as MN-major operands).
 // Every wait is bounded (FLAG_TIMEOUT), as in the GEMM.
+//
+// GRP: the same kernels over groups of answers that share a prompt (group.cuh).
+// The tile goes past the blocks that it needs only, blocks that are not seen
+// whole take a 64-bit mask a row, and tiles of padding write zeros.  Padding may
+// hold anything: a masked probability is 0, and 0 times a NaN is a NaN, so the
+// block in which the padding begins has its rows of the operand whose rows the
+// product sums over (V; K; Q and dO) cleared in shared memory.
 #include "tt_internal.h"
+#include "group.cuh"
 #include "tc_ptx.cuh"
 
 #include <math.h>
@@ -98,6 +106,67 @@ __device__ __forceinline__ void init_done() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// The 64-wide blocks that a 128-row tile of queries (keys) goes past, and which
+// of them are masked: causal attention over T positions, or a group.
+template <bool GRP> struct Tile;
+template <> struct Tile<false> {
+    int qt, end, n;
+    __device__ __forceinline__ Tile(const int32_t*, int, int, int T, int qt_)
+        : qt(qt_), end(T), n(min(2 * qt_ + 2, (T + BN - 1) / BN)) {}
+    __device__ __forceinline__ int block(int j) const { return j; }
+    __device__ __forceinline__ bool masked(int j, int) const { return j >= 2 * qt; }
+    __device__ __forceinline__ void check(int, int, int, int*) const {}
+    __device__ __forceinline__ int start_of(int) const { return 0; }
+    __device__ __forceinline__ unsigned long long keys(int, int, int) const { return 0; }
+};
+template <> struct Tile<true> : group::Group {
+    int q0, n, npre, skip, last_start;
+    __device__ __forceinline__ Tile(const int32_t* starts, int b, int K, int T, int qt)
+        : group::Group(starts, b, K, T), q0(qt * BQ) {
+        if (q0 >= end) return;
+        const group::QueryTile t(*this, q0, BQ);
+        n = t.n; npre = t.npre; skip = t.skip; last_start = t.last_start;
+    }
+    __device__ __forceinline__ int block(int j) const { return j < npre ? j : j + skip; }
+    __device__ __forceinline__ bool masked(int, int k0) const {
+        return !((k0 + BN <= P || k0 >= last_start) && k0 + BN - 1 <= q0);
+    }
+};
+template <bool GRP> struct KTile;
+template <> struct KTile<false> {
+    int end, n;
+    __device__ __forceinline__ KTile(const int32_t*, int, int, int T, int kt) : end(T), n((T + BN - 1) / BN - 2 * kt) {}
+    __device__ __forceinline__ bool masked(int i, int) const { return i < 2; }
+    __device__ __forceinline__ int end_of(int) const { return 0; }
+    __device__ __forceinline__ unsigned long long queries(int, int, int) const { return 0; }
+};
+template <> struct KTile<true> : group::Group {
+    int n, last, min_end;
+    __device__ __forceinline__ KTile(const int32_t* starts, int b, int K, int T, int kt) : group::Group(starts, b, K, T) {
+        if (kt * BQ >= end) return;
+        const group::KeyTile t(*this, kt * BQ, BQ);
+        n = t.n; last = t.last; min_end = t.min_end;
+    }
+    __device__ __forceinline__ bool masked(int, int q0) const { return !(q0 >= last && q0 + BN <= min_end); }
+};
+
+// 64 columns at `col` of the rows first..last - 1 of a tile of padding, and its
+// column sums, where they are wanted (bpart: the tile's row of 3C)
+__device__ __forceinline__ void clear_padding(bf16* dqkv, int row0, int first, int last, int C, int col, float* bpart) {
+    for (int i = first * 8 + (int)threadIdx.x; i < last * 8; i += blockDim.x)
+        reinterpret_cast<uint4*>(dqkv + (long long)(row0 + (i >> 3)) * 3 * C + col)[i & 7] = make_uint4(0, 0, 0, 0);
+    if (bpart && threadIdx.x < D) bpart[col + threadIdx.x] = 0.0f;
+}
+__device__ __forceinline__ void zero_out32(bf16* dst) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// the rows from `from` on of a 64-row tile are cleared by `threads` threads
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int tid, int threads) {
+    for (int i = from * 8 + tid; i < BN * 8; i += threads) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // ================================================================== forward
 // The softmax warps never wait for the P.V product of the previous block in
 // the common case: P is double-buffered in shared memory (buffer j & 1, with
@@ -112,11 +181,11 @@ constexpr int F_BAR = F_P + 2 * T128;
 constexpr int F_SMEM = F_BAR + 256 + 1024;
 constexpr uint32_t F_TMEM = 128;    // S: cols 0..63, O: 64..127
 
-template <bool F16>
+template <bool F16, bool GRP>
 __global__ void __launch_bounds__(THREADS, 3)
 k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
               bf16* __restrict__ y, float* __restrict__ lse, int T, int C, int H, int nbh, int* flags,
-              long long wl) {
+              long long wl, const int32_t* __restrict__ starts, int K) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = align1024(smem_raw);
     uint64_t* bars = (uint64_t*)(sm + F_BAR);
@@ -138,9 +207,21 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     const int nqt = gridDim.y;
     const int qt = nqt - 1 - (int)blockIdx.y;  // longest rows first within the band
     const int b = bh / H, h = bh % H;
-    const int nkv = min(2 * qt + 2, (T + BN - 1) / BN);
     const int row0 = b * T;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (GRP) pdl_enter();  // the lists of starts are read from here on
+    const Tile<GRP> tile(starts, b, K, T, qt);
+    if (GRP) {
+        if (qt == 0 && h == 0) tile.check(threadIdx.x, THREADS, T, flags);
+        if (tile.end <= qt * BQ) {  // padding only (uniform over the CTA)
+            const int last = min(qt * BQ + BQ, T);
+            for (int i = qt * BQ * 8 + threadIdx.x; i < last * 8; i += THREADS)
+                reinterpret_cast<uint4*>(y + (long long)(row0 + (i >> 3)) * C + h * D)[i & 7] = make_uint4(0, 0, 0, 0);
+            for (int q = qt * BQ + threadIdx.x; q < last; q += THREADS) lse[((long long)b * H + h) * T + q] = 0.0f;
+            return;
+        }
+    }
+    const int nkv = tile.n;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -165,7 +246,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
+    if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
         if (lane == 0) {
@@ -180,7 +261,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 const int st = j & 1;
                 if (!mbar_wait(&k_empty[st], ((j >> 1) & 1) ^ 1, abort_flag, flags, 0x100 + 1, wl)) return false;
                 mbar_expect_tx(&k_full[st], T64);
-                tma_load_2d(smem_u32(sm + F_K + st * T64), &tk, &k_full[st], xk, row0 + j * BN);
+                tma_load_2d(smem_u32(sm + F_K + st * T64), &tk, &k_full[st], xk, row0 + tile.block(j) * BN);
                 ++issued_k;
                 return true;
             };
@@ -188,7 +269,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             for (int j = 0; j < nkv && ok; j++) {
                 if (!mbar_wait(v_empty, (j & 1) ^ 1, abort_flag, flags, 0x100 + 2, wl)) { ok = false; break; }
                 mbar_expect_tx(v_full, T64);
-                tma_load_2d(smem_u32(sm + F_V), &tk, v_full, xv, row0 + j * BN);
+                tma_load_2d(smem_u32(sm + F_V), &tk, v_full, xv, row0 + tile.block(j) * BN);
                 ++issued_v;
                 if (j + 2 < nkv && !load_k(j + 2)) { ok = false; break; }
             }
@@ -251,13 +332,19 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         // rescaled in place -- only when some row of the warp exceeds it by
         // more than 8 (P <= 2^8 otherwise); the decision is a warp vote since
         // the TMEM loads and stores of O are warp-collective
-        float m = -INFINITY, l = 0.0f;
+        // (GRP: a row may see nothing of its first blocks; m then starts below
+        // any score, but finite, so that no difference is infinity minus infinity)
+        float m = GRP ? -3e38f : -INFINITY, l = 0.0f;
         bool ok = true;
+        const int st0 = GRP ? tile.start_of(q) : 0;
         for (int j = 0; j < nkv; j++) {
             if (!mbar_wait_warp(s_full, j & 1, abort_flag, flags, 0x100 + 8, wl)) { ok = false; break; }
             tc_fence_after();
-            const bool diag = (j >= 2 * qt);
-            const int kq = q - j * BN;  // on the diagonal, key columns > kq are masked
+            const int kb = tile.block(j) * BN;
+            const bool diag = tile.masked(j, kb);
+            const int kq = q - kb;  // on the diagonal, key columns > kq are masked
+            const unsigned long long seen = GRP && diag ? tile.keys(q, st0, kb) : 0ull;
+            const uint32_t seen0 = (uint32_t)seen, seen1 = (uint32_t)(seen >> 32);
             uint32_t w0[32], w1[32];
             tmem_ld32x2(tl, w0, tl + 32, w1);
             tc_fence_before();
@@ -275,6 +362,13 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
+                    if (GRP) {
+                        if (seen0 >> e & 1u) mq[0] = fmaxf(mq[0], __uint_as_float(w0[e]));
+                        if (seen0 >> (e + 1) & 1u) mq[1] = fmaxf(mq[1], __uint_as_float(w0[e + 1]));
+                        if (seen1 >> e & 1u) mq[2] = fmaxf(mq[2], __uint_as_float(w1[e]));
+                        if (seen1 >> (e + 1) & 1u) mq[3] = fmaxf(mq[3], __uint_as_float(w1[e + 1]));
+                        continue;
+                    }
                     if (e <= kq) mq[0] = fmaxf(mq[0], __uint_as_float(w0[e]));
                     if (e + 1 <= kq) mq[1] = fmaxf(mq[1], __uint_as_float(w0[e + 1]));
                     if (32 + e <= kq) mq[2] = fmaxf(mq[2], __uint_as_float(w1[e]));
@@ -306,7 +400,10 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 for (int e = 0; e < 32; e += 2) {
                     const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), sl2, nm);
                     float2 p = make_float2(ex2(x.x), ex2(x.y));
-                    if (diag) {
+                    if (GRP && diag) {
+                        if (!((c ? seen1 : seen0) >> e & 1u)) p.x = 0.0f;
+                        if (!((c ? seen1 : seen0) >> (e + 1) & 1u)) p.y = 0.0f;
+                    } else if (diag) {
                         if (32 * c + e > kq) p.x = 0.0f;
                         if (32 * c + e + 1 > kq) p.y = 0.0f;
                     }
@@ -338,6 +435,16 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 l *= corr;
             }
             l += rs;
+            if (GRP && j == nkv - 1 && kb + BN > tile.end) {
+                // V_j has arrived once its barrier's phase is over; that the
+                // phase before it is, P_{j-1} V_{j-1} being done tells
+                if ((j > 0 && !mbar_wait_warp(&o_full[pb ^ 1], ((j - 1) >> 1) & 1, abort_flag, flags, 0x100 + 12, wl)) ||
+                    !mbar_wait_warp(v_full, j & 1, abort_flag, flags, 0x100 + 13, wl)) {
+                    ok = false;
+                    break;
+                }
+                clear_rows(sm + F_V, tile.end - kb, threadIdx.x - 64, 128);
+            }
             tc_fence_before();  // orders the TMEM stores of a rescale before the next MMA
             fence_proxy_async_smem();
             mbar_arrive(&p_full[pb]);
@@ -353,6 +460,12 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             tmem_ld32(tl + BN + 32, v);
 #pragma unroll
             for (int d = 0; d < 32; d++) o[32 + d] = __uint_as_float(v[d]);
+            if (GRP && q >= tile.end) {
+#pragma unroll
+                for (int d = 0; d < D; d++) o[d] = 0.0f;
+                m = 0.0f;
+                l = 1.0f;
+            }
             if (q < T) {
                 store_out64<F16>(y + (long long)(row0 + q) * C + h * D, o, 1.0f / l);
                 lse[((long long)b * H + h) * T + q] = (m + log2f(l)) * LN2;
@@ -445,12 +558,13 @@ constexpr int Q_SMEM = Q_BAR + 256 + 1024;
 constexpr uint32_t Q_TMEM = 256;         // S 0..63, dP 64..127, dS[2] 128..191, dQ 192..255
 constexpr uint32_t Q_TS = 0, Q_TP = 64, Q_TDS = 128, Q_TACC = 192;
 
-template <bool F16>
+template <bool F16, bool GRP>
 __global__ void __launch_bounds__(BW_THREADS, 2)
 k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap to, const bf16* __restrict__ y,
                  const float* __restrict__ lse, float* __restrict__ Dlt, bf16* __restrict__ dqkv,
-                 float* __restrict__ bpart, int T, int C, int H, int nbh, int* flags, long long wl) {
+                 float* __restrict__ bpart, int T, int C, int H, int nbh, int* flags, long long wl,
+                 const int32_t* __restrict__ starts, int K) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = align1024(smem_raw);
     uint64_t* bars = (uint64_t*)(sm + Q_BAR);
@@ -471,9 +585,19 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     const int nqt = gridDim.y;
     const int qt = nqt - 1 - (int)blockIdx.y;  // longest rows first within the band
     const int b = bh / H, h = bh % H;
-    const int nkv = min(2 * qt + 2, (T + BN - 1) / BN);
     const int row0 = b * T;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (GRP) pdl_enter();
+    const Tile<GRP> tile(starts, b, K, T, qt);
+    if (GRP) {
+        if (qt == 0 && h == 0) tile.check(threadIdx.x, BW_THREADS, T, flags);
+        if (tile.end <= qt * BQ) {
+            clear_padding(dqkv, row0, qt * BQ, min(qt * BQ + BQ, T), C, h * D,
+                          bpart ? bpart + ((long long)b * nqt + qt) * 3 * C : nullptr);
+            return;
+        }
+    }
+    const int nkv = tile.n;
 
     if (threadIdx.x == 0) {
         mbar_init(qo_full, 1);
@@ -497,7 +621,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
+    if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
         if (lane == 0) {
@@ -511,12 +635,12 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const int ks = j % Q_KST, kr = j / Q_KST;
                 if (!mbar_wait(&k_empty[ks], (kr & 1) ^ 1, abort_flag, flags, 0x200 + 1, wl)) { ok = false; break; }
                 mbar_expect_tx(&k_full[ks], T64);
-                tma_load_2d(smem_u32(sm + Q_K + ks * T64), &tk, &k_full[ks], xk, row0 + j * BN);
+                tma_load_2d(smem_u32(sm + Q_K + ks * T64), &tk, &k_full[ks], xk, row0 + tile.block(j) * BN);
                 ++issued_k;
                 const int vs = j & 1;
                 if (!mbar_wait(&v_empty[vs], ((j >> 1) & 1) ^ 1, abort_flag, flags, 0x200 + 10, wl)) { ok = false; break; }
                 mbar_expect_tx(&v_full[vs], T64);
-                tma_load_2d(smem_u32(sm + Q_V + vs * T64), &tk, &v_full[vs], xv, row0 + j * BN);
+                tma_load_2d(smem_u32(sm + Q_V + vs * T64), &tk, &v_full[vs], xv, row0 + tile.block(j) * BN);
                 ++issued_v;
             }
             if (!ok) {  // let issued copies land before the CTA exits
@@ -576,7 +700,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         const int half = (warp - 2) >> 2;
         const int r = quarter * 32 + lane;
         const int q = qt * BQ + r;
-        const bool qv = q < T;
+        const bool qv = q < tile.end;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         const long long bhl = (long long)b * H + h;
         float* dpart = reinterpret_cast<float*>(sm + Q_DP);
@@ -610,11 +734,14 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             if (qv && half == 0) Dlt[bhl * T + q] = Dq;
         }
         const float Lq = qv ? lse[bhl * T + q] * LOG2E : 0.0f;
+        const int st0 = GRP ? tile.start_of(q) : 0;
         for (int j = 0; j < nkv && ok; j++) {
             if (!mbar_wait_warp(s_full, j & 1, abort_flag, flags, 0x200 + 7, wl)) { ok = false; break; }
             tc_fence_after();
-            const bool diag = (j >= 2 * qt);
-            const int kq = q - j * BN - 32 * half;  // on the diagonal, this half's columns > kq are masked
+            const int kb = tile.block(j) * BN;
+            const bool diag = tile.masked(j, kb);
+            const int kq = q - kb - 32 * half;  // on the diagonal, this half's columns > kq are masked
+            const uint32_t seen = GRP && diag ? (uint32_t)(tile.keys(q, st0, kb) >> (32 * half)) : 0u;
             uint32_t sw[32], pw[32];
             tmem_ld32x2(tl + Q_TS + 32 * half, sw, tl + Q_TP + 32 * half, pw);
             // dS = P o (dP - D), packed bf16
@@ -626,7 +753,10 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(sw[e]), __uint_as_float(sw[e + 1])), sl2, nl);
                 const float2 dd = __fadd2_rn(make_float2(__uint_as_float(pw[e]), __uint_as_float(pw[e + 1])), nd);
                 float2 d = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), dd);
-                if (diag) {
+                if (GRP && diag) {
+                    if (!(seen >> e & 1u)) d.x = 0.0f;
+                    if (!(seen >> (e + 1) & 1u)) d.y = 0.0f;
+                } else if (diag) {
                     if (e > kq) d.x = 0.0f;
                     if (e + 1 > kq) d.y = 0.0f;
                 }
@@ -634,6 +764,10 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             }
             tmem_st16(tl + Q_TDS + 32 * (j & 1) + 16 * half, pk);
             tmem_st_wait();
+            if (GRP && j == nkv - 1 && kb + BN > tile.end) {  // S_j is done, dS_j K_j is to come
+                clear_rows(sm + Q_K + (j % Q_KST) * T64, tile.end - kb, threadIdx.x - 64, BW_ROWS);
+                fence_proxy_async_smem();
+            }
             tc_fence_before();
             warp_arrive(ds_full, lane);
         }
@@ -648,6 +782,8 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 store_out32<F16>(dqkv + (long long)(row0 + q) * 3 * C + h * D + 32 * half, w, 0.125f);
 #pragma unroll
                 for (int d = 0; d < 32; d++) cv[d] = __uint_as_float(w[d]) * 0.125f;
+            } else if (GRP && q < T) {
+                zero_out32(dqkv + (long long)(row0 + q) * 3 * C + h * D + 32 * half);
             }
         }
         if (bpart)  // the qkv bias gradient's partial: this tile's column sums of dQ
@@ -678,12 +814,12 @@ constexpr int K_SMEM = K_BAR + 256 + 1024;
 constexpr uint32_t K_TMEM = 256;         // S^T 0..63, dP^T 64..127, dV 128..191, dK 192..255
 constexpr uint32_t K_TS = 0, K_TP = 64, K_TV = 128, K_TK = 192;
 
-template <bool F16>
+template <bool F16, bool GRP>
 __global__ void __launch_bounds__(BW_THREADS, 2)
 k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap to, const float* __restrict__ lse,
                    const float* __restrict__ Dlt, bf16* __restrict__ dqkv, float* __restrict__ bpart, int T,
-                   int C, int H, int nbh, int* flags, long long wl) {
+                   int C, int H, int nbh, int* flags, long long wl, const int32_t* __restrict__ starts, int K) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = align1024(smem_raw);
     uint64_t* bars = (uint64_t*)(sm + K_BAR);
@@ -702,10 +838,17 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const int kt = (int)blockIdx.y;  // key tile; low tiles see the most query blocks
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
-    const int nqb = (T + BN - 1) / BN;
-    const int j0 = 2 * kt;
-    const int nq = nqb - j0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (GRP) pdl_enter();
+    const KTile<GRP> tile(starts, b, K, T, kt);
+    if (GRP && tile.end <= kt * BQ) {
+        float* brow = bpart ? bpart + ((long long)b * gridDim.y + kt) * 3 * C : nullptr;
+        clear_padding(dqkv, row0, kt * BQ, min(kt * BQ + BQ, T), C, C + h * D, brow);
+        clear_padding(dqkv, row0, kt * BQ, min(kt * BQ + BQ, T), C, 2 * C + h * D, brow);
+        return;
+    }
+    const int j0 = 2 * kt;
+    const int nq = tile.n;
 
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
@@ -725,7 +868,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
+    if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
         if (lane == 0) {
@@ -804,10 +947,11 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         float Ln, Dn;
         auto fetch = [&](int i) {
             const int qq = (j0 + i) * BN + 32 * half + lane;
-            Ln = qq < T ? __ldg(lrow + qq) * LOG2E : INFINITY;
-            Dn = qq < T ? __ldg(drow + qq) : 0.0f;
+            Ln = qq < tile.end ? __ldg(lrow + qq) * LOG2E : INFINITY;
+            Dn = qq < tile.end ? __ldg(drow + qq) : 0.0f;
         };
         fetch(0);
+        const int kend = GRP && key < tile.end ? tile.end_of(key) : 0;
         for (int i = 0; i < nq; i++) {
             const int j = j0 + i;
             __syncwarp();  // the previous block's reads of the slice are done
@@ -817,8 +961,9 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (i + 1 < nq) fetch(i + 1);
             if (!mbar_wait_warp(st_full, i & 1, abort_flag, flags, 0x300 + 6, wl)) { ok = false; break; }
             tc_fence_after();
-            const bool diag = (i < 2);  // query blocks that overlap this key tile
+            const bool diag = tile.masked(i, j * BN);  // else all keys are seen by the whole block
             const int q0 = j * BN + 32 * half;
+            const uint32_t seen = GRP && diag ? (uint32_t)(tile.queries(key, kend, j * BN) >> (32 * half)) : 0u;
             uint32_t sw[32], dw[32];
             tmem_ld32x2(tl + K_TS + 32 * half, sw, tl + K_TP + 32 * half, dw);
             uint32_t pk[16], dk[16];
@@ -831,18 +976,30 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(sw[e]), __uint_as_float(sw[e + 1])),
                                             make_float2(SL2, SL2), L2);
                 float2 p = make_float2(ex2(x.x), ex2(x.y));
-                if (diag) {
+                if (GRP && diag) {
+                    if (!(seen >> e & 1u)) p.x = 0.0f;
+                    if (!(seen >> (e + 1) & 1u)) p.y = 0.0f;
+                } else if (diag) {
                     if (q0 + e < key) p.x = 0.0f;
                     if (q0 + e + 1 < key) p.y = 0.0f;
                 }
                 pk[e >> 1] = pack2<F16>(p.x, p.y);
-                const float2 d =
+                float2 d =
                     __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(dw[e]), __uint_as_float(dw[e + 1])), D2));
+                if (GRP && diag) {  // dP may be NaN where dO is padding
+                    if (!(seen >> e & 1u)) d.x = 0.0f;
+                    if (!(seen >> (e + 1) & 1u)) d.y = 0.0f;
+                }
                 dk[e >> 1] = pack2<F16>(d.x, d.y);
             }
             tmem_st16(tl + K_TS + 32 * half, pk);
             tmem_st16(tl + K_TP + 32 * half, dk);
             tmem_st_wait();
+            if (GRP && j * BN + BN > tile.end) {  // S^T_i and dP^T_i are done, the products with Q_i and dO_i to come
+                clear_rows(sm + K_Q + (i % K_ST) * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
+                clear_rows(sm + K_O + (i % K_ST) * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
+                fence_proxy_async_smem();
+            }
             tc_fence_before();
             warp_arrive(ps_full, lane);
         }
@@ -860,10 +1017,12 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (got) {
                 uint32_t w[32];
                 tmem_ld32(tl + (which ? K_TK : K_TV) + 32 * half, w);
-                if (key < T) {
+                if (key < tile.end) {
                     store_out32<F16>(base + (which ? C : 2 * C), w, scale);
 #pragma unroll
                     for (int d = 0; d < 32; d++) v[d] = __uint_as_float(w[d]) * scale;
+                } else if (GRP && key < T) {
+                    zero_out32(base + (which ? C : 2 * C));
                 }
             }
             if (brow) tile_colsum(v, reinterpret_cast<float*>(sm + K_CS), brow + (which ? C : 2 * C), half, quarter, lane);
@@ -882,15 +1041,15 @@ bool attention_tc_eligible(bool bf16, int C, int H) {
     return bf16 && H > 0 && C % H == 0 && C / H == fa5::D && C % 8 == 0;
 }
 
-template <bool F16>
+template <bool F16, bool GRP>
 static bool attn_set_smem() {
     static PerDevice done;
     return done.once([] {
-        return cudaFuncSetAttribute(fa5::k_attn_fwd_tc<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa5::k_attn_fwd_tc<F16, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     fa5::F_SMEM) == cudaSuccess &&
-               cudaFuncSetAttribute(fa5::k_attn_bwd_dq_tc<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+               cudaFuncSetAttribute(fa5::k_attn_bwd_dq_tc<F16, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     fa5::Q_SMEM) == cudaSuccess &&
-               cudaFuncSetAttribute(fa5::k_attn_bwd_dkdv_tc<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+               cudaFuncSetAttribute(fa5::k_attn_bwd_dkdv_tc<F16, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     fa5::K_SMEM) == cudaSuccess;
     });
 }
@@ -900,22 +1059,24 @@ static dim3 attn_grid(int bh, int tiles) {
     return dim3((unsigned)band, (unsigned)tiles, (unsigned)((bh + band - 1) / band));
 }
 
-template <bool F16>
-static bool attn_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T, int C, int H) {
+// starts [B, K + 1] (GRP): the groups
+template <bool F16, bool GRP>
+static bool attn_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T, int C, int H,
+                        const int32_t* starts, int K) {
     CUtensorMap tq, tk;
     if (!tc::make_tmap_bf16(&tq, qkv, 3LL * C, (long long)B * T, 3LL * C, fa5::D, fa5::BQ)) return false;
     if (!tc::make_tmap_bf16(&tk, qkv, 3LL * C, (long long)B * T, 3LL * C, fa5::D, fa5::BN)) return false;
-    if (!attn_set_smem<F16>()) return false;
+    if (!attn_set_smem<F16, GRP>()) return false;
     const dim3 grid = attn_grid(B * H, (T + fa5::BQ - 1) / fa5::BQ);
     L.count();
-    launch_k(L, fa5::k_attn_fwd_tc<F16>, dim3(grid), dim3(fa5::THREADS), fa5::F_SMEM, tq, tk, (fa5::bf16*)y, lse, T, C, H,
-                                                                          B * H, L.flags, L.wait_cycles);
+    launch_k(L, fa5::k_attn_fwd_tc<F16, GRP>, dim3(grid), dim3(fa5::THREADS), fa5::F_SMEM, tq, tk, (fa5::bf16*)y, lse, T,
+             C, H, B * H, L.flags, L.wait_cycles, starts, K);
     return true;
 }
 
-template <bool F16>
+template <bool F16, bool GRP>
 static bool attn_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse, const void* dy,
-                        void* dqkv, int B, int T, int C, int H, float* Dlt, float* bpart) {
+                        void* dqkv, int B, int T, int C, int H, float* Dlt, float* bpart, const int32_t* starts, int K) {
     // the maps only move 16-bit elements (no conversion), for bf16 and half alike
     CUtensorMap tq, tk, to128, to64;
     if (!tc::make_tmap_bf16(&tq, qkv, 3LL * C, (long long)B * T, 3LL * C, fa5::D, fa5::BQ)) return false;
@@ -924,30 +1085,35 @@ static bool attn_bwd_tc(const Launch& L, const void* qkv, const void* y, const f
         return false;
     if (!tc::make_tmap_bf16(&to64, dy, (long long)C, (long long)B * T, (long long)C, fa5::D, fa5::BN))
         return false;
-    if (!attn_set_smem<F16>()) return false;
+    if (!attn_set_smem<F16, GRP>()) return false;
     const dim3 grid = attn_grid(B * H, (T + fa5::BQ - 1) / fa5::BQ);
     L.count();
-    launch_k(L, fa5::k_attn_bwd_dq_tc<F16>, dim3(grid), dim3(fa5::BW_THREADS), fa5::Q_SMEM, 
-        tq, tk, to128, (const fa5::bf16*)y, lse, Dlt, (fa5::bf16*)dqkv, bpart, T, C, H, B * H, L.flags,
-        L.wait_cycles);
+    launch_k(L, fa5::k_attn_bwd_dq_tc<F16, GRP>, dim3(grid), dim3(fa5::BW_THREADS), fa5::Q_SMEM, tq, tk, to128,
+             (const fa5::bf16*)y, lse, Dlt, (fa5::bf16*)dqkv, bpart, T, C, H, B * H, L.flags, L.wait_cycles, starts, K);
     L.count();
-    launch_k(L, fa5::k_attn_bwd_dkdv_tc<F16>, dim3(grid), dim3(fa5::BW_THREADS), fa5::K_SMEM, 
-        tq, tk, to64, lse, Dlt, (fa5::bf16*)dqkv, bpart, T, C, H, B * H, L.flags, L.wait_cycles);
+    launch_k(L, fa5::k_attn_bwd_dkdv_tc<F16, GRP>, dim3(grid), dim3(fa5::BW_THREADS), fa5::K_SMEM, tq, tk, to64, lse,
+             Dlt, (fa5::bf16*)dqkv, bpart, T, C, H, B * H, L.flags, L.wait_cycles, starts, K);
     return true;
 }
 
-bool launch_attention_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T,
-                             int C, int H) {
+bool launch_attention_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T, int C, int H,
+                             const int32_t* starts, int K) {
     if (L.dry) return true;
-    return L.f16 ? attn_fwd_tc<true>(L, qkv, y, lse, B, T, C, H) : attn_fwd_tc<false>(L, qkv, y, lse, B, T, C, H);
+    if (starts)
+        return L.f16 ? attn_fwd_tc<true, true>(L, qkv, y, lse, B, T, C, H, starts, K)
+                     : attn_fwd_tc<false, true>(L, qkv, y, lse, B, T, C, H, starts, K);
+    return L.f16 ? attn_fwd_tc<true, false>(L, qkv, y, lse, B, T, C, H, nullptr, 0)
+                 : attn_fwd_tc<false, false>(L, qkv, y, lse, B, T, C, H, nullptr, 0);
 }
 
-bool launch_attention_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse,
-                             const void* dy, void* dqkv, int B, int T, int C, int H, float* Dlt,
-                             float* bpart) {
+bool launch_attention_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse, const void* dy, void* dqkv,
+                             int B, int T, int C, int H, float* Dlt, float* bpart, const int32_t* starts, int K) {
     if (L.dry) return true;
-    return L.f16 ? attn_bwd_tc<true>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart)
-                 : attn_bwd_tc<false>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart);
+    if (starts)
+        return L.f16 ? attn_bwd_tc<true, true>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, starts, K)
+                     : attn_bwd_tc<false, true>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, starts, K);
+    return L.f16 ? attn_bwd_tc<true, false>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, nullptr, 0)
+                 : attn_bwd_tc<false, false>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, nullptr, 0);
 }
 
 }  // namespace tt

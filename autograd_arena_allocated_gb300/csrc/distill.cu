@@ -733,11 +733,14 @@ bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, co
     else if (dtype == TT_FP16) ok = distill<__half>(L, z, dz, a);
     else ok = distill<__nv_bfloat16>(L, z, dz, a);
     if (!ok) return false;
-    if (mean_loss) {
-        L.count();
-        launch_k(L, k_row_mean, dim3(1), dim3(1024), 0, row_loss, M, mean_loss, L.flags);
-    }
+    if (mean_loss) launch_row_mean(L, row_loss, M, mean_loss);
     return true;
+}
+
+void launch_row_mean(const Launch& L, const float* row_loss, int M, float* mean) {
+    if (L.dry) return;
+    L.count();
+    launch_k(L, k_row_mean, dim3(1), dim3(1024), 0, row_loss, M, mean, L.flags);
 }
 
 }  // namespace tt

@@ -946,11 +946,11 @@ __global__ void k_attn_bwd_dkv_simt(const T* __restrict__ qkv, const float* __re
 // D = rowsum(dO o O) [B, H, T], then the qkv bias-gradient partials: one row
 // of 3C per (sequence, 128-row tile) for the tensor-core kernels, or the
 // column-sum partials of the generic pass, whichever is larger
-static size_t attn_d_floats(int B, int T, int H) { return ((size_t)B * H * T + 63) / 64 * 64; }
+size_t attention_d_floats(int B, int T, int H) { return ((size_t)B * H * T + 63) / 64 * 64; }
 size_t attention_bwd_scratch_floats(int B, int T, int C, int H) {
     const size_t tiles = (size_t)B * ((T + 127) / 128) * 3 * C;
     const size_t cs = colsum_scratch_floats(B * T, 3 * C);
-    return attn_d_floats(B, T, H) + (tiles > cs ? tiles : cs) + 64;
+    return attention_d_floats(B, T, H) + (tiles > cs ? tiles : cs) + 64;
 }
 
 template <typename T, int HD>
@@ -1013,7 +1013,7 @@ void launch_attention_bwd(const Launch& L, bool bf16, const void* qkv, const voi
                           int H, float* scratch, float* dbias, bool acc_bias) {
     if (L.dry) return;
     const bool bf_only = bf16 && !L.f16;
-    float* bpart = scratch + attn_d_floats(B, T, H);
+    float* bpart = scratch + attention_d_floats(B, T, H);
     if (attention_tc_eligible(bf16, C, H) &&
         launch_attention_bwd_tc(L, qkv, y, lse, dy, dqkv, B, T, C, H, scratch, dbias ? bpart : nullptr)) {
         if (dbias) launch_sum_rows(L, bpart, B * ((T + 127) / 128), 3 * C, 3 * C, dbias, nullptr, acc_bias);

@@ -78,12 +78,12 @@ struct Record {
 enum ProfKind : int {
     PK_GEMM_FWD, PK_GEMM_DX, PK_GEMM_DW, PK_COLSUM, PK_ATTN_FWD, PK_ATTN_BWD, PK_LN_FWD,
     PK_LN_BWD, PK_XENT, PK_EMBED_FWD, PK_EMBED_BWD, PK_ADAMW, PK_CAST, PK_TOP, PK_DISTILL,
-    PK_BEAM_SELECT, PK_BEAM_REORDER, PK_COUNT
+    PK_BEAM_SELECT, PK_BEAM_REORDER, PK_LOGPROBS, PK_POLICY, PK_PREFERENCE, PK_COUNT
 };
 static const char* const PROF_NAMES[PK_COUNT] = {
     "gemm_fwd", "gemm_dx", "gemm_dw", "colsum", "attn_fwd", "attn_bwd", "ln_fwd",
     "ln_bwd", "xent", "embed_fwd", "embed_bwd", "adamw", "cast", "top_logits", "distill",
-    "beam_select", "beam_reorder"};
+    "beam_select", "beam_reorder", "logprobs", "policy", "preference"};
 
 struct ProfEntry {
     int kind;
@@ -1045,6 +1045,43 @@ static const char* distill_refusal(tt_dtype dtype, const float* t_vals, const in
     return list_refusal(dtype, V, k, tau);
 }
 
+// What the operators on answers refuse, as a text; NULL when the arguments are fine.
+static const char* tau_refusal(float tau) {
+    if (!(tau > 0.0f) || !std::isfinite(tau) || !std::isfinite(1.4426950408889634f / tau))
+        return "tau must be positive and finite, and so must log2(e) / tau";
+    return nullptr;
+}
+
+static const char* policy_refusal(const PolicyLoss& p, float tau) {
+    if (!p.adv) return "NULL advantages";
+    if (!(p.lo >= 0.0f && p.lo < 1.0f) || !(p.hi >= 0.0f) || !std::isfinite(p.hi))
+        return "eps_low must be in [0, 1), eps_high at least 0 and finite";
+    if (!(p.beta >= 0.0f) || !std::isfinite(p.beta)) return "beta must be at least 0 and finite";
+    if (p.beta > 0.0f && !p.ref_logp) return "beta > 0 needs the reference's log probabilities";
+    return tau_refusal(tau);
+}
+
+static const char* preference_refusal(const PreferenceLoss& p, float tau) {
+    if (!p.spans) return "NULL spans";
+    if (p.pairs < 1 || p.pairs > INT32_MAX / 4) return "there must be at least one pair";
+    if (!(p.beta > 0.0f) || !std::isfinite(p.beta)) return "beta must be positive and finite";
+    if (!std::isfinite(p.gamma)) return "gamma must be finite";
+    if (!(p.smooth >= 0.0f && p.smooth < 0.5f)) return "smoothing must be in [0, 0.5)";
+    return tau_refusal(tau);
+}
+
+// positions and heads are counted in an int, tiles of 64 positions in a grid
+static const char* group_refusal(tt_dtype dtype, int B, int T, int C, int H, int K) {
+    if (dtype != TT_FP32 && dtype != TT_BF16 && dtype != TT_FP16) return "bad dtype";
+    if (B <= 0 || T <= 0 || C <= 0 || H <= 0 || K <= 0 || C % H || C % 8) return "bad shape";
+    const int hd = C / H;
+    if (hd != 16 && hd != 32 && hd != 64) return "head dim must be 16, 32 or 64";
+    if (B > INT32_MAX / T || K > INT32_MAX / 4 || (long long)B * H * ((T + 63LL) / 64) > INT32_MAX || T > 65535 * 64 ||
+        (long long)B * H > 65535LL * 64)
+        return "too many positions";
+    return nullptr;
+}
+
 static void begin_step(tt_ctx* c) {
     c->tensors.clear();
     c->tape.clear();
@@ -1904,6 +1941,121 @@ tt_status tt_op_beam_reorder(tt_ctx* c, void* state, const int32_t* parents, int
             return fail(c, TT_ERR_ARG, "beam_reorder: state too large");
     }
     return op_epilogue(c, "beam_reorder");
+}
+
+// ------------------------------------------------------------------ training on answers
+static const char* answer_rows_refusal(tt_dtype dtype, const void* z, const void* dz, int M, int V, int ld) {
+    if (dtype != TT_FP32 && dtype != TT_BF16 && dtype != TT_FP16) return "bad dtype";
+    if (!z || M <= 0 || V <= 0 || ld < V || misaligned(dtype, z, dz)) return "bad arguments";
+    if (!head_row_ok(dtype, V)) return "V is larger than a row may be";
+    return nullptr;
+}
+
+tt_status tt_op_logprobs(tt_ctx* c, tt_dtype dtype, const void* logits, const int32_t* targets, float* logp, float* lse,
+                         int M, int V, int ld, float tau) {
+    TT_HEAD_PROLOGUE();
+    const char* why = answer_rows_refusal(dtype, logits, nullptr, M, V, ld);
+    if (!why && (!targets || !logp || off_words({targets, logp, lse}))) why = "bad arguments";
+    if (!why) why = tau_refusal(tau);
+    if (why) return fail(c, TT_ERR_ARG, "logprobs: %s", why);
+    c->oom = false;
+    {
+        ProfScope ps(c, PK_LOGPROBS, 0.0, (double)M * V * esize(dtype) + 12.0 * M);
+        launch_logprobs(op_launch(c), dtype, logits, targets, logp, lse, M, V, ld, tau);
+    }
+    return op_epilogue(c, "logprobs");
+}
+
+tt_status tt_op_policy(tt_ctx* c, tt_dtype dtype, const void* logits, const int32_t* targets, const float* old_logp,
+                       const float* ref_logp, const float* adv, const float* weight, void* dlogits, float* logp,
+                       float* row_loss, float* mean_loss, int M, int V, int ld, float eps_low, float eps_high, float beta,
+                       float tau, float dscale) {
+    TT_HEAD_PROLOGUE();
+    const PolicyLoss p{old_logp, ref_logp, adv, weight, eps_low, eps_high, beta};
+    const char* why = answer_rows_refusal(dtype, logits, dlogits, M, V, ld);
+    if (!why && (!targets || !row_loss ||
+                 off_words({targets, old_logp, ref_logp, adv, weight, logp, row_loss, mean_loss})))
+        why = "bad arguments";
+    if (!why) why = policy_refusal(p, tau);
+    if (why) return fail(c, TT_ERR_ARG, "policy: %s", why);
+    c->oom = false;
+    {
+        ProfScope ps(c, PK_POLICY, 0.0, (dlogits ? 2.0 : 1.0) * M * ld * esize(dtype) + 24.0 * M);
+        launch_policy(op_launch(c), dtype, logits, dlogits, p, targets, logp, row_loss, mean_loss, M, V, ld, tau, dscale,
+                      nullptr);
+    }
+    return op_epilogue(c, "policy");
+}
+
+tt_status tt_op_preference(tt_ctx* c, tt_dtype dtype, const void* logits, const int32_t* targets, const float* ref_logp,
+                           const int32_t* spans, void* dlogits, float* seq_logp, float* pair_loss, float* mean_loss, int M,
+                           int V, int ld, int pairs, float beta, float gamma, float smoothing, int mean, float tau,
+                           float dscale) {
+    TT_HEAD_PROLOGUE();
+    const PreferenceLoss p{ref_logp, spans, pairs, beta, gamma, smoothing, mean != 0};
+    const char* why = answer_rows_refusal(dtype, logits, dlogits, M, V, ld);
+    if (!why && (!targets || !pair_loss || off_words({targets, ref_logp, spans, seq_logp, pair_loss, mean_loss})))
+        why = "bad arguments";
+    if (!why) why = preference_refusal(p, tau);
+    if (why) return fail(c, TT_ERR_ARG, "preference: %s", why);
+    const size_t mark = c->off;
+    c->oom = false;
+    void* s = arena_alloc(c, preference_scratch_bytes(M));
+    if (!c->oom) {
+        ProfScope ps(c, PK_PREFERENCE, 0.0, (dlogits ? 3.0 : 1.0) * M * ld * esize(dtype) + 40.0 * M);
+        launch_preference(op_launch(c), dtype, logits, dlogits, p, targets, seq_logp, pair_loss, mean_loss, M, V, ld, tau,
+                          dscale, nullptr, s);
+    }
+    if (!c->capturing || c->oom) c->off = mark;  // a recording keeps its scratch: it is written at every replay
+    return op_epilogue(c, "preference");
+}
+
+static bool off_lines(std::initializer_list<const void*> ptrs) {
+    uintptr_t all = 0;
+    for (const void* p : ptrs) all |= (uintptr_t)p;
+    return (all & 15) != 0;
+}
+static Launch group_launch(tt_ctx* c, tt_dtype dtype) {
+    Launch L = op_launch(c);
+    L.f16 = dtype == TT_FP16;
+    return L;
+}
+
+tt_status tt_op_group_attention_fwd(tt_ctx* c, tt_dtype dtype, const void* qkv, const int32_t* starts, void* y, float* lse,
+                                    int B, int T, int C, int H, int K) {
+    TT_HEAD_PROLOGUE();
+    const char* why = group_refusal(dtype, B, T, C, H, K);
+    if (!why && (!qkv || !starts || !y || !lse || off_lines({qkv, y}) || off_words({starts, lse}))) why = "bad arguments";
+    if (why) return fail(c, TT_ERR_ARG, "group_attention_fwd: %s", why);
+    c->oom = false;
+    bool ok;
+    {
+        ProfScope ps(c, PK_ATTN_FWD, 4.0 * ((double)B * T * (T + 1) / 2.0) * C, 4.0 * B * T * C * esize(dtype));
+        ok = launch_group_attention_fwd(group_launch(c, dtype), dtype != TT_FP32, qkv, starts, y, lse, B, T, C, H, K);
+    }
+    if (!ok) return fail(c, TT_ERR_CUDA, "group_attention_fwd: launch failed");
+    return op_epilogue(c, "group_attention_fwd");
+}
+
+tt_status tt_op_group_attention_bwd(tt_ctx* c, tt_dtype dtype, const void* qkv, const int32_t* starts, const void* y,
+                                    const float* lse, const void* dy, void* dqkv, int B, int T, int C, int H, int K) {
+    TT_HEAD_PROLOGUE();
+    const char* why = group_refusal(dtype, B, T, C, H, K);
+    if (!why && (!qkv || !starts || !y || !lse || !dy || !dqkv || off_lines({qkv, y, dy, dqkv}) || off_words({starts, lse})))
+        why = "bad arguments";
+    if (why) return fail(c, TT_ERR_ARG, "group_attention_bwd: %s", why);
+    const size_t mark = c->off;
+    c->oom = false;
+    float* s = (float*)arena_alloc(c, attention_d_floats(B, T, H) * 4);
+    bool ok = true;
+    if (!c->oom) {
+        ProfScope ps(c, PK_ATTN_BWD, 10.0 * ((double)B * T * (T + 1) / 2.0) * C, 8.0 * B * T * C * esize(dtype));
+        ok = launch_group_attention_bwd(group_launch(c, dtype), dtype != TT_FP32, qkv, starts, y, lse, dy, dqkv, B, T, C, H,
+                                        K, s);
+    }
+    if (!c->capturing || c->oom) c->off = mark;  // a recording keeps its scratch: it is written at every replay
+    if (!ok) return fail(c, TT_ERR_CUDA, "group_attention_bwd: launch failed");
+    return op_epilogue(c, "group_attention_bwd");
 }
 
 // ------------------------------------------------------------------ generic tensor graph

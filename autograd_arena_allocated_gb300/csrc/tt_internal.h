@@ -237,13 +237,25 @@ bool launch_embed_chunks(const Launch& L, bool bf16, const void* dx, const int32
 
 // tcgen05 attention (attn_tc.cu); false = not taken (then the mma.sync path runs)
 bool attention_tc_eligible(bool bf16, int C, int H);
+// starts [B, K + 1]: groups of answers that share a prompt (group.cuh); NULL: causal
 bool launch_attention_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T,
-                             int C, int H);
+                             int C, int H, const int32_t* starts = nullptr, int K = 0);
 // bpart (may be NULL): per (sequence, 128-row tile) row of 3C column sums of
 // dqkv over the tile's rows (the qkv bias gradient's partials)
 bool launch_attention_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse,
                              const void* dy, void* dqkv, int B, int T, int C, int H, float* Dlt,
-                             float* bpart = nullptr);
+                             float* bpart = nullptr, const int32_t* starts = nullptr, int K = 0);
+
+// attention over groups (attn_group.cu, and the tensor-core kernels for 16-bit
+// heads of 64): L.f16 as in launch_attention_fwd; false: not launched.  scratch
+// as for launch_attention_bwd, whose first part alone, attention_d_floats(), is
+// used without dbias (which may be NULL, as there).
+size_t attention_d_floats(int B, int T, int H);
+bool launch_group_attention_fwd(const Launch& L, bool bf16, const void* qkv, const int32_t* starts, void* y, float* lse,
+                                int B, int T, int C, int H, int K);
+bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, const int32_t* starts, const void* y,
+                                const float* lse, const void* dy, void* dqkv, int B, int T, int C, int H, int K,
+                                float* scratch, float* dbias = nullptr, bool acc_bias = false);
 
 // decoding with a key/value cache (decode.cu); cache per layer [B, maxT, 2C].
 // The decode-step kernels read the newest position from device memory
@@ -300,6 +312,32 @@ bool launch_distill(const Launch& L, tt_dtype dtype, const void* z, void* dz, co
                     const int32_t* t_idx, const float* t_lse, const int32_t* targets, float* row_loss,
                     float* mean_loss, int M, int V, int ld, int k, float alpha, float tau, float dscale,
                     const float* scale_dev);
+
+// *mean = mean of M row losses in a fixed order; not finite: the non-finite flag
+void launch_row_mean(const Launch& L, const float* row_loss, int M, float* mean);
+
+// losses on the probabilities of given tokens (answer.cu): targets [M], -1 for
+// a row without one; logp, lse, mean_loss, seq_logp, dz and scale_dev may be NULL
+void launch_logprobs(const Launch& L, tt_dtype dtype, const void* z, const int32_t* targets, float* logp, float* lse, int M,
+                     int V, int ld, float tau);
+struct PolicyLoss {
+    const float *old_logp, *ref_logp, *adv, *weight;  // old_logp, ref_logp (beta 0), weight may be NULL
+    float lo, hi, beta;
+};
+void launch_policy(const Launch& L, tt_dtype dtype, const void* z, void* dz, const PolicyLoss& p, const int32_t* targets,
+                   float* logp, float* row_loss, float* mean_loss, int M, int V, int ld, float tau, float dscale,
+                   const float* scale_dev);
+struct PreferenceLoss {
+    const float* ref_logp;  // may be NULL
+    const int32_t* spans;   // [2 pairs, 2]
+    int pairs;
+    float beta, gamma, smooth;
+    bool mean;
+};
+size_t preference_scratch_bytes(int M);
+void launch_preference(const Launch& L, tt_dtype dtype, const void* z, void* dz, const PreferenceLoss& p,
+                       const int32_t* targets, float* seq_logp, float* pair_loss, float* mean_loss, int M, int V, int ld,
+                       float tau, float dscale, const float* scale_dev, void* scratch);
 
 // beam search (beam.cu).  tok_hist/par_hist (may be NULL): the choice is also
 // written to [slot][*pos_dev] of these [B n, ld_hist] tables.

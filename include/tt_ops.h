@@ -6,7 +6,7 @@
  * Every call enqueues on the context's stream and takes device pointers.
  * `dtype` selects the storage type of activations and weights: TT_FP32 (all
  * fp32) or TT_BF16 (bf16 storage, fp32 arithmetic), and in the calls over
- * lists of logits TT_FP16 as well.  Parameter gradients,
+ * lists of logits and those of training on answers TT_FP16 as well.  Parameter gradients,
  * LayerNorm statistics, log-sum-exp values and losses are always fp32.
  * Scratch memory, where a call needs it, is bump-allocated from the context's
  * arena (reset the arena between calls to reclaim it); TT_ERR_ARENA_OOM if
@@ -200,6 +200,100 @@ tt_status tt_op_beam_select(tt_ctx* ctx, tt_dtype dtype, const void* logits, con
  * Rows that are their own parent are not touched.  1 <= K <= TT_BEAM_MAX. */
 tt_status tt_op_beam_reorder(tt_ctx* ctx, void* state, const int32_t* parents, int N, int B, int K,
                              size_t row_bytes, size_t first, size_t count);
+
+/* ------------------------------------------------------ training on answers
+ * Operators of training a model on whole answers to prompts: the log
+ * probabilities of given tokens, the clipped policy loss, the loss of pairs of a
+ * preferred and a rejected answer, and attention over the answers to one prompt
+ * with the prompt's positions computed once.  They take TT_FP32, TT_BF16 and
+ * TT_FP16 storage; statistics, log probabilities, losses and weights are fp32.
+ * For the losses, rows are ld elements apart, the columns V..ld-1 are padding
+ * that no result depends on (a row's V logits are at most TT_ROW_BYTES_MAX), and
+ * a row's targets entry is the label of its position, or -1 for none (the
+ * prompt's positions, and those behind an answer's end): a row without a label
+ * is not read, has log probability and loss 0 and a gradient of zeros, whatever
+ * its logits hold.  A target outside [-1, V) raises the bad token flag
+ * (tt_ctx_sync: TT_ERR_ARG) and counts as -1.  Neither ld nor the pointers need
+ * more than the element's alignment, 4 bytes for indices, log probabilities,
+ * weights and losses (without it: TT_ERR_ARG).  All are deterministic and can be
+ * recorded (tt_graph.h); a recorded call keeps its scratch until the reset.  The
+ * context's device has to be the current one (else TT_ERR_STATE).  The pages
+ * have no counterpart to these calls: they extend the fused cross entropy
+ * (tinytorch 三.5) and the causal attention (Forge page, 最硬的一关). */
+
+/* logp [M] = z_y / tau - log sum_v exp(z_v / tau), y = targets [M];
+ * lse [M] fp32 or NULL: that log-sum-exp (0 in rows without a label).  A NaN
+ * logit makes a row NaN; a label whose logit is -inf has logp = -inf.
+ * tau > 0 (log2(e) / tau within fp32). */
+tt_status tt_op_logprobs(tt_ctx* ctx, tt_dtype dtype, const void* logits, const int32_t* targets, float* logp,
+                         float* lse, int M, int V, int ld, float tau);
+
+/* Clipped policy loss, loss and gradient in one call.  With lp the log
+ * probability of a row's label as tt_op_logprobs forms it, r = exp(lp -
+ * old_logp) (1, with its derivative, where old_logp is NULL), A = adv and
+ * x = ref_logp - lp:
+ *   row_loss = weight (-min(r A, clip(r, 1 - eps_low, 1 + eps_high) A)
+ *                      + beta (exp(x) - x - 1))
+ *   dlogits  = d row_loss / d z * dscale, pad columns 0
+ * (the first term's derivative is 0 where the clipped one is the smaller; a
+ * ratio on the bound counts as not clipped).  old_logp, ref_logp, adv, weight
+ * [M]; ref_logp may be NULL when beta is 0, weight when every row counts
+ * once.  mean_loss (may be NULL) receives the mean over all M rows, with label
+ * or without; dscale is usually 1/M, and other means are a matter of the
+ * weights.  logp [M] (may be NULL) receives lp.  dlogits [M, ld] may be logits
+ * itself (the call is then in place) or NULL (loss only); any other overlap is
+ * not allowed.  A loss that is not finite raises the non-finite flag where
+ * mean_loss is given (tt_ctx_sync: TT_ERR_NONFINITE).  0 <= eps_low < 1,
+ * eps_high >= 0, beta >= 0, all finite; tau as above. */
+tt_status tt_op_policy(tt_ctx* ctx, tt_dtype dtype, const void* logits, const int32_t* targets, const float* old_logp,
+                       const float* ref_logp, const float* adv, const float* weight, void* dlogits, float* logp,
+                       float* row_loss, float* mean_loss, int M, int V, int ld, float eps_low, float eps_high,
+                       float beta, float tau, float dscale);
+
+/* Loss of pairs of answers, loss and gradient in one call.  Answer 2p of pair
+ * p is the preferred one, 2p + 1 the rejected one; spans [2 pairs, 2]: an
+ * answer's first row and the one behind its last, 0 <= first <= last <= M (it
+ * may be empty).  Over the labelled rows of an answer, n of them,
+ *   seq_logp = sum lp,   S = sum (lp - ref_logp)  (ref_logp NULL: sum lp)
+ * S divided by n where mean != 0 (an answer of none has S = 0), and
+ *   v = beta (S_2p - S_2p+1) - gamma
+ *   pair_loss = (1 - smoothing) ln(1 + exp(-v)) + smoothing ln(1 + exp(v))
+ *   dlogits   = d pair_loss / d z * dscale, pad columns 0
+ * A row belongs to one answer at most; rows of none get a gradient of zeros.
+ * Spans out of range (they count as empty) or that share a labelled row (what
+ * the pair then receives is undefined) raise the bad token flag.  seq_logp
+ * [2 pairs] may be NULL; mean_loss (may be NULL) receives the mean over the
+ * pairs; dscale is usually 1/pairs.  dlogits and errors as for tt_op_policy.
+ * beta > 0, 0 <= smoothing < 0.5, gamma finite.  Scratch from the arena:
+ * 20 bytes a row. */
+tt_status tt_op_preference(tt_ctx* ctx, tt_dtype dtype, const void* logits, const int32_t* targets,
+                           const float* ref_logp, const int32_t* spans, void* dlogits, float* seq_logp,
+                           float* pair_loss, float* mean_loss, int M, int V, int ld, int pairs, float beta,
+                           float gamma, float smoothing, int mean, float tau, float dscale);
+
+/* Causal self-attention over groups: each of the B sequences of T positions
+ * holds a prompt, K answers that follow it independently of each other, and
+ * padding.  starts int32 [B, K + 1], device, ascending in [0, T]: entry 0 of a
+ * sequence is the prompt's length, answer k the positions from entry k to entry
+ * k + 1, and the padding begins at entry K (prompt and answers may be empty;
+ * K = 1 is plain causal attention over the first starts[b, 1] positions, and
+ * with no prompt the answers are sequences of their own).  A position sees the
+ * prompt up to itself and the positions of its own answer up to itself; qkv, y,
+ * lse as in tt_op_attention_fwd.  Padded positions receive y = 0 and lse = 0,
+ * and what qkv holds there reaches no other position.  A list that does not
+ * ascend in [0, T] raises the bad token flag; what its sequence receives is
+ * undefined.  Head dimensions 16, 32 and 64; C a multiple of 8, and qkv, y (and
+ * dy, dqkv) on 16-byte boundaries; B T and B H (T + 63) / 64 within an int. */
+tt_status tt_op_group_attention_fwd(tt_ctx* ctx, tt_dtype dtype, const void* qkv, const int32_t* starts, void* y,
+                                    float* lse, int B, int T, int C, int H, int K);
+
+/* Its backward: dqkv [B*T, 3C] is overwritten, with zeros in padded positions
+ * (what dy and y hold there is not used).  A prompt's keys and values get the
+ * gradients of all its answers, summed in a fixed order.  Scratch from the
+ * arena: 4 B H T bytes. */
+tt_status tt_op_group_attention_bwd(tt_ctx* ctx, tt_dtype dtype, const void* qkv, const int32_t* starts,
+                                    const void* y, const float* lse, const void* dy, void* dqkv, int B, int T, int C,
+                                    int H, int K);
 
 /* ------------------------------------------------------ allocation-free call
  * The pages have no counterpart to this entry point.  It serves callers of
