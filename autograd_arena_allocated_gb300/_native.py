@@ -70,6 +70,12 @@ SIGNATURES = {
     "tt_gpt2_step_distill": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _i, _i, _i, _vp,
                                    C.POINTER(_f)]),
     "tt_gpt2_top_logits": (_st, [_vp, _vp, _vp, _i, _i, _i, _f, _vp, _vp, _vp]),
+    "tt_gpt2_answers_arena_bytes": (_sz, [_vp, _i, _i, _i]),
+    "tt_gpt2_logprobs": (_st, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _vp, _vp]),
+    "tt_gpt2_step_policy": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _f, _f, _f, _vp, _i, _i, _i, _i, _vp,
+                                  _vp, C.POINTER(_f)]),
+    "tt_gpt2_step_preference": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _f, _i, _f, _vp, _i, _i, _i, _i,
+                                      _vp, _vp, C.POINTER(_f)]),
     "tt_gpt2_generate_beam_arena_bytes": (_sz, [_vp, _i, _i, _i, _i]),
     "tt_gpt2_generate_beam": (_st, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]),
     # tt_ops.h

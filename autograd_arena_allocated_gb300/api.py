@@ -57,6 +57,11 @@ def generate_beam_arena_bytes(cfg, B: int, T_prompt: int, n_new: int, K: int) ->
     return int(lib().tt_gpt2_generate_beam_arena_bytes(C.byref(cfg), int(B), int(T_prompt), int(n_new), int(K)))
 
 
+def answers_arena_bytes(cfg, B: int, T: int, K: int = 0) -> int:
+    """Most arena bytes of Context.logprobs_of, step_policy and step_preference (K answers a group, 0: no groups)."""
+    return int(lib().tt_gpt2_answers_arena_bytes(C.byref(cfg), int(B), int(T), int(K)))
+
+
 def arena_bytes(cfg: GPT2Config, B: int, T: int) -> int:
     return int(lib().tt_gpt2_arena_bytes(C.byref(cfg), B, T))
 
@@ -184,6 +189,37 @@ class Context:
         """tt_gpt2_top_logits: the k largest logits of every position."""
         self._check(lib().tt_gpt2_top_logits(self.h, _ptr(params), _ptr(tokens), int(B), int(T), int(k), float(tau),
                                              _ptr(vals), _ptr(idx), _ptr(lse)))
+
+    def logprobs_of(self, params, tokens, targets, B: int, T: int, logp, lse=None, tau: float = 1.0, starts=None, K: int = 0):
+        """tt_gpt2_logprobs: the log probability of every label (device tensors logp, lse)."""
+        self._check(lib().tt_gpt2_logprobs(self.h, _ptr(params), _ptr(tokens), _ptr(targets), _ptr(starts), int(K), int(B),
+                                           int(T), float(tau), _ptr(logp), _ptr(lse)))
+
+    def step_policy(self, params, grads, tokens, targets, old_logp, ref_logp, adv, weight, eps_low: float, eps_high: float,
+                    beta: float, B: int, T: int, tau: float = 1.0, starts=None, K: int = 0, accumulate: bool = False,
+                    loss_scale=None, logp=None, sync: bool = True):
+        """tt_gpt2_step_policy: the step with the clipped policy loss; starts
+        [B, K + 1]: over groups of K answers that share a prompt."""
+        loss = C.c_float()
+        self._check(lib().tt_gpt2_step_policy(self.h, _ptr(params), _ptr(grads), _ptr(tokens), _ptr(targets),
+                                              _ptr(old_logp), _ptr(ref_logp), _ptr(adv), _ptr(weight), float(eps_low),
+                                              float(eps_high), float(beta), float(tau), _ptr(starts), int(K), int(B),
+                                              int(T), 1 if accumulate else 0, _ptr(loss_scale), _ptr(logp),
+                                              C.byref(loss) if sync else None))
+        return float(loss.value) if sync else None
+
+    def step_preference(self, params, grads, tokens, targets, ref_logp, spans, pairs: int, beta: float, B: int, T: int,
+                        gamma: float = 0.0, smoothing: float = 0.0, mean: bool = False, tau: float = 1.0, starts=None,
+                        K: int = 0, accumulate: bool = False, loss_scale=None, seq_logp=None, sync: bool = True):
+        """tt_gpt2_step_preference: the step with the loss of pairs of answers
+        (answer 2p of spans preferred to 2p + 1); starts as in step_policy."""
+        loss = C.c_float()
+        self._check(lib().tt_gpt2_step_preference(self.h, _ptr(params), _ptr(grads), _ptr(tokens), _ptr(targets),
+                                                  _ptr(ref_logp), _ptr(spans), int(pairs), float(beta), float(gamma),
+                                                  float(smoothing), int(bool(mean)), float(tau), _ptr(starts), int(K),
+                                                  int(B), int(T), 1 if accumulate else 0, _ptr(loss_scale),
+                                                  _ptr(seq_logp), C.byref(loss) if sync else None))
+        return float(loss.value) if sync else None
 
     def grad_stats(self, grads, stats, loss_scale=None, n=None):
         """stats (device float[2]) = (||grads / scale||, not finite)."""

@@ -4,6 +4,7 @@
 // kernels do not take).  All reductions run in a fixed order: no floating-point
 // atomics anywhere, so every result is bitwise reproducible run to run.
 #include "tt_internal.h"
+#include "group.cuh"
 
 #include <math.h>
 
@@ -77,11 +78,69 @@ __global__ void k_embed_fwd(const T* __restrict__ wte, const T* __restrict__ wpe
     st(x, i, v);
 }
 
+// The same over groups (group.cuh): an answer's positions follow its prompt's,
+// and a padded position gets zeros, whatever its token is.  A CTA a position.
+template <typename T>
+__global__ void __launch_bounds__(128)
+k_embed_group_fwd(const T* __restrict__ wte, const T* __restrict__ wpe, const int32_t* __restrict__ tok,
+                  T* __restrict__ x, int T_, int C, int V, int maxT, const int32_t* __restrict__ starts, int K,
+                  int* flags) {
+    pdl_enter();
+    const long long m = blockIdx.x;
+    const int b = (int)(m / T_), i = (int)(m % T_);
+    const group::Group g(starts, b, K, T_);
+    const int id = tok[m], t = i < g.P ? i : g.P + i - g.start_of(i);
+    const bool real = i < g.end, good = real && id >= 0 && id < V && t < maxT;
+    if (real && !good && threadIdx.x == 0) atomicOr(&flags[FLAG_BAD_TOKEN], 1);
+    for (int c = threadIdx.x; c < C; c += blockDim.x)
+        st(x, m * C + c, good ? ld(wte, (long long)id * C + c) + ld(wpe, (long long)t * C + c) : 0.0f);
+}
+
+// dwpe[t] over groups: the prompts' positions t, then, for a t behind a prompt,
+// each answer's, in the order of sequences and answers.  A CTA a position.
+template <typename T>
+__global__ void __launch_bounds__(128)
+k_embed_group_wpe(const T* __restrict__ dx, int B, int T_, int C, const int32_t* __restrict__ starts, int K,
+                  float* __restrict__ dwpe, int acc) {
+    pdl_enter();
+    const int t = blockIdx.x;
+    for (int c = threadIdx.x; c < C; c += blockDim.x) {
+        float s = 0.0f;
+        for (int b = 0; b < B; b++) {
+            const group::Group g(starts, b, K, T_);
+            const T* d = dx + (long long)b * T_ * C + c;
+            if (t < g.P) {
+                s += ld(d, (long long)t * C);
+                continue;
+            }
+            for (int k = 0; k < K; k++) {
+                const int first = group::clampi(g.s[k], g.P, g.end), last = group::clampi(g.s[k + 1], first, g.end);
+                if (t - g.P < last - first) s += ld(d, (long long)(first + t - g.P) * C);
+            }
+        }
+        const long long i = (long long)t * C + c;
+        dwpe[i] = acc ? dwpe[i] + s : s;
+    }
+}
+
 void launch_embed_fwd(const Launch& L, bool bf16, const void* wte, const void* wpe,
-                      const int32_t* tok, void* x, int B, int T, int C, int V) {
+                      const int32_t* tok, void* x, int B, int T, int C, int V, const int32_t* starts, int K, int maxT) {
     if (L.dry) return;
     long long total = (long long)B * T * C;
     L.count();
+    if (starts) {
+        const dim3 grid((unsigned)(B * T));
+        if (bf16 && L.f16)
+            launch_k(L, k_embed_group_fwd<__half>, grid, dim3(128), 0, (const __half*)wte, (const __half*)wpe, tok,
+                     (__half*)x, T, C, V, maxT, starts, K, L.flags);
+        else if (bf16)
+            launch_k(L, k_embed_group_fwd<__nv_bfloat16>, grid, dim3(128), 0, (const __nv_bfloat16*)wte,
+                     (const __nv_bfloat16*)wpe, tok, (__nv_bfloat16*)x, T, C, V, maxT, starts, K, L.flags);
+        else
+            launch_k(L, k_embed_group_fwd<float>, grid, dim3(128), 0, (const float*)wte, (const float*)wpe, tok, (float*)x,
+                     T, C, V, maxT, starts, K, L.flags);
+        return;
+    }
     if (bf16 && L.f16)
         launch_k(L, k_embed_fwd<__half>, dim3(blocks_for(total, 256)), dim3(256), 0, 
             (const __half*)wte, (const __half*)wpe, tok, (__half*)x, T, C, V,
@@ -262,7 +321,7 @@ size_t embed_bwd_scratch_bytes(int M, int C) {
 
 void launch_embed_bwd(const Launch& L, bool bf16, const void* dx, const int32_t* tok,
                       float* dwte, float* dwpe, int B, int T, int C, int V, int maxT,
-                      void* scratch, bool acc_params) {
+                      void* scratch, bool acc_params, const int32_t* starts, int K) {
     if (L.dry) return;
     const int M = B * T;
     int32_t* s = (int32_t*)scratch;
@@ -304,6 +363,19 @@ void launch_embed_bwd(const Launch& L, bool bf16, const void* dx, const int32_t*
     }
     long long n = (long long)maxT * C;
     L.count();
+    if (starts) {
+        const dim3 grid((unsigned)maxT);
+        if (bf16 && L.f16)
+            launch_k(L, k_embed_group_wpe<__half>, grid, dim3(128), 0, (const __half*)dx, B, T, C, starts, K, dwpe,
+                     acc_params ? 1 : 0);
+        else if (bf16)
+            launch_k(L, k_embed_group_wpe<__nv_bfloat16>, grid, dim3(128), 0, (const __nv_bfloat16*)dx, B, T, C, starts, K,
+                     dwpe, acc_params ? 1 : 0);
+        else
+            launch_k(L, k_embed_group_wpe<float>, grid, dim3(128), 0, (const float*)dx, B, T, C, starts, K, dwpe,
+                     acc_params ? 1 : 0);
+        return;
+    }
     if (bf16 && L.f16)
         launch_k(L, k_embed_wpe<__half>, dim3(blocks_for(n, 256)), dim3(256), 0, 
             (const __half*)dx, B, T, C, maxT, dwpe, acc_params ? 1 : 0);

@@ -136,6 +136,11 @@ struct tt_ctx {
     // caller's buffers, and the device loss scale that seeds the backward
     bool accum_params = false;
     const float* loss_scale_dev = nullptr;
+    size_t row_losses = 0;  // how many row_loss_dev holds
+    const char* failed = nullptr;  // a launch of the step's forward that was not made
+    // the step's sequences are groups of answers that share a prompt (group.cuh)
+    const int32_t* group_starts = nullptr;
+    int group_K = 0;
     // a recording of graph calls (tt_capture_begin / tt_capture_end / tt_replay)
     bool capturing = false;
     cudaStream_t cap_stream = nullptr, saved_stream = nullptr;
@@ -294,7 +299,9 @@ static int op_embed(tt_ctx* c, const void* wte, const void* wpe, float* dwte, fl
     const bool bf = m.dtype != TT_FP32;  // 16-bit storage (bf16 or half)
     int out = new_tensor(c, (long long)B * T, m.C, esize(m.dtype));
     ProfScope ps(c, PK_EMBED_FWD, 0.0, 3.0 * B * T * m.C * esize(m.dtype) + 4.0 * B * T);
-    if (!c->oom) launch_embed_fwd(launch_of(c), bf, wte, wpe, tok, c->tensors[out].data, B, T, m.C, m.V);
+    if (!c->oom)
+        launch_embed_fwd(launch_of(c), bf, wte, wpe, tok, c->tensors[out].data, B, T, m.C, m.V, c->group_starts, c->group_K,
+                         m.maxT);
     Record r;
     r.kind = R_EMBED;
     r.out = out;
@@ -377,9 +384,14 @@ static int op_attention(tt_ctx* c, int qkv, int B, int T) {
     const double pairs = (double)B * m.H * T * (T + 1) / 2.0;
     ProfScope ps(c, PK_ATTN_FWD, 4.0 * pairs * (m.C / m.H),
                  (3.0 + 1.0) * M * m.C * esize(m.dtype) + 4.0 * B * m.H * T);
-    if (!c->oom)
+    if (!c->oom && c->group_starts) {
+        if (!launch_group_attention_fwd(launch_of(c), bf, c->tensors[qkv].data, c->group_starts, c->tensors[out].data, lse,
+                                        B, T, m.C, m.H, c->group_K))
+            c->failed = "attention over groups: launch failed";
+    } else if (!c->oom) {
         launch_attention_fwd(launch_of(c), bf, c->tensors[qkv].data, c->tensors[out].data, lse, B, T,
                              m.C, m.H);
+    }
     Record r;
     r.kind = R_ATTN;
     r.in = qkv; r.out = out; r.lse = lse; r.B = B; r.T = T; r.H = m.H; r.N = m.C; r.M = M;
@@ -389,14 +401,20 @@ static int op_attention(tt_ctx* c, int qkv, int B, int T) {
     return out;
 }
 
+// Where a step's loss over M rows leaves its mean and row losses.
+static void loss_buffers(tt_ctx* c, int M) {
+    c->row_loss_dev = (float*)arena_alloc(c, (size_t)M * 4);
+    c->loss_dev = (float*)arena_alloc(c, 4);
+    c->row_losses = (size_t)M;
+}
+
 // Cross entropy, forward and backward fused: the logits are replaced by their
 // gradient in the same pass, so the logits tensor's gradient is its own buffer.
 static void op_xent(tt_ctx* c, int z, const int32_t* targets, int V) {
     const tt_gpt2_config& m = c->cfg;
     const bool bf = m.dtype != TT_FP32;  // 16-bit storage (bf16 or half)
     const int M = (int)c->tensors[z].rows, ld = (int)c->tensors[z].cols;
-    c->row_loss_dev = (float*)arena_alloc(c, (size_t)M * 4);
-    c->loss_dev = (float*)arena_alloc(c, 4);
+    loss_buffers(c, M);
     ProfScope ps(c, PK_XENT, 0.0, 2.0 * M * ld * esize(m.dtype) + 8.0 * M);
     if (!c->oom)
         launch_xent(launch_of(c), bf, c->tensors[z].data, targets, c->row_loss_dev, c->loss_dev, M, V,
@@ -423,8 +441,7 @@ struct Teacher {
 static bool op_distill(tt_ctx* c, int z, const int32_t* targets, int V, const Teacher& t) {
     const tt_gpt2_config& m = c->cfg;
     const int M = (int)c->tensors[z].rows, ld = (int)c->tensors[z].cols;
-    c->row_loss_dev = (float*)arena_alloc(c, (size_t)M * 4);
-    c->loss_dev = (float*)arena_alloc(c, 4);
+    loss_buffers(c, M);
     ProfScope ps(c, PK_DISTILL, 0.0, 2.0 * M * ld * esize(m.dtype) + 8.0 * M * t.k);
     bool ok = true;
     if (!c->oom)
@@ -438,6 +455,43 @@ static bool op_distill(tt_ctx* c, int z, const int32_t* targets, int V, const Te
     add_consumer(c, z, (int)c->tape.size() - 1);
     c->tensors[z].grad = c->tensors[z].data;
     return ok;
+}
+
+// Losses on given tokens in the place of the cross entropy (answer.cu), as
+// tt_gpt2_step_policy and tt_gpt2_step_preference give them.
+struct AnswerLoss {
+    const PolicyLoss* policy = nullptr;
+    const PreferenceLoss* pref = nullptr;  // else this one
+    float tau = 1.0f;
+    float* logp = nullptr;  // policy: [M], may be NULL; pairs: [2 pairs], may be NULL
+};
+
+static void op_answer(tt_ctx* c, int z, const int32_t* targets, int V, const AnswerLoss& a) {
+    const tt_gpt2_config& m = c->cfg;
+    const int M = (int)c->tensors[z].rows, ld = (int)c->tensors[z].cols;
+    void* data = c->tensors[z].data;
+    loss_buffers(c, M);
+    if (a.policy) {
+        ProfScope ps(c, PK_POLICY, 0.0, 2.0 * M * ld * esize(m.dtype) + 24.0 * M);
+        if (!c->oom)
+            launch_policy(launch_of(c), m.dtype, data, data, *a.policy, targets, a.logp, c->row_loss_dev, c->loss_dev, M, V,
+                          ld, a.tau, 1.0f / (float)M, c->loss_scale_dev);
+    } else {
+        const size_t mark = c->off;
+        void* scratch = arena_alloc(c, preference_scratch_bytes(M));
+        ProfScope ps(c, PK_PREFERENCE, 0.0, 3.0 * M * ld * esize(m.dtype) + 40.0 * M);
+        if (!c->oom)
+            launch_preference(launch_of(c), m.dtype, data, data, *a.pref, targets, a.logp, c->row_loss_dev, c->loss_dev, M,
+                              V, ld, a.tau, 1.0f / (float)a.pref->pairs, c->loss_scale_dev, scratch);
+        c->off = mark;
+        c->row_losses = (size_t)a.pref->pairs;
+    }
+    Record r;
+    r.kind = R_XENT;
+    r.in = z; r.M = M; r.N = V; r.idx = targets;
+    c->tape.push_back(r);
+    add_consumer(c, z, (int)c->tape.size() - 1);
+    c->tensors[z].grad = c->tensors[z].data;
 }
 
 // ------------------------------------------------------------------ backward
@@ -607,9 +661,15 @@ static tt_status backward_record(tt_ctx* c, int idx) {
         const double pairs = (double)r.B * r.H * r.T * (r.T + 1) / 2.0;
         ProfScope ps(c, PK_ATTN_BWD, 10.0 * pairs * (r.N / r.H),
                      (3.0 + 2.0 + 3.0) * r.M * r.N * esize(m.dtype) + 4.0 * r.B * r.H * r.T);
-        if (!c->oom)
+        if (!c->oom && c->group_starts) {
+            if (!launch_group_attention_bwd(L, bf, c->tensors[r.in].data, c->group_starts, y.data, r.lse, y.grad, dqkv,
+                                            r.B, r.T, r.N, r.H, c->group_K, s, prod ? prod->db : nullptr,
+                                            c->accum_params))
+                return fail(c, TT_ERR_CUDA, "attention over groups: launch failed");
+        } else if (!c->oom) {
             launch_attention_bwd(L, bf, c->tensors[r.in].data, y.data, r.lse, y.grad, dqkv, r.B, r.T,
                                  r.N, r.H, s, prod ? prod->db : nullptr, c->accum_params);
+        }
         c->off = mark;
         return TT_OK;
     }
@@ -627,7 +687,7 @@ static tt_status backward_record(tt_ctx* c, int idx) {
                      (double)r.B * r.T * r.N * (esize(m.dtype) + 8.0) + 4.0 * r.maxT * r.N);
         if (!c->oom)
             launch_embed_bwd(L, bf, y.grad, r.idx, r.dW, r.dwpe, r.B, r.T, r.N, r.V, r.maxT, s,
-                             c->accum_params);
+                             c->accum_params, c->group_starts, c->group_K);
         c->off = mark;
         return TT_OK;
     }
@@ -717,9 +777,11 @@ static int gpt2_forward(tt_ctx* c, const void* params, float* grads, const int32
 
 static tt_status gpt2_forward_backward(tt_ctx* c, const void* params, float* grads,
                                        const int32_t* tok, const int32_t* tgt, int B, int T,
-                                       const Teacher* teacher = nullptr) {
+                                       const Teacher* teacher = nullptr, const AnswerLoss* answer = nullptr) {
     int z = gpt2_forward(c, params, grads, tok, B, T);
-    if (!teacher) op_xent(c, z, tgt, c->cfg.V);
+    if (c->failed) return fail(c, TT_ERR_CUDA, "%s", c->failed);
+    if (answer) op_answer(c, z, tgt, c->cfg.V, *answer);
+    else if (!teacher) op_xent(c, z, tgt, c->cfg.V);
     else if (!op_distill(c, z, tgt, c->cfg.V, *teacher)) return fail(c, TT_ERR_CUDA, "distillation: launch failed");
     if (c->oom) return TT_ERR_ARENA_OOM;
     return tape_backward(c);
@@ -1087,6 +1149,9 @@ static void begin_step(tt_ctx* c) {
     c->tape.clear();
     c->grad_written.clear();
     c->oom = false;
+    c->failed = nullptr;
+    c->group_starts = nullptr;
+    c->group_K = 0;
 }
 
 static bool is_host_pointer(const void* p) {
@@ -1294,8 +1359,7 @@ tt_status tt_gpt2_param_offset(const tt_gpt2_config* m, int layer, int which, si
     return TT_OK;
 }
 
-size_t tt_gpt2_arena_bytes(const tt_gpt2_config* m, int B, int T) {
-    if (!cfg_ok(m) || !batch_ok(m, B, T)) return 0;
+static size_t step_plan_bytes(const tt_gpt2_config* m, int B, int T) {
     tt_ctx c;
     c.cap = (size_t)-1 / 2;
     c.cfg = *m;
@@ -1316,27 +1380,43 @@ size_t tt_gpt2_arena_bytes(const tt_gpt2_config* m, int B, int T) {
     return c.high - ARENA_HEADER;
 }
 
+size_t tt_gpt2_arena_bytes(const tt_gpt2_config* m, int B, int T) {
+    if (!cfg_ok(m) || !batch_ok(m, B, T)) return 0;
+    return step_plan_bytes(m, B, T);
+}
+
+size_t tt_gpt2_answers_arena_bytes(const tt_gpt2_config* m, int B, int T, int K) {
+    if (!cfg_ok(m) || K < 0 || (K == 0 ? !batch_ok(m, B, T) : group_refusal(m->dtype, B, T, m->C, m->H, K) != nullptr))
+        return 0;
+    return step_plan_bytes(m, B, T) + preference_scratch_bytes(B * T) + ARENA_ALIGN;
+}
+
 tt_status tt_gpt2_step(tt_ctx* c, const void* params, float* grads, const int32_t* tokens,
                        const int32_t* targets, int B, int T, float* loss) {
     return tt_gpt2_step_ex(c, params, grads, tokens, targets, B, T, 0, nullptr, loss);
 }
 
-// The step with the cross entropy, or with the distillation loss of `teacher`
-// (targets may then be NULL).
+// The step with the cross entropy, with the distillation loss of `teacher`
+// (targets may then be NULL), or with one of `answer`, over sequences or, with
+// starts, groups of K answers each.
 static tt_status step_with(tt_ctx* c, const void* params, float* grads, const int32_t* tokens, const int32_t* targets,
-                           const Teacher* teacher, int B, int T, int flags, const float* loss_scale, float* loss) {
+                           const Teacher* teacher, int B, int T, int flags, const float* loss_scale, float* loss,
+                           const AnswerLoss* answer = nullptr, const int32_t* starts = nullptr, int K = 0) {
     if (!c) return TT_ERR_ARG;
     if (!live(c)) return TT_ERR_STALE;
     if (c->capturing) return fail(c, TT_ERR_STATE, "GPT-2 calls cannot be recorded");
     if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
     if (!params || !grads || !tokens || (!targets && !teacher))
         return fail(c, TT_ERR_ARG, "NULL parameter, gradient or token pointer");
-    if (!batch_ok(&c->cfg, B, T))
-        return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, c->cfg.maxT);
+    const char* why = starts ? group_refusal(c->cfg.dtype, B, T, c->cfg.C, c->cfg.H, K) : nullptr;
+    if (why || (!starts && !batch_ok(&c->cfg, B, T)))
+        return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)%s%s", B, T, c->cfg.maxT, why ? ": " : "",
+                    why ? why : "");
     const size_t M = (size_t)B * T;
     // exact plan first: nothing is launched if it does not fit
     {
-        const size_t need = tt_gpt2_arena_bytes(&c->cfg, B, T);
+        const size_t need = answer ? tt_gpt2_answers_arena_bytes(&c->cfg, B, T, starts ? K : 0)
+                                   : tt_gpt2_arena_bytes(&c->cfg, B, T);
         const size_t at = (c->off + ARENA_ALIGN - 1) & ~(ARENA_ALIGN - 1);
         if (need == 0 || at + need > c->cap)
             return fail(c, TT_ERR_ARENA_OOM, "arena too small: step needs %zu bytes, %zu free", need,
@@ -1361,9 +1441,12 @@ static tt_status step_with(tt_ctx* c, const void* params, float* grads, const in
     if (flags & ~TT_STEP_ACCUMULATE) return fail(c, TT_ERR_ARG, "unknown step flags 0x%x", (unsigned)flags);
     c->accum_params = (flags & TT_STEP_ACCUMULATE) != 0;
     c->loss_scale_dev = loss_scale;
-    tt_status s = gpt2_forward_backward(c, params, grads, tok, tgt, B, T, teacher);
+    c->group_starts = starts;
+    c->group_K = K;
+    tt_status s = gpt2_forward_backward(c, params, grads, tok, tgt, B, T, teacher, answer);
     c->accum_params = false;
     c->loss_scale_dev = nullptr;
+    c->group_starts = nullptr;
     if (s != TT_OK) {
         if (s == TT_ERR_ARENA_OOM) return fail(c, s, "arena exhausted during the step");
         return s;
@@ -1400,6 +1483,57 @@ tt_status tt_gpt2_step_distill(tt_ctx* c, const void* params, float* grads, cons
             return fail(c, TT_ERR_ARG, "step_distill: lists off a 4-byte boundary");
     }
     return step_with(c, params, grads, tokens, targets, &t, B, T, flags, loss_scale, loss);
+}
+
+// what the steps on answers refuse of their lists beside the loss's own
+// arguments (targets may be in host memory, the lists may not)
+static const char* answer_lists_refusal(const int32_t* targets, std::initializer_list<const void*> lists) {
+    if (!targets) return "NULL targets";
+    for (const void* p : lists)
+        if (p && is_host_pointer(p)) return "the lists must be device memory";
+    if (off_words(lists) || (!is_host_pointer(targets) && off_words({targets}))) return "lists off a 4-byte boundary";
+    return nullptr;
+}
+
+tt_status tt_gpt2_step_policy(tt_ctx* c, const void* params, float* grads, const int32_t* tokens, const int32_t* targets,
+                              const float* old_logp, const float* ref_logp, const float* adv, const float* weight,
+                              float eps_low, float eps_high, float beta, float tau, const int32_t* starts, int K, int B,
+                              int T, int flags, const float* loss_scale, float* logp, float* loss) {
+    if (!c) return TT_ERR_ARG;
+    if (!live(c)) return TT_ERR_STALE;
+    const PolicyLoss p{old_logp, ref_logp, adv, weight, eps_low, eps_high, beta};
+    AnswerLoss a;
+    a.policy = &p;
+    a.tau = tau;
+    a.logp = logp;
+    if (c->has_model) {
+        const char* why = policy_refusal(p, tau);
+        if (!why) why = answer_lists_refusal(targets, {old_logp, ref_logp, adv, weight, logp, starts, loss_scale});
+        if (!why && !head_row_ok(c->cfg.dtype, c->cfg.V)) why = "V is larger than a row may be";
+        if (why) return fail(c, TT_ERR_ARG, "step_policy: %s", why);
+    }
+    return step_with(c, params, grads, tokens, targets, nullptr, B, T, flags, loss_scale, loss, &a, starts, K);
+}
+
+tt_status tt_gpt2_step_preference(tt_ctx* c, const void* params, float* grads, const int32_t* tokens,
+                                  const int32_t* targets, const float* ref_logp, const int32_t* spans, int pairs,
+                                  float beta, float gamma, float smoothing, int mean, float tau, const int32_t* starts,
+                                  int K, int B, int T, int flags, const float* loss_scale, float* seq_logp, float* loss) {
+    if (!c) return TT_ERR_ARG;
+    if (!live(c)) return TT_ERR_STALE;
+    const PreferenceLoss p{ref_logp, spans, pairs, beta, gamma, smoothing, mean != 0};
+    AnswerLoss a;
+    a.pref = &p;
+    a.tau = tau;
+    a.logp = seq_logp;
+    if (c->has_model) {
+        const char* why = preference_refusal(p, tau);
+        if (!why && B > 0 && T > 0 && (long long)pairs > (long long)B * T) why = "more pairs than positions";
+        if (!why) why = answer_lists_refusal(targets, {ref_logp, spans, seq_logp, starts, loss_scale});
+        if (!why && !head_row_ok(c->cfg.dtype, c->cfg.V)) why = "V is larger than a row may be";
+        if (why) return fail(c, TT_ERR_ARG, "step_preference: %s", why);
+    }
+    return step_with(c, params, grads, tokens, targets, nullptr, B, T, flags, loss_scale, loss, &a, starts, K);
 }
 
 // Token inputs may be host or device buffers; host ones are staged into the arena.
@@ -1553,6 +1687,49 @@ tt_status tt_gpt2_top_logits(tt_ctx* c, const void* params, const int32_t* token
     return op_epilogue(c, "top_logits");
 }
 
+tt_status tt_gpt2_logprobs(tt_ctx* c, const void* params, const int32_t* tokens, const int32_t* targets,
+                           const int32_t* starts, int K, int B, int T, float tau, float* logp, float* lse) {
+    if (!c) return TT_ERR_ARG;
+    if (!live(c)) return TT_ERR_STALE;
+    if (c->capturing) return fail(c, TT_ERR_STATE, "GPT-2 calls cannot be recorded");
+    if (!c->has_model) return fail(c, TT_ERR_STATE, "tt_ctx_set_model was not called");
+    if (!params || !tokens || !logp) return fail(c, TT_ERR_ARG, "NULL parameter, token or list pointer");
+    const tt_gpt2_config& m = c->cfg;
+    const char* why = tau_refusal(tau);
+    if (!why) why = answer_lists_refusal(targets, {logp, lse, starts});
+    if (!why && !head_row_ok(m.dtype, m.V)) why = "V is larger than a row may be";
+    if (!why && starts) why = group_refusal(m.dtype, B, T, m.C, m.H, K);
+    if (why) return fail(c, TT_ERR_ARG, "logprobs: %s", why);
+    if (!starts && !batch_ok(&m, B, T))
+        return fail(c, TT_ERR_ARG, "bad batch shape B=%d T=%d (maxT=%d)", B, T, m.maxT);
+    {
+        const size_t need = tt_gpt2_answers_arena_bytes(&m, B, T, starts ? K : 0);
+        const size_t at = (c->off + ARENA_ALIGN - 1) & ~(ARENA_ALIGN - 1);
+        if (at + need > c->cap)
+            return fail(c, TT_ERR_ARENA_OOM, "arena too small: the forward needs %zu bytes, %zu free", need,
+                        c->cap > at ? c->cap - at : (size_t)0);
+    }
+    begin_step(c);
+    c->loss_dev = c->row_loss_dev = nullptr;  // no loss in this pass
+    tt_status st;
+    const int32_t* tok = stage_tokens(c, tokens, (size_t)B * T, &st);
+    if (st != TT_OK) return st;
+    const int32_t* tgt = stage_tokens(c, targets, (size_t)B * T, &st);
+    if (st != TT_OK) return st;
+    c->group_starts = starts;
+    c->group_K = K;
+    const int z = gpt2_forward(c, params, nullptr, tok, B, T);
+    c->group_starts = nullptr;
+    if (c->failed) return fail(c, TT_ERR_CUDA, "%s", c->failed);
+    if (c->oom) return fail(c, TT_ERR_ARENA_OOM, "arena exhausted during the forward");
+    const int M = B * T, ld = (int)c->tensors[z].cols;
+    {
+        ProfScope ps(c, PK_LOGPROBS, 0.0, (double)M * m.V * esize(m.dtype) + 12.0 * M);
+        launch_logprobs(launch_of(c), m.dtype, c->tensors[z].data, tgt, logp, lse, M, m.V, ld, tau);
+    }
+    return op_epilogue(c, "logprobs");
+}
+
 size_t tt_gpt2_generate_beam_arena_bytes(const tt_gpt2_config* m, int B, int T_prompt, int n_new, int K) {
     if (!cfg_ok(m) || m->dtype == TT_FP16 || B <= 0 || T_prompt <= 0 || n_new < 0 || T_prompt > m->maxT ||
         n_new > m->maxT - T_prompt || K < 1 || K > TT_BEAM_MAX || K > m->V || B > INT32_MAX / K / m->maxT)
@@ -1637,8 +1814,7 @@ tt_status tt_ctx_copy_row_losses(tt_ctx* c, float* dst, size_t n) {
     if (!c || !dst) return TT_ERR_ARG;
     if (!live(c)) return TT_ERR_STALE;
     if (!c->row_loss_dev) return fail(c, TT_ERR_STATE, "no step since the last reset");
-    if (!c->tensors.empty() && n > (size_t)c->tensors[0].rows)
-        return fail(c, TT_ERR_ARG, "n exceeds B*T");
+    if (n > c->row_losses) return fail(c, TT_ERR_ARG, "n exceeds the last loss's %zu rows", c->row_losses);
     if (cudaMemcpyAsync(dst, c->row_loss_dev, n * 4, cudaMemcpyDefault, c->stream) != cudaSuccess ||
         cudaStreamSynchronize(c->stream) != cudaSuccess)
         return fail(c, TT_ERR_CUDA, "row loss copy: %s", cudaGetErrorString(cudaGetLastError()));

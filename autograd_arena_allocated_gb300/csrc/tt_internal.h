@@ -165,12 +165,13 @@ void gemm_simt_launch(const Launch& L, const GemmArgs& g);
 
 // ------------------------------------------------------------ other kernels
 void launch_embed_fwd(const Launch& L, bool bf16, const void* wte, const void* wpe,
-                      const int32_t* tok, void* x, int B, int T, int C, int V);
+                      const int32_t* tok, void* x, int B, int T, int C, int V, const int32_t* starts = nullptr,
+                      int K = 0, int maxT = 0);  // starts [B, K + 1]: the sequences are groups (group.cuh)
 // scratch: the stable sort of positions by token id plus chunk partial sums
 size_t embed_bwd_scratch_bytes(int M, int C);
 void launch_embed_bwd(const Launch& L, bool bf16, const void* dx, const int32_t* tok,
                       float* dwte, float* dwpe, int B, int T, int C, int V, int maxT,
-                      void* scratch, bool acc_params = false);
+                      void* scratch, bool acc_params = false, const int32_t* starts = nullptr, int K = 0);
 
 size_t layernorm_bwd_scratch_floats(int M, int C);
 void launch_layernorm_fwd(const Launch& L, bool bf16, const void* x, const void* w,

@@ -177,12 +177,13 @@ tt_status tt_gpt2_step(tt_ctx* ctx, const void* params, float* grads,
                        int B, int T, float* loss);
 
 /* Device pointers to the last step's mean loss (1 float) and per-position
- * losses (B*T floats, row-major).  Valid until the next reset. */
+ * losses (B*T floats, row-major; after tt_gpt2_step_preference the pairs'
+ * losses).  Valid until the next reset. */
 tt_status tt_ctx_loss_device(const tt_ctx* ctx, const float** mean_loss,
                              const float** row_losses);
 
-/* Copy the last step's per-position losses (n <= B*T floats) to dst, which
- * may be host or device memory; synchronizes the context's stream. */
+/* Copy the last step's per-position losses (n <= B*T floats; after
+ * tt_gpt2_step_preference n <= pairs) to dst, which may be host or device memory; synchronizes the context's stream. */
 tt_status tt_ctx_copy_row_losses(tt_ctx* ctx, float* dst, size_t n);
 
 /* ---------------------------------------------------------------- step variants
@@ -223,6 +224,51 @@ tt_status tt_gpt2_step_distill(tt_ctx* ctx, const void* params, float* grads, co
                                const int32_t* targets, const float* t_vals, const int32_t* t_idx,
                                const float* t_lse, int k, float alpha, float tau, int B, int T, int flags,
                                const float* loss_scale, float* loss);
+
+/* ------------------------------------------------------ training on answers
+ * Steps on whole answers to prompts (the operators of tt_ops.h's training on
+ * answers in the place of the cross entropy), over sequences or over groups.
+ * The label of a position is the token that follows it in its answer, -1 in
+ * the prompt and behind the end.
+ *   starts == NULL: B sequences of T <= maxT positions (K is not used).
+ *   starts int32 [B, K + 1], device (tt_op_group_attention_fwd): each sequence
+ * is a group, its prompt computed once for all its K answers.  An answer's
+ * positions follow the prompt's, so T may exceed maxT as long as no prompt and
+ * answer together do (else: the bad token flag, tt_ctx_sync: TT_ERR_ARG).  A
+ * row of logits predicts one token, so the last token of the prompt stands at
+ * the head of each answer and not in the prompt.  Tokens of padded positions
+ * are not used, their targets must be -1.
+ * Arguments, arena and errors are otherwise those of tt_gpt2_step_ex: targets in
+ * device or host memory, every other list in device memory (loss_scale too);
+ * the mean is over all B*T positions (policy) or over the pairs. */
+
+/* Most arena bytes of the three calls below, K = 0 without groups; 0 for an
+ * invalid config or batch. */
+size_t tt_gpt2_answers_arena_bytes(const tt_gpt2_config* cfg, int B, int T, int K);
+
+/* The log probability of every label after a forward pass (tt_op_logprobs): the
+ * reference model's side of the two steps, or the old policy's.  logp, lse [B*T]
+ * (lse may be NULL) are device memory.  Does not synchronize; there is no last
+ * loss to read until the next step. */
+tt_status tt_gpt2_logprobs(tt_ctx* ctx, const void* params, const int32_t* tokens, const int32_t* targets,
+                           const int32_t* starts, int K, int B, int T, float tau, float* logp, float* lse);
+
+/* The step with the clipped policy loss (tt_op_policy): old_logp, ref_logp,
+ * adv, weight, logp [B*T] as there. */
+tt_status tt_gpt2_step_policy(tt_ctx* ctx, const void* params, float* grads, const int32_t* tokens,
+                              const int32_t* targets, const float* old_logp, const float* ref_logp, const float* adv,
+                              const float* weight, float eps_low, float eps_high, float beta, float tau,
+                              const int32_t* starts, int K, int B, int T, int flags, const float* loss_scale,
+                              float* logp, float* loss);
+
+/* The step with the loss of pairs of answers (tt_op_preference): spans
+ * [2 pairs, 2] in rows b*T + t, ref_logp [B*T] or NULL, seq_logp [2 pairs] or
+ * NULL; 1 <= pairs <= B*T. */
+tt_status tt_gpt2_step_preference(tt_ctx* ctx, const void* params, float* grads, const int32_t* tokens,
+                                  const int32_t* targets, const float* ref_logp, const int32_t* spans, int pairs,
+                                  float beta, float gamma, float smoothing, int mean, float tau,
+                                  const int32_t* starts, int K, int B, int T, int flags, const float* loss_scale,
+                                  float* seq_logp, float* loss);
 
 /* Global gradient statistics, on the device: stats[0] = sqrt(sum_i (g_i /
  * s)^2) and stats[1] = 1 if that sum is not finite (an Inf or NaN gradient, or
