@@ -265,7 +265,7 @@ tt_status tt_op_policy(tt_ctx* ctx, tt_dtype dtype, const void* logits, const in
  * [2 pairs] may be NULL; mean_loss (may be NULL) receives the mean over the
  * pairs; dscale is usually 1/pairs.  dlogits and errors as for tt_op_policy.
  * beta > 0, 0 <= smoothing < 0.5, gamma finite.  Scratch from the arena:
- * 20 bytes a row. */
+ * 20 M + 4 bytes. */
 tt_status tt_op_preference(tt_ctx* ctx, tt_dtype dtype, const void* logits, const int32_t* targets,
                            const float* ref_logp, const int32_t* spans, void* dlogits, float* seq_logp,
                            float* pair_loss, float* mean_loss, int M, int V, int ld, int pairs, float beta,
