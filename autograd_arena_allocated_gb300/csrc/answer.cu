@@ -348,14 +348,29 @@ __global__ void __launch_bounds__(2 * PAIR_THREADS) k_pairs(const PairArgs a) {
     first += tid % PAIR_THREADS;
     double total = 0.0, score = 0.0;
     int n = 0;
-    for (long long r = first; r < last; r += PAIR_THREADS) {
-        const int y = a.targets[r];
-        const float lp = a.stat[r].w, ref = a.ref ? a.ref[r] : 0.0f;
-        if (y < 0 || y >= a.V) continue;
-        if (atomicExch(&a.claim[r], 1)) bad = true;  // in two answers
-        total += lp;
-        score += (double)lp - (double)ref;
-        n++;
+    constexpr int U = 4;  // rows in flight
+    for (long long r0 = first; r0 < last; r0 += U * PAIR_THREADS) {
+        float lp[U], ref[U];
+        int claimed[U];
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const long long r = r0 + u * PAIR_THREADS;
+            const int y = r < last ? a.targets[r] : -1;
+            on[u] = y >= 0 && y < a.V;
+            lp[u] = r < last ? a.stat[r].w : 0.0f;
+            ref[u] = r < last && a.ref ? a.ref[r] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) claimed[u] = on[u] ? atomicExch(&a.claim[r0 + u * PAIR_THREADS], 1) : 0;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (!on[u]) continue;
+            bad |= claimed[u] != 0;  // in two answers
+            total += lp[u];
+            score += (double)lp[u] - (double)ref[u];
+            n++;
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -405,9 +420,13 @@ __global__ void __launch_bounds__(2 * PAIR_THREADS) k_pairs(const PairArgs a) {
         }
     }
     __syncthreads();
-    for (long long r = first; r < last; r += PAIR_THREADS) {
-        const int y = a.targets[r];
-        if (y >= 0 && y < a.V) a.stat[r].z = s_coef[w];
+    for (long long r0 = first; r0 < last; r0 += U * PAIR_THREADS) {
+        int y[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) y[u] = r0 + u * PAIR_THREADS < last ? a.targets[r0 + u * PAIR_THREADS] : -1;
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (y[u] >= 0 && y[u] < a.V) a.stat[r0 + u * PAIR_THREADS].z = s_coef[w];
     }
     if (!a.mean_loss || a.pairs == 1 || !s_last) return;
     double sum = 0.0;
@@ -427,21 +446,22 @@ __global__ void __launch_bounds__(2 * PAIR_THREADS) k_pairs(const PairArgs a) {
 }
 
 // Threads that a row of G granules gets, 32 at least, then a warp of a CTA that
-// has ROWS of them.  As few as keep every SM busy with its 1024 (twice over
-// where a row is long, so that the last round of rows is a small part): fewer
-// threads a row are fewer barriers and less of a row's own latency.  At most
-// 512, and at least eight granules each.  In bf16, log probabilities of 20000 rows of
-// 2500 logits take 27 us by warps, 38 by 64 threads, 54 by 128 (20000 of 5000 36,
-// 40, 54; 300 of 50257 15 by 256 or 512, 19 by 1024); 32768 of 50257, half of them labelled, 279 by warps or 64 threads, 283
-// by 128, 337 by 256; 4000 of 150000 166 by 64, 128 by 128, 132 by 256.  (A row over
-// a cluster of two to eight CTAs: 2 us less for up to 16 rows, more from 64 rows
-// on: 150 rows 15 to 24.)
+// has ROWS of them.  Fewer threads a row are fewer barriers and less of a row's
+// own latency, as long as there are rows enough that every SM has its 1024, and
+// as long as a row is not so slow by itself (four loads in flight a thread) that
+// a last round of a few rows takes long: 80 granules a thread are some 16 us.  At
+// most 512, and at least eight granules each.  In bf16, log probabilities of
+// 20000 rows of 2500 logits take 27 us by warps, 38 by 64 threads, 54 by 128
+// (20000 of 5000 36, 40, 54; 300 of 50257 15 by 256 or 512, 19 by 1024); 32768 of
+// 50257, half of them labelled, 279 by warps or 64 threads, 283 by 128, 337 by
+// 256; 4000 of 150000 166 by 64, 128 by 128, 132 by 256.  (A row over a cluster of
+// two to eight CTAs: 2 us less for up to 16 rows, more from 64 rows on: 150 rows
+// 15 to 24.)
 constexpr int ROWS = 4;
 
 int row_threads(const Launch& L, int G, long long M) {
-    const long long want = L.num_sms * (G > 16384 ? 2048LL : 1024LL);
     int N = 32;
-    while (N < 512 && M * N < want && G >= 16 * N) N *= 2;
+    while (N < 512 && ((M * N < L.num_sms * 1024LL && G >= 16 * N) || G > 80 * N)) N *= 2;
     return N;
 }
 

@@ -1,6 +1,6 @@
 // attn_group.cu -- attention over groups of answers that share a prompt
-// (group.cuh), for fp32 and for head dimensions of 16 and 32; 16-bit heads of 64
-// take the tensor-core kernels (attn_tc.cu).
+// (group.cuh) in fp32, and the choice of the kernels: 16-bit heads of 64 take
+// attn_tc.cu's, of 16 and 32 attn_group_mma.cu's.
 //
 //   k_group_fwd   64 queries a CTA past blocks of 64 keys: S = Q K^T / sqrt(D),
 //                 running maximum and sum, O += P V
@@ -29,44 +29,13 @@ constexpr int NT = 256;
 constexpr int PS = BLK + 4;  // row of a 64 x 64 product
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float* f);
-template <> __device__ __forceinline__ void load8<float>(const float* p, float* f) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* f) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-template <> __device__ __forceinline__ void load8<__half>(const __half* p, float* f) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-    }
-}
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
-
 // 64 rows of D elements, ld apart, into shared memory; rows from `valid` on are zeros
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float* s, const T* g, long long ld, int valid) {
-    for (int i = threadIdx.x; i < BLK * (D / 8); i += NT) {
-        const int r = i / (D / 8), c = i % (D / 8) * 8;
-        float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (r < valid) load8(g + (long long)r * ld + c, f);
-        float4* d = reinterpret_cast<float4*>(s + r * (D + 4) + c);
-        d[0] = make_float4(f[0], f[1], f[2], f[3]);
-        d[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <int D>
+__device__ __forceinline__ void load_tile(float* s, const float* g, long long ld, int valid) {
+    for (int i = threadIdx.x; i < BLK * (D / 4); i += NT) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        *reinterpret_cast<float4*>(s + r * (D + 4) + c) =
+            r < valid ? *reinterpret_cast<const float4*>(g + (long long)r * ld + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 }
 
@@ -126,9 +95,16 @@ __device__ __forceinline__ void accumulate(const float* P, const float* X, int t
         for (int i = 0; i < 4; i++) {
             const float w[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
 #pragma unroll
-            for (int u = 0; u < 4; u++)
+            for (int u = 0; u < 4; u++) {
+                if (E == 1) o[i][0] = fmaf(w[u], x[u][0], o[i][0]);
 #pragma unroll
-                for (int e = 0; e < E; e++) o[i][e] = fmaf(w[u], x[u][e], o[i][e]);
+                for (int e = 0; e + 1 < E; e += 2) {
+                    const float2 r = __ffma2_rn(make_float2(w[u], w[u]), make_float2(x[u][e], x[u][e + 1]),
+                                                make_float2(o[i][e], o[i][e + 1]));
+                    o[i][e] = r.x;
+                    o[i][e + 1] = r.y;
+                }
+            }
         }
     }
 }
@@ -151,9 +127,9 @@ struct Place {
     }
 };
 
-template <typename T, int E> __device__ __forceinline__ void store_row(T* d, const float (&v)[E], float scale) {
+template <int E> __device__ __forceinline__ void store_row(float* d, const float (&v)[E], float scale) {
 #pragma unroll
-    for (int e = 0; e < E; e++) put(d + e, v[e] * scale);
+    for (int e = 0; e < E; e++) d[e] = v[e] * scale;
 }
 
 __device__ __forceinline__ float row_max(float v) {  // over the 16 lanes of a row
@@ -169,8 +145,8 @@ __device__ __forceinline__ float row_sum(float v) {
 
 template <int D> __host__ __device__ constexpr int tile_floats() { return BLK * (D + 4); }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(NT, 2) k_group_fwd(const T* qkv, T* y, float* lse, const GroupArgs a) {
+template <int D>
+__global__ void __launch_bounds__(NT, 2) k_group_fwd(const float* qkv, float* y, float* lse, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sK = sQ + tile_floats<D>(), *sV = sK + tile_floats<D>(), *sP = sV + tile_floats<D>();
@@ -179,8 +155,8 @@ __global__ void __launch_bounds__(NT, 2) k_group_fwd(const T* qkv, T* y, float* 
     const Group g(a.starts, at.b, a.K, a.T);
     const int q0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
-    const T* base = qkv + row0 * ld + at.h * D;
-    T* yb = y + row0 * a.C + at.h * D + tx * E;
+    const float* base = qkv + row0 * ld + at.h * D;
+    float* yb = y + row0 * a.C + at.h * D + tx * E;
     float* lb = lse + ((long long)at.b * a.H + at.h) * a.T;
     if (at.tile == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
     float o[4][E], m[4], l[4];
@@ -196,12 +172,12 @@ __global__ void __launch_bounds__(NT, 2) k_group_fwd(const T* qkv, T* y, float* 
     if (q0 < g.end) {  // uniform over the CTA
         const group::QueryTile tile(g, q0, BLK);
         const float sl2 = rsqrtf((float)D) * LOG2E;
-        load_tile<T, D>(sQ, base + q0 * ld, ld, g.end - q0);
+        load_tile<D>(sQ, base + q0 * ld, ld, g.end - q0);
         for (int j = 0; j < tile.n; j++) {
             const int k0 = tile.block(j) * BLK;
             __syncthreads();  // the block before has been used
-            load_tile<T, D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
-            load_tile<T, D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
+            load_tile<D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
+            load_tile<D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
             __syncthreads();
             float s[4][4];
             product<D>(sQ, sK, tx, ty, s);
@@ -245,9 +221,9 @@ __global__ void __launch_bounds__(NT, 2) k_group_fwd(const T* qkv, T* y, float* 
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT, 2)
-k_group_dq(const T* qkv, const T* y, const float* lse, const T* dy, T* dqkv, float* Dlt, const GroupArgs a) {
+k_group_dq(const float* qkv, const float* y, const float* lse, const float* dy, float* dqkv, float* Dlt, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sO = sQ + tile_floats<D>(), *sK = sO + tile_floats<D>(), *sV = sK + tile_floats<D>(),
@@ -257,7 +233,7 @@ k_group_dq(const T* qkv, const T* y, const float* lse, const T* dy, T* dqkv, flo
     const Group g(a.starts, at.b, a.K, a.T);
     const int q0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
-    const T* base = qkv + row0 * ld + at.h * D;
+    const float* base = qkv + row0 * ld + at.h * D;
     const long long bh = ((long long)at.b * a.H + at.h) * a.T;
     if (at.tile == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
     float o[4][E];
@@ -269,9 +245,9 @@ k_group_dq(const T* qkv, const T* y, const float* lse, const T* dy, T* dqkv, flo
     if (q0 < g.end) {
         const group::QueryTile tile(g, q0, BLK);
         const float sl2 = scale * LOG2E;
-        load_tile<T, D>(sQ, base + q0 * ld, ld, g.end - q0);
-        load_tile<T, D>(sO, dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
-        load_tile<T, D>(sK, y + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);  // y, for D alone
+        load_tile<D>(sQ, base + q0 * ld, ld, g.end - q0);
+        load_tile<D>(sO, dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
+        load_tile<D>(sK, y + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);  // y, for D alone
         __syncthreads();
         float L[4], Dr[4];
         int st[4];
@@ -289,8 +265,8 @@ k_group_dq(const T* qkv, const T* y, const float* lse, const T* dy, T* dqkv, flo
         for (int j = 0; j < tile.n; j++) {
             const int k0 = tile.block(j) * BLK;
             __syncthreads();
-            load_tile<T, D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
-            load_tile<T, D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
+            load_tile<D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
+            load_tile<D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
             __syncthreads();
             float s[4][4], dp[4][4];
             product<D>(sQ, sK, tx, ty, s);
@@ -309,7 +285,7 @@ k_group_dq(const T* qkv, const T* y, const float* lse, const T* dy, T* dqkv, flo
             accumulate<D>(sS, sK, tx, ty, o);
         }
     }
-    T* ob = dqkv + row0 * ld + at.h * D + tx * E;
+    float* ob = dqkv + row0 * ld + at.h * D + tx * E;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int q = q0 + ty + 16 * i;
@@ -317,9 +293,9 @@ k_group_dq(const T* qkv, const T* y, const float* lse, const T* dy, T* dqkv, flo
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT, 2)
-k_group_dkdv(const T* qkv, const float* lse, const T* dy, T* dqkv, const float* Dlt, const GroupArgs a) {
+k_group_dkdv(const float* qkv, const float* lse, const float* dy, float* dqkv, const float* Dlt, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
     float *sK = sm, *sV = sK + tile_floats<D>(), *sQ = sV + tile_floats<D>(), *sO = sQ + tile_floats<D>(),
@@ -330,7 +306,7 @@ k_group_dkdv(const T* qkv, const float* lse, const T* dy, T* dqkv, const float* 
     const Group g(a.starts, at.b, a.K, a.T);
     const int k0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
-    const T* base = qkv + row0 * ld + at.h * D;
+    const float* base = qkv + row0 * ld + at.h * D;
     const long long bh = ((long long)at.b * a.H + at.h) * a.T;
     const float scale = rsqrtf((float)D);
     float dk[4][E], dv[4][E];
@@ -341,8 +317,8 @@ k_group_dkdv(const T* qkv, const float* lse, const T* dy, T* dqkv, const float* 
     if (k0 < g.end) {
         const group::KeyTile tile(g, k0, BLK);
         const float sl2 = scale * LOG2E;
-        load_tile<T, D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
-        load_tile<T, D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
+        load_tile<D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
+        load_tile<D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
         int kend[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -352,8 +328,8 @@ k_group_dkdv(const T* qkv, const float* lse, const T* dy, T* dqkv, const float* 
         for (int j = 0; j < tile.n; j++) {
             const int q0 = (tile.j0 + j) * BLK;
             __syncthreads();
-            load_tile<T, D>(sQ, base + q0 * ld, ld, g.end - q0);
-            load_tile<T, D>(sO, dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
+            load_tile<D>(sQ, base + q0 * ld, ld, g.end - q0);
+            load_tile<D>(sO, dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
             if (threadIdx.x < BLK) {
                 const int q = q0 + threadIdx.x;
                 s_L[threadIdx.x] = q < g.end ? lse[bh + q] * LOG2E : 0.0f;
@@ -382,7 +358,7 @@ k_group_dkdv(const T* qkv, const float* lse, const T* dy, T* dqkv, const float* 
             accumulate<D>(sS, sQ, tx, ty, dk);
         }
     }
-    T* ob = dqkv + row0 * ld + at.h * D + tx * E;
+    float* ob = dqkv + row0 * ld + at.h * D + tx * E;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int k = k0 + ty + 16 * i;
@@ -398,37 +374,27 @@ template <typename K> bool allow(PerDevice& done, K kern, size_t smem) {
     });
 }
 
-template <typename T, int D>
-bool fwd(const Launch& L, const void* qkv, void* y, float* lse, const GroupArgs& a, int ctas) {
+template <int D> bool fwd(const Launch& L, const float* qkv, float* y, float* lse, const GroupArgs& a, int ctas) {
     static PerDevice done;
     constexpr size_t smem = (3 * tile_floats<D>() + BLK * PS) * 4;
-    if (!allow(done, k_group_fwd<T, D>, smem)) return false;
+    if (!allow(done, k_group_fwd<D>, smem)) return false;
     L.count();
-    launch_k(L, k_group_fwd<T, D>, dim3(ctas), dim3(NT), smem, (const T*)qkv, (T*)y, lse, a);
+    launch_k(L, k_group_fwd<D>, dim3(ctas), dim3(NT), smem, qkv, y, lse, a);
     return true;
 }
 
-template <typename T, int D>
-bool bwd(const Launch& L, const void* qkv, const void* y, const float* lse, const void* dy, void* dqkv, float* Dlt,
+template <int D>
+bool bwd(const Launch& L, const float* qkv, const float* y, const float* lse, const float* dy, float* dqkv, float* Dlt,
          const GroupArgs& a, int ctas) {
     static PerDevice done_q, done_k;
     constexpr size_t sq = (4 * tile_floats<D>() + BLK * PS) * 4, sk = (4 * tile_floats<D>() + 2 * BLK * PS) * 4;
-    if (!allow(done_q, k_group_dq<T, D>, sq) || !allow(done_k, k_group_dkdv<T, D>, sk)) return false;
+    if (!allow(done_q, k_group_dq<D>, sq) || !allow(done_k, k_group_dkdv<D>, sk)) return false;
     L.count();
-    launch_k(L, k_group_dq<T, D>, dim3(ctas), dim3(NT), sq, (const T*)qkv, (const T*)y, lse, (const T*)dy, (T*)dqkv, Dlt, a);
+    launch_k(L, k_group_dq<D>, dim3(ctas), dim3(NT), sq, qkv, y, lse, dy, dqkv, Dlt, a);
     L.count();
-    launch_k(L, k_group_dkdv<T, D>, dim3(ctas), dim3(NT), sk, (const T*)qkv, lse, (const T*)dy, (T*)dqkv, (const float*)Dlt,
-             a);
+    launch_k(L, k_group_dkdv<D>, dim3(ctas), dim3(NT), sk, qkv, lse, dy, dqkv, (const float*)Dlt, a);
     return true;
 }
-
-// FN over the storage type and the head dimension (16-bit heads of 64 go elsewhere)
-#define GROUP_DISPATCH(FN, ...)                                               \
-    (!bf16   ? hd == 16   ? FN<float, 16>(__VA_ARGS__)                        \
-               : hd == 32 ? FN<float, 32>(__VA_ARGS__)                        \
-                          : FN<float, 64>(__VA_ARGS__)                        \
-     : L.f16 ? hd == 16 ? FN<__half, 16>(__VA_ARGS__) : FN<__half, 32>(__VA_ARGS__) \
-             : hd == 16 ? FN<__nv_bfloat16, 16>(__VA_ARGS__) : FN<__nv_bfloat16, 32>(__VA_ARGS__))
 
 GroupArgs args_of(const Launch& L, const int32_t* starts, int T, int C, int H, int K) {
     GroupArgs a{};
@@ -445,8 +411,15 @@ bool launch_group_attention_fwd(const Launch& L, bool bf16, const void* qkv, con
     if (L.dry) return true;
     const int hd = C / H;
     if (bf16 && hd == 64) return launch_attention_fwd_tc(L, qkv, y, lse, B, T, C, H, starts, K);
+    if (bf16) {
+        launch_group_fwd_mma(L, qkv, starts, y, lse, B, T, C, H, K);
+        return true;
+    }
     const GroupArgs a = args_of(L, starts, T, C, H, K);
-    return GROUP_DISPATCH(fwd, L, qkv, y, lse, a, a.tiles * B * H);
+    const int ctas = a.tiles * B * H;
+    const auto *q = (const float*)qkv;
+    auto* o = (float*)y;
+    return hd == 16 ? fwd<16>(L, q, o, lse, a, ctas) : hd == 32 ? fwd<32>(L, q, o, lse, a, ctas) : fwd<64>(L, q, o, lse, a, ctas);
 }
 
 bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, const int32_t* starts, const void* y,
@@ -461,8 +434,16 @@ bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, con
         if (dbias) launch_sum_rows(L, bpart, B * ((T + 127) / 128), 3 * C, 3 * C, dbias, nullptr, acc_bias);
         return true;
     }
-    const GroupArgs a = args_of(L, starts, T, C, H, K);
-    if (!GROUP_DISPATCH(bwd, L, qkv, y, lse, dy, dqkv, scratch, a, a.tiles * B * H)) return false;
+    if (bf16) {
+        launch_group_bwd_mma(L, qkv, starts, y, lse, dy, dqkv, B, T, C, H, K, scratch);
+    } else {
+        const GroupArgs a = args_of(L, starts, T, C, H, K);
+        const int ctas = a.tiles * B * H;
+        auto run = [&](auto f) {
+            return f(L, (const float*)qkv, (const float*)y, lse, (const float*)dy, (float*)dqkv, scratch, a, ctas);
+        };
+        if (!(hd == 16 ? run(bwd<16>) : hd == 32 ? run(bwd<32>) : run(bwd<64>))) return false;
+    }
     if (dbias) launch_colsum(L, bf16, dqkv, B * T, 3 * C, dbias, bpart, acc_bias);
     return true;
 }

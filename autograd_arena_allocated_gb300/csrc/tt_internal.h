@@ -247,8 +247,7 @@ bool launch_attention_bwd_tc(const Launch& L, const void* qkv, const void* y, co
                              const void* dy, void* dqkv, int B, int T, int C, int H, float* Dlt,
                              float* bpart = nullptr, const int32_t* starts = nullptr, int K = 0);
 
-// attention over groups (attn_group.cu, and the tensor-core kernels for 16-bit
-// heads of 64): L.f16 as in launch_attention_fwd; false: not launched.  scratch
+// attention over groups (attn_group.cu): L.f16 as in launch_attention_fwd; false: not launched.  scratch
 // as for launch_attention_bwd, whose first part alone, attention_d_floats(), is
 // used without dbias (which may be NULL, as there).
 size_t attention_d_floats(int B, int T, int H);
@@ -257,6 +256,11 @@ bool launch_group_attention_fwd(const Launch& L, bool bf16, const void* qkv, con
 bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, const int32_t* starts, const void* y,
                                 const float* lse, const void* dy, void* dqkv, int B, int T, int C, int H, int K,
                                 float* scratch, float* dbias = nullptr, bool acc_bias = false);
+// its 16-bit heads of 16 and 32 (attn_group_mma.cu)
+void launch_group_fwd_mma(const Launch& L, const void* qkv, const int32_t* starts, void* y, float* lse, int B, int T, int C,
+                          int H, int K);
+void launch_group_bwd_mma(const Launch& L, const void* qkv, const int32_t* starts, const void* y, const float* lse,
+                          const void* dy, void* dqkv, int B, int T, int C, int H, int K, float* Dlt);
 
 // decoding with a key/value cache (decode.cu); cache per layer [B, maxT, 2C].
 // The decode-step kernels read the newest position from device memory
