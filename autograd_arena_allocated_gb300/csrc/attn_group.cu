@@ -8,16 +8,17 @@
 //   k_group_dkdv  64 keys a CTA past blocks of 64 queries: dV += P^T dO,
 //                 dK += dS^T Q (a prompt's keys: every answer's queries, in order)
 //
-// All in fp32 FMAs, two lanes an instruction; the operands lie in shared memory
-// as rows of D floats, padded by four so that the rows of eight lanes fall in
-// different banks.  A thread of the 16 x 16 owns rows ty + 16 i and columns
-// tx + 16 j of a 64 x 64 product, and rows ty + 16 i and D / 16 neighbouring
-// columns of a 64 x D one: eight 16-byte loads for 64 multiply-adds, which is
-// what bounds it.
+// All in fp32 FMAs, two rows an instruction.  A thread of the 8 x 16 owns rows 8 ty
+// .. + 7 and columns 4 tx .. + 3 of a 64 x 64 product, and the same rows and D / 16
+// columns of a 64 x D one: 32 multiply-adds take three 16-byte loads from shared
+// memory.  The tiles that a product sums over D lie transposed.  The next block is
+// fetched into registers while the products run.  What bounds it is the issue of
+// instructions, half of them FMAs: 8 groups of 1000 positions, 12 heads of 64, 374
+// us forward and 1013 backward, 27 and 25 TFLOP/s of some 74 (one group of 1976, 16
+// heads, 258 and 681; by pieces of 4 x 4 that read two rows a time, without the
+// fetch ahead, 293 and 913).
 #include "tt_internal.h"
 #include "group.cuh"
-
-#include <algorithm>
 
 namespace tt {
 namespace {
@@ -25,111 +26,136 @@ namespace {
 using group::BLK;
 using group::Group;
 
-constexpr int NT = 256;
-constexpr int PS = BLK + 4;  // row of a 64 x 64 product
+constexpr int NT = 128;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// 64 rows of D elements, ld apart, into shared memory; rows from `valid` on are zeros
-template <int D>
-__device__ __forceinline__ void load_tile(float* s, const float* g, long long ld, int valid) {
-    for (int i = threadIdx.x; i < BLK * (D / 4); i += NT) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        *reinterpret_cast<float4*>(s + r * (D + 4) + c) =
-            r < valid ? *reinterpret_cast<const float4*>(g + (long long)r * ld + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
+// places in the tiles, in floats: [64][D] by rows, [D][64] transposed, and a 64 x 64
+// product transposed, [column][row].  Loads meet no bank twice; the stores of a
+// row tile and of a product do four times, which costs less than the arithmetic of
+// a swizzle in the loops that load.
+constexpr int PS = BLK + 4;
+template <int D> __device__ __forceinline__ int at_row(int row, int col) { return row * D + col; }
+__device__ __forceinline__ int at_col(int d, int row) { return d * BLK + row; }
+__device__ __forceinline__ int at_prod(int col, int row) { return col * PS + row; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// acc[i][j] = sum_d A[ty + 16 i][d] B[tx + 16 j][d]
-template <int D>
-__device__ __forceinline__ void product(const float* A, const float* B, int tx, int ty, float (&acc)[4][4]) {
-    float2 s[4][4];
+// a thread's part of 64 rows of D floats: two neighbouring threads have a row
+template <int D> struct Piece {
+    float4 v[D / 8];
+    // rows of g, ld apart; those from `valid` on are zeros
+    __device__ __forceinline__ void load(const float* g, long long ld, int valid) {
+        const int r = threadIdx.x >> 1;
+#pragma unroll
+        for (int i = 0; i < D / 8; i++)
+            v[i] = r < valid ? *reinterpret_cast<const float4*>(g + r * ld + 4 * ((threadIdx.x & 1) + 2 * i))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void rows(float* s) const {
+        const int r = threadIdx.x >> 1;
+#pragma unroll
+        for (int i = 0; i < D / 8; i++) *reinterpret_cast<float4*>(s + at_row<D>(r, 4 * ((threadIdx.x & 1) + 2 * i))) = v[i];
+    }
+    __device__ __forceinline__ void cols(float* s) const {
+        const int r = threadIdx.x >> 1;
+#pragma unroll
+        for (int i = 0; i < D / 8; i++) {
+            const int d = 4 * ((threadIdx.x & 1) + 2 * i);
+            s[at_col(d, r)] = v[i].x;
+            s[at_col(d + 1, r)] = v[i].y;
+            s[at_col(d + 2, r)] = v[i].z;
+            s[at_col(d + 3, r)] = v[i].w;
+        }
+    }
+};
+
+// acc[i][j]: rows 8 ty + 2 i, + 1 of column 4 tx + j
+using Acc = float2[4][4];
+
+// sum over d of A[row][d] B[col][d], both tiles transposed
+template <int D> __device__ __forceinline__ void product(const float* A, const float* B, int tx, int ty, Acc& s) {
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) s[i][j] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-        float4 a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * (D + 4) + d);
-#pragma unroll
-        for (int j = 0; j < 4; j++) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (D + 4) + d);
+#pragma unroll 8
+    for (int d = 0; d < D; d++) {
+        const float4 a0 = *reinterpret_cast<const float4*>(A + at_col(d, 8 * ty));
+        const float4 a1 = *reinterpret_cast<const float4*>(A + at_col(d, 8 * ty + 4));
+        const float4 b = *reinterpret_cast<const float4*>(B + at_col(d, 4 * tx));
+        const float2 a[4] = {make_float2(a0.x, a0.y), make_float2(a0.z, a0.w), make_float2(a1.x, a1.y), make_float2(a1.z, a1.w)};
+        const float c[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                s[i][j] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s[i][j]);
-                s[i][j] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s[i][j]);
-            }
+            for (int j = 0; j < 4; j++) s[i][j] = __ffma2_rn(a[i], make_float2(c[j], c[j]), s[i][j]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = s[i][j].x + s[i][j].y;
 }
 
-// o[i][e] += sum_k P[ty + 16 i][k] X[k][tx E + e], E = D / 16
+// o[i][e] += sum over k of P[k][rows 8 ty + 2 i, + 1] X[k][tx E + e], E = D / 16
 template <int D>
-__device__ __forceinline__ void accumulate(const float* P, const float* X, int tx, int ty, float (&o)[4][D / 16]) {
+__device__ __forceinline__ void accumulate(const float* P, const float* X, int tx, int ty, float2 (&o)[4][D / 16]) {
     constexpr int E = D / 16;
-#pragma unroll 4
-    for (int k = 0; k < BLK; k += 4) {
-        float4 p[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) p[i] = *reinterpret_cast<const float4*>(P + (ty + 16 * i) * PS + k);
-        float x[4][E];
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            const float* r = X + (k + u) * (D + 4) + tx * E;
-            if (E == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(r);
-                x[u][0] = v.x; x[u][E > 1 ? 1 : 0] = v.y; x[u][E > 2 ? 2 : 0] = v.z; x[u][E > 3 ? 3 : 0] = v.w;
-            } else if (E == 2) {
-                const float2 v = *reinterpret_cast<const float2*>(r);
-                x[u][0] = v.x; x[u][E > 1 ? 1 : 0] = v.y;
-            } else {
-                x[u][0] = *r;
-            }
+#pragma unroll 8
+    for (int k = 0; k < BLK; k++) {
+        const float4 a0 = *reinterpret_cast<const float4*>(P + at_prod(k, 8 * ty));
+        const float4 a1 = *reinterpret_cast<const float4*>(P + at_prod(k, 8 * ty + 4));
+        const float2 a[4] = {make_float2(a0.x, a0.y), make_float2(a0.z, a0.w), make_float2(a1.x, a1.y), make_float2(a1.z, a1.w)};
+        const float* x = X + at_row<D>(k, tx * E);
+        float c[4];
+        if (E == 4) {
+            const float4 b = *reinterpret_cast<const float4*>(x);
+            c[0] = b.x; c[1] = b.y; c[2] = b.z; c[3] = b.w;
+        } else if (E == 2) {
+            const float2 b = *reinterpret_cast<const float2*>(x);
+            c[0] = b.x; c[1] = b.y;
+        } else {
+            c[0] = *x;
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float w[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                if (E == 1) o[i][0] = fmaf(w[u], x[u][0], o[i][0]);
-#pragma unroll
-                for (int e = 0; e + 1 < E; e += 2) {
-                    const float2 r = __ffma2_rn(make_float2(w[u], w[u]), make_float2(x[u][e], x[u][e + 1]),
-                                                make_float2(o[i][e], o[i][e + 1]));
-                    o[i][e] = r.x;
-                    o[i][e + 1] = r.y;
-                }
-            }
-        }
+            for (int e = 0; e < E; e++) o[i][e] = __ffma2_rn(a[i], make_float2(c[e], c[e]), o[i][e]);
     }
+}
+
+// row r = 0 .. 7 of a thread's
+__device__ __forceinline__ float& of(Acc& s, int r, int j) { return r & 1 ? s[r >> 1][j].y : s[r >> 1][j].x; }
+
+// a product goes to shared memory for accumulate; its 16 lanes of a row group alone
+// read it
+__device__ __forceinline__ void put_product(float* P, const Acc& s, int tx, int ty) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        *reinterpret_cast<float4*>(P + at_prod(4 * tx + j, 8 * ty)) = make_float4(s[0][j].x, s[0][j].y, s[1][j].x, s[1][j].y);
+        *reinterpret_cast<float4*>(P + at_prod(4 * tx + j, 8 * ty + 4)) =
+            make_float4(s[2][j].x, s[2][j].y, s[3][j].x, s[3][j].y);
+    }
+    __syncwarp();
 }
 
 struct GroupArgs {
     const int32_t* starts;
-    int T, C, H, K, tiles;
+    int T, C, H, K, tiles, pairs;
     int* flags;
 };
 
-// CTA -> (tile, head, sequence): a head's tiles side by side, so that they share
-// its keys in L2; the tiles with the most work first
-struct Place {
-    int tile, h, b;
-    __device__ __forceinline__ Place(const GroupArgs& a, bool last_first) {
-        const int t = blockIdx.x % a.tiles, bh = blockIdx.x / a.tiles;
-        tile = last_first ? a.tiles - 1 - t : t;
-        b = bh / a.H;
-        h = bh % a.H;
-    }
-};
-
-template <int E> __device__ __forceinline__ void store_row(float* d, const float (&v)[E], float scale) {
+template <int E> __device__ __forceinline__ void zero(float2 (&o)[4][E]) {
 #pragma unroll
-    for (int e = 0; e < E; e++) d[e] = v[e] * scale;
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int e = 0; e < E; e++) o[i][e] = make_float2(0.0f, 0.0f);
+}
+
+// row r of a thread's E columns, times scale; zeros where it is padding
+template <int E> __device__ __forceinline__ void store_row(float* d, const float2 (&o)[4][E], int r, float scale, bool real) {
+#pragma unroll
+    for (int e = 0; e < E; e++) d[e] = real ? (r & 1 ? o[r >> 1][e].y : o[r >> 1][e].x) * scale : 0.0f;
 }
 
 __device__ __forceinline__ float row_max(float v) {  // over the 16 lanes of a row
@@ -143,81 +169,86 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-template <int D> __host__ __device__ constexpr int tile_floats() { return BLK * (D + 4); }
-
-template <int D>
-__global__ void __launch_bounds__(NT, 2) k_group_fwd(const float* qkv, float* y, float* lse, const GroupArgs a) {
+template <int D> __global__ void __launch_bounds__(NT, 3) k_group_fwd(const float* qkv, float* y, float* lse, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sK = sQ + tile_floats<D>(), *sV = sK + tile_floats<D>(), *sP = sV + tile_floats<D>();
+    float *sQ = sm, *sK = sQ + BLK * D, *sV = sK + BLK * D, *sP = sV + BLK * D;
     constexpr int E = D / 16;
-    const Place at(a, true);
+    const group::Place at(a.tiles, a.pairs, a.H, true);
     const Group g(a.starts, at.b, a.K, a.T);
     const int q0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
     const float* base = qkv + row0 * ld + at.h * D;
-    float* yb = y + row0 * a.C + at.h * D + tx * E;
-    float* lb = lse + ((long long)at.b * a.H + at.h) * a.T;
-    if (at.tile == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
-    float o[4][E], m[4], l[4];
-    int st[4];
+    if (q0 == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
+    float2 o[4][E];
+    zero(o);
+    float m[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        m[i] = -3e38f;  // finite: a row may see nothing of a block
-        l[i] = 0.0f;
-        st[i] = g.start_of(q0 + ty + 16 * i);
-#pragma unroll
-        for (int e = 0; e < E; e++) o[i][e] = 0.0f;
+    for (int r = 0; r < 8; r++) {
+        m[r] = -3e38f;  // finite: a row may see nothing of a block
+        l[r] = 0.0f;
     }
+    const float sl2 = rsqrtf((float)D) * LOG2E;
     if (q0 < g.end) {  // uniform over the CTA
         const group::QueryTile tile(g, q0, BLK);
-        const float sl2 = rsqrtf((float)D) * LOG2E;
-        load_tile<D>(sQ, base + q0 * ld, ld, g.end - q0);
+        Piece<D> k, v;
+        k.load(base + q0 * ld, ld, g.end - q0);
+        k.cols(sQ);
+        auto fetch = [&](int j) {
+            const int k0 = tile.block(j) * BLK;
+            k.load(base + a.C + k0 * ld, ld, g.end - k0);
+            v.load(base + 2 * a.C + k0 * ld, ld, g.end - k0);
+        };
+        fetch(0);
         for (int j = 0; j < tile.n; j++) {
             const int k0 = tile.block(j) * BLK;
             __syncthreads();  // the block before has been used
-            load_tile<D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
-            load_tile<D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
+            k.cols(sK);
+            v.rows(sV);
             __syncthreads();
-            float s[4][4];
+            if (j + 1 < tile.n) fetch(j + 1);
+            Acc s;
             product<D>(sQ, sK, tx, ty, s);
-            const bool masked = tile.masked(k0);
+            if (tile.masked(k0)) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const unsigned long long seen = masked ? g.keys(q0 + ty + 16 * i, st[i], k0) : ~0ull;
-                float mx = -3e38f;
+                for (int r = 0; r < 8; r++) {
+                    const int q = q0 + 8 * ty + r;
+                    const uint32_t seen = (uint32_t)(g.keys(q, g.start_of(q), k0) >> (4 * tx));
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    s[i][c] *= sl2;
-                    if (seen >> (tx + 16 * c) & 1) mx = fmaxf(mx, s[i][c]);
+                    for (int c = 0; c < 4; c++)
+                        if (!(seen >> c & 1u)) of(s, r, c) = -INFINITY;
                 }
-                const float mn = fmaxf(m[i], row_max(mx)), corr = exp2f(m[i] - mn);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; r++) {
+                // m is the largest score, before the scale
+                const float mx = row_max(fmaxf(fmaxf(of(s, r, 0), of(s, r, 1)), fmaxf(of(s, r, 2), of(s, r, 3))));
+                const float mn = fmaxf(m[r], mx), corr = ex2((m[r] - mn) * sl2);
                 float rs = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                    const float p = seen >> (tx + 16 * c) & 1 ? exp2f(s[i][c] - mn) : 0.0f;
-                    sP[(ty + 16 * i) * PS + tx + 16 * c] = p;
-                    rs += p;
+                    of(s, r, c) = ex2((of(s, r, c) - mn) * sl2);  // of -inf: 0
+                    rs += of(s, r, c);
                 }
-                m[i] = mn;
-                l[i] = l[i] * corr + row_sum(rs);
+                m[r] = mn;
+                l[r] = l[r] * corr + rs;  // this lane's columns; the lanes' sums meet at the end
 #pragma unroll
-                for (int e = 0; e < E; e++) o[i][e] *= corr;
+                for (int e = 0; e < E; e++) {
+                    if (r & 1) o[r >> 1][e].y *= corr;
+                    else o[r >> 1][e].x *= corr;
+                }
             }
-            __syncwarp();  // a row of P is its 16 lanes' own
+            put_product(sP, s, tx, ty);
             accumulate<D>(sP, sV, tx, ty, o);
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int q = q0 + ty + 16 * i;
+    for (int r = 0; r < 8; r++) {
+        const int q = q0 + 8 * ty + r;
+        const float sum = row_sum(l[r]);
         if (q >= a.T) continue;
-        const bool on = q < g.end;
-        float v[E];
-#pragma unroll
-        for (int e = 0; e < E; e++) v[e] = on ? o[i][e] / l[i] : 0.0f;
-        store_row(yb + (long long)q * a.C, v, 1.0f);
-        if (tx == 0) lb[q] = on ? (m[i] + log2f(l[i])) * LN2 : 0.0f;
+        store_row(y + (row0 + q) * a.C + at.h * D + tx * E, o, r, 1.0f / sum, q < g.end);
+        if (tx == 0) lse[((long long)at.b * a.H + at.h) * a.T + q] = q < g.end ? (m[r] * sl2 + log2f(sum)) * LN2 : 0.0f;
     }
 }
 
@@ -226,70 +257,82 @@ __global__ void __launch_bounds__(NT, 2)
 k_group_dq(const float* qkv, const float* y, const float* lse, const float* dy, float* dqkv, float* Dlt, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sO = sQ + tile_floats<D>(), *sK = sO + tile_floats<D>(), *sV = sK + tile_floats<D>(),
-          *sS = sV + tile_floats<D>();
+    float *sQ = sm, *sO = sQ + BLK * D, *sK = sO + BLK * D, *sV = sK + BLK * D, *sX = sV + BLK * D, *sS = sX + BLK * D;
     constexpr int E = D / 16;
-    const Place at(a, true);
+    const group::Place at(a.tiles, a.pairs, a.H, true);
     const Group g(a.starts, at.b, a.K, a.T);
     const int q0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
+    const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T, bh = ((long long)at.b * a.H + at.h) * a.T;
     const float* base = qkv + row0 * ld + at.h * D;
-    const long long bh = ((long long)at.b * a.H + at.h) * a.T;
-    if (at.tile == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
-    float o[4][E];
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int e = 0; e < E; e++) o[i][e] = 0.0f;
+    if (q0 == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
+    float2 o[4][E];
+    zero(o);
     const float scale = rsqrtf((float)D);
     if (q0 < g.end) {
         const group::QueryTile tile(g, q0, BLK);
         const float sl2 = scale * LOG2E;
-        load_tile<D>(sQ, base + q0 * ld, ld, g.end - q0);
-        load_tile<D>(sO, dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
-        load_tile<D>(sK, y + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);  // y, for D alone
-        __syncthreads();
-        float L[4], Dr[4];
-        int st[4];
+        __shared__ float s_D[BLK];
+        Piece<D> k, v;
+        k.load(base + q0 * ld, ld, g.end - q0);
+        k.cols(sQ);
+        // D = rowsum(dO o O): the two threads of a row add their halves
+        k.load(dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
+        k.cols(sO);
+        v.load(y + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
+        float d = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int r = ty + 16 * i, q = q0 + r;
-            float d = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; e++) d = fmaf(sO[r * (D + 4) + tx * E + e], sK[r * (D + 4) + tx * E + e], d);
-            Dr[i] = row_sum(d);
-            L[i] = q < g.end ? lse[bh + q] * LOG2E : 0.0f;
-            st[i] = g.start_of(q);
-            if (tx == 0 && q < g.end) Dlt[bh + q] = Dr[i];
+        for (int i = 0; i < D / 8; i++)
+            d = fmaf(k.v[i].x, v.v[i].x, fmaf(k.v[i].y, v.v[i].y, fmaf(k.v[i].z, v.v[i].z, fmaf(k.v[i].w, v.v[i].w, d))));
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        if ((threadIdx.x & 1) == 0) {
+            const int q = q0 + (threadIdx.x >> 1);
+            s_D[threadIdx.x >> 1] = d;
+            if (q < g.end) Dlt[bh + q] = d;
         }
+        float L[8];
+#pragma unroll
+        for (int r = 0; r < 8; r++) L[r] = q0 + 8 * ty + r < g.end ? lse[bh + q0 + 8 * ty + r] * LOG2E : 0.0f;
+        auto fetch = [&](int j) {
+            const int k0 = tile.block(j) * BLK;
+            k.load(base + a.C + k0 * ld, ld, g.end - k0);
+            v.load(base + 2 * a.C + k0 * ld, ld, g.end - k0);
+        };
+        fetch(0);
         for (int j = 0; j < tile.n; j++) {
             const int k0 = tile.block(j) * BLK;
             __syncthreads();
-            load_tile<D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
-            load_tile<D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
+            k.cols(sK);
+            k.rows(sX);
+            v.cols(sV);
             __syncthreads();
-            float s[4][4], dp[4][4];
+            if (j + 1 < tile.n) fetch(j + 1);
+            Acc s, dp;
             product<D>(sQ, sK, tx, ty, s);
             product<D>(sO, sV, tx, ty, dp);
-            const bool masked = tile.masked(k0);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const unsigned long long seen =
-                    masked ? g.keys(q0 + ty + 16 * i, st[i], k0) : q0 + ty + 16 * i < g.end ? ~0ull : 0ull;
+            for (int r = 0; r < 8; r++) {
+                const float Dr = s_D[8 * ty + r];
 #pragma unroll
-                for (int c = 0; c < 4; c++)
-                    sS[(ty + 16 * i) * PS + tx + 16 * c] =
-                        seen >> (tx + 16 * c) & 1 ? exp2f(fmaf(s[i][c], sl2, -L[i])) * (dp[i][c] - Dr[i]) : 0.0f;
+                for (int c = 0; c < 4; c++) of(s, r, c) = ex2(fmaf(of(s, r, c), sl2, -L[r])) * (of(dp, r, c) - Dr);
             }
-            __syncwarp();
-            accumulate<D>(sS, sK, tx, ty, o);
+            if (tile.masked(k0)) {
+#pragma unroll
+                for (int r = 0; r < 8; r++) {
+                    const int q = q0 + 8 * ty + r;
+                    const uint32_t seen = (uint32_t)(g.keys(q, g.start_of(q), k0) >> (4 * tx));
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        if (!(seen >> c & 1u)) of(s, r, c) = 0.0f;
+                }
+            }
+            put_product(sS, s, tx, ty);
+            accumulate<D>(sS, sX, tx, ty, o);
         }
     }
-    float* ob = dqkv + row0 * ld + at.h * D + tx * E;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int q = q0 + ty + 16 * i;
-        if (q < a.T) store_row(ob + (long long)q * ld, o[i], q < g.end ? scale : 0.0f);
+    for (int r = 0; r < 8; r++) {
+        const int q = q0 + 8 * ty + r;
+        if (q < a.T) store_row(dqkv + (row0 + q) * ld + at.h * D + tx * E, o, r, scale, q < g.end);
     }
 }
 
@@ -298,73 +341,81 @@ __global__ void __launch_bounds__(NT, 2)
 k_group_dkdv(const float* qkv, const float* lse, const float* dy, float* dqkv, const float* Dlt, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
-    float *sK = sm, *sV = sK + tile_floats<D>(), *sQ = sV + tile_floats<D>(), *sO = sQ + tile_floats<D>(),
-          *sP = sO + tile_floats<D>(), *sS = sP + BLK * PS;
-    __shared__ float s_L[BLK], s_D[BLK];
+    float *sK = sm, *sV = sK + BLK * D, *sQ = sV + BLK * D, *sO = sQ + BLK * D, *sX = sO + BLK * D, *sY = sX + BLK * D,
+          *sP = sY + BLK * D;
     constexpr int E = D / 16;
-    const Place at(a, false);
+    const group::Place at(a.tiles, a.pairs, a.H, false);
     const Group g(a.starts, at.b, a.K, a.T);
     const int k0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
+    const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T, bh = ((long long)at.b * a.H + at.h) * a.T;
     const float* base = qkv + row0 * ld + at.h * D;
-    const long long bh = ((long long)at.b * a.H + at.h) * a.T;
     const float scale = rsqrtf((float)D);
-    float dk[4][E], dv[4][E];
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int e = 0; e < E; e++) dk[i][e] = dv[i][e] = 0.0f;
+    float2 dk[4][E], dv[4][E];
+    zero(dk);
+    zero(dv);
     if (k0 < g.end) {
         const group::KeyTile tile(g, k0, BLK);
         const float sl2 = scale * LOG2E;
-        load_tile<D>(sK, base + a.C + k0 * ld, ld, g.end - k0);
-        load_tile<D>(sV, base + 2 * a.C + k0 * ld, ld, g.end - k0);
-        int kend[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int k = k0 + ty + 16 * i;
-            kend[i] = k < g.end ? g.end_of(k) : 0;
-        }
+        Piece<D> q, o;
+        q.load(base + a.C + k0 * ld, ld, g.end - k0);
+        q.cols(sK);
+        q.load(base + 2 * a.C + k0 * ld, ld, g.end - k0);
+        q.cols(sV);
+        auto fetch = [&](int j) {
+            const int q0 = (tile.j0 + j) * BLK;
+            q.load(base + q0 * ld, ld, g.end - q0);
+            o.load(dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
+        };
+        fetch(0);
         for (int j = 0; j < tile.n; j++) {
             const int q0 = (tile.j0 + j) * BLK;
             __syncthreads();
-            load_tile<D>(sQ, base + q0 * ld, ld, g.end - q0);
-            load_tile<D>(sO, dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
-            if (threadIdx.x < BLK) {
-                const int q = q0 + threadIdx.x;
-                s_L[threadIdx.x] = q < g.end ? lse[bh + q] * LOG2E : 0.0f;
-                s_D[threadIdx.x] = q < g.end ? Dlt[bh + q] : 0.0f;
-            }
+            q.cols(sQ);
+            q.rows(sX);
+            o.cols(sO);
+            o.rows(sY);
             __syncthreads();
-            float s[4][4], dp[4][4];
+            if (j + 1 < tile.n) fetch(j + 1);
+            float L[4], Dr[4];  // of the thread's four queries
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const int i = q0 + 4 * tx + c;
+                L[c] = i < g.end ? lse[bh + i] * LOG2E : 0.0f;
+                Dr[c] = i < g.end ? Dlt[bh + i] : 0.0f;
+            }
+            Acc s, dp;
             product<D>(sK, sQ, tx, ty, s);
             product<D>(sV, sO, tx, ty, dp);
-            const bool masked = tile.masked(q0);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int k = k0 + ty + 16 * i;
-                const unsigned long long seen = masked ? g.queries(k, kend[i], q0) : k < g.end ? ~0ull : 0ull;
+            for (int r = 0; r < 8; r++)
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                    const int q = tx + 16 * c;
-                    const bool on = seen >> q & 1;
-                    const float p = on ? exp2f(fmaf(s[i][c], sl2, -s_L[q])) : 0.0f;
-                    sP[(ty + 16 * i) * PS + q] = p;
-                    sS[(ty + 16 * i) * PS + q] = on ? p * (dp[i][c] - s_D[q]) : 0.0f;
+                    of(s, r, c) = ex2(fmaf(of(s, r, c), sl2, -L[c]));
+                    of(dp, r, c) = of(s, r, c) * (of(dp, r, c) - Dr[c]);
+                }
+            if (tile.masked(q0)) {
+#pragma unroll
+                for (int r = 0; r < 8; r++) {
+                    const int k = k0 + 8 * ty + r;
+                    const uint32_t seen = k < g.end ? (uint32_t)(g.queries(k, g.end_of(k), q0) >> (4 * tx)) : 0u;
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        if (!(seen >> c & 1u)) of(s, r, c) = of(dp, r, c) = 0.0f;
                 }
             }
-            __syncwarp();
-            accumulate<D>(sP, sO, tx, ty, dv);
-            accumulate<D>(sS, sQ, tx, ty, dk);
+            put_product(sP, s, tx, ty);
+            accumulate<D>(sP, sY, tx, ty, dv);
+            put_product(sP, dp, tx, ty);
+            accumulate<D>(sP, sX, tx, ty, dk);
         }
     }
-    float* ob = dqkv + row0 * ld + at.h * D + tx * E;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int k = k0 + ty + 16 * i;
+    for (int r = 0; r < 8; r++) {
+        const int k = k0 + 8 * ty + r;
         if (k >= a.T) continue;
-        store_row(ob + (long long)k * ld + a.C, dk[i], k < g.end ? scale : 0.0f);
-        store_row(ob + (long long)k * ld + 2 * a.C, dv[i], k < g.end ? 1.0f : 0.0f);
+        float* d = dqkv + (row0 + k) * ld + at.h * D + tx * E;
+        store_row(d + a.C, dk, r, scale, k < g.end);
+        store_row(d + 2 * a.C, dv, r, 1.0f, k < g.end);
     }
 }
 
@@ -374,12 +425,14 @@ template <typename K> bool allow(PerDevice& done, K kern, size_t smem) {
     });
 }
 
+// `tiles` tiles of 64 rows and one product
+template <int D> constexpr size_t smem_of(int tiles) { return (size_t)(tiles * BLK * D + BLK * PS) * sizeof(float); }
+
 template <int D> bool fwd(const Launch& L, const float* qkv, float* y, float* lse, const GroupArgs& a, int ctas) {
     static PerDevice done;
-    constexpr size_t smem = (3 * tile_floats<D>() + BLK * PS) * 4;
-    if (!allow(done, k_group_fwd<D>, smem)) return false;
+    if (!allow(done, k_group_fwd<D>, smem_of<D>(3))) return false;
     L.count();
-    launch_k(L, k_group_fwd<D>, dim3(ctas), dim3(NT), smem, qkv, y, lse, a);
+    launch_k(L, k_group_fwd<D>, dim3(ctas), dim3(NT), smem_of<D>(3), qkv, y, lse, a);
     return true;
 }
 
@@ -387,19 +440,19 @@ template <int D>
 bool bwd(const Launch& L, const float* qkv, const float* y, const float* lse, const float* dy, float* dqkv, float* Dlt,
          const GroupArgs& a, int ctas) {
     static PerDevice done_q, done_k;
-    constexpr size_t sq = (4 * tile_floats<D>() + BLK * PS) * 4, sk = (4 * tile_floats<D>() + 2 * BLK * PS) * 4;
-    if (!allow(done_q, k_group_dq<D>, sq) || !allow(done_k, k_group_dkdv<D>, sk)) return false;
+    if (!allow(done_q, k_group_dq<D>, smem_of<D>(5)) || !allow(done_k, k_group_dkdv<D>, smem_of<D>(6))) return false;
     L.count();
-    launch_k(L, k_group_dq<D>, dim3(ctas), dim3(NT), sq, qkv, y, lse, dy, dqkv, Dlt, a);
+    launch_k(L, k_group_dq<D>, dim3(ctas), dim3(NT), smem_of<D>(5), qkv, y, lse, dy, dqkv, Dlt, a);
     L.count();
-    launch_k(L, k_group_dkdv<D>, dim3(ctas), dim3(NT), sk, qkv, lse, dy, dqkv, (const float*)Dlt, a);
+    launch_k(L, k_group_dkdv<D>, dim3(ctas), dim3(NT), smem_of<D>(6), qkv, lse, dy, dqkv, (const float*)Dlt, a);
     return true;
 }
 
-GroupArgs args_of(const Launch& L, const int32_t* starts, int T, int C, int H, int K) {
+GroupArgs args_of(const Launch& L, const int32_t* starts, int B, int T, int C, int H, int K) {
     GroupArgs a{};
     a.starts = starts; a.T = T; a.C = C; a.H = H; a.K = K;
     a.tiles = (T + BLK - 1) / BLK;
+    a.pairs = B * H;
     a.flags = L.flags;
     return a;
 }
@@ -415,7 +468,7 @@ bool launch_group_attention_fwd(const Launch& L, bool bf16, const void* qkv, con
         launch_group_fwd_mma(L, qkv, starts, y, lse, B, T, C, H, K);
         return true;
     }
-    const GroupArgs a = args_of(L, starts, T, C, H, K);
+    const GroupArgs a = args_of(L, starts, B, T, C, H, K);
     const int ctas = a.tiles * B * H;
     const auto *q = (const float*)qkv;
     auto* o = (float*)y;
@@ -437,7 +490,7 @@ bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, con
     if (bf16) {
         launch_group_bwd_mma(L, qkv, starts, y, lse, dy, dqkv, B, T, C, H, K, scratch);
     } else {
-        const GroupArgs a = args_of(L, starts, T, C, H, K);
+        const GroupArgs a = args_of(L, starts, B, T, C, H, K);
         const int ctas = a.tiles * B * H;
         auto run = [&](auto f) {
             return f(L, (const float*)qkv, (const float*)y, lse, (const float*)dy, (float*)dqkv, scratch, a, ctas);

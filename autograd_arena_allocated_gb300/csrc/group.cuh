@@ -93,5 +93,21 @@ struct KeyTile {
     __device__ __forceinline__ bool masked(int q0) const { return !(q0 >= last && q0 + BLK <= min_end); }
 };
 
+// CTA -> (tile, head, sequence) in a grid of one dimension: bands of 64 (sequence,
+// head) pairs, whose keys L2 holds together, and in a band every pair's tile with
+// the most work first (the last for queries, the first for keys), so that short
+// tiles fill the band's end.
+struct Place {
+    int tile, h, b;
+    __device__ __forceinline__ Place(int tiles, int pairs, int H, bool last_first) {
+        constexpr int BAND = 64;
+        const int band = blockIdx.x / (tiles * BAND), width = min(BAND, pairs - band * BAND);
+        const int i = blockIdx.x - band * tiles * BAND, t = i / width, pair = band * BAND + i % width;
+        tile = last_first ? tiles - 1 - t : t;
+        b = pair / H;
+        h = pair % H;
+    }
+};
+
 }  // namespace group
 }  // namespace tt
