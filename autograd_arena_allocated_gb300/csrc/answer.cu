@@ -2,7 +2,8 @@
 //
 //   k_answer        rows of more than 256 granules: a label's log probability, or
 //                   the clipped policy loss and its gradient; a CTA a row
-//   k_answer_short  the same for shorter rows, a warp a row, in registers
+//   k_answer_short  the same for shorter rows, a warp or a part of one a row, in
+//                   registers
 //   k_pairs         the loss of pairs of answers from their labels' log
 //                   probabilities, and each row's coefficient
 //   k_answer_grad   coefficient times (onehot - softmax)
@@ -26,6 +27,12 @@
 //
 // Statistics, losses and coefficients are fp32, sums over an answer 64 bits.
 // Rows without a label are not read: a loss of 0, and a gradient of zeros.
+//
+// All but the shortest rows are bound by memory.  32768 rows of 50257 in bf16, the
+// lm head's logits, 54% of them labelled (rates by the bytes that have to move):
+// log probabilities 267 us, 6.6 TB/s; the policy step 789 us, 6.2 TB/s, reads and
+// writes in turn; the preference step 1023 us, of which the second reading of the
+// logits is some 260, 6.7 TB/s with it counted.
 #include "row_view.cuh"
 
 namespace tt {
@@ -398,11 +405,14 @@ __global__ void __launch_bounds__(2 * PAIR_THREADS) k_pairs(const PairArgs a) {
         }
         if (a.seq_logp && lane < 2 * WARPS && lane % WARPS == 0) a.seq_logp[2 * pair + lane / WARPS] = (float)total;
         const float inv = a.mean && n > 1 ? 1.0f / (float)n : 1.0f;
+        if (a.mean && n > 1) {  // a step of Newton's: 1 / n in 64 bits without their division
+            const double x = inv;
+            score *= x * (2.0 - n * x);
+        }
         const double other = __shfl_sync(0xffffffffu, score, WARPS);
         const float inv1 = __shfl_sync(0xffffffffu, inv, WARPS);
         if (lane == 0) {
-            const float d = a.mean ? (float)score * inv - (float)other * inv1 : (float)(score - other);
-            const float v = fmaf(a.beta, d, -a.gamma), e = a.smooth;
+            const float v = fmaf(a.beta, (float)(score - other), -a.gamma), e = a.smooth;
             const float loss = (1.0f - e) * softplus(-v) + (e > 0.0f ? e * softplus(v) : 0.0f);
             const float dv = e / (1.0f + expf(-v)) - (1.0f - e) / (1.0f + expf(v));
             const float k = dv * a.beta * a.k * (a.scale_dev ? *a.scale_dev : 1.0f);
@@ -466,10 +476,11 @@ int row_threads(const Launch& L, int G, long long M) {
 }
 
 // With the gradient (and without it, so that the loss has the same bits) the rows
-// in flight, which are read a second time, also have to stay in L2: below 92 MB of them where every SM has 1024 threads.  In bf16,
-// 32768 rows of 50257 take 848 us by 256 threads, 893 by 128, 982 by warps, 992 by
-// 512; 4000 of 150000 339 by 512, 370 by 256 or 1024; 20000 of 5000 62 by warps or
-// 64 threads, 78 by 128.
+// in flight, which are read a second time, also have to stay in L2: below 92 MB of
+// them where every SM has 1024 threads.  In bf16, 32768 rows of 50257 take 848 us by
+// 256 threads, 893 by 128, 982 by warps, 992 by 512 (789 by 256 once the rows' other
+// inputs were loaded with the label); 4000 of 150000 339 by 512, 370 by 256 or 1024;
+// 20000 of 5000 62 by warps or 64 threads, 78 by 128.
 int policy_threads(const Launch& L, int G, long long M) {
     int N = row_threads(L, G, M);
     while (N < AN_THREADS && L.num_sms * 1024LL / N * G * 16 > 92000000LL) N *= 2;

@@ -9,9 +9,9 @@
 //                 dK += dS^T Q (a prompt's keys: every answer's queries, in order)
 //
 // All in fp32 FMAs, two rows an instruction.  A thread of the 8 x 16 owns rows 8 ty
-// .. + 7 and columns 4 tx .. + 3 of a 64 x 64 product, and the same rows and D / 16
-// columns of a 64 x D one: 32 multiply-adds take three 16-byte loads from shared
-// memory.  The tiles that a product sums over D lie transposed.  The next block is
+// .. + 7 (heads of 16: of 16 x 16, 4 rows) and columns 4 tx .. + 3 of a 64 x 64
+// product, and the same rows and D / 16 columns of a 64 x D one: 32 multiply-adds
+// take three 16-byte loads from shared memory.  The tiles that a product sums over D lie transposed.  The next block is
 // fetched into registers while the products run.  What bounds it is the issue of
 // instructions, half of them FMAs: 8 groups of 1000 positions, 12 heads of 64, 374
 // us forward and 1013 backward, 27 and 25 TFLOP/s of some 74 (one group of 1976, 16
@@ -26,7 +26,12 @@ namespace {
 using group::BLK;
 using group::Group;
 
-constexpr int NT = 128;
+// Rows of a product that a thread has, and the threads of a CTA.  Heads of 16 have so
+// little to do a block that a thread's own chain of instructions counts: 4 rows and
+// 256 threads, one group of 7900 positions, 4 heads: 301 us forward and 1008 backward
+// (8 rows and 128 threads 348 and 1016), 4 groups of 40, 4 heads: 5.6 (7.1).
+template <int D> constexpr int R_OF = D == 16 ? 4 : 8;
+template <int D> constexpr int NT_OF = 16 * BLK / R_OF<D>;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // places in the tiles, in floats: [64][D] by rows, [D][64] transposed, and a 64 x 64
@@ -44,67 +49,74 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// a thread's part of 64 rows of D floats: two neighbouring threads have a row
+// a thread's part of 64 rows of D floats: two (four) neighbouring threads have a row
 template <int D> struct Piece {
-    float4 v[D / 8];
+    static constexpr int TPR = NT_OF<D> / BLK, N = D / 4 / TPR;
+    float4 v[N];
+    static __device__ __forceinline__ int row() { return threadIdx.x / TPR; }
+    static __device__ __forceinline__ int col(int i) { return 4 * (threadIdx.x % TPR + TPR * i); }
     // rows of g, ld apart; those from `valid` on are zeros
     __device__ __forceinline__ void load(const float* g, long long ld, int valid) {
-        const int r = threadIdx.x >> 1;
 #pragma unroll
-        for (int i = 0; i < D / 8; i++)
-            v[i] = r < valid ? *reinterpret_cast<const float4*>(g + r * ld + 4 * ((threadIdx.x & 1) + 2 * i))
-                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = 0; i < N; i++)
+            v[i] = row() < valid ? *reinterpret_cast<const float4*>(g + row() * ld + col(i)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     __device__ __forceinline__ void rows(float* s) const {
-        const int r = threadIdx.x >> 1;
 #pragma unroll
-        for (int i = 0; i < D / 8; i++) *reinterpret_cast<float4*>(s + at_row<D>(r, 4 * ((threadIdx.x & 1) + 2 * i))) = v[i];
+        for (int i = 0; i < N; i++) *reinterpret_cast<float4*>(s + at_row<D>(row(), col(i))) = v[i];
     }
     __device__ __forceinline__ void cols(float* s) const {
-        const int r = threadIdx.x >> 1;
 #pragma unroll
-        for (int i = 0; i < D / 8; i++) {
-            const int d = 4 * ((threadIdx.x & 1) + 2 * i);
-            s[at_col(d, r)] = v[i].x;
-            s[at_col(d + 1, r)] = v[i].y;
-            s[at_col(d + 2, r)] = v[i].z;
-            s[at_col(d + 3, r)] = v[i].w;
+        for (int i = 0; i < N; i++) {
+            s[at_col(col(i), row())] = v[i].x;
+            s[at_col(col(i) + 1, row())] = v[i].y;
+            s[at_col(col(i) + 2, row())] = v[i].z;
+            s[at_col(col(i) + 3, row())] = v[i].w;
         }
     }
 };
 
-// acc[i][j]: rows 8 ty + 2 i, + 1 of column 4 tx + j
-using Acc = float2[4][4];
+// acc[i][j]: rows R ty + 2 i, + 1 of column 4 tx + j
+template <int D> using Acc = float2[R_OF<D> / 2][4];
+
+// a thread's R rows of column c of a transposed tile, as pairs
+template <int R> __device__ __forceinline__ void row_pairs(const float* p, float2 (&a)[R / 2]) {
+#pragma unroll
+    for (int i = 0; i < R / 4; i++) {
+        const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+        a[2 * i] = make_float2(v.x, v.y);
+        a[2 * i + 1] = make_float2(v.z, v.w);
+    }
+}
 
 // sum over d of A[row][d] B[col][d], both tiles transposed
-template <int D> __device__ __forceinline__ void product(const float* A, const float* B, int tx, int ty, Acc& s) {
+template <int D> __device__ __forceinline__ void product(const float* A, const float* B, int tx, int ty, Acc<D>& s) {
+    constexpr int R = R_OF<D>;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < R / 2; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) s[i][j] = make_float2(0.0f, 0.0f);
 #pragma unroll 8
     for (int d = 0; d < D; d++) {
-        const float4 a0 = *reinterpret_cast<const float4*>(A + at_col(d, 8 * ty));
-        const float4 a1 = *reinterpret_cast<const float4*>(A + at_col(d, 8 * ty + 4));
+        float2 a[R / 2];
+        row_pairs<R>(A + at_col(d, R * ty), a);
         const float4 b = *reinterpret_cast<const float4*>(B + at_col(d, 4 * tx));
-        const float2 a[4] = {make_float2(a0.x, a0.y), make_float2(a0.z, a0.w), make_float2(a1.x, a1.y), make_float2(a1.z, a1.w)};
         const float c[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < R / 2; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) s[i][j] = __ffma2_rn(a[i], make_float2(c[j], c[j]), s[i][j]);
     }
 }
 
-// o[i][e] += sum over k of P[k][rows 8 ty + 2 i, + 1] X[k][tx E + e], E = D / 16
+// o[i][e] += sum over k of P[k][rows R ty + 2 i, + 1] X[k][tx E + e], E = D / 16
 template <int D>
-__device__ __forceinline__ void accumulate(const float* P, const float* X, int tx, int ty, float2 (&o)[4][D / 16]) {
-    constexpr int E = D / 16;
+__device__ __forceinline__ void accumulate(const float* P, const float* X, int tx, int ty, float2 (&o)[R_OF<D> / 2][D / 16]) {
+    constexpr int E = D / 16, R = R_OF<D>;
 #pragma unroll 8
     for (int k = 0; k < BLK; k++) {
-        const float4 a0 = *reinterpret_cast<const float4*>(P + at_prod(k, 8 * ty));
-        const float4 a1 = *reinterpret_cast<const float4*>(P + at_prod(k, 8 * ty + 4));
-        const float2 a[4] = {make_float2(a0.x, a0.y), make_float2(a0.z, a0.w), make_float2(a1.x, a1.y), make_float2(a1.z, a1.w)};
+        float2 a[R / 2];
+        row_pairs<R>(P + at_prod(k, R * ty), a);
         const float* x = X + at_row<D>(k, tx * E);
         float c[4];
         if (E == 4) {
@@ -117,25 +129,25 @@ __device__ __forceinline__ void accumulate(const float* P, const float* X, int t
             c[0] = *x;
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < R / 2; i++)
 #pragma unroll
             for (int e = 0; e < E; e++) o[i][e] = __ffma2_rn(a[i], make_float2(c[e], c[e]), o[i][e]);
     }
 }
 
-// row r = 0 .. 7 of a thread's
-__device__ __forceinline__ float& of(Acc& s, int r, int j) { return r & 1 ? s[r >> 1][j].y : s[r >> 1][j].x; }
+// row r of a thread's
+template <int N> __device__ __forceinline__ float& of(float2 (&s)[N][4], int r, int j) { return r & 1 ? s[r >> 1][j].y : s[r >> 1][j].x; }
 
 // a product goes to shared memory for accumulate; its 16 lanes of a row group alone
 // read it
-__device__ __forceinline__ void put_product(float* P, const Acc& s, int tx, int ty) {
+template <int N> __device__ __forceinline__ void put_product(float* P, const float2 (&s)[N][4], int tx, int ty) {
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        *reinterpret_cast<float4*>(P + at_prod(4 * tx + j, 8 * ty)) = make_float4(s[0][j].x, s[0][j].y, s[1][j].x, s[1][j].y);
-        *reinterpret_cast<float4*>(P + at_prod(4 * tx + j, 8 * ty + 4)) =
-            make_float4(s[2][j].x, s[2][j].y, s[3][j].x, s[3][j].y);
-    }
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            *reinterpret_cast<float4*>(P + at_prod(4 * tx + j, 2 * N * ty + 2 * i)) =
+                make_float4(s[i][j].x, s[i][j].y, s[i + 1][j].x, s[i + 1][j].y);
     __syncwarp();
 }
 
@@ -145,15 +157,15 @@ struct GroupArgs {
     int* flags;
 };
 
-template <int E> __device__ __forceinline__ void zero(float2 (&o)[4][E]) {
+template <int N, int E> __device__ __forceinline__ void zero(float2 (&o)[N][E]) {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < N; i++)
 #pragma unroll
         for (int e = 0; e < E; e++) o[i][e] = make_float2(0.0f, 0.0f);
 }
 
 // row r of a thread's E columns, times scale; zeros where it is padding
-template <int E> __device__ __forceinline__ void store_row(float* d, const float2 (&o)[4][E], int r, float scale, bool real) {
+template <int N, int E> __device__ __forceinline__ void store_row(float* d, const float2 (&o)[N][E], int r, float scale, bool real) {
 #pragma unroll
     for (int e = 0; e < E; e++) d[e] = real ? (r & 1 ? o[r >> 1][e].y : o[r >> 1][e].x) * scale : 0.0f;
 }
@@ -169,22 +181,22 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-template <int D> __global__ void __launch_bounds__(NT, 3) k_group_fwd(const float* qkv, float* y, float* lse, const GroupArgs a) {
+template <int D> __global__ void __launch_bounds__(NT_OF<D>, D == 16 ? 2 : 3) k_group_fwd(const float* qkv, float* y, float* lse, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sK = sQ + BLK * D, *sV = sK + BLK * D, *sP = sV + BLK * D;
-    constexpr int E = D / 16;
+    constexpr int E = D / 16, R = R_OF<D>;
     const group::Place at(a.tiles, a.pairs, a.H, true);
     const Group g(a.starts, at.b, a.K, a.T);
     const int q0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T;
     const float* base = qkv + row0 * ld + at.h * D;
-    if (q0 == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
-    float2 o[4][E];
+    if (q0 == 0 && at.h == 0) g.check(threadIdx.x, NT_OF<D>, a.T, a.flags);
+    float2 o[R / 2][E];
     zero(o);
-    float m[8], l[8];
+    float m[R], l[R];
 #pragma unroll
-    for (int r = 0; r < 8; r++) {
+    for (int r = 0; r < R; r++) {
         m[r] = -3e38f;  // finite: a row may see nothing of a block
         l[r] = 0.0f;
     }
@@ -207,12 +219,12 @@ template <int D> __global__ void __launch_bounds__(NT, 3) k_group_fwd(const floa
             v.rows(sV);
             __syncthreads();
             if (j + 1 < tile.n) fetch(j + 1);
-            Acc s;
+            Acc<D> s;
             product<D>(sQ, sK, tx, ty, s);
             if (tile.masked(k0)) {
 #pragma unroll
-                for (int r = 0; r < 8; r++) {
-                    const int q = q0 + 8 * ty + r;
+                for (int r = 0; r < R; r++) {
+                    const int q = q0 + R * ty + r;
                     const uint32_t seen = (uint32_t)(g.keys(q, g.start_of(q), k0) >> (4 * tx));
 #pragma unroll
                     for (int c = 0; c < 4; c++)
@@ -220,7 +232,7 @@ template <int D> __global__ void __launch_bounds__(NT, 3) k_group_fwd(const floa
                 }
             }
 #pragma unroll
-            for (int r = 0; r < 8; r++) {
+            for (int r = 0; r < R; r++) {
                 // m is the largest score, before the scale
                 const float mx = row_max(fmaxf(fmaxf(of(s, r, 0), of(s, r, 1)), fmaxf(of(s, r, 2), of(s, r, 3))));
                 const float mn = fmaxf(m[r], mx), corr = ex2((m[r] - mn) * sl2);
@@ -243,8 +255,8 @@ template <int D> __global__ void __launch_bounds__(NT, 3) k_group_fwd(const floa
         }
     }
 #pragma unroll
-    for (int r = 0; r < 8; r++) {
-        const int q = q0 + 8 * ty + r;
+    for (int r = 0; r < R; r++) {
+        const int q = q0 + R * ty + r;
         const float sum = row_sum(l[r]);
         if (q >= a.T) continue;
         store_row(y + (row0 + q) * a.C + at.h * D + tx * E, o, r, 1.0f / sum, q < g.end);
@@ -253,19 +265,19 @@ template <int D> __global__ void __launch_bounds__(NT, 3) k_group_fwd(const floa
 }
 
 template <int D>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT_OF<D>, D == 16 ? 1 : 2)
 k_group_dq(const float* qkv, const float* y, const float* lse, const float* dy, float* dqkv, float* Dlt, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sO = sQ + BLK * D, *sK = sO + BLK * D, *sV = sK + BLK * D, *sX = sV + BLK * D, *sS = sX + BLK * D;
-    constexpr int E = D / 16;
+    constexpr int E = D / 16, R = R_OF<D>;
     const group::Place at(a.tiles, a.pairs, a.H, true);
     const Group g(a.starts, at.b, a.K, a.T);
     const int q0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T, bh = ((long long)at.b * a.H + at.h) * a.T;
     const float* base = qkv + row0 * ld + at.h * D;
-    if (q0 == 0 && at.h == 0) g.check(threadIdx.x, NT, a.T, a.flags);
-    float2 o[4][E];
+    if (q0 == 0 && at.h == 0) g.check(threadIdx.x, NT_OF<D>, a.T, a.flags);
+    float2 o[R / 2][E];
     zero(o);
     const float scale = rsqrtf((float)D);
     if (q0 < g.end) {
@@ -275,23 +287,24 @@ k_group_dq(const float* qkv, const float* y, const float* lse, const float* dy, 
         Piece<D> k, v;
         k.load(base + q0 * ld, ld, g.end - q0);
         k.cols(sQ);
-        // D = rowsum(dO o O): the two threads of a row add their halves
+        // D = rowsum(dO o O): the threads of a row add their parts
         k.load(dy + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
         k.cols(sO);
         v.load(y + (row0 + q0) * a.C + at.h * D, a.C, g.end - q0);
         float d = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 8; i++)
+        for (int i = 0; i < Piece<D>::N; i++)
             d = fmaf(k.v[i].x, v.v[i].x, fmaf(k.v[i].y, v.v[i].y, fmaf(k.v[i].z, v.v[i].z, fmaf(k.v[i].w, v.v[i].w, d))));
-        d += __shfl_xor_sync(0xffffffffu, d, 1);
-        if ((threadIdx.x & 1) == 0) {
-            const int q = q0 + (threadIdx.x >> 1);
-            s_D[threadIdx.x >> 1] = d;
-            if (q < g.end) Dlt[bh + q] = d;
-        }
-        float L[8];
 #pragma unroll
-        for (int r = 0; r < 8; r++) L[r] = q0 + 8 * ty + r < g.end ? lse[bh + q0 + 8 * ty + r] * LOG2E : 0.0f;
+        for (int x = 1; x < Piece<D>::TPR; x *= 2) d += __shfl_xor_sync(0xffffffffu, d, x);
+        if (threadIdx.x % Piece<D>::TPR == 0) {
+            const int r = Piece<D>::row();
+            s_D[r] = d;
+            if (q0 + r < g.end) Dlt[bh + q0 + r] = d;
+        }
+        float L[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) L[r] = q0 + R * ty + r < g.end ? lse[bh + q0 + R * ty + r] * LOG2E : 0.0f;
         auto fetch = [&](int j) {
             const int k0 = tile.block(j) * BLK;
             k.load(base + a.C + k0 * ld, ld, g.end - k0);
@@ -306,19 +319,19 @@ k_group_dq(const float* qkv, const float* y, const float* lse, const float* dy, 
             v.cols(sV);
             __syncthreads();
             if (j + 1 < tile.n) fetch(j + 1);
-            Acc s, dp;
+            Acc<D> s, dp;
             product<D>(sQ, sK, tx, ty, s);
             product<D>(sO, sV, tx, ty, dp);
 #pragma unroll
-            for (int r = 0; r < 8; r++) {
-                const float Dr = s_D[8 * ty + r];
+            for (int r = 0; r < R; r++) {
+                const float Dr = s_D[R * ty + r];
 #pragma unroll
                 for (int c = 0; c < 4; c++) of(s, r, c) = ex2(fmaf(of(s, r, c), sl2, -L[r])) * (of(dp, r, c) - Dr);
             }
             if (tile.masked(k0)) {
 #pragma unroll
-                for (int r = 0; r < 8; r++) {
-                    const int q = q0 + 8 * ty + r;
+                for (int r = 0; r < R; r++) {
+                    const int q = q0 + R * ty + r;
                     const uint32_t seen = (uint32_t)(g.keys(q, g.start_of(q), k0) >> (4 * tx));
 #pragma unroll
                     for (int c = 0; c < 4; c++)
@@ -330,27 +343,27 @@ k_group_dq(const float* qkv, const float* y, const float* lse, const float* dy, 
         }
     }
 #pragma unroll
-    for (int r = 0; r < 8; r++) {
-        const int q = q0 + 8 * ty + r;
+    for (int r = 0; r < R; r++) {
+        const int q = q0 + R * ty + r;
         if (q < a.T) store_row(dqkv + (row0 + q) * ld + at.h * D + tx * E, o, r, scale, q < g.end);
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT_OF<D>, D == 16 ? 1 : 2)
 k_group_dkdv(const float* qkv, const float* lse, const float* dy, float* dqkv, const float* Dlt, const GroupArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float sm[];
     float *sK = sm, *sV = sK + BLK * D, *sQ = sV + BLK * D, *sO = sQ + BLK * D, *sX = sO + BLK * D, *sY = sX + BLK * D,
           *sP = sY + BLK * D;
-    constexpr int E = D / 16;
+    constexpr int E = D / 16, R = R_OF<D>;
     const group::Place at(a.tiles, a.pairs, a.H, false);
     const Group g(a.starts, at.b, a.K, a.T);
     const int k0 = at.tile * BLK, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const long long ld = 3LL * a.C, row0 = (long long)at.b * a.T, bh = ((long long)at.b * a.H + at.h) * a.T;
     const float* base = qkv + row0 * ld + at.h * D;
     const float scale = rsqrtf((float)D);
-    float2 dk[4][E], dv[4][E];
+    float2 dk[R / 2][E], dv[R / 2][E];
     zero(dk);
     zero(dv);
     if (k0 < g.end) {
@@ -383,11 +396,11 @@ k_group_dkdv(const float* qkv, const float* lse, const float* dy, float* dqkv, c
                 L[c] = i < g.end ? lse[bh + i] * LOG2E : 0.0f;
                 Dr[c] = i < g.end ? Dlt[bh + i] : 0.0f;
             }
-            Acc s, dp;
+            Acc<D> s, dp;
             product<D>(sK, sQ, tx, ty, s);
             product<D>(sV, sO, tx, ty, dp);
 #pragma unroll
-            for (int r = 0; r < 8; r++)
+            for (int r = 0; r < R; r++)
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     of(s, r, c) = ex2(fmaf(of(s, r, c), sl2, -L[c]));
@@ -395,8 +408,8 @@ k_group_dkdv(const float* qkv, const float* lse, const float* dy, float* dqkv, c
                 }
             if (tile.masked(q0)) {
 #pragma unroll
-                for (int r = 0; r < 8; r++) {
-                    const int k = k0 + 8 * ty + r;
+                for (int r = 0; r < R; r++) {
+                    const int k = k0 + R * ty + r;
                     const uint32_t seen = k < g.end ? (uint32_t)(g.queries(k, g.end_of(k), q0) >> (4 * tx)) : 0u;
 #pragma unroll
                     for (int c = 0; c < 4; c++)
@@ -410,8 +423,8 @@ k_group_dkdv(const float* qkv, const float* lse, const float* dy, float* dqkv, c
         }
     }
 #pragma unroll
-    for (int r = 0; r < 8; r++) {
-        const int k = k0 + 8 * ty + r;
+    for (int r = 0; r < R; r++) {
+        const int k = k0 + R * ty + r;
         if (k >= a.T) continue;
         float* d = dqkv + (row0 + k) * ld + at.h * D + tx * E;
         store_row(d + a.C, dk, r, scale, k < g.end);
@@ -432,7 +445,7 @@ template <int D> bool fwd(const Launch& L, const float* qkv, float* y, float* ls
     static PerDevice done;
     if (!allow(done, k_group_fwd<D>, smem_of<D>(3))) return false;
     L.count();
-    launch_k(L, k_group_fwd<D>, dim3(ctas), dim3(NT), smem_of<D>(3), qkv, y, lse, a);
+    launch_k(L, k_group_fwd<D>, dim3(ctas), dim3(NT_OF<D>), smem_of<D>(3), qkv, y, lse, a);
     return true;
 }
 
@@ -442,9 +455,9 @@ bool bwd(const Launch& L, const float* qkv, const float* y, const float* lse, co
     static PerDevice done_q, done_k;
     if (!allow(done_q, k_group_dq<D>, smem_of<D>(5)) || !allow(done_k, k_group_dkdv<D>, smem_of<D>(6))) return false;
     L.count();
-    launch_k(L, k_group_dq<D>, dim3(ctas), dim3(NT), smem_of<D>(5), qkv, y, lse, dy, dqkv, Dlt, a);
+    launch_k(L, k_group_dq<D>, dim3(ctas), dim3(NT_OF<D>), smem_of<D>(5), qkv, y, lse, dy, dqkv, Dlt, a);
     L.count();
-    launch_k(L, k_group_dkdv<D>, dim3(ctas), dim3(NT), smem_of<D>(6), qkv, lse, dy, dqkv, (const float*)Dlt, a);
+    launch_k(L, k_group_dkdv<D>, dim3(ctas), dim3(NT_OF<D>), smem_of<D>(6), qkv, lse, dy, dqkv, (const float*)Dlt, a);
     return true;
 }
 
