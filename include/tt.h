@@ -183,7 +183,8 @@ tt_status tt_ctx_loss_device(const tt_ctx* ctx, const float** mean_loss,
                              const float** row_losses);
 
 /* Copy the last step's per-position losses (n <= B*T floats; after
- * tt_gpt2_step_preference n <= pairs) to dst, which may be host or device memory; synchronizes the context's stream. */
+ * tt_gpt2_step_preference n <= pairs) to dst, which may be host or device
+ * memory; synchronizes the context's stream. */
 tt_status tt_ctx_copy_row_losses(tt_ctx* ctx, float* dst, size_t n);
 
 /* ---------------------------------------------------------------- step variants

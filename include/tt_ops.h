@@ -215,7 +215,8 @@ tt_status tt_op_beam_reorder(tt_ctx* ctx, void* state, const int32_t* parents, i
  * its logits hold.  A target outside [-1, V) raises the bad token flag
  * (tt_ctx_sync: TT_ERR_ARG) and counts as -1.  Neither ld nor the pointers need
  * more than the element's alignment, 4 bytes for indices, log probabilities,
- * weights and losses (without it: TT_ERR_ARG).  All are deterministic and can be
+ * weights and losses (without it: TT_ERR_ARG).  No output overlaps an input or
+ * another output, but dlogits as said there.  All are deterministic and can be
  * recorded (tt_graph.h); a recorded call keeps its scratch until the reset.  The
  * context's device has to be the current one (else TT_ERR_STATE).  The pages
  * have no counterpart to these calls: they extend the fused cross entropy
@@ -280,7 +281,8 @@ tt_status tt_op_preference(tt_ctx* ctx, tt_dtype dtype, const void* logits, cons
  * with no prompt the answers are sequences of their own).  A position sees the
  * prompt up to itself and the positions of its own answer up to itself; qkv, y,
  * lse as in tt_op_attention_fwd.  Padded positions receive y = 0 and lse = 0,
- * and what qkv holds there reaches no other position.  A list that does not
+ * and what qkv holds there reaches no other position (a value that is not finite
+ * in any other position may reach all of its group).  A list that does not
  * ascend in [0, T] raises the bad token flag; what its sequence receives is
  * undefined.  Head dimensions 16, 32 and 64; C a multiple of 8, and qkv, y (and
  * dy, dqkv) on 16-byte boundaries; B T and B H (T + 63) / 64 within an int. */

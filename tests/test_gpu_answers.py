@@ -805,6 +805,71 @@ def test_group_attention_flags_bad_starts(ctx):
     ctx.reset()
 
 
+@pytest.mark.parametrize("dtype,C,H", [("bf16", 128, 2), ("fp16", 96, 3), ("bf16", 32, 2), ("fp32", 128, 2), ("fp32", 64, 2),
+                                       ("fp32", 32, 2)])
+def test_group_attention_of_many_answers(ctx, dtype, C, H):
+    """Hundreds of answers of a few tokens, many of them empty, past a prompt of several blocks and past none."""
+    g = gen(91)
+    many = lambda first, T: [first] + sorted(torch.randint(first, T + 1, (300,), generator=g, device=DEV).tolist())  # noqa: E731
+    check_group(ctx, dtype, [many(150, 640), many(0, 640), list(range(301)), [640] * 301], 640, C, H, seed=92)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 16), ("fp16", 32), ("bf16", 64), ("fp32", 16), ("fp32", 32), ("fp32", 64)])
+def test_group_attention_of_many_heads(ctx, dtype, D):
+    """More (sequence, head) pairs than a band of the grid holds, the last band with a few."""
+    B, H = 5, 14
+    check_group(ctx, dtype, [[20 + 20 * b, 100, 140 + b, 150] for b in range(B)], 151, H * D, H, seed=93)
+
+
+@pytest.mark.parametrize("dtype,D,spread", [("bf16", 16, 5.0), ("fp16", 32, 4.0), ("fp32", 16, 5.0), ("fp32", 32, 0.0)])
+def test_narrow_heads_of_sharp_and_flat_scores(ctx, dtype, D, spread):
+    check_group(ctx, dtype, [[100, 180, 290], [0, 150, 300]], 300, 2 * D, 2, seed=94, spread=spread)
+
+
+def test_narrow_heads_flag_bad_starts(ctx):
+    T = 100
+    for dtype, C, H in (("bf16", 48, 3), ("fp16", 64, 2), ("fp32", 64, 2), ("fp32", 64, 1)):
+        for s in ([-1, 50, 100], [10, 50, 101], [60, 50, 100], [2 ** 31 - 1, 5, -2 ** 31], [50, 100, 99]):
+            qkv, st = group_case(dtype, [[0, 50, 100], [0, 50, 100]], T, C, 95, pad=0.0)
+            st[1] = torch.tensor(s, dtype=torch.int32)
+            y, lse = run_group_fwd(ctx, dtype, qkv, st, T, C, H, sync=False)
+            with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+                ctx.sync()
+            run_group_bwd(ctx, dtype, qkv, st, y, lse, y, T, C, H, sync=False)
+            with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+                ctx.sync()
+            want, tol, _, _ = group_refs(dtype, qkv[:T], [[0, 50, 100]], C, H)
+            within(y[:T], want, tol + stored(want, dtype), "the other group")
+    ctx.reset()
+
+
+@pytest.mark.parametrize("dtype,C,H", [("bf16", 64, 1), ("fp16", 64, 2), ("fp32", 64, 1)])
+def test_groups_at_16_byte_boundaries(ctx, dtype, C, H):
+    """Every tensor 16 bytes past a longer boundary, its neighbours left as they are."""
+    T, starts = 90, [[20, 50, 85], [0, 45, 90]]
+    M, n = 2 * T, 16 // torch.empty(0, dtype=TYPES[dtype]).element_size()
+    qkv, st = group_case(dtype, starts, T, C, 96)
+    y0, l0, d0 = check_group(ctx, dtype, starts, T, C, H, seed=96)
+
+    def off(x, fill=7.0, n=n):
+        b = torch.full((x.numel() + 2 * n,), fill, dtype=x.dtype, device=DEV)
+        b[n:-n] = x.reshape(-1)
+        return b, b[n:-n].view(x.shape)
+
+    (_, q), (_, s) = off(qkv), off(st, 0, 1)
+    (yb, y), (lb, lse), (db, d) = off(torch.zeros_like(y0)), off(torch.zeros_like(l0), n=1), off(torch.zeros_like(d0))
+    ctx.reset()
+    ctx.group_attention_fwd(dtype, q, s, y, lse, 2, T, C, H, 2)
+    ctx.sync()
+    assert torch.equal(y, y0) and torch.equal(lse, l0)
+    dy = torch.randn(M, C, generator=gen(97), device=DEV).to(TYPES[dtype])
+    ctx.group_attention_bwd(dtype, q, s, y, lse, off(dy)[1], d, 2, T, C, H, 2)
+    ctx.sync()
+    assert torch.equal(d, d0)
+    for b, k in ((yb, n), (lb, 1), (db, n)):
+        assert (b[:k] == 7).all() and (b[-k:] == 7).all()
+
+
 def test_groups_past_32_bits(ctx):
     """More than 2^31 elements of qkv: the last group's values and gradients."""
     T, C, H, K = 8192, 1024, 16, 128
