@@ -46,6 +46,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace tt {
 namespace fa5 {
 
@@ -395,27 +397,31 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             // the sums in two independent packed chains)
             float2 rsa = make_float2(0.0f, 0.0f), rsb = make_float2(0.0f, 0.0f);
             const float2 sl2 = make_float2(SL2, SL2), nm = make_float2(-m, -m);
+            auto probabilities = [&](auto masked) {
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                const uint32_t(&w)[32] = c ? w1 : w0;
-                uint32_t pk[16];
+                for (int c = 0; c < 2; c++) {
+                    const uint32_t(&w)[32] = c ? w1 : w0;
+                    uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), sl2, nm);
-                    float2 p = make_float2(ex2(x.x), ex2(x.y));
-                    if (GRP && diag) {
-                        if (!((c ? seen1 : seen0) >> e & 1u)) p.x = 0.0f;
-                        if (!((c ? seen1 : seen0) >> (e + 1) & 1u)) p.y = 0.0f;
-                    } else if (diag) {
-                        if (32 * c + e > kq) p.x = 0.0f;
-                        if (32 * c + e + 1 > kq) p.y = 0.0f;
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), sl2, nm);
+                        float2 p = make_float2(ex2(x.x), ex2(x.y));
+                        if (GRP && masked.value) {
+                            if (!((c ? seen1 : seen0) >> e & 1u)) p.x = 0.0f;
+                            if (!((c ? seen1 : seen0) >> (e + 1) & 1u)) p.y = 0.0f;
+                        } else if (masked.value) {
+                            if (32 * c + e > kq) p.x = 0.0f;
+                            if (32 * c + e + 1 > kq) p.y = 0.0f;
+                        }
+                        if (e & 2) rsb = __fadd2_rn(rsb, p);
+                        else rsa = __fadd2_rn(rsa, p);
+                        pk[e >> 1] = pack2<F16>(p.x, p.y);
                     }
-                    if (e & 2) rsb = __fadd2_rn(rsb, p);
-                    else rsa = __fadd2_rn(rsa, p);
-                    pk[e >> 1] = pack2<F16>(p.x, p.y);
+                    store_row32(pbuf, r, 32 * c, pk);
                 }
-                store_row32(pbuf, r, 32 * c, pk);
-            }
+            };
+            if (diag) probabilities(std::true_type{});
+            else probabilities(std::false_type{});
             const float rs = (rsa.x + rsb.x) + (rsa.y + rsb.y);
             if (rescale) {
                 // O must hold P_{j-1} V_{j-1} before it is scaled
@@ -546,9 +552,10 @@ __device__ __forceinline__ void tile_colsum(float (&v)[32], float* cs, float* ds
 //
 // A tcgen05.mma costs its issuing thread tens of cycles, about twice the
 // tensor time of an N = 64 product, so the MMA thread is the critical
-// resource: the dQ MMAs of block j - 1 are issued after S_j and dP_j, while
-// the row threads work on block j, and dS is double-buffered so that block
-// j's dS never overwrites the operand of block j - 1's dQ MMAs.
+// resource: S_{j+1} and dP_{j+1} are issued once the row threads have block j's in
+// registers, and run while those work on it; dS is double-buffered so that block
+// j's dS never overwrites the operand of block j - 1's dQ MMAs (done when S_{j+1},
+// issued after them, is).
 constexpr int Q_Q = 0;
 constexpr int Q_O = Q_Q + T128;          // dO tile
 constexpr int Q_KST = 3;                 // K stages: K_j is read by S_j and by dQ_j
@@ -577,10 +584,11 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     uint64_t* v_full = bars + 7;    // [2]
     uint64_t* v_empty = bars + 9;   // [2]
     uint64_t* s_full = bars + 11;   // S_j, dP_j (and every earlier MMA) done
-    uint64_t* ds_full = bars + 12;  // block j's S, dP read and its dS written
+    uint64_t* ds_full = bars + 12;  // block j's dS written
     uint64_t* acc_full = bars + 13;
     uint64_t* drain = bars + 14;    // MMAs issued before an abort are done
-    uint32_t* tmem_holder = (uint32_t*)(bars + 15);
+    uint64_t* s_free = bars + 15;   // S_j and dP_j are in registers
+    uint32_t* tmem_holder = (uint32_t*)(bars + 16);
     volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
 
     const int bh = (int)(blockIdx.z * gridDim.x + blockIdx.x);
@@ -614,6 +622,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         }
         mbar_init(s_full, 1);
         mbar_init(ds_full, BW_ROWS / 32);
+        mbar_init(s_free, BW_ROWS / 32);
         mbar_init(acc_full, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -671,13 +680,14 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                                  (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(&k_empty[j % Q_KST]);
             };
-            for (int j = 0; j < nkv && ok; j++) {
+            // S_j and dP_j: two independent chains, interleaved
+            auto issue_s = [&](int j) {
                 const int ks = j % Q_KST, vs = j & 1;
-                if (!mbar_wait(&k_full[ks], (j / Q_KST) & 1, abort_flag, flags, 0x200 + 3, wl)) { ok = false; break; }
-                if (!mbar_wait(&v_full[vs], (j >> 1) & 1, abort_flag, flags, 0x200 + 11, wl)) { ok = false; break; }
+                if (!mbar_wait(&k_full[ks], (j / Q_KST) & 1, abort_flag, flags, 0x200 + 3, wl)) return false;
+                if (!mbar_wait(&v_full[vs], (j >> 1) & 1, abort_flag, flags, 0x200 + 11, wl)) return false;
+                if (j > 0 && !mbar_wait(s_free, (j - 1) & 1, abort_flag, flags, 0x200 + 4, wl)) return false;
                 tc_fence_after();
                 const uint32_t sk = smem_u32(sm + Q_K + ks * T64), sv = smem_u32(sm + Q_V + vs * T64);
-                // S_j and dP_j: two independent chains, interleaved
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
                     umma_bf16(tmem + Q_TS, sdesc(sq + 32 * k, 16, 1024), sdesc(sk + 32 * k, 16, 1024), ID, k > 0);
@@ -686,12 +696,17 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 issued = true;
                 umma_commit(s_full);
                 umma_commit(&v_empty[vs]);  // V_j is no longer needed
-                if (j > 0) issue_dq(j - 1);  // overlaps the row threads' work on block j
+                return true;
+            };
+            ok = ok && issue_s(0);
+            for (int j = 0; j < nkv && ok; j++) {
+                // the next block's scores while the row threads work on this one's
+                if (j + 1 < nkv && !issue_s(j + 1)) { ok = false; break; }
                 if (!mbar_wait(ds_full, j & 1, abort_flag, flags, 0x200 + 5, wl)) { ok = false; break; }
                 tc_fence_after();
+                issue_dq(j);
             }
             if (ok) {
-                issue_dq(nkv - 1);
                 umma_commit(acc_full);
             } else if (issued) {  // the MMAs already issued finish before tensor memory is freed
                 umma_commit(drain);
@@ -747,24 +762,30 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             const uint32_t seen = GRP && diag ? (uint32_t)(tile.keys(q, st0, kb) >> (32 * half)) : 0u;
             uint32_t sw[32], pw[32];
             tmem_ld32x2(tl + Q_TS + 32 * half, sw, tl + Q_TP + 32 * half, pw);
+            tc_fence_before();
+            warp_arrive(s_free, lane);  // the next block's scores may be computed
             // dS = P o (dP - D), packed bf16
             // (packed fp32x2: the same roundings as the scalar fma, sub and mul)
             uint32_t pk[16];
             const float2 sl2 = make_float2(SL2, SL2), nl = make_float2(-Lq, -Lq), nd = make_float2(-Dq, -Dq);
+            auto slopes = [&](auto masked) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sw[e]), __uint_as_float(sw[e + 1])), sl2, nl);
-                const float2 dd = __fadd2_rn(make_float2(__uint_as_float(pw[e]), __uint_as_float(pw[e + 1])), nd);
-                float2 d = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), dd);
-                if (GRP && diag) {
-                    if (!(seen >> e & 1u)) d.x = 0.0f;
-                    if (!(seen >> (e + 1) & 1u)) d.y = 0.0f;
-                } else if (diag) {
-                    if (e > kq) d.x = 0.0f;
-                    if (e + 1 > kq) d.y = 0.0f;
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(sw[e]), __uint_as_float(sw[e + 1])), sl2, nl);
+                    const float2 dd = __fadd2_rn(make_float2(__uint_as_float(pw[e]), __uint_as_float(pw[e + 1])), nd);
+                    float2 d = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), dd);
+                    if (GRP && masked.value) {
+                        if (!(seen >> e & 1u)) d.x = 0.0f;
+                        if (!(seen >> (e + 1) & 1u)) d.y = 0.0f;
+                    } else if (masked.value) {
+                        if (e > kq) d.x = 0.0f;
+                        if (e + 1 > kq) d.y = 0.0f;
+                    }
+                    pk[e >> 1] = pack2<F16>(d.x, d.y);
                 }
-                pk[e >> 1] = pack2<F16>(qv ? d.x : 0.0f, qv ? d.y : 0.0f);
-            }
+            };
+            if (diag) slopes(std::true_type{});
+            else slopes(std::false_type{});
             tmem_st16(tl + Q_TDS + 32 * (j & 1) + 16 * half, pk);
             tmem_st_wait();
             if (GRP && j == nkv - 1 && kb + BN > tile.end) {  // S_j is done, dS_j K_j is to come
@@ -804,7 +825,9 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 // after the diagonal: S^T = K Q_j^T and dP^T = V dO_j^T (K and V as A operands
 // from shared memory), then P^T and dS^T into tensor memory, and
 // dV += P^T dO_j, dK += dS^T Q_j (Q_j and dO_j read again as MN-major
-// operands) accumulate in tensor memory.
+// operands) accumulate in tensor memory.  P^T and dS^T are handed over one after the
+// other: dV's products and the next block's S^T run while the rows form dS^T, dK's
+// and the next dP^T while they take the next block's exponentials.
 constexpr int K_K = 0;
 constexpr int K_V = K_K + T128;
 constexpr int K_ST = 3;                  // Q / dO block stages
@@ -829,11 +852,13 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     uint64_t* kv_full = bars + 0;
     uint64_t* qo_full = bars + 1;   // [3]
     uint64_t* qo_empty = bars + 4;  // [3]
-    uint64_t* st_full = bars + 7;   // S^T_i, dP^T_i (and every earlier MMA) done
-    uint64_t* ps_full = bars + 8;   // P^T_i, dS^T_i written to tensor memory
-    uint64_t* acc_full = bars + 9;
-    uint64_t* drain = bars + 10;
-    uint32_t* tmem_holder = (uint32_t*)(bars + 11);
+    uint64_t* s_full = bars + 7;    // S^T_i (and every earlier MMA) done
+    uint64_t* dp_full = bars + 8;   // dP^T_i likewise
+    uint64_t* p_full = bars + 9;    // P^T_i written to tensor memory
+    uint64_t* ds_full = bars + 10;  // dS^T_i likewise
+    uint64_t* acc_full = bars + 11;
+    uint64_t* drain = bars + 12;
+    uint32_t* tmem_holder = (uint32_t*)(bars + 13);
     volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
 
     const int bh = (int)(blockIdx.z * gridDim.x + blockIdx.x);
@@ -859,8 +884,10 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mbar_init(&qo_full[i], 1);
             mbar_init(&qo_empty[i], 1);
         }
-        mbar_init(st_full, 1);
-        mbar_init(ps_full, BW_ROWS / 32);
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_full, BW_ROWS / 32);
+        mbar_init(ds_full, BW_ROWS / 32);
         mbar_init(acc_full, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -902,29 +929,45 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const uint32_t sk = smem_u32(sm + K_K), sv = smem_u32(sm + K_V);
             bool ok = mbar_wait(kv_full, 0, abort_flag, flags, 0x300 + 2, wl);
             bool issued = false;
-            for (int i = 0; i < nq && ok; i++) {
-                const int st = i % K_ST;
-                if (!mbar_wait(&qo_full[st], (i / K_ST) & 1, abort_flag, flags, 0x300 + 3, wl)) { ok = false; break; }
+            auto q_of = [&](int i) { return smem_u32(sm + K_Q + (i % K_ST) * T64); };
+            auto o_of = [&](int i) { return smem_u32(sm + K_O + (i % K_ST) * T64); };
+            auto issue_s = [&](int i) {  // overwrites P^T_{i-1}, read by MMAs issued before
+                if (!mbar_wait(&qo_full[i % K_ST], (i / K_ST) & 1, abort_flag, flags, 0x300 + 3, wl)) return false;
                 tc_fence_after();
-                const uint32_t sq = smem_u32(sm + K_Q + st * T64), so = smem_u32(sm + K_O + st * T64);
-                // S^T_i and dP^T_i (two independent chains, interleaved); they
-                // overwrite P^T_{i-1} and dS^T_{i-1}, read by MMAs issued before
+                const uint32_t sq = q_of(i);
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
+                for (int k = 0; k < D / 16; k++)
                     umma_bf16(tmem + K_TS, sdesc(sk + 32 * k, 16, 1024), sdesc(sq + 32 * k, 16, 1024), ID, k > 0);
-                    umma_bf16(tmem + K_TP, sdesc(sv + 32 * k, 16, 1024), sdesc(so + 32 * k, 16, 1024), ID, k > 0);
-                }
                 issued = true;
-                umma_commit(st_full);
-                if (!mbar_wait(ps_full, i & 1, abort_flag, flags, 0x300 + 5, wl)) { ok = false; break; }
+                umma_commit(s_full);
+                return true;
+            };
+            auto issue_dp = [&](int i) {  // overwrites dS^T_{i-1} likewise
+                const uint32_t so = o_of(i);
+#pragma unroll
+                for (int k = 0; k < D / 16; k++)
+                    umma_bf16(tmem + K_TP, sdesc(sv + 32 * k, 16, 1024), sdesc(so + 32 * k, 16, 1024), ID, k > 0);
+                umma_commit(dp_full);
+            };
+            ok = ok && issue_s(0);
+            if (ok) issue_dp(0);
+            for (int i = 0; i < nq && ok; i++) {
+                const uint32_t sq = q_of(i), so = o_of(i);
+                if (!mbar_wait(p_full, i & 1, abort_flag, flags, 0x300 + 4, wl)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < BN / 16; k++) {
-                    const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
-                    umma_bf16_ts(tmem + K_TV, tmem + K_TS + split_a_col(k), sdesc(so + k * 2048, T64, 1024), ID_A, acc);
-                    umma_bf16_ts(tmem + K_TK, tmem + K_TP + split_a_col(k), sdesc(sq + k * 2048, T64, 1024), ID_A, acc);
-                }
-                umma_commit(&qo_empty[st]);
+                for (int k = 0; k < BN / 16; k++)
+                    umma_bf16_ts(tmem + K_TV, tmem + K_TS + split_a_col(k), sdesc(so + k * 2048, T64, 1024), ID_A,
+                                 (i > 0 || k > 0) ? 1u : 0u);
+                if (i + 1 < nq && !issue_s(i + 1)) { ok = false; break; }
+                if (!mbar_wait(ds_full, i & 1, abort_flag, flags, 0x300 + 5, wl)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < BN / 16; k++)
+                    umma_bf16_ts(tmem + K_TK, tmem + K_TP + split_a_col(k), sdesc(sq + k * 2048, T64, 1024), ID_A,
+                                 (i > 0 || k > 0) ? 1u : 0u);
+                umma_commit(&qo_empty[i % K_ST]);
+                if (i + 1 < nq) issue_dp(i + 1);
             }
             if (ok) umma_commit(acc_full);
             else if (issued) {
@@ -962,49 +1005,63 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             sl[32 + lane] = -Dn;
             __syncwarp();
             if (i + 1 < nq) fetch(i + 1);
-            if (!mbar_wait_warp(st_full, i & 1, abort_flag, flags, 0x300 + 6, wl)) { ok = false; break; }
+            if (!mbar_wait_warp(s_full, i & 1, abort_flag, flags, 0x300 + 6, wl)) { ok = false; break; }
             tc_fence_after();
             const bool diag = tile.masked(i, j * BN);  // else all keys are seen by the whole block
             const int q0 = j * BN + 32 * half;
             const uint32_t seen = GRP && diag ? (uint32_t)(tile.queries(key, kend, j * BN) >> (32 * half)) : 0u;
-            uint32_t sw[32], dw[32];
-            tmem_ld32x2(tl + K_TS + 32 * half, sw, tl + K_TP + 32 * half, dw);
-            uint32_t pk[16], dk[16];
+            // P^T, packed fp32x2 with the scalar operations' roundings; -L and -D
+            // from the slice
+            float2 p[16];
+            {
+                uint32_t w[32], pk[16];
+                tmem_ld32(tl + K_TS + 32 * half, w);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                // -L and -D from the slice; packed fp32x2 with the scalar
-                // operations' roundings
-                const float2 L2 = *reinterpret_cast<const float2*>(sl + e);
-                const float2 D2 = *reinterpret_cast<const float2*>(sl + 32 + e);
-                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sw[e]), __uint_as_float(sw[e + 1])),
-                                            make_float2(SL2, SL2), L2);
-                float2 p = make_float2(ex2(x.x), ex2(x.y));
-                if (GRP && diag) {
-                    if (!(seen >> e & 1u)) p.x = 0.0f;
-                    if (!(seen >> (e + 1) & 1u)) p.y = 0.0f;
-                } else if (diag) {
-                    if (q0 + e < key) p.x = 0.0f;
-                    if (q0 + e + 1 < key) p.y = 0.0f;
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
+                                                make_float2(SL2, SL2), *reinterpret_cast<const float2*>(sl + e));
+                    p[e >> 1] = make_float2(ex2(x.x), ex2(x.y));
                 }
-                pk[e >> 1] = pack2<F16>(p.x, p.y);
-                float2 d =
-                    __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(dw[e]), __uint_as_float(dw[e + 1])), D2));
-                if (GRP && diag) {  // dP may be NaN where dO is padding
-                    if (!(seen >> e & 1u)) d.x = 0.0f;
-                    if (!(seen >> (e + 1) & 1u)) d.y = 0.0f;
+                if (diag) {
+#pragma unroll
+                    for (int e = 0; e < 32; e++)
+                        if (GRP ? !(seen >> e & 1u) : q0 + e < key) (e & 1 ? p[e >> 1].y : p[e >> 1].x) = 0.0f;
                 }
-                dk[e >> 1] = pack2<F16>(d.x, d.y);
+#pragma unroll
+                for (int e = 0; e < 16; e++) pk[e] = pack2<F16>(p[e].x, p[e].y);
+                tmem_st16(tl + K_TS + 32 * half, pk);
+                tmem_st_wait();
             }
-            tmem_st16(tl + K_TS + 32 * half, pk);
-            tmem_st16(tl + K_TP + 32 * half, dk);
-            tmem_st_wait();
             if (GRP && j * BN + BN > tile.end) {  // S^T_i and dP^T_i are done, the products with Q_i and dO_i to come
+                if (!mbar_wait_warp(dp_full, i & 1, abort_flag, flags, 0x300 + 7, wl)) { ok = false; break; }
                 clear_rows(sm + K_Q + (i % K_ST) * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
                 clear_rows(sm + K_O + (i % K_ST) * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
-            warp_arrive(ps_full, lane);
+            warp_arrive(p_full, lane);
+            // dS^T
+            if (!mbar_wait_warp(dp_full, i & 1, abort_flag, flags, 0x300 + 9, wl)) { ok = false; break; }
+            tc_fence_after();
+            {
+                uint32_t w[32], pk[16];
+                tmem_ld32(tl + K_TP + 32 * half, w);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    p[e >> 1] = __fmul2_rn(p[e >> 1], __fadd2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
+                                                                 *reinterpret_cast<const float2*>(sl + 32 + e)));
+                if (GRP && diag) {  // dP may be NaN where dO is padding
+#pragma unroll
+                    for (int e = 0; e < 32; e++)
+                        if (!(seen >> e & 1u)) (e & 1 ? p[e >> 1].y : p[e >> 1].x) = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e++) pk[e] = pack2<F16>(p[e].x, p[e].y);
+                tmem_st16(tl + K_TP + 32 * half, pk);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            warp_arrive(ds_full, lane);
         }
         const bool got = ok && mbar_wait_warp(acc_full, 0, abort_flag, flags, 0x300 + 8, wl);
         if (got) tc_fence_after();
