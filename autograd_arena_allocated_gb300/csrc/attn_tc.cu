@@ -111,6 +111,12 @@ __device__ __forceinline__ void init_done() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// Descriptors of the tiles' first K step, formed once; the next K step of a K-major
+// tile is 32 bytes on, of an MN-major one 16 rows, the next stage T64 bytes.
+__device__ __forceinline__ uint64_t kmajor(uint32_t saddr) { return sdesc(saddr, 16, 1024); }
+__device__ __forceinline__ uint64_t mnmajor(uint32_t saddr) { return sdesc(saddr, T64, 1024); }
+constexpr uint32_t DESC_T64 = T64 >> 4;
+
 // The 64-wide blocks that a 128-row tile of queries (keys) goes past, and which
 // of them are masked: causal attention over T positions, or a group.
 template <bool GRP> struct Tile;
@@ -289,7 +295,8 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         if (lane == 0) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_O = idesc16<F16>(BQ, D, false, true);
-            const uint32_t sq = smem_u32(sm + F_Q), sv = smem_u32(sm + F_V);
+            const uint64_t dq = kmajor(smem_u32(sm + F_Q)), dv = mnmajor(smem_u32(sm + F_V)), dk = kmajor(smem_u32(sm + F_K)),
+                           dp = kmajor(smem_u32(sm + F_P));
             bool ok = mbar_wait(q_full, 0, abort_flag, flags, 0x100 + 3, wl);
             bool issued = false;
             // S_{j+1} is issued as soon as the row threads hold S_j in registers,
@@ -299,10 +306,9 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 if (!mbar_wait(&k_full[st], (j >> 1) & 1, abort_flag, flags, 0x100 + 4, wl)) return false;
                 if (!mbar_wait(s_free, (j & 1) ^ 1, abort_flag, flags, 0x100 + 5, wl)) return false;
                 tc_fence_after();
-                const uint32_t sk = smem_u32(sm + F_K + st * T64);
+                const uint64_t dks = dk + st * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++)
-                    umma_bf16(tmem, sdesc(sq + 32 * k, 16, 1024), sdesc(sk + 32 * k, 16, 1024), ID, k > 0);
+                for (int k = 0; k < D / 16; k++) umma_bf16(tmem, dq + 2 * k, dks + 2 * k, ID, k > 0);
                 issued = true;
                 umma_commit(s_full);
                 umma_commit(&k_empty[st]);
@@ -315,11 +321,10 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 if (!mbar_wait(&p_full[pb], (j >> 1) & 1, abort_flag, flags, 0x100 + 6, wl)) { ok = false; break; }
                 if (!mbar_wait(v_full, j & 1, abort_flag, flags, 0x100 + 7, wl)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t sp = smem_u32(sm + F_P + pb * T128);
+                const uint64_t dps = dp + pb * 2 * DESC_T64;
 #pragma unroll
                 for (int k = 0; k < BN / 16; k++)
-                    umma_bf16(tmem + BN, sdesc(sp + 32 * k, 16, 1024), sdesc(sv + k * 2048, T64, 1024), ID_O,
-                              (j > 0 || k > 0) ? 1u : 0u);
+                    umma_bf16(tmem + BN, dps + 2 * k, dv + 128 * k, ID_O, (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(&o_full[pb]);
                 umma_commit(v_empty);
             }
@@ -667,17 +672,17 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         if (lane == 0) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_Q = idesc16<F16>(BQ, D, false, true);
-            const uint32_t sq = smem_u32(sm + Q_Q), so = smem_u32(sm + Q_O);
+            const uint64_t dq = kmajor(smem_u32(sm + Q_Q)), dout = kmajor(smem_u32(sm + Q_O)), dk = kmajor(smem_u32(sm + Q_K)),
+                           dkt = mnmajor(smem_u32(sm + Q_K)), dv = kmajor(smem_u32(sm + Q_V));
             bool ok = mbar_wait(qo_full, 0, abort_flag, flags, 0x200 + 2, wl);
             bool issued = false;
             // dQ += dS_j K_j: dS from tensor-memory buffer j & 1, K_j read MN-major
             auto issue_dq = [&](int j) {
-                const uint32_t sk = smem_u32(sm + Q_K + (j % Q_KST) * T64);
+                const uint64_t dks = dkt + (j % Q_KST) * DESC_T64;
                 const uint32_t ta = tmem + Q_TDS + 32 * (j & 1);
 #pragma unroll
                 for (int k = 0; k < BN / 16; k++)
-                    umma_bf16_ts(tmem + Q_TACC, ta + 8 * k, sdesc(sk + k * 2048, T64, 1024), ID_Q,
-                                 (j > 0 || k > 0) ? 1u : 0u);
+                    umma_bf16_ts(tmem + Q_TACC, ta + 8 * k, dks + 128 * k, ID_Q, (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(&k_empty[j % Q_KST]);
             };
             // S_j and dP_j: two independent chains, interleaved
@@ -687,11 +692,11 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 if (!mbar_wait(&v_full[vs], (j >> 1) & 1, abort_flag, flags, 0x200 + 11, wl)) return false;
                 if (j > 0 && !mbar_wait(s_free, (j - 1) & 1, abort_flag, flags, 0x200 + 4, wl)) return false;
                 tc_fence_after();
-                const uint32_t sk = smem_u32(sm + Q_K + ks * T64), sv = smem_u32(sm + Q_V + vs * T64);
+                const uint64_t dks = dk + ks * DESC_T64, dvs = dv + vs * DESC_T64;
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
-                    umma_bf16(tmem + Q_TS, sdesc(sq + 32 * k, 16, 1024), sdesc(sk + 32 * k, 16, 1024), ID, k > 0);
-                    umma_bf16(tmem + Q_TP, sdesc(so + 32 * k, 16, 1024), sdesc(sv + 32 * k, 16, 1024), ID, k > 0);
+                    umma_bf16(tmem + Q_TS, dq + 2 * k, dks + 2 * k, ID, k > 0);
+                    umma_bf16(tmem + Q_TP, dout + 2 * k, dvs + 2 * k, ID, k > 0);
                 }
                 issued = true;
                 umma_commit(s_full);
@@ -926,48 +931,46 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (lane == 0) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_A = idesc16<F16>(BQ, D, false, true);
-            const uint32_t sk = smem_u32(sm + K_K), sv = smem_u32(sm + K_V);
+            const uint64_t dk = kmajor(smem_u32(sm + K_K)), dv = kmajor(smem_u32(sm + K_V));
+            const uint64_t dq = kmajor(smem_u32(sm + K_Q)), dqt = mnmajor(smem_u32(sm + K_Q));
+            const uint64_t dout = kmajor(smem_u32(sm + K_O)), doutt = mnmajor(smem_u32(sm + K_O));
             bool ok = mbar_wait(kv_full, 0, abort_flag, flags, 0x300 + 2, wl);
             bool issued = false;
-            auto q_of = [&](int i) { return smem_u32(sm + K_Q + (i % K_ST) * T64); };
-            auto o_of = [&](int i) { return smem_u32(sm + K_O + (i % K_ST) * T64); };
-            auto issue_s = [&](int i) {  // overwrites P^T_{i-1}, read by MMAs issued before
-                if (!mbar_wait(&qo_full[i % K_ST], (i / K_ST) & 1, abort_flag, flags, 0x300 + 3, wl)) return false;
+            auto issue_s = [&](int i, int st) {  // overwrites P^T_{i-1}, read by MMAs issued before
+                if (!mbar_wait(&qo_full[st], (i / K_ST) & 1, abort_flag, flags, 0x300 + 3, wl)) return false;
                 tc_fence_after();
-                const uint32_t sq = q_of(i);
+                const uint64_t ds = dq + st * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++)
-                    umma_bf16(tmem + K_TS, sdesc(sk + 32 * k, 16, 1024), sdesc(sq + 32 * k, 16, 1024), ID, k > 0);
+                for (int k = 0; k < D / 16; k++) umma_bf16(tmem + K_TS, dk + 2 * k, ds + 2 * k, ID, k > 0);
                 issued = true;
                 umma_commit(s_full);
                 return true;
             };
-            auto issue_dp = [&](int i) {  // overwrites dS^T_{i-1} likewise
-                const uint32_t so = o_of(i);
+            auto issue_dp = [&](int st) {  // overwrites dS^T_{i-1} likewise
+                const uint64_t ds = dout + st * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++)
-                    umma_bf16(tmem + K_TP, sdesc(sv + 32 * k, 16, 1024), sdesc(so + 32 * k, 16, 1024), ID, k > 0);
+                for (int k = 0; k < D / 16; k++) umma_bf16(tmem + K_TP, dv + 2 * k, ds + 2 * k, ID, k > 0);
                 umma_commit(dp_full);
             };
-            ok = ok && issue_s(0);
+            ok = ok && issue_s(0, 0);
             if (ok) issue_dp(0);
-            for (int i = 0; i < nq && ok; i++) {
-                const uint32_t sq = q_of(i), so = o_of(i);
+            for (int i = 0, st = 0; i < nq && ok; i++) {
+                const int next = st + 1 == K_ST ? 0 : st + 1;
+                const uint64_t dos = doutt + st * DESC_T64, dqs = dqt + st * DESC_T64;
                 if (!mbar_wait(p_full, i & 1, abort_flag, flags, 0x300 + 4, wl)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < BN / 16; k++)
-                    umma_bf16_ts(tmem + K_TV, tmem + K_TS + split_a_col(k), sdesc(so + k * 2048, T64, 1024), ID_A,
-                                 (i > 0 || k > 0) ? 1u : 0u);
-                if (i + 1 < nq && !issue_s(i + 1)) { ok = false; break; }
+                    umma_bf16_ts(tmem + K_TV, tmem + K_TS + split_a_col(k), dos + 128 * k, ID_A, (i > 0 || k > 0) ? 1u : 0u);
+                if (i + 1 < nq && !issue_s(i + 1, next)) { ok = false; break; }
                 if (!mbar_wait(ds_full, i & 1, abort_flag, flags, 0x300 + 5, wl)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < BN / 16; k++)
-                    umma_bf16_ts(tmem + K_TK, tmem + K_TP + split_a_col(k), sdesc(sq + k * 2048, T64, 1024), ID_A,
-                                 (i > 0 || k > 0) ? 1u : 0u);
-                umma_commit(&qo_empty[i % K_ST]);
-                if (i + 1 < nq) issue_dp(i + 1);
+                    umma_bf16_ts(tmem + K_TK, tmem + K_TP + split_a_col(k), dqs + 128 * k, ID_A, (i > 0 || k > 0) ? 1u : 0u);
+                umma_commit(&qo_empty[st]);
+                if (i + 1 < nq) issue_dp(next);
+                st = next;
             }
             if (ok) umma_commit(acc_full);
             else if (issued) {
