@@ -111,6 +111,17 @@ __device__ __forceinline__ void init_done() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// One lane of a converged warp, and a value that all its lanes have.  A branch on
+// elect.sync, over operands the compiler knows as the warp's, lets a tcgen05.mma take
+// them from uniform registers: alone on the SM, 64 x 16 from tensor memory 33 cycles
+// each, by `lane == 0` 47 (from shared memory, 48 cycles of reading, 50 and 53).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+template <typename T> __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Descriptors of the tiles' first K step, formed once; the next K step of a K-major
 // tile is 32 bytes on, of an MN-major one 16 rows, the next stage T64 bytes.
 __device__ __forceinline__ uint64_t kmajor(uint32_t saddr) { return sdesc(saddr, 16, 1024); }
@@ -219,7 +230,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     const int qt = nqt - 1 - (int)blockIdx.y;  // longest rows first within the band
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (GRP) pdl_enter();  // the lists of starts are read from here on
     const Tile<GRP> tile(starts, b, K, T, qt);
     if (GRP) {
@@ -256,11 +267,11 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = uniform(*tmem_holder);
     if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
             mbar_expect_tx(q_full, T128);
             tma_load_2d(smem_u32(sm + F_Q), &tq, q_full, xq, row0 + qt * BQ);
@@ -292,7 +303,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_O = idesc16<F16>(BQ, D, false, true);
             const uint64_t dq = kmajor(smem_u32(sm + F_Q)), dv = mnmajor(smem_u32(sm + F_V)), dk = kmajor(smem_u32(sm + F_K)),
@@ -532,6 +543,12 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
+// four bytes to shared memory, seen by the thread itself after cp_async_wait
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Named barrier for the 256 row threads only.
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -602,7 +619,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     const int qt = nqt - 1 - (int)blockIdx.y;  // longest rows first within the band
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (GRP) pdl_enter();
     const Tile<GRP> tile(starts, b, K, T, qt);
     if (GRP) {
@@ -637,11 +654,11 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = uniform(*tmem_holder);
     if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
             mbar_expect_tx(qo_full, 2 * T128);
             tma_load_2d(smem_u32(sm + Q_Q), &tq, qo_full, xq, row0 + qt * BQ);
@@ -669,7 +686,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_Q = idesc16<F16>(BQ, D, false, true);
             const uint64_t dq = kmajor(smem_u32(sm + Q_Q)), dout = kmajor(smem_u32(sm + Q_O)), dk = kmajor(smem_u32(sm + Q_K)),
@@ -838,8 +855,8 @@ constexpr int K_V = K_K + T128;
 constexpr int K_ST = 3;                  // Q / dO block stages
 constexpr int K_Q = K_V + T128;
 constexpr int K_O = K_Q + K_ST * T64;
-constexpr int K_LD = K_O + K_ST * T64;   // per row warp: log-sum-exp and D of its 32 queries
-constexpr int K_CS = K_LD + 8 * 64 * 4;  // column sums [2 halves][4 quarters][32]
+constexpr int K_LD = K_O + K_ST * T64;   // per row warp: log-sum-exp and D of its 32 queries, and the next 32
+constexpr int K_CS = K_LD + 8 * 128 * 4;  // column sums [2 halves][4 quarters][32]
 constexpr int K_BAR = K_CS + 2 * 4 * 32 * 4;
 constexpr int K_SMEM = K_BAR + 256 + 1024;
 constexpr uint32_t K_TMEM = 256;         // S^T 0..63, dP^T 64..127, dV 128..191, dK 192..255
@@ -871,7 +888,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const int kt = (int)blockIdx.y;  // key tile; low tiles see the most query blocks
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (GRP) pdl_enter();
     const KTile<GRP> tile(starts, b, K, T, kt);
     if (GRP && tile.end <= kt * BQ) {
@@ -902,11 +919,11 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = uniform(*tmem_holder);
     if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
             mbar_expect_tx(kv_full, 2 * T128);
             tma_load_2d(smem_u32(sm + K_K), &tq, kv_full, xk, row0 + kt * BQ);
@@ -928,7 +945,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_A = idesc16<F16>(BQ, D, false, true);
             const uint64_t dk = kmajor(smem_u32(sm + K_K)), dv = kmajor(smem_u32(sm + K_V));
@@ -988,24 +1005,28 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const float* lrow = lse + bhl * T;
         const float* drow = Dlt + bhl * T;
         bool ok = true;
-        // The log-sum-exp (base 2) and D of this warp's 32 queries of block i
-        // are fetched one block ahead (lane l: query 64 (j0 + i) + 32 half + l),
-        // then placed in this warp's slice of shared memory, from which every
-        // lane reads them as broadcasts.
-        float* sl = reinterpret_cast<float*>(sm + K_LD) + (warp - 2) * 64;  // [32 L | 32 D]
-        float Ln, Dn;
+        // The log-sum-exp and D of this warp's 32 queries of block i (lane l: query
+        // 64 (j0 + i) + 32 half + l) are copied one block ahead into shared memory
+        // (in registers they would be spilled, and the warp wait for the load),
+        // and placed negated, the log-sum-exp in base 2, in this warp's slice, from
+        // which every lane reads them as broadcasts.
+        float* sl = reinterpret_cast<float*>(sm + K_LD) + (warp - 2) * 128;  // [32 L | 32 D | the next 32 L | 32 D]
         auto fetch = [&](int i) {
             const int qq = (j0 + i) * BN + 32 * half + lane;
-            Ln = qq < tile.end ? __ldg(lrow + qq) * LOG2E : INFINITY;
-            Dn = qq < tile.end ? __ldg(drow + qq) : 0.0f;
+            if (qq < tile.end) {
+                cp_async4(sl + 64 + lane, lrow + qq);
+                cp_async4(sl + 96 + lane, drow + qq);
+            }
         };
         fetch(0);
         const int kend = GRP && key < tile.end ? tile.end_of(key) : 0;
         for (int i = 0; i < nq; i++) {
             const int j = j0 + i;
+            cp_async_wait();
             __syncwarp();  // the previous block's reads of the slice are done
-            sl[lane] = -Ln;  // negated: the packed fma and add below take them as addends
-            sl[32 + lane] = -Dn;
+            const bool there = j * BN + 32 * half + lane < tile.end;
+            sl[lane] = there ? -(sl[64 + lane] * LOG2E) : -INFINITY;
+            sl[32 + lane] = there ? -sl[96 + lane] : 0.0f;
             __syncwarp();
             if (i + 1 < nq) fetch(i + 1);
             if (!mbar_wait_warp(s_full, i & 1, abort_flag, flags, 0x300 + 6, wl)) { ok = false; break; }
