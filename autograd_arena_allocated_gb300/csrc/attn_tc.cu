@@ -374,11 +374,11 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (!diag) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    mq[0] = fmaxf(mq[0], __uint_as_float(w0[e]));
-                    mq[1] = fmaxf(mq[1], __uint_as_float(w0[e + 1]));
-                    mq[2] = fmaxf(mq[2], __uint_as_float(w1[e]));
-                    mq[3] = fmaxf(mq[3], __uint_as_float(w1[e + 1]));
+                for (int e = 0; e < 32; e += 4) {  // two values an instruction
+                    mq[0] = fmaxf(fmaxf(mq[0], __uint_as_float(w0[e])), __uint_as_float(w0[e + 1]));
+                    mq[1] = fmaxf(fmaxf(mq[1], __uint_as_float(w0[e + 2])), __uint_as_float(w0[e + 3]));
+                    mq[2] = fmaxf(fmaxf(mq[2], __uint_as_float(w1[e])), __uint_as_float(w1[e + 1]));
+                    mq[3] = fmaxf(fmaxf(mq[3], __uint_as_float(w1[e + 2])), __uint_as_float(w1[e + 3]));
                 }
             } else {
 #pragma unroll
@@ -542,12 +542,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
 }
-
-// four bytes to shared memory, seen by the thread itself after cp_async_wait
-__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Named barrier for the 256 row threads only.
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -855,8 +849,8 @@ constexpr int K_V = K_K + T128;
 constexpr int K_ST = 3;                  // Q / dO block stages
 constexpr int K_Q = K_V + T128;
 constexpr int K_O = K_Q + K_ST * T64;
-constexpr int K_LD = K_O + K_ST * T64;   // per row warp: log-sum-exp and D of its 32 queries, and the next 32
-constexpr int K_CS = K_LD + 8 * 128 * 4;  // column sums [2 halves][4 quarters][32]
+constexpr int K_LD = K_O + K_ST * T64;   // per stage: -log-sum-exp (base 2) [64], -D [64]
+constexpr int K_CS = K_LD + K_ST * 128 * 4;  // column sums [2 halves][4 quarters][32]
 constexpr int K_BAR = K_CS + 2 * 4 * 32 * 4;
 constexpr int K_SMEM = K_BAR + 256 + 1024;
 constexpr uint32_t K_TMEM = 256;         // S^T 0..63, dP^T 64..127, dV 128..191, dK 192..255
@@ -903,7 +897,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
         for (int i = 0; i < K_ST; i++) {
-            mbar_init(&qo_full[i], 1);
+            mbar_init(&qo_full[i], 2);  // the copies' and the log-sum-exps'
             mbar_init(&qo_empty[i], 1);
         }
         mbar_init(s_full, 1);
@@ -923,26 +917,47 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
 
     if (warp == 0) {
+        // The whole warp: one lane starts the copies, all of them bring the block's
+        // log-sum-exps and Ds, negated (the rows' packed fma and add take them as
+        // addends), so that the row warps, which everything waits for, do not.
+        const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
+        const long long bhl = (long long)b * H + h;
         if (elect_one()) {
-            const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
             mbar_expect_tx(kv_full, 2 * T128);
             tma_load_2d(smem_u32(sm + K_K), &tq, kv_full, xk, row0 + kt * BQ);
             tma_load_2d(smem_u32(sm + K_V), &tq, kv_full, xv, row0 + kt * BQ);
-            int issued = 0;
-            bool ok = true;
-            for (int i = 0; i < nq; i++) {
-                const int st = i % K_ST, j = j0 + i;
-                if (!mbar_wait(&qo_empty[st], ((i / K_ST) & 1) ^ 1, abort_flag, flags, 0x300 + 1, wl)) { ok = false; break; }
+        }
+        int issued = 0;
+        bool ok = true;
+        for (int i = 0, st = 0; i < nq; i++) {
+            const int j = j0 + i;
+            float L[2], Dq[2];
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                const int qq = j * BN + 32 * u + lane;
+                L[u] = qq < tile.end ? __ldg(lse + bhl * T + qq) : INFINITY;
+                Dq[u] = qq < tile.end ? __ldg(Dlt + bhl * T + qq) : 0.0f;
+            }
+            if (!mbar_wait_warp(&qo_empty[st], ((i / K_ST) & 1) ^ 1, abort_flag, flags, 0x300 + 1, wl)) { ok = false; break; }
+            if (elect_one()) {
                 mbar_expect_tx(&qo_full[st], 2 * T64);
                 tma_load_2d(smem_u32(sm + K_Q + st * T64), &tk, &qo_full[st], xq, row0 + j * BN);
                 tma_load_2d(smem_u32(sm + K_O + st * T64), &to, &qo_full[st], h * D, row0 + j * BN);
-                ++issued;
             }
-            if (!ok) {
-                mbar_drain(kv_full, 0);
-                for (int i = (issued > K_ST ? issued - K_ST : 0); i < issued; i++)
-                    mbar_drain(&qo_full[i % K_ST], (i / K_ST) & 1);
+            ++issued;
+            float* ld = reinterpret_cast<float*>(sm + K_LD) + st * 128;
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                ld[32 * u + lane] = -(L[u] * LOG2E);
+                ld[64 + 32 * u + lane] = -Dq[u];
             }
+            warp_arrive(&qo_full[st], lane);
+            st = st + 1 == K_ST ? 0 : st + 1;
+        }
+        if (!ok && lane == 0) {  // let issued copies land before the CTA exits
+            mbar_drain(kv_full, 0);
+            for (int i = (issued > K_ST ? issued - K_ST : 0); i < issued; i++)
+                mbar_drain(&qo_full[i % K_ST], (i / K_ST) & 1);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -1001,34 +1016,13 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int r = quarter * 32 + lane;
         const int key = kt * BQ + r;
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-        const long long bhl = (long long)b * H + h;
-        const float* lrow = lse + bhl * T;
-        const float* drow = Dlt + bhl * T;
         bool ok = true;
-        // The log-sum-exp and D of this warp's 32 queries of block i (lane l: query
-        // 64 (j0 + i) + 32 half + l) are copied one block ahead into shared memory
-        // (in registers they would be spilled, and the warp wait for the load),
-        // and placed negated, the log-sum-exp in base 2, in this warp's slice, from
-        // which every lane reads them as broadcasts.
-        float* sl = reinterpret_cast<float*>(sm + K_LD) + (warp - 2) * 128;  // [32 L | 32 D | the next 32 L | 32 D]
-        auto fetch = [&](int i) {
-            const int qq = (j0 + i) * BN + 32 * half + lane;
-            if (qq < tile.end) {
-                cp_async4(sl + 64 + lane, lrow + qq);
-                cp_async4(sl + 96 + lane, drow + qq);
-            }
-        };
-        fetch(0);
         const int kend = GRP && key < tile.end ? tile.end_of(key) : 0;
-        for (int i = 0; i < nq; i++) {
+        for (int i = 0, st = 0; i < nq; i++, st = st + 1 == K_ST ? 0 : st + 1) {
             const int j = j0 + i;
-            cp_async_wait();
-            __syncwarp();  // the previous block's reads of the slice are done
-            const bool there = j * BN + 32 * half + lane < tile.end;
-            sl[lane] = there ? -(sl[64 + lane] * LOG2E) : -INFINITY;
-            sl[32 + lane] = there ? -sl[96 + lane] : 0.0f;
-            __syncwarp();
-            if (i + 1 < nq) fetch(i + 1);
+            // -L and -D of this half's queries, read as broadcasts
+            const float* sl = reinterpret_cast<const float*>(sm + K_LD) + st * 128 + 32 * half;
+            if (!mbar_wait_warp(&qo_full[st], (i / K_ST) & 1, abort_flag, flags, 0x300 + 10, wl)) { ok = false; break; }
             if (!mbar_wait_warp(s_full, i & 1, abort_flag, flags, 0x300 + 6, wl)) { ok = false; break; }
             tc_fence_after();
             const bool diag = tile.masked(i, j * BN);  // else all keys are seen by the whole block
@@ -1041,10 +1035,14 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 uint32_t w[32], pk[16];
                 tmem_ld32(tl + K_TS + 32 * half, w);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(sl + e);
                     const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
-                                                make_float2(SL2, SL2), *reinterpret_cast<const float2*>(sl + e));
+                                                make_float2(SL2, SL2), make_float2(l.x, l.y));
+                    const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])),
+                                                 make_float2(SL2, SL2), make_float2(l.z, l.w));
                     p[e >> 1] = make_float2(ex2(x.x), ex2(x.y));
+                    p[(e >> 1) + 1] = make_float2(ex2(x2.x), ex2(x2.y));
                 }
                 if (diag) {
 #pragma unroll
@@ -1058,8 +1056,8 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
             if (GRP && j * BN + BN > tile.end) {  // S^T_i and dP^T_i are done, the products with Q_i and dO_i to come
                 if (!mbar_wait_warp(dp_full, i & 1, abort_flag, flags, 0x300 + 7, wl)) { ok = false; break; }
-                clear_rows(sm + K_Q + (i % K_ST) * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
-                clear_rows(sm + K_O + (i % K_ST) * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
+                clear_rows(sm + K_Q + st * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
+                clear_rows(sm + K_O + st * T64, tile.end - j * BN, threadIdx.x - 64, BW_ROWS);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
@@ -1071,9 +1069,13 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 uint32_t w[32], pk[16];
                 tmem_ld32(tl + K_TP + 32 * half, w);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 d = *reinterpret_cast<const float4*>(sl + 64 + e);
                     p[e >> 1] = __fmul2_rn(p[e >> 1], __fadd2_rn(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
-                                                                 *reinterpret_cast<const float2*>(sl + 32 + e)));
+                                                                 make_float2(d.x, d.y)));
+                    p[(e >> 1) + 1] = __fmul2_rn(p[(e >> 1) + 1], __fadd2_rn(make_float2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])),
+                                                                             make_float2(d.z, d.w)));
+                }
                 if (GRP && diag) {  // dP may be NaN where dO is padding
 #pragma unroll
                     for (int e = 0; e < 32; e++)
