@@ -600,11 +600,11 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     uint64_t* v_full = bars + 7;    // [2]
     uint64_t* v_empty = bars + 9;   // [2]
     uint64_t* s_full = bars + 11;   // S_j, dP_j (and every earlier MMA) done
-    uint64_t* ds_full = bars + 12;  // block j's dS written
-    uint64_t* acc_full = bars + 13;
-    uint64_t* drain = bars + 14;    // MMAs issued before an abort are done
-    uint64_t* s_free = bars + 15;   // S_j and dP_j are in registers
-    uint32_t* tmem_holder = (uint32_t*)(bars + 16);
+    uint64_t* ds_full = bars + 12;  // [2] block j's dS written: the rows may be a block ahead of the MMA thread's wait
+    uint64_t* acc_full = bars + 14;
+    uint64_t* drain = bars + 15;    // MMAs issued before an abort are done
+    uint64_t* s_free = bars + 16;   // S_j and dP_j are in registers
+    uint32_t* tmem_holder = (uint32_t*)(bars + 17);
     volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
 
     const int bh = (int)(blockIdx.z * gridDim.x + blockIdx.x);
@@ -637,7 +637,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             mbar_init(&v_empty[i], 1);
         }
         mbar_init(s_full, 1);
-        mbar_init(ds_full, BW_ROWS / 32);
+        for (int i = 0; i < 2; i++) mbar_init(&ds_full[i], BW_ROWS / 32);
         mbar_init(s_free, BW_ROWS / 32);
         mbar_init(acc_full, 1);
         mbar_init(drain, 1);
@@ -718,7 +718,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
             for (int j = 0; j < nkv && ok; j++) {
                 // the next block's scores while the row threads work on this one's
                 if (j + 1 < nkv && !issue_s(j + 1)) { ok = false; break; }
-                if (!mbar_wait(ds_full, j & 1, abort_flag, flags, 0x200 + 5, wl)) { ok = false; break; }
+                if (!mbar_wait(&ds_full[j & 1], (j >> 1) & 1, abort_flag, flags, 0x200 + 5, wl)) { ok = false; break; }
                 tc_fence_after();
                 issue_dq(j);
             }
@@ -809,7 +809,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 fence_proxy_async_smem();
             }
             tc_fence_before();
-            warp_arrive(ds_full, lane);
+            warp_arrive(&ds_full[j & 1], lane);
         }
         float cv[32];
 #pragma unroll
