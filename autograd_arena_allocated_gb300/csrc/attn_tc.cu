@@ -84,29 +84,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 32 bf16 values (columns k0..k0+31, k0 in {0, 32}) of row r of a K-major,
-// 128-byte-swizzled [128 rows x 64 columns] operand (16-byte chunk c of row r
-// at c ^ (r mod 8)).  Rows of 32 consecutive lanes: conflict-free.
-__device__ __forceinline__ void store_row32(uint8_t* base, int r, int k0, const uint32_t (&w)[16]) {
-    uint8_t* row = base + r * 128;
-    const int c0 = k0 >> 3;
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        *reinterpret_cast<uint4*>(row + (((c0 + i) ^ (r & 7)) << 4)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-}
-
-template <bool F16>
-__device__ __forceinline__ void store_out64(bf16* dst, const float* v, float scale) {
-    uint4* o = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-        o[i] = make_uint4(pack2<F16>(v[8 * i] * scale, v[8 * i + 1] * scale),
-                          pack2<F16>(v[8 * i + 2] * scale, v[8 * i + 3] * scale),
-                          pack2<F16>(v[8 * i + 4] * scale, v[8 * i + 5] * scale),
-                          pack2<F16>(v[8 * i + 6] * scale, v[8 * i + 7] * scale));
-}
-
 __device__ __forceinline__ void init_done() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -189,22 +166,43 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int tid, int
     for (int i = from * 8 + tid; i < BN * 8; i += threads) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
 }
 
+// tensor-memory column of the A operand for K step k (16 elements) of a
+// 64-wide bf16 operand written as two 16-column halves 32 columns apart
+__device__ __forceinline__ uint32_t split_a_col(int k) { return (uint32_t)(8 * k + (k >= 2 ? 16 : 0)); }
+
+template <bool F16>
+__device__ __forceinline__ void store_out32(bf16* dst, const uint32_t (&w)[32], float scale) {
+    uint4* o = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        o[i] = make_uint4(pack2<F16>(__uint_as_float(w[8 * i]) * scale, __uint_as_float(w[8 * i + 1]) * scale),
+                          pack2<F16>(__uint_as_float(w[8 * i + 2]) * scale, __uint_as_float(w[8 * i + 3]) * scale),
+                          pack2<F16>(__uint_as_float(w[8 * i + 4]) * scale, __uint_as_float(w[8 * i + 5]) * scale),
+                          pack2<F16>(__uint_as_float(w[8 * i + 6]) * scale, __uint_as_float(w[8 * i + 7]) * scale));
+}
+
+// One arrival per warp: every lane has passed its own fences (the caller's
+// tcgen05.fence / fence.proxy.async) before lane 0 arrives for the warp.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
 // ================================================================== forward
-// The softmax warps never wait for the P.V product of the previous block in
-// the common case: P is double-buffered in shared memory (buffer j & 1, with
-// its own full / consumed barriers), the exponentials of block j are
-// computed in registers while P_{j-1} V_{j-1} runs, and the warps wait for
-// the previous product only when the row maximum forces a rescale of O.
+// Four CTAs an SM, whose phases fill each other's gaps.  P_j, bf16, replaces S_j in
+// tensor memory (its halves 32 columns apart), the A operand of O += P_j V_j; S_{j+1}
+// is issued behind that product, so that a row that sees it knows O to be whole, and
+// may rescale it in place.  A row keeps 32 of its 64 scores in registers and reads the
+// other half again from tensor memory.
 constexpr int F_Q = 0;
 constexpr int F_K = F_Q + T128;     // 2 stages
 constexpr int F_V = F_K + 2 * T64;  // 1 stage
-constexpr int F_P = F_V + T64;      // P: 2 x [128 x 64] bf16
-constexpr int F_BAR = F_P + 2 * T128;
+constexpr int F_BAR = F_V + T64;
 constexpr int F_SMEM = F_BAR + 256 + 1024;
-constexpr uint32_t F_TMEM = 128;    // S: cols 0..63, O: 64..127
+constexpr uint32_t F_TMEM = 128;    // S, P: cols 0..63, O: 64..127
 
 template <bool F16, bool GRP>
-__global__ void __launch_bounds__(THREADS, 3)
+__global__ void __launch_bounds__(THREADS, 4)
 k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
               bf16* __restrict__ y, float* __restrict__ lse, int T, int C, int H, int nbh, int* flags,
               long long wl, const int32_t* __restrict__ starts, int K) {
@@ -217,11 +215,10 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     uint64_t* v_full = bars + 5;
     uint64_t* v_empty = bars + 6;
     uint64_t* s_full = bars + 7;
-    uint64_t* s_free = bars + 8;
-    uint64_t* p_full = bars + 9;   // [2]: P buffer written
-    uint64_t* o_full = bars + 11;  // [2]: P.V of a block in buffer s done (buffer s consumed)
-    uint64_t* drain = bars + 13;   // MMAs issued before an abort are done
-    uint32_t* tmem_holder = (uint32_t*)(bars + 14);
+    uint64_t* p_full = bars + 8;   // S_j read, P_j in tensor memory
+    uint64_t* o_full = bars + 9;   // the last product done
+    uint64_t* drain = bars + 10;   // MMAs issued before an abort are done
+    uint32_t* tmem_holder = (uint32_t*)(bars + 11);
     volatile int* abort_flag = (volatile int*)(tmem_holder + 1);
 
     const int bh = (int)(blockIdx.z * gridDim.x + blockIdx.x);
@@ -254,11 +251,8 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         mbar_init(v_full, 1);
         mbar_init(v_empty, 1);
         mbar_init(s_full, 1);
-        mbar_init(s_free, 128);
-        mbar_init(&p_full[0], 128);
-        mbar_init(&p_full[1], 128);
-        mbar_init(&o_full[0], 1);
-        mbar_init(&o_full[1], 1);
+        mbar_init(p_full, 4);
+        mbar_init(o_full, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
         init_done();
@@ -306,16 +300,12 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_O = idesc16<F16>(BQ, D, false, true);
-            const uint64_t dq = kmajor(smem_u32(sm + F_Q)), dv = mnmajor(smem_u32(sm + F_V)), dk = kmajor(smem_u32(sm + F_K)),
-                           dp = kmajor(smem_u32(sm + F_P));
+            const uint64_t dq = kmajor(smem_u32(sm + F_Q)), dv = mnmajor(smem_u32(sm + F_V)), dk = kmajor(smem_u32(sm + F_K));
             bool ok = mbar_wait(q_full, 0, abort_flag, flags, 0x100 + 3, wl);
             bool issued = false;
-            // S_{j+1} is issued as soon as the row threads hold S_j in registers,
-            // so that it overlaps the softmax of block j
-            auto issue_s = [&](int j) -> bool {
+            auto issue_s = [&](int j) -> bool {  // overwrites P_{j-1}, read by MMAs issued before
                 const int st = j & 1;
                 if (!mbar_wait(&k_full[st], (j >> 1) & 1, abort_flag, flags, 0x100 + 4, wl)) return false;
-                if (!mbar_wait(s_free, (j & 1) ^ 1, abort_flag, flags, 0x100 + 5, wl)) return false;
                 tc_fence_after();
                 const uint64_t dks = dk + st * DESC_T64;
 #pragma unroll
@@ -327,18 +317,16 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             };
             if (ok) ok = issue_s(0);
             for (int j = 0; j < nkv && ok; j++) {
-                if (j + 1 < nkv && !issue_s(j + 1)) { ok = false; break; }
-                const int pb = j & 1;
-                if (!mbar_wait(&p_full[pb], (j >> 1) & 1, abort_flag, flags, 0x100 + 6, wl)) { ok = false; break; }
                 if (!mbar_wait(v_full, j & 1, abort_flag, flags, 0x100 + 7, wl)) { ok = false; break; }
+                if (!mbar_wait(p_full, j & 1, abort_flag, flags, 0x100 + 6, wl)) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t dps = dp + pb * 2 * DESC_T64;
 #pragma unroll
                 for (int k = 0; k < BN / 16; k++)
-                    umma_bf16(tmem + BN, dps + 2 * k, dv + 128 * k, ID_O, (j > 0 || k > 0) ? 1u : 0u);
-                umma_commit(&o_full[pb]);
+                    umma_bf16_ts(tmem + BN, tmem + split_a_col(k), dv + 128 * k, ID_O, (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(v_empty);
+                if (j + 1 < nkv && !issue_s(j + 1)) { ok = false; break; }
             }
+            if (ok) umma_commit(o_full);
             if (!ok && issued) {  // the MMAs already issued finish before tensor memory is freed
                 umma_commit(drain);
                 mbar_drain(drain, 0);
@@ -366,34 +354,23 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             const int kq = q - kb;  // on the diagonal, key columns > kq are masked
             const unsigned long long seen = GRP && diag ? tile.keys(q, st0, kb) : 0ull;
             const uint32_t seen0 = (uint32_t)seen, seen1 = (uint32_t)(seen >> 32);
-            uint32_t w0[32], w1[32];
-            tmem_ld32x2(tl, w0, tl + 32, w1);
-            tc_fence_before();
-            mbar_arrive(s_free);  // S is in registers: the next S may be computed
-            // row max over four independent chains (max is exact in any order)
+            uint32_t w[32];
+            // row max over four independent chains (max is exact in any order), the
+            // second half of the columns first
             float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (!diag) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {  // two values an instruction
-                    mq[0] = fmaxf(fmaxf(mq[0], __uint_as_float(w0[e])), __uint_as_float(w0[e + 1]));
-                    mq[1] = fmaxf(fmaxf(mq[1], __uint_as_float(w0[e + 2])), __uint_as_float(w0[e + 3]));
-                    mq[2] = fmaxf(fmaxf(mq[2], __uint_as_float(w1[e])), __uint_as_float(w1[e + 1]));
-                    mq[3] = fmaxf(fmaxf(mq[3], __uint_as_float(w1[e + 2])), __uint_as_float(w1[e + 3]));
-                }
-            } else {
+            for (int c = 1; c >= 0; c--) {
+                tmem_ld32(tl + 32 * c, w);
+                if (!diag) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    if (GRP) {
-                        if (seen0 >> e & 1u) mq[0] = fmaxf(mq[0], __uint_as_float(w0[e]));
-                        if (seen0 >> (e + 1) & 1u) mq[1] = fmaxf(mq[1], __uint_as_float(w0[e + 1]));
-                        if (seen1 >> e & 1u) mq[2] = fmaxf(mq[2], __uint_as_float(w1[e]));
-                        if (seen1 >> (e + 1) & 1u) mq[3] = fmaxf(mq[3], __uint_as_float(w1[e + 1]));
-                        continue;
-                    }
-                    if (e <= kq) mq[0] = fmaxf(mq[0], __uint_as_float(w0[e]));
-                    if (e + 1 <= kq) mq[1] = fmaxf(mq[1], __uint_as_float(w0[e + 1]));
-                    if (32 + e <= kq) mq[2] = fmaxf(mq[2], __uint_as_float(w1[e]));
-                    if (33 + e <= kq) mq[3] = fmaxf(mq[3], __uint_as_float(w1[e + 1]));
+                    for (int e = 0; e < 32; e += 8)  // two values an instruction
+#pragma unroll
+                        for (int u = 0; u < 4; u++)
+                            mq[u] = fmaxf(fmaxf(mq[u], __uint_as_float(w[e + 2 * u])), __uint_as_float(w[e + 2 * u + 1]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e++)
+                        if (GRP ? (c ? seen1 : seen0) >> e & 1u : 32 * c + e <= kq) mq[e & 3] = fmaxf(mq[e & 3], __uint_as_float(w[e]));
                 }
             }
             const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
@@ -401,14 +378,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             const bool rescale = j > 0 && __any_sync(0xffffffffu, mn > m + 8.0f);
             const float m_old = m;
             if (j == 0 || rescale) m = mn;
-            const int pb = j & 1;
-            // buffer pb was last read by P_{j-2} V_{j-2} (long done, as a rule)
-            if (j >= 2 && !mbar_wait_warp(&o_full[pb], ((j - 2) >> 1) & 1, abort_flag, flags, 0x100 + 9, wl)) {
-                ok = false;
-                break;
-            }
-            // P = 2^(s*scale - m) as bf16, each 32-column half straight to shared memory
-            uint8_t* pbuf = sm + F_P + pb * T128;
+            // P = 2^(s*scale - m) as bf16, each 32-column half over its scores
             // (packed fp32x2 scale-and-subtract and sums: two lanes per instruction;
             // the sums in two independent packed chains)
             float2 rsa = make_float2(0.0f, 0.0f), rsb = make_float2(0.0f, 0.0f);
@@ -416,7 +386,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             auto probabilities = [&](auto masked) {
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const uint32_t(&w)[32] = c ? w1 : w0;
+                    if (c) tmem_ld32(tl + 32, w);
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -433,66 +403,51 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                         else rsa = __fadd2_rn(rsa, p);
                         pk[e >> 1] = pack2<F16>(p.x, p.y);
                     }
-                    store_row32(pbuf, r, 32 * c, pk);
+                    tmem_st16(tl + 32 * c, pk);
                 }
             };
             if (diag) probabilities(std::true_type{});
             else probabilities(std::false_type{});
             const float rs = (rsa.x + rsb.x) + (rsa.y + rsb.y);
-            if (rescale) {
-                // O must hold P_{j-1} V_{j-1} before it is scaled
-                if (!mbar_wait_warp(&o_full[pb ^ 1], ((j - 1) >> 1) & 1, abort_flag, flags, 0x100 + 10, wl)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            if (rescale) {  // O holds P_{j-1} V_{j-1}, which S_j was issued behind
                 const float corr = ex2(m_old - m);
-                uint32_t v[32];
-                tmem_ld32(tl + BN, v);
 #pragma unroll
-                for (int d = 0; d < 32; d++) v[d] = __float_as_uint(__uint_as_float(v[d]) * corr);
-                tmem_st32(tl + BN, v);
-                tmem_ld32(tl + BN + 32, v);
+                for (int c = 0; c < 2; c++) {
+                    tmem_ld32(tl + BN + 32 * c, w);
 #pragma unroll
-                for (int d = 0; d < 32; d++) v[d] = __float_as_uint(__uint_as_float(v[d]) * corr);
-                tmem_st32(tl + BN + 32, v);
-                tmem_st_wait();
+                    for (int d = 0; d < 32; d++) w[d] = __float_as_uint(__uint_as_float(w[d]) * corr);
+                    tmem_st32(tl + BN + 32 * c, w);
+                }
                 l *= corr;
             }
             l += rs;
             if (GRP && j == nkv - 1 && kb + BN > tile.end) {
-                // V_j has arrived once its barrier's phase is over; that the
-                // phase before it is, P_{j-1} V_{j-1} being done tells
-                if ((j > 0 && !mbar_wait_warp(&o_full[pb ^ 1], ((j - 1) >> 1) & 1, abort_flag, flags, 0x100 + 12, wl)) ||
-                    !mbar_wait_warp(v_full, j & 1, abort_flag, flags, 0x100 + 13, wl)) {
+                // V_j has arrived once its barrier's phase is over; the phase before
+                // it is: S_j was issued behind P_{j-1} V_{j-1}
+                if (!mbar_wait_warp(v_full, j & 1, abort_flag, flags, 0x100 + 13, wl)) {
                     ok = false;
                     break;
                 }
                 clear_rows(sm + F_V, tile.end - kb, threadIdx.x - 64, 128);
+                fence_proxy_async_smem();
             }
-            tc_fence_before();  // orders the TMEM stores of a rescale before the next MMA
-            fence_proxy_async_smem();
-            mbar_arrive(&p_full[pb]);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(p_full, lane);
         }
-        const int jl = nkv - 1;
-        if (ok && mbar_wait_warp(&o_full[jl & 1], (jl >> 1) & 1, abort_flag, flags, 0x100 + 11, wl)) {
+        if (ok && mbar_wait_warp(o_full, 0, abort_flag, flags, 0x100 + 11, wl)) {
             tc_fence_after();
-            float o[D];
-            uint32_t v[32];
-            tmem_ld32(tl + BN, v);
+            const bool none = GRP && q >= tile.end;
+            if (none) m = 0.0f, l = 1.0f;
+            bf16* out = y + (long long)(row0 + q) * C + h * D;
 #pragma unroll
-            for (int d = 0; d < 32; d++) o[d] = __uint_as_float(v[d]);
-            tmem_ld32(tl + BN + 32, v);
-#pragma unroll
-            for (int d = 0; d < 32; d++) o[32 + d] = __uint_as_float(v[d]);
-            if (GRP && q >= tile.end) {
-#pragma unroll
-                for (int d = 0; d < D; d++) o[d] = 0.0f;
-                m = 0.0f;
-                l = 1.0f;
+            for (int c = 0; c < 2; c++) {
+                uint32_t v[32];
+                tmem_ld32(tl + BN + 32 * c, v);
+                if (none && q < T) zero_out32(out + 32 * c);
+                else if (q < T) store_out32<F16>(out + 32 * c, v, 1.0f / l);
             }
             if (q < T) {
-                store_out64<F16>(y + (long long)(row0 + q) * C + h * D, o, 1.0f / l);
                 lse[((long long)b * H + h) * T + q] = (m + log2f(l)) * LN2;
             }
         }
@@ -520,28 +475,6 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
 // that read them, and one thread's tcgen05.mma operations run in issue order.
 constexpr int BW_THREADS = 320;
 constexpr int BW_ROWS = 256;  // row threads
-
-// tensor-memory column of the A operand for K step k (16 elements) of a
-// 64-wide bf16 operand written as two 16-column halves 32 columns apart
-__device__ __forceinline__ uint32_t split_a_col(int k) { return (uint32_t)(8 * k + (k >= 2 ? 16 : 0)); }
-
-template <bool F16>
-__device__ __forceinline__ void store_out32(bf16* dst, const uint32_t (&w)[32], float scale) {
-    uint4* o = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        o[i] = make_uint4(pack2<F16>(__uint_as_float(w[8 * i]) * scale, __uint_as_float(w[8 * i + 1]) * scale),
-                          pack2<F16>(__uint_as_float(w[8 * i + 2]) * scale, __uint_as_float(w[8 * i + 3]) * scale),
-                          pack2<F16>(__uint_as_float(w[8 * i + 4]) * scale, __uint_as_float(w[8 * i + 5]) * scale),
-                          pack2<F16>(__uint_as_float(w[8 * i + 6]) * scale, __uint_as_float(w[8 * i + 7]) * scale));
-}
-
-// One arrival per warp: every lane has passed its own fences (the caller's
-// tcgen05.fence / fence.proxy.async) before lane 0 arrives for the warp.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-}
 
 // Named barrier for the 256 row threads only.
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
