@@ -3,25 +3,21 @@
 //
 // Every kernel streams 64-wide blocks of the other sequence past a
 // 128-row tile, so that the score block (128 x 64 fp32) needs only 64 TMEM
-// columns and several CTAs fit on one SM; each CTA has 192 threads:
+// columns and several CTAs fit on one SM:
 //   warp 0      TMA (128-byte-swizzled tiles straight from the packed
 //               [B*T, 3C] qkv buffer and the [B*T, C] output gradient)
 //   warp 1      TMEM allocation and the MMAs (one elected lane)
-//   warps 2..5  one thread per tile row: reads its row of the score block
-//               from TMEM, does the elementwise work in fp32, and writes the
-//               bf16 operand of the next MMA into shared memory in the
-//               128-byte-swizzled K-major layout the MMA reads.
+//   the others  one or two threads per tile row: a row of the score block from
+//               TMEM, the elementwise work in fp32, and the 16-bit operand of the
+//               next MMA back into TMEM.
 //
-// In every kernel the MMA warp issues the next block's score MMAs as soon as
-// the row threads have copied the current scores from TMEM to registers, and
-// the row threads compute the next MMA operand in registers before they wait
-// for its shared-memory buffer, so the tensor pipe and the elementwise work
-// overlap instead of taking turns.
+// The MMA warp issues what does not wait for the rows' present work behind what
+// does, so that the tensor pipe and the elementwise work overlap.
 //
-// Forward (one CTA per 128 queries, 3 CTAs/SM): S = Q K_j^T; online softmax
-//   in base 2; P_j to shared memory (two buffers); O += P_j V_j accumulates in
-//   TMEM (V read as an MN-major operand), rescaled in place only when the row
-//   max grows by more than 2^8; finally y = O / l and the row's log-sum-exp.
+// Forward (one CTA per 128 queries, 4 CTAs/SM): S = Q K_j^T; online softmax
+//   in base 2; P_j over S; O += P_j V_j accumulates in TMEM (V read as an
+//   MN-major operand), rescaled in place only when the row max grows by more
+//   than 2^8; finally y = O / l and the row's log-sum-exp.
 // Backward, deterministic (no atomics):
 //   dQ kernel (one CTA per 128 queries, 2 CTAs/SM): D = rowsum(dO o O);
 //     S = Q K_j^T, dP = dO V_j^T; dS = P o (dP - D) with P from the saved
@@ -29,6 +25,10 @@
 //   dK/dV kernel (one CTA per 128 keys, 2 CTAs/SM): S^T = K Q_j^T,
 //     dP^T = V dO_j^T; P^T and dS^T; dV += P^T dO_j, dK += dS^T Q_j in TMEM
 //     (Q_j and dO_j, loaded K-major, are read again as MN-major operands).
+//
+// What bounds them: the row warps, by their own latencies (issue 43 to 47%, special
+// functions below a third); the MMAs take 34, 76 and 60% of the time at the rates
+// below.
 // Every wait is bounded (FLAG_TIMEOUT), as in the GEMM.
 //
 // GRP: the same kernels over groups of answers that share a prompt (group.cuh).
@@ -37,9 +37,9 @@
 // hold anything: a masked probability is 0, and 0 times a NaN is a NaN, so the
 // block in which the padding begins has its rows of the operand whose rows the
 // product sums over (V; K; Q and dO) cleared in shared memory.  Eight groups of 2048
-// positions (half of them the prompt, four answers), 12 heads: 96 us forward (400
-// TFLOP/s) and 374 backward (257); 16% of the blocks' pairs are masked, and by block
-// they run as the causal ones do (106 and 415 us for as many causal positions).
+// positions (half of them the prompt, four answers), 12 heads: 78 us forward (492
+// TFLOP/s) and 235 backward (409); 16% of the blocks' pairs are masked, and by block
+// they run as the causal ones do (85 and 255 us for as many causal positions).
 #include "tt_internal.h"
 #include "group.cuh"
 #include "tc_ptx.cuh"

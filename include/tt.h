@@ -65,7 +65,7 @@ typedef enum { TT_FP32 = 0, TT_BF16 = 1, TT_FP16 = 2 } tt_dtype;
  * (tt_gpt2_step_ex's loss_scale).  The half step runs on the SIMT kernels
  * (the tensor-core kernels are bf16).  tt_gpt2_eval takes it too; the
  * generating calls take TT_FP32 and TT_BF16 only, and so do the op-level calls
- * but those over lists of logits (tt_ops.h). */
+ * but those over lists of logits and of training on answers (tt_ops.h). */
 typedef struct {
     int L, C, H, V, maxT;
     tt_dtype dtype;
