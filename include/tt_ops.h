@@ -291,8 +291,10 @@ tt_status tt_op_group_attention_fwd(tt_ctx* ctx, tt_dtype dtype, const void* qkv
 
 /* Its backward: dqkv [B*T, 3C] is overwritten, with zeros in padded positions
  * (what dy and y hold there is not used).  A prompt's keys and values get the
- * gradients of all its answers, summed in a fixed order.  Scratch from the
- * arena: 4 B H T bytes. */
+ * gradients of all its answers, summed in a fixed order.  With 16-bit storage
+ * the probabilities and the scores' gradients are rounded to it for their
+ * products, in half beyond 65504 to infinity.  Scratch from the arena: 4 B H T
+ * bytes. */
 tt_status tt_op_group_attention_bwd(tt_ctx* ctx, tt_dtype dtype, const void* qkv, const int32_t* starts,
                                     const void* y, const float* lse, const void* dy, void* dqkv, int B, int T, int C,
                                     int H, int K);
