@@ -1,6 +1,5 @@
 // attn_group.cu -- attention over groups of answers that share a prompt
-// (group.cuh) in fp32, and the choice of the kernels: 16-bit heads of 64 take
-// attn_tc.cu's, of 16 and 32 attn_group_mma.cu's.
+// (group.cuh) in fp32, and the choice of the kernels: 16 bits take attn_tc.cu's.
 //
 //   k_group_fwd   64 queries a CTA past blocks of 64 keys: S = Q K^T / sqrt(D),
 //                 running maximum and sum, O += P V
@@ -476,11 +475,7 @@ bool launch_group_attention_fwd(const Launch& L, bool bf16, const void* qkv, con
                                 int B, int T, int C, int H, int K) {
     if (L.dry) return true;
     const int hd = C / H;
-    if (bf16 && hd == 64) return launch_attention_fwd_tc(L, qkv, y, lse, B, T, C, H, starts, K);
-    if (bf16) {
-        launch_group_fwd_mma(L, qkv, starts, y, lse, B, T, C, H, K);
-        return true;
-    }
+    if (bf16) return launch_attention_fwd_tc(L, qkv, y, lse, B, T, C, H, starts, K);
     const GroupArgs a = args_of(L, starts, B, T, C, H, K);
     const int ctas = a.tiles * B * H;
     const auto *q = (const float*)qkv;
@@ -501,7 +496,7 @@ bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, con
         return true;
     }
     if (bf16) {
-        launch_group_bwd_mma(L, qkv, starts, y, lse, dy, dqkv, B, T, C, H, K, scratch);
+        if (!launch_attention_bwd_tc(L, qkv, y, lse, dy, dqkv, B, T, C, H, scratch, nullptr, starts, K)) return false;
     } else {
         const GroupArgs a = args_of(L, starts, B, T, C, H, K);
         const int ctas = a.tiles * B * H;

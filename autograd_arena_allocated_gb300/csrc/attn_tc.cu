@@ -40,6 +40,12 @@
 // positions (half of them the prompt, four answers), 12 heads: 78 us forward (492
 // TFLOP/s) and 235 backward (409); 16% of the blocks' pairs are masked, and by block
 // they run as the causal ones do (85 and 255 us for as many causal positions).
+// HD (groups only): heads of 32 and 16 load the 64 columns that theirs are among.
+// Scores take the K steps of their own columns, the products into O, dQ, dK and dV
+// all 64, of which theirs are stored: an MMA costs the same at N = 16 and at 64, and
+// what bounds the kernels, the exponentials and their hand-overs, does not change.
+// Four groups of 1400, 16 heads of 32, half: 28 us forward and 74 backward (by
+// mma.sync, scores in registers, 57 and 173).
 #include "tt_internal.h"
 #include "group.cuh"
 #include "tc_ptx.cuh"
@@ -62,7 +68,9 @@ constexpr int T128 = 128 * 128;  // 128 rows x 128 bytes
 constexpr int T64 = 64 * 128;    // 64 rows x 128 bytes
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float SL2 = 0.125f * LOG2E;  // 1/sqrt(64), base-2 units
+// 1 / sqrt(head dim), and in base-2 units
+template <int HD> constexpr float SCALE = HD == 64 ? 0.125f : HD == 32 ? 0.17677669529663687f : 0.25f;
+template <int HD> constexpr float SCALE2 = SCALE<HD> * LOG2E;
 
 // Grid (band, tiles, bands): blockIdx.x is a (batch, head) pair within a band
 // of BAND pairs, y the tile (heaviest first), z the band.  The hardware hands
@@ -149,16 +157,14 @@ template <> struct KTile<true> : group::Group {
     __device__ __forceinline__ bool masked(int, int q0) const { return !(q0 >= last && q0 + BN <= min_end); }
 };
 
-// 64 columns at `col` of the rows first..last - 1 of a tile of padding, and its
-// column sums, where they are wanted (bpart: the tile's row of 3C)
+// A head's columns at `col` of the rows first..last - 1 of a tile of padding, and
+// their column sums, where they are wanted (bpart: the tile's row of 3C)
+template <int HD>
 __device__ __forceinline__ void clear_padding(bf16* dqkv, int row0, int first, int last, int C, int col, float* bpart) {
-    for (int i = first * 8 + (int)threadIdx.x; i < last * 8; i += blockDim.x)
-        reinterpret_cast<uint4*>(dqkv + (long long)(row0 + (i >> 3)) * 3 * C + col)[i & 7] = make_uint4(0, 0, 0, 0);
-    if (bpart && threadIdx.x < D) bpart[col + threadIdx.x] = 0.0f;
-}
-__device__ __forceinline__ void zero_out32(bf16* dst) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+    constexpr int G = HD / 8;
+    for (int i = first * G + (int)threadIdx.x; i < last * G; i += blockDim.x)
+        reinterpret_cast<uint4*>(dqkv + (long long)(row0 + i / G) * 3 * C + col)[i % G] = make_uint4(0, 0, 0, 0);
+    if (bpart && threadIdx.x < HD) bpart[col + threadIdx.x] = 0.0f;
 }
 
 // the rows from `from` on of a 64-row tile are cleared by `threads` threads
@@ -170,15 +176,30 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int tid, int
 // 64-wide bf16 operand written as two 16-column halves 32 columns apart
 __device__ __forceinline__ uint32_t split_a_col(int k) { return (uint32_t)(8 * k + (k >= 2 ? 16 : 0)); }
 
-template <bool F16>
-__device__ __forceinline__ void store_out32(bf16* dst, const uint32_t (&w)[32], float scale) {
+// N columns of an output row
+template <bool F16, int N>
+__device__ __forceinline__ void store_out(bf16* dst, const uint32_t (&w)[N], float scale) {
     uint4* o = reinterpret_cast<uint4*>(dst);
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < N / 8; i++)
         o[i] = make_uint4(pack2<F16>(__uint_as_float(w[8 * i]) * scale, __uint_as_float(w[8 * i + 1]) * scale),
                           pack2<F16>(__uint_as_float(w[8 * i + 2]) * scale, __uint_as_float(w[8 * i + 3]) * scale),
                           pack2<F16>(__uint_as_float(w[8 * i + 4]) * scale, __uint_as_float(w[8 * i + 5]) * scale),
                           pack2<F16>(__uint_as_float(w[8 * i + 6]) * scale, __uint_as_float(w[8 * i + 7]) * scale));
+}
+template <int N> __device__ __forceinline__ void zero_out(bf16* dst) {
+#pragma unroll
+    for (int i = 0; i < N / 8; i++) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 // One arrival per warp: every lane has passed its own fences (the caller's
@@ -201,7 +222,7 @@ constexpr int F_BAR = F_V + T64;
 constexpr int F_SMEM = F_BAR + 256 + 1024;
 constexpr uint32_t F_TMEM = 128;    // S, P: cols 0..63, O: 64..127
 
-template <bool F16, bool GRP>
+template <bool F16, bool GRP, int HD>
 __global__ void __launch_bounds__(THREADS, 4)
 k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
               bf16* __restrict__ y, float* __restrict__ lse, int T, int C, int H, int nbh, int* flags,
@@ -227,6 +248,9 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     const int qt = nqt - 1 - (int)blockIdx.y;  // longest rows first within the band
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
+    // the head's columns, the 64 that are loaded, its place among them
+    const int hc = h * HD, hx = hc & ~63, co = HD == 64 ? 0 : hc & 63;
+    constexpr float SL2 = SCALE2<HD>;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (GRP) pdl_enter();  // the lists of starts are read from here on
     const Tile<GRP> tile(starts, b, K, T, qt);
@@ -234,8 +258,9 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         if (qt == 0 && h == 0) tile.check(threadIdx.x, THREADS, T, flags);
         if (tile.end <= qt * BQ) {  // padding only (uniform over the CTA)
             const int last = min(qt * BQ + BQ, T);
-            for (int i = qt * BQ * 8 + threadIdx.x; i < last * 8; i += THREADS)
-                reinterpret_cast<uint4*>(y + (long long)(row0 + (i >> 3)) * C + h * D)[i & 7] = make_uint4(0, 0, 0, 0);
+            constexpr int G = HD / 8;
+            for (int i = qt * BQ * G + threadIdx.x; i < last * G; i += THREADS)
+                reinterpret_cast<uint4*>(y + (long long)(row0 + i / G) * C + hc)[i % G] = make_uint4(0, 0, 0, 0);
             for (int q = qt * BQ + threadIdx.x; q < last; q += THREADS) lse[((long long)b * H + h) * T + q] = 0.0f;
             return;
         }
@@ -266,7 +291,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
 
     if (warp == 0) {
         if (elect_one()) {
-            const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
+            const int xq = hx, xk = C + hx, xv = 2 * C + hx;
             mbar_expect_tx(q_full, T128);
             tma_load_2d(smem_u32(sm + F_Q), &tq, q_full, xq, row0 + qt * BQ);
             // K runs two blocks ahead of V: K_{j+2} needs only S_j done, while
@@ -300,7 +325,8 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_O = idesc16<F16>(BQ, D, false, true);
-            const uint64_t dq = kmajor(smem_u32(sm + F_Q)), dv = mnmajor(smem_u32(sm + F_V)), dk = kmajor(smem_u32(sm + F_K));
+            const uint64_t dq = kmajor(smem_u32(sm + F_Q) + 2 * co), dv = mnmajor(smem_u32(sm + F_V)),
+                           dk = kmajor(smem_u32(sm + F_K) + 2 * co);
             bool ok = mbar_wait(q_full, 0, abort_flag, flags, 0x100 + 3, wl);
             bool issued = false;
             auto issue_s = [&](int j) -> bool {  // overwrites P_{j-1}, read by MMAs issued before
@@ -309,7 +335,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
                 tc_fence_after();
                 const uint64_t dks = dk + st * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) umma_bf16(tmem, dq + 2 * k, dks + 2 * k, ID, k > 0);
+                for (int k = 0; k < HD / 16; k++) umma_bf16(tmem, dq + 2 * k, dks + 2 * k, ID, k > 0);
                 issued = true;
                 umma_commit(s_full);
                 umma_commit(&k_empty[st]);
@@ -439,13 +465,14 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             tc_fence_after();
             const bool none = GRP && q >= tile.end;
             if (none) m = 0.0f, l = 1.0f;
-            bf16* out = y + (long long)(row0 + q) * C + h * D;
+            bf16* out = y + (long long)(row0 + q) * C + hc;
+            constexpr int N = HD < 32 ? HD : 32;
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                uint32_t v[32];
-                tmem_ld32(tl + BN + 32 * c, v);
-                if (none && q < T) zero_out32(out + 32 * c);
-                else if (q < T) store_out32<F16>(out + 32 * c, v, 1.0f / l);
+            for (int c = 0; c < HD; c += N) {
+                uint32_t v[N];
+                tmem_ld_cols(tl + BN + co + c, v);
+                if (none && q < T) zero_out<N>(out + c);
+                else if (q < T) store_out<F16, N>(out + c, v, 1.0f / l);
             }
             if (q < T) {
                 lse[((long long)b * H + h) * T + q] = (m + log2f(l)) * LN2;
@@ -517,7 +544,7 @@ constexpr int Q_SMEM = Q_BAR + 256 + 1024;
 constexpr uint32_t Q_TMEM = 256;         // S 0..63, dP 64..127, dS[2] 128..191, dQ 192..255
 constexpr uint32_t Q_TS = 0, Q_TP = 64, Q_TDS = 128, Q_TACC = 192;
 
-template <bool F16, bool GRP>
+template <bool F16, bool GRP, int HD>
 __global__ void __launch_bounds__(BW_THREADS, 2)
 k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap to, const bf16* __restrict__ y,
@@ -546,13 +573,16 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     const int qt = nqt - 1 - (int)blockIdx.y;  // longest rows first within the band
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
+    // the head's columns, the 64 that are loaded, its place among them
+    const int hc = h * HD, hx = hc & ~63, co = HD == 64 ? 0 : hc & 63;
+    constexpr float SL2 = SCALE2<HD>;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (GRP) pdl_enter();
     const Tile<GRP> tile(starts, b, K, T, qt);
     if (GRP) {
         if (qt == 0 && h == 0) tile.check(threadIdx.x, BW_THREADS, T, flags);
         if (tile.end <= qt * BQ) {
-            clear_padding(dqkv, row0, qt * BQ, min(qt * BQ + BQ, T), C, h * D,
+            clear_padding<HD>(dqkv, row0, qt * BQ, min(qt * BQ + BQ, T), C, hc,
                           bpart ? bpart + ((long long)b * nqt + qt) * 3 * C : nullptr);
             return;
         }
@@ -586,10 +616,10 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
 
     if (warp == 0) {
         if (elect_one()) {
-            const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
+            const int xq = hx, xk = C + hx, xv = 2 * C + hx;
             mbar_expect_tx(qo_full, 2 * T128);
             tma_load_2d(smem_u32(sm + Q_Q), &tq, qo_full, xq, row0 + qt * BQ);
-            tma_load_2d(smem_u32(sm + Q_O), &to, qo_full, h * D, row0 + qt * BQ);
+            tma_load_2d(smem_u32(sm + Q_O), &to, qo_full, hx, row0 + qt * BQ);
             int issued_k = 0, issued_v = 0;
             bool ok = true;
             for (int j = 0; j < nkv; j++) {
@@ -616,8 +646,9 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_Q = idesc16<F16>(BQ, D, false, true);
-            const uint64_t dq = kmajor(smem_u32(sm + Q_Q)), dout = kmajor(smem_u32(sm + Q_O)), dk = kmajor(smem_u32(sm + Q_K)),
-                           dkt = mnmajor(smem_u32(sm + Q_K)), dv = kmajor(smem_u32(sm + Q_V));
+            const uint64_t dq = kmajor(smem_u32(sm + Q_Q) + 2 * co), dout = kmajor(smem_u32(sm + Q_O) + 2 * co),
+                           dk = kmajor(smem_u32(sm + Q_K) + 2 * co), dkt = mnmajor(smem_u32(sm + Q_K)),
+                           dv = kmajor(smem_u32(sm + Q_V) + 2 * co);
             bool ok = mbar_wait(qo_full, 0, abort_flag, flags, 0x200 + 2, wl);
             bool issued = false;
             // dQ += dS_j K_j: dS from tensor-memory buffer j & 1, K_j read MN-major
@@ -638,7 +669,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                 tc_fence_after();
                 const uint64_t dks = dk + ks * DESC_T64, dvs = dv + vs * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
+                for (int k = 0; k < HD / 16; k++) {
                     umma_bf16(tmem + Q_TS, dq + 2 * k, dks + 2 * k, ID, k > 0);
                     umma_bf16(tmem + Q_TP, dout + 2 * k, dvs + 2 * k, ID, k > 0);
                 }
@@ -672,17 +703,17 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         const long long bhl = (long long)b * H + h;
         float* dpart = reinterpret_cast<float*>(sm + Q_DP);
         bool ok = mbar_wait_warp(qo_full, 0, abort_flag, flags, 0x200 + 6, wl);
-        // This thread's half of D = rowsum(dO o O) (16-byte chunks 4 half ..
-        // 4 half + 3 of the swizzled dO row); the two halves meet in shared memory.
+        // This thread's half of D = rowsum(dO o O) (half of the head's 16-byte
+        // chunks of the swizzled dO row); the two halves meet in shared memory.
         float Dq = 0.0f;
         if (ok) {
             const uint8_t* orow = sm + Q_O + r * 128;
             float part = 0.0f;
             if (qv) {
-                const uint4* yr = reinterpret_cast<const uint4*>(y + (long long)(row0 + q) * C + h * D + 32 * half);
+                const uint4* yr = reinterpret_cast<const uint4*>(y + (long long)(row0 + q) * C + hc + HD / 2 * half);
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(orow + (((4 * half + c) ^ (r & 7)) << 4));
+                for (int c = 0; c < HD / 16; c++) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(orow + (((co / 8 + HD / 16 * half + c) ^ (r & 7)) << 4));
                     const uint4 bb = yr[c];
                     const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
                     const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
@@ -749,19 +780,24 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         for (int d = 0; d < 32; d++) cv[d] = 0.0f;
         if (ok && mbar_wait_warp(acc_full, 0, abort_flag, flags, 0x200 + 9, wl)) {
             tc_fence_after();
-            uint32_t w[32];
-            tmem_ld32(tl + Q_TACC + 32 * half, w);
-            if (qv) {
-                store_out32<F16>(dqkv + (long long)(row0 + q) * 3 * C + h * D + 32 * half, w, 0.125f);
+            // half the head's columns a thread, or, narrow heads, all of them by the first half
+            constexpr int N = HD < 32 ? HD : 32;
+            uint32_t w[N];
+            if (HD == 64 || half == 0) {
+                tmem_ld_cols(tl + Q_TACC + co + 32 * half, w);
+                bf16* out = dqkv + (long long)(row0 + q) * 3 * C + hc + 32 * half;
+                if (qv) {
+                    store_out<F16, N>(out, w, SCALE<HD>);
 #pragma unroll
-                for (int d = 0; d < 32; d++) cv[d] = __uint_as_float(w[d]) * 0.125f;
-            } else if (GRP && q < T) {
-                zero_out32(dqkv + (long long)(row0 + q) * 3 * C + h * D + 32 * half);
+                    for (int d = 0; d < N; d++) cv[d] = __uint_as_float(w[d]) * SCALE<HD>;
+                } else if (GRP && q < T) {
+                    zero_out<N>(out);
+                }
             }
         }
         if (bpart)  // the qkv bias gradient's partial: this tile's column sums of dQ
             tile_colsum(cv, reinterpret_cast<float*>(sm + Q_CS),
-                        bpart + ((long long)b * nqt + qt) * 3 * C + h * D + 32 * half, half, quarter, lane);
+                        bpart + ((long long)b * nqt + qt) * 3 * C + hc + 32 * half, half, quarter, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -789,7 +825,7 @@ constexpr int K_SMEM = K_BAR + 256 + 1024;
 constexpr uint32_t K_TMEM = 256;         // S^T 0..63, dP^T 64..127, dV 128..191, dK 192..255
 constexpr uint32_t K_TS = 0, K_TP = 64, K_TV = 128, K_TK = 192;
 
-template <bool F16, bool GRP>
+template <bool F16, bool GRP, int HD>
 __global__ void __launch_bounds__(BW_THREADS, 2)
 k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap to, const float* __restrict__ lse,
@@ -815,13 +851,16 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const int kt = (int)blockIdx.y;  // key tile; low tiles see the most query blocks
     const int b = bh / H, h = bh % H;
     const int row0 = b * T;
+    // the head's columns, the 64 that are loaded, its place among them
+    const int hc = h * HD, hx = hc & ~63, co = HD == 64 ? 0 : hc & 63;
+    constexpr float SL2 = SCALE2<HD>;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (GRP) pdl_enter();
     const KTile<GRP> tile(starts, b, K, T, kt);
     if (GRP && tile.end <= kt * BQ) {
         float* brow = bpart ? bpart + ((long long)b * gridDim.y + kt) * 3 * C : nullptr;
-        clear_padding(dqkv, row0, kt * BQ, min(kt * BQ + BQ, T), C, C + h * D, brow);
-        clear_padding(dqkv, row0, kt * BQ, min(kt * BQ + BQ, T), C, 2 * C + h * D, brow);
+        clear_padding<HD>(dqkv, row0, kt * BQ, min(kt * BQ + BQ, T), C, C + hc, brow);
+        clear_padding<HD>(dqkv, row0, kt * BQ, min(kt * BQ + BQ, T), C, 2 * C + hc, brow);
         return;
     }
     const int j0 = 2 * kt;
@@ -853,7 +892,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // The whole warp: one lane starts the copies, all of them bring the block's
         // log-sum-exps and Ds, negated (the rows' packed fma and add take them as
         // addends), so that the row warps, which everything waits for, do not.
-        const int xq = h * D, xk = C + h * D, xv = 2 * C + h * D;
+        const int xq = hx, xk = C + hx, xv = 2 * C + hx;
         const long long bhl = (long long)b * H + h;
         if (elect_one()) {
             mbar_expect_tx(kv_full, 2 * T128);
@@ -875,7 +914,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (elect_one()) {
                 mbar_expect_tx(&qo_full[st], 2 * T64);
                 tma_load_2d(smem_u32(sm + K_Q + st * T64), &tk, &qo_full[st], xq, row0 + j * BN);
-                tma_load_2d(smem_u32(sm + K_O + st * T64), &to, &qo_full[st], h * D, row0 + j * BN);
+                tma_load_2d(smem_u32(sm + K_O + st * T64), &to, &qo_full[st], hx, row0 + j * BN);
             }
             ++issued;
             float* ld = reinterpret_cast<float*>(sm + K_LD) + st * 128;
@@ -896,9 +935,9 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (elect_one()) {
             constexpr uint32_t ID = idesc16<F16>(BQ, BN, false, false);
             constexpr uint32_t ID_A = idesc16<F16>(BQ, D, false, true);
-            const uint64_t dk = kmajor(smem_u32(sm + K_K)), dv = kmajor(smem_u32(sm + K_V));
-            const uint64_t dq = kmajor(smem_u32(sm + K_Q)), dqt = mnmajor(smem_u32(sm + K_Q));
-            const uint64_t dout = kmajor(smem_u32(sm + K_O)), doutt = mnmajor(smem_u32(sm + K_O));
+            const uint64_t dk = kmajor(smem_u32(sm + K_K) + 2 * co), dv = kmajor(smem_u32(sm + K_V) + 2 * co);
+            const uint64_t dq = kmajor(smem_u32(sm + K_Q) + 2 * co), dqt = mnmajor(smem_u32(sm + K_Q));
+            const uint64_t dout = kmajor(smem_u32(sm + K_O) + 2 * co), doutt = mnmajor(smem_u32(sm + K_O));
             bool ok = mbar_wait(kv_full, 0, abort_flag, flags, 0x300 + 2, wl);
             bool issued = false;
             auto issue_s = [&](int i, int st) {  // overwrites P^T_{i-1}, read by MMAs issued before
@@ -906,7 +945,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
                 tc_fence_after();
                 const uint64_t ds = dq + st * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) umma_bf16(tmem + K_TS, dk + 2 * k, ds + 2 * k, ID, k > 0);
+                for (int k = 0; k < HD / 16; k++) umma_bf16(tmem + K_TS, dk + 2 * k, ds + 2 * k, ID, k > 0);
                 issued = true;
                 umma_commit(s_full);
                 return true;
@@ -914,7 +953,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
             auto issue_dp = [&](int st) {  // overwrites dS^T_{i-1} likewise
                 const uint64_t ds = dout + st * DESC_T64;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) umma_bf16(tmem + K_TP, dv + 2 * k, ds + 2 * k, ID, k > 0);
+                for (int k = 0; k < HD / 16; k++) umma_bf16(tmem + K_TP, dv + 2 * k, ds + 2 * k, ID, k > 0);
                 umma_commit(dp_full);
             };
             ok = ok && issue_s(0, 0);
@@ -1024,24 +1063,25 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         const bool got = ok && mbar_wait_warp(acc_full, 0, abort_flag, flags, 0x300 + 8, wl);
         if (got) tc_fence_after();
-        bf16* base = dqkv + (long long)(row0 + key) * 3 * C + h * D + 32 * half;
+        bf16* base = dqkv + (long long)(row0 + key) * 3 * C + hc + 32 * half;
         // the qkv bias gradient's partials: this tile's column sums of dV, then dK
-        float* brow = bpart ? bpart + ((long long)b * gridDim.y + kt) * 3 * C + h * D + 32 * half : nullptr;
+        float* brow = bpart ? bpart + ((long long)b * gridDim.y + kt) * 3 * C + hc + 32 * half : nullptr;
 #pragma unroll 1
         for (int which = 0; which < 2; which++) {  // 0: dV, 1: dK (times 1/sqrt(64))
-            const float scale = which ? 0.125f : 1.0f;
+            const float scale = which ? SCALE<HD> : 1.0f;
             float v[32];
 #pragma unroll
             for (int d = 0; d < 32; d++) v[d] = 0.0f;
-            if (got) {
-                uint32_t w[32];
-                tmem_ld32(tl + (which ? K_TK : K_TV) + 32 * half, w);
+            if (got && (HD == 64 || half == 0)) {
+                constexpr int N = HD < 32 ? HD : 32;
+                uint32_t w[N];
+                tmem_ld_cols(tl + (which ? K_TK : K_TV) + co + 32 * half, w);
                 if (key < tile.end) {
-                    store_out32<F16>(base + (which ? C : 2 * C), w, scale);
+                    store_out<F16, N>(base + (which ? C : 2 * C), w, scale);
 #pragma unroll
-                    for (int d = 0; d < 32; d++) v[d] = __uint_as_float(w[d]) * scale;
+                    for (int d = 0; d < N; d++) v[d] = __uint_as_float(w[d]) * scale;
                 } else if (GRP && key < T) {
-                    zero_out32(base + (which ? C : 2 * C));
+                    zero_out<N>(base + (which ? C : 2 * C));
                 }
             }
             if (brow) tile_colsum(v, reinterpret_cast<float*>(sm + K_CS), brow + (which ? C : 2 * C), half, quarter, lane);
@@ -1060,15 +1100,15 @@ bool attention_tc_eligible(bool bf16, int C, int H) {
     return bf16 && H > 0 && C % H == 0 && C / H == fa5::D && C % 8 == 0;
 }
 
-template <bool F16, bool GRP>
+template <bool F16, bool GRP, int HD>
 static bool attn_set_smem() {
     static PerDevice done;
     return done.once([] {
-        return cudaFuncSetAttribute(fa5::k_attn_fwd_tc<F16, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa5::k_attn_fwd_tc<F16, GRP, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     fa5::F_SMEM) == cudaSuccess &&
-               cudaFuncSetAttribute(fa5::k_attn_bwd_dq_tc<F16, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+               cudaFuncSetAttribute(fa5::k_attn_bwd_dq_tc<F16, GRP, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     fa5::Q_SMEM) == cudaSuccess &&
-               cudaFuncSetAttribute(fa5::k_attn_bwd_dkdv_tc<F16, GRP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+               cudaFuncSetAttribute(fa5::k_attn_bwd_dkdv_tc<F16, GRP, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     fa5::K_SMEM) == cudaSuccess;
     });
 }
@@ -1079,21 +1119,21 @@ static dim3 attn_grid(int bh, int tiles) {
 }
 
 // starts [B, K + 1] (GRP): the groups
-template <bool F16, bool GRP>
+template <bool F16, bool GRP, int HD>
 static bool attn_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T, int C, int H,
                         const int32_t* starts, int K) {
     CUtensorMap tq, tk;
     if (!tc::make_tmap_bf16(&tq, qkv, 3LL * C, (long long)B * T, 3LL * C, fa5::D, fa5::BQ)) return false;
     if (!tc::make_tmap_bf16(&tk, qkv, 3LL * C, (long long)B * T, 3LL * C, fa5::D, fa5::BN)) return false;
-    if (!attn_set_smem<F16, GRP>()) return false;
+    if (!attn_set_smem<F16, GRP, HD>()) return false;
     const dim3 grid = attn_grid(B * H, (T + fa5::BQ - 1) / fa5::BQ);
     L.count();
-    launch_k(L, fa5::k_attn_fwd_tc<F16, GRP>, dim3(grid), dim3(fa5::THREADS), fa5::F_SMEM, tq, tk, (fa5::bf16*)y, lse, T,
+    launch_k(L, fa5::k_attn_fwd_tc<F16, GRP, HD>, dim3(grid), dim3(fa5::THREADS), fa5::F_SMEM, tq, tk, (fa5::bf16*)y, lse, T,
              C, H, B * H, L.flags, L.wait_cycles, starts, K);
     return true;
 }
 
-template <bool F16, bool GRP>
+template <bool F16, bool GRP, int HD>
 static bool attn_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse, const void* dy,
                         void* dqkv, int B, int T, int C, int H, float* Dlt, float* bpart, const int32_t* starts, int K) {
     // the maps only move 16-bit elements (no conversion), for bf16 and half alike
@@ -1104,35 +1144,42 @@ static bool attn_bwd_tc(const Launch& L, const void* qkv, const void* y, const f
         return false;
     if (!tc::make_tmap_bf16(&to64, dy, (long long)C, (long long)B * T, (long long)C, fa5::D, fa5::BN))
         return false;
-    if (!attn_set_smem<F16, GRP>()) return false;
+    if (!attn_set_smem<F16, GRP, HD>()) return false;
     const dim3 grid = attn_grid(B * H, (T + fa5::BQ - 1) / fa5::BQ);
     L.count();
-    launch_k(L, fa5::k_attn_bwd_dq_tc<F16, GRP>, dim3(grid), dim3(fa5::BW_THREADS), fa5::Q_SMEM, tq, tk, to128,
+    launch_k(L, fa5::k_attn_bwd_dq_tc<F16, GRP, HD>, dim3(grid), dim3(fa5::BW_THREADS), fa5::Q_SMEM, tq, tk, to128,
              (const fa5::bf16*)y, lse, Dlt, (fa5::bf16*)dqkv, bpart, T, C, H, B * H, L.flags, L.wait_cycles, starts, K);
     L.count();
-    launch_k(L, fa5::k_attn_bwd_dkdv_tc<F16, GRP>, dim3(grid), dim3(fa5::BW_THREADS), fa5::K_SMEM, tq, tk, to64, lse,
+    launch_k(L, fa5::k_attn_bwd_dkdv_tc<F16, GRP, HD>, dim3(grid), dim3(fa5::BW_THREADS), fa5::K_SMEM, tq, tk, to64, lse,
              Dlt, (fa5::bf16*)dqkv, bpart, T, C, H, B * H, L.flags, L.wait_cycles, starts, K);
     return true;
+}
+
+// the form by storage, by groups and, over those, by the head's width
+template <typename F>
+static bool attn_form(const Launch& L, bool groups, int hd, F&& f) {
+    using std::integral_constant;
+    auto by_type = [&](auto grp, auto width) { return L.f16 ? f(std::true_type{}, grp, width) : f(std::false_type{}, grp, width); };
+    if (!groups) return by_type(std::false_type{}, integral_constant<int, 64>{});
+    if (hd == 64) return by_type(std::true_type{}, integral_constant<int, 64>{});
+    if (hd == 32) return by_type(std::true_type{}, integral_constant<int, 32>{});
+    return by_type(std::true_type{}, integral_constant<int, 16>{});
 }
 
 bool launch_attention_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T, int C, int H,
                              const int32_t* starts, int K) {
     if (L.dry) return true;
-    if (starts)
-        return L.f16 ? attn_fwd_tc<true, true>(L, qkv, y, lse, B, T, C, H, starts, K)
-                     : attn_fwd_tc<false, true>(L, qkv, y, lse, B, T, C, H, starts, K);
-    return L.f16 ? attn_fwd_tc<true, false>(L, qkv, y, lse, B, T, C, H, nullptr, 0)
-                 : attn_fwd_tc<false, false>(L, qkv, y, lse, B, T, C, H, nullptr, 0);
+    return attn_form(L, starts != nullptr, C / H, [&](auto f16, auto grp, auto hd) {
+        return attn_fwd_tc<f16.value, grp.value, hd.value>(L, qkv, y, lse, B, T, C, H, starts, K);
+    });
 }
 
 bool launch_attention_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse, const void* dy, void* dqkv,
                              int B, int T, int C, int H, float* Dlt, float* bpart, const int32_t* starts, int K) {
     if (L.dry) return true;
-    if (starts)
-        return L.f16 ? attn_bwd_tc<true, true>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, starts, K)
-                     : attn_bwd_tc<false, true>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, starts, K);
-    return L.f16 ? attn_bwd_tc<true, false>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, nullptr, 0)
-                 : attn_bwd_tc<false, false>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, nullptr, 0);
+    return attn_form(L, starts != nullptr, C / H, [&](auto f16, auto grp, auto hd) {
+        return attn_bwd_tc<f16.value, grp.value, hd.value>(L, qkv, y, lse, dy, dqkv, B, T, C, H, Dlt, bpart, starts, K);
+    });
 }
 
 }  // namespace tt

@@ -238,10 +238,11 @@ bool launch_embed_chunks(const Launch& L, bool bf16, const void* dx, const int32
 
 // tcgen05 attention (attn_tc.cu); false = not taken (then the mma.sync path runs)
 bool attention_tc_eligible(bool bf16, int C, int H);
-// starts [B, K + 1]: groups of answers that share a prompt (group.cuh); NULL: causal
+// starts [B, K + 1]: groups of answers that share a prompt (group.cuh), heads of 16,
+// 32 and 64; NULL: causal, heads of 64
 bool launch_attention_fwd_tc(const Launch& L, const void* qkv, void* y, float* lse, int B, int T,
                              int C, int H, const int32_t* starts = nullptr, int K = 0);
-// bpart (may be NULL): per (sequence, 128-row tile) row of 3C column sums of
+// bpart (may be NULL, heads of 64): per (sequence, 128-row tile) row of 3C column sums of
 // dqkv over the tile's rows (the qkv bias gradient's partials)
 bool launch_attention_bwd_tc(const Launch& L, const void* qkv, const void* y, const float* lse,
                              const void* dy, void* dqkv, int B, int T, int C, int H, float* Dlt,
@@ -256,11 +257,6 @@ bool launch_group_attention_fwd(const Launch& L, bool bf16, const void* qkv, con
 bool launch_group_attention_bwd(const Launch& L, bool bf16, const void* qkv, const int32_t* starts, const void* y,
                                 const float* lse, const void* dy, void* dqkv, int B, int T, int C, int H, int K,
                                 float* scratch, float* dbias = nullptr, bool acc_bias = false);
-// its 16-bit heads of 16 and 32 (attn_group_mma.cu)
-void launch_group_fwd_mma(const Launch& L, const void* qkv, const int32_t* starts, void* y, float* lse, int B, int T, int C,
-                          int H, int K);
-void launch_group_bwd_mma(const Launch& L, const void* qkv, const int32_t* starts, const void* y, const float* lse,
-                          const void* dy, void* dqkv, int B, int T, int C, int H, int K, float* Dlt);
 
 // decoding with a key/value cache (decode.cu); cache per layer [B, maxT, 2C].
 // The decode-step kernels read the newest position from device memory

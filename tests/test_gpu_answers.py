@@ -821,6 +821,23 @@ def test_group_attention_of_many_heads(ctx, dtype, D):
     check_group(ctx, dtype, [[20 + 20 * b, 100, 140 + b, 150] for b in range(B)], 151, H * D, H, seed=93)
 
 
+@pytest.mark.parametrize("dtype,H,D", [("bf16", 1, 16), ("fp16", 1, 32), ("bf16", 5, 16), ("fp16", 3, 32), ("bf16", 6, 16), ("fp32", 1, 16)])
+def test_group_attention_of_widths_beside_64(ctx, dtype, H, D):
+    """Channels that 64 does not divide, one narrow head alone among them; a NaN in another head's columns stays there."""
+    T, starts, C = 200, [[60, 100, 190], [0, 70, 200], [130, 130, 131]], H * D
+    y, lse, d = check_group(ctx, dtype, starts, T, C, H, seed=99)
+    if H == 1:
+        return
+    qkv, st = group_case(dtype, starts, T, C, 99)
+    qkv.view(-1, 3, H, D)[:, :, H - 1] = math.nan
+    y2, l2 = run_group_fwd(ctx, dtype, qkv, st, T, C, H)
+    own = slice(0, (H - 1) * D)
+    assert torch.equal(y2[:, own], y[:, own]) and torch.equal(l2[:, :H - 1], lse[:, :H - 1])
+    dy = torch.randn(y.shape, generator=gen(100), device=DEV).to(TYPES[dtype])
+    d2 = run_group_bwd(ctx, dtype, qkv, st, y2, l2, dy, T, C, H)
+    assert torch.equal(d2.view(-1, 3, C)[:, :, own], d.view(-1, 3, C)[:, :, own])
+
+
 @pytest.mark.parametrize("dtype,D,spread", [("bf16", 16, 5.0), ("fp16", 32, 4.0), ("fp32", 16, 5.0), ("fp32", 32, 0.0)])
 def test_narrow_heads_of_sharp_and_flat_scores(ctx, dtype, D, spread):
     check_group(ctx, dtype, [[100, 180, 290], [0, 150, 300]], 300, 2 * D, 2, seed=94, spread=spread)
