@@ -366,7 +366,9 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
         // P is taken relative to a reference max m that is raised -- and O, l
         // rescaled in place -- only when some row of the warp exceeds it by
         // more than 8 (P <= 2^8 otherwise); the decision is a warp vote since
-        // the TMEM loads and stores of O are warp-collective
+        // the TMEM loads and stores of O are warp-collective.  Rows that are no
+        // result (padding, and the next sequence's rows in a tile that runs past
+        // its own) have no vote: the rows beside them would be rounded otherwise
         // (GRP: a row may see nothing of its first blocks; m then starts below
         // any score, but finite, so that no difference is infinity minus infinity)
         float m = GRP ? -3e38f : -INFINITY, l = 0.0f;
@@ -401,7 +403,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
             }
             const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
             const float mn = fmaxf(m, mx * SL2);
-            const bool rescale = j > 0 && __any_sync(0xffffffffu, mn > m + 8.0f);
+            const bool rescale = j > 0 && __any_sync(0xffffffffu, q < tile.end && mn > m + 8.0f);
             const float m_old = m;
             if (j == 0 || rescale) m = mn;
             // P = 2^(s*scale - m) as bf16, each 32-column half over its scores
