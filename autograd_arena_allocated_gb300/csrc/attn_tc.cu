@@ -92,6 +92,16 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The next kernel may start once every CTA of this one has its tensor memory: a CTA
+// of the next that takes tensor memory and then waits for this kernel's end would
+// otherwise hold what this one still needs.  Causal, the set-up overlaps the previous
+// kernel's end, and global memory is touched only from here on; groups have waited at
+// the top, for their lists.
+template <bool GRP> __device__ __forceinline__ void enter_after_setup() {
+    if (GRP) pdl_trigger();
+    else pdl_enter();
+}
+
 __device__ __forceinline__ void init_done() {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -252,7 +262,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     const int hc = h * HD, hx = hc & ~63, co = HD == 64 ? 0 : hc & 63;
     constexpr float SL2 = SCALE2<HD>;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (GRP) pdl_enter();  // the lists of starts are read from here on
+    if (GRP) pdl_wait();  // the lists of starts are read from here on
     const Tile<GRP> tile(starts, b, K, T, qt);
     if (GRP) {
         if (qt == 0 && h == 0) tile.check(threadIdx.x, THREADS, T, flags);
@@ -287,7 +297,7 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_holder);
-    if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
+    enter_after_setup<GRP>();
 
     if (warp == 0) {
         if (elect_one()) {
@@ -579,7 +589,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     const int hc = h * HD, hx = hc & ~63, co = HD == 64 ? 0 : hc & 63;
     constexpr float SL2 = SCALE2<HD>;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (GRP) pdl_enter();
+    if (GRP) pdl_wait();
     const Tile<GRP> tile(starts, b, K, T, qt);
     if (GRP) {
         if (qt == 0 && h == 0) tile.check(threadIdx.x, BW_THREADS, T, flags);
@@ -614,7 +624,7 @@ k_attn_bwd_dq_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_holder);
-    if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
+    enter_after_setup<GRP>();
 
     if (warp == 0) {
         if (elect_one()) {
@@ -857,7 +867,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const int hc = h * HD, hx = hc & ~63, co = HD == 64 ? 0 : hc & 63;
     constexpr float SL2 = SCALE2<HD>;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (GRP) pdl_enter();
+    if (GRP) pdl_wait();
     const KTile<GRP> tile(starts, b, K, T, kt);
     if (GRP && tile.end <= kt * BQ) {
         float* brow = bpart ? bpart + ((long long)b * gridDim.y + kt) * 3 * C : nullptr;
@@ -888,7 +898,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_holder);
-    if (!GRP) pdl_enter();  // the set-up above overlaps the previous kernel's end; global memory only from here
+    enter_after_setup<GRP>();
 
     if (warp == 0) {
         // The whole warp: one lane starts the copies, all of them bring the block's
