@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(2 * PAIR_THREADS) k_pairs(const PairArgs a) {
     __shared__ bool s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = tid / PAIR_THREADS;
     const long long pair = blockIdx.x;
-    int first = a.spans[(2 * pair + w) * 2], last = a.spans[(2 * pair + w) * 2 + 1];
+    // (64 bits: a row behind the last, by a thread's number, may be past 2^31)
+    long long first = a.spans[(2 * pair + w) * 2], last = a.spans[(2 * pair + w) * 2 + 1];
     bool bad = false;
     if (first < 0 || first > last || last > a.M) {
         bad = true;

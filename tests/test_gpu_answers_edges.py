@@ -49,3 +49,34 @@ def test_the_next_sequence_moves_no_bit_of_causal_attention(ctx, T):
         out.append((y[:T], lse[0], d[:T]))
     for alone, beside in zip(*out):
         assert torch.equal(alone, beside)
+
+
+def test_pairs_at_the_last_rows(ctx):
+    """2^31 - 1 rows: answers that begin and end at the last of them, empty ones among them.  With two columns of
+    equal logits every log probability is -ln 2, the gradient +-k / 2."""
+    M, V = 2 ** 31 - 1, 2
+    z = torch.zeros(M, V, dtype=torch.bfloat16, device=DEV)
+    t = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    t[:5] = 0
+    t[-300:] = 1
+    spans = torch.tensor([[M - 300, M - 100], [M - 100, M], [0, 5], [M, M], [M, M], [M, M]], dtype=torch.int32, device=DEV)
+    seq, pair, mean = torch.empty(6, device=DEV), torch.empty(3, device=DEV), torch.empty(1, device=DEV)
+    big = api.Context(20 * M + (1 << 20))
+    big.preference("bf16", z, t, None, spans, z, seq, pair, mean, M, V, V, 3, 0.01, 0.0, 0.0, False, 1.0, 1.0)
+    big.sync()
+    big.close()
+    ln2 = math.log(2.0)
+    want = -ln2 * torch.tensor([200.0, 100.0, 5.0, 0.0, 0.0, 0.0])
+    assert torch.allclose(seq.cpu(), want, rtol=1e-5, atol=0.0)  # sums of 200 at most, each term off by 4 u
+    v = 0.01 * (want[0::2] - want[1::2])
+    loss = torch.nn.functional.softplus(-v)
+    assert torch.allclose(pair.cpu(), loss, rtol=1e-5) and abs(float(mean) - float(loss.mean())) < 1e-5
+    k = 0.01 * torch.sigmoid(-v)  # -d loss / d S of the preferred answer
+    half = lambda x: torch.tensor([0.5 * x, -0.5 * x]).bfloat16().double()  # noqa: E731
+    for rows, sign, hot in ((slice(M - 300, M - 100), -k[0], 1), (slice(M - 100, M), k[0], 1), (slice(0, 5), -k[1], 0)):
+        g = z[rows].cpu().double()
+        w = half(float(sign)) if hot == 0 else half(float(sign)).flip(0)
+        assert bool(((g - w).abs() <= 2 ** -7 * w.abs()).all())  # a step of bf16
+    assert not z[5:M - 300].any()
+    del z, t
+    torch.cuda.empty_cache()
