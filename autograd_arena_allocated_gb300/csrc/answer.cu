@@ -75,6 +75,22 @@ __device__ __forceinline__ int label_of(const int32_t* targets, long long row, i
 __device__ __forceinline__ float logp_of(float zy, float R, float s, float it) { return fmaf(zy - R, it, -logf(s)); }
 __device__ __forceinline__ float lse_f(float R, float s, float it) { return fmaf(R, it, logf(s)); }
 
+// e^x - x - 1, em1 = e^x - 1.  Near 0, where a policy starts out from its reference,
+// the difference is an x of rounding beside x^2 / 2: up to 1/2 the series (what is
+// left out, x^10 / 10! and on, is below 2^-28 of the sum).  Never below 0.
+__device__ __forceinline__ float exp_minus(float x, float em1) {
+    if (!(fabsf(x) < 0.5f)) return em1 - x;
+    float s = 1.0f / 362880.0f;
+    s = fmaf(s, x, 1.0f / 40320.0f);
+    s = fmaf(s, x, 1.0f / 5040.0f);
+    s = fmaf(s, x, 1.0f / 720.0f);
+    s = fmaf(s, x, 1.0f / 120.0f);
+    s = fmaf(s, x, 1.0f / 24.0f);
+    s = fmaf(s, x, 1.0f / 6.0f);
+    s = fmaf(s, x, 0.5f);
+    return x * x * s;
+}
+
 // what the policy loss of a row needs beside its logits (loaded with the label,
 // so that the row waits once)
 struct PolicyRow {
@@ -95,7 +111,7 @@ struct PolicyRow {
         float v = A == 0.0f && d == d ? 0.0f : -r * A, c = inside || v != v ? v : 0.0f;
         if (a.beta > 0.0f) {
             const float x = ref - lp, e = expm1f(x);
-            v = fmaf(a.beta, e - x, v);
+            v = fmaf(a.beta, exp_minus(x, e), v);
             c = fmaf(-a.beta, e, c);
         }
         return make_float2(w * v, w * c);

@@ -9,7 +9,7 @@ import torch
 
 from autograd_arena_allocated_gb300 import api
 from test_gpu_answers import group_case, run_group_bwd, run_group_fwd
-from test_gpu_head import DEV, TYPES, ctx, gen, make_logits  # noqa: F401 (ctx: a fixture)
+from test_gpu_head import DEV, TYPES, U, ctx, gen, make_logits  # noqa: F401 (ctx: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,36 @@ def test_pairs_at_the_last_rows(ctx):
     assert not z[5:M - 300].any()
     del z, t
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("V", [65, 3000])
+def test_reference_term_near_zero(ctx, V):
+    """beta (e^x - x - 1) alone (no advantage, beta 1), x = ref - lp from a unit in lp's last place to 3.  x is the
+    same fp32 difference here and there, and the product with beta adds to 0, so what is left is the term's own
+    error.  Up to |x| = 1/2 a series: its sum 2 u (later terms are below a third of the first), the square and the
+    product u each, what is left out below u / 10, the last rounding u; 8 u with room.  Beyond: e^x - 1 off by a unit in
+    the last place, 2 u |e^x - 1|, and two roundings of the term."""
+    M = 4000
+    z = make_logits("fp32", M, V, V, 61)
+    t = torch.randint(0, V, (M,), generator=gen(62), device=DEV).int()
+    zero, row = torch.zeros(M, device=DEV), torch.empty(M, device=DEV)
+
+    def go(ref):
+        lp = torch.empty(M, device=DEV)
+        ctx.reset()
+        ctx.policy("fp32", z, t, None, ref, zero, None, None, lp, row, None, M, V, V, 0.2, 0.2, 1.0, 1.0, 1.0)
+        ctx.sync()
+        return lp
+
+    lp = go(zero)
+    size = 10.0 ** (-6.5 + 7.0 * torch.rand(M, generator=gen(63), device=DEV))
+    ref = lp + torch.where(torch.rand(M, generator=gen(64), device=DEV) < 0.5, size, -size)
+    assert torch.equal(go(ref), lp)
+    x = (ref - lp).double()
+    assert int((x.abs() < 1e-5).sum()) > 300
+    # in 64 bits e^x - 1 - x is off by 2^-53 |x|, below 2^-31 of the term from |x| = 2e-7 on
+    want = torch.where(x.abs() < 1e-3, x * x * (0.5 + x * (1 / 6 + x * (1 / 24 + x / 120))), torch.expm1(x) - x)
+    bound = torch.where(x.abs() <= 0.5, 8 * U * want, 2 * U * torch.expm1(x).abs() + 4 * U * want)
+    got = row.double()
+    assert bool((got >= 0).all())
+    assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() / want)[x != 0].max())
