@@ -79,19 +79,21 @@ __global__ void k_embed_fwd(const T* __restrict__ wte, const T* __restrict__ wpe
 }
 
 // The same over groups (group.cuh): an answer's positions follow its prompt's,
-// and a padded position gets zeros, whatever its token is.  A CTA a position.
+// and a padded position gets zeros, whatever its token is; a label there (tgt, may
+// be NULL) would be a wrong loss.  A CTA a position.
 template <typename T>
 __global__ void __launch_bounds__(128)
 k_embed_group_fwd(const T* __restrict__ wte, const T* __restrict__ wpe, const int32_t* __restrict__ tok,
                   T* __restrict__ x, int T_, int C, int V, int maxT, const int32_t* __restrict__ starts, int K,
-                  int* flags) {
+                  const int32_t* __restrict__ tgt, int* flags) {
     pdl_enter();
     const long long m = blockIdx.x;
     const int b = (int)(m / T_), i = (int)(m % T_);
     const group::Group g(starts, b, K, T_);
     const int id = tok[m], t = i < g.P ? i : g.P + i - g.start_of(i);
     const bool real = i < g.end, good = real && id >= 0 && id < V && t < maxT;
-    if (real && !good && threadIdx.x == 0) atomicOr(&flags[FLAG_BAD_TOKEN], 1);
+    const bool bad = real ? !good : tgt && tgt[m] != -1;
+    if (bad && threadIdx.x == 0) atomicOr(&flags[FLAG_BAD_TOKEN], 1);
     for (int c = threadIdx.x; c < C; c += blockDim.x)
         st(x, m * C + c, good ? ld(wte, (long long)id * C + c) + ld(wpe, (long long)t * C + c) : 0.0f);
 }
@@ -124,7 +126,8 @@ k_embed_group_wpe(const T* __restrict__ dx, int B, int T_, int C, const int32_t*
 }
 
 void launch_embed_fwd(const Launch& L, bool bf16, const void* wte, const void* wpe,
-                      const int32_t* tok, void* x, int B, int T, int C, int V, const int32_t* starts, int K, int maxT) {
+                      const int32_t* tok, void* x, int B, int T, int C, int V, const int32_t* starts, int K, int maxT,
+                      const int32_t* targets) {
     if (L.dry) return;
     long long total = (long long)B * T * C;
     L.count();
@@ -132,13 +135,13 @@ void launch_embed_fwd(const Launch& L, bool bf16, const void* wte, const void* w
         const dim3 grid((unsigned)(B * T));
         if (bf16 && L.f16)
             launch_k(L, k_embed_group_fwd<__half>, grid, dim3(128), 0, (const __half*)wte, (const __half*)wpe, tok,
-                     (__half*)x, T, C, V, maxT, starts, K, L.flags);
+                     (__half*)x, T, C, V, maxT, starts, K, targets, L.flags);
         else if (bf16)
             launch_k(L, k_embed_group_fwd<__nv_bfloat16>, grid, dim3(128), 0, (const __nv_bfloat16*)wte,
-                     (const __nv_bfloat16*)wpe, tok, (__nv_bfloat16*)x, T, C, V, maxT, starts, K, L.flags);
+                     (const __nv_bfloat16*)wpe, tok, (__nv_bfloat16*)x, T, C, V, maxT, starts, K, targets, L.flags);
         else
             launch_k(L, k_embed_group_fwd<float>, grid, dim3(128), 0, (const float*)wte, (const float*)wpe, tok, (float*)x,
-                     T, C, V, maxT, starts, K, L.flags);
+                     T, C, V, maxT, starts, K, targets, L.flags);
         return;
     }
     if (bf16 && L.f16)

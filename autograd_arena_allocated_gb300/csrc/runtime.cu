@@ -141,6 +141,7 @@ struct tt_ctx {
     // the step's sequences are groups of answers that share a prompt (group.cuh)
     const int32_t* group_starts = nullptr;
     int group_K = 0;
+    const int32_t* group_targets = nullptr;  // their labels, which padding must not have
     // a recording of graph calls (tt_capture_begin / tt_capture_end / tt_replay)
     bool capturing = false;
     cudaStream_t cap_stream = nullptr, saved_stream = nullptr;
@@ -301,7 +302,7 @@ static int op_embed(tt_ctx* c, const void* wte, const void* wpe, float* dwte, fl
     ProfScope ps(c, PK_EMBED_FWD, 0.0, 3.0 * B * T * m.C * esize(m.dtype) + 4.0 * B * T);
     if (!c->oom)
         launch_embed_fwd(launch_of(c), bf, wte, wpe, tok, c->tensors[out].data, B, T, m.C, m.V, c->group_starts, c->group_K,
-                         m.maxT);
+                         m.maxT, c->group_targets);
     Record r;
     r.kind = R_EMBED;
     r.out = out;
@@ -1150,7 +1151,7 @@ static void begin_step(tt_ctx* c) {
     c->grad_written.clear();
     c->oom = false;
     c->failed = nullptr;
-    c->group_starts = nullptr;
+    c->group_starts = c->group_targets = nullptr;
     c->group_K = 0;
 }
 
@@ -1443,10 +1444,11 @@ static tt_status step_with(tt_ctx* c, const void* params, float* grads, const in
     c->loss_scale_dev = loss_scale;
     c->group_starts = starts;
     c->group_K = K;
+    c->group_targets = tgt;
     tt_status s = gpt2_forward_backward(c, params, grads, tok, tgt, B, T, teacher, answer);
     c->accum_params = false;
     c->loss_scale_dev = nullptr;
-    c->group_starts = nullptr;
+    c->group_starts = c->group_targets = nullptr;
     if (s != TT_OK) {
         if (s == TT_ERR_ARENA_OOM) return fail(c, s, "arena exhausted during the step");
         return s;
@@ -1718,8 +1720,9 @@ tt_status tt_gpt2_logprobs(tt_ctx* c, const void* params, const int32_t* tokens,
     if (st != TT_OK) return st;
     c->group_starts = starts;
     c->group_K = K;
+    c->group_targets = tgt;
     const int z = gpt2_forward(c, params, nullptr, tok, B, T);
-    c->group_starts = nullptr;
+    c->group_starts = c->group_targets = nullptr;
     if (c->failed) return fail(c, TT_ERR_CUDA, "%s", c->failed);
     if (c->oom) return fail(c, TT_ERR_ARENA_OOM, "arena exhausted during the forward");
     const int M = B * T, ld = (int)c->tensors[z].cols;

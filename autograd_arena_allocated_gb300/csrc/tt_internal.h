@@ -166,7 +166,8 @@ void gemm_simt_launch(const Launch& L, const GemmArgs& g);
 // ------------------------------------------------------------ other kernels
 void launch_embed_fwd(const Launch& L, bool bf16, const void* wte, const void* wpe,
                       const int32_t* tok, void* x, int B, int T, int C, int V, const int32_t* starts = nullptr,
-                      int K = 0, int maxT = 0);  // starts [B, K + 1]: the sequences are groups (group.cuh)
+                      int K = 0, int maxT = 0,  // starts [B, K + 1]: the sequences are groups (group.cuh),
+                      const int32_t* targets = nullptr);  // whose padding has no labels: the bad token flag
 // scratch: the stable sort of positions by token id plus chunk partial sums
 size_t embed_bwd_scratch_bytes(int M, int C);
 void launch_embed_bwd(const Launch& L, bool bf16, const void* dx, const int32_t* tok,

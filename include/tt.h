@@ -238,7 +238,7 @@ tt_status tt_gpt2_step_distill(tt_ctx* ctx, const void* params, float* grads, co
  * answer together do (else: the bad token flag, tt_ctx_sync: TT_ERR_ARG).  A
  * row of logits predicts one token, so the last token of the prompt stands at
  * the head of each answer and not in the prompt.  Tokens of padded positions
- * are not used, their targets must be -1.
+ * are not used, their targets must be -1 (else: the bad token flag).
  * Arguments, arena and errors are otherwise those of tt_gpt2_step_ex: targets in
  * device or host memory, every other list in device memory (loss_scale too);
  * the mean is over all B*T positions (policy) or over the pairs. */

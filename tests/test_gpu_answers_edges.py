@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from autograd_arena_allocated_gb300 import api
+from autograd_arena_allocated_gb300 import api, synth
 from test_gpu_answers import group_case, run_group_bwd, run_group_fwd
 from test_gpu_head import DEV, TYPES, U, ctx, gen, make_logits  # noqa: F401 (ctx: a fixture)
 
@@ -113,3 +113,40 @@ def test_reference_term_near_zero(ctx, V):
     got = row.double()
     assert bool((got >= 0).all())
     assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() / want)[x != 0].max())
+
+
+
+@pytest.mark.parametrize("name,dtype", [("tiny_fp32", "fp32"), ("char_bf16", "bf16"), ("tiny_fp32", "fp16")])
+def test_labels_behind_a_groups_end_are_reported(name, dtype):
+    """Padding has no embedding and no gradient: a label there would be a wrong loss."""
+    sh = synth.WORKLOADS[name].shape
+    p = synth.init_params(sh)
+    B, T = 2, 32
+    tok = torch.zeros(B, T, dtype=torch.int32, device=DEV)
+    f = torch.ones(B * T, device=DEV)
+    st = torch.tensor([[4, 12, 20], [0, 16, T]], dtype=torch.int32, device=DEV)
+    spans = torch.tensor([[4, 12], [12, 20]], dtype=torch.int32, device=DEV)
+    cfg = api.make_config(sh.L, sh.C, sh.H, sh.V, sh.maxT, dtype)
+    with api.Context(api.answers_arena_bytes(cfg, B, T, 2)) as c:
+        c.set_model(cfg)
+        ws = torch.from_numpy(p).to(DEV).to(TYPES[dtype])
+        g, out = torch.empty(p.size, device=DEV), torch.empty(B * T, device=DEV)
+        calls = [lambda tgt, s: c.step_policy(ws, g, tok, tgt, None, None, f, None, 0.2, 0.2, 0.0, B=B, T=T, starts=s, K=2),
+                 lambda tgt, s: c.step_preference(ws, g, tok, tgt, None, spans, 1, 0.1, B=B, T=T, starts=s, K=2),
+                 lambda tgt, s: (c.logprobs_of(ws, tok, tgt, B, T, out, starts=s, K=2), c.sync())]
+        tgt = torch.full((B, T), -1, dtype=torch.int32)
+        tgt[0, 4:20] = 1
+        tgt[1, T - 1] = 2
+        for call in calls:
+            for host in (True, False):
+                x = tgt if host else tgt.to(DEV)
+                c.reset()
+                call(x, st)  # the last position of a group without padding may have one
+                for at in (20, T - 1):
+                    bad = tgt.clone()
+                    bad[0, at] = 0
+                    c.reset()
+                    with pytest.raises(api.TTError, match="TT_ERR_ARG"):
+                        call(bad if host else bad.to(DEV), st)
+                    c.reset()
+                    call(bad if host else bad.to(DEV), None)  # without groups it is a label like others
