@@ -382,7 +382,8 @@ static int op_attention(tt_ctx* c, int qkv, int B, int T) {
     int out = new_tensor(c, M, m.C, esize(m.dtype));
     float* lse = (float*)arena_alloc(c, (size_t)B * m.H * T * 4);
     // causal: QK^T and PV over the T(T+1)/2 unmasked pairs
-    const double pairs = (double)B * m.H * T * (T + 1) / 2.0;
+    // how many pairs of positions groups have is in device memory: no products are counted
+    const double pairs = c->group_starts ? 0.0 : (double)B * m.H * T * (T + 1) / 2.0;
     ProfScope ps(c, PK_ATTN_FWD, 4.0 * pairs * (m.C / m.H),
                  (3.0 + 1.0) * M * m.C * esize(m.dtype) + 4.0 * B * m.H * T);
     if (!c->oom && c->group_starts) {
@@ -659,7 +660,7 @@ static tt_status backward_record(tt_ctx* c, int idx) {
         size_t mark = c->off;
         float* s = (float*)arena_alloc(c, attention_bwd_scratch_floats(r.B, r.T, r.N, r.H) * 4);
         // recompute QK^T, then dV, dP, dQ, dK: five products over the causal pairs
-        const double pairs = (double)r.B * r.H * r.T * (r.T + 1) / 2.0;
+        const double pairs = c->group_starts ? 0.0 : (double)r.B * r.H * r.T * (r.T + 1) / 2.0;
         ProfScope ps(c, PK_ATTN_BWD, 10.0 * pairs * (r.N / r.H),
                      (3.0 + 2.0 + 3.0) * r.M * r.N * esize(m.dtype) + 4.0 * r.B * r.H * r.T);
         if (!c->oom && c->group_starts) {
@@ -2209,7 +2210,7 @@ tt_status tt_op_group_attention_fwd(tt_ctx* c, tt_dtype dtype, const void* qkv, 
     c->oom = false;
     bool ok;
     {
-        ProfScope ps(c, PK_ATTN_FWD, 4.0 * ((double)B * T * (T + 1) / 2.0) * C, 4.0 * B * T * C * esize(dtype));
+        ProfScope ps(c, PK_ATTN_FWD, 0.0, 4.0 * B * T * C * esize(dtype) + 4.0 * B * H * T);
         ok = launch_group_attention_fwd(group_launch(c, dtype), dtype != TT_FP32, qkv, starts, y, lse, B, T, C, H, K);
     }
     if (!ok) return fail(c, TT_ERR_CUDA, "group_attention_fwd: launch failed");
@@ -2228,7 +2229,7 @@ tt_status tt_op_group_attention_bwd(tt_ctx* c, tt_dtype dtype, const void* qkv, 
     float* s = (float*)arena_alloc(c, attention_d_floats(B, T, H) * 4);
     bool ok = true;
     if (!c->oom) {
-        ProfScope ps(c, PK_ATTN_BWD, 10.0 * ((double)B * T * (T + 1) / 2.0) * C, 8.0 * B * T * C * esize(dtype));
+        ProfScope ps(c, PK_ATTN_BWD, 0.0, 8.0 * B * T * C * esize(dtype) + 4.0 * B * H * T);
         ok = launch_group_attention_bwd(group_launch(c, dtype), dtype != TT_FP32, qkv, starts, y, lse, dy, dqkv, B, T, C, H,
                                         K, s);
     }

@@ -114,9 +114,13 @@ uint64_t tt_ctx_launch_count(const tt_ctx* ctx);
 /* Per-op timing (tracing).  While on, every kernel group the context launches
  * is bracketed by CUDA events on the context's stream and tagged with its op
  * kind and its algorithmic FLOPs and bytes (the method's own work: each
- * operand read once, each result written once).  tt_ctx_profile_read
- * synchronizes the stream and returns one row per op kind seen since
- * profiling was switched on (at most max_rows), then clears the records. */
+ * operand read once, each result written once).  What lists in device memory
+ * decide is not known to the host: attention over groups counts bytes only, of
+ * all T positions, and the losses on answers count every row, with a label or
+ * without (which is not read), so that their bytes are upper bounds.
+ * tt_ctx_profile_read synchronizes the stream and returns one row per op kind
+ * seen since profiling was switched on (at most max_rows), then clears the
+ * records. */
 typedef struct {
     char name[24];      /* op kind, e.g. "gemm_fwd", "attn_bwd", "xent" */
     uint64_t calls;     /* bracketed groups */

@@ -115,7 +115,6 @@ def test_reference_term_near_zero(ctx, V):
     assert bool(((got - want).abs() <= bound).all()), float(((got - want).abs() / want)[x != 0].max())
 
 
-
 @pytest.mark.parametrize("name,dtype", [("tiny_fp32", "fp32"), ("char_bf16", "bf16"), ("tiny_fp32", "fp16")])
 def test_labels_behind_a_groups_end_are_reported(name, dtype):
     """Padding has no embedding and no gradient: a label there would be a wrong loss."""
@@ -150,3 +149,23 @@ def test_labels_behind_a_groups_end_are_reported(name, dtype):
                         call(bad if host else bad.to(DEV), st)
                     c.reset()
                     call(bad if host else bad.to(DEV), None)  # without groups it is a label like others
+
+
+def test_profile_counts_no_products_of_groups(ctx):
+    """How many pairs of positions a group has is in device memory: its calls count bytes only."""
+    T, C, H = 100, 64, 1
+    qkv, st = group_case("bf16", [[20, 60, 100]], T, C, 71)
+    y, lse = run_group_fwd(ctx, "bf16", qkv, st, T, C, H)
+    d = torch.empty_like(qkv)
+    ctx.set_profiling(True)
+    try:
+        ctx.group_attention_fwd("bf16", qkv, st, y, lse, 1, T, C, H, 2)
+        ctx.group_attention_bwd("bf16", qkv, st, y, lse, y, d, 1, T, C, H, 2)
+        rows = ctx.profile()
+        assert set(rows) == {"attn_fwd", "attn_bwd"}  # with the statistics, 4 bytes a row and head
+        assert all(r["flops"] == 0.0 and r["calls"] == 1 for r in rows.values())
+        assert rows["attn_fwd"]["bytes"] == 4 * T * C * 2 + 4 * T and rows["attn_bwd"]["bytes"] == 8 * T * C * 2 + 4 * T
+        ctx.attention_fwd("bf16", qkv, y, lse, 1, T, C, H)
+        assert ctx.profile()["attn_fwd"]["flops"] > 0.0
+    finally:
+        ctx.set_profiling(False)
