@@ -137,17 +137,15 @@ template <> struct Tile<false> {
     __device__ __forceinline__ unsigned long long keys(int, int, int) const { return 0; }
 };
 template <> struct Tile<true> : group::Group {
-    int q0, n, npre, skip, last_start;
-    __device__ __forceinline__ Tile(const int32_t* starts, int b, int K, int T, int qt)
-        : group::Group(starts, b, K, T), q0(qt * BQ) {
-        if (q0 >= end) return;
-        const group::QueryTile t(*this, q0, BQ);
-        n = t.n; npre = t.npre; skip = t.skip; last_start = t.last_start;
+    group::QueryTile t;  // unused where the tile is padding
+    int n;
+    __device__ __forceinline__ Tile(const int32_t* starts, int b, int K, int T, int qt) : group::Group(starts, b, K, T) {
+        if (qt * BQ >= end) return;
+        t = group::QueryTile(*this, qt * BQ, BQ);
+        n = t.n;
     }
-    __device__ __forceinline__ int block(int j) const { return j < npre ? j : j + skip; }
-    __device__ __forceinline__ bool masked(int, int k0) const {
-        return !((k0 + BN <= P || k0 >= last_start) && k0 + BN - 1 <= q0);
-    }
+    __device__ __forceinline__ int block(int j) const { return t.block(j); }
+    __device__ __forceinline__ bool masked(int, int k0) const { return t.masked(k0); }
 };
 template <bool GRP> struct KTile;
 template <> struct KTile<false> {
@@ -158,13 +156,14 @@ template <> struct KTile<false> {
     __device__ __forceinline__ unsigned long long queries(int, int, int) const { return 0; }
 };
 template <> struct KTile<true> : group::Group {
-    int n, last, min_end;
+    group::KeyTile t;  // unused where the tile is padding
+    int n;
     __device__ __forceinline__ KTile(const int32_t* starts, int b, int K, int T, int kt) : group::Group(starts, b, K, T) {
         if (kt * BQ >= end) return;
-        const group::KeyTile t(*this, kt * BQ, BQ);
-        n = t.n; last = t.last; min_end = t.min_end;
+        t = group::KeyTile(*this, kt * BQ, BQ);
+        n = t.n;
     }
-    __device__ __forceinline__ bool masked(int, int q0) const { return !(q0 >= last && q0 + BN <= min_end); }
+    __device__ __forceinline__ bool masked(int, int q0) const { return t.masked(q0); }
 };
 
 // A head's columns at `col` of the rows first..last - 1 of a tile of padding, and

@@ -69,6 +69,7 @@ struct Group {
 // the key blocks of the query tile [q0, q0 + rows), q0 < end
 struct QueryTile {
     int q0, P, npre, skip, n, last_start;
+    QueryTile() = default;
     __device__ __forceinline__ QueryTile(const Group& g, int q0_, int rows) : q0(q0_), P(g.P) {
         const int last = min(q0 + rows, g.end) - 1, first_block = g.start_of(q0) / BLK;
         npre = (P + BLK - 1) / BLK;
@@ -85,6 +86,7 @@ struct QueryTile {
 // the query blocks j0, j0 + 1, .. of the key tile [k0, k0 + rows), k0 < end
 struct KeyTile {
     int j0, n, last, min_end;
+    KeyTile() = default;
     __device__ __forceinline__ KeyTile(const Group& g, int k0, int rows) : j0(k0 / BLK) {
         last = min(k0 + rows, g.end) - 1;
         n = ((k0 < g.P ? g.end : g.end_of(last)) - 1) / BLK + 1 - j0;
