@@ -30,9 +30,9 @@
 //
 // All but the shortest rows are bound by memory.  32768 rows of 50257 in bf16, the
 // lm head's logits, 54% of them labelled (rates by the bytes that have to move):
-// log probabilities 267 us, 6.6 TB/s; the policy step 789 us, 6.2 TB/s, reads and
-// writes in turn; the preference step 1023 us, of which the second reading of the
-// logits is some 260, 6.7 TB/s with it counted.
+// log probabilities 267 to 271 us, 6.6 TB/s; the policy step 784 to 789 us, 6.2 TB/s,
+// reads and writes in turn; the preference step 1022 us, of which the second reading
+// of the logits is some 260, 6.7 TB/s with it counted.
 #include "row_view.cuh"
 
 namespace tt {
@@ -495,7 +495,7 @@ int row_threads(const Launch& L, int G, long long M) {
 // With the gradient (and without it, so that the loss has the same bits) the rows
 // in flight, which are read a second time, also have to stay in L2: below 92 MB of
 // them where every SM has 1024 threads.  In bf16, 32768 rows of 50257 take 848 us by
-// 256 threads, 893 by 128, 982 by warps, 992 by 512 (789 by 256 once the rows' other
+// 256 threads, 893 by 128, 982 by warps, 992 by 512 (784 by 256 once the rows' other
 // inputs were loaded with the label); 4000 of 150000 339 by 512, 370 by 256 or 1024;
 // 20000 of 5000 62 by warps or 64 threads, 78 by 128.
 int policy_threads(const Launch& L, int G, long long M) {

@@ -15,7 +15,9 @@
 // instructions, half of them FMAs: 8 groups of 1000 positions, 12 heads of 64, 374
 // us forward and 1013 backward, 27 and 25 TFLOP/s of some 74 (one group of 1976, 16
 // heads, 258 and 681; by pieces of 4 x 4 that read two rows a time, without the
-// fetch ahead, 293 and 913).
+// fetch ahead, 293 and 913).  Registers set how much is resident: three CTAs an SM
+// forward (heads of 16: two), two backward (one), and at heads of 64 the forward
+// spills 96 bytes, the keys' kernel 8.
 #include "tt_internal.h"
 #include "group.cuh"
 

@@ -1,5 +1,6 @@
 // attn_tc.cu -- causal self-attention on the 5th-generation tensor cores
-// (tcgen05, bf16 in, fp32 accumulate in tensor memory), head dim 64.
+// (tcgen05, bf16 or half in, fp32 accumulate in tensor memory), heads of 64, and the
+// same over groups of answers, heads of 16, 32 and 64 (GRP, HD below).
 //
 // Every kernel streams 64-wide blocks of the other sequence past a
 // 128-row tile, so that the score block (128 x 64 fp32) needs only 64 TMEM
@@ -26,9 +27,14 @@
 //     dP^T = V dO_j^T; P^T and dS^T; dV += P^T dO_j, dK += dS^T Q_j in TMEM
 //     (Q_j and dO_j, loaded K-major, are read again as MN-major operands).
 //
-// What bounds them: the row warps, by their own latencies (issue 43 to 47%, special
-// functions below a third); the MMAs take 34, 76 and 60% of the time at the rates
-// below.
+// P and dS are rounded to the storage type, as operands of the second products (tf32
+// operands would run at half the rate and take twice the tensor memory); the row sum
+// takes P before that.  Against 64 bits y and dqkv are off by 1.3 to 1.4 times what
+// their own rounding alone leaves.
+//
+// What bounds them: the row warps' chains of dependent steps (issue 43 to 47%, special
+// functions below a third, no unit of the SM saturated); the MMAs take 34, 76 and 60%
+// of the time at the rates below.
 // Every wait is bounded (FLAG_TIMEOUT), as in the GEMM.
 //
 // GRP: the same kernels over groups of answers that share a prompt (group.cuh).
@@ -37,8 +43,8 @@
 // hold anything: a masked probability is 0, and 0 times a NaN is a NaN, so the
 // block in which the padding begins has its rows of the operand whose rows the
 // product sums over (V; K; Q and dO) cleared in shared memory.  Eight groups of 2048
-// positions (half of them the prompt, four answers), 12 heads: 78 us forward (492
-// TFLOP/s) and 235 backward (409); 16% of the blocks' pairs are masked, and by block
+// positions (half of them the prompt, four answers), 12 heads: 80 us forward (482
+// TFLOP/s) and 236 backward (407); 16% of the blocks' pairs are masked, and by block
 // they run as the causal ones do (85 and 255 us for as many causal positions).
 // HD (groups only): heads of 32 and 16 load the 64 columns that theirs are among.
 // Scores take the K steps of their own columns, the products into O, dQ, dK and dV
@@ -223,7 +229,10 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 // tensor memory (its halves 32 columns apart), the A operand of O += P_j V_j; S_{j+1}
 // is issued behind that product, so that a row that sees it knows O to be whole, and
 // may rescale it in place.  A row keeps 32 of its 64 scores in registers and reads the
-// other half again from tensor memory.
+// other half again from tensor memory.  Four CTAs leave a thread 80 registers, too
+// few for all forms: 68 bytes are spilled in the causal one, 80 over groups with heads
+// of 64, 84 with narrower ones (140, 164 and 172 bytes of loads).  It is the faster
+// form all the same: three CTAs with P in shared memory took 88 us, this 79.
 constexpr int F_Q = 0;
 constexpr int F_K = F_Q + T128;     // 2 stages
 constexpr int F_V = F_K + 2 * T64;  // 1 stage
@@ -504,13 +513,14 @@ k_attn_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CU
 // columns [32 half, 32 half + 32).  Each thread therefore owns one row and
 // 32 columns of the score block.
 //
-// The bf16 operand that the row threads produce (dS in the dQ kernel, P^T and
-// dS^T in the dK/dV kernel) is written into tensor memory over the scores it
-// was computed from -- half h writes the 16 columns [32 h, 32 h + 16) of its
-// own 32 -- and the next MMAs read it from there as their A operand, so the
-// N = 64 products read only their B operand from shared memory.  The next
-// block's score MMAs overwrite those columns; they are issued after the MMAs
-// that read them, and one thread's tcgen05.mma operations run in issue order.
+// The 16-bit operand that the row threads produce is written into tensor memory
+// and the next MMAs read it from there as their A operand, so the N = 64 products
+// read only their B operand from shared memory.  P^T and dS^T of the dK/dV kernel
+// go over the scores they were computed from -- half h writes the 16 columns
+// [32 h, 32 h + 16) of its own 32.  The next block's score MMAs overwrite those
+// columns; they are issued after the MMAs that read them, and one thread's
+// tcgen05.mma operations run in issue order.  dS of the dQ kernel has two buffers
+// of its own (Q_TDS).
 constexpr int BW_THREADS = 320;
 constexpr int BW_ROWS = 256;  // row threads
 
@@ -537,12 +547,10 @@ __device__ __forceinline__ void tile_colsum(float (&v)[32], float* cs, float* ds
 // buffers in tensor memory; dQ += dS K_j accumulates in tensor memory.
 // D = rowsum(dO o O) is computed here and saved for the dK/dV kernel.
 //
-// A tcgen05.mma costs its issuing thread tens of cycles, about twice the
-// tensor time of an N = 64 product, so the MMA thread is the critical
-// resource: S_{j+1} and dP_{j+1} are issued once the row threads have block j's in
-// registers, and run while those work on it; dS is double-buffered so that block
-// j's dS never overwrites the operand of block j - 1's dQ MMAs (done when S_{j+1},
-// issued after them, is).
+// S_{j+1} and dP_{j+1} are issued once the row threads have block j's in
+// registers, ahead of dQ_j, and run while those work on it; dS is double-buffered so
+// that block j's dS never overwrites the operand of block j - 1's dQ MMAs (done when
+// S_{j+1}, issued after them, is).
 constexpr int Q_Q = 0;
 constexpr int Q_O = Q_Q + T128;          // dO tile
 constexpr int Q_KST = 3;                 // K stages: K_j is read by S_j and by dQ_j
@@ -1078,7 +1086,7 @@ k_attn_bwd_dkdv_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // the qkv bias gradient's partials: this tile's column sums of dV, then dK
         float* brow = bpart ? bpart + ((long long)b * gridDim.y + kt) * 3 * C + hc + 32 * half : nullptr;
 #pragma unroll 1
-        for (int which = 0; which < 2; which++) {  // 0: dV, 1: dK (times 1/sqrt(64))
+        for (int which = 0; which < 2; which++) {  // 0: dV, 1: dK (times 1/sqrt(HD))
             const float scale = which ? SCALE<HD> : 1.0f;
             float v[32];
 #pragma unroll

@@ -62,10 +62,11 @@ typedef enum { TT_FP32 = 0, TT_BF16 = 1, TT_FP16 = 2 } tt_dtype;
  * TT_FP16: the same split with IEEE half storage (the mixed precision of the
  * dl-scratch page, 3.4): a 10-bit mantissa but a 5-bit exponent, so small
  * activation gradients underflow unless the loss is scaled
- * (tt_gpt2_step_ex's loss_scale).  The half step runs on the SIMT kernels
- * (the tensor-core kernels are bf16).  tt_gpt2_eval takes it too; the
- * generating calls take TT_FP32 and TT_BF16 only, and so do the op-level calls
- * but those over lists of logits and of training on answers (tt_ops.h). */
+ * (tt_gpt2_step_ex's loss_scale).  The half step runs on the tensor cores where
+ * the bf16 one does: its GEMMs, and attention with heads of 64 (over groups of 16
+ * and 32 too).  tt_gpt2_eval takes it as well; the generating calls take TT_FP32
+ * and TT_BF16 only, and so do the op-level calls but those over lists of logits
+ * and of training on answers (tt_ops.h). */
 typedef struct {
     int L, C, H, V, maxT;
     tt_dtype dtype;

@@ -230,9 +230,9 @@ tt_status tt_op_logprobs(tt_ctx* ctx, tt_dtype dtype, const void* logits, const 
                          float* lse, int M, int V, int ld, float tau);
 
 /* Clipped policy loss, loss and gradient in one call.  With lp the log
- * probability of a row's label as tt_op_logprobs forms it, r = exp(lp -
- * old_logp) (1, with its derivative, where old_logp is NULL), A = adv and
- * x = ref_logp - lp:
+ * probability of a row's label (that of tt_op_logprobs to rounding: the sums may
+ * be taken in another order), r = exp(lp - old_logp) (1, with its derivative,
+ * where old_logp is NULL), A = adv and x = ref_logp - lp:
  *   row_loss = weight (-min(r A, clip(r, 1 - eps_low, 1 + eps_high) A)
  *                      + beta (exp(x) - x - 1))
  *   dlogits  = d row_loss / d z * dscale, pad columns 0
@@ -284,8 +284,10 @@ tt_status tt_op_preference(tt_ctx* ctx, tt_dtype dtype, const void* logits, cons
  * and what qkv holds there reaches no other position (a value that is not finite
  * in any other position may reach all of its group).  A list that does not
  * ascend in [0, T] raises the bad token flag; what its sequence receives is
- * undefined.  Head dimensions 16, 32 and 64; C a multiple of 8, and qkv, y (and
- * dy, dqkv) on 16-byte boundaries; B T and B H (T + 63) / 64 within an int. */
+ * undefined.  With 16-bit storage the probabilities are rounded to it for their
+ * product with the values, as in tt_op_attention_fwd; in fp32 they are not.  Head
+ * dimensions 16, 32 and 64; C a multiple of 8, and qkv, y (and dy, dqkv) on 16-byte
+ * boundaries; B T and B H (T + 63) / 64 within an int. */
 tt_status tt_op_group_attention_fwd(tt_ctx* ctx, tt_dtype dtype, const void* qkv, const int32_t* starts, void* y,
                                     float* lse, int B, int T, int C, int H, int K);
 
