@@ -50,7 +50,7 @@
 // Scores take the K steps of their own columns, the products into O, dQ, dK and dV
 // all 64, of which theirs are stored: an MMA costs the same at N = 16 and at 64, and
 // what bounds the kernels, the exponentials and their hand-overs, does not change.
-// Four groups of 1400, 16 heads of 32, half: 28 us forward and 74 backward (by
+// Four groups of 1400, 16 heads of 32, half: 28 us forward and 75 backward (by
 // mma.sync, scores in registers, 57 and 173).
 #include "tt_internal.h"
 #include "group.cuh"

@@ -31,6 +31,22 @@ def test_padding_moves_no_bit_of_a_group(ctx, dtype, C, H):
     assert torch.equal(run_group_bwd(ctx, dtype, qkv, st, y2, lse2, dy, T, C, H), d)
 
 
+@pytest.mark.parametrize("dtype,C,H", [("bf16", 128, 2), ("fp16", 64, 2), ("bf16", 64, 4), ("fp32", 64, 1)])
+def test_the_next_group_moves_no_bit(ctx, dtype, C, H):
+    """A group without padding, alone and in front of one whose queries its last tile loads."""
+    T, starts = 200, [[140, 160, 200], [20, 100, 200]]
+    qkv, st = group_case(dtype, starts, T, C, 27)
+    qkv[T:] *= 30.0
+    dy = torch.randn(2 * T, C, generator=gen(28), device=DEV).to(TYPES[dtype])
+    out = []
+    for n in (1, 2):
+        y, lse = run_group_fwd(ctx, dtype, qkv[:n * T], st[:n].contiguous(), T, C, H)
+        d = run_group_bwd(ctx, dtype, qkv[:n * T], st[:n].contiguous(), y, lse, dy[:n * T], T, C, H)
+        out.append((y[:T], lse[0], d[:T]))
+    for alone, beside in zip(*out):
+        assert torch.equal(alone, beside)
+
+
 @pytest.mark.parametrize("T", [70, 200, 300])
 def test_the_next_sequence_moves_no_bit_of_causal_attention(ctx, T):
     """A tile that runs past its sequence's end loads the next one's queries."""
